@@ -67,7 +67,9 @@ typedef enum {
     TTT_ERR_ALIGN = -3,        /* pointer misaligned for the bulk-copy engine         */
     TTT_ERR_LAUNCH = -4,       /* CUDA reported an error at or before launch          */
     TTT_ERR_TIMEOUT = -5,      /* a kernel wait ran out (reported by ttt_sync_status) */
-    TTT_ERR_SCRATCH = -6       /* ttt_linear_fwd_seqpar_noalloc: more than its fixed scratch */
+    TTT_ERR_SCRATCH = -6,      /* ttt_linear_fwd_seqpar_noalloc: more than its fixed scratch */
+    TTT_ERR_RANGE = -7         /* ttt_rope: a position outside its table (reported by
+                                  ttt_sync_status; the launch itself stays in bounds)  */
 } ttt_status;
 
 typedef enum { TTT_F32 = 0, TTT_BF16 = 1 } ttt_dtype;
@@ -286,8 +288,53 @@ typedef struct {
 ttt_status ttt_eta_gate(const ttt_gate_desc *desc, const void *x, const void *theta, float eta_base,
                         float *eta, void *stream);
 
-/* Waits for `stream`, then reports (and clears) a kernel wait timeout recorded on
- * the current device, or a CUDA error seen while waiting. */
+/* Rotary positions problem description.  Strides are in elements, in the order
+ * batch, head, token; the features of one head are contiguous.  A batch, head or
+ * token stride of an input may be 0 (a broadcast input). */
+typedef struct {
+    int B, T;                  /* batch, tokens per sequence                            */
+    int Hq, Hk;                /* heads of q; heads of k and v                          */
+    int d;                     /* head dim, 1 .. 1024 (TTT_ERR_UNSUPPORTED above)       */
+    int rot;                   /* leading features that are rotated, even, 0 .. d; the
+                                  rest is copied                                        */
+    int interleaved;           /* 0: feature i pairs with i + rot/2; 1: 2i with 2i + 1  */
+    int inverse;               /* 1: the transposed rotation, which turns the gradients
+                                  of the outputs into those of the inputs               */
+    ttt_dtype io_dtype;
+    int table_rows;            /* positions the table covers: 0 .. table_rows - 1       */
+    int period;                /* > 0: positions are taken modulo period (<= table_rows),
+                                  e.g. the mini-batch of the TTT layer                  */
+    long long pos0;            /* position of token 0 when positions is NULL, >= 0      */
+    long long positions_batch_stride; /* T, or 0: positions is [T] for every batch entry */
+    long long q_stride[3], k_stride[3], v_stride[3];
+    long long q_out_stride[3], k_out_stride[3], v_out_stride[3];
+} ttt_rope_desc;
+
+/*
+ * Rotary positions on the layer's queries and keys, with the change of layout from
+ * the projections (e.g. one [B,T,3,H,d] buffer) to the [B,H,T,d] the layer reads:
+ *     out_a = a cos - b sin,  out_b = a sin + b cos
+ * for every feature pair (a, b) of the first rot features, (cos, sin) =
+ * table[position][pair].  v, when given, is copied into its new layout in the same
+ * launch; k and v may be NULL.
+ *   table     : [table_rows, rot/2, 2] fp32, cos and sin of every position and pair,
+ *               8-byte aligned; scaled for long contexts by whoever makes it
+ *   positions : [B,T] (or [T]) 64-bit integers on the device, or NULL for pos0 + t.
+ *               A position < 0 or (with period 0) >= table_rows reads nothing: the
+ *               token's rotated features become NaN and ttt_sync_status returns
+ *               TTT_ERR_RANGE.  pos0 + t is checked before the launch (TTT_ERR_ARG).
+ * An output may be its own input (same pointer and strides) and may not overlap an
+ * input otherwise, except as interleaved slices of one buffer with equal strides
+ * (TTT_ERR_ARG).  Data pointers: aligned to their element (TTT_ERR_ALIGN); 16-byte
+ * aligned pointers and strides with rot/2 a multiple of 8 (bf16) or 4 (fp32) move 16
+ * bytes at a time.  The rotation is computed in fp32 and rounded once.
+ */
+ttt_status ttt_rope(const ttt_rope_desc *desc, const void *q, const void *k, const void *v, const float *table,
+                    const long long *positions, void *q_out, void *k_out, void *v_out, void *stream);
+
+/* Waits for `stream`, then reports (and clears) a kernel wait timeout
+ * (TTT_ERR_TIMEOUT) or a position out of range (TTT_ERR_RANGE) recorded on the current
+ * device, or a CUDA error seen while waiting. */
 ttt_status ttt_sync_status(void *stream);
 
 /* Static description of a status code. */

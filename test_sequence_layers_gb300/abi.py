@@ -17,12 +17,13 @@ LIB_PATH = os.path.join(_HERE, "libttt.so")
 
 TTT_F32, TTT_BF16 = 0, 1
 STATUS = {0: "TTT_OK", -1: "TTT_ERR_ARG", -2: "TTT_ERR_UNSUPPORTED", -3: "TTT_ERR_ALIGN",
-          -4: "TTT_ERR_LAUNCH", -5: "TTT_ERR_TIMEOUT", -6: "TTT_ERR_SCRATCH"}
+          -4: "TTT_ERR_LAUNCH", -5: "TTT_ERR_TIMEOUT", -6: "TTT_ERR_SCRATCH",
+          -7: "TTT_ERR_RANGE"}
 
 # every symbol include/ttt.h declares
 EXPORTS = ("ttt_linear_fwd", "ttt_linear_seqpar_workspace", "ttt_linear_fwd_seqpar",
            "ttt_linear_fwd_seqpar_noalloc", "ttt_dwconv_fwd", "ttt_eta_gate",
-           "ttt_mlp_fwd", "ttt_sync_status", "ttt_status_str", "ttt_launch_count",
+           "ttt_mlp_fwd", "ttt_rope", "ttt_sync_status", "ttt_status_str", "ttt_launch_count",
            "ttt_debug_wait_limit")
 
 
@@ -55,6 +56,14 @@ ACTIVATIONS = {"silu": 0, "gelu": 1}
 
 class GateDesc(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int), ("dm", ctypes.c_int)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("Hq", ctypes.c_int), ("Hk", ctypes.c_int),
+                ("d", ctypes.c_int), ("rot", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("inverse", ctypes.c_int), ("io_dtype", ctypes.c_int), ("table_rows", ctypes.c_int),
+                ("period", ctypes.c_int), ("pos0", ctypes.c_longlong),
+                ("positions_batch_stride", ctypes.c_longlong), ("strides", ctypes.c_longlong * 18)]
 
 
 class TTTError(RuntimeError):
@@ -92,6 +101,8 @@ def lib():
         L.ttt_mlp_fwd.restype = ctypes.c_int
         L.ttt_eta_gate.argtypes = [ctypes.POINTER(GateDesc), vp, vp, f, fp, vp]
         L.ttt_eta_gate.restype = ctypes.c_int
+        L.ttt_rope.argtypes = [ctypes.POINTER(RopeDesc), vp, vp, vp, fp, vp, vp, vp, vp, vp]
+        L.ttt_rope.restype = ctypes.c_int
         L.ttt_sync_status.argtypes = [vp]
         L.ttt_sync_status.restype = ctypes.c_int
         L.ttt_status_str.argtypes = [ctypes.c_int]
@@ -373,6 +384,104 @@ def ttt_eta_gate(x, theta, eta_base=1.0, eta=None, stream=None):
     if rc != 0:
         raise TTTError("ttt_eta_gate", rc)
     return eta
+
+
+_IO = {torch.bfloat16: TTT_BF16, torch.float32: TTT_F32}
+
+
+def _tokens(name, t, dims, like=None):
+    """A token tensor of the streaming operators: CUDA, bf16 or fp32, `dims` dimensions,
+    the last one contiguous; `like`: shares its dtype and device."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions")
+    if t.dtype not in _IO:
+        raise ValueError(f"{name} must be bfloat16 or float32")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must share the dtype and device of the first tensor")
+    return t
+
+
+def _call(fn, dev, stream, *args):
+    """Runs one library entry point on dev's current stream (or `stream`)."""
+    if stream is None:
+        raw = torch.cuda.current_stream(dev).cuda_stream
+    elif stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device} but the tensors on {dev}")
+    else:
+        raw = stream.cuda_stream
+    f = getattr(lib(), fn)
+    if torch.cuda.current_device() == dev.index:
+        rc = f(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args, raw)
+    if rc != 0:
+        raise TTTError(fn, rc)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def ttt_rope(q, k, v, table, positions=None, pos0=0, period=0, interleaved=False, inverse=False, q_out=None,
+             k_out=None, v_out=None, stream=None):
+    """Rotary positions on q and k, with the change of head layout; v (if given) is
+    copied to its new layout in the same launch.
+
+    q: [B,H,T,d] bf16 or fp32 with any strides as long as a head's features are
+    contiguous (a [B,T,3,H,d] projection passes permuted views); k, v: [B,Hk,T,d] or None.
+    table: fp32 [rows, rot/2, 2] cos and sin (rotary.rope_table).  positions: int64 [B,T]
+    or [T] on the device, or None for pos0 + t; period > 0 takes them modulo period.
+    interleaved: pairs (2i, 2i+1) instead of (i, i + rot/2).  inverse=True rotates back:
+    the gradients of q, k, v from those of the outputs.  Outputs are contiguous
+    [B,H,T,d] unless q_out, k_out, v_out are given (any strides; an output may be its
+    own input).  Returns (q_out, k_out, v_out).  A position outside the table gives NaN
+    and TTT_ERR_RANGE from ttt_sync_status."""
+    _tokens("q", q, 4)
+    B, H, T, d = q.shape
+    dev = q.device
+    hk = 0
+    for name, t in (("k", k), ("v", v)):
+        if t is not None:
+            _tokens(name, t, 4, q)
+            if t.shape[0] != B or t.shape[2:] != q.shape[2:] or (hk and t.shape[1] != hk):
+                raise ValueError(f"{name} must be [B,Hk,T,d] with q's B, T and d")
+            hk = t.shape[1]
+    if (not table.is_cuda or table.dtype != torch.float32 or table.device != dev or table.dim() != 3
+            or table.shape[2] != 2 or not table.is_contiguous()):
+        raise ValueError("table must be a contiguous float32 [rows, rot/2, 2] tensor on q's device")
+    pbs = 0
+    if positions is not None:
+        if positions.dtype != torch.int64 or positions.device != dev or not positions.is_contiguous():
+            raise ValueError("positions must be a contiguous int64 tensor on q's device")
+        if tuple(positions.shape) == (B, T):
+            pbs = T
+        elif tuple(positions.shape) != (T,):
+            raise ValueError("positions must be [B,T] or [T]")
+    ins, outs, strides = (q, k, v), [q_out, k_out, v_out], []
+    for i, (name, t) in enumerate((("q_out", q), ("k_out", k), ("v_out", v))):
+        o = outs[i]
+        if t is None:
+            if o is not None:
+                raise ValueError(f"{name} given without its input")
+            continue
+        if o is None:
+            outs[i] = torch.empty(t.shape, dtype=t.dtype, device=dev)
+        else:
+            _tokens(name, o, 4, q)
+            if o.shape != t.shape:
+                raise ValueError(f"{name} must have the shape of its input")
+    for t in (*ins, *outs):
+        strides += (0, 0, 0) if t is None else t.stride()[:3]
+    desc = RopeDesc(B, T, H, hk, d, 2 * table.shape[1], 1 if interleaved else 0, 1 if inverse else 0, _IO[q.dtype],
+                    table.shape[0], int(period), int(pos0), pbs, (ctypes.c_longlong * 18)(*strides))
+    _call("ttt_rope", dev, stream, desc, _addr(q), _addr(k), _addr(v), table.data_ptr(), _addr(positions),
+          _addr(outs[0]), _addr(outs[1]), _addr(outs[2]))
+    return tuple(outs)
 
 
 def ttt_sync_status(stream=None):

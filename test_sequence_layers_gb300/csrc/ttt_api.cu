@@ -10,6 +10,7 @@
 
 #include "../../include/ttt.h"
 #include "ttt_internal.h"
+#include "ttt_vec.cuh"
 
 // Status word written by kernels whose bounded on-chip wait ran out (one per
 // device: every device that loads the library has its own copy).
@@ -450,6 +451,90 @@ ttt_status ttt_eta_gate(const ttt_gate_desc *desc, const void *x, const void *th
     return code(rc);
 }
 
+namespace {
+
+// Elements from the first to one past the last of a [B,H,T,d] view with these strides.
+long long span(const long long st[3], int B, int H, int T, int d)
+{
+    return st[0] * (B - 1) + st[1] * (H - 1) + st[2] * (T - 1) + d;
+}
+
+bool same_strides(const long long a[3], const long long b[3]) { return a[0] == b[0] && a[1] == b[1] && a[2] == b[2]; }
+
+}  // namespace
+
+ttt_status ttt_rope(const ttt_rope_desc *desc, const void *q, const void *k, const void *v, const float *table,
+                    const long long *positions, void *q_out, void *k_out, void *v_out, void *stream)
+{
+    if (!desc) return TTT_ERR_ARG;
+    const ttt_rope_desc D = *desc;
+    if (D.B < 0 || D.T < 0 || D.Hq < 1 || D.Hk < 0 || D.d < 1 || D.rot < 0 || D.rot > D.d || D.rot % 2) return TTT_ERR_ARG;
+    if (D.interleaved < 0 || D.interleaved > 1 || D.inverse < 0 || D.inverse > 1) return TTT_ERR_ARG;
+    if (D.io_dtype != TTT_F32 && D.io_dtype != TTT_BF16) return TTT_ERR_ARG;
+    if (D.table_rows < 0 || D.period < 0 || D.period > D.table_rows || D.pos0 < 0 || D.pos0 > (1LL << 62) || D.positions_batch_stride < 0)
+        return TTT_ERR_ARG;
+    if (D.d > 1024 || (long long)D.B * D.T > 0x7fffffffLL) return TTT_ERR_UNSUPPORTED;
+    if (D.B == 0 || D.T == 0) return TTT_OK;
+    if (!q || !q_out || (k && !k_out) || (v && !v_out) || ((k || v) && D.Hk < 1)) return TTT_ERR_ARG;
+    if (D.rot > 0 && !table) return TTT_ERR_ARG;
+    if (D.rot > 0 && !positions && D.period == 0 && D.pos0 > (long long)D.table_rows - D.T) return TTT_ERR_ARG;
+    const int es = D.io_dtype == TTT_BF16 ? 2 : 4;
+    ttt::RopeArgs a = {};
+    const void *in[3] = {q, k, v};
+    void *out[3] = {q_out, k_out, v_out};
+    const long long *is[3] = {D.q_stride, D.k_stride, D.v_stride};
+    const long long *os[3] = {D.q_out_stride, D.k_out_stride, D.v_out_stride};
+    const int H[3] = {D.Hq, D.Hk, D.Hk}, dim[3] = {D.B, 0, D.T};
+    for (int i = 0; i < 3; ++i) {
+        if (!in[i]) continue;
+        if (!aligned(in[i], es) || !aligned(out[i], es)) return TTT_ERR_ALIGN;
+        for (int j = 0; j < 3; ++j) {
+            const int n = j == 1 ? H[i] : dim[j];
+            if (is[i][j] < 0 || os[i][j] < 0 || (n > 1 && os[i][j] == 0)) return TTT_ERR_ARG;
+            // a dimension of one entry is never stepped over: its stride says nothing
+            a.in_stride[i][j] = n > 1 ? is[i][j] : 0;
+            a.out_stride[i][j] = n > 1 ? os[i][j] : 0;
+        }
+    }
+    if (D.rot > 0 && (!aligned(table, 8) || (positions && !aligned(positions, 8)))) return TTT_ERR_ALIGN;
+    for (int i = 0; i < 3; ++i)
+        for (int j = 0; j < 3; ++j) {
+            if (!in[i] || !in[j]) continue;
+            const bool apart = !overlaps(in[i], es * span(a.in_stride[i], D.B, H[i], D.T, D.d), out[j],
+                                         es * span(a.out_stride[j], D.B, H[j], D.T, D.d));
+            if (apart) continue;
+            if (!same_strides(a.in_stride[i], a.out_stride[j]) || (i == j ? in[i] != out[j] : in[i] == out[j]))
+                return TTT_ERR_ARG;
+        }
+    a.B = D.B;
+    a.T = D.T;
+    a.Hq = D.Hq;
+    a.Hk = D.Hk;
+    a.d = D.d;
+    a.rot = D.rot;
+    a.interleaved = D.interleaved;
+    a.inverse = D.inverse;
+    a.bf16 = D.io_dtype == TTT_BF16;
+    a.table_rows = D.table_rows;
+    a.period = D.period;
+    a.pos0 = D.pos0;
+    a.pos_bstride = D.positions_batch_stride;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.table = table;
+    a.positions = positions;
+    a.status = status_word();
+    a.stream = static_cast<cudaStream_t>(stream);
+    if (!a.status) return TTT_ERR_LAUNCH;
+    const int rc = ttt::launch_rope(a);
+    if (rc == 0) g_launches.fetch_add(1, std::memory_order_relaxed);
+    return code(rc);
+}
+
 ttt_status ttt_sync_status(void *stream)
 {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return TTT_ERR_LAUNCH;
@@ -458,7 +543,7 @@ ttt_status ttt_sync_status(void *stream)
     if (v != 0) {
         const int zero = 0;
         cudaMemcpyToSymbol(g_ttt_status, &zero, sizeof(int));
-        return TTT_ERR_TIMEOUT;
+        return v == ttt::kSitePositionRange ? TTT_ERR_RANGE : TTT_ERR_TIMEOUT;
     }
     return TTT_OK;
 }
@@ -473,6 +558,7 @@ const char *ttt_status_str(ttt_status s)
     case TTT_ERR_LAUNCH: return "CUDA error at launch";
     case TTT_ERR_TIMEOUT: return "kernel wait timed out";
     case TTT_ERR_SCRATCH: return "the split run needs more than the library's fixed 4 MiB scratch";
+    case TTT_ERR_RANGE: return "a position lies outside the rotary table";
     }
     return "unknown status";
 }

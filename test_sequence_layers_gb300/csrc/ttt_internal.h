@@ -64,6 +64,18 @@ struct GateArgs {
     cudaStream_t stream;
 };
 
+struct RopeArgs {
+    int B, T, Hq, Hk, d, rot, interleaved, inverse, bf16, table_rows, period;
+    long long pos0, pos_bstride;
+    const void *q, *k, *v;  // k, v may be null
+    void *q_out, *k_out, *v_out;
+    long long in_stride[3][3], out_stride[3][3];  // [q, k, v][batch, head, token], elements
+    const float *table;          // [table_rows][rot/2][2] cos, sin
+    const long long *positions;  // or null: pos0 + t
+    int *status;                 // device status word (positions out of range)
+    cudaStream_t stream;
+};
+
 // TMA descriptor of a bf16 token tensor viewed as [BH][T][d]: boxes of `rows`
 // tokens x `cols` features (0: min(d, 64)), swizzled to the box row length, rows
 // past T zero-filled on loads and dropped on stores.  Returns false if the driver
@@ -127,6 +139,7 @@ int launch_linear_seqpar_serial(const LinearArgs &a, const SeqparPlan &pl, void 
 size_t dwconv_smem(int hh, int ww, int d, int es);
 int launch_dwconv(const DwconvArgs &a);
 int launch_eta_gate(const GateArgs &a);  // H <= 64; -2 otherwise
+int launch_rope(const RopeArgs &a);
 
 // Largest d*m the fp32 MLP path holds on chip.
 bool mlp_f32_fits(int d, int m);
