@@ -332,6 +332,78 @@ typedef struct {
 ttt_status ttt_rope(const ttt_rope_desc *desc, const void *q, const void *k, const void *v, const float *table,
                     const long long *positions, void *q_out, void *k_out, void *v_out, void *stream);
 
+/* Norms of ttt_block_norm_fwd / _bwd, over the D features of a token.
+ *   TTT_NORM_RMS:   w v / sqrt(mean(v^2) + eps)
+ *   TTT_NORM_LAYER: w (v - mean) / sqrt(var + eps) + b */
+typedef enum { TTT_NORM_NONE = 0, TTT_NORM_RMS = 1, TTT_NORM_LAYER = 2 } ttt_norm;
+
+/* The gate's activation (TTT_GATE_NONE: no gate tensor). */
+typedef enum { TTT_GATE_NONE = 0, TTT_GATE_SIGMOID = 1, TTT_GATE_SILU = 2, TTT_GATE_GELU = 3 } ttt_gate_act;
+
+/* Block norm problem description.  Strides are in elements; features are contiguous
+ * (y: inside each head). */
+typedef struct {
+    int B, T, D;               /* batch, tokens, features 1 .. 8192 (TTT_ERR_UNSUPPORTED above) */
+    int heads;                 /* y is [B,heads,T,D/heads] (the TTT layer's z); 1: [B,T,D]      */
+    ttt_dtype io_dtype;        /* dtype of every token tensor                                   */
+    int post, pre;             /* ttt_norm of y and of h                                        */
+    int act;                   /* ttt_gate_act                                                  */
+    float post_eps, pre_eps;   /* >= 0; 0 only where no row is constant zero                    */
+    float alpha;               /* factor of the residual x                                      */
+    long long y_stride[3];     /* batch, head, token                                            */
+    long long x_stride[2], gate_stride[2], dh_stride[2], du_stride[2]; /* batch, token          */
+} ttt_block_norm_desc;
+
+/* Parameter vectors, fp32 [D] on the device, each may be NULL (weights and scale 1,
+ * biases 0); biases go with TTT_NORM_LAYER only. */
+typedef struct {
+    const float *post_weight, *post_bias, *scale, *pre_weight, *pre_bias;
+} ttt_block_norm_params;
+
+/* Their gradients (overwritten, not added to), each may be NULL. */
+typedef struct {
+    float *post_weight, *post_bias, *scale, *pre_weight, *pre_bias;
+} ttt_block_norm_grads;
+
+/*
+ * The norms before and after a block, its gate and its residual in one pass:
+ *     p = N_post(y),  h = alpha x + scale * act(gate) * p,  u = N_pre(h)
+ * y is the inner layer's output, gate [B,T,D] its gate's argument, x [B,T,D] the
+ * residual stream (NULL: h = scale * act(gate) * p, the input of an output projection),
+ * h the new residual stream and u the next layer's input (written when pre is not
+ * TTT_NORM_NONE).  ("Learning to (Learn at Test Time)" walkthrough, section 2.2.1: the
+ * layer norm behind the layer; the backbone's gate and residual around it.)
+ *   h, u  : [B,T,D] contiguous io_dtype; u NULL exactly when pre is TTT_NORM_NONE
+ *   stats : [B,T,4] fp32, 16-byte aligned, or NULL: mean and 1/spread of both norms,
+ *           which the backward pass reads
+ * u is the norm of h before its rounding to io_dtype.  Outputs may not overlap inputs,
+ * except h being x (same pointer, contiguous).  Data pointers: aligned to their
+ * element; 16-byte aligned pointers, strides of whole 16 bytes and D and D / heads
+ * multiples of 8 move 16 bytes at a time.
+ */
+ttt_status ttt_block_norm_fwd(const ttt_block_norm_desc *desc, const ttt_block_norm_params *params, const void *y,
+                              const void *x, const void *gate, void *h, void *u, float *stats, void *stream);
+
+/* Bytes of workspace the backward pass needs (0 for a description it refuses). */
+size_t ttt_block_norm_bwd_workspace(const ttt_block_norm_desc *desc);
+
+/*
+ * Gradients of ttt_block_norm_fwd: from dh and du (of h and u; dh NULL: zero; du NULL
+ * exactly when pre is TTT_NORM_NONE), the forward's inputs and its stats.
+ *   dy    : contiguous in y's layout ([B,heads,T,D/heads] or [B,T,D])
+ *   dx    : [B,T,D] or NULL;  dgate: [B,T,D], NULL exactly when act is TTT_GATE_NONE
+ *   grads : gradients of the parameter vectors, summed over all tokens in an order that
+ *           depends on the sizes only (the same bits on every run), or NULL
+ *   workspace : device scratch, 16-byte aligned, at least
+ *           ttt_block_norm_bwd_workspace(desc) bytes (NULL allowed when no parameter
+ *           gradient is asked for), free again once the work on `stream` is done
+ * Outputs may not overlap inputs.
+ */
+ttt_status ttt_block_norm_bwd(const ttt_block_norm_desc *desc, const ttt_block_norm_params *params, const void *dh,
+                              const void *du, const void *y, const void *x, const void *gate, const float *stats,
+                              void *dy, void *dx, void *dgate, const ttt_block_norm_grads *grads, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
 /* Waits for `stream`, then reports (and clears) a kernel wait timeout
  * (TTT_ERR_TIMEOUT) or a position out of range (TTT_ERR_RANGE) recorded on the current
  * device, or a CUDA error seen while waiting. */

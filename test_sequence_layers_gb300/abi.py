@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -23,7 +24,8 @@ STATUS = {0: "TTT_OK", -1: "TTT_ERR_ARG", -2: "TTT_ERR_UNSUPPORTED", -3: "TTT_ER
 # every symbol include/ttt.h declares
 EXPORTS = ("ttt_linear_fwd", "ttt_linear_seqpar_workspace", "ttt_linear_fwd_seqpar",
            "ttt_linear_fwd_seqpar_noalloc", "ttt_dwconv_fwd", "ttt_eta_gate",
-           "ttt_mlp_fwd", "ttt_rope", "ttt_sync_status", "ttt_status_str", "ttt_launch_count",
+           "ttt_mlp_fwd", "ttt_rope", "ttt_block_norm_fwd", "ttt_block_norm_bwd_workspace",
+           "ttt_block_norm_bwd", "ttt_sync_status", "ttt_status_str", "ttt_launch_count",
            "ttt_debug_wait_limit")
 
 
@@ -66,6 +68,21 @@ class RopeDesc(ctypes.Structure):
                 ("positions_batch_stride", ctypes.c_longlong), ("strides", ctypes.c_longlong * 18)]
 
 
+class BlockNormDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("D", ctypes.c_int), ("heads", ctypes.c_int),
+                ("io_dtype", ctypes.c_int), ("post", ctypes.c_int), ("pre", ctypes.c_int), ("act", ctypes.c_int),
+                ("post_eps", ctypes.c_float), ("pre_eps", ctypes.c_float), ("alpha", ctypes.c_float),
+                ("strides", ctypes.c_longlong * 11)]
+
+
+class BlockNormVectors(ctypes.Structure):
+    """ttt_block_norm_params and ttt_block_norm_grads."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("post_weight", "post_bias", "scale", "pre_weight", "pre_bias")]
+
+NORMS = {"none": 0, "rms": 1, "layer": 2}
+GATES = {"none": 0, "sigmoid": 1, "silu": 2, "gelu": 3}
+
+
 class TTTError(RuntimeError):
     def __init__(self, fn, rc):
         self.code = rc
@@ -103,6 +120,15 @@ def lib():
         L.ttt_eta_gate.restype = ctypes.c_int
         L.ttt_rope.argtypes = [ctypes.POINTER(RopeDesc), vp, vp, vp, fp, vp, vp, vp, vp, vp]
         L.ttt_rope.restype = ctypes.c_int
+        L.ttt_block_norm_fwd.argtypes = [ctypes.POINTER(BlockNormDesc), ctypes.POINTER(BlockNormVectors), vp, vp, vp,
+                                         vp, vp, fp, vp]
+        L.ttt_block_norm_fwd.restype = ctypes.c_int
+        L.ttt_block_norm_bwd_workspace.argtypes = [ctypes.POINTER(BlockNormDesc)]
+        L.ttt_block_norm_bwd_workspace.restype = ctypes.c_size_t
+        L.ttt_block_norm_bwd.argtypes = [ctypes.POINTER(BlockNormDesc), ctypes.POINTER(BlockNormVectors), vp, vp, vp,
+                                         vp, vp, fp, vp, vp, vp, ctypes.POINTER(BlockNormVectors), vp,
+                                         ctypes.c_size_t, vp]
+        L.ttt_block_norm_bwd.restype = ctypes.c_int
         L.ttt_sync_status.argtypes = [vp]
         L.ttt_sync_status.restype = ctypes.c_int
         L.ttt_status_str.argtypes = [ctypes.c_int]
@@ -482,6 +508,118 @@ def ttt_rope(q, k, v, table, positions=None, pos0=0, period=0, interleaved=False
     _call("ttt_rope", dev, stream, desc, _addr(q), _addr(k), _addr(v), table.data_ptr(), _addr(positions),
           _addr(outs[0]), _addr(outs[1]), _addr(outs[2]))
     return tuple(outs)
+
+
+def _like(name, t, shape, dtype, dev):
+    """A contiguous tensor of the given shape, dtype and device (outputs, saved data)."""
+    if t.dtype != dtype or t.device != dev or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
+    return t
+
+
+def _norm_prologue(y, x, gate, act, post, pre, post_eps, pre_eps, alpha, vectors, dh=None, du=None):
+    """Checks of both block-norm wrappers; returns (B, T, D, descriptor, parameters)."""
+    _tokens("y", y, 4 if y.dim() == 4 else 3)
+    if y.dim() == 4:
+        B, heads, T, d = y.shape
+        D, ys = heads * d, y.stride()[:3]
+    else:
+        (B, T, D), heads = y.shape, 1
+        ys = (y.stride(0), 0, y.stride(1))
+    if (gate is None) != (act == "none"):
+        raise ValueError('a gate goes with an act other than "none"')
+    strides = [*ys]
+    for name, t in (("x", x), ("gate", gate), ("dh", dh), ("du", du)):
+        if t is None:
+            strides += (0, 0)
+            continue
+        _tokens(name, t, 3, y)
+        if t.shape != (B, T, D):
+            raise ValueError(f"{name} must be [B,T,D] = {(B, T, D)}")
+        strides += t.stride()[:2]
+    for name, t in vectors.items():
+        if t is not None:
+            _like(name, t, (D,), torch.float32, y.device)
+    desc = BlockNormDesc(B, T, D, heads, _IO[y.dtype], NORMS[post], NORMS[pre], GATES[act], post_eps, pre_eps, alpha,
+                         (ctypes.c_longlong * 11)(*strides))
+    return B, T, D, desc, BlockNormVectors(*(_addr(t) for t in vectors.values()))
+
+
+def ttt_block_norm_fwd(y, x=None, gate=None, act=None, post="none", post_weight=None, post_bias=None, scale=None,
+                       alpha=1.0, pre="none", pre_weight=None, pre_bias=None, post_eps=1e-6, pre_eps=1e-6,
+                       want_stats=False, h=None, u=None, stats=None, stream=None):
+    """The norms before and after a block, its gate and its residual in one pass:
+        h = alpha x + scale * act(gate) * N_post(y),   u = N_pre(h)
+    y: [B,T,D] or the layer's head-major [B,H,T,d] (D = H d); x, gate: [B,T,D] or None;
+    bf16 or fp32, strided as long as the features are contiguous.  act "none", "sigmoid",
+    "silu" or "gelu" (default: "silu" with a gate); post, pre "none", "rms" or "layer".
+    Weights, biases and scale: fp32 [D] or None.  want_stats (or stats) for the backward
+    pass.  h may be x.  Returns (h, u or None, stats or None)."""
+    if act is None:
+        act = "none" if gate is None else "silu"
+    B, T, D, desc, par = _norm_prologue(y, x, gate, act, post, pre, post_eps, pre_eps, alpha,
+                                        dict(post_weight=post_weight, post_bias=post_bias, scale=scale,
+                                             pre_weight=pre_weight, pre_bias=pre_bias))
+    dev = y.device
+    h = torch.empty((B, T, D), dtype=y.dtype, device=dev) if h is None else _like("h", h, (B, T, D), y.dtype, dev)
+    if pre == "none":
+        if u is not None:
+            raise ValueError("u is written with a pre norm only")
+    else:
+        u = torch.empty((B, T, D), dtype=y.dtype, device=dev) if u is None else _like("u", u, (B, T, D), y.dtype, dev)
+    if stats is not None:
+        _like("stats", stats, (B, T, 4), torch.float32, dev)
+    elif want_stats:
+        stats = torch.empty((B, T, 4), dtype=torch.float32, device=dev)
+    _call("ttt_block_norm_fwd", dev, stream, desc, par, y.data_ptr(), _addr(x), _addr(gate), h.data_ptr(), _addr(u),
+          _addr(stats))
+    return h, u, stats
+
+
+class BlockNormGrads(NamedTuple):
+    """Gradients of ttt_block_norm_fwd's inputs, None for an absent input."""
+    y: torch.Tensor
+    x: Optional[torch.Tensor]
+    gate: Optional[torch.Tensor]
+    post_weight: Optional[torch.Tensor]
+    post_bias: Optional[torch.Tensor]
+    scale: Optional[torch.Tensor]
+    pre_weight: Optional[torch.Tensor]
+    pre_bias: Optional[torch.Tensor]
+
+
+def ttt_block_norm_bwd(dh, du, y, stats, x=None, gate=None, act=None, post="none", post_weight=None, post_bias=None,
+                       scale=None, alpha=1.0, pre="none", pre_weight=None, pre_bias=None, post_eps=1e-6, pre_eps=1e-6,
+                       workspace=None, stream=None):
+    """Gradients of ttt_block_norm_fwd from dh (or None) and du (None without a pre norm),
+    the forward's inputs and its stats.  Returns BlockNormGrads: y's in y's shape
+    (contiguous), fp32 [D] for every parameter vector given.  workspace: a CUDA uint8
+    tensor of ttt_block_norm_bwd_workspace(...) bytes, allocated here when None."""
+    if act is None:
+        act = "none" if gate is None else "silu"
+    vectors = dict(post_weight=post_weight, post_bias=post_bias, scale=scale, pre_weight=pre_weight, pre_bias=pre_bias)
+    B, T, D, desc, par = _norm_prologue(y, x, gate, act, post, pre, post_eps, pre_eps, alpha, vectors, dh, du)
+    dev = y.device
+    _like("stats", stats, (B, T, 4), torch.float32, dev)
+    dy = torch.empty(y.shape, dtype=y.dtype, device=dev)
+    dx = None if x is None else torch.empty((B, T, D), dtype=y.dtype, device=dev)
+    dg = None if gate is None else torch.empty((B, T, D), dtype=y.dtype, device=dev)
+    gv = [None if t is None else torch.empty(D, dtype=torch.float32, device=dev) for t in vectors.values()]
+    need = int(lib().ttt_block_norm_bwd_workspace(desc))
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on y's device")
+    _call("ttt_block_norm_bwd", dev, stream, desc, par, _addr(dh), _addr(du), y.data_ptr(), _addr(x), _addr(gate),
+          stats.data_ptr(), dy.data_ptr(), _addr(dx), _addr(dg), BlockNormVectors(*(_addr(t) for t in gv)),
+          workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return BlockNormGrads(dy, dx, dg, *gv)
+
+
+def ttt_block_norm_bwd_workspace(B, T, D) -> int:
+    """Workspace bytes of ttt_block_norm_bwd for B x T tokens of D features."""
+    desc = BlockNormDesc(B, T, D, 1, TTT_BF16, 0, 0, 0, 1e-6, 1e-6, 1.0)
+    return int(lib().ttt_block_norm_bwd_workspace(desc))
 
 
 def ttt_sync_status(stream=None):

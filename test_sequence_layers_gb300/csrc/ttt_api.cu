@@ -535,6 +535,195 @@ ttt_status ttt_rope(const ttt_rope_desc *desc, const void *q, const void *k, con
     return code(rc);
 }
 
+namespace {
+
+bool norm_desc_ok(const ttt_block_norm_desc &D)
+{
+    if (D.B < 0 || D.T < 0 || D.D < 1 || D.heads < 1 || D.D % D.heads) return false;
+    if (D.io_dtype != TTT_F32 && D.io_dtype != TTT_BF16) return false;
+    if (D.post < 0 || D.post > 2 || D.pre < 0 || D.pre > 2 || D.act < 0 || D.act > 3) return false;
+    return (!D.post || D.post_eps >= 0.f) && (!D.pre || D.pre_eps >= 0.f);
+}
+
+constexpr int kNormMaxD = 8192;
+
+// Checks the part both directions share and fills the launch arguments; TTT_OK with
+// *empty set when there are no tokens.
+ttt_status norm_args(const ttt_block_norm_desc *desc, const ttt_block_norm_params *params, const void *y, const void *x,
+                     const void *gate, void *stream, ttt::BlockNormArgs &a, bool *empty)
+{
+    if (!desc || !params) return TTT_ERR_ARG;
+    const ttt_block_norm_desc &D = *desc;
+    const ttt_block_norm_params &P = *params;
+    if (!norm_desc_ok(D)) return TTT_ERR_ARG;
+    if ((P.post_bias && D.post != TTT_NORM_LAYER) || (P.post_weight && !D.post) ||
+        (P.pre_bias && D.pre != TTT_NORM_LAYER) || (P.pre_weight && !D.pre))
+        return TTT_ERR_ARG;
+    if (D.D > kNormMaxD || (long long)D.B * D.T > 0x7fffffffLL) return TTT_ERR_UNSUPPORTED;
+    for (const float *v : {P.post_weight, P.post_bias, P.scale, P.pre_weight, P.pre_bias})
+        if (v && !aligned(v, 4)) return TTT_ERR_ALIGN;
+    *empty = D.B == 0 || D.T == 0;
+    const int es = D.io_dtype == TTT_BF16 ? 2 : 4;
+    if (!*empty) {
+        if (!y || (D.act != TTT_GATE_NONE) != (gate != nullptr)) return TTT_ERR_ARG;
+        if (!aligned(y, es) || (x && !aligned(x, es)) || (gate && !aligned(gate, es))) return TTT_ERR_ALIGN;
+    }
+    for (int i = 0; i < 3; ++i)
+        if (D.y_stride[i] < 0) return TTT_ERR_ARG;
+    for (int i = 0; i < 2; ++i)
+        if (D.x_stride[i] < 0 || D.gate_stride[i] < 0 || D.dh_stride[i] < 0 || D.du_stride[i] < 0) return TTT_ERR_ARG;
+    a = {};
+    a.B = D.B;
+    a.T = D.T;
+    a.D = D.D;
+    a.dh = D.D / D.heads;
+    a.bf16 = D.io_dtype == TTT_BF16;
+    a.post = D.post;
+    a.pre = D.pre;
+    a.act = D.act;
+    a.eps1 = D.post_eps;
+    a.eps2 = D.pre_eps;
+    a.alpha = D.alpha;
+    a.y = y;
+    a.x = x;
+    a.gate = gate;
+    // strides of dimensions with one entry, or of absent tensors, say nothing
+    const int n[2] = {D.B, D.T};
+    for (int i = 0; i < 3; ++i) a.ys[i] = (i == 1 ? D.heads : n[i / 2]) > 1 ? D.y_stride[i] : 0;
+    if (D.heads == 1) a.ys[1] = 0;
+    for (int i = 0; i < 2; ++i) {
+        a.xs[i] = x && n[i] > 1 ? D.x_stride[i] : 0;
+        a.gs[i] = gate && n[i] > 1 ? D.gate_stride[i] : 0;
+        a.dhs[i] = n[i] > 1 ? D.dh_stride[i] : 0;
+        a.dus[i] = n[i] > 1 ? D.du_stride[i] : 0;
+    }
+    a.w1 = P.post_weight;
+    a.b1 = P.post_bias;
+    a.scale = P.scale;
+    a.w2 = P.pre_weight;
+    a.b2 = P.pre_bias;
+    a.stream = static_cast<cudaStream_t>(stream);
+    return TTT_OK;
+}
+
+size_t rows_span(const long long st[2], int B, int T, int D, int es)
+{
+    return es * (st[0] * (B - 1) + st[1] * (T - 1) + D);
+}
+
+struct Range {
+    const void *p;
+    size_t n;
+};
+
+// Does any output overlap any input?
+bool clash(const Range *out, int no, const Range *in, int ni)
+{
+    for (int i = 0; i < no; ++i)
+        for (int j = 0; j < ni; ++j)
+            if (out[i].p && in[j].p && overlaps(out[i].p, out[i].n, in[j].p, in[j].n)) return true;
+    return false;
+}
+
+}  // namespace
+
+ttt_status ttt_block_norm_fwd(const ttt_block_norm_desc *desc, const ttt_block_norm_params *params, const void *y,
+                              const void *x, const void *gate, void *h, void *u, float *stats, void *stream)
+{
+    ttt::BlockNormArgs a;
+    bool empty;
+    const ttt_status st = norm_args(desc, params, y, x, gate, stream, a, &empty);
+    if (st != TTT_OK || empty) return st;
+    if (!h || (a.pre != 0) != (u != nullptr)) return TTT_ERR_ARG;
+    const int es = a.bf16 ? 2 : 4;
+    if (!aligned(h, es) || (u && !aligned(u, es)) || (stats && !aligned(stats, 16))) return TTT_ERR_ALIGN;
+    const size_t nt = (size_t)a.B * a.T, n = nt * a.D * es, nd = (size_t)a.D * 4;
+    // h may be x itself: a thread reads its features of a row before it writes them
+    const bool in_place = x == h && (a.T == 1 || a.xs[1] == a.D) && (a.B == 1 || a.xs[0] == (long long)a.T * a.D);
+    const long long ys[3] = {a.ys[0], a.ys[1], a.ys[2]};
+    const Range in[] = {{y, es * (size_t)span(ys, a.B, desc->heads, a.T, a.dh)},
+                        {gate, rows_span(a.gs, a.B, a.T, a.D, es)},
+                        {a.w1, nd}, {a.b1, nd}, {a.scale, nd}, {a.w2, nd}, {a.b2, nd},
+                        {in_place ? nullptr : x, rows_span(a.xs, a.B, a.T, a.D, es)}};
+    const Range out[] = {{h, n}, {u, n}, {stats, nt * 16}}, xr = {x, rows_span(a.xs, a.B, a.T, a.D, es)};
+    if (clash(out, 3, in, 8) || clash(out + 1, 2, &xr, 1) || clash(out, 1, out + 1, 2) || clash(out + 1, 1, out + 2, 1))
+        return TTT_ERR_ARG;
+    a.h = h;
+    a.u = u;
+    a.stats = stats;
+    const int rc = ttt::launch_block_norm_fwd(a);
+    if (rc == 0) g_launches.fetch_add(1, std::memory_order_relaxed);
+    return code(rc);
+}
+
+size_t ttt_block_norm_bwd_workspace(const ttt_block_norm_desc *desc)
+{
+    if (!desc || !norm_desc_ok(*desc) || desc->D > kNormMaxD) return 0;
+    const long long rows = (long long)desc->B * desc->T;
+    return (size_t)ttt::block_norm_bwd_blocks(desc->D, rows) * 5 * desc->D * 4;
+}
+
+ttt_status ttt_block_norm_bwd(const ttt_block_norm_desc *desc, const ttt_block_norm_params *params, const void *dh,
+                              const void *du, const void *y, const void *x, const void *gate, const float *stats,
+                              void *dy, void *dx, void *dgate, const ttt_block_norm_grads *grads, void *workspace,
+                              size_t workspace_bytes, void *stream)
+{
+    ttt::BlockNormArgs a;
+    bool empty;
+    const ttt_status st = norm_args(desc, params, y, x, gate, stream, a, &empty);
+    if (st != TTT_OK) return st;
+    const int es = a.bf16 ? 2 : 4;
+    const size_t nt = (size_t)a.B * a.T, n = nt * a.D * es, nd = (size_t)a.D * 4;
+    int nvec = 0;
+    if (grads) {
+        float *const g[5] = {grads->post_weight, grads->post_bias, grads->scale, grads->pre_weight, grads->pre_bias};
+        // gradients exist for what takes part: a norm's weight and (layer norm) bias, the scale
+        const bool there[5] = {a.post != 0, a.post == 2, true, a.pre != 0, a.pre == 2};
+        for (int i = 0; i < 5; ++i) {
+            if (g[i] && !there[i]) return TTT_ERR_ARG;
+            if (g[i] && !aligned(g[i], 4)) return TTT_ERR_ALIGN;
+            a.dvec[i] = g[i];
+            nvec += g[i] != nullptr;
+        }
+        if (g[2] && !a.scale) return TTT_ERR_ARG;
+    }
+    if (!empty) {
+        if (!dy || !stats || (a.pre != 0) != (du != nullptr) || (!dh && !du)) return TTT_ERR_ARG;
+        if ((gate != nullptr) != (dgate != nullptr) || (dx && !x)) return TTT_ERR_ARG;
+        if (!aligned(stats, 16)) return TTT_ERR_ALIGN;
+        for (const void *q : {dh, du, (const void *)dy, (const void *)dx, (const void *)dgate})
+            if (q && !aligned(q, es)) return TTT_ERR_ALIGN;
+        const size_t need = nvec ? ttt_block_norm_bwd_workspace(desc) : 0;
+        if (need && (!workspace || workspace_bytes < need)) return TTT_ERR_ARG;
+        if (need && !aligned(workspace, 16)) return TTT_ERR_ALIGN;
+        if (!dh) a.dhs[0] = a.dhs[1] = 0;
+        if (!du) a.dus[0] = a.dus[1] = 0;
+        const long long ys[3] = {a.ys[0], a.ys[1], a.ys[2]};
+        const Range in[] = {{y, es * (size_t)span(ys, a.B, desc->heads, a.T, a.dh)},
+                            {gate, rows_span(a.gs, a.B, a.T, a.D, es)},
+                            {x, rows_span(a.xs, a.B, a.T, a.D, es)},
+                            {dh, rows_span(a.dhs, a.B, a.T, a.D, es)},
+                            {du, rows_span(a.dus, a.B, a.T, a.D, es)},
+                            {stats, nt * 16}, {a.w1, nd}, {a.b1, nd}, {a.scale, nd}, {a.w2, nd}, {a.b2, nd}};
+        const Range out[] = {{dy, n}, {dx, n}, {dgate, n}, {need ? workspace : nullptr, need},
+                             {a.dvec[0], nd}, {a.dvec[1], nd}, {a.dvec[2], nd}, {a.dvec[3], nd}, {a.dvec[4], nd}};
+        if (clash(out, 9, in, 11)) return TTT_ERR_ARG;
+        for (int i = 0; i < 9; ++i)
+            if (clash(out + i, 1, out + i + 1, 8 - i)) return TTT_ERR_ARG;
+    }
+    a.dh_in = dh;
+    a.du = du;
+    a.stats = const_cast<float *>(stats);
+    a.dy = dy;
+    a.dx = dx;
+    a.dgate = dgate;
+    a.ws = workspace;
+    if (empty && !nvec) return TTT_OK;
+    const int rc = ttt::launch_block_norm_bwd(a);
+    if (rc == 0) g_launches.fetch_add((empty ? 0 : 1) + (nvec ? 1 : 0), std::memory_order_relaxed);
+    return code(rc);
+}
+
 ttt_status ttt_sync_status(void *stream)
 {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return TTT_ERR_LAUNCH;

@@ -76,6 +76,21 @@ struct RopeArgs {
     cudaStream_t stream;
 };
 
+struct BlockNormArgs {
+    int B, T, D, dh, bf16, post, pre, act;  // dh = D / heads
+    float eps1, eps2, alpha;
+    const void *y, *x, *gate;
+    long long ys[3], xs[2], gs[2], dhs[2], dus[2];
+    const float *w1, *b1, *scale, *w2, *b2;
+    void *h, *u;   // forward
+    float *stats;  // written by the forward, read by the backward
+    const void *dh_in, *du;
+    void *dy, *dx, *dgate;
+    float *dvec[5];  // gradients of w1, b1, scale, w2, b2 (null: not asked for)
+    void *ws;
+    cudaStream_t stream;
+};
+
 // TMA descriptor of a bf16 token tensor viewed as [BH][T][d]: boxes of `rows`
 // tokens x `cols` features (0: min(d, 64)), swizzled to the box row length, rows
 // past T zero-filled on loads and dropped on stores.  Returns false if the driver
@@ -140,6 +155,9 @@ size_t dwconv_smem(int hh, int ww, int d, int es);
 int launch_dwconv(const DwconvArgs &a);
 int launch_eta_gate(const GateArgs &a);  // H <= 64; -2 otherwise
 int launch_rope(const RopeArgs &a);
+int launch_block_norm_fwd(const BlockNormArgs &a);
+int launch_block_norm_bwd(const BlockNormArgs &a);
+int block_norm_bwd_blocks(int D, long long rows);  // partial sums per parameter gradient
 
 // Largest d*m the fp32 MLP path holds on chip.
 bool mlp_f32_fits(int d, int m);

@@ -106,6 +106,9 @@ class _Dev:
     def is_contiguous(self):
         return self.last == 1
 
+    def numel(self):
+        return self.shape.numel()
+
     def data_ptr(self):
         raise AssertionError("the binding reached the library with a bad argument")
 
