@@ -404,6 +404,57 @@ ttt_status ttt_block_norm_bwd(const ttt_block_norm_desc *desc, const ttt_block_n
                               void *dy, void *dx, void *dgate, const ttt_block_norm_grads *grads, void *workspace,
                               size_t workspace_bytes, void *stream);
 
+/* Gate of the recurrence below.
+ *   TTT_RECUR_DECAY:   a = f, c = 1         (f is the decay itself)
+ *   TTT_RECUR_SIGMOID: a = sigma(f), c = 1
+ *   TTT_RECUR_MIX:     a = sigma(f), c = 1 - a */
+typedef enum { TTT_RECUR_DECAY = 0, TTT_RECUR_SIGMOID = 1, TTT_RECUR_MIX = 2 } ttt_recurrence_mode;
+
+/* Tokens from one stored state to the next (ttt_recurrence_fwd's states). */
+#define TTT_RECURRENCE_CHUNK 128
+
+/* Gated linear recurrence problem description.  Strides in elements (batch, token);
+ * channels are contiguous. */
+typedef struct {
+    int B, T, C;               /* batch (<= 65535), tokens, channels                    */
+    ttt_dtype io_dtype;        /* dtype of x, f, h, dh, dx, df                          */
+    int mode;                  /* ttt_recurrence_mode                                   */
+    long long x_stride[2], f_stride[2], dh_stride[2];
+} ttt_recurrence_desc;
+
+/*
+ * Gated linear recurrence, every channel by itself:
+ *     h_t = a_t h_{t-1} + c_t x_t
+ * TTT_RECUR_MIX is the TTT layer whose inner model is a constant, f(k; w) = w, trained
+ * on 1/2 ||w - x_t||^2 by one gradient step a token with the rate 1 - a_t of every
+ * channel (w_t = w_{t-1} - (1 - a_t)(w_{t-1} - x_t)), mini-batches of one token.
+ *   x, f   : [B,T,C] io_dtype
+ *   reset  : [B,T] bytes or NULL; where not zero, h_{t-1} is taken as zero (a packed
+ *            sequence begins), whatever it held
+ *   h0     : [B,C] fp32 start states or NULL (zeros)
+ *   h      : [B,T,C] io_dtype, contiguous
+ *   h_last : [B,C] fp32 or NULL: the last state (h0 when T = 0); may be h0 itself, so
+ *            that a decoder steps its states in place
+ *   states : [B, ceil(T / TTT_RECURRENCE_CHUNK), C] fp32 or NULL: the state before every
+ *            chunk of tokens, which the backward pass reads
+ * States are fp32 throughout; sums run in an order that depends on the sizes only.  Data
+ * pointers: aligned to their element; 16-byte alignment, strides of whole 16 bytes and C a
+ * multiple of 8 move wide vectors.  Outputs may not overlap inputs (h_last as above).
+ */
+ttt_status ttt_recurrence_fwd(const ttt_recurrence_desc *desc, const void *x, const void *f,
+                              const unsigned char *reset, const float *h0, void *h, float *h_last, float *states,
+                              void *stream);
+
+/*
+ * Gradients of ttt_recurrence_fwd from dh [B,T,C] (of h; NULL: zero) and dh_last [B,C]
+ * fp32 (of h_last; NULL: zero), the forward's x, f, reset and the states it stored.
+ *   dx, df : [B,T,C] io_dtype, contiguous (df: of f, the logit or the decay itself)
+ *   dh0    : [B,C] fp32 or NULL
+ */
+ttt_status ttt_recurrence_bwd(const ttt_recurrence_desc *desc, const void *dh, const void *x, const void *f,
+                              const unsigned char *reset, const float *states, const float *dh_last, void *dx,
+                              void *df, float *dh0, void *stream);
+
 /* Waits for `stream`, then reports (and clears) a kernel wait timeout
  * (TTT_ERR_TIMEOUT) or a position out of range (TTT_ERR_RANGE) recorded on the current
  * device, or a CUDA error seen while waiting. */

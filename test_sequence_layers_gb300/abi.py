@@ -25,7 +25,7 @@ STATUS = {0: "TTT_OK", -1: "TTT_ERR_ARG", -2: "TTT_ERR_UNSUPPORTED", -3: "TTT_ER
 EXPORTS = ("ttt_linear_fwd", "ttt_linear_seqpar_workspace", "ttt_linear_fwd_seqpar",
            "ttt_linear_fwd_seqpar_noalloc", "ttt_dwconv_fwd", "ttt_eta_gate",
            "ttt_mlp_fwd", "ttt_rope", "ttt_block_norm_fwd", "ttt_block_norm_bwd_workspace",
-           "ttt_block_norm_bwd", "ttt_sync_status", "ttt_status_str", "ttt_launch_count",
+           "ttt_block_norm_bwd", "ttt_recurrence_fwd", "ttt_recurrence_bwd", "ttt_sync_status", "ttt_status_str", "ttt_launch_count",
            "ttt_debug_wait_limit")
 
 
@@ -83,6 +83,14 @@ NORMS = {"none": 0, "rms": 1, "layer": 2}
 GATES = {"none": 0, "sigmoid": 1, "silu": 2, "gelu": 3}
 
 
+class RecurrenceDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("C", ctypes.c_int), ("io_dtype", ctypes.c_int),
+                ("mode", ctypes.c_int), ("strides", ctypes.c_longlong * 6)]
+
+RECURRENCE_MODES = {"decay": 0, "sigmoid": 1, "mix": 2}
+RECURRENCE_CHUNK = 128
+
+
 class TTTError(RuntimeError):
     def __init__(self, fn, rc):
         self.code = rc
@@ -129,6 +137,10 @@ def lib():
                                          vp, vp, fp, vp, vp, vp, ctypes.POINTER(BlockNormVectors), vp,
                                          ctypes.c_size_t, vp]
         L.ttt_block_norm_bwd.restype = ctypes.c_int
+        L.ttt_recurrence_fwd.argtypes = [ctypes.POINTER(RecurrenceDesc), vp, vp, vp, fp, vp, fp, fp, vp]
+        L.ttt_recurrence_fwd.restype = ctypes.c_int
+        L.ttt_recurrence_bwd.argtypes = [ctypes.POINTER(RecurrenceDesc), vp, vp, vp, vp, fp, fp, vp, vp, fp, vp]
+        L.ttt_recurrence_bwd.restype = ctypes.c_int
         L.ttt_sync_status.argtypes = [vp]
         L.ttt_sync_status.restype = ctypes.c_int
         L.ttt_status_str.argtypes = [ctypes.c_int]
@@ -620,6 +632,71 @@ def ttt_block_norm_bwd_workspace(B, T, D) -> int:
     """Workspace bytes of ttt_block_norm_bwd for B x T tokens of D features."""
     desc = BlockNormDesc(B, T, D, 1, TTT_BF16, 0, 0, 0, 1e-6, 1e-6, 1.0)
     return int(lib().ttt_block_norm_bwd_workspace(desc))
+
+
+def _recurrence_prologue(x, f, mode, reset, dh=None):
+    """Checks of both recurrence wrappers; returns (B, T, C, descriptor)."""
+    _tokens("x", x, 3)
+    B, T, C = x.shape
+    strides = [*x.stride()[:2]]
+    for name, t in (("f", f), ("dh", dh)):
+        if t is None:
+            strides += (0, 0)
+            continue
+        _tokens(name, t, 3, x)
+        if t.shape != x.shape:
+            raise ValueError(f"{name} must be [B,T,C] like x")
+        strides += t.stride()[:2]
+    if reset is not None and (reset.dtype not in (torch.bool, torch.uint8) or reset.device != x.device
+                              or tuple(reset.shape) != (B, T) or not reset.is_contiguous()):
+        raise ValueError("reset must be a contiguous bool or uint8 [B,T] tensor on x's device")
+    return B, T, C, RecurrenceDesc(B, T, C, _IO[x.dtype], RECURRENCE_MODES[mode], (ctypes.c_longlong * 6)(*strides))
+
+
+def ttt_recurrence_fwd(x, f, h0=None, mode="mix", reset=None, h=None, h_last=None, want_states=False, states=None,
+                       stream=None):
+    """Gated linear recurrence h_t = a_t h_{t-1} + c_t x_t of every channel.  x, f: [B,T,C]
+    bf16 or fp32, strided as long as the channels are contiguous.  mode "decay": a = f,
+    c = 1; "sigmoid": a = sigmoid(f), c = 1; "mix": a = sigmoid(f), c = 1 - a.  reset:
+    bool or uint8 [B,T], True where a packed sequence begins (h_{t-1} taken as zero).
+    h0: fp32 [B,C] or None; h_last may be h0 (a decoder's states stepped in place).
+    want_states (or states) for the backward pass.  Returns (h, h_last, states or None)."""
+    B, T, C, desc = _recurrence_prologue(x, f, mode, reset)
+    dev = x.device
+    if h0 is not None:
+        _like("h0", h0, (B, C), torch.float32, dev)
+    h = torch.empty((B, T, C), dtype=x.dtype, device=dev) if h is None else _like("h", h, (B, T, C), x.dtype, dev)
+    if h_last is None:
+        h_last = torch.empty((B, C), dtype=torch.float32, device=dev)
+    else:
+        _like("h_last", h_last, (B, C), torch.float32, dev)
+    shape = (B, -(-T // RECURRENCE_CHUNK), C)
+    if states is not None:
+        _like("states", states, shape, torch.float32, dev)
+    elif want_states:
+        states = torch.empty(shape, dtype=torch.float32, device=dev)
+    _call("ttt_recurrence_fwd", dev, stream, desc, x.data_ptr(), f.data_ptr(), _addr(reset), _addr(h0), h.data_ptr(),
+          h_last.data_ptr(), _addr(states))
+    return h, h_last, states
+
+
+def ttt_recurrence_bwd(dh, x, f, states, mode="mix", reset=None, dh_last=None, dx=None, df=None, dh0=None, stream=None):
+    """Gradients of ttt_recurrence_fwd from dh ([B,T,C] or None) and dh_last (fp32 [B,C]
+    or None), with the forward's inputs and the states it stored.  Returns (dx, df, dh0)."""
+    B, T, C, desc = _recurrence_prologue(x, f, mode, reset, dh)
+    dev = x.device
+    _like("states", states, (B, -(-T // RECURRENCE_CHUNK), C), torch.float32, dev)
+    if dh_last is not None:
+        _like("dh_last", dh_last, (B, C), torch.float32, dev)
+    dx = torch.empty((B, T, C), dtype=x.dtype, device=dev) if dx is None else _like("dx", dx, (B, T, C), x.dtype, dev)
+    df = torch.empty((B, T, C), dtype=x.dtype, device=dev) if df is None else _like("df", df, (B, T, C), x.dtype, dev)
+    if dh0 is None:
+        dh0 = torch.empty((B, C), dtype=torch.float32, device=dev)
+    else:
+        _like("dh0", dh0, (B, C), torch.float32, dev)
+    _call("ttt_recurrence_bwd", dev, stream, desc, _addr(dh), x.data_ptr(), f.data_ptr(), _addr(reset),
+          states.data_ptr(), _addr(dh_last), dx.data_ptr(), df.data_ptr(), dh0.data_ptr())
+    return dx, df, dh0
 
 
 def ttt_sync_status(stream=None):

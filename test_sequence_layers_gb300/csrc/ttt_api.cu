@@ -724,6 +724,118 @@ ttt_status ttt_block_norm_bwd(const ttt_block_norm_desc *desc, const ttt_block_n
     return code(rc);
 }
 
+namespace {
+
+static_assert(ttt::kRecurChunk == TTT_RECURRENCE_CHUNK && ttt::kRecurMix == TTT_RECUR_MIX, "");
+
+ttt_status recurrence_args(const ttt_recurrence_desc *desc, const void *x, const void *f, const unsigned char *reset,
+                           void *stream, ttt::RecurArgs &a)
+{
+    if (!desc) return TTT_ERR_ARG;
+    const ttt_recurrence_desc &D = *desc;
+    if (D.B < 0 || D.T < 0 || D.C < 1 || D.mode < 0 || D.mode > 2) return TTT_ERR_ARG;
+    if (D.io_dtype != TTT_F32 && D.io_dtype != TTT_BF16) return TTT_ERR_ARG;
+    for (int i = 0; i < 2; ++i)
+        if (D.x_stride[i] < 0 || D.f_stride[i] < 0 || D.dh_stride[i] < 0) return TTT_ERR_ARG;
+    if (D.B > 65535) return TTT_ERR_UNSUPPORTED;
+    const int es = D.io_dtype == TTT_BF16 ? 2 : 4;
+    if (D.B > 0 && D.T > 0) {
+        if (!x || !f) return TTT_ERR_ARG;
+        if (!aligned(x, es) || !aligned(f, es)) return TTT_ERR_ALIGN;
+    }
+    a = {};
+    a.B = D.B;
+    a.T = D.T;
+    a.C = D.C;
+    a.bf16 = D.io_dtype == TTT_BF16;
+    a.mode = D.mode;
+    a.x = x;
+    a.f = f;
+    a.reset = reset;
+    const int n[2] = {D.B, D.T};
+    for (int i = 0; i < 2; ++i) {
+        a.xs[i] = n[i] > 1 ? D.x_stride[i] : 0;
+        a.fs[i] = n[i] > 1 ? D.f_stride[i] : 0;
+        a.ds[i] = n[i] > 1 ? D.dh_stride[i] : 0;
+    }
+    a.stream = static_cast<cudaStream_t>(stream);
+    return TTT_OK;
+}
+
+// The first or last state of a call without tokens: dst = src or zeros.
+ttt_status copy_states(float *dst, const float *src, size_t n, cudaStream_t st)
+{
+    if (!dst || dst == src || n == 0) return TTT_OK;
+    const cudaError_t e = src ? cudaMemcpyAsync(dst, src, n * 4, cudaMemcpyDeviceToDevice, st)
+                              : cudaMemsetAsync(dst, 0, n * 4, st);
+    return e == cudaSuccess ? TTT_OK : TTT_ERR_LAUNCH;
+}
+
+}  // namespace
+
+ttt_status ttt_recurrence_fwd(const ttt_recurrence_desc *desc, const void *x, const void *f,
+                              const unsigned char *reset, const float *h0, void *h, float *h_last, float *states,
+                              void *stream)
+{
+    ttt::RecurArgs a;
+    const ttt_status st = recurrence_args(desc, x, f, reset, stream, a);
+    if (st != TTT_OK) return st;
+    if ((h0 && !aligned(h0, 4)) || (h_last && !aligned(h_last, 4)) || (states && !aligned(states, 4))) return TTT_ERR_ALIGN;
+    const size_t nbc = (size_t)a.B * a.C;
+    if (h0 != h_last && h0 && h_last && overlaps(h0, nbc * 4, h_last, nbc * 4)) return TTT_ERR_ARG;
+    if (a.B == 0 || a.T == 0) return copy_states(h_last, h0, nbc, a.stream);
+    const int es = a.bf16 ? 2 : 4;
+    if (!h) return TTT_ERR_ARG;
+    if (!aligned(h, es)) return TTT_ERR_ALIGN;
+    const size_t n = nbc * a.T * es, ns = nbc * ((a.T + ttt::kRecurChunk - 1) / ttt::kRecurChunk) * 4;
+    const Range in[] = {{x, rows_span(a.xs, a.B, a.T, a.C, es)}, {f, rows_span(a.fs, a.B, a.T, a.C, es)},
+                        {reset, (size_t)a.B * a.T}, {h0 == h_last ? nullptr : h0, nbc * 4}};
+    const Range out[] = {{h, n}, {h_last, nbc * 4}, {states, ns}}, start = {h0, nbc * 4};
+    if (clash(out, 3, in, 4) || clash(out, 1, out + 1, 2) || clash(out + 1, 1, out + 2, 1) || clash(out, 1, &start, 1) ||
+        clash(out + 2, 1, &start, 1))
+        return TTT_ERR_ARG;
+    a.h0 = h0;
+    a.h = h;
+    a.h_last = h_last;
+    a.states = states;
+    const int rc = ttt::launch_recurrence(a, false);
+    if (rc == 0) g_launches.fetch_add(1, std::memory_order_relaxed);
+    return code(rc);
+}
+
+ttt_status ttt_recurrence_bwd(const ttt_recurrence_desc *desc, const void *dh, const void *x, const void *f,
+                              const unsigned char *reset, const float *states, const float *dh_last, void *dx,
+                              void *df, float *dh0, void *stream)
+{
+    ttt::RecurArgs a;
+    const ttt_status st = recurrence_args(desc, x, f, reset, stream, a);
+    if (st != TTT_OK) return st;
+    if ((dh_last && !aligned(dh_last, 4)) || (dh0 && !aligned(dh0, 4)) || (states && !aligned(states, 4)))
+        return TTT_ERR_ALIGN;
+    const size_t nbc = (size_t)a.B * a.C;
+    if (dh0 && dh_last && overlaps(dh0, nbc * 4, dh_last, nbc * 4)) return TTT_ERR_ARG;
+    if (a.B == 0 || a.T == 0) return copy_states(dh0, dh_last, nbc, a.stream);
+    const int es = a.bf16 ? 2 : 4;
+    if (!dx || !df || !states) return TTT_ERR_ARG;
+    if (!aligned(dx, es) || !aligned(df, es) || (dh && !aligned(dh, es))) return TTT_ERR_ALIGN;
+    if (!dh) a.ds[0] = a.ds[1] = 0;
+    const size_t n = nbc * a.T * es, ns = nbc * ((a.T + ttt::kRecurChunk - 1) / ttt::kRecurChunk) * 4;
+    const Range in[] = {{x, rows_span(a.xs, a.B, a.T, a.C, es)}, {f, rows_span(a.fs, a.B, a.T, a.C, es)},
+                        {dh, rows_span(a.ds, a.B, a.T, a.C, es)}, {reset, (size_t)a.B * a.T},
+                        {states, ns}, {dh_last, nbc * 4}};
+    const Range out[] = {{dx, n}, {df, n}, {dh0, nbc * 4}};
+    if (clash(out, 3, in, 6) || clash(out, 1, out + 1, 2) || clash(out + 1, 1, out + 2, 1)) return TTT_ERR_ARG;
+    a.dh = dh;
+    a.dh_last = dh_last;
+    a.states = const_cast<float *>(states);
+    a.dx = dx;
+    a.df = df;
+    a.dh0 = dh0;
+    const int rc = ttt::launch_recurrence(a, true);
+    if (rc == 0) g_launches.fetch_add(1, std::memory_order_relaxed);
+    return code(rc);
+}
+
 ttt_status ttt_sync_status(void *stream)
 {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return TTT_ERR_LAUNCH;

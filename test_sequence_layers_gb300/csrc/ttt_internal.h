@@ -91,6 +91,20 @@ struct BlockNormArgs {
     cudaStream_t stream;
 };
 
+constexpr int kRecurDecay = 0, kRecurSigmoid = 1, kRecurMix = 2;
+constexpr int kRecurChunk = 128;  // tokens from one stored state to the next
+
+struct RecurArgs {
+    int B, T, C, bf16, mode;
+    const void *x, *f, *dh;
+    long long xs[2], fs[2], ds[2];
+    const unsigned char *reset;
+    const float *h0, *dh_last;
+    void *h, *dx, *df;
+    float *h_last, *states, *dh0;  // states: written by the forward, read by the backward
+    cudaStream_t stream;
+};
+
 // TMA descriptor of a bf16 token tensor viewed as [BH][T][d]: boxes of `rows`
 // tokens x `cols` features (0: min(d, 64)), swizzled to the box row length, rows
 // past T zero-filled on loads and dropped on stores.  Returns false if the driver
@@ -155,6 +169,7 @@ size_t dwconv_smem(int hh, int ww, int d, int es);
 int launch_dwconv(const DwconvArgs &a);
 int launch_eta_gate(const GateArgs &a);  // H <= 64; -2 otherwise
 int launch_rope(const RopeArgs &a);
+int launch_recurrence(const RecurArgs &a, bool backward);
 int launch_block_norm_fwd(const BlockNormArgs &a);
 int launch_block_norm_bwd(const BlockNormArgs &a);
 int block_norm_bwd_blocks(int D, long long rows);  // partial sums per parameter gradient
