@@ -11,6 +11,7 @@
 // chunks of eight features in fp32 registers, so a row's statistics and its outputs come
 // from one read.  The variance is taken about the mean (each warp's own, joined by the
 // parallel-variance formula), never as a difference of squares.
+#include "ttt_device.cuh"
 #include "ttt_internal.h"
 #include "ttt_vec.cuh"
 
@@ -19,6 +20,27 @@ namespace {
 
 constexpr int kSMs = 152;
 constexpr int kC = 8;  // features of a chunk
+
+// row / T for rows below 2^31: multiply by ceil(2^(32 + shift) / T), keep the high part
+// (Granlund and Montgomery, Division by invariant integers using multiplication).
+struct Div {
+    uint32_t d, mul, shift;
+    __device__ __forceinline__ uint32_t operator()(uint32_t n) const
+    {
+        return d == 1 ? n : __umulhi(n, mul) >> shift;
+    }
+};
+
+Div make_div(int d)
+{
+    Div r = {(uint32_t)d, 0, 0};
+    if (d > 1) {
+        while ((1u << r.shift) < (uint32_t)d) ++r.shift;  // 2^shift >= d, shift >= 1
+        --r.shift;
+        r.mul = (uint32_t)(((1ull << (32 + r.shift)) + d - 1) / d);
+    }
+    return r;
+}
 
 struct Vectors {  // fp32 [D], null: 1 (weights, scale) or 0 (biases)
     const float *w1, *b1, *sc, *w2, *b2;
@@ -30,7 +52,8 @@ struct FwdParams {
     float *stats;
     Vectors v;
     long long ys[3], xs[2], gs[2];
-    long long rows;
+    uint32_t rows;
+    Div byT;
     int T, D, dh, lanes, post, pre, act;
     float eps1, eps2, alpha;
 };
@@ -42,7 +65,8 @@ struct BwdParams {
     float *part;  // [blocks][nvec][D] partial parameter gradients
     Vectors v;
     long long ys[3], xs[2], gs[2], dhs[2], dus[2];
-    long long rows;
+    uint32_t rows;
+    Div byT;
     int T, D, dh, lanes, post, pre, act;
     int slot[5];  // slot of each parameter gradient among the nvec, -1: absent
     int nvec;
@@ -51,135 +75,151 @@ struct BwdParams {
 
 // ------------------------------------------------------------------- activations
 
-// act(g) and its derivative: 0 none, 1 sigmoid, 2 SiLU, 3 GELU (g Phi(g)).
-__device__ __forceinline__ float act_value(int act, float g)
+// act(g) and its derivative: 1 sigmoid, 2 SiLU, 3 GELU (g Phi(g)).  The logistic from
+// exp(-g): past the range of exp it is 0 or 1.  Phi: for bf16 tensors by Abramowitz &
+// Stegun 7.1.26 (|error| <= 1.5e-7, far below the rounding of the output, one exponential
+// shared with the density), for fp32 CUDA's normcdff.
+__device__ __forceinline__ float logistic(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+
+template <typename T> __device__ __forceinline__ float gelu_cdf(float g, float &density)
 {
-    if (act == 0) return 1.f;
-    if (act == 3) return g * normcdff(g);
-    const float s = 1.f / (1.f + __expf(-g));
-    return act == 1 ? s : g * s;
+    float e, c;
+    if constexpr (sizeof(T) == 2) {
+        c = norm_cdf(g, e);
+    } else {
+        c = normcdff(g);
+        e = __expf(-0.5f * g * g);
+    }
+    density = e * 0.3989422804014327f;
+    return c;
 }
 
-__device__ __forceinline__ float act_value(int act, float g, float &deriv)
+// v *= act(g)
+template <typename T> __device__ __forceinline__ void apply_act(int act, const float (&g)[8], float (&v)[8])
 {
-    if (act == 0) {
-        deriv = 0.f;
-        return 1.f;
+    if (act == 2) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= g[j] * logistic(g[j]);
+    } else if (act == 3) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float d;
+            v[j] *= g[j] * gelu_cdf<T>(g[j], d);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= logistic(g[j]);
     }
-    if (act == 3) {
-        const float c = normcdff(g);
-        deriv = fmaf(g * 0.3989422804014327f, __expf(-0.5f * g * g), c);
-        return g * c;
+}
+
+template <typename T> __device__ __forceinline__ void act_and_slope(int act, const float (&g)[8], float (&a)[8], float (&da)[8])
+{
+    if (act == 2) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float s = logistic(g[j]);
+            a[j] = g[j] * s;
+            da[j] = fmaf(a[j], 1.f - s, s);
+        }
+    } else if (act == 3) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float d;
+            const float c = gelu_cdf<T>(g[j], d);
+            a[j] = g[j] * c;
+            da[j] = fmaf(g[j], d, c);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            a[j] = logistic(g[j]);
+            da[j] = a[j] * (1.f - a[j]);
+        }
     }
-    const float s = 1.f / (1.f + __expf(-g));
-    if (act == 1) {
-        deriv = s * (1.f - s);
-        return s;
-    }
-    deriv = s * fmaf(g, 1.f - s, 1.f);
-    return g * s;
 }
 
 // ------------------------------------------------------------------ chunk access
 
-// Eight features of a row: consecutive (VEC) or `lanes` apart, features past D absent.
+// Eight features as they lie in memory.
+template <typename T, bool VEC> struct Raw {
+    static constexpr int V = VEC ? 16 / (int)sizeof(T) : 1, N = kC / V;
+    Pack<T, V> q[N];
+    __device__ __forceinline__ void get(float (&v)[kC]) const
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float w[V];
+            unpack(q[i], w);
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[i * V + j] = w[j];
+        }
+    }
+    __device__ __forceinline__ void put(const float (&v)[kC])
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float w[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) w[j] = v[i * V + j];
+            pack(q[i], w);
+        }
+    }
+};
+
+// Which eight features of a row a thread holds: consecutive ones (VEC) or `lanes` apart;
+// features past D are absent and read as zeros.
 template <typename T, bool VEC> struct Chunk {
+    using R = Raw<T, VEC>;
     int c0, step, D;
     __device__ __forceinline__ Chunk(int r, int k, int lanes, int D_)
         : c0(VEC ? (k * lanes + r) * kC : r + k * kC * lanes), step(VEC ? 1 : lanes), D(D_)
     {
     }
     __device__ __forceinline__ bool has(int j) const { return VEC ? c0 < D : c0 + j * step < D; }
-    // RW: the tensor may also be an output (h written over x)
-    template <bool RW = false> __device__ __forceinline__ void load(const T *row, float (&v)[kC]) const
+    // plain loads: h may be written over x
+    __device__ __forceinline__ void load(const T *row, R &r) const
     {
-        if constexpr (VEC) {
-            constexpr int V = 16 / sizeof(T);
 #pragma unroll
-            for (int i = 0; i < kC; i += V) {
-                float w[V] = {};
-                if (c0 < D) {
-                    Pack<T, V> q;
-                    if (RW) q.load_rw(row + c0 + i);
-                    else q.load(row + c0 + i);
-                    unpack(q, w);
-                }
-#pragma unroll
-                for (int j = 0; j < V; ++j) v[i + j] = w[j];
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < kC; ++j) {
-                float w[1] = {};
-                if (has(j)) {
-                    Pack<T, 1> q;
-                    if (RW) q.load_rw(row + c0 + j * step);
-                    else q.load(row + c0 + j * step);
-                    unpack(q, w);
-                }
-                v[j] = w[0];
-            }
+        for (int i = 0; i < R::N; ++i) {
+            r.q[i].raw = {};
+            if (has(i)) r.q[i].load_rw(row + c0 + i * (VEC ? R::V : step));
         }
     }
     __device__ __forceinline__ void store(T *row, const float (&v)[kC]) const
     {
-        if constexpr (VEC) {
-            constexpr int V = 16 / sizeof(T);
-            if (c0 < D)
+        R r;
+        r.put(v);
 #pragma unroll
-                for (int i = 0; i < kC; i += V) {
-                    float w[V];
-#pragma unroll
-                    for (int j = 0; j < V; ++j) w[j] = v[i + j];
-                    Pack<T, V> q;
-                    pack(q, w);
-                    q.store(row + c0 + i);
-                }
-        } else {
-#pragma unroll
-            for (int j = 0; j < kC; ++j)
-                if (has(j)) {
-                    const float w[1] = {v[j]};
-                    Pack<T, 1> q;
-                    pack(q, w);
-                    q.store(row + c0 + j * step);
-                }
-        }
+        for (int i = 0; i < R::N; ++i)
+            if (has(i)) r.q[i].store(row + c0 + i * (VEC ? R::V : step));
     }
-    // the same through a tensor whose features lie in heads of dh, sh elements apart
-    __device__ __forceinline__ void load_heads(const T *tok, int dh, long long sh, float (&v)[kC]) const
+    // through a tensor whose features lie in heads of dh, sh elements apart; with VEC the
+    // chunk lies inside one head (dh is a multiple of eight) and hoff() is its offset
+    __device__ __forceinline__ long long hoff(int dh, long long sh) const { return (long long)(c0 / dh) * (sh - dh); }
+    __device__ __forceinline__ void load_heads(const T *tok, int dh, long long sh, long long off, R &r) const
     {
         if constexpr (VEC) {
-            // the chunk lies inside one head (dh is a multiple of eight)
-            load(tok + (long long)(c0 / dh) * (sh - dh), v);
+            load(tok + off, r);
         } else {
 #pragma unroll
             for (int j = 0; j < kC; ++j) {
                 const int c = c0 + j * step;
-                float w[1] = {};
-                if (c < D) {
-                    Pack<T, 1> q;
-                    q.load(tok + (long long)(c / dh) * (sh - dh) + c);
-                    unpack(q, w);
-                }
-                v[j] = w[0];
+                r.q[j].raw = {};
+                if (c < D) r.q[j].load_rw(tok + (long long)(c / dh) * (sh - dh) + c);
             }
         }
     }
-    __device__ __forceinline__ void store_heads(T *tok, int dh, long long sh, const float (&v)[kC]) const
+    __device__ __forceinline__ void store_heads(T *tok, int dh, long long sh, long long off, const float (&v)[kC]) const
     {
         if constexpr (VEC) {
-            store(tok + (long long)(c0 / dh) * (sh - dh), v);
+            store(tok + off, v);
         } else {
+            R r;
+            r.put(v);
 #pragma unroll
             for (int j = 0; j < kC; ++j) {
                 const int c = c0 + j * step;
-                if (c < D) {
-                    const float w[1] = {v[j]};
-                    Pack<T, 1> q;
-                    pack(q, w);
-                    q.store(tok + (long long)(c / dh) * (sh - dh) + c);
-                }
+                if (c < D) r.q[j].store(tok + (long long)(c / dh) * (sh - dh) + c);
             }
         }
     }
@@ -329,25 +369,49 @@ __device__ __forceinline__ float2 row_stats(Group<BLOCK> &g, int kind, float eps
 
 // ----------------------------------------------------------------------- forward
 
+// A row's tensors are loaded one row ahead: each register set is refilled for the next
+// row as soon as this row's values are unpacked.
 template <typename T, bool VEC, int K, bool BLOCK>
-__global__ void __launch_bounds__(512) ttt_block_norm_fwd_kernel(const __grid_constant__ FwdParams p)
+__global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(const __grid_constant__ FwdParams p)
 {
     __shared__ GroupShared sh;
     const int lanes = p.lanes, r = BLOCK ? threadIdx.x : threadIdx.x % lanes;
-    const int per = BLOCK ? 1 : blockDim.x / lanes, mine = BLOCK ? 0 : threadIdx.x / lanes;
+    const uint32_t per = BLOCK ? 1 : blockDim.x / lanes, mine = BLOCK ? 0 : threadIdx.x / lanes;
     Group<BLOCK> g = make_group<T, VEC, K, BLOCK>(sh, r, lanes, p.D);
     // a warp's groups leave the loop together: rows past the end are computed, not written
-    const int warp_first = BLOCK ? 0 : (threadIdx.x & ~31) / lanes;
-    for (long long base = (long long)blockIdx.x * per; base + warp_first < p.rows; base += (long long)gridDim.x * per) {
-        const bool live = base + mine < p.rows;
-        const long long row = live ? base + mine : p.rows - 1;
-        const long long b = row / p.T, t = row % p.T;
-        const T *y = static_cast<const T *>(p.y) + b * p.ys[0] + t * p.ys[2];
-        const T *x = static_cast<const T *>(p.x) + b * p.xs[0] + t * p.xs[1];
-        const T *gt = static_cast<const T *>(p.g) + b * p.gs[0] + t * p.gs[1];
-        float v[K][kC], w[kC], q[kC];
+    const uint32_t warp_first = BLOCK ? 0 : (threadIdx.x & ~31u) / lanes;
+    const T *yb = static_cast<const T *>(p.y), *xb = static_cast<const T *>(p.x), *gb = static_cast<const T *>(p.g);
+    long long hoff[K];
 #pragma unroll
-        for (int k = 0; k < K; ++k) Chunk<T, VEC>(r, k, lanes, p.D).load_heads(y, p.dh, p.ys[1], v[k]);
+    for (int k = 0; k < K; ++k) hoff[k] = Chunk<T, VEC>(r, k, lanes, p.D).hoff(p.dh, p.ys[1]);
+    Raw<T, VEC> yr[K], xr[K], gr[K];
+    uint32_t base = blockIdx.x * per;
+    if (base + warp_first >= p.rows) return;
+    uint32_t row = min(base + mine, p.rows - 1), b = p.byT(row), t = row - b * p.T;
+    {
+        const T *y = yb + b * p.ys[0] + t * p.ys[2], *gt = gb + b * p.gs[0] + t * p.gs[1], *x = xb + b * p.xs[0] + t * p.xs[1];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const Chunk<T, VEC> c(r, k, lanes, p.D);
+            c.load_heads(y, p.dh, p.ys[1], hoff[k], yr[k]);
+            if (p.act) c.load(gt, gr[k]);
+            if (xb) c.load(x, xr[k]);
+        }
+    }
+    while (true) {
+        const bool live = base + mine < p.rows;
+        const uint32_t next = base + gridDim.x * per, row0 = row;
+        const bool more = next + warp_first < p.rows;
+        row = min(next + mine, p.rows - 1);
+        b = p.byT(row);
+        t = row - b * p.T;
+        float v[K][kC], w[kC], q[kC];
+        const T *y = yb + b * p.ys[0] + t * p.ys[2], *gt = gb + b * p.gs[0] + t * p.gs[1], *x = xb + b * p.xs[0] + t * p.xs[1];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            yr[k].get(v[k]);
+            if (more) Chunk<T, VEC>(r, k, lanes, p.D).load_heads(y, p.dh, p.ys[1], hoff[k], yr[k]);
+        }
         float2 s1 = make_float2(0.f, 1.f), s2 = make_float2(0.f, 1.f);
         if (p.post) s1 = row_stats<T, VEC, K, BLOCK>(g, p.post, p.eps1, v, r, p.D);
 #pragma unroll
@@ -360,24 +424,25 @@ __global__ void __launch_bounds__(512) ttt_block_norm_fwd_kernel(const __grid_co
                 for (int j = 0; j < kC; ++j) v[k][j] = fmaf((v[k][j] - s1.x) * s1.y, w[j], q[j]);
             }
             if (p.act) {
-                c.load(gt, w);
-#pragma unroll
-                for (int j = 0; j < kC; ++j) v[k][j] *= act_value(p.act, w[j]);
+                gr[k].get(w);
+                if (more) c.load(gt, gr[k]);
+                apply_act<T>(p.act, w, v[k]);
             }
             if (p.v.sc) {
                 c.vec(p.v.sc, 1.f, w);
 #pragma unroll
                 for (int j = 0; j < kC; ++j) v[k][j] *= w[j];
             }
-            if (p.x) {
-                c.template load<true>(x, w);
+            if (xb) {
+                xr[k].get(w);
+                if (more) c.load(x, xr[k]);
 #pragma unroll
                 for (int j = 0; j < kC; ++j) v[k][j] = fmaf(p.alpha, w[j], v[k][j]);
             }
 #pragma unroll
             for (int j = 0; j < kC; ++j)
                 if (!c.has(j)) v[k][j] = 0.f;
-            if (live) c.store(static_cast<T *>(p.h) + row * p.D, v[k]);
+            if (live) c.store(static_cast<T *>(p.h) + (size_t)row0 * p.D, v[k]);
         }
         if (p.pre) {
             // of h in fp32, before the rounding that stores it
@@ -389,11 +454,13 @@ __global__ void __launch_bounds__(512) ttt_block_norm_fwd_kernel(const __grid_co
                 c.vec(p.v.b2, 0.f, q);
 #pragma unroll
                 for (int j = 0; j < kC; ++j) v[k][j] = fmaf((v[k][j] - s2.x) * s2.y, w[j], q[j]);
-                if (live) c.store(static_cast<T *>(p.u) + row * p.D, v[k]);
+                if (live) c.store(static_cast<T *>(p.u) + (size_t)row0 * p.D, v[k]);
             }
         }
         if (p.stats && live && r == 0)
-            *reinterpret_cast<float4 *>(p.stats + 4 * row) = make_float4(s1.x, s1.y, s2.x, s2.y);
+            *reinterpret_cast<float4 *>(p.stats + 4 * (size_t)row0) = make_float4(s1.x, s1.y, s2.x, s2.y);
+        if (!more) break;
+        base = next;
     }
 }
 
@@ -402,15 +469,15 @@ __global__ void __launch_bounds__(512) ttt_block_norm_fwd_kernel(const __grid_co
 // Parameter gradients: every thread sums its own features over the block's rows (K = 1:
 // in registers; K > 1: in shared memory), blocks write partial sums, a second kernel adds
 // those in order.  The result depends on the sizes and the SM count only.
-template <typename T, bool VEC, int K, bool BLOCK>
-__global__ void __launch_bounds__(512) ttt_block_norm_bwd_kernel(const __grid_constant__ BwdParams p)
+template <typename T, bool VEC, int K, bool BLOCK, int MAXT>
+__global__ void __launch_bounds__(MAXT) ttt_block_norm_bwd_kernel(const __grid_constant__ BwdParams p)
 {
     __shared__ GroupShared sh;
     extern __shared__ float accs[];  // K > 1: [nvec][K][8][threads]; K = 1, not BLOCK: [threads][8]
     const int lanes = p.lanes, r = BLOCK ? threadIdx.x : threadIdx.x % lanes;
-    const int per = BLOCK ? 1 : blockDim.x / lanes, mine = BLOCK ? 0 : threadIdx.x / lanes;
+    const uint32_t per = BLOCK ? 1 : blockDim.x / lanes, mine = BLOCK ? 0 : threadIdx.x / lanes;
     Group<BLOCK> g = make_group<T, VEC, K, BLOCK>(sh, r, lanes, p.D);
-    const int warp_first = BLOCK ? 0 : (threadIdx.x & ~31) / lanes;
+    const uint32_t warp_first = BLOCK ? 0 : (threadIdx.x & ~31u) / lanes;
     float acc[K == 1 ? 5 : 1][kC];
 #pragma unroll
     for (int i = 0; i < (K == 1 ? 5 : 1); ++i)
@@ -429,54 +496,84 @@ __global__ void __launch_bounds__(512) ttt_block_norm_bwd_kernel(const __grid_co
         }
     };
     const float inv = 1.f / (float)p.D;
-    for (long long base = (long long)blockIdx.x * per; base + warp_first < p.rows; base += (long long)gridDim.x * per) {
-        const bool live = base + mine < p.rows;
-        const long long row = live ? base + mine : p.rows - 1;
-        const long long b = row / p.T, t = row % p.T;
-        const T *y = static_cast<const T *>(p.y) + b * p.ys[0] + t * p.ys[2];
-        const T *x = static_cast<const T *>(p.x) + b * p.xs[0] + t * p.xs[1];
-        const T *gt = static_cast<const T *>(p.g) + b * p.gs[0] + t * p.gs[1];
-        const T *dhp = static_cast<const T *>(p.dh_in) + b * p.dhs[0] + t * p.dhs[1];
-        const T *dup = static_cast<const T *>(p.du) + b * p.dus[0] + t * p.dus[1];
-        const float4 st = *reinterpret_cast<const float4 *>(p.stats + 4 * row);
-        float yn[K][kC], G[K][kC], w[kC], q[kC];
+    const T *yb = static_cast<const T *>(p.y), *xb = static_cast<const T *>(p.x), *gb = static_cast<const T *>(p.g);
+    const T *dhb = static_cast<const T *>(p.dh_in), *dub = static_cast<const T *>(p.du);
+    long long hoff[K], dyoff[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        hoff[k] = Chunk<T, VEC>(r, k, lanes, p.D).hoff(p.dh, p.ys[1]);
+        dyoff[k] = Chunk<T, VEC>(r, k, lanes, p.D).hoff(p.dh, (long long)p.T * p.dh);
+    }
+    Raw<T, VEC> yr[K], xr[K], gr[K], hr[K], ur[K];
+    float4 sn;
+    uint32_t base = blockIdx.x * per, row = 0, b = 0, t = 0;
+    if (base + warp_first < p.rows) {
+        row = min(base + mine, p.rows - 1);
+        b = p.byT(row);
+        t = row - b * p.T;
+        sn = *reinterpret_cast<const float4 *>(p.stats + 4 * (size_t)row);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            Chunk<T, VEC>(r, k, lanes, p.D).load_heads(y, p.dh, p.ys[1], yn[k]);
+            const Chunk<T, VEC> c(r, k, lanes, p.D);
+            c.load_heads(yb + b * p.ys[0] + t * p.ys[2], p.dh, p.ys[1], hoff[k], yr[k]);
+            if (p.act) c.load(gb + b * p.gs[0] + t * p.gs[1], gr[k]);
+            if (p.pre) {
+                if (xb) c.load(xb + b * p.xs[0] + t * p.xs[1], xr[k]);
+                c.load(dub + b * p.dus[0] + t * p.dus[1], ur[k]);
+            }
+            if (dhb) c.load(dhb + b * p.dhs[0] + t * p.dhs[1], hr[k]);
+        }
+    }
+    for (; base + warp_first < p.rows; base += gridDim.x * per) {
+        const bool live = base + mine < p.rows;
+        const uint32_t row0 = row, b0 = b, t0 = t, next = base + gridDim.x * per;
+        const bool more = next + warp_first < p.rows;
+        const float4 st = sn;
+        if (more) {
+            row = min(next + mine, p.rows - 1);
+            b = p.byT(row);
+            t = row - b * p.T;
+            sn = *reinterpret_cast<const float4 *>(p.stats + 4 * (size_t)row);
+        }
+        float yn[K][kC], A[K][kC], dA[K][kC], hn[K][kC], G[K][kC], pv[kC], w[kC], q[kC];
+        float a = 0.f, c2 = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const Chunk<T, VEC> c(r, k, lanes, p.D);
+            yr[k].get(yn[k]);
+            if (more) c.load_heads(yb + b * p.ys[0] + t * p.ys[2], p.dh, p.ys[1], hoff[k], yr[k]);
 #pragma unroll
             for (int j = 0; j < kC; ++j) yn[k][j] = (yn[k][j] - st.x) * st.y;  // y itself without a post norm
-        }
-        if (p.pre) {
-            // h again from the inputs, its normalised form, and the norm's backward sums
-            float hn[K][kC], a = 0.f, c2 = 0.f;
+            if (p.act) {
+                gr[k].get(w);
+                if (more) c.load(gb + b * p.gs[0] + t * p.gs[1], gr[k]);
+                act_and_slope<T>(p.act, w, A[k], dA[k]);
+            } else {
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const Chunk<T, VEC> c(r, k, lanes, p.D);
-                if (p.post) {
-                    c.vec(p.v.w1, 1.f, w);
-                    c.vec(p.v.b1, 0.f, q);
-#pragma unroll
-                    for (int j = 0; j < kC; ++j) hn[k][j] = fmaf(yn[k][j], w[j], q[j]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < kC; ++j) hn[k][j] = yn[k][j];
+                for (int j = 0; j < kC; ++j) {
+                    A[k][j] = 1.f;
+                    dA[k][j] = 0.f;
                 }
-                if (p.act) {
-                    c.load(gt, w);
+            }
+            if (p.pre) {
+                // h again from the inputs, its normalised form, and the norm's backward sums
+                c.vec(p.v.w1, 1.f, w);
+                c.vec(p.v.b1, 0.f, q);
 #pragma unroll
-                    for (int j = 0; j < kC; ++j) hn[k][j] *= act_value(p.act, w[j]);
-                }
+                for (int j = 0; j < kC; ++j) hn[k][j] = fmaf(yn[k][j], w[j], q[j]) * A[k][j];
                 if (p.v.sc) {
                     c.vec(p.v.sc, 1.f, w);
 #pragma unroll
                     for (int j = 0; j < kC; ++j) hn[k][j] *= w[j];
                 }
-                if (p.x) {
-                    c.load(x, w);
+                if (xb) {
+                    xr[k].get(w);
+                    if (more) c.load(xb + b * p.xs[0] + t * p.xs[1], xr[k]);
 #pragma unroll
                     for (int j = 0; j < kC; ++j) hn[k][j] = fmaf(p.alpha, w[j], hn[k][j]);
                 }
-                c.load(dup, G[k]);
+                ur[k].get(G[k]);
+                if (more) c.load(dub + b * p.dus[0] + t * p.dus[1], ur[k]);
                 c.vec(p.v.w2, 1.f, w);
 #pragma unroll
                 for (int j = 0; j < kC; ++j) {
@@ -494,70 +591,50 @@ __global__ void __launch_bounds__(512) ttt_block_norm_bwd_kernel(const __grid_co
                     c2 = fmaf(G[k][j], hn[k][j], c2);
                 }
             }
-            const float2 m = g.sum2(a, c2);
-            const float ma = p.pre == 2 ? m.x * inv : 0.f, mc = m.y * inv;
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-#pragma unroll
-                for (int j = 0; j < kC; ++j) G[k][j] = st.w * (G[k][j] - ma - hn[k][j] * mc);
-        } else {
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-#pragma unroll
-                for (int j = 0; j < kC; ++j) G[k][j] = 0.f;
         }
-        float a = 0.f, c2 = 0.f;
+        float ma = 0.f, mc = 0.f;
+        if (p.pre) {
+            const float2 m = g.sum2(a, c2);
+            if (p.pre == 2) ma = m.x * inv;
+            mc = m.y * inv;
+        }
+        a = c2 = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const Chunk<T, VEC> c(r, k, lanes, p.D);
-            if (p.dh_in) {
-                c.load(dhp, w);
+#pragma unroll
+            for (int j = 0; j < kC; ++j) G[k][j] = p.pre ? st.w * (G[k][j] - ma - hn[k][j] * mc) : 0.f;
+            if (dhb) {
+                hr[k].get(w);
+                if (more) c.load(dhb + b * p.dhs[0] + t * p.dhs[1], hr[k]);
 #pragma unroll
                 for (int j = 0; j < kC; ++j) G[k][j] += w[j];
             }
             if (p.dx && live) {
 #pragma unroll
                 for (int j = 0; j < kC; ++j) w[j] = p.alpha * G[k][j];
-                c.store(static_cast<T *>(p.dx) + row * p.D, w);
+                c.store(static_cast<T *>(p.dx) + (size_t)row0 * p.D, w);
             }
-            float pv[kC];
-            if (p.post) {
-                c.vec(p.v.w1, 1.f, w);
-                c.vec(p.v.b1, 0.f, q);
+            c.vec(p.v.w1, 1.f, w);
+            c.vec(p.v.b1, 0.f, q);
 #pragma unroll
-                for (int j = 0; j < kC; ++j) pv[j] = fmaf(yn[k][j], w[j], q[j]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < kC; ++j) pv[j] = yn[k][j];
-            }
-            if (p.act) {
-                float A[kC], dA[kC];
-                c.load(gt, w);
-#pragma unroll
-                for (int j = 0; j < kC; ++j) A[j] = act_value(p.act, w[j], dA[j]);
-                if (p.v.sc) {
-                    c.vec(p.v.sc, 1.f, w);
-#pragma unroll
-                    for (int j = 0; j < kC; ++j) {
-                        q[j] = G[k][j] * A[j] * pv[j];
-                        G[k][j] *= w[j];
-                    }
-                    if (live) add(2, k, q);
-                }
-#pragma unroll
-                for (int j = 0; j < kC; ++j) {
-                    q[j] = G[k][j] * pv[j] * dA[j];
-                    G[k][j] *= A[j];
-                }
-                if (live) c.store(static_cast<T *>(p.dg) + row * p.D, q);
-            } else if (p.v.sc) {
+            for (int j = 0; j < kC; ++j) pv[j] = fmaf(yn[k][j], w[j], q[j]);
+            if (p.v.sc) {
                 c.vec(p.v.sc, 1.f, w);
 #pragma unroll
                 for (int j = 0; j < kC; ++j) {
-                    q[j] = G[k][j] * pv[j];
+                    q[j] = G[k][j] * A[k][j] * pv[j];
                     G[k][j] *= w[j];
                 }
                 if (live) add(2, k, q);
+            }
+            if (p.act) {
+#pragma unroll
+                for (int j = 0; j < kC; ++j) {
+                    q[j] = G[k][j] * pv[j] * dA[k][j];
+                    G[k][j] *= A[k][j];
+                }
+                if (live) c.store(static_cast<T *>(p.dg) + (size_t)row0 * p.D, q);
             }
             // G is now dp
             if (p.post) {
@@ -576,20 +653,21 @@ __global__ void __launch_bounds__(512) ttt_block_norm_bwd_kernel(const __grid_co
                 }
             }
         }
-        float ma = 0.f, mc = 0.f;
+        ma = mc = 0.f;
         if (p.post) {
             const float2 m = g.sum2(a, c2);
             if (p.post == 2) ma = m.x * inv;
             mc = m.y * inv;
         }
-        const long long drow = b * (long long)p.T * p.D;  // dy is contiguous in y's own layout
+        // dy is contiguous in y's own layout
+        T *dy = static_cast<T *>(p.dy) + (size_t)b0 * p.T * p.D + (size_t)t0 * p.dh;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const Chunk<T, VEC> c(r, k, lanes, p.D);
             if (p.post)
 #pragma unroll
                 for (int j = 0; j < kC; ++j) G[k][j] = st.y * (G[k][j] - ma - yn[k][j] * mc);
-            if (live) c.store_heads(static_cast<T *>(p.dy) + drow + t * p.dh, p.dh, (long long)p.T * p.dh, G[k]);
+            if (live) c.store_heads(dy, p.dh, (long long)p.T * p.dh, dyoff[k], G[k]);
         }
     }
     if (p.nvec == 0) return;
@@ -656,24 +734,27 @@ __global__ void __launch_bounds__(512) ttt_block_norm_reduce_kernel(const __grid
 
 // ------------------------------------------------------------------------ launch
 
-// Threads of a row and chunks of a thread: part of a warp up to 256 features, then one
-// block a row, eight features a thread, sixteen past 4096.
+// Threads of a row and chunks of a thread.  Forward: part of a warp up to 256 features, a
+// warp with up to four chunks a lane up to 1024 (no barrier), then one block a row.
+// Backward: its sums want few features a thread, so blocks from 256 features on.  Blocks
+// hold one chunk a thread, two past 4096 features.
 struct Shape {
     int lanes, threads, K;
     bool block;
 };
 
-Shape row_shape(int D)
+Shape row_shape(int D, bool wide_warps)
 {
     Shape s;
-    s.block = D > 32 * kC;
-    s.K = D > 512 * kC ? 2 : 1;
+    s.block = D > 32 * kC * (wide_warps ? 4 : 1);
     if (s.block) {
+        s.K = D > 512 * kC ? 2 : 1;
         const int need = (D + kC * s.K - 1) / (kC * s.K);
         s.lanes = s.threads = (need + 31) / 32 * 32;
     } else {
-        s.lanes = 1;
-        while (s.lanes * kC < D) s.lanes *= 2;
+        s.K = (D + 32 * kC - 1) / (32 * kC);
+        s.lanes = s.K > 1 ? 32 : 1;
+        while (s.lanes * kC * s.K < D) s.lanes *= 2;
         s.threads = 128;
     }
     return s;
@@ -703,35 +784,44 @@ bool vector_ok(int es, int D, int dh, const void *const *ptr, int np, const long
 template <typename T, bool VEC>
 void run_fwd(const FwdParams &p, const Shape &s, int blocks, cudaStream_t st)
 {
-    if (!s.block) ttt_block_norm_fwd_kernel<T, VEC, 1, false><<<blocks, s.threads, 0, st>>>(p);
-    else if (s.K == 1) ttt_block_norm_fwd_kernel<T, VEC, 1, true><<<blocks, s.threads, 0, st>>>(p);
-    else ttt_block_norm_fwd_kernel<T, VEC, 2, true><<<blocks, s.threads, 0, st>>>(p);
+    if (s.block) {
+        if (s.K == 1) ttt_block_norm_fwd_kernel<T, VEC, 1, true><<<blocks, s.threads, 0, st>>>(p);
+        else ttt_block_norm_fwd_kernel<T, VEC, 2, true><<<blocks, s.threads, 0, st>>>(p);
+        return;
+    }
+    switch (s.K) {
+    case 1: ttt_block_norm_fwd_kernel<T, VEC, 1, false><<<blocks, s.threads, 0, st>>>(p); break;
+    case 2: ttt_block_norm_fwd_kernel<T, VEC, 2, false><<<blocks, s.threads, 0, st>>>(p); break;
+    case 3: ttt_block_norm_fwd_kernel<T, VEC, 3, false><<<blocks, s.threads, 0, st>>>(p); break;
+    default: ttt_block_norm_fwd_kernel<T, VEC, 4, false><<<blocks, s.threads, 0, st>>>(p); break;
+    }
 }
 
 template <typename T, bool VEC>
 int run_bwd(const BwdParams &p, const Shape &s, int blocks, cudaStream_t st)
 {
     if (!s.block) {
-        ttt_block_norm_bwd_kernel<T, VEC, 1, false><<<blocks, s.threads, s.threads * kC * 4, st>>>(p);
+        ttt_block_norm_bwd_kernel<T, VEC, 1, false, 128><<<blocks, s.threads, s.threads * kC * 4, st>>>(p);
     } else if (s.K == 1) {
-        ttt_block_norm_bwd_kernel<T, VEC, 1, true><<<blocks, s.threads, 0, st>>>(p);
+        if (s.threads <= 256) ttt_block_norm_bwd_kernel<T, VEC, 1, true, 256><<<blocks, s.threads, 0, st>>>(p);
+        else ttt_block_norm_bwd_kernel<T, VEC, 1, true, 512><<<blocks, s.threads, 0, st>>>(p);
     } else {
         const int smem = p.nvec * 2 * kC * s.threads * 4;
-        if (cudaFuncSetAttribute(ttt_block_norm_bwd_kernel<T, VEC, 2, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 5 * 2 * kC * 512 * 4) != cudaSuccess)
+        if (cudaFuncSetAttribute(ttt_block_norm_bwd_kernel<T, VEC, 2, true, 512>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, 5 * 2 * kC * 512 * 4) != cudaSuccess)
             return -4;
-        ttt_block_norm_bwd_kernel<T, VEC, 2, true><<<blocks, s.threads, smem, st>>>(p);
+        ttt_block_norm_bwd_kernel<T, VEC, 2, true, 512><<<blocks, s.threads, smem, st>>>(p);
     }
     return 0;
 }
 
 }  // namespace
 
-int block_norm_bwd_blocks(int D, long long rows) { return grid_blocks(row_shape(D), rows, kBwdThreadsPerSM); }
+int block_norm_bwd_blocks(int D, long long rows) { return grid_blocks(row_shape(D, false), rows, kBwdThreadsPerSM); }
 
 int launch_block_norm_fwd(const BlockNormArgs &a)
 {
-    const Shape s = row_shape(a.D);
+    const Shape s = row_shape(a.D, true);
     FwdParams p;
     p.y = a.y;
     p.x = a.x;
@@ -745,7 +835,8 @@ int launch_block_norm_fwd(const BlockNormArgs &a)
         p.xs[i] = a.xs[i];
         p.gs[i] = a.gs[i];
     }
-    p.rows = (long long)a.B * a.T;
+    p.rows = (uint32_t)((long long)a.B * a.T);
+    p.byT = make_div(a.T > 0 ? a.T : 1);
     p.T = a.T;
     p.D = a.D;
     p.dh = a.dh;
@@ -770,7 +861,7 @@ int launch_block_norm_fwd(const BlockNormArgs &a)
 
 int launch_block_norm_bwd(const BlockNormArgs &a)
 {
-    const Shape s = row_shape(a.D);
+    const Shape s = row_shape(a.D, false);
     BwdParams p;
     p.y = a.y;
     p.x = a.x;
@@ -790,7 +881,8 @@ int launch_block_norm_bwd(const BlockNormArgs &a)
         p.dhs[i] = a.dhs[i];
         p.dus[i] = a.dus[i];
     }
-    p.rows = (long long)a.B * a.T;
+    p.rows = (uint32_t)((long long)a.B * a.T);
+    p.byT = make_div(a.T > 0 ? a.T : 1);
     p.T = a.T;
     p.D = a.D;
     p.dh = a.dh;
