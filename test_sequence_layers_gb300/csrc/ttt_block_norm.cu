@@ -11,7 +11,6 @@
 // chunks of eight features in fp32 registers, so a row's statistics and its outputs come
 // from one read.  The variance is taken about the mean (each warp's own, joined by the
 // parallel-variance formula), never as a difference of squares.
-#include "ttt_device.cuh"
 #include "ttt_internal.h"
 #include "ttt_vec.cuh"
 
@@ -75,65 +74,168 @@ struct BwdParams {
 
 // ------------------------------------------------------------------- activations
 
-// act(g) and its derivative: 1 sigmoid, 2 SiLU, 3 GELU (g Phi(g)).  The logistic from
-// exp(-g): past the range of exp it is 0 or 1.  Phi: for bf16 tensors by Abramowitz &
-// Stegun 7.1.26 (|error| <= 1.5e-7, far below the rounding of the output, one exponential
-// shared with the density), for fp32 CUDA's normcdff.
-__device__ __forceinline__ float logistic(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
-
-template <typename T> __device__ __forceinline__ float gelu_cdf(float g, float &density)
+// Eight features as four pairs: the arithmetic is on paired fp32 instructions, which
+// halves what these kernels are short of, issue slots.
+constexpr int kP = kC / 2;
+struct V8 {
+    float2 p[kP];
+};
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ V8 splat(float v)
 {
-    float e, c;
+    V8 r;
+#pragma unroll
+    for (int i = 0; i < kP; ++i) r.p[i] = both(v);
+    return r;
+}
+__device__ __forceinline__ V8 mul(const V8 &a, const V8 &b)
+{
+    V8 r;
+#pragma unroll
+    for (int i = 0; i < kP; ++i) r.p[i] = __fmul2_rn(a.p[i], b.p[i]);
+    return r;
+}
+__device__ __forceinline__ V8 mul(const V8 &a, float b)
+{
+    V8 r;
+#pragma unroll
+    for (int i = 0; i < kP; ++i) r.p[i] = __fmul2_rn(a.p[i], both(b));
+    return r;
+}
+__device__ __forceinline__ V8 add(const V8 &a, const V8 &b)
+{
+    V8 r;
+#pragma unroll
+    for (int i = 0; i < kP; ++i) r.p[i] = __fadd2_rn(a.p[i], b.p[i]);
+    return r;
+}
+__device__ __forceinline__ V8 fma(const V8 &a, const V8 &b, const V8 &c)
+{
+    V8 r;
+#pragma unroll
+    for (int i = 0; i < kP; ++i) r.p[i] = __ffma2_rn(a.p[i], b.p[i], c.p[i]);
+    return r;
+}
+__device__ __forceinline__ V8 fma(const V8 &a, float b, const V8 &c)
+{
+    V8 r;
+#pragma unroll
+    for (int i = 0; i < kP; ++i) r.p[i] = __ffma2_rn(a.p[i], both(b), c.p[i]);
+    return r;
+}
+// (a - m) r: the difference first, so that what it cancels does not come back scaled
+__device__ __forceinline__ V8 centre(const V8 &a, float m, float r)
+{
+    V8 v;
+#pragma unroll
+    for (int i = 0; i < kP; ++i) v.p[i] = __fmul2_rn(__fadd2_rn(a.p[i], both(-m)), both(r));
+    return v;
+}
+__device__ __forceinline__ float total(const V8 &a)
+{
+    const float2 s = __fadd2_rn(__fadd2_rn(a.p[0], a.p[1]), __fadd2_rn(a.p[2], a.p[3]));
+    return s.x + s.y;
+}
+__device__ __forceinline__ float dot(const V8 &a, const V8 &b)
+{
+    float2 s = __fmul2_rn(a.p[0], b.p[0]);
+#pragma unroll
+    for (int i = 1; i < kP; ++i) s = __ffma2_rn(a.p[i], b.p[i], s);
+    return s.x + s.y;
+}
+
+// ------------------------------------------------------------------- activations
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 1 / (1 + exp(-g)); 0 and 1 where exp(-g) leaves the range
+__device__ __forceinline__ float2 logistic(float2 g)
+{
+    const float2 t = __fmul2_rn(g, both(-1.4426950408889634f));
+    const float2 d = __fadd2_rn(make_float2(exp2_approx(t.x), exp2_approx(t.y)), both(1.f));
+    return make_float2(rcp_approx(d.x), rcp_approx(d.y));
+}
+
+// Phi(g) and the normal density.  For bf16 tensors Phi is 1 - w or w with w =
+// poly(1 / (1 + 0.3275911 |g| / sqrt 2)) exp(-g^2 / 2) / 2 (Abramowitz & Stegun 7.1.26, error
+// below 1e-7, far below the output's rounding; the exponential is the density's too); for
+// fp32 tensors CUDA's normcdff.
+template <typename T> __device__ __forceinline__ float2 gelu_cdf(float2 g, float2 &density)
+{
     if constexpr (sizeof(T) == 2) {
-        c = norm_cdf(g, e);
+        const float2 m = make_float2(fabsf(g.x), fabsf(g.y));
+        const float2 d = __ffma2_rn(m, both(0.3275911f * 0.70710678118654752f), both(1.f));
+        const float2 t = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+        const float2 q = __fmul2_rn(__fmul2_rn(g, g), both(-0.5f * 1.4426950408889634f));
+        const float2 e = make_float2(exp2_approx(q.x), exp2_approx(q.y));
+        float2 w = __ffma2_rn(t, both(0.5f * 1.061405429f), both(-0.5f * 1.453152027f));
+        w = __ffma2_rn(t, w, both(0.5f * 1.421413741f));
+        w = __ffma2_rn(t, w, both(-0.5f * 0.284496736f));
+        w = __ffma2_rn(t, w, both(0.5f * 0.254829592f));
+        w = __fmul2_rn(__fmul2_rn(t, w), e);
+        density = __fmul2_rn(e, both(0.3989422804014327f));
+        const float2 h = __ffma2_rn(w, both(-1.f), both(0.5f));
+        return __fadd2_rn(make_float2(copysignf(h.x, g.x), copysignf(h.y, g.y)), both(0.5f));
     } else {
-        c = normcdff(g);
-        e = __expf(-0.5f * g * g);
-    }
-    density = e * 0.3989422804014327f;
-    return c;
-}
-
-// v *= act(g)
-template <typename T> __device__ __forceinline__ void apply_act(int act, const float (&g)[8], float (&v)[8])
-{
-    if (act == 2) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= g[j] * logistic(g[j]);
-    } else if (act == 3) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float d;
-            v[j] *= g[j] * gelu_cdf<T>(g[j], d);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= logistic(g[j]);
+        density = make_float2(expf(-0.5f * g.x * g.x) * 0.3989422804014327f, expf(-0.5f * g.y * g.y) * 0.3989422804014327f);
+        return make_float2(normcdff(g.x), normcdff(g.y));
     }
 }
 
-template <typename T> __device__ __forceinline__ void act_and_slope(int act, const float (&g)[8], float (&a)[8], float (&da)[8])
+// act(g): 1 sigmoid, 2 SiLU, 3 GELU (g Phi(g))
+template <typename T> __device__ __forceinline__ V8 act_value(int act, const V8 &g)
 {
+    V8 r;
     if (act == 2) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float s = logistic(g[j]);
-            a[j] = g[j] * s;
-            da[j] = fmaf(a[j], 1.f - s, s);
-        }
+        for (int i = 0; i < kP; ++i) r.p[i] = __fmul2_rn(g.p[i], logistic(g.p[i]));
     } else if (act == 3) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float d;
-            const float c = gelu_cdf<T>(g[j], d);
-            a[j] = g[j] * c;
-            da[j] = fmaf(g[j], d, c);
+        for (int i = 0; i < kP; ++i) {
+            float2 d;
+            r.p[i] = __fmul2_rn(g.p[i], gelu_cdf<T>(g.p[i], d));
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            a[j] = logistic(g[j]);
-            da[j] = a[j] * (1.f - a[j]);
+        for (int i = 0; i < kP; ++i) r.p[i] = logistic(g.p[i]);
+    }
+    return r;
+}
+
+// act(g) and its derivative
+template <typename T> __device__ __forceinline__ void act_and_slope(int act, const V8 &g, V8 &a, V8 &da)
+{
+    if (act == 2) {
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+            const float2 s = logistic(g.p[i]);
+            a.p[i] = __fmul2_rn(g.p[i], s);
+            da.p[i] = __ffma2_rn(a.p[i], __ffma2_rn(s, both(-1.f), both(1.f)), s);
+        }
+    } else if (act == 3) {
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+            float2 d;
+            const float2 c = gelu_cdf<T>(g.p[i], d);
+            a.p[i] = __fmul2_rn(g.p[i], c);
+            da.p[i] = __ffma2_rn(g.p[i], d, c);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+            a.p[i] = logistic(g.p[i]);
+            da.p[i] = __fmul2_rn(a.p[i], __ffma2_rn(a.p[i], both(-1.f), both(1.f)));
         }
     }
 }
@@ -144,8 +246,10 @@ template <typename T> __device__ __forceinline__ void act_and_slope(int act, con
 template <typename T, bool VEC> struct Raw {
     static constexpr int V = VEC ? 16 / (int)sizeof(T) : 1, N = kC / V;
     Pack<T, V> q[N];
-    __device__ __forceinline__ void get(float (&v)[kC]) const
+    __device__ __forceinline__ V8 get() const
     {
+        V8 r;
+        float *v = &r.p[0].x;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             float w[V];
@@ -153,9 +257,11 @@ template <typename T, bool VEC> struct Raw {
 #pragma unroll
             for (int j = 0; j < V; ++j) v[i * V + j] = w[j];
         }
+        return r;
     }
-    __device__ __forceinline__ void put(const float (&v)[kC])
+    __device__ __forceinline__ void put(const V8 &r)
     {
+        const float *v = &r.p[0].x;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             float w[V];
@@ -176,16 +282,23 @@ template <typename T, bool VEC> struct Chunk {
     {
     }
     __device__ __forceinline__ bool has(int j) const { return VEC ? c0 < D : c0 + j * step < D; }
-    // plain loads: h may be written over x
+    // zeros in the absent features
+    __device__ __forceinline__ void mask(V8 &v) const
+    {
+        float *f = &v.p[0].x;
+#pragma unroll
+        for (int j = 0; j < kC; ++j) f[j] = has(j) ? f[j] : 0.f;
+    }
+    // not through the read-only path: h may be written over x
     __device__ __forceinline__ void load(const T *row, R &r) const
     {
 #pragma unroll
         for (int i = 0; i < R::N; ++i) {
             r.q[i].raw = {};
-            if (has(i)) r.q[i].load_rw(row + c0 + i * (VEC ? R::V : step));
+            if (has(i)) r.q[i].load_once(row + c0 + i * (VEC ? R::V : step));
         }
     }
-    __device__ __forceinline__ void store(T *row, const float (&v)[kC]) const
+    __device__ __forceinline__ void store(T *row, const V8 &v) const
     {
         R r;
         r.put(v);
@@ -209,7 +322,7 @@ template <typename T, bool VEC> struct Chunk {
             }
         }
     }
-    __device__ __forceinline__ void store_heads(T *tok, int dh, long long sh, long long off, const float (&v)[kC]) const
+    __device__ __forceinline__ void store_heads(T *tok, int dh, long long sh, long long off, const V8 &v) const
     {
         if constexpr (VEC) {
             store(tok + off, v);
@@ -223,27 +336,32 @@ template <typename T, bool VEC> struct Chunk {
             }
         }
     }
-    // a parameter vector (or its default)
-    __device__ __forceinline__ void vec(const float *p, float none, float (&v)[kC]) const
+    // a parameter vector
+    __device__ __forceinline__ V8 vec(const float *p) const
     {
-#pragma unroll
-        for (int j = 0; j < kC; ++j) v[j] = none;
-        if (!p) return;
+        V8 r = {};
         if constexpr (VEC) {
             if (c0 < D)
 #pragma unroll
-                for (int j = 0; j < kC; j += 4) {
-                    const float4 w = __ldg(reinterpret_cast<const float4 *>(p + c0 + j));
-                    v[j] = w.x;
-                    v[j + 1] = w.y;
-                    v[j + 2] = w.z;
-                    v[j + 3] = w.w;
+                for (int j = 0; j < kP; j += 2) {
+                    const float4 w = __ldg(reinterpret_cast<const float4 *>(p + c0 + 2 * j));
+                    r.p[j] = make_float2(w.x, w.y);
+                    r.p[j + 1] = make_float2(w.z, w.w);
                 }
         } else {
+            float *v = &r.p[0].x;
 #pragma unroll
             for (int j = 0; j < kC; ++j)
                 if (has(j)) v[j] = __ldg(p + c0 + j * step);
         }
+        return r;
+    }
+    // v w + b with parameter vectors that may be absent
+    __device__ __forceinline__ V8 scale_shift(const V8 &v, const float *w, const float *b) const
+    {
+        if (w && b) return fma(v, vec(w), vec(b));
+        if (w) return mul(v, vec(w));
+        return b ? add(v, vec(b)) : v;
     }
 };
 
@@ -252,119 +370,88 @@ template <typename T, bool VEC> struct Chunk {
 // Sums over a row's group of threads.  BLOCK: over the block, through two shared slots
 // used in turn (a slot is written again only after the next reduction's barrier).
 template <bool BLOCK> struct Group {
-    int lanes, nw, turn;
-    float2 (*red)[32];
-    float n;          // features held by this warp's (or group's) threads
-    const float *nb;  // BLOCK: that count for every warp
+    int lanes, half_nw, turn;
+    float4 (*red)[16];  // pairs of two warps
 
     __device__ __forceinline__ float warp_sum(float v) const
     {
         for (int o = (BLOCK ? 32 : lanes) >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         return v;
     }
-    __device__ __forceinline__ float2 *post(float a, float b)
-    {
-        float2 *q = red[turn];
-        if ((threadIdx.x & 31) == 0) q[threadIdx.x >> 5] = make_float2(a, b);
-        __syncthreads();
-        turn ^= 1;
-        return q;
-    }
     __device__ __forceinline__ float2 sum2(float a, float b)
     {
         a = warp_sum(a);
         b = warp_sum(b);
+        float2 s = make_float2(a, b);
         if constexpr (BLOCK) {
-            const float2 *q = post(a, b);
-            a = b = 0.f;
-            for (int i = 0; i < nw; ++i) {
-                a += q[i].x;
-                b += q[i].y;
+            float4 *q = red[turn];
+            if ((threadIdx.x & 31) == 0) reinterpret_cast<float2 *>(q)[threadIdx.x >> 5] = s;
+            __syncthreads();
+            turn ^= 1;
+            s = make_float2(0.f, 0.f);
+            for (int i = 0; i < half_nw; ++i) {
+                const float4 w = q[i];
+                s = __fadd2_rn(s, __fadd2_rn(make_float2(w.x, w.y), make_float2(w.z, w.w)));
             }
         }
-        return make_float2(a, b);
+        return s;
     }
-    // mean of the row and mean square about it; s: this thread's sum, dev(m): its sum of
-    // squares about m
-    template <typename F> __device__ __forceinline__ float2 moments(float s, int D, F dev)
+    __device__ __forceinline__ float sum1(float a)
     {
-        float mean = warp_sum(s) / n;
-        float m2 = warp_sum(dev(mean));
+        a = warp_sum(a);
         if constexpr (BLOCK) {
-            const float2 *q = post(mean, m2);
-            mean = m2 = 0.f;
-            for (int i = 0; i < nw; ++i) mean = fmaf(nb[i], q[i].x, mean);
-            mean /= (float)D;
-            for (int i = 0; i < nw; ++i) {
-                const float d = q[i].x - mean;
-                m2 += fmaf(nb[i] * d, d, q[i].y);
-            }
+            float2 *q = reinterpret_cast<float2 *>(red[turn]);  // one number a warp
+            if ((threadIdx.x & 31) == 0) reinterpret_cast<float *>(q)[threadIdx.x >> 5] = a;
+            __syncthreads();
+            turn ^= 1;
+            a = 0.f;
+            for (int i = 0; i < half_nw; ++i) a += q[i].x + q[i].y;
         }
-        return make_float2(mean, m2 / (float)D);
+        return a;
     }
 };
 
 struct GroupShared {
-    float2 red[2][32];
-    float nb[32];
+    float4 red[2][16];
 };
 
-template <typename T, bool VEC, int K, bool BLOCK>
-__device__ __forceinline__ Group<BLOCK> make_group(GroupShared &sh, int r, int lanes, int D)
+template <bool BLOCK> __device__ __forceinline__ Group<BLOCK> make_group(GroupShared &sh, int lanes)
 {
-    int n = 0;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const Chunk<T, VEC> c(r, k, lanes, D);
-#pragma unroll
-        for (int j = 0; j < kC; ++j) n += c.has(j);
-    }
     Group<BLOCK> g;
     g.lanes = lanes;
-    g.nw = (blockDim.x + 31) >> 5;
     g.turn = 0;
     g.red = sh.red;
-    g.nb = sh.nb;
-    for (int o = (BLOCK ? 32 : lanes) >> 1; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    g.n = (float)max(n, 1);  // a warp without features: mean 0 with weight 0
-    if constexpr (BLOCK) {
-        if ((threadIdx.x & 31) == 0) sh.nb[threadIdx.x >> 5] = (float)n;
+    g.half_nw = ((int)((blockDim.x + 31) >> 5) + 1) >> 1;
+    if constexpr (BLOCK) {  // an odd number of warps: the missing one's slot stays zero
+        for (int i = threadIdx.x; i < 32; i += blockDim.x) (&sh.red[0][0])[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         __syncthreads();
     }
     return g;
 }
 
-// mean and 1 / sqrt(.. + eps) of a row held as v[K][8] (absent features are zeros)
+// mean and 1 / sqrt(.. + eps) of a row held as v[K] (absent features are zeros)
 template <typename T, bool VEC, int K, bool BLOCK>
-__device__ __forceinline__ float2 row_stats(Group<BLOCK> &g, int kind, float eps, const float (&v)[K][kC], int r, int D)
+__device__ __forceinline__ float2 row_stats(Group<BLOCK> &g, int kind, float eps, float inv, const V8 (&v)[K], int r, int D)
 {
-    if (kind == 1) {
-        float s = 0.f;
+    float mean = 0.f, s = 0.f;
+    if (kind == 2) {
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-            for (int j = 0; j < kC; ++j) s = fmaf(v[k][j], v[k][j], s);
-        return make_float2(0.f, rsqrtf(g.sum2(s, 0.f).x / (float)D + eps));
-    }
-    float s = 0.f;
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int j = 0; j < kC; ++j) s += v[k][j];
-    const float2 m = g.moments(s, D, [&](float mean) {
-        float q = 0.f;
+        for (int k = 0; k < K; ++k) s += total(v[k]);
+        mean = g.sum1(s) * inv;
+        s = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const Chunk<T, VEC> c(r, k, g.lanes, D);
-#pragma unroll
-            for (int j = 0; j < kC; ++j) {
-                const float d = v[k][j] - mean;
-                if (c.has(j)) q = fmaf(d, d, q);
-            }
+            V8 d = add(v[k], splat(-mean));
+            if constexpr (!VEC) c.mask(d);
+            const float q = dot(d, d);
+            s += !VEC || c.has(0) ? q : 0.f;
         }
-        return q;
-    });
-    return make_float2(m.x, rsqrtf(m.y + eps));
+    } else {
+#pragma unroll
+        for (int k = 0; k < K; ++k) s += dot(v[k], v[k]);
+    }
+    return make_float2(mean, rsqrtf(g.sum1(s) * inv + eps));
 }
 
 // ----------------------------------------------------------------------- forward
@@ -377,10 +464,11 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(c
     __shared__ GroupShared sh;
     const int lanes = p.lanes, r = BLOCK ? threadIdx.x : threadIdx.x % lanes;
     const uint32_t per = BLOCK ? 1 : blockDim.x / lanes, mine = BLOCK ? 0 : threadIdx.x / lanes;
-    Group<BLOCK> g = make_group<T, VEC, K, BLOCK>(sh, r, lanes, p.D);
+    Group<BLOCK> g = make_group<BLOCK>(sh, lanes);
     // a warp's groups leave the loop together: rows past the end are computed, not written
     const uint32_t warp_first = BLOCK ? 0 : (threadIdx.x & ~31u) / lanes;
     const T *yb = static_cast<const T *>(p.y), *xb = static_cast<const T *>(p.x), *gb = static_cast<const T *>(p.g);
+    const float inv = 1.f / (float)p.D;
     long long hoff[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) hoff[k] = Chunk<T, VEC>(r, k, lanes, p.D).hoff(p.dh, p.ys[1]);
@@ -405,55 +493,39 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(c
         row = min(next + mine, p.rows - 1);
         b = p.byT(row);
         t = row - b * p.T;
-        float v[K][kC], w[kC], q[kC];
+        V8 v[K];
         const T *y = yb + b * p.ys[0] + t * p.ys[2], *gt = gb + b * p.gs[0] + t * p.gs[1], *x = xb + b * p.xs[0] + t * p.xs[1];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            yr[k].get(v[k]);
+            v[k] = yr[k].get();
             if (more) Chunk<T, VEC>(r, k, lanes, p.D).load_heads(y, p.dh, p.ys[1], hoff[k], yr[k]);
         }
         float2 s1 = make_float2(0.f, 1.f), s2 = make_float2(0.f, 1.f);
-        if (p.post) s1 = row_stats<T, VEC, K, BLOCK>(g, p.post, p.eps1, v, r, p.D);
+        if (p.post) s1 = row_stats<T, VEC, K, BLOCK>(g, p.post, p.eps1, inv, v, r, p.D);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const Chunk<T, VEC> c(r, k, lanes, p.D);
-            if (p.post) {
-                c.vec(p.v.w1, 1.f, w);
-                c.vec(p.v.b1, 0.f, q);
-#pragma unroll
-                for (int j = 0; j < kC; ++j) v[k][j] = fmaf((v[k][j] - s1.x) * s1.y, w[j], q[j]);
-            }
+            if (p.post) v[k] = c.scale_shift(centre(v[k], s1.x, s1.y), p.v.w1, p.v.b1);
             if (p.act) {
-                gr[k].get(w);
+                const V8 w = gr[k].get();
                 if (more) c.load(gt, gr[k]);
-                apply_act<T>(p.act, w, v[k]);
+                v[k] = mul(v[k], act_value<T>(p.act, w));
             }
-            if (p.v.sc) {
-                c.vec(p.v.sc, 1.f, w);
-#pragma unroll
-                for (int j = 0; j < kC; ++j) v[k][j] *= w[j];
-            }
+            if (p.v.sc) v[k] = mul(v[k], c.vec(p.v.sc));
             if (xb) {
-                xr[k].get(w);
+                v[k] = fma(xr[k].get(), p.alpha, v[k]);
                 if (more) c.load(x, xr[k]);
-#pragma unroll
-                for (int j = 0; j < kC; ++j) v[k][j] = fmaf(p.alpha, w[j], v[k][j]);
             }
-#pragma unroll
-            for (int j = 0; j < kC; ++j)
-                if (!c.has(j)) v[k][j] = 0.f;
             if (live) c.store(static_cast<T *>(p.h) + (size_t)row0 * p.D, v[k]);
+            if (!VEC || !c.has(0)) c.mask(v[k]);
         }
         if (p.pre) {
             // of h in fp32, before the rounding that stores it
-            s2 = row_stats<T, VEC, K, BLOCK>(g, p.pre, p.eps2, v, r, p.D);
+            s2 = row_stats<T, VEC, K, BLOCK>(g, p.pre, p.eps2, inv, v, r, p.D);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 const Chunk<T, VEC> c(r, k, lanes, p.D);
-                c.vec(p.v.w2, 1.f, w);
-                c.vec(p.v.b2, 0.f, q);
-#pragma unroll
-                for (int j = 0; j < kC; ++j) v[k][j] = fmaf((v[k][j] - s2.x) * s2.y, w[j], q[j]);
+                v[k] = c.scale_shift(centre(v[k], s2.x, s2.y), p.v.w2, p.v.b2);
                 if (live) c.store(static_cast<T *>(p.u) + (size_t)row0 * p.D, v[k]);
             }
         }
@@ -470,31 +542,34 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(c
 // in registers; K > 1: in shared memory), blocks write partial sums, a second kernel adds
 // those in order.  The result depends on the sizes and the SM count only.
 template <typename T, bool VEC, int K, bool BLOCK, int MAXT>
-__global__ void __launch_bounds__(MAXT) ttt_block_norm_bwd_kernel(const __grid_constant__ BwdParams p)
+__global__ void __launch_bounds__(MAXT, 512 / MAXT) ttt_block_norm_bwd_kernel(const __grid_constant__ BwdParams p)
 {
     __shared__ GroupShared sh;
-    extern __shared__ float accs[];  // K > 1: [nvec][K][8][threads]; K = 1, not BLOCK: [threads][8]
+    extern __shared__ float2 accs[];  // K > 1: [nvec][K][4][threads]; K = 1, not BLOCK: [4][threads]
     const int lanes = p.lanes, r = BLOCK ? threadIdx.x : threadIdx.x % lanes;
     const uint32_t per = BLOCK ? 1 : blockDim.x / lanes, mine = BLOCK ? 0 : threadIdx.x / lanes;
-    Group<BLOCK> g = make_group<T, VEC, K, BLOCK>(sh, r, lanes, p.D);
+    Group<BLOCK> g = make_group<BLOCK>(sh, lanes);
     const uint32_t warp_first = BLOCK ? 0 : (threadIdx.x & ~31u) / lanes;
-    float acc[K == 1 ? 5 : 1][kC];
+    V8 acc[K == 1 ? 5 : 1];
 #pragma unroll
-    for (int i = 0; i < (K == 1 ? 5 : 1); ++i)
-#pragma unroll
-        for (int j = 0; j < kC; ++j) acc[i][j] = 0.f;
-    if constexpr (K > 1)
-        for (int i = threadIdx.x; i < p.nvec * K * kC * (int)blockDim.x; i += blockDim.x) accs[i] = 0.f;
-    __syncthreads();
-    auto add = [&](int which, int k, const float (&v)[kC]) {
+    for (int i = 0; i < (K == 1 ? 5 : 1); ++i) acc[i] = splat(0.f);
+    if constexpr (K > 1) {
+        for (int i = threadIdx.x; i < p.nvec * K * kP * (int)blockDim.x; i += blockDim.x) accs[i] = make_float2(0.f, 0.f);
+        __syncthreads();
+    }
+    // += a b
+    auto add_to = [&](int which, int k, const V8 &x, const V8 &y) {
         if constexpr (K == 1) {
-#pragma unroll
-            for (int j = 0; j < kC; ++j) acc[which][j] += v[j];
+            acc[which] = fma(x, y, acc[which]);
         } else if (p.slot[which] >= 0) {
 #pragma unroll
-            for (int j = 0; j < kC; ++j) accs[((p.slot[which] * K + k) * kC + j) * blockDim.x + threadIdx.x] += v[j];
+            for (int i = 0; i < kP; ++i) {
+                float2 &s = accs[((p.slot[which] * K + k) * kP + i) * blockDim.x + threadIdx.x];
+                s = __ffma2_rn(x.p[i], y.p[i], s);
+            }
         }
     };
+    const V8 one = splat(1.f);
     const float inv = 1.f / (float)p.D;
     const T *yb = static_cast<const T *>(p.y), *xb = static_cast<const T *>(p.x), *gb = static_cast<const T *>(p.g);
     const T *dhb = static_cast<const T *>(p.dh_in), *dub = static_cast<const T *>(p.du);
@@ -535,61 +610,39 @@ __global__ void __launch_bounds__(MAXT) ttt_block_norm_bwd_kernel(const __grid_c
             t = row - b * p.T;
             sn = *reinterpret_cast<const float4 *>(p.stats + 4 * (size_t)row);
         }
-        float yn[K][kC], A[K][kC], dA[K][kC], hn[K][kC], G[K][kC], pv[kC], w[kC], q[kC];
+        V8 yn[K], A[K], dA[K], hn[K], G[K];
         float a = 0.f, c2 = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const Chunk<T, VEC> c(r, k, lanes, p.D);
-            yr[k].get(yn[k]);
+            yn[k] = centre(yr[k].get(), st.x, st.y);  // y itself without a post norm
             if (more) c.load_heads(yb + b * p.ys[0] + t * p.ys[2], p.dh, p.ys[1], hoff[k], yr[k]);
-#pragma unroll
-            for (int j = 0; j < kC; ++j) yn[k][j] = (yn[k][j] - st.x) * st.y;  // y itself without a post norm
+            if (!VEC || !c.has(0)) c.mask(yn[k]);
             if (p.act) {
-                gr[k].get(w);
+                const V8 w = gr[k].get();
                 if (more) c.load(gb + b * p.gs[0] + t * p.gs[1], gr[k]);
                 act_and_slope<T>(p.act, w, A[k], dA[k]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < kC; ++j) {
-                    A[k][j] = 1.f;
-                    dA[k][j] = 0.f;
-                }
             }
             if (p.pre) {
                 // h again from the inputs, its normalised form, and the norm's backward sums
-                c.vec(p.v.w1, 1.f, w);
-                c.vec(p.v.b1, 0.f, q);
-#pragma unroll
-                for (int j = 0; j < kC; ++j) hn[k][j] = fmaf(yn[k][j], w[j], q[j]) * A[k][j];
-                if (p.v.sc) {
-                    c.vec(p.v.sc, 1.f, w);
-#pragma unroll
-                    for (int j = 0; j < kC; ++j) hn[k][j] *= w[j];
-                }
+                V8 h = c.scale_shift(yn[k], p.v.w1, p.v.b1);
+                if (p.act) h = mul(h, A[k]);
+                if (p.v.sc) h = mul(h, c.vec(p.v.sc));
                 if (xb) {
-                    xr[k].get(w);
+                    h = fma(xr[k].get(), p.alpha, h);
                     if (more) c.load(xb + b * p.xs[0] + t * p.xs[1], xr[k]);
-#pragma unroll
-                    for (int j = 0; j < kC; ++j) hn[k][j] = fmaf(p.alpha, w[j], hn[k][j]);
                 }
-                ur[k].get(G[k]);
+                hn[k] = centre(h, st.z, st.w);
+                if (!VEC || !c.has(0)) c.mask(hn[k]);
+                G[k] = ur[k].get();
                 if (more) c.load(dub + b * p.dus[0] + t * p.dus[1], ur[k]);
-                c.vec(p.v.w2, 1.f, w);
-#pragma unroll
-                for (int j = 0; j < kC; ++j) {
-                    hn[k][j] = c.has(j) ? (hn[k][j] - st.z) * st.w : 0.f;
-                    q[j] = G[k][j] * hn[k][j];
-                }
                 if (live) {
-                    add(3, k, q);
-                    add(4, k, G[k]);
+                    add_to(3, k, G[k], hn[k]);
+                    add_to(4, k, G[k], one);
                 }
-#pragma unroll
-                for (int j = 0; j < kC; ++j) {
-                    G[k][j] *= w[j];
-                    a += G[k][j];
-                    c2 = fmaf(G[k][j], hn[k][j], c2);
-                }
+                if (p.v.w2) G[k] = mul(G[k], c.vec(p.v.w2));
+                a += total(G[k]);
+                c2 += dot(G[k], hn[k]);
             }
         }
         float ma = 0.f, mc = 0.f;
@@ -602,55 +655,36 @@ __global__ void __launch_bounds__(MAXT) ttt_block_norm_bwd_kernel(const __grid_c
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const Chunk<T, VEC> c(r, k, lanes, p.D);
-#pragma unroll
-            for (int j = 0; j < kC; ++j) G[k][j] = p.pre ? st.w * (G[k][j] - ma - hn[k][j] * mc) : 0.f;
+            // G = dh + r (dn - mean(dn) - n mean(dn n))
+            if (p.pre) {
+                G[k] = centre(fma(hn[k], -mc, G[k]), ma, st.w);
+            } else {
+                G[k] = splat(0.f);
+            }
             if (dhb) {
-                hr[k].get(w);
+                G[k] = add(G[k], hr[k].get());
                 if (more) c.load(dhb + b * p.dhs[0] + t * p.dhs[1], hr[k]);
-#pragma unroll
-                for (int j = 0; j < kC; ++j) G[k][j] += w[j];
             }
-            if (p.dx && live) {
-#pragma unroll
-                for (int j = 0; j < kC; ++j) w[j] = p.alpha * G[k][j];
-                c.store(static_cast<T *>(p.dx) + (size_t)row0 * p.D, w);
-            }
-            c.vec(p.v.w1, 1.f, w);
-            c.vec(p.v.b1, 0.f, q);
-#pragma unroll
-            for (int j = 0; j < kC; ++j) pv[j] = fmaf(yn[k][j], w[j], q[j]);
+            if (p.dx && live) c.store(static_cast<T *>(p.dx) + (size_t)row0 * p.D, mul(G[k], p.alpha));
+            V8 pv = c.scale_shift(yn[k], p.v.w1, p.v.b1);
             if (p.v.sc) {
-                c.vec(p.v.sc, 1.f, w);
-#pragma unroll
-                for (int j = 0; j < kC; ++j) {
-                    q[j] = G[k][j] * A[k][j] * pv[j];
-                    G[k][j] *= w[j];
-                }
-                if (live) add(2, k, q);
+                if (live) add_to(2, k, p.act ? mul(G[k], A[k]) : G[k], pv);
+                G[k] = mul(G[k], c.vec(p.v.sc));
             }
             if (p.act) {
-#pragma unroll
-                for (int j = 0; j < kC; ++j) {
-                    q[j] = G[k][j] * pv[j] * dA[k][j];
-                    G[k][j] *= A[k][j];
-                }
-                if (live) c.store(static_cast<T *>(p.dg) + (size_t)row0 * p.D, q);
+                if (live) c.store(static_cast<T *>(p.dg) + (size_t)row0 * p.D, mul(mul(G[k], pv), dA[k]));
+                G[k] = mul(G[k], A[k]);
             }
             // G is now dp
             if (p.post) {
-#pragma unroll
-                for (int j = 0; j < kC; ++j) q[j] = c.has(j) ? G[k][j] * yn[k][j] : 0.f;
                 if (live) {
-                    add(0, k, q);
-                    add(1, k, G[k]);
+                    add_to(0, k, G[k], yn[k]);
+                    add_to(1, k, G[k], one);
                 }
-                c.vec(p.v.w1, 1.f, w);
-#pragma unroll
-                for (int j = 0; j < kC; ++j) {
-                    G[k][j] = c.has(j) ? G[k][j] * w[j] : 0.f;
-                    a += G[k][j];
-                    c2 = fmaf(G[k][j], yn[k][j], c2);
-                }
+                if (p.v.w1) G[k] = mul(G[k], c.vec(p.v.w1));
+                if (!VEC || !c.has(0)) c.mask(G[k]);
+                a += total(G[k]);
+                c2 += dot(G[k], yn[k]);
             }
         }
         ma = mc = 0.f;
@@ -664,9 +698,7 @@ __global__ void __launch_bounds__(MAXT) ttt_block_norm_bwd_kernel(const __grid_c
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const Chunk<T, VEC> c(r, k, lanes, p.D);
-            if (p.post)
-#pragma unroll
-                for (int j = 0; j < kC; ++j) G[k][j] = st.y * (G[k][j] - ma - yn[k][j] * mc);
+            if (p.post) G[k] = centre(fma(yn[k], -mc, G[k]), ma, st.y);
             if (live) c.store_heads(dy, p.dh, (long long)p.T * p.dh, dyoff[k], G[k]);
         }
     }
@@ -679,30 +711,30 @@ __global__ void __launch_bounds__(MAXT) ttt_block_norm_bwd_kernel(const __grid_c
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const Chunk<T, VEC> c(r, k, lanes, p.D);
-            float s[kC];
+            V8 s;
             if constexpr (K > 1) {
 #pragma unroll
-                for (int j = 0; j < kC; ++j) s[j] = accs[((p.slot[i] * K + k) * kC + j) * blockDim.x + threadIdx.x];
+                for (int j = 0; j < kP; ++j) s.p[j] = accs[((p.slot[i] * K + k) * kP + j) * blockDim.x + threadIdx.x];
             } else if constexpr (BLOCK) {
-#pragma unroll
-                for (int j = 0; j < kC; ++j) s[j] = acc[i][j];
+                s = acc[i];
             } else {
                 // the block's row groups, added in order
 #pragma unroll
-                for (int j = 0; j < kC; ++j) accs[j * blockDim.x + threadIdx.x] = acc[i][j];
+                for (int j = 0; j < kP; ++j) accs[j * blockDim.x + threadIdx.x] = acc[i].p[j];
                 __syncthreads();
+                s = splat(0.f);
+                if (mine == 0)
 #pragma unroll
-                for (int j = 0; j < kC; ++j) {
-                    s[j] = 0.f;
-                    if (mine == 0)
-                        for (int m = 0; m < per; ++m) s[j] += accs[j * blockDim.x + m * lanes + r];
-                }
+                    for (int j = 0; j < kP; ++j)
+                        for (uint32_t m = 0; m < per; ++m)
+                            s.p[j] = __fadd2_rn(s.p[j], accs[j * blockDim.x + m * lanes + r]);
                 __syncthreads();
             }
+            const float *f = &s.p[0].x;
             if (mine == 0)
 #pragma unroll
                 for (int j = 0; j < kC; ++j)
-                    if (c.has(j)) part[(size_t)p.slot[i] * p.D + c.c0 + j * c.step] = s[j];
+                    if (c.has(j)) part[(size_t)p.slot[i] * p.D + c.c0 + j * c.step] = f[j];
         }
     }
 }

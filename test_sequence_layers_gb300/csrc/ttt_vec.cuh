@@ -26,6 +26,17 @@ template <typename T, int V> struct Pack {
     __device__ __forceinline__ void load(const T *p) { raw = __ldg(reinterpret_cast<const Raw *>(p)); }
     // a plain load: for data the same kernel also writes (in-place operation)
     __device__ __forceinline__ void load_rw(const T *p) { raw = *reinterpret_cast<const Raw *>(p); }
+    // data read once: kept out of L1, where it would evict what is read again
+    __device__ __forceinline__ void load_once(const T *p)
+    {
+        if constexpr (sizeof(Raw) == 16)
+            asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(raw.x), "=r"(raw.y), "=r"(raw.z), "=r"(raw.w)
+                         : "l"(p)
+                         : "memory");
+        else
+            raw = *reinterpret_cast<const Raw *>(p);
+    }
     __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<Raw *>(p) = raw; }
 };
 
