@@ -242,23 +242,10 @@ template <typename T> __device__ __forceinline__ void act_and_slope(int act, con
 
 // ------------------------------------------------------------------ chunk access
 
-// Eight features as they lie in memory.
+// Eight features in the I/O type, for storing.
 template <typename T, bool VEC> struct Raw {
     static constexpr int V = VEC ? 16 / (int)sizeof(T) : 1, N = kC / V;
     Pack<T, V> q[N];
-    __device__ __forceinline__ V8 get() const
-    {
-        V8 r;
-        float *v = &r.p[0].x;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float w[V];
-            unpack(q[i], w);
-#pragma unroll
-            for (int j = 0; j < V; ++j) v[i * V + j] = w[j];
-        }
-        return r;
-    }
     __device__ __forceinline__ void put(const V8 &r)
     {
         const float *v = &r.p[0].x;
@@ -274,8 +261,20 @@ template <typename T, bool VEC> struct Raw {
 
 // Which eight features of a row a thread holds: consecutive ones (VEC) or `lanes` apart;
 // features past D are absent and read as zeros.
-template <typename T, bool VEC> struct Chunk {
+//
+// A row comes through shared memory: fetch() starts copies of the thread's own eight
+// features, get() reads them back once they have landed.  Only the thread itself reads
+// what it copied, so there is no barrier, and no load waits in a register.  slot: the
+// thread's place in a stage, 16-byte units `pitch` apart.  Where the copies do not go
+// (DIRECT: bf16 rows that are not 16-byte aligned, as copies are 4 bytes at least, and
+// widths whose sums leave no room for stages) the slot holds the row's address and get()
+// loads.
+template <typename T, bool VEC, bool DIRECT = (!VEC && sizeof(T) == 2)> struct Chunk {
     using R = Raw<T, VEC>;
+    static constexpr int kUnits = DIRECT ? 1 : kC * (int)sizeof(T) / 16;  // 16-byte units of a chunk
+    // rows in flight or landed: enough to cover the latency, few enough to leave room for
+    // the blocks of an SM
+    static constexpr int kAhead = DIRECT ? 1 : sizeof(T) == 2 ? 3 : 2;
     int c0, step, D;
     __device__ __forceinline__ Chunk(int r, int k, int lanes, int D_)
         : c0(VEC ? (k * lanes + r) * kC : r + k * kC * lanes), step(VEC ? 1 : lanes), D(D_)
@@ -289,14 +288,65 @@ template <typename T, bool VEC> struct Chunk {
 #pragma unroll
         for (int j = 0; j < kC; ++j) f[j] = has(j) ? f[j] : 0.f;
     }
-    // not through the read-only path: h may be written over x
-    __device__ __forceinline__ void load(const T *row, R &r) const
+    // row: the token's first feature; dh, sh: features of a head and elements from one head
+    // to the next (dh = D: no heads).  With VEC a chunk lies inside one head and off =
+    // hoff() is what its head adds.
+    __device__ __forceinline__ long long hoff(int dh, long long sh) const { return (long long)(c0 / dh) * (sh - dh); }
+    __device__ __forceinline__ void fetch(const T *row, int dh, long long sh, long long off, uint4 *slot, int pitch) const
     {
+        if constexpr (DIRECT) {
+            *reinterpret_cast<const T **>(slot) = row;
+        } else if constexpr (VEC) {
+            if (c0 < D)
 #pragma unroll
-        for (int i = 0; i < R::N; ++i) {
-            r.q[i].raw = {};
-            if (has(i)) r.q[i].load_once(row + c0 + i * (VEC ? R::V : step));
+                for (int i = 0; i < kUnits; ++i) copy_async16(slot + i * pitch, row + off + c0 + i * (16 / (int)sizeof(T)));
+        } else {
+#pragma unroll
+            for (int j = 0; j < kC; ++j) {
+                const int c = c0 + j * step;
+                if (c < D)
+                    copy_async4(reinterpret_cast<float *>(slot + j / 4 * pitch) + j % 4,
+                                row + (dh < D ? (long long)(c / dh) * (sh - dh) : 0) + c);
+            }
         }
+    }
+    __device__ __forceinline__ V8 get(const uint4 *slot, int pitch, int dh, long long sh, long long off) const
+    {
+        constexpr int V = 16 / (int)sizeof(T);
+        V8 r = {};
+        float *v = &r.p[0].x;
+        if constexpr (!DIRECT || VEC) {
+            const T *row = DIRECT ? *reinterpret_cast<const T *const *>(slot) + off + c0 : nullptr;
+#pragma unroll
+            for (int i = 0; i < kC / V; ++i) {
+                Pack<T, V> q;
+                if constexpr (DIRECT) {
+                    q.raw = {};
+                    if (c0 < D) q.load_rw(row + i * V);
+                } else {
+                    q.raw = slot[i * pitch];
+                }
+                float w[V];
+                unpack(q, w);
+#pragma unroll
+                for (int j = 0; j < V; ++j) v[i * V + j] = w[j];
+            }
+            if (!DIRECT && (!VEC || c0 >= D)) mask(r);  // nothing was copied there
+        } else {
+            const T *row = *reinterpret_cast<const T *const *>(slot);
+#pragma unroll
+            for (int j = 0; j < kC; ++j) {
+                const int c = c0 + j * step;
+                if (c < D) {
+                    Pack<T, 1> q;
+                    float w[1];
+                    q.load_rw(row + (dh < D ? (long long)(c / dh) * (sh - dh) : 0) + c);
+                    unpack(q, w);
+                    v[j] = w[0];
+                }
+            }
+        }
+        return r;
     }
     __device__ __forceinline__ void store(T *row, const V8 &v) const
     {
@@ -305,22 +355,6 @@ template <typename T, bool VEC> struct Chunk {
 #pragma unroll
         for (int i = 0; i < R::N; ++i)
             if (has(i)) r.q[i].store(row + c0 + i * (VEC ? R::V : step));
-    }
-    // through a tensor whose features lie in heads of dh, sh elements apart; with VEC the
-    // chunk lies inside one head (dh is a multiple of eight) and hoff() is its offset
-    __device__ __forceinline__ long long hoff(int dh, long long sh) const { return (long long)(c0 / dh) * (sh - dh); }
-    __device__ __forceinline__ void load_heads(const T *tok, int dh, long long sh, long long off, R &r) const
-    {
-        if constexpr (VEC) {
-            load(tok + off, r);
-        } else {
-#pragma unroll
-            for (int j = 0; j < kC; ++j) {
-                const int c = c0 + j * step;
-                r.q[j].raw = {};
-                if (c < D) r.q[j].load_rw(tok + (long long)(c / dh) * (sh - dh) + c);
-            }
-        }
     }
     __device__ __forceinline__ void store_heads(T *tok, int dh, long long sh, long long off, const V8 &v) const
     {
@@ -456,83 +490,78 @@ __device__ __forceinline__ float2 row_stats(Group<BLOCK> &g, int kind, float eps
 
 // ----------------------------------------------------------------------- forward
 
-// A row's tensors are loaded one row ahead: each register set is refilled for the next
-// row as soon as this row's values are unpacked.
+// The rows' tensors are copied kAhead rows ahead into the thread's ring of stages.
 template <typename T, bool VEC, int K, bool BLOCK>
 __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(const __grid_constant__ FwdParams p)
 {
+    using C = Chunk<T, VEC>;
+    constexpr int kAhead = C::kAhead;
     __shared__ GroupShared sh;
-    const int lanes = p.lanes, r = BLOCK ? threadIdx.x : threadIdx.x % lanes;
+    extern __shared__ uint4 stages[];  // [kAhead][3][K][units][threads]
+    const int lanes = p.lanes, r = BLOCK ? threadIdx.x : threadIdx.x % lanes, pitch = blockDim.x;
     const uint32_t per = BLOCK ? 1 : blockDim.x / lanes, mine = BLOCK ? 0 : threadIdx.x / lanes;
     Group<BLOCK> g = make_group<BLOCK>(sh, lanes);
     // a warp's groups leave the loop together: rows past the end are computed, not written
     const uint32_t warp_first = BLOCK ? 0 : (threadIdx.x & ~31u) / lanes;
     const T *yb = static_cast<const T *>(p.y), *xb = static_cast<const T *>(p.x), *gb = static_cast<const T *>(p.g);
     const float inv = 1.f / (float)p.D;
+    const uint32_t stride = gridDim.x * per;
     long long hoff[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) hoff[k] = Chunk<T, VEC>(r, k, lanes, p.D).hoff(p.dh, p.ys[1]);
-    Raw<T, VEC> yr[K], xr[K], gr[K];
+    for (int k = 0; k < K; ++k) hoff[k] = C(r, k, lanes, p.D).hoff(p.dh, p.ys[1]);
+    auto slot = [&](int stage, int tensor, int k) {
+        return stages + ((stage * 3 + tensor) * K + k) * C::kUnits * pitch + threadIdx.x;
+    };
+    auto fetch = [&](uint32_t base, int stage) {
+        if (base + warp_first < p.rows) {
+            const uint32_t row = min(base + mine, p.rows - 1), b = p.byT(row), t = row - b * p.T;
+            const T *y = yb + b * p.ys[0] + t * p.ys[2];
+            const T *gt = gb + b * p.gs[0] + t * p.gs[1], *x = xb + b * p.xs[0] + t * p.xs[1];
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const C c(r, k, lanes, p.D);
+                c.fetch(y, p.dh, p.ys[1], hoff[k], slot(stage, 0, k), pitch);
+                if (p.act) c.fetch(gt, p.D, 0, 0, slot(stage, 1, k), pitch);
+                if (xb) c.fetch(x, p.D, 0, 0, slot(stage, 2, k), pitch);
+            }
+        }
+        copy_commit();
+    };
     uint32_t base = blockIdx.x * per;
-    if (base + warp_first >= p.rows) return;
-    uint32_t row = min(base + mine, p.rows - 1), b = p.byT(row), t = row - b * p.T;
-    {
-        const T *y = yb + b * p.ys[0] + t * p.ys[2], *gt = gb + b * p.gs[0] + t * p.gs[1], *x = xb + b * p.xs[0] + t * p.xs[1];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const Chunk<T, VEC> c(r, k, lanes, p.D);
-            c.load_heads(y, p.dh, p.ys[1], hoff[k], yr[k]);
-            if (p.act) c.load(gt, gr[k]);
-            if (xb) c.load(x, xr[k]);
-        }
-    }
-    while (true) {
+    for (int i = 0; i < kAhead; ++i) fetch(base + i * stride, i);
+    for (int stage = 0; base + warp_first < p.rows; base += stride, stage = stage + 1 == kAhead ? 0 : stage + 1) {
         const bool live = base + mine < p.rows;
-        const uint32_t next = base + gridDim.x * per, row0 = row;
-        const bool more = next + warp_first < p.rows;
-        row = min(next + mine, p.rows - 1);
-        b = p.byT(row);
-        t = row - b * p.T;
+        const uint32_t row = min(base + mine, p.rows - 1);
+        copy_wait<kAhead - 1>();
         V8 v[K];
-        const T *y = yb + b * p.ys[0] + t * p.ys[2], *gt = gb + b * p.gs[0] + t * p.gs[1], *x = xb + b * p.xs[0] + t * p.xs[1];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            v[k] = yr[k].get();
-            if (more) Chunk<T, VEC>(r, k, lanes, p.D).load_heads(y, p.dh, p.ys[1], hoff[k], yr[k]);
-        }
+        for (int k = 0; k < K; ++k) v[k] = C(r, k, lanes, p.D).get(slot(stage, 0, k), pitch, p.dh, p.ys[1], hoff[k]);
         float2 s1 = make_float2(0.f, 1.f), s2 = make_float2(0.f, 1.f);
         if (p.post) s1 = row_stats<T, VEC, K, BLOCK>(g, p.post, p.eps1, inv, v, r, p.D);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const Chunk<T, VEC> c(r, k, lanes, p.D);
+            const C c(r, k, lanes, p.D);
             if (p.post) v[k] = c.scale_shift(centre(v[k], s1.x, s1.y), p.v.w1, p.v.b1);
-            if (p.act) {
-                const V8 w = gr[k].get();
-                if (more) c.load(gt, gr[k]);
-                v[k] = mul(v[k], act_value<T>(p.act, w));
-            }
+            if (p.act) v[k] = mul(v[k], act_value<T>(p.act, c.get(slot(stage, 1, k), pitch, p.D, 0, 0)));
             if (p.v.sc) v[k] = mul(v[k], c.vec(p.v.sc));
-            if (xb) {
-                v[k] = fma(xr[k].get(), p.alpha, v[k]);
-                if (more) c.load(x, xr[k]);
-            }
-            if (live) c.store(static_cast<T *>(p.h) + (size_t)row0 * p.D, v[k]);
+            if (xb) v[k] = fma(c.get(slot(stage, 2, k), pitch, p.D, 0, 0), p.alpha, v[k]);
+            if (live) c.store(static_cast<T *>(p.h) + (size_t)row * p.D, v[k]);
             if (!VEC || !c.has(0)) c.mask(v[k]);
         }
+        fetch(base + kAhead * stride, stage);
         if (p.pre) {
             // of h in fp32, before the rounding that stores it
             s2 = row_stats<T, VEC, K, BLOCK>(g, p.pre, p.eps2, inv, v, r, p.D);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const Chunk<T, VEC> c(r, k, lanes, p.D);
+                const C c(r, k, lanes, p.D);
                 v[k] = c.scale_shift(centre(v[k], s2.x, s2.y), p.v.w2, p.v.b2);
-                if (live) c.store(static_cast<T *>(p.u) + (size_t)row0 * p.D, v[k]);
+                if (live) c.store(static_cast<T *>(p.u) + (size_t)row * p.D, v[k]);
             }
         }
         if (p.stats && live && r == 0)
-            *reinterpret_cast<float4 *>(p.stats + 4 * (size_t)row0) = make_float4(s1.x, s1.y, s2.x, s2.y);
-        if (!more) break;
-        base = next;
+            *reinterpret_cast<float4 *>(p.stats + 4 * (size_t)row) = make_float4(s1.x, s1.y, s2.x, s2.y);
     }
 }
 
@@ -545,8 +574,14 @@ template <typename T, bool VEC, int K, bool BLOCK, int MAXT>
 __global__ void __launch_bounds__(MAXT, 512 / MAXT) ttt_block_norm_bwd_kernel(const __grid_constant__ BwdParams p)
 {
     __shared__ GroupShared sh;
-    extern __shared__ float2 accs[];  // K > 1: [nvec][K][4][threads]; K = 1, not BLOCK: [4][threads]
-    const int lanes = p.lanes, r = BLOCK ? threadIdx.x : threadIdx.x % lanes;
+    constexpr bool DIRECT = K > 1 || (!VEC && sizeof(T) == 2);
+    using C = Chunk<T, VEC, DIRECT>;
+    constexpr int kAhead = C::kAhead;
+    extern __shared__ uint4 stages[];  // [kAhead][5 units + 1][threads], then the sums:
+    // K > 1: [nvec][K][4][threads]; K = 1, not BLOCK: [4][threads]
+    constexpr int kStage = 5 * C::kUnits + 1;
+    float2 *accs = reinterpret_cast<float2 *>(stages + kAhead * kStage * blockDim.x);
+    const int lanes = p.lanes, r = BLOCK ? threadIdx.x : threadIdx.x % lanes, pitch = blockDim.x;
     const uint32_t per = BLOCK ? 1 : blockDim.x / lanes, mine = BLOCK ? 0 : threadIdx.x / lanes;
     Group<BLOCK> g = make_group<BLOCK>(sh, lanes);
     const uint32_t warp_first = BLOCK ? 0 : (threadIdx.x & ~31u) / lanes;
@@ -576,66 +611,59 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) ttt_block_norm_bwd_kernel(co
     long long hoff[K], dyoff[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        hoff[k] = Chunk<T, VEC>(r, k, lanes, p.D).hoff(p.dh, p.ys[1]);
-        dyoff[k] = Chunk<T, VEC>(r, k, lanes, p.D).hoff(p.dh, (long long)p.T * p.dh);
+        hoff[k] = C(r, k, lanes, p.D).hoff(p.dh, p.ys[1]);
+        dyoff[k] = C(r, k, lanes, p.D).hoff(p.dh, (long long)p.T * p.dh);
     }
-    Raw<T, VEC> yr[K], xr[K], gr[K], hr[K], ur[K];
-    float4 sn;
-    uint32_t base = blockIdx.x * per, row = 0, b = 0, t = 0;
-    if (base + warp_first < p.rows) {
-        row = min(base + mine, p.rows - 1);
-        b = p.byT(row);
-        t = row - b * p.T;
-        sn = *reinterpret_cast<const float4 *>(p.stats + 4 * (size_t)row);
+    const uint32_t stride = gridDim.x * per;
+    // K > 1 keeps addresses, which the chunks of a row share
+    auto slot = [&](int stage, int tensor, int) {
+        return stages + (stage * kStage + tensor * C::kUnits) * pitch + threadIdx.x;
+    };
+    auto fetch = [&](uint32_t base, int stage) {
+        if (base + warp_first < p.rows) {
+            const uint32_t row = min(base + mine, p.rows - 1), b = p.byT(row), t = row - b * p.T;
+            copy_async16(slot(stage, 5, 0), p.stats + 4 * (size_t)row);
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const Chunk<T, VEC> c(r, k, lanes, p.D);
-            c.load_heads(yb + b * p.ys[0] + t * p.ys[2], p.dh, p.ys[1], hoff[k], yr[k]);
-            if (p.act) c.load(gb + b * p.gs[0] + t * p.gs[1], gr[k]);
-            if (p.pre) {
-                if (xb) c.load(xb + b * p.xs[0] + t * p.xs[1], xr[k]);
-                c.load(dub + b * p.dus[0] + t * p.dus[1], ur[k]);
+            for (int k = 0; k < K; ++k) {
+                const C c(r, k, lanes, p.D);
+                c.fetch(yb + b * p.ys[0] + t * p.ys[2], p.dh, p.ys[1], hoff[k], slot(stage, 0, k), pitch);
+                if (p.act) c.fetch(gb + b * p.gs[0] + t * p.gs[1], p.D, 0, 0, slot(stage, 1, k), pitch);
+                if (p.pre) {
+                    if (xb) c.fetch(xb + b * p.xs[0] + t * p.xs[1], p.D, 0, 0, slot(stage, 2, k), pitch);
+                    c.fetch(dub + b * p.dus[0] + t * p.dus[1], p.D, 0, 0, slot(stage, 3, k), pitch);
+                }
+                if (dhb) c.fetch(dhb + b * p.dhs[0] + t * p.dhs[1], p.D, 0, 0, slot(stage, 4, k), pitch);
             }
-            if (dhb) c.load(dhb + b * p.dhs[0] + t * p.dhs[1], hr[k]);
         }
-    }
-    for (; base + warp_first < p.rows; base += gridDim.x * per) {
+        copy_commit();
+    };
+    uint32_t base = blockIdx.x * per;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch(base + i * stride, i);
+    for (int stage = 0; base + warp_first < p.rows; base += stride, stage = stage + 1 == kAhead ? 0 : stage + 1) {
         const bool live = base + mine < p.rows;
-        const uint32_t row0 = row, b0 = b, t0 = t, next = base + gridDim.x * per;
-        const bool more = next + warp_first < p.rows;
-        const float4 st = sn;
-        if (more) {
-            row = min(next + mine, p.rows - 1);
-            b = p.byT(row);
-            t = row - b * p.T;
-            sn = *reinterpret_cast<const float4 *>(p.stats + 4 * (size_t)row);
-        }
+        const uint32_t row = min(base + mine, p.rows - 1);
+        copy_wait<kAhead - 1>();
+        const float4 st = *reinterpret_cast<const float4 *>(slot(stage, 5, 0));
         V8 yn[K], A[K], dA[K], hn[K], G[K];
         float a = 0.f, c2 = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const Chunk<T, VEC> c(r, k, lanes, p.D);
-            yn[k] = centre(yr[k].get(), st.x, st.y);  // y itself without a post norm
-            if (more) c.load_heads(yb + b * p.ys[0] + t * p.ys[2], p.dh, p.ys[1], hoff[k], yr[k]);
+            const C c(r, k, lanes, p.D);
+            yn[k] = centre(c.get(slot(stage, 0, k), pitch, p.dh, p.ys[1], hoff[k]), st.x, st.y);  // y itself without a post norm
             if (!VEC || !c.has(0)) c.mask(yn[k]);
             if (p.act) {
-                const V8 w = gr[k].get();
-                if (more) c.load(gb + b * p.gs[0] + t * p.gs[1], gr[k]);
-                act_and_slope<T>(p.act, w, A[k], dA[k]);
+                act_and_slope<T>(p.act, c.get(slot(stage, 1, k), pitch, p.D, 0, 0), A[k], dA[k]);
             }
             if (p.pre) {
                 // h again from the inputs, its normalised form, and the norm's backward sums
                 V8 h = c.scale_shift(yn[k], p.v.w1, p.v.b1);
                 if (p.act) h = mul(h, A[k]);
                 if (p.v.sc) h = mul(h, c.vec(p.v.sc));
-                if (xb) {
-                    h = fma(xr[k].get(), p.alpha, h);
-                    if (more) c.load(xb + b * p.xs[0] + t * p.xs[1], xr[k]);
-                }
+                if (xb) h = fma(c.get(slot(stage, 2, k), pitch, p.D, 0, 0), p.alpha, h);
                 hn[k] = centre(h, st.z, st.w);
                 if (!VEC || !c.has(0)) c.mask(hn[k]);
-                G[k] = ur[k].get();
-                if (more) c.load(dub + b * p.dus[0] + t * p.dus[1], ur[k]);
+                G[k] = c.get(slot(stage, 3, k), pitch, p.D, 0, 0);
                 if (live) {
                     add_to(3, k, G[k], hn[k]);
                     add_to(4, k, G[k], one);
@@ -654,25 +682,22 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) ttt_block_norm_bwd_kernel(co
         a = c2 = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const Chunk<T, VEC> c(r, k, lanes, p.D);
+            const C c(r, k, lanes, p.D);
             // G = dh + r (dn - mean(dn) - n mean(dn n))
             if (p.pre) {
                 G[k] = centre(fma(hn[k], -mc, G[k]), ma, st.w);
             } else {
                 G[k] = splat(0.f);
             }
-            if (dhb) {
-                G[k] = add(G[k], hr[k].get());
-                if (more) c.load(dhb + b * p.dhs[0] + t * p.dhs[1], hr[k]);
-            }
-            if (p.dx && live) c.store(static_cast<T *>(p.dx) + (size_t)row0 * p.D, mul(G[k], p.alpha));
+            if (dhb) G[k] = add(G[k], c.get(slot(stage, 4, k), pitch, p.D, 0, 0));
+            if (p.dx && live) c.store(static_cast<T *>(p.dx) + (size_t)row * p.D, mul(G[k], p.alpha));
             V8 pv = c.scale_shift(yn[k], p.v.w1, p.v.b1);
             if (p.v.sc) {
                 if (live) add_to(2, k, p.act ? mul(G[k], A[k]) : G[k], pv);
                 G[k] = mul(G[k], c.vec(p.v.sc));
             }
             if (p.act) {
-                if (live) c.store(static_cast<T *>(p.dg) + (size_t)row0 * p.D, mul(mul(G[k], pv), dA[k]));
+                if (live) c.store(static_cast<T *>(p.dg) + (size_t)row * p.D, mul(mul(G[k], pv), dA[k]));
                 G[k] = mul(G[k], A[k]);
             }
             // G is now dp
@@ -687,6 +712,7 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) ttt_block_norm_bwd_kernel(co
                 c2 += dot(G[k], yn[k]);
             }
         }
+        fetch(base + kAhead * stride, stage);
         ma = mc = 0.f;
         if (p.post) {
             const float2 m = g.sum2(a, c2);
@@ -694,10 +720,11 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) ttt_block_norm_bwd_kernel(co
             mc = m.y * inv;
         }
         // dy is contiguous in y's own layout
+        const uint32_t b0 = p.byT(row), t0 = row - b0 * p.T;
         T *dy = static_cast<T *>(p.dy) + (size_t)b0 * p.T * p.D + (size_t)t0 * p.dh;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const Chunk<T, VEC> c(r, k, lanes, p.D);
+            const C c(r, k, lanes, p.D);
             if (p.post) G[k] = centre(fma(yn[k], -mc, G[k]), ma, st.y);
             if (live) c.store_heads(dy, p.dh, (long long)p.T * p.dh, dyoff[k], G[k]);
         }
@@ -710,7 +737,7 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) ttt_block_norm_bwd_kernel(co
         if (p.slot[i] < 0) continue;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const Chunk<T, VEC> c(r, k, lanes, p.D);
+            const C c(r, k, lanes, p.D);
             V8 s;
             if constexpr (K > 1) {
 #pragma unroll
@@ -813,38 +840,43 @@ bool vector_ok(int es, int D, int dh, const void *const *ptr, int np, const long
     return true;
 }
 
-template <typename T, bool VEC>
-void run_fwd(const FwdParams &p, const Shape &s, int blocks, cudaStream_t st)
+template <typename P> int launch(void (*kernel)(P), const P &p, int blocks, int threads, int smem, cudaStream_t st)
 {
-    if (s.block) {
-        if (s.K == 1) ttt_block_norm_fwd_kernel<T, VEC, 1, true><<<blocks, s.threads, 0, st>>>(p);
-        else ttt_block_norm_fwd_kernel<T, VEC, 2, true><<<blocks, s.threads, 0, st>>>(p);
-        return;
-    }
+    if (smem > 40 * 1024 &&  // with the static part, past the 48 KB that need no asking
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return -4;
+    kernel<<<blocks, threads, smem, st>>>(p);
+    return cudaGetLastError() == cudaSuccess ? 0 : -4;
+}
+
+template <typename T, bool VEC>
+int run_fwd(const FwdParams &p, const Shape &s, int blocks, cudaStream_t st)
+{
+    using C = Chunk<T, VEC>;
+    const int smem = C::kAhead * 3 * s.K * C::kUnits * s.threads * 16;
+    if (s.block)
+        return s.K == 1 ? launch(ttt_block_norm_fwd_kernel<T, VEC, 1, true>, p, blocks, s.threads, smem, st)
+                        : launch(ttt_block_norm_fwd_kernel<T, VEC, 2, true>, p, blocks, s.threads, smem, st);
     switch (s.K) {
-    case 1: ttt_block_norm_fwd_kernel<T, VEC, 1, false><<<blocks, s.threads, 0, st>>>(p); break;
-    case 2: ttt_block_norm_fwd_kernel<T, VEC, 2, false><<<blocks, s.threads, 0, st>>>(p); break;
-    case 3: ttt_block_norm_fwd_kernel<T, VEC, 3, false><<<blocks, s.threads, 0, st>>>(p); break;
-    default: ttt_block_norm_fwd_kernel<T, VEC, 4, false><<<blocks, s.threads, 0, st>>>(p); break;
+    case 1: return launch(ttt_block_norm_fwd_kernel<T, VEC, 1, false>, p, blocks, s.threads, smem, st);
+    case 2: return launch(ttt_block_norm_fwd_kernel<T, VEC, 2, false>, p, blocks, s.threads, smem, st);
+    case 3: return launch(ttt_block_norm_fwd_kernel<T, VEC, 3, false>, p, blocks, s.threads, smem, st);
+    default: return launch(ttt_block_norm_fwd_kernel<T, VEC, 4, false>, p, blocks, s.threads, smem, st);
     }
 }
 
 template <typename T, bool VEC>
 int run_bwd(const BwdParams &p, const Shape &s, int blocks, cudaStream_t st)
 {
-    if (!s.block) {
-        ttt_block_norm_bwd_kernel<T, VEC, 1, false, 128><<<blocks, s.threads, s.threads * kC * 4, st>>>(p);
-    } else if (s.K == 1) {
-        if (s.threads <= 256) ttt_block_norm_bwd_kernel<T, VEC, 1, true, 256><<<blocks, s.threads, 0, st>>>(p);
-        else ttt_block_norm_bwd_kernel<T, VEC, 1, true, 512><<<blocks, s.threads, 0, st>>>(p);
-    } else {
-        const int smem = p.nvec * 2 * kC * s.threads * 4;
-        if (cudaFuncSetAttribute(ttt_block_norm_bwd_kernel<T, VEC, 2, true, 512>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, 5 * 2 * kC * 512 * 4) != cudaSuccess)
-            return -4;
-        ttt_block_norm_bwd_kernel<T, VEC, 2, true, 512><<<blocks, s.threads, smem, st>>>(p);
-    }
-    return 0;
+    const int sums = s.K > 1 ? p.nvec * s.K * kC * 4 : s.block ? 0 : kC * 4;
+    using C1 = Chunk<T, VEC>;
+    using C2 = Chunk<T, VEC, true>;
+    const int stage = s.K > 1 ? C2::kAhead * (5 * C2::kUnits + 1) * 16 : C1::kAhead * (5 * C1::kUnits + 1) * 16;
+    const int smem = (stage + sums) * s.threads;
+    if (!s.block) return launch(ttt_block_norm_bwd_kernel<T, VEC, 1, false, 128>, p, blocks, s.threads, smem, st);
+    if (s.K == 2) return launch(ttt_block_norm_bwd_kernel<T, VEC, 2, true, 512>, p, blocks, s.threads, smem, st);
+    return s.threads <= 256 ? launch(ttt_block_norm_bwd_kernel<T, VEC, 1, true, 256>, p, blocks, s.threads, smem, st)
+                            : launch(ttt_block_norm_bwd_kernel<T, VEC, 1, true, 512>, p, blocks, s.threads, smem, st);
 }
 
 }  // namespace
@@ -884,11 +916,9 @@ int launch_block_norm_fwd(const BlockNormArgs &a)
     const int blocks = grid_blocks(s, p.rows, kFwdThreadsPerSM);
     const bool vec = vector_ok(a.bf16 ? 2 : 4, a.D, a.dh, ptr, 10, st, 7);
     if (a.bf16)
-        if (vec) run_fwd<__nv_bfloat16, true>(p, s, blocks, a.stream);
-        else run_fwd<__nv_bfloat16, false>(p, s, blocks, a.stream);
-    else if (vec) run_fwd<float, true>(p, s, blocks, a.stream);
-    else run_fwd<float, false>(p, s, blocks, a.stream);
-    return cudaGetLastError() == cudaSuccess ? 0 : -4;
+        return vec ? run_fwd<__nv_bfloat16, true>(p, s, blocks, a.stream)
+                   : run_fwd<__nv_bfloat16, false>(p, s, blocks, a.stream);
+    return vec ? run_fwd<float, true>(p, s, blocks, a.stream) : run_fwd<float, false>(p, s, blocks, a.stream);
 }
 
 int launch_block_norm_bwd(const BlockNormArgs &a)
@@ -941,7 +971,7 @@ int launch_block_norm_bwd(const BlockNormArgs &a)
         rc = vec ? run_bwd<__nv_bfloat16, true>(p, s, blocks, a.stream) : run_bwd<__nv_bfloat16, false>(p, s, blocks, a.stream);
     else
         rc = vec ? run_bwd<float, true>(p, s, blocks, a.stream) : run_bwd<float, false>(p, s, blocks, a.stream);
-    if (rc || cudaGetLastError() != cudaSuccess) return -4;
+    if (rc) return rc;
     if (p.nvec) {
         q.part = p.part;
         q.nblocks = blocks;  // 0 rows: the sums are zeros

@@ -26,17 +26,6 @@ template <typename T, int V> struct Pack {
     __device__ __forceinline__ void load(const T *p) { raw = __ldg(reinterpret_cast<const Raw *>(p)); }
     // a plain load: for data the same kernel also writes (in-place operation)
     __device__ __forceinline__ void load_rw(const T *p) { raw = *reinterpret_cast<const Raw *>(p); }
-    // data read once: kept out of L1, where it would evict what is read again
-    __device__ __forceinline__ void load_once(const T *p)
-    {
-        if constexpr (sizeof(Raw) == 16)
-            asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(raw.x), "=r"(raw.y), "=r"(raw.z), "=r"(raw.w)
-                         : "l"(p)
-                         : "memory");
-        else
-            raw = *reinterpret_cast<const Raw *>(p);
-    }
     __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<Raw *>(p) = raw; }
 };
 
@@ -104,5 +93,20 @@ __device__ __forceinline__ void pack(Pack<__nv_bfloat16, 8> &p, const float (&v)
 {
     p.raw = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
 }
+
+// Copies 16 or 4 bytes to shared memory behind the thread's back; a thread waits for its
+// own groups of copies, oldest first.
+__device__ __forceinline__ void copy_async16(void *dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_async4(void *dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
 
 }  // namespace ttt
