@@ -423,6 +423,7 @@ template <bool BLOCK> struct Group {
             __syncthreads();
             turn ^= 1;
             s = make_float2(0.f, 0.f);
+#pragma unroll 4
             for (int i = 0; i < half_nw; ++i) {
                 const float4 w = q[i];
                 s = __fadd2_rn(s, __fadd2_rn(make_float2(w.x, w.y), make_float2(w.z, w.w)));
@@ -439,6 +440,7 @@ template <bool BLOCK> struct Group {
             __syncthreads();
             turn ^= 1;
             a = 0.f;
+#pragma unroll 4
             for (int i = 0; i < half_nw; ++i) a += q[i].x + q[i].y;
         }
         return a;
@@ -793,27 +795,26 @@ __global__ void __launch_bounds__(512) ttt_block_norm_reduce_kernel(const __grid
 
 // ------------------------------------------------------------------------ launch
 
-// Threads of a row and chunks of a thread.  Forward: part of a warp up to 256 features, a
-// warp with up to four chunks a lane up to 1024 (no barrier), then one block a row.
-// Backward: its sums want few features a thread, so blocks from 256 features on.  Blocks
-// hold one chunk a thread, two past 4096 features.
+// Threads of a row and chunks of a thread: part of a warp up to 256 features, then one
+// block a row with one chunk a thread, two past 4096 features.  (A warp with three chunks
+// a lane for 768 features, no barrier: 42 us against 33 for a block of three warps at 8 x
+// 2048 x 768, sandwich forward; the chunks cost the registers that hide its latency.)
 struct Shape {
     int lanes, threads, K;
     bool block;
 };
 
-Shape row_shape(int D, bool wide_warps)
+Shape row_shape(int D)
 {
     Shape s;
-    s.block = D > 32 * kC * (wide_warps ? 4 : 1);
+    s.block = D > 32 * kC;
+    s.K = D > 512 * kC ? 2 : 1;
     if (s.block) {
-        s.K = D > 512 * kC ? 2 : 1;
         const int need = (D + kC * s.K - 1) / (kC * s.K);
         s.lanes = s.threads = (need + 31) / 32 * 32;
     } else {
-        s.K = (D + 32 * kC - 1) / (32 * kC);
-        s.lanes = s.K > 1 ? 32 : 1;
-        while (s.lanes * kC * s.K < D) s.lanes *= 2;
+        s.lanes = 1;
+        while (s.lanes * kC < D) s.lanes *= 2;
         s.threads = 128;
     }
     return s;
@@ -854,15 +855,9 @@ int run_fwd(const FwdParams &p, const Shape &s, int blocks, cudaStream_t st)
 {
     using C = Chunk<T, VEC>;
     const int smem = C::kAhead * 3 * s.K * C::kUnits * s.threads * 16;
-    if (s.block)
-        return s.K == 1 ? launch(ttt_block_norm_fwd_kernel<T, VEC, 1, true>, p, blocks, s.threads, smem, st)
-                        : launch(ttt_block_norm_fwd_kernel<T, VEC, 2, true>, p, blocks, s.threads, smem, st);
-    switch (s.K) {
-    case 1: return launch(ttt_block_norm_fwd_kernel<T, VEC, 1, false>, p, blocks, s.threads, smem, st);
-    case 2: return launch(ttt_block_norm_fwd_kernel<T, VEC, 2, false>, p, blocks, s.threads, smem, st);
-    case 3: return launch(ttt_block_norm_fwd_kernel<T, VEC, 3, false>, p, blocks, s.threads, smem, st);
-    default: return launch(ttt_block_norm_fwd_kernel<T, VEC, 4, false>, p, blocks, s.threads, smem, st);
-    }
+    if (!s.block) return launch(ttt_block_norm_fwd_kernel<T, VEC, 1, false>, p, blocks, s.threads, smem, st);
+    return s.K == 1 ? launch(ttt_block_norm_fwd_kernel<T, VEC, 1, true>, p, blocks, s.threads, smem, st)
+                    : launch(ttt_block_norm_fwd_kernel<T, VEC, 2, true>, p, blocks, s.threads, smem, st);
 }
 
 template <typename T, bool VEC>
@@ -881,11 +876,11 @@ int run_bwd(const BwdParams &p, const Shape &s, int blocks, cudaStream_t st)
 
 }  // namespace
 
-int block_norm_bwd_blocks(int D, long long rows) { return grid_blocks(row_shape(D, false), rows, kBwdThreadsPerSM); }
+int block_norm_bwd_blocks(int D, long long rows) { return grid_blocks(row_shape(D), rows, kBwdThreadsPerSM); }
 
 int launch_block_norm_fwd(const BlockNormArgs &a)
 {
-    const Shape s = row_shape(a.D, true);
+    const Shape s = row_shape(a.D);
     FwdParams p;
     p.y = a.y;
     p.x = a.x;
@@ -923,7 +918,7 @@ int launch_block_norm_fwd(const BlockNormArgs &a)
 
 int launch_block_norm_bwd(const BlockNormArgs &a)
 {
-    const Shape s = row_shape(a.D, false);
+    const Shape s = row_shape(a.D);
     BwdParams p;
     p.y = a.y;
     p.x = a.x;
