@@ -104,6 +104,22 @@ bool ttt::encode_token_map(CUtensorMap *m, const void *ptr, int BH, int T, int d
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool ttt::encode_rows_map(CUtensorMap *m, const void *ptr, bool bf16, int width, int rows, int batch, long long row_stride,
+                          long long batch_stride, int cols, int height)
+{
+    EncodeTiledFn fn = encode_fn();
+    const long long es = bf16 ? 2 : 4, rs = row_stride * es, bs = batch_stride * es;
+    if (!fn || rs <= 0 || bs <= 0 || rs % 16 || bs % 16 || rs >= (1LL << 40) || bs >= (1LL << 40)) return false;
+    if (reinterpret_cast<uintptr_t>(ptr) % 16) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)rows, (cuuint64_t)batch};
+    const cuuint64_t strides[2] = {(cuuint64_t)rs, (cuuint64_t)bs};
+    const cuuint32_t box[3] = {(cuuint32_t)cols, (cuuint32_t)height, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void *>(ptr),
+              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool ttt::encode_grid_map(CUtensorMap *m, const void *ptr, bool bf16, int BH, int hh, int ww, int d)
 {
     EncodeTiledFn fn = encode_fn();
@@ -737,7 +753,7 @@ ttt_status recurrence_args(const ttt_recurrence_desc *desc, const void *x, const
     if (D.io_dtype != TTT_F32 && D.io_dtype != TTT_BF16) return TTT_ERR_ARG;
     for (int i = 0; i < 2; ++i)
         if (D.x_stride[i] < 0 || D.f_stride[i] < 0 || D.dh_stride[i] < 0) return TTT_ERR_ARG;
-    if (D.B > 65535) return TTT_ERR_UNSUPPORTED;
+    if (D.B > 65535 || D.T > 0x7fff0000) return TTT_ERR_UNSUPPORTED;
     const int es = D.io_dtype == TTT_BF16 ? 2 : 4;
     if (D.B > 0 && D.T > 0) {
         if (!x || !f) return TTT_ERR_ARG;
@@ -798,6 +814,8 @@ ttt_status ttt_recurrence_fwd(const ttt_recurrence_desc *desc, const void *x, co
     a.h = h;
     a.h_last = h_last;
     a.states = states;
+    a.status = status_word();
+    if (!a.status) return TTT_ERR_LAUNCH;
     const int rc = ttt::launch_recurrence(a, false);
     if (rc == 0) g_launches.fetch_add(1, std::memory_order_relaxed);
     return code(rc);
@@ -831,6 +849,8 @@ ttt_status ttt_recurrence_bwd(const ttt_recurrence_desc *desc, const void *dh, c
     a.dx = dx;
     a.df = df;
     a.dh0 = dh0;
+    a.status = status_word();
+    if (!a.status) return TTT_ERR_LAUNCH;
     const int rc = ttt::launch_recurrence(a, true);
     if (rc == 0) g_launches.fetch_add(1, std::memory_order_relaxed);
     return code(rc);

@@ -102,6 +102,7 @@ struct RecurArgs {
     const float *h0, *dh_last;
     void *h, *dx, *df;
     float *h_last, *states, *dh0;  // states: written by the forward, read by the backward
+    int *status;                   // device status word (timeouts)
     cudaStream_t stream;
 };
 
@@ -116,6 +117,13 @@ bool encode_token_map(CUtensorMap *m, const void *ptr, int BH, int T, int d, int
 // the border read as zeros (out of range).  False if d > 256, hh + 2 or ww + 2 > 256,
 // or the encoding fails.
 bool encode_grid_map(CUtensorMap *m, const void *ptr, bool bf16, int BH, int hh, int ww, int d);
+
+// Descriptor of rows [batch][rows][width] (bf16 or fp32) with element strides, boxes of
+// `height` rows x `cols` elements, out-of-range elements read as zeros.  False if a stride
+// is zero or not a multiple of 16 bytes, the pointer is not 16-byte aligned, or the
+// encoding fails.
+bool encode_rows_map(CUtensorMap *m, const void *ptr, bool bf16, int width, int rows, int batch, long long row_stride,
+                     long long batch_stride, int cols, int height);
 
 // q, k, v descriptors (zeroed, unused when T == 0); false on an encoding failure.
 inline bool encode_qkv(CUtensorMap *maps, const void *q, const void *k, const void *v, int BH, int T,

@@ -7,6 +7,9 @@
 //     dx = c s,  dL/da = s (h_{t-1} [- x_t for mix]),  df = dL/da a (1 - a) unless a = f,
 // with h_{t-1} computed again from the states that the forward pass leaves every
 // kRecurChunk tokens: no rounded h is read, and no more bytes than reading it would take.
+#include <cuda.h>
+
+#include "ttt_device.cuh"
 #include "ttt_internal.h"
 #include "ttt_vec.cuh"
 
@@ -24,6 +27,7 @@ struct RecurParams {
     long long xs[2], fs[2], ds[2];
     int B, T, C, chunks;
     int cluster, cblocks;  // tile kernels: blocks of a cluster, channel blocks of a batch entry
+    int *status;           // device status word (timeouts)
 };
 
 // a and 1 - a, each accurate on its own: with e = exp(-|f|) <= 1 the smaller of the two is
@@ -119,17 +123,100 @@ __global__ void __launch_bounds__(kThreads) ttt_recurrence_bwd_kernel(const __gr
 //
 // A warp takes kS tokens of 32 CPL channels, a block of kW warps a tile of kRecurChunk
 // tokens, a cluster of P blocks P neighbouring tiles, and the cluster walks along the
-// sequence in rounds of P tiles, the next round's loads in flight.  Every tensor is read
-// once: the round's data stay in registers while the warps' maps h -> A h + H (the
-// product of the decays, and the tokens' own contribution) are joined, in shared memory
-// inside the block and through the cluster's distributed shared memory between blocks.
-// The join order is fixed by position, so results do not depend on timing.  NaN and
-// infinities do not pass a reset: a map with a reset in it (cut) ignores its input.
+// sequence in rounds of P tiles.  Every tensor is read once, by TMA into a ring of stages
+// (TMA; rows or pointers that are not 16-byte aligned by plain loads a round ahead).  A
+// warp folds its tokens into one map h -> A h + H (the product of the decays, the tokens'
+// own contribution); the warps' maps are joined in shared memory, the blocks' totals
+// through the cluster's distributed shared memory (stores that complete on the reader's
+// mbarrier: a cluster barrier would wait for the round's global stores as well).  The join
+// order is fixed by position, so results do not depend on timing.  NaN and infinities do
+// not pass a reset: a map with a reset in it (cut) ignores its input.
 
 constexpr int kS = 16, kW = 8;
 static_assert(kS * kW == kRecurChunk, "a tile is one stored-state chunk");
+constexpr int kRowBytes = 128;                       // a tile's row of one tensor, by TMA
+constexpr int kPlane = kRecurChunk * kRowBytes;      // one tensor of a stage
+constexpr int kFwdStages = 2, kBwdStages = 2;
 
-// this block's rank in its cluster, cluster barrier, stores to another block's shared memory
+// N channels of a lane, with paired instructions for two.
+template <int N> struct F;
+template <> struct F<1> {
+    float x;
+};
+template <> struct alignas(8) F<2> {
+    float x, y;
+};
+__device__ __forceinline__ float2 f2(const F<2> &a) { return make_float2(a.x, a.y); }
+__device__ __forceinline__ F<2> f2(float2 a) { return {a.x, a.y}; }
+__device__ __forceinline__ F<1> fma(F<1> a, F<1> b, F<1> c) { return {fmaf(a.x, b.x, c.x)}; }
+__device__ __forceinline__ F<2> fma(F<2> a, F<2> b, F<2> c) { return f2(__ffma2_rn(f2(a), f2(b), f2(c))); }
+__device__ __forceinline__ F<1> mul(F<1> a, F<1> b) { return {a.x * b.x}; }
+__device__ __forceinline__ F<2> mul(F<2> a, F<2> b) { return f2(__fmul2_rn(f2(a), f2(b))); }
+__device__ __forceinline__ F<1> add(F<1> a, F<1> b) { return {a.x + b.x}; }
+__device__ __forceinline__ F<2> add(F<2> a, F<2> b) { return f2(__fadd2_rn(f2(a), f2(b))); }
+__device__ __forceinline__ F<1> sub(F<1> a, F<1> b) { return {a.x - b.x}; }
+__device__ __forceinline__ F<2> sub(F<2> a, F<2> b) { return f2(__fadd2_rn(f2(a), make_float2(-b.x, -b.y))); }
+template <int N> __device__ __forceinline__ F<N> splat(float v);
+template <> __device__ __forceinline__ F<1> splat<1>(float v) { return {v}; }
+template <> __device__ __forceinline__ F<2> splat<2>(float v) { return {v, v}; }
+
+template <typename T, int MODE> __device__ __forceinline__ void gates(F<1> f, F<1> &a, F<1> &eta)
+{
+    gate<T, MODE>(f.x, a.x, eta.x);
+}
+template <typename T, int MODE> __device__ __forceinline__ void gates(F<2> f, F<2> &a, F<2> &eta)
+{
+    gate<T, MODE>(f.x, a.x, eta.x);
+    gate<T, MODE>(f.y, a.y, eta.y);
+}
+template <typename T> __device__ __forceinline__ F<1> widen(const Pack<T, 1> &p)
+{
+    float v[1];
+    unpack(p, v);
+    return {v[0]};
+}
+template <typename T> __device__ __forceinline__ F<2> widen(const Pack<T, 2> &p)
+{
+    float v[2];
+    unpack(p, v);
+    return {v[0], v[1]};
+}
+template <typename T> __device__ __forceinline__ void put(T *p, F<1> a)
+{
+    const float v[1] = {a.x};
+    Pack<T, 1> q;
+    pack(q, v);
+    q.store(p);
+}
+template <typename T> __device__ __forceinline__ void put(T *p, F<2> a)
+{
+    const float v[2] = {a.x, a.y};
+    Pack<T, 2> q;
+    pack(q, v);
+    q.store(p);
+}
+
+// A map of one direction: v -> a v + c.
+template <int N> struct alignas(8 * N) Map {
+    F<N> a, c;
+};
+template <int N> __device__ __forceinline__ F<N> apply(const Map<N> &m, F<N> v, bool cut)
+{
+    return cut ? m.c : fma(m.a, v, m.c);
+}
+
+// The warps' maps of a round, double-buffered over rounds.  One barrier a round is enough:
+// a buffer is written again two rounds later, behind the next round's barrier.  The
+// blocks' totals lie behind the stages, [2][P][32].  BWD: beside the forward maps the
+// constant terms of the backward ones, whose factors are the same.
+template <int N, bool BWD> struct TileShared {
+    Map<N> w[2][kW][32];
+    F<N> r[BWD ? 2 : 1][BWD ? kW : 1][32];
+    int wcut[2][kW];
+    int tcut[2][8];
+    unsigned long long full[2], joined[2];  // mbarriers: a stage's copies, the cluster's totals
+};
+
 __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
@@ -141,32 +228,54 @@ __device__ __forceinline__ void cluster_barrier()
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void st_remote(const void *local, uint32_t rank, float v)
+__device__ __forceinline__ uint32_t remote(uint32_t local, uint32_t rank)
 {
-    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(local)), r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(r), "f"(v) : "memory");
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
+    return r;
+}
+// stores to a block of the cluster that count on its mbarrier as they land
+__device__ __forceinline__ void send(uint32_t dst, uint32_t bar, const Map<2> &m)
+{
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%2,%3,%4,%5}, [%1];" ::"r"(dst),
+                 "r"(bar), "f"(m.a.x), "f"(m.a.y), "f"(m.c.x), "f"(m.c.y)
+                 : "memory");
+}
+__device__ __forceinline__ void send(uint32_t dst, uint32_t bar, const Map<1> &m)
+{
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%2,%3}, [%1];" ::"r"(dst),
+                 "r"(bar), "f"(m.a.x), "f"(m.c.x)
+                 : "memory");
+}
+__device__ __forceinline__ void send(uint32_t dst, uint32_t bar, int v)
+{
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %2, [%1];" ::"r"(dst), "r"(bar),
+                 "r"(v)
+                 : "memory");
 }
 
-// The maps of a round, double-buffered over rounds: per warp (w) and per block of the
-// cluster (t).  One barrier a round is enough: a buffer is written again two rounds later,
-// behind the next round's barrier.
-template <int CPL, int NV> struct TileShared {
-    float w[2][NV][kW][32 * CPL];
-    float t[2][NV][8][32 * CPL];
-    int wcut[2][kW];
-    float tcut[2][8];
-};
-
-template <int CPL> __device__ __forceinline__ void lds(const float *p, float (&v)[CPL])
+// Tells every block of the cluster this block's total and waits for theirs; then carry
+// goes through all of them, and the value before this block's tile is returned.
+template <int N, bool RESET, bool BWD>
+__device__ __forceinline__ F<N> join_blocks(TileShared<N, BWD> &sh, Map<N> *totals, const Map<N> &total, bool cut, F<N> &carry,
+                                            int P, int rank, int buf, int phase, int *status, bool &ok)
 {
-    if constexpr (CPL == 2) {
-        const float2 q = *reinterpret_cast<const float2 *>(p);
-        v[0] = q.x;
-        v[1] = q.y;
-    } else {
-        v[0] = *p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t bar = smem_u32(&sh.joined[buf]);
+    totals += buf * P * 32 + lane;
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, P * (32 * (int)sizeof(Map<N>) + (RESET ? 4 : 0)));
+    if (warp < P) {  // warp i tells block i
+        const uint32_t rbar = remote(bar, warp);
+        send(remote(smem_u32(totals + rank * 32), warp), rbar, total);
+        if (RESET && lane == 0) send(remote(smem_u32(&sh.tcut[buf][rank]), warp), rbar, (int)cut);
     }
+    ok &= mbar_wait(bar, phase, status, kSiteStage);
+    F<N> before = carry;
+    for (int i = 0; i < P; ++i) {
+        carry = apply(totals[i * 32], carry, RESET && sh.tcut[buf][i]);
+        if (i < rank) before = carry;
+    }
+    return before;
 }
 
 // The reset bits of a warp's tokens t0 .. t0 + n - 1.
@@ -175,25 +284,54 @@ __device__ __forceinline__ unsigned reset_bits(const unsigned char *reset, int t
     return __ballot_sync(0xffffffffu, lane < n && reset[t0 + lane] != 0);
 }
 
-template <typename T, int MODE, int CPL, bool RESET>
-__global__ void __launch_bounds__(32 * kW, 2) ttt_recurrence_fwd_tile_kernel(const __grid_constant__ RecurParams p)
+// A block that gave up waiting (never expected) lets its copies land, then leaves with
+// its cluster.
+__device__ __forceinline__ void drain(unsigned long long *full, int rounds_issued, int stages, int *status)
 {
-    constexpr int CH = 32 * CPL;
-    __shared__ TileShared<CPL, 2> sh;
+    for (int r = max(0, rounds_issued - stages); r < rounds_issued; ++r)
+        if (!mbar_wait(smem_u32(&full[r % stages]), (r / stages) & 1, status, kSiteDrain)) break;
+}
+
+template <typename T, int MODE, bool RESET, bool TMA>
+__global__ void __launch_bounds__(32 * kW, 2)
+    ttt_recurrence_fwd_tile_kernel(const __grid_constant__ RecurParams p, const __grid_constant__ CUtensorMap tf,
+                                   const __grid_constant__ CUtensorMap tx)
+{
+    constexpr int N = TMA ? 4 / (int)sizeof(T) : 1, CH = 32 * N;
+    using P_ = Pack<T, N>;
+    __shared__ TileShared<N, false> sh;
+    extern __shared__ unsigned char dynamic[];
+    unsigned char *stages = dynamic + (-smem_u32(dynamic) & 127u);  // TMA: [kFwdStages][f, x][kPlane]
+    Map<N> *totals = reinterpret_cast<Map<N> *>(stages + (TMA ? kFwdStages * 2 * kPlane : 0));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int P = p.cluster, rank = P > 1 ? (int)cluster_rank() : 0;
-    const int chain = blockIdx.x / P, b = chain / p.cblocks, c = (chain % p.cblocks) * CH + lane * CPL;
-    const bool on = c < p.C;  // CPL divides C
-    const T *x = static_cast<const T *>(p.x) + b * p.xs[0] + c, *f = static_cast<const T *>(p.f) + b * p.fs[0] + c;
+    const int chain = blockIdx.x / P, b = chain / p.cblocks, c0 = (chain % p.cblocks) * CH, c = c0 + lane * N;
+    const bool on = c < p.C;  // N divides C
     const unsigned char *reset = RESET ? p.reset + (size_t)b * p.T : nullptr;
     const size_t bc = (size_t)b * p.C + c;
-    float carry[CPL];
-#pragma unroll
-    for (int j = 0; j < CPL; ++j) carry[j] = on && p.h0 ? p.h0[bc + j] : 0.f;
-
-    Pack<T, CPL> fr[kS], xr[kS];
+    const int rounds = (p.chunks + P - 1) / P;
+    auto issue = [&](int round) {
+        const int st = round % kFwdStages;
+        const uint32_t dst = smem_u32(stages) + st * 2 * kPlane, bar = smem_u32(&sh.full[st]);
+        mbar_arrive_expect_tx(bar, 2 * kPlane);
+        tma_load_3d(dst, &tf, bar, c0, (round * P + rank) * kRecurChunk, b);
+        tma_load_3d(dst + kPlane, &tx, bar, c0, (round * P + rank) * kRecurChunk, b);
+    };
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sh.full[i]), 1);
+            mbar_init(smem_u32(&sh.joined[i]), 1);
+        }
+        fence_barrier_init();
+        if (TMA)
+            for (int i = 0; i < kFwdStages && i < rounds; ++i) issue(i);
+    }
+    F<N> carry = splat<N>(0.f);
+    if (on && p.h0) carry = widen(*reinterpret_cast<const Pack<float, N> *>(p.h0 + bc));
+    P_ fr[kS], xr[kS];
     auto fetch = [&](int t0) {
-        const T *fp = f + t0 * p.fs[1], *xp = x + t0 * p.xs[1];
+        const T *fp = static_cast<const T *>(p.f) + b * p.fs[0] + c + t0 * p.fs[1];
+        const T *xp = static_cast<const T *>(p.x) + b * p.xs[0] + c + t0 * p.xs[1];
 #pragma unroll
         for (int s = 0; s < kS; ++s)
             if (on && t0 + s < p.T) {
@@ -201,371 +339,265 @@ __global__ void __launch_bounds__(32 * kW, 2) ttt_recurrence_fwd_tile_kernel(con
                 xr[s].load(xp + s * p.xs[1]);
             }
     };
-    const int rounds = (p.chunks + P - 1) / P;
-    int t0 = rank * kRecurChunk + warp * kS, buf = 0;
-    fetch(t0);
-    if (P > 1) cluster_barrier();  // every block runs before its shared memory is written
-    for (int round = 0; round < rounds; ++round, t0 += P * kRecurChunk, buf ^= 1) {
+    int t0 = rank * kRecurChunk + warp * kS;
+    if (!TMA) fetch(t0);
+    __syncthreads();
+    if (P > 1) cluster_barrier();  // every block runs, its barriers set, before it is written to
+    bool ok = true;
+    int round = 0;
+    for (; round < rounds; ++round, t0 += P * kRecurChunk) {
+        const int buf = round & 1;
         const int n = min(max(p.T - t0, 0), kS);  // this warp's tokens
         const unsigned cuts = RESET ? reset_bits(reset, t0, n, lane) : 0u;
-        float a[kS][CPL], u[kS][CPL];
+        const unsigned char *mine = stages + (round % kFwdStages) * 2 * kPlane + warp * kS * kRowBytes + lane * 4;
+        if (TMA) ok &= mbar_wait(smem_u32(&sh.full[round % kFwdStages]), (round / kFwdStages) & 1, p.status, kSiteConsumerFull);
+        F<N> a[kS], u[kS];
+        Map<N> m = {splat<N>(1.f), splat<N>(0.f)};
 #pragma unroll
         for (int s = 0; s < kS; ++s) {
-            float fv[CPL], xv[CPL];
-            unpack(fr[s], fv);
-            unpack(xr[s], xv);
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) {
-                float eta;
-                gate<T, MODE>(fv[j], a[s][j], eta);
-                u[s][j] = MODE == kRecurMix ? eta * xv[j] : xv[j];
+            if (TMA) {
+                fr[s] = *reinterpret_cast<const P_ *>(mine + s * kRowBytes);
+                xr[s] = *reinterpret_cast<const P_ *>(mine + kPlane + s * kRowBytes);
             }
+            F<N> eta;
+            gates<T, MODE>(widen(fr[s]), a[s], eta);
+            u[s] = MODE == kRecurMix ? mul(eta, widen(xr[s])) : widen(xr[s]);
         }
-        if (round + 1 < rounds) fetch(t0 + P * kRecurChunk);
+        if (!TMA && round + 1 < rounds) fetch(t0 + P * kRecurChunk);
         if (n < kS) {  // tokens past the end: the identity
 #pragma unroll
             for (int s = 0; s < kS; ++s)
-                if (s >= n)
-#pragma unroll
-                    for (int j = 0; j < CPL; ++j) {
-                        a[s][j] = 1.f;
-                        u[s][j] = 0.f;
-                    }
-        }
-        // the warp's map
-        float A[CPL], H[CPL];
-#pragma unroll
-        for (int j = 0; j < CPL; ++j) {
-            A[j] = 1.f;
-            H[j] = 0.f;
+                if (s >= n) {
+                    a[s] = splat<N>(1.f);
+                    u[s] = splat<N>(0.f);
+                }
         }
 #pragma unroll
         for (int s = 0; s < kS; ++s) {
-            if (RESET && (cuts >> s & 1u))
-#pragma unroll
-                for (int j = 0; j < CPL; ++j) H[j] = 0.f;
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) {
-                H[j] = fmaf(a[s][j], H[j], u[s][j]);
-                A[j] *= a[s][j];
-            }
+            if (RESET && (cuts >> s & 1u)) m.c = splat<N>(0.f);
+            m.c = fma(a[s], m.c, u[s]);
+            m.a = mul(m.a, a[s]);
         }
-#pragma unroll
-        for (int j = 0; j < CPL; ++j) {
-            sh.w[buf][0][warp][lane * CPL + j] = A[j];
-            sh.w[buf][1][warp][lane * CPL + j] = H[j];
-        }
+        sh.w[buf][warp][lane] = m;
         if (RESET && lane == 0) sh.wcut[buf][warp] = cuts != 0;
-        __syncthreads();
+        ok = __syncthreads_and(ok);
+        if (!ok) break;
+        if (TMA && threadIdx.x == 0 && round + kFwdStages < rounds) issue(round + kFwdStages);
         // the state before this block's tile, and the next round's
-        float st[CPL];
+        F<N> st = carry;
         if (P > 1) {
-            float TA[CPL], TH[CPL];
-            bool cut = false;
+            Map<N> total = sh.w[buf][0][lane];
+            bool cut = RESET && sh.wcut[buf][0];
 #pragma unroll
-            for (int j = 0; j < CPL; ++j) {
-                TA[j] = 1.f;
-                TH[j] = 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < kW; ++i) {
-                float wa[CPL], wh[CPL];
-                lds<CPL>(&sh.w[buf][0][i][lane * CPL], wa);
-                lds<CPL>(&sh.w[buf][1][i][lane * CPL], wh);
+            for (int i = 1; i < kW; ++i) {
+                const Map<N> w = sh.w[buf][i][lane];
                 const bool ci = RESET && sh.wcut[buf][i];
+                total.c = apply(w, total.c, ci);
+                total.a = mul(w.a, total.a);
                 cut |= ci;
-#pragma unroll
-                for (int j = 0; j < CPL; ++j) {
-                    TH[j] = ci ? wh[j] : fmaf(wa[j], TH[j], wh[j]);
-                    TA[j] *= wa[j];
-                }
             }
-            if (warp < P) {  // warp i tells block i
-#pragma unroll
-                for (int j = 0; j < CPL; ++j) {
-                    st_remote(&sh.t[buf][0][rank][lane * CPL + j], warp, TA[j]);
-                    st_remote(&sh.t[buf][1][rank][lane * CPL + j], warp, TH[j]);
-                }
-                if (RESET && lane == 0) st_remote(&sh.tcut[buf][rank], warp, cut ? 1.f : 0.f);
-            }
-            cluster_barrier();
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) st[j] = carry[j];
-            for (int i = 0; i < P; ++i) {
-                float wa[CPL], wh[CPL];
-                lds<CPL>(&sh.t[buf][0][i][lane * CPL], wa);
-                lds<CPL>(&sh.t[buf][1][i][lane * CPL], wh);
-                const bool ci = RESET && sh.tcut[buf][i] != 0.f;
-#pragma unroll
-                for (int j = 0; j < CPL; ++j) {
-                    carry[j] = ci ? wh[j] : fmaf(wa[j], carry[j], wh[j]);
-                    if (i < rank) st[j] = carry[j];
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) st[j] = carry[j];
+            st = join_blocks<N, RESET>(sh, totals, total, cut, carry, P, rank, buf, (round >> 1) & 1, p.status, ok);
         }
         if (warp == 0 && p.states && on && n > 0)
-#pragma unroll
-            for (int j = 0; j < CPL; ++j)
-                p.states[((size_t)b * p.chunks + t0 / kRecurChunk) * p.C + c + j] = st[j];
+            put(p.states + ((size_t)b * p.chunks + t0 / kRecurChunk) * p.C + c, st);
         // the state before this warp's tokens
-        float h[CPL];
-#pragma unroll
-        for (int j = 0; j < CPL; ++j) h[j] = st[j];
+        F<N> h = st;
 #pragma unroll
         for (int i = 0; i < kW; ++i) {
-            float wa[CPL], wh[CPL];
-            lds<CPL>(&sh.w[buf][0][i][lane * CPL], wa);
-            lds<CPL>(&sh.w[buf][1][i][lane * CPL], wh);
-            const bool ci = RESET && sh.wcut[buf][i];
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) {
-                st[j] = ci ? wh[j] : fmaf(wa[j], st[j], wh[j]);
-                if (i < warp) h[j] = st[j];
-            }
+            st = apply(sh.w[buf][i][lane], st, RESET && sh.wcut[buf][i]);
+            if (i + 1 == warp) h = st;
         }
-        if (P == 1)
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) carry[j] = st[j];
+        if (P == 1) carry = st;
         T *hp = static_cast<T *>(p.h) + ((size_t)b * p.T + t0) * p.C + c;
 #pragma unroll
         for (int s = 0; s < kS; ++s) {
-            if (RESET && (cuts >> s & 1u))
-#pragma unroll
-                for (int j = 0; j < CPL; ++j) h[j] = 0.f;
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) h[j] = fmaf(a[s][j], h[j], u[s][j]);
-            if (on && s < n) {
-                Pack<T, CPL> q;
-                pack(q, h);
-                q.store(hp + (size_t)s * p.C);
-            }
+            if (RESET && (cuts >> s & 1u)) h = splat<N>(0.f);
+            h = fma(a[s], h, u[s]);
+            if (on && s < n) put(hp + (size_t)s * p.C, h);
         }
     }
-    if (p.h_last && on && rank == 0 && warp == 0)
-#pragma unroll
-        for (int j = 0; j < CPL; ++j) p.h_last[bc + j] = carry[j];
+    if (!ok && TMA && threadIdx.x == 0) drain(sh.full, min(rounds, round + kFwdStages), kFwdStages, p.status);
+    if (P > 1) cluster_barrier();  // no block leaves while another may write to it
+    if (ok && p.h_last && on && rank == 0 && warp == 0) put(p.h_last + bc, carry);
 }
 
-// Backward: the same tiles from the end of the sequence to its start.  The warps' maps
-// carry three numbers a channel: the product A of the decays (shared by both
-// directions), the forward contribution H, which brings h_{t-1} to every warp from the
-// tile's stored state, and the backward one R of r -> A r + R.
-template <typename T, int MODE, int CPL, bool RESET>
-__global__ void __launch_bounds__(32 * kW) ttt_recurrence_bwd_tile_kernel(const __grid_constant__ RecurParams p)
+// Backward: the same tiles from the end of the sequence to its start.  Each warp has two
+// maps with the same product of decays: forward from the tile's stored state, which brings
+// it h_{t-1}, and backward r -> A r + R with R = sum_s (a_0 .. a_s) dh_s, gathered in token
+// order beside the forward one.  x and dh are read again from the stage for the outputs,
+// so a stage is refilled one round after its own.
+template <typename T, int MODE, bool RESET, bool TMA>
+__global__ void __launch_bounds__(32 * kW, 2)
+    ttt_recurrence_bwd_tile_kernel(const __grid_constant__ RecurParams p, const __grid_constant__ CUtensorMap tf,
+                                   const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap td)
 {
-    constexpr int CH = 32 * CPL;
-    __shared__ TileShared<CPL, 3> sh;
+    constexpr int N = TMA ? 4 / (int)sizeof(T) : 1, CH = 32 * N;
+    using P_ = Pack<T, N>;
+    __shared__ TileShared<N, true> sh;
+    extern __shared__ unsigned char dynamic[];
+    unsigned char *stages = dynamic + (-smem_u32(dynamic) & 127u);  // TMA: [kBwdStages][f, x, dh][kPlane]
+    Map<N> *totals = reinterpret_cast<Map<N> *>(stages + (TMA ? kBwdStages * 3 * kPlane : 0));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int P = p.cluster, rank = P > 1 ? (int)cluster_rank() : 0;
-    const int chain = blockIdx.x / P, b = chain / p.cblocks, c = (chain % p.cblocks) * CH + lane * CPL;
+    const int chain = blockIdx.x / P, b = chain / p.cblocks, c0 = (chain % p.cblocks) * CH, c = c0 + lane * N;
     const bool on = c < p.C;
-    const T *x = static_cast<const T *>(p.x) + b * p.xs[0] + c, *f = static_cast<const T *>(p.f) + b * p.fs[0] + c;
-    const T *dh = static_cast<const T *>(p.dh) + b * p.ds[0] + c;
     const unsigned char *reset = RESET ? p.reset + (size_t)b * p.T : nullptr;
     const size_t bc = (size_t)b * p.C + c;
-    float carry[CPL];
-#pragma unroll
-    for (int j = 0; j < CPL; ++j) carry[j] = on && p.dh_last ? p.dh_last[bc + j] : 0.f;
-
-    Pack<T, CPL> fr[kS], xr[kS], dr[kS];
-    float sr[CPL] = {};  // the tile's stored state
-    auto fetch = [&](int tile) {
-        const int t0 = tile * kRecurChunk + warp * kS;
-        if (tile < 0 || tile >= p.chunks || !on) return;
-#pragma unroll
-        for (int j = 0; j < CPL; ++j) sr[j] = p.states_in[((size_t)b * p.chunks + tile) * p.C + c + j];
-#pragma unroll
-        for (int s = 0; s < kS; ++s)
-            if (t0 + s < p.T) {
-                fr[s].load(f + (t0 + s) * p.fs[1]);
-                xr[s].load(x + (t0 + s) * p.xs[1]);
-                if (p.dh) dr[s].load(dh + (t0 + s) * p.ds[1]);
-            }
-    };
     const int rounds = (p.chunks + P - 1) / P;
-    // rank 0 holds the last tile of a round; tiles past the end are empty
-    int tile = rounds * P - 1 - rank, buf = 0;
-    fetch(tile);
+    // rank 0 holds the last tile of a round; tiles past the end of the sequence are empty
+    const int last = rounds * P - 1 - rank;
+    const int planes = p.dh ? 3 : 2;
+    auto issue = [&](int round) {
+        const int st = round % kBwdStages, t0 = (last - round * P) * kRecurChunk;
+        const uint32_t dst = smem_u32(stages) + st * 3 * kPlane, bar = smem_u32(&sh.full[st]);
+        mbar_arrive_expect_tx(bar, planes * kPlane);
+        tma_load_3d(dst, &tf, bar, c0, t0, b);
+        tma_load_3d(dst + kPlane, &tx, bar, c0, t0, b);
+        if (p.dh) tma_load_3d(dst + 2 * kPlane, &td, bar, c0, t0, b);
+    };
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sh.full[i]), 1);
+            mbar_init(smem_u32(&sh.joined[i]), 1);
+        }
+        fence_barrier_init();
+        if (TMA)
+            for (int i = 0; i < kBwdStages && i < rounds; ++i) issue(i);
+    }
+    F<N> carry = splat<N>(0.f), next_start = splat<N>(0.f);
+    if (on && p.dh_last) carry = widen(*reinterpret_cast<const Pack<float, N> *>(p.dh_last + bc));
+    P_ fr[TMA ? 1 : kS], xr[TMA ? 1 : kS], dr[TMA ? 1 : kS];
+    auto fetch = [&](int tile) {
+        const long long t0 = tile * kRecurChunk + warp * kS;
+        if (tile >= p.chunks || !on) return;
+        next_start = widen(*reinterpret_cast<const Pack<float, N> *>(p.states_in + ((size_t)b * p.chunks + tile) * p.C + c));
+        if constexpr (!TMA) {
+            const T *fp = static_cast<const T *>(p.f) + b * p.fs[0] + c + t0 * p.fs[1];
+            const T *xp = static_cast<const T *>(p.x) + b * p.xs[0] + c + t0 * p.xs[1];
+            const T *dp = static_cast<const T *>(p.dh) + b * p.ds[0] + c + t0 * p.ds[1];
+#pragma unroll
+            for (int s = 0; s < kS; ++s)
+                if (t0 + s < p.T) {
+                    fr[s].load(fp + s * p.fs[1]);
+                    xr[s].load(xp + s * p.xs[1]);
+                    if (p.dh) dr[s].load(dp + s * p.ds[1]);
+                }
+        }
+    };
+    fetch(last);
+    __syncthreads();
     if (P > 1) cluster_barrier();
-    for (int round = 0; round < rounds; ++round, tile -= P, buf ^= 1) {
-        const int t0 = tile * kRecurChunk + warp * kS;
+    bool ok = true;
+    int round = 0;
+    for (; round < rounds; ++round) {
+        const int tile = last - round * P, t0 = tile * kRecurChunk + warp * kS, buf = round & 1;
         const int n = min(max(p.T - t0, 0), kS);
         const unsigned cuts = RESET ? reset_bits(reset, t0, n, lane) : 0u;
-        float a[kS][CPL], eta[kS][CPL], xv[kS][CPL], dv[kS][CPL], start[CPL];
+        const unsigned char *mine = stages + (round % kBwdStages) * 3 * kPlane + warp * kS * kRowBytes + lane * 4;
+        if (TMA) ok &= mbar_wait(smem_u32(&sh.full[round % kBwdStages]), (round / kBwdStages) & 1, p.status, kSiteConsumerFull);
+        F<N> xv[TMA ? 1 : kS] = {}, dv[TMA ? 1 : kS] = {};
+        auto load_x = [&](int s) {
+            if constexpr (TMA) return widen(*reinterpret_cast<const P_ *>(mine + kPlane + s * kRowBytes));
+            else return xv[s];
+        };
+        auto load_d = [&](int s) {
+            if (!p.dh) return splat<N>(0.f);
+            if constexpr (TMA) return widen(*reinterpret_cast<const P_ *>(mine + 2 * kPlane + s * kRowBytes));
+            else return dv[s];
+        };
+        if constexpr (!TMA)
 #pragma unroll
-        for (int j = 0; j < CPL; ++j) start[j] = sr[j];
+            for (int s = 0; s < kS; ++s) {
+                xv[s] = s < n ? widen(xr[s]) : splat<N>(0.f);
+                dv[s] = s < n ? widen(dr[s]) : splat<N>(0.f);
+            }
+        F<N> a[kS], eta[kS], h = next_start, r;
 #pragma unroll
         for (int s = 0; s < kS; ++s) {
-            float fv[CPL];
-            unpack(fr[s], fv);
-            unpack(xr[s], xv[s]);
-            unpack(dr[s], dv[s]);
+            if constexpr (TMA) gates<T, MODE>(widen(*reinterpret_cast<const P_ *>(mine + s * kRowBytes)), a[s], eta[s]);
+            else gates<T, MODE>(widen(fr[s]), a[s], eta[s]);
+        }
+        if (n < kS) {  // tokens past the end, whose x and dh read as zeros: the identity
 #pragma unroll
-            for (int j = 0; j < CPL; ++j) {
-                gate<T, MODE>(fv[j], a[s][j], eta[s][j]);
-                if (!p.dh) dv[s][j] = 0.f;
+            for (int s = 0; s < kS; ++s)
                 if (s >= n) {
-                    a[s][j] = 1.f;
-                    eta[s][j] = xv[s][j] = dv[s][j] = 0.f;
+                    a[s] = splat<N>(1.f);
+                    eta[s] = splat<N>(0.f);
                 }
-            }
         }
         if (round + 1 < rounds) fetch(tile - P);
-        float A[CPL], H[CPL], R[CPL];
-#pragma unroll
-        for (int j = 0; j < CPL; ++j) {
-            A[j] = 1.f;
-            H[j] = R[j] = 0.f;
-        }
+        Map<N> mf = {splat<N>(1.f), splat<N>(0.f)};
+        F<N> back = splat<N>(0.f);
+        F<N> live = splat<N>(1.f);  // a_0 .. a_s, and zero from a reset on
 #pragma unroll
         for (int s = 0; s < kS; ++s) {
-            if (RESET && (cuts >> s & 1u))
-#pragma unroll
-                for (int j = 0; j < CPL; ++j) H[j] = 0.f;
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) {
-                H[j] = fmaf(a[s][j], H[j], MODE == kRecurMix ? eta[s][j] * xv[s][j] : xv[s][j]);
-                A[j] *= a[s][j];
+            if (RESET && (cuts >> s & 1u)) {
+                mf.c = splat<N>(0.f);
+                live = splat<N>(0.f);
             }
+            mf.c = fma(a[s], mf.c, MODE == kRecurMix ? mul(eta[s], load_x(s)) : load_x(s));
+            live = mul(live, a[s]);
+            // dh behind a reset does not count, whatever it is
+            if (!RESET || !(cuts & ((2u << s) - 1u))) back = fma(live, load_d(s), back);
+            mf.a = mul(mf.a, a[s]);
         }
-#pragma unroll
-        for (int s = kS - 1; s >= 0; --s) {
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) R[j] = a[s][j] * (dv[s][j] + R[j]);
-            if (RESET && (cuts >> s & 1u))
-#pragma unroll
-                for (int j = 0; j < CPL; ++j) R[j] = 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < CPL; ++j) {
-            sh.w[buf][0][warp][lane * CPL + j] = A[j];
-            sh.w[buf][1][warp][lane * CPL + j] = H[j];
-            sh.w[buf][2][warp][lane * CPL + j] = R[j];
-        }
+        sh.w[buf][warp][lane] = mf;
+        sh.r[buf][warp][lane] = back;
         if (RESET && lane == 0) sh.wcut[buf][warp] = cuts != 0;
-        __syncthreads();
-        float st[CPL];  // r behind this block's tile
+        ok = __syncthreads_and(ok);
+        if (!ok) break;
+        // every warp is done with the round before
+        if (TMA && threadIdx.x == 0 && round > 0 && round + 1 < rounds && round + 1 >= kBwdStages) issue(round + 1);
+        F<N> st = carry;  // r behind this block's tile
         if (P > 1) {
-            float TA[CPL], TR[CPL];
-            bool cut = false;
+            Map<N> total = {sh.w[buf][kW - 1][lane].a, sh.r[buf][kW - 1][lane]};
+            bool cut = RESET && sh.wcut[buf][kW - 1];
 #pragma unroll
-            for (int j = 0; j < CPL; ++j) {
-                TA[j] = 1.f;
-                TR[j] = 0.f;
-            }
-#pragma unroll
-            for (int i = kW - 1; i >= 0; --i) {
-                float wa[CPL], wr[CPL];
-                lds<CPL>(&sh.w[buf][0][i][lane * CPL], wa);
-                lds<CPL>(&sh.w[buf][2][i][lane * CPL], wr);
+            for (int i = kW - 2; i >= 0; --i) {
+                const Map<N> w = {sh.w[buf][i][lane].a, sh.r[buf][i][lane]};
                 const bool ci = RESET && sh.wcut[buf][i];
+                total.c = apply(w, total.c, ci);
+                total.a = mul(w.a, total.a);
                 cut |= ci;
-#pragma unroll
-                for (int j = 0; j < CPL; ++j) {
-                    TR[j] = ci ? wr[j] : fmaf(wa[j], TR[j], wr[j]);
-                    TA[j] *= wa[j];
-                }
             }
-            if (warp < P) {
-#pragma unroll
-                for (int j = 0; j < CPL; ++j) {
-                    st_remote(&sh.t[buf][0][rank][lane * CPL + j], warp, TA[j]);
-                    st_remote(&sh.t[buf][2][rank][lane * CPL + j], warp, TR[j]);
-                }
-                if (RESET && lane == 0) st_remote(&sh.tcut[buf][rank], warp, cut ? 1.f : 0.f);
-            }
-            cluster_barrier();
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) st[j] = carry[j];
-            for (int i = 0; i < P; ++i) {
-                float wa[CPL], wr[CPL];
-                lds<CPL>(&sh.t[buf][0][i][lane * CPL], wa);
-                lds<CPL>(&sh.t[buf][2][i][lane * CPL], wr);
-                const bool ci = RESET && sh.tcut[buf][i] != 0.f;
-#pragma unroll
-                for (int j = 0; j < CPL; ++j) {
-                    carry[j] = ci ? wr[j] : fmaf(wa[j], carry[j], wr[j]);
-                    if (i < rank) st[j] = carry[j];
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) st[j] = carry[j];
-        }
-        float h[CPL], r[CPL];
-#pragma unroll
-        for (int j = 0; j < CPL; ++j) {
-            h[j] = start[j];
-            r[j] = st[j];
+            st = join_blocks<N, RESET>(sh, totals, total, cut, carry, P, rank, buf, (round >> 1) & 1, p.status, ok);
         }
 #pragma unroll
-        for (int i = 0; i < kW; ++i) {
-            float wa[CPL], wh[CPL];
-            if (i < warp) {
-                lds<CPL>(&sh.w[buf][0][i][lane * CPL], wa);
-                lds<CPL>(&sh.w[buf][1][i][lane * CPL], wh);
-                const bool ci = RESET && sh.wcut[buf][i];
-#pragma unroll
-                for (int j = 0; j < CPL; ++j) h[j] = ci ? wh[j] : fmaf(wa[j], h[j], wh[j]);
-            }
-        }
+        for (int i = 0; i < kW - 1; ++i)
+            if (i < warp) h = apply(sh.w[buf][i][lane], h, RESET && sh.wcut[buf][i]);
+        r = st;
 #pragma unroll
         for (int i = kW - 1; i >= 0; --i) {
-            float wa[CPL], wr[CPL];
-            lds<CPL>(&sh.w[buf][0][i][lane * CPL], wa);
-            lds<CPL>(&sh.w[buf][2][i][lane * CPL], wr);
-            const bool ci = RESET && sh.wcut[buf][i];
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) {
-                st[j] = ci ? wr[j] : fmaf(wa[j], st[j], wr[j]);
-                if (i > warp) r[j] = st[j];
-            }
+            const Map<N> w = {sh.w[buf][i][lane].a, sh.r[buf][i][lane]};
+            st = apply(w, st, RESET && sh.wcut[buf][i]);
+            if (i == warp + 1) r = st;
         }
-        if (P == 1)
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) carry[j] = st[j];
-        // h_{t-1} forward, kept in place of x for what df needs of both
-        float hb[kS][CPL];
+        if (P == 1) carry = st;
+        // h_{t-1} [- x_t] in token order, then the outputs from the last token back
+        F<N> g[kS];
 #pragma unroll
         for (int s = 0; s < kS; ++s) {
-            if (RESET && (cuts >> s & 1u))
-#pragma unroll
-                for (int j = 0; j < CPL; ++j) h[j] = 0.f;
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) {
-                hb[s][j] = MODE == kRecurMix ? h[j] - xv[s][j] : h[j];
-                h[j] = fmaf(a[s][j], h[j], MODE == kRecurMix ? eta[s][j] * xv[s][j] : xv[s][j]);
-            }
+            if (RESET && (cuts >> s & 1u)) h = splat<N>(0.f);
+            const F<N> x = load_x(s);
+            g[s] = MODE == kRecurMix ? sub(h, x) : h;
+            h = fma(a[s], h, MODE == kRecurMix ? mul(eta[s], x) : x);
         }
         const size_t o = ((size_t)b * p.T + t0) * p.C + c;
+        T *dx = static_cast<T *>(p.dx) + o, *df = static_cast<T *>(p.df) + o;
 #pragma unroll
         for (int s = kS - 1; s >= 0; --s) {
-            float gx[CPL], gf[CPL];
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) {
-                const float sv = dv[s][j] + r[j];
-                r[j] = a[s][j] * sv;
-                gx[j] = MODE == kRecurMix ? eta[s][j] * sv : sv;
-                gf[j] = MODE == kRecurDecay ? sv * hb[s][j] : r[j] * hb[s][j] * eta[s][j];
-            }
-            if (RESET && (cuts >> s & 1u))
-#pragma unroll
-                for (int j = 0; j < CPL; ++j) r[j] = 0.f;
+            const F<N> sv = add(load_d(s), r);
+            r = mul(a[s], sv);
             if (on && s < n) {
-                Pack<T, CPL> q;
-                pack(q, gx);
-                q.store(static_cast<T *>(p.dx) + o + (size_t)s * p.C);
-                pack(q, gf);
-                q.store(static_cast<T *>(p.df) + o + (size_t)s * p.C);
+                put(dx + (size_t)s * p.C, MODE == kRecurMix ? mul(eta[s], sv) : sv);
+                put(df + (size_t)s * p.C, MODE == kRecurDecay ? mul(sv, g[s]) : mul(mul(r, g[s]), eta[s]));
             }
+            if (RESET && (cuts >> s & 1u)) r = splat<N>(0.f);
         }
     }
-    if (p.dh0 && on && rank == 0 && warp == 0)
-#pragma unroll
-        for (int j = 0; j < CPL; ++j) p.dh0[bc + j] = carry[j];
+    if (!ok && TMA && threadIdx.x == 0) drain(sh.full, min(rounds, max(round + 1, kBwdStages)), kBwdStages, p.status);
+    if (P > 1) cluster_barrier();
+    if (ok && p.dh0 && on && rank == 0 && warp == 0) put(p.dh0 + bc, carry);
 }
 
 RecurParams params_of(const RecurArgs &a)
@@ -589,6 +621,7 @@ RecurParams params_of(const RecurArgs &a)
         p.fs[i] = a.fs[i];
         p.ds[i] = a.ds[i];
     }
+    p.status = a.status;
     p.B = a.B;
     p.T = a.T;
     p.C = a.C;
@@ -598,54 +631,73 @@ RecurParams params_of(const RecurArgs &a)
 
 constexpr int kSMs = 152;
 
-template <typename K> int launch_clusters(K kernel, const RecurParams &p, int blocks, cudaStream_t st)
+template <typename... KArgs, typename... Args>
+int launch_clusters(void (*kernel)(KArgs...), int cluster, int blocks, int smem, cudaStream_t st, Args... args)
 {
+    if (smem > 40 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return -4;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(32 * kW);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = p.cluster;
+    at.val.clusterDim.x = cluster;
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? 0 : -4;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? 0 : -4;
 }
 
-template <typename T, int MODE, int CPL> int run_tiles(RecurParams p, bool bwd, cudaStream_t st)
+template <typename T, int MODE, bool RESET, bool TMA>
+int run_tiles(RecurParams p, const CUtensorMap *maps, bool bwd, cudaStream_t st)
 {
-    p.cblocks = (p.C + 32 * CPL - 1) / (32 * CPL);
+    constexpr int CH = TMA ? 128 / (int)sizeof(T) : 32;
+    p.cblocks = (p.C + CH - 1) / CH;
     const long long chains = (long long)p.B * p.cblocks;
     p.cluster = 1;
     while (p.cluster < 8 && chains * p.cluster < 2 * kSMs && p.cluster < p.chunks) p.cluster *= 2;
     const int blocks = (int)(chains * p.cluster);
+    const int totals = 128 + 2 * p.cluster * CH * 8;  // alignment, and the blocks' totals
     if (bwd)
-        return p.reset ? launch_clusters(ttt_recurrence_bwd_tile_kernel<T, MODE, CPL, true>, p, blocks, st)
-                       : launch_clusters(ttt_recurrence_bwd_tile_kernel<T, MODE, CPL, false>, p, blocks, st);
-    return p.reset ? launch_clusters(ttt_recurrence_fwd_tile_kernel<T, MODE, CPL, true>, p, blocks, st)
-                   : launch_clusters(ttt_recurrence_fwd_tile_kernel<T, MODE, CPL, false>, p, blocks, st);
+        return launch_clusters(ttt_recurrence_bwd_tile_kernel<T, MODE, RESET, TMA>, p.cluster, blocks,
+                               totals + (TMA ? kBwdStages * 3 * kPlane : 0), st, p, maps[0], maps[1], maps[2]);
+    return launch_clusters(ttt_recurrence_fwd_tile_kernel<T, MODE, RESET, TMA>, p.cluster, blocks,
+                           totals + (TMA ? kFwdStages * 2 * kPlane : 0), st, p, maps[0], maps[1]);
 }
 
-// Two bf16 channels a lane need even strides and pointers aligned to the pair.
-bool pairs_ok(const RecurArgs &a)
+// Descriptors of f, x and dh in boxes of kRecurChunk tokens x 128 bytes of channels, rows
+// past T and channels past C read as zeros.  False: plain loads instead (TMA wants
+// 16-byte pointers and strides; bf16 channels go in pairs, so C is even).
+bool make_maps(const RecurArgs &a, CUtensorMap *maps)
 {
-    long long m = a.C;
-    for (int i = 0; i < 2; ++i) m |= a.xs[i] | a.fs[i] | a.ds[i];
-    uintptr_t q = 0;
-    for (const void *v : {a.x, a.f, a.dh, (const void *)a.h, (const void *)a.dx, (const void *)a.df})
-        q |= reinterpret_cast<uintptr_t>(v);
-    return m % 2 == 0 && q % 4 == 0;
+    const int es = a.bf16 ? 2 : 4;
+    if (a.bf16 && a.C % 2) return false;
+    for (const void *v : {(const void *)a.h, (const void *)a.dx, (const void *)a.df})
+        if (reinterpret_cast<uintptr_t>(v) % 4) return false;
+    for (const void *v : {(const void *)a.h0, (const void *)a.dh_last, (const void *)a.h_last, (const void *)a.states,
+                          (const void *)a.dh0})
+        if (reinterpret_cast<uintptr_t>(v) % 8) return false;
+    const void *ptr[3] = {a.f, a.x, a.dh};
+    const long long *st[3] = {a.fs, a.xs, a.ds};
+    for (int i = 0; i < 3; ++i) {
+        if (!ptr[i]) continue;
+        const long long sb = a.B > 1 ? st[i][0] : (long long)a.T * st[i][1];
+        if (!encode_rows_map(&maps[i], ptr[i], a.bf16, a.C, a.T, a.B, st[i][1], sb, 128 / es, kRecurChunk)) return false;
+    }
+    return true;
 }
 
 template <typename T, int MODE> int run(const RecurArgs &a, bool bwd)
 {
     const RecurParams p = params_of(a);
     if (a.T > kS) {
-        // a lane holds 4 bytes of a token: one fp32 channel, two of bf16
-        if constexpr (sizeof(T) == 2)
-            if (pairs_ok(a)) return run_tiles<T, MODE, 2>(p, bwd, a.stream);
-        return run_tiles<T, MODE, 1>(p, bwd, a.stream);
+        CUtensorMap maps[3] = {};
+        if (make_maps(a, maps))
+            return a.reset ? run_tiles<T, MODE, true, true>(p, maps, bwd, a.stream)
+                           : run_tiles<T, MODE, false, true>(p, maps, bwd, a.stream);
+        return a.reset ? run_tiles<T, MODE, true, false>(p, maps, bwd, a.stream)
+                       : run_tiles<T, MODE, false, false>(p, maps, bwd, a.stream);
     }
     const dim3 grid((a.C + kThreads - 1) / kThreads, a.B);
     if (bwd) ttt_recurrence_bwd_kernel<T, MODE><<<grid, kThreads, 0, a.stream>>>(p);
