@@ -7,6 +7,8 @@
 //     dx = c s,  dL/da = s (h_{t-1} [- x_t for mix]),  df = dL/da a (1 - a) unless a = f,
 // with h_{t-1} computed again from the states that the forward pass leaves every
 // kRecurChunk tokens: no rounded h is read, and no more bytes than reading it would take.
+#include <mutex>
+
 #include <cuda.h>
 
 #include "ttt_device.cuh"
@@ -30,6 +32,26 @@ struct RecurParams {
     int *status;           // device status word (timeouts)
 };
 
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// exp(-|f|): for bf16 tensors by one ex2 (good to 2^-20 over the range that matters), for
+// fp32 the accurate one
+template <typename T> __device__ __forceinline__ float exp_neg_abs(float f)
+{
+    return sizeof(T) == 2 ? exp2_approx(fabsf(f) * -1.4426950408889634f) : expf(-fabsf(f));
+}
+
 // a and 1 - a, each accurate on its own: with e = exp(-|f|) <= 1 the smaller of the two is
 // e / (1 + e) and the larger 1 / (1 + e), so neither is a difference and nothing overflows.
 template <typename T, int MODE> __device__ __forceinline__ void gate(float f, float &a, float &eta)
@@ -39,9 +61,7 @@ template <typename T, int MODE> __device__ __forceinline__ void gate(float f, fl
         eta = 1.f;
         return;
     }
-    // bf16 tensors: exp good to 2^-20; fp32: the accurate one
-    const float e = sizeof(T) == 2 ? __expf(-fabsf(f)) : expf(-fabsf(f));
-    const float big = __fdividef(1.f, 1.f + e), small = e * big;
+    const float e = exp_neg_abs<T>(f), big = rcp_approx(1.f + e), small = e * big;
     a = f > 0.f ? big : small;
     eta = f > 0.f ? small : big;
 }
@@ -136,6 +156,7 @@ constexpr int kS = 16, kW = 8;
 static_assert(kS * kW == kRecurChunk, "a tile is one stored-state chunk");
 constexpr int kRowBytes = 128;                       // a tile's row of one tensor, by TMA
 constexpr int kPlane = kRecurChunk * kRowBytes;      // one tensor of a stage
+constexpr int kMaxCluster = 16;
 constexpr int kFwdStages = 2, kBwdStages = 2;
 
 // N channels of a lane, with paired instructions for two.
@@ -155,7 +176,7 @@ __device__ __forceinline__ F<2> mul(F<2> a, F<2> b) { return f2(__fmul2_rn(f2(a)
 __device__ __forceinline__ F<1> add(F<1> a, F<1> b) { return {a.x + b.x}; }
 __device__ __forceinline__ F<2> add(F<2> a, F<2> b) { return f2(__fadd2_rn(f2(a), f2(b))); }
 __device__ __forceinline__ F<1> sub(F<1> a, F<1> b) { return {a.x - b.x}; }
-__device__ __forceinline__ F<2> sub(F<2> a, F<2> b) { return f2(__fadd2_rn(f2(a), make_float2(-b.x, -b.y))); }
+__device__ __forceinline__ F<2> sub(F<2> a, F<2> b) { return f2(__ffma2_rn(f2(b), make_float2(-1.f, -1.f), f2(a))); }
 template <int N> __device__ __forceinline__ F<N> splat(float v);
 template <> __device__ __forceinline__ F<1> splat<1>(float v) { return {v}; }
 template <> __device__ __forceinline__ F<2> splat<2>(float v) { return {v, v}; }
@@ -166,8 +187,15 @@ template <typename T, int MODE> __device__ __forceinline__ void gates(F<1> f, F<
 }
 template <typename T, int MODE> __device__ __forceinline__ void gates(F<2> f, F<2> &a, F<2> &eta)
 {
-    gate<T, MODE>(f.x, a.x, eta.x);
-    gate<T, MODE>(f.y, a.y, eta.y);
+    if (MODE == kRecurDecay) {
+        a = f;
+        eta = {1.f, 1.f};
+        return;
+    }
+    const F<2> e = {exp_neg_abs<T>(f.x), exp_neg_abs<T>(f.y)}, d = add(e, F<2>{1.f, 1.f});
+    const F<2> big = {rcp_approx(d.x), rcp_approx(d.y)}, small = mul(e, big);
+    a = {f.x > 0.f ? big.x : small.x, f.y > 0.f ? big.y : small.y};
+    eta = {f.x > 0.f ? small.x : big.x, f.y > 0.f ? small.y : big.y};
 }
 template <typename T> __device__ __forceinline__ F<1> widen(const Pack<T, 1> &p)
 {
@@ -213,7 +241,7 @@ template <int N, bool BWD> struct TileShared {
     Map<N> w[2][kW][32];
     F<N> r[BWD ? 2 : 1][BWD ? kW : 1][32];
     int wcut[2][kW];
-    int tcut[2][8];
+    int tcut[2][kMaxCluster];
     unsigned long long full[2], joined[2];  // mbarriers: a stage's copies, the cluster's totals
 };
 
@@ -264,10 +292,10 @@ __device__ __forceinline__ F<N> join_blocks(TileShared<N, BWD> &sh, Map<N> *tota
     const uint32_t bar = smem_u32(&sh.joined[buf]);
     totals += buf * P * 32 + lane;
     if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, P * (32 * (int)sizeof(Map<N>) + (RESET ? 4 : 0)));
-    if (warp < P) {  // warp i tells block i
-        const uint32_t rbar = remote(bar, warp);
-        send(remote(smem_u32(totals + rank * 32), warp), rbar, total);
-        if (RESET && lane == 0) send(remote(smem_u32(&sh.tcut[buf][rank]), warp), rbar, (int)cut);
+    for (int i = warp; i < P; i += kW) {  // warp i tells block i (and i + kW)
+        const uint32_t rbar = remote(bar, i);
+        send(remote(smem_u32(totals + rank * 32), i), rbar, total);
+        if (RESET && lane == 0) send(remote(smem_u32(&sh.tcut[buf][rank]), i), rbar, (int)cut);
     }
     ok &= mbar_wait(bar, phase, status, kSiteStage);
     F<N> before = carry;
@@ -277,6 +305,18 @@ __device__ __forceinline__ F<N> join_blocks(TileShared<N, BWD> &sh, Map<N> *tota
     }
     return before;
 }
+
+// A box of shared memory to a tensor; elements out of range are dropped.
+__device__ __forceinline__ void tma_store_3d(const void *tmap, uint32_t src, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(tmap)),
+                 "r"(src), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// this thread's stores have read their shared memory
+__device__ __forceinline__ void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
 // The reset bits of a warp's tokens t0 .. t0 + n - 1.
 __device__ __forceinline__ unsigned reset_bits(const unsigned char *reset, int t0, int n, int lane)
@@ -295,14 +335,14 @@ __device__ __forceinline__ void drain(unsigned long long *full, int rounds_issue
 template <typename T, int MODE, bool RESET, bool TMA>
 __global__ void __launch_bounds__(32 * kW, 2)
     ttt_recurrence_fwd_tile_kernel(const __grid_constant__ RecurParams p, const __grid_constant__ CUtensorMap tf,
-                                   const __grid_constant__ CUtensorMap tx)
+                                   const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap th)
 {
     constexpr int N = TMA ? 4 / (int)sizeof(T) : 1, CH = 32 * N;
     using P_ = Pack<T, N>;
     __shared__ TileShared<N, false> sh;
     extern __shared__ unsigned char dynamic[];
-    unsigned char *stages = dynamic + (-smem_u32(dynamic) & 127u);  // TMA: [kFwdStages][f, x][kPlane]
-    Map<N> *totals = reinterpret_cast<Map<N> *>(stages + (TMA ? kFwdStages * 2 * kPlane : 0));
+    unsigned char *stages = dynamic + (-smem_u32(dynamic) & 127u);  // TMA: [kFwdStages][f, x][kPlane], h [kPlane]
+    Map<N> *totals = reinterpret_cast<Map<N> *>(stages + (TMA ? (kFwdStages * 2 + 1) * kPlane : 0));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int P = p.cluster, rank = P > 1 ? (int)cluster_rank() : 0;
     const int chain = blockIdx.x / P, b = chain / p.cblocks, c0 = (chain % p.cblocks) * CH, c = c0 + lane * N;
@@ -408,14 +448,32 @@ __global__ void __launch_bounds__(32 * kW, 2)
             if (i + 1 == warp) h = st;
         }
         if (P == 1) carry = st;
-        T *hp = static_cast<T *>(p.h) + ((size_t)b * p.T + t0) * p.C + c;
+        if constexpr (TMA) {
+            // the warp's rows through shared memory: no addresses, and the copy drops what is
+            // out of range
+            unsigned char *out = stages + kFwdStages * 2 * kPlane + warp * kS * kRowBytes;
+            if (lane == 0) tma_store_read();
+            __syncwarp();
 #pragma unroll
-        for (int s = 0; s < kS; ++s) {
-            if (RESET && (cuts >> s & 1u)) h = splat<N>(0.f);
-            h = fma(a[s], h, u[s]);
-            if (on && s < n) put(hp + (size_t)s * p.C, h);
+            for (int s = 0; s < kS; ++s) {
+                if (RESET && (cuts >> s & 1u)) h = splat<N>(0.f);
+                h = fma(a[s], h, u[s]);
+                put(reinterpret_cast<T *>(out + s * kRowBytes + lane * 4), h);
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0 && n > 0) tma_store_3d(&th, smem_u32(out), c0, t0, b);
+        } else {
+            T *hp = static_cast<T *>(p.h) + ((size_t)b * p.T + t0) * p.C + c;
+#pragma unroll
+            for (int s = 0; s < kS; ++s) {
+                if (RESET && (cuts >> s & 1u)) h = splat<N>(0.f);
+                h = fma(a[s], h, u[s]);
+                if (on && s < n) put(hp + (size_t)s * p.C, h);
+            }
         }
     }
+    if (TMA && lane == 0) tma_store_read();
     if (!ok && TMA && threadIdx.x == 0) drain(sh.full, min(rounds, round + kFwdStages), kFwdStages, p.status);
     if (P > 1) cluster_barrier();  // no block leaves while another may write to it
     if (ok && p.h_last && on && rank == 0 && warp == 0) put(p.h_last + bc, carry);
@@ -429,7 +487,8 @@ __global__ void __launch_bounds__(32 * kW, 2)
 template <typename T, int MODE, bool RESET, bool TMA>
 __global__ void __launch_bounds__(32 * kW, 2)
     ttt_recurrence_bwd_tile_kernel(const __grid_constant__ RecurParams p, const __grid_constant__ CUtensorMap tf,
-                                   const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap td)
+                                   const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap td,
+                                   const __grid_constant__ CUtensorMap tdx, const __grid_constant__ CUtensorMap tdf)
 {
     constexpr int N = TMA ? 4 / (int)sizeof(T) : 1, CH = 32 * N;
     using P_ = Pack<T, N>;
@@ -493,7 +552,7 @@ __global__ void __launch_bounds__(32 * kW, 2)
         const int tile = last - round * P, t0 = tile * kRecurChunk + warp * kS, buf = round & 1;
         const int n = min(max(p.T - t0, 0), kS);
         const unsigned cuts = RESET ? reset_bits(reset, t0, n, lane) : 0u;
-        const unsigned char *mine = stages + (round % kBwdStages) * 3 * kPlane + warp * kS * kRowBytes + lane * 4;
+        unsigned char *rows = stages + (round % kBwdStages) * 3 * kPlane + warp * kS * kRowBytes, *mine = rows + lane * 4;
         if (TMA) ok &= mbar_wait(smem_u32(&sh.full[round % kBwdStages]), (round / kBwdStages) & 1, p.status, kSiteConsumerFull);
         F<N> xv[TMA ? 1 : kS] = {}, dv[TMA ? 1 : kS] = {};
         auto load_x = [&](int s) {
@@ -536,14 +595,15 @@ __global__ void __launch_bounds__(32 * kW, 2)
                 live = splat<N>(0.f);
             }
             mf.c = fma(a[s], mf.c, MODE == kRecurMix ? mul(eta[s], load_x(s)) : load_x(s));
-            live = mul(live, a[s]);
-            // dh behind a reset does not count, whatever it is
-            if (!RESET || !(cuts & ((2u << s) - 1u))) back = fma(live, load_d(s), back);
             mf.a = mul(mf.a, a[s]);
+            // dh behind a reset does not count, whatever it is
+            live = RESET ? mul(live, a[s]) : mf.a;
+            if (!RESET || !(cuts & ((2u << s) - 1u))) back = fma(live, load_d(s), back);
         }
         sh.w[buf][warp][lane] = mf;
         sh.r[buf][warp][lane] = back;
         if (RESET && lane == 0) sh.wcut[buf][warp] = cuts != 0;
+        if (TMA && lane == 0) tma_store_read();  // the round before has left its stage
         ok = __syncthreads_and(ok);
         if (!ok) break;
         // every warp is done with the round before
@@ -588,13 +648,27 @@ __global__ void __launch_bounds__(32 * kW, 2)
         for (int s = kS - 1; s >= 0; --s) {
             const F<N> sv = add(load_d(s), r);
             r = mul(a[s], sv);
-            if (on && s < n) {
-                put(dx + (size_t)s * p.C, MODE == kRecurMix ? mul(eta[s], sv) : sv);
-                put(df + (size_t)s * p.C, MODE == kRecurDecay ? mul(sv, g[s]) : mul(mul(r, g[s]), eta[s]));
+            const F<N> gx = MODE == kRecurMix ? mul(eta[s], sv) : sv;
+            const F<N> gf = MODE == kRecurDecay ? mul(sv, g[s]) : mul(mul(r, g[s]), eta[s]);
+            if constexpr (TMA) {  // over x and dh, which this lane has read
+                put(reinterpret_cast<T *>(mine + kPlane + s * kRowBytes), gx);
+                put(reinterpret_cast<T *>(mine + 2 * kPlane + s * kRowBytes), gf);
+            } else if (on && s < n) {
+                put(dx + (size_t)s * p.C, gx);
+                put(df + (size_t)s * p.C, gf);
             }
             if (RESET && (cuts >> s & 1u)) r = splat<N>(0.f);
         }
+        if constexpr (TMA) {
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0 && n > 0) {
+                tma_store_3d(&tdx, smem_u32(rows + kPlane), c0, t0, b);
+                tma_store_3d(&tdf, smem_u32(rows + 2 * kPlane), c0, t0, b);
+            }
+        }
     }
+    if (TMA && lane == 0) tma_store_read();
     if (!ok && TMA && threadIdx.x == 0) drain(sh.full, min(rounds, max(round + 1, kBwdStages)), kBwdStages, p.status);
     if (P > 1) cluster_barrier();
     if (ok && p.dh0 && on && rank == 0 && warp == 0) put(p.dh0 + bc, carry);
@@ -629,62 +703,137 @@ RecurParams params_of(const RecurArgs &a)
     return p;
 }
 
-constexpr int kSMs = 152;
-
-template <typename... KArgs, typename... Args>
-int launch_clusters(void (*kernel)(KArgs...), int cluster, int blocks, int smem, cudaStream_t st, Args... args)
+template <typename... KArgs>
+bool cluster_config(void (*kernel)(KArgs...), int cluster, int blocks, int smem, cudaStream_t st, cudaLaunchConfig_t &cfg,
+                    cudaLaunchAttribute &at)
 {
-    if (smem > 40 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return -4;
-    cudaLaunchConfig_t cfg = {};
+    if (cluster > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return false;
+    if (smem > 40 * 1024 &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return false;
+    cfg = {};
     cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(32 * kW);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = cluster;
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? 0 : -4;
+    return true;
+}
+
+// How many clusters of P blocks the GPU holds at once: as many blocks to an SM as fit
+// (any), and one to an SM (alone).
+struct Capacity {
+    int any[kMaxCluster + 1], alone[kMaxCluster + 1];
+};
+
+template <typename... KArgs> Capacity query_capacity(void (*kernel)(KArgs...), int smem, int per_block)
+{
+    Capacity c = {};
+    for (int P = 1; P <= kMaxCluster; ++P)
+        for (int one = 0; one < 2; ++one) {
+            cudaLaunchConfig_t cfg;
+            cudaLaunchAttribute at;
+            int n = 0;
+            // more than half of an SM's shared memory: no second block beside it
+            const int need = smem + per_block * P, bytes = one && need < 128 * 1024 ? 128 * 1024 : need;
+            if (!cluster_config(kernel, P, P, bytes, nullptr, cfg, at) ||
+                cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                n = 0;
+            }
+            (one ? c.alone : c.any)[P] = n;
+        }
+    return c;
+}
+
+// Blocks of a cluster.  A round of a block alone on its SM is the unit of time, 1.2 us
+// forward and 2.1 us backward (bf16, mix); 1.33 with the exchange between blocks; two
+// blocks on an SM take 1.95 each; a start costs about 3, that of a later wave of clusters
+// 6.  Timed over 12 shapes of 1 .. 768 chains and 2 .. 256 chunks with every P of 1 .. 16,
+// this picks the fastest P or one within 6% of it: 64 chains of 256 chunks forward 150 us
+// at P = 4 against 305, 203, 166 at 1, 2, 8; 12 chains 50 us at 16 against 303 and 59 at 1
+// and 8; 192 chains of 8 chunks 20 us at 1 against 26 and 29 at 2 and 4.
+int plan_cluster(long long chains, int chunks, const Capacity &cap)
+{
+    int best = 1;
+    double least = 0.0;
+    for (int P = 1; P <= kMaxCluster && P <= chunks; ++P) {
+        if (cap.any[P] < 1) continue;
+        const int rounds = (chunks + P - 1) / P;
+        const long long full = chains / cap.any[P], rest = chains % cap.any[P];
+        const double later = P > 1 ? 6.0 : 3.0;
+        double t = full * (rounds * 1.95 + later) + 3.0 - (full ? later : 0.0);
+        if (rest) t += rounds * (rest > cap.alone[P] ? 1.95 : P > 1 ? 1.33 : 1.0) + (full ? later : 0.0);
+        if (P == 1 || t < least) {
+            least = t;
+            best = P;
+        }
+    }
+    return best;
+}
+
+template <typename... KArgs, typename... Args>
+int launch_tiles(void (*kernel)(KArgs...), RecurParams p, int ch, int smem, cudaStream_t st, Args... maps)
+{
+    p.cblocks = (p.C + ch - 1) / ch;
+    const long long chains = (long long)p.B * p.cblocks;
+    const int per_block = 2 * ch * 8;  // each block's totals, twice
+    smem += 128;                       // alignment
+    static std::mutex mu;
+    static Capacity caps[64];
+    static bool known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -4;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!known[dev]) caps[dev] = query_capacity(kernel, smem, per_block);
+        known[dev] = true;
+    }
+    p.cluster = plan_cluster(chains, p.chunks, caps[dev]);
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute at;
+    if (chains * p.cluster > 0x7fffffffLL ||
+        !cluster_config(kernel, p.cluster, (int)(chains * p.cluster), smem + per_block * p.cluster, st, cfg, at))
+        return -4;
+    return cudaLaunchKernelEx(&cfg, kernel, p, maps...) == cudaSuccess ? 0 : -4;
 }
 
 template <typename T, int MODE, bool RESET, bool TMA>
-int run_tiles(RecurParams p, const CUtensorMap *maps, bool bwd, cudaStream_t st)
+int run_tiles(const RecurParams &p, const CUtensorMap *maps, bool bwd, cudaStream_t st)
 {
     constexpr int CH = TMA ? 128 / (int)sizeof(T) : 32;
-    p.cblocks = (p.C + CH - 1) / CH;
-    const long long chains = (long long)p.B * p.cblocks;
-    p.cluster = 1;
-    while (p.cluster < 8 && chains * p.cluster < 2 * kSMs && p.cluster < p.chunks) p.cluster *= 2;
-    const int blocks = (int)(chains * p.cluster);
-    const int totals = 128 + 2 * p.cluster * CH * 8;  // alignment, and the blocks' totals
     if (bwd)
-        return launch_clusters(ttt_recurrence_bwd_tile_kernel<T, MODE, RESET, TMA>, p.cluster, blocks,
-                               totals + (TMA ? kBwdStages * 3 * kPlane : 0), st, p, maps[0], maps[1], maps[2]);
-    return launch_clusters(ttt_recurrence_fwd_tile_kernel<T, MODE, RESET, TMA>, p.cluster, blocks,
-                           totals + (TMA ? kFwdStages * 2 * kPlane : 0), st, p, maps[0], maps[1]);
+        return launch_tiles(ttt_recurrence_bwd_tile_kernel<T, MODE, RESET, TMA>, p, CH, TMA ? kBwdStages * 3 * kPlane : 0,
+                            st, maps[0], maps[1], maps[2], maps[3], maps[4]);
+    return launch_tiles(ttt_recurrence_fwd_tile_kernel<T, MODE, RESET, TMA>, p, CH,
+                        TMA ? (kFwdStages * 2 + 1) * kPlane : 0, st, maps[0], maps[1], maps[3]);
 }
 
-// Descriptors of f, x and dh in boxes of kRecurChunk tokens x 128 bytes of channels, rows
-// past T and channels past C read as zeros.  False: plain loads instead (TMA wants
-// 16-byte pointers and strides; bf16 channels go in pairs, so C is even).
-bool make_maps(const RecurArgs &a, CUtensorMap *maps)
+// Descriptors of f, x and dh in boxes of kRecurChunk tokens x 128 bytes of channels (rows
+// past T and channels past C read as zeros) and of the outputs, in a warp's kS tokens.
+// False: plain loads and stores instead (TMA wants 16-byte pointers and strides).
+bool make_maps(const RecurArgs &a, bool bwd, CUtensorMap *maps)
 {
-    const int es = a.bf16 ? 2 : 4;
-    if (a.bf16 && a.C % 2) return false;
-    for (const void *v : {(const void *)a.h, (const void *)a.dx, (const void *)a.df})
-        if (reinterpret_cast<uintptr_t>(v) % 4) return false;
+    const int es = a.bf16 ? 2 : 4, cols = 128 / es;
     for (const void *v : {(const void *)a.h0, (const void *)a.dh_last, (const void *)a.h_last, (const void *)a.states,
                           (const void *)a.dh0})
         if (reinterpret_cast<uintptr_t>(v) % 8) return false;
-    const void *ptr[3] = {a.f, a.x, a.dh};
+    const void *in[3] = {a.f, a.x, a.dh};
     const long long *st[3] = {a.fs, a.xs, a.ds};
     for (int i = 0; i < 3; ++i) {
-        if (!ptr[i]) continue;
+        if (!in[i]) continue;
         const long long sb = a.B > 1 ? st[i][0] : (long long)a.T * st[i][1];
-        if (!encode_rows_map(&maps[i], ptr[i], a.bf16, a.C, a.T, a.B, st[i][1], sb, 128 / es, kRecurChunk)) return false;
+        if (!encode_rows_map(&maps[i], in[i], a.bf16, a.C, a.T, a.B, st[i][1], sb, cols, kRecurChunk)) return false;
     }
+    void *out[2] = {bwd ? a.dx : a.h, bwd ? a.df : nullptr};
+    for (int i = 0; i < 2; ++i)
+        if (out[i] && !encode_rows_map(&maps[3 + i], out[i], a.bf16, a.C, a.T, a.B, a.C, (long long)a.T * a.C, cols, kS))
+            return false;
     return true;
 }
 
@@ -692,8 +841,8 @@ template <typename T, int MODE> int run(const RecurArgs &a, bool bwd)
 {
     const RecurParams p = params_of(a);
     if (a.T > kS) {
-        CUtensorMap maps[3] = {};
-        if (make_maps(a, maps))
+        CUtensorMap maps[5] = {};
+        if (make_maps(a, bwd, maps))
             return a.reset ? run_tiles<T, MODE, true, true>(p, maps, bwd, a.stream)
                            : run_tiles<T, MODE, false, true>(p, maps, bwd, a.stream);
         return a.reset ? run_tiles<T, MODE, true, false>(p, maps, bwd, a.stream)
