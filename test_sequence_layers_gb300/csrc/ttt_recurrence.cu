@@ -143,8 +143,9 @@ __global__ void __launch_bounds__(kThreads) ttt_recurrence_bwd_kernel(const __gr
 //
 // A warp takes kS tokens of 32 CPL channels, a block of kW warps a tile of kRecurChunk
 // tokens, a cluster of P blocks P neighbouring tiles, and the cluster walks along the
-// sequence in rounds of P tiles.  Every tensor is read once, by TMA into a ring of stages
-// (TMA; rows or pointers that are not 16-byte aligned by plain loads a round ahead).  A
+// sequence in rounds of P tiles.  Every tensor is read once, by TMA into a ring of stages;
+// where rows or pointers are not 16-byte aligned (TMA = false) every lane copies its own
+// channels into the same places, fp32 a round ahead with cp.async.  A
 // warp folds its tokens into one map h -> A h + H (the product of the decays, the tokens'
 // own contribution); the warps' maps are joined in shared memory, the blocks' totals
 // through the cluster's distributed shared memory (stores that complete on the reader's
@@ -222,6 +223,57 @@ template <typename T> __device__ __forceinline__ void put(T *p, F<2> a)
     Pack<T, 2> q;
     pack(q, v);
     q.store(p);
+}
+
+// A lane's channels of a [B,C] fp32 array (WIDE: C a multiple of N, aligned to N).
+template <int N, bool WIDE> __device__ __forceinline__ F<N> get_state(const float *p, int c, int C)
+{
+    if constexpr (WIDE) return widen(*reinterpret_cast<const Pack<float, N> *>(p + c));
+    F<N> v = splat<N>(0.f);
+    float *f = &v.x;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        if (c + j < C) f[j] = p[c + j];
+    return v;
+}
+template <int N, bool WIDE, typename T> __device__ __forceinline__ void put_part(T *p, int c, int C, F<N> v)
+{
+    if constexpr (WIDE) {
+        put(p + c, v);
+    } else {
+        const float *f = &v.x;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (c + j < C) st1(p + c + j, f[j]);
+    }
+}
+
+// A lane's channels of a warp's tokens t0 .. t0 + n - 1 into the stage, zeros behind them:
+// cp.async for fp32, loads and stores for bf16.
+template <typename T, int N>
+__device__ __forceinline__ void copy_rows(const T *src, long long stride, int c, int C, int n, unsigned char *dst)
+{
+    src += c;
+    if (n == kS && c + N <= C) {
+#pragma unroll
+        for (int s = 0; s < kS; ++s, src += stride) {
+            if constexpr (N == 1) copy_async4(dst + s * kRowBytes, src);
+            else *reinterpret_cast<uint32_t *>(dst + s * kRowBytes) = pack2(ld1(src), ld1(src + 1));
+        }
+        return;
+    }
+    src -= c;
+    for (int s = 0; s < kS; ++s, dst += kRowBytes) {
+        if (s < n && c < C && N == 1) {
+            copy_async4(dst, src + s * stride + c);
+        } else {
+            float v[2] = {0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (s < n && c + j < C) v[j] = ld1(src + s * stride + c + j);
+            *reinterpret_cast<uint32_t *>(dst) = N == 1 ? 0u : pack2(v[0], v[1]);
+        }
+    }
 }
 
 // A map of one direction: v -> a v + c.
@@ -337,18 +389,18 @@ __global__ void __launch_bounds__(32 * kW, 2)
     ttt_recurrence_fwd_tile_kernel(const __grid_constant__ RecurParams p, const __grid_constant__ CUtensorMap tf,
                                    const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap th)
 {
-    constexpr int N = TMA ? 4 / (int)sizeof(T) : 1, CH = 32 * N;
+    constexpr int N = 4 / (int)sizeof(T), CH = 32 * N;
     using P_ = Pack<T, N>;
     __shared__ TileShared<N, false> sh;
     extern __shared__ unsigned char dynamic[];
-    unsigned char *stages = dynamic + (-smem_u32(dynamic) & 127u);  // TMA: [kFwdStages][f, x][kPlane], h [kPlane]
-    Map<N> *totals = reinterpret_cast<Map<N> *>(stages + (TMA ? (kFwdStages * 2 + 1) * kPlane : 0));
+    unsigned char *stages = dynamic + (-smem_u32(dynamic) & 127u);  // [kFwdStages][f, x][kPlane], h [kPlane]
+    Map<N> *totals = reinterpret_cast<Map<N> *>(stages + (kFwdStages * 2 + 1) * kPlane);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int P = p.cluster, rank = P > 1 ? (int)cluster_rank() : 0;
     const int chain = blockIdx.x / P, b = chain / p.cblocks, c0 = (chain % p.cblocks) * CH, c = c0 + lane * N;
-    const bool on = c < p.C;  // N divides C
+    const bool on = c < p.C;
     const unsigned char *reset = RESET ? p.reset + (size_t)b * p.T : nullptr;
-    const size_t bc = (size_t)b * p.C + c;
+    const size_t bC = (size_t)b * p.C;
     const int rounds = (p.chunks + P - 1) / P;
     auto issue = [&](int round) {
         const int st = round % kFwdStages;
@@ -367,20 +419,19 @@ __global__ void __launch_bounds__(32 * kW, 2)
             for (int i = 0; i < kFwdStages && i < rounds; ++i) issue(i);
     }
     F<N> carry = splat<N>(0.f);
-    if (on && p.h0) carry = widen(*reinterpret_cast<const Pack<float, N> *>(p.h0 + bc));
-    P_ fr[kS], xr[kS];
-    auto fetch = [&](int t0) {
-        const T *fp = static_cast<const T *>(p.f) + b * p.fs[0] + c + t0 * p.fs[1];
-        const T *xp = static_cast<const T *>(p.x) + b * p.xs[0] + c + t0 * p.xs[1];
-#pragma unroll
-        for (int s = 0; s < kS; ++s)
-            if (on && t0 + s < p.T) {
-                fr[s].load(fp + s * p.fs[1]);
-                xr[s].load(xp + s * p.xs[1]);
-            }
+    if (on && p.h0) carry = get_state<N, TMA>(p.h0 + bC, c, p.C);
+    auto copy = [&](int round) {  // not TMA: this lane's part of its warp's tokens
+        const long long t0 = (long long)(round * P + rank) * kRecurChunk + warp * kS;
+        const int n = (int)min(max(p.T - t0, 0LL), (long long)kS);
+        unsigned char *dst = stages + (round % kFwdStages) * 2 * kPlane + warp * kS * kRowBytes + lane * 4;
+        copy_rows<T, N>(static_cast<const T *>(p.f) + b * p.fs[0] + t0 * p.fs[1], p.fs[1], c, p.C, n, dst);
+        copy_rows<T, N>(static_cast<const T *>(p.x) + b * p.xs[0] + t0 * p.xs[1], p.xs[1], c, p.C, n, dst + kPlane);
     };
     int t0 = rank * kRecurChunk + warp * kS;
-    if (!TMA) fetch(t0);
+    if (!TMA) {
+        copy(0);
+        copy_commit();
+    }
     __syncthreads();
     if (P > 1) cluster_barrier();  // every block runs, its barriers set, before it is written to
     bool ok = true;
@@ -390,20 +441,22 @@ __global__ void __launch_bounds__(32 * kW, 2)
         const int n = min(max(p.T - t0, 0), kS);  // this warp's tokens
         const unsigned cuts = RESET ? reset_bits(reset, t0, n, lane) : 0u;
         const unsigned char *mine = stages + (round % kFwdStages) * 2 * kPlane + warp * kS * kRowBytes + lane * 4;
-        if (TMA) ok &= mbar_wait(smem_u32(&sh.full[round % kFwdStages]), (round / kFwdStages) & 1, p.status, kSiteConsumerFull);
+        if (TMA) {
+            ok &= mbar_wait(smem_u32(&sh.full[round % kFwdStages]), (round / kFwdStages) & 1, p.status, kSiteConsumerFull);
+        } else {
+            if (round + 1 < rounds) copy(round + 1);
+            copy_commit();
+            copy_wait<1>();
+        }
         F<N> a[kS], u[kS];
         Map<N> m = {splat<N>(1.f), splat<N>(0.f)};
 #pragma unroll
         for (int s = 0; s < kS; ++s) {
-            if (TMA) {
-                fr[s] = *reinterpret_cast<const P_ *>(mine + s * kRowBytes);
-                xr[s] = *reinterpret_cast<const P_ *>(mine + kPlane + s * kRowBytes);
-            }
+            const F<N> x = widen(*reinterpret_cast<const P_ *>(mine + kPlane + s * kRowBytes));
             F<N> eta;
-            gates<T, MODE>(widen(fr[s]), a[s], eta);
-            u[s] = MODE == kRecurMix ? mul(eta, widen(xr[s])) : widen(xr[s]);
+            gates<T, MODE>(widen(*reinterpret_cast<const P_ *>(mine + s * kRowBytes)), a[s], eta);
+            u[s] = MODE == kRecurMix ? mul(eta, x) : x;
         }
-        if (!TMA && round + 1 < rounds) fetch(t0 + P * kRecurChunk);
         if (n < kS) {  // tokens past the end: the identity
 #pragma unroll
             for (int s = 0; s < kS; ++s)
@@ -439,7 +492,7 @@ __global__ void __launch_bounds__(32 * kW, 2)
             st = join_blocks<N, RESET>(sh, totals, total, cut, carry, P, rank, buf, (round >> 1) & 1, p.status, ok);
         }
         if (warp == 0 && p.states && on && n > 0)
-            put(p.states + ((size_t)b * p.chunks + t0 / kRecurChunk) * p.C + c, st);
+            put_part<N, TMA>(p.states + ((size_t)b * p.chunks + t0 / kRecurChunk) * p.C, c, p.C, st);
         // the state before this warp's tokens
         F<N> h = st;
 #pragma unroll
@@ -464,19 +517,19 @@ __global__ void __launch_bounds__(32 * kW, 2)
             __syncwarp();
             if (lane == 0 && n > 0) tma_store_3d(&th, smem_u32(out), c0, t0, b);
         } else {
-            T *hp = static_cast<T *>(p.h) + ((size_t)b * p.T + t0) * p.C + c;
+            T *hp = static_cast<T *>(p.h) + ((size_t)b * p.T + t0) * p.C;
 #pragma unroll
             for (int s = 0; s < kS; ++s) {
                 if (RESET && (cuts >> s & 1u)) h = splat<N>(0.f);
                 h = fma(a[s], h, u[s]);
-                if (on && s < n) put(hp + (size_t)s * p.C, h);
+                if (s < n) put_part<N, false>(hp + (size_t)s * p.C, c, p.C, h);
             }
         }
     }
     if (TMA && lane == 0) tma_store_read();
     if (!ok && TMA && threadIdx.x == 0) drain(sh.full, min(rounds, round + kFwdStages), kFwdStages, p.status);
     if (P > 1) cluster_barrier();  // no block leaves while another may write to it
-    if (ok && p.h_last && on && rank == 0 && warp == 0) put(p.h_last + bc, carry);
+    if (ok && p.h_last && on && rank == 0 && warp == 0) put_part<N, TMA>(p.h_last + bC, c, p.C, carry);
 }
 
 // Backward: the same tiles from the end of the sequence to its start.  Each warp has two
@@ -490,18 +543,18 @@ __global__ void __launch_bounds__(32 * kW, 2)
                                    const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap td,
                                    const __grid_constant__ CUtensorMap tdx, const __grid_constant__ CUtensorMap tdf)
 {
-    constexpr int N = TMA ? 4 / (int)sizeof(T) : 1, CH = 32 * N;
+    constexpr int N = 4 / (int)sizeof(T), CH = 32 * N;
     using P_ = Pack<T, N>;
     __shared__ TileShared<N, true> sh;
     extern __shared__ unsigned char dynamic[];
-    unsigned char *stages = dynamic + (-smem_u32(dynamic) & 127u);  // TMA: [kBwdStages][f, x, dh][kPlane]
-    Map<N> *totals = reinterpret_cast<Map<N> *>(stages + (TMA ? kBwdStages * 3 * kPlane : 0));
+    unsigned char *stages = dynamic + (-smem_u32(dynamic) & 127u);  // [kBwdStages][f, x, dh][kPlane]
+    Map<N> *totals = reinterpret_cast<Map<N> *>(stages + kBwdStages * 3 * kPlane);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int P = p.cluster, rank = P > 1 ? (int)cluster_rank() : 0;
     const int chain = blockIdx.x / P, b = chain / p.cblocks, c0 = (chain % p.cblocks) * CH, c = c0 + lane * N;
     const bool on = c < p.C;
     const unsigned char *reset = RESET ? p.reset + (size_t)b * p.T : nullptr;
-    const size_t bc = (size_t)b * p.C + c;
+    const size_t bC = (size_t)b * p.C;
     const int rounds = (p.chunks + P - 1) / P;
     // rank 0 holds the last tile of a round; tiles past the end of the sequence are empty
     const int last = rounds * P - 1 - rank;
@@ -524,25 +577,24 @@ __global__ void __launch_bounds__(32 * kW, 2)
             for (int i = 0; i < kBwdStages && i < rounds; ++i) issue(i);
     }
     F<N> carry = splat<N>(0.f), next_start = splat<N>(0.f);
-    if (on && p.dh_last) carry = widen(*reinterpret_cast<const Pack<float, N> *>(p.dh_last + bc));
-    P_ fr[TMA ? 1 : kS], xr[TMA ? 1 : kS], dr[TMA ? 1 : kS];
+    if (on && p.dh_last) carry = get_state<N, TMA>(p.dh_last + bC, c, p.C);
+    // the tile's stored state, a round ahead
     auto fetch = [&](int tile) {
-        const long long t0 = tile * kRecurChunk + warp * kS;
-        if (tile >= p.chunks || !on) return;
-        next_start = widen(*reinterpret_cast<const Pack<float, N> *>(p.states_in + ((size_t)b * p.chunks + tile) * p.C + c));
-        if constexpr (!TMA) {
-            const T *fp = static_cast<const T *>(p.f) + b * p.fs[0] + c + t0 * p.fs[1];
-            const T *xp = static_cast<const T *>(p.x) + b * p.xs[0] + c + t0 * p.xs[1];
-            const T *dp = static_cast<const T *>(p.dh) + b * p.ds[0] + c + t0 * p.ds[1];
-#pragma unroll
-            for (int s = 0; s < kS; ++s)
-                if (t0 + s < p.T) {
-                    fr[s].load(fp + s * p.fs[1]);
-                    xr[s].load(xp + s * p.xs[1]);
-                    if (p.dh) dr[s].load(dp + s * p.ds[1]);
-                }
-        }
+        if (tile < p.chunks && on) next_start = get_state<N, TMA>(p.states_in + ((size_t)b * p.chunks + tile) * p.C, c, p.C);
     };
+    auto copy = [&](int round) {  // not TMA: this lane's part of its warp's tokens
+        const long long t0 = (long long)(last - round * P) * kRecurChunk + warp * kS;
+        const int n = (int)min(max(p.T - t0, 0LL), (long long)kS);
+        unsigned char *dst = stages + (round % kBwdStages) * 3 * kPlane + warp * kS * kRowBytes + lane * 4;
+        copy_rows<T, N>(static_cast<const T *>(p.f) + b * p.fs[0] + t0 * p.fs[1], p.fs[1], c, p.C, n, dst);
+        copy_rows<T, N>(static_cast<const T *>(p.x) + b * p.xs[0] + t0 * p.xs[1], p.xs[1], c, p.C, n, dst + kPlane);
+        if (p.dh)
+            copy_rows<T, N>(static_cast<const T *>(p.dh) + b * p.ds[0] + t0 * p.ds[1], p.ds[1], c, p.C, n, dst + 2 * kPlane);
+    };
+    if (!TMA) {
+        copy(0);
+        copy_commit();
+    }
     fetch(last);
     __syncthreads();
     if (P > 1) cluster_barrier();
@@ -553,29 +605,21 @@ __global__ void __launch_bounds__(32 * kW, 2)
         const int n = min(max(p.T - t0, 0), kS);
         const unsigned cuts = RESET ? reset_bits(reset, t0, n, lane) : 0u;
         unsigned char *rows = stages + (round % kBwdStages) * 3 * kPlane + warp * kS * kRowBytes, *mine = rows + lane * 4;
-        if (TMA) ok &= mbar_wait(smem_u32(&sh.full[round % kBwdStages]), (round / kBwdStages) & 1, p.status, kSiteConsumerFull);
-        F<N> xv[TMA ? 1 : kS] = {}, dv[TMA ? 1 : kS] = {};
-        auto load_x = [&](int s) {
-            if constexpr (TMA) return widen(*reinterpret_cast<const P_ *>(mine + kPlane + s * kRowBytes));
-            else return xv[s];
-        };
+        if (TMA) {
+            ok &= mbar_wait(smem_u32(&sh.full[round % kBwdStages]), (round / kBwdStages) & 1, p.status, kSiteConsumerFull);
+        } else {
+            if (round + 1 < rounds) copy(round + 1);
+            copy_commit();
+            copy_wait<1>();
+        }
+        auto load_x = [&](int s) { return widen(*reinterpret_cast<const P_ *>(mine + kPlane + s * kRowBytes)); };
         auto load_d = [&](int s) {
-            if (!p.dh) return splat<N>(0.f);
-            if constexpr (TMA) return widen(*reinterpret_cast<const P_ *>(mine + 2 * kPlane + s * kRowBytes));
-            else return dv[s];
+            return p.dh ? widen(*reinterpret_cast<const P_ *>(mine + 2 * kPlane + s * kRowBytes)) : splat<N>(0.f);
         };
-        if constexpr (!TMA)
-#pragma unroll
-            for (int s = 0; s < kS; ++s) {
-                xv[s] = s < n ? widen(xr[s]) : splat<N>(0.f);
-                dv[s] = s < n ? widen(dr[s]) : splat<N>(0.f);
-            }
         F<N> a[kS], eta[kS], h = next_start, r;
 #pragma unroll
-        for (int s = 0; s < kS; ++s) {
-            if constexpr (TMA) gates<T, MODE>(widen(*reinterpret_cast<const P_ *>(mine + s * kRowBytes)), a[s], eta[s]);
-            else gates<T, MODE>(widen(fr[s]), a[s], eta[s]);
-        }
+        for (int s = 0; s < kS; ++s)
+            gates<T, MODE>(widen(*reinterpret_cast<const P_ *>(mine + s * kRowBytes)), a[s], eta[s]);
         if (n < kS) {  // tokens past the end, whose x and dh read as zeros: the identity
 #pragma unroll
             for (int s = 0; s < kS; ++s)
@@ -642,7 +686,7 @@ __global__ void __launch_bounds__(32 * kW, 2)
             g[s] = MODE == kRecurMix ? sub(h, x) : h;
             h = fma(a[s], h, MODE == kRecurMix ? mul(eta[s], x) : x);
         }
-        const size_t o = ((size_t)b * p.T + t0) * p.C + c;
+        const size_t o = ((size_t)b * p.T + t0) * p.C;
         T *dx = static_cast<T *>(p.dx) + o, *df = static_cast<T *>(p.df) + o;
 #pragma unroll
         for (int s = kS - 1; s >= 0; --s) {
@@ -653,9 +697,9 @@ __global__ void __launch_bounds__(32 * kW, 2)
             if constexpr (TMA) {  // over x and dh, which this lane has read
                 put(reinterpret_cast<T *>(mine + kPlane + s * kRowBytes), gx);
                 put(reinterpret_cast<T *>(mine + 2 * kPlane + s * kRowBytes), gf);
-            } else if (on && s < n) {
-                put(dx + (size_t)s * p.C, gx);
-                put(df + (size_t)s * p.C, gf);
+            } else if (s < n) {
+                put_part<N, false>(dx + (size_t)s * p.C, c, p.C, gx);
+                put_part<N, false>(df + (size_t)s * p.C, c, p.C, gf);
             }
             if (RESET && (cuts >> s & 1u)) r = splat<N>(0.f);
         }
@@ -671,7 +715,7 @@ __global__ void __launch_bounds__(32 * kW, 2)
     if (TMA && lane == 0) tma_store_read();
     if (!ok && TMA && threadIdx.x == 0) drain(sh.full, min(rounds, max(round + 1, kBwdStages)), kBwdStages, p.status);
     if (P > 1) cluster_barrier();
-    if (ok && p.dh0 && on && rank == 0 && warp == 0) put(p.dh0 + bc, carry);
+    if (ok && p.dh0 && on && rank == 0 && warp == 0) put_part<N, TMA>(p.dh0 + bC, c, p.C, carry);
 }
 
 RecurParams params_of(const RecurArgs &a)
@@ -753,12 +797,13 @@ template <typename... KArgs> Capacity query_capacity(void (*kernel)(KArgs...), i
 
 // Blocks of a cluster.  A round of a block alone on its SM is the unit of time, 1.2 us
 // forward and 2.1 us backward (bf16, mix); 1.33 with the exchange between blocks; two
-// blocks on an SM take 1.95 each; a start costs about 3, that of a later wave of clusters
+// blocks on an SM take `two` each, 1.95 in bf16, 1.5 in fp32, which has half the channels
+// to compute for the same bytes; a start costs about 3, that of a later wave of clusters
 // 6.  Timed over 12 shapes of 1 .. 768 chains and 2 .. 256 chunks with every P of 1 .. 16,
 // this picks the fastest P or one within 6% of it: 64 chains of 256 chunks forward 150 us
 // at P = 4 against 305, 203, 166 at 1, 2, 8; 12 chains 50 us at 16 against 303 and 59 at 1
 // and 8; 192 chains of 8 chunks 20 us at 1 against 26 and 29 at 2 and 4.
-int plan_cluster(long long chains, int chunks, const Capacity &cap)
+int plan_cluster(long long chains, int chunks, double two, const Capacity &cap)
 {
     int best = 1;
     double least = 0.0;
@@ -767,8 +812,8 @@ int plan_cluster(long long chains, int chunks, const Capacity &cap)
         const int rounds = (chunks + P - 1) / P;
         const long long full = chains / cap.any[P], rest = chains % cap.any[P];
         const double later = P > 1 ? 6.0 : 3.0;
-        double t = full * (rounds * 1.95 + later) + 3.0 - (full ? later : 0.0);
-        if (rest) t += rounds * (rest > cap.alone[P] ? 1.95 : P > 1 ? 1.33 : 1.0) + (full ? later : 0.0);
+        double t = full * (rounds * two + later) + 3.0 - (full ? later : 0.0);
+        if (rest) t += rounds * (rest > cap.alone[P] ? two : P > 1 ? 1.33 : 1.0) + (full ? later : 0.0);
         if (P == 1 || t < least) {
             least = t;
             best = P;
@@ -794,7 +839,7 @@ int launch_tiles(void (*kernel)(KArgs...), RecurParams p, int ch, int smem, cuda
         if (!known[dev]) caps[dev] = query_capacity(kernel, smem, per_block);
         known[dev] = true;
     }
-    p.cluster = plan_cluster(chains, p.chunks, caps[dev]);
+    p.cluster = plan_cluster(chains, p.chunks, ch < 64 ? 1.5 : 1.95, caps[dev]);
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute at;
     if (chains * p.cluster > 0x7fffffffLL ||
@@ -806,12 +851,12 @@ int launch_tiles(void (*kernel)(KArgs...), RecurParams p, int ch, int smem, cuda
 template <typename T, int MODE, bool RESET, bool TMA>
 int run_tiles(const RecurParams &p, const CUtensorMap *maps, bool bwd, cudaStream_t st)
 {
-    constexpr int CH = TMA ? 128 / (int)sizeof(T) : 32;
+    constexpr int CH = 128 / (int)sizeof(T);
     if (bwd)
-        return launch_tiles(ttt_recurrence_bwd_tile_kernel<T, MODE, RESET, TMA>, p, CH, TMA ? kBwdStages * 3 * kPlane : 0,
-                            st, maps[0], maps[1], maps[2], maps[3], maps[4]);
-    return launch_tiles(ttt_recurrence_fwd_tile_kernel<T, MODE, RESET, TMA>, p, CH,
-                        TMA ? (kFwdStages * 2 + 1) * kPlane : 0, st, maps[0], maps[1], maps[3]);
+        return launch_tiles(ttt_recurrence_bwd_tile_kernel<T, MODE, RESET, TMA>, p, CH, kBwdStages * 3 * kPlane, st,
+                            maps[0], maps[1], maps[2], maps[3], maps[4]);
+    return launch_tiles(ttt_recurrence_fwd_tile_kernel<T, MODE, RESET, TMA>, p, CH, (kFwdStages * 2 + 1) * kPlane, st,
+                        maps[0], maps[1], maps[3]);
 }
 
 // Descriptors of f, x and dh in boxes of kRecurChunk tokens x 128 bytes of channels (rows
