@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import NamedTuple, Optional
 
 import torch
@@ -424,45 +425,82 @@ def ttt_eta_gate(x, theta, eta_base=1.0, eta=None, stream=None):
     return eta
 
 
+# ------------------------------------------------------- the streaming operators
+#
+# A decoding step calls these on a few hundred KB, where the host's time is the whole
+# cost: descriptors are packed bytes, the current stream and device are read without their
+# Python wrappers, and each check is one expression that only asks why when it fails.
+
 _IO = {torch.bfloat16: TTT_BF16, torch.float32: TTT_F32}
+_ROPE_DESC, _NORM_DESC, _NORM_PAR = struct.Struct("@11i20q"), struct.Struct("@8i3f11q"), struct.Struct("@5Q")
+_RECUR_DESC = struct.Struct("@5i6q")
+_NO_STRIDE2, _NO_STRIDE3 = (0, 0), (0, 0, 0)
+_empty = torch.empty
+_fns: dict = {}
+
+
+def _fn(name):
+    """An entry point taking addresses and packed descriptors as they are."""
+    f = _fns.get(name)
+    if f is None:
+        f = lib()[name]
+        n = {"ttt_rope": 10, "ttt_block_norm_fwd": 9, "ttt_block_norm_bwd": 15, "ttt_recurrence_fwd": 9,
+             "ttt_recurrence_bwd": 11}[name]
+        f.argtypes = [ctypes.c_void_p] * n
+        f.restype = ctypes.c_int
+        _fns[name] = f
+    return f
 
 
 def _tokens(name, t, dims, like=None):
-    """A token tensor of the streaming operators: CUDA, bf16 or fp32, `dims` dimensions,
-    the last one contiguous; `like`: shares its dtype and device."""
+    """Why a token tensor is refused: CUDA, bf16 or fp32, `dims` dimensions, the last one
+    contiguous; `like`: shares its dtype and device."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions")
     if t.dtype not in _IO:
         raise ValueError(f"{name} must be bfloat16 or float32")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    if t.stride()[-1] != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must be contiguous along its last dimension")
     if like is not None and (t.dtype != like.dtype or t.device != like.device):
         raise ValueError(f"{name} must share the dtype and device of the first tensor")
+
+
+def _rows(name, t, like, shape, dt, dev):
+    """Strides (all but the last) of a token tensor of this shape, dtype and device."""
+    st = t.stride()
+    if t.dtype != dt or t.device != dev or t.shape != shape or st[-1] != 1:
+        _tokens(name, t, len(shape), like)
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return st[:-1]
+
+
+def _like(name, t, shape, dtype, dev):
+    """A contiguous tensor of the given shape, dtype and device."""
+    if t.dtype != dtype or t.device != dev or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
     return t
 
 
-def _call(fn, dev, stream, *args):
+def _call(name, dev, stream, *args):
     """Runs one library entry point on dev's current stream (or `stream`)."""
+    i = dev.index
     if stream is None:
-        raw = torch.cuda.current_stream(dev).cuda_stream
+        raw = torch._C._cuda_getCurrentRawStream(i)
     elif stream.device != dev:
         raise ValueError(f"the stream is on {stream.device} but the tensors on {dev}")
     else:
         raw = stream.cuda_stream
-    f = getattr(lib(), fn)
-    if torch.cuda.current_device() == dev.index:
+    f = _fns.get(name) or _fn(name)
+    if torch._C._cuda_getDevice() == i:
         rc = f(*args, raw)
     else:
         with torch.cuda.device(dev):
             rc = f(*args, raw)
     if rc != 0:
-        raise TTTError(fn, rc)
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
+        raise TTTError(name, rc)
 
 
 def ttt_rope(q, k, v, table, positions=None, pos0=0, period=0, interleaved=False, inverse=False, q_out=None,
@@ -479,82 +517,99 @@ def ttt_rope(q, k, v, table, positions=None, pos0=0, period=0, interleaved=False
     [B,H,T,d] unless q_out, k_out, v_out are given (any strides; an output may be its
     own input).  Returns (q_out, k_out, v_out).  A position outside the table gives NaN
     and TTT_ERR_RANGE from ttt_sync_status."""
-    _tokens("q", q, 4)
-    B, H, T, d = q.shape
-    dev = q.device
-    hk = 0
-    for name, t in (("k", k), ("v", v)):
-        if t is not None:
-            _tokens(name, t, 4, q)
-            if t.shape[0] != B or t.shape[2:] != q.shape[2:] or (hk and t.shape[1] != hk):
-                raise ValueError(f"{name} must be [B,Hk,T,d] with q's B, T and d")
-            hk = t.shape[1]
-    if (not table.is_cuda or table.dtype != torch.float32 or table.device != dev or table.dim() != 3
-            or table.shape[2] != 2 or not table.is_contiguous()):
+    dt, dev, sq = q.dtype, q.device, q.stride()
+    io = _IO.get(dt)
+    if io is None or not q.is_cuda or len(sq) != 4 or sq[3] != 1:
+        _tokens("q", q, 4)
+    B, H, T, d = shape = q.shape
+    hk, sk, sv = 0, _NO_STRIDE3, _NO_STRIDE3
+    if k is not None:
+        hk = k.shape[1]
+        sk = _rows("k", k, q, shape if hk == H else (B, hk, T, d), dt, dev)
+    if v is not None:
+        if k is None:
+            hk = v.shape[1]
+        sv = _rows("v", v, q, shape if hk == H else (B, hk, T, d), dt, dev)
+    tshape = table.shape
+    if (table.dtype != torch.float32 or table.device != dev or len(tshape) != 3 or tshape[2] != 2
+            or not table.is_contiguous()):
         raise ValueError("table must be a contiguous float32 [rows, rot/2, 2] tensor on q's device")
     pbs = 0
     if positions is not None:
         if positions.dtype != torch.int64 or positions.device != dev or not positions.is_contiguous():
             raise ValueError("positions must be a contiguous int64 tensor on q's device")
-        if tuple(positions.shape) == (B, T):
+        if positions.shape == (B, T):
             pbs = T
-        elif tuple(positions.shape) != (T,):
+        elif positions.shape != (T,):
             raise ValueError("positions must be [B,T] or [T]")
-    ins, outs, strides = (q, k, v), [q_out, k_out, v_out], []
-    for i, (name, t) in enumerate((("q_out", q), ("k_out", k), ("v_out", v))):
-        o = outs[i]
-        if t is None:
-            if o is not None:
-                raise ValueError(f"{name} given without its input")
-            continue
-        if o is None:
-            outs[i] = torch.empty(t.shape, dtype=t.dtype, device=dev)
-        else:
-            _tokens(name, o, 4, q)
-            if o.shape != t.shape:
-                raise ValueError(f"{name} must have the shape of its input")
-    for t in (*ins, *outs):
-        strides += (0, 0, 0) if t is None else t.stride()[:3]
-    desc = RopeDesc(B, T, H, hk, d, 2 * table.shape[1], 1 if interleaved else 0, 1 if inverse else 0, _IO[q.dtype],
-                    table.shape[0], int(period), int(pos0), pbs, (ctypes.c_longlong * 18)(*strides))
-    _call("ttt_rope", dev, stream, desc, _addr(q), _addr(k), _addr(v), table.data_ptr(), _addr(positions),
-          _addr(outs[0]), _addr(outs[1]), _addr(outs[2]))
-    return tuple(outs)
+    Td = T * d
+    if q_out is None:
+        q_out, so = _empty(shape, dtype=dt, device=dev), (H * Td, Td, d)
+    else:
+        so = _rows("q_out", q_out, q, shape, dt, dev)
+    sko = svo = _NO_STRIDE3
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out given without its input")
+    elif k_out is None:
+        k_out, sko = _empty(k.shape, dtype=dt, device=dev), (hk * Td, Td, d)
+    else:
+        sko = _rows("k_out", k_out, q, k.shape, dt, dev)
+    if v is None:
+        if v_out is not None:
+            raise ValueError("v_out given without its input")
+    elif v_out is None:
+        v_out, svo = _empty(v.shape, dtype=dt, device=dev), (hk * Td, Td, d)
+    else:
+        svo = _rows("v_out", v_out, q, v.shape, dt, dev)
+    desc = _ROPE_DESC.pack(B, T, H, hk, d, 2 * tshape[1], interleaved, inverse, io, tshape[0], period, pos0, pbs,
+                           *sq[:3], *sk, *sv, *so, *sko, *svo)
+    _call("ttt_rope", dev, stream, desc, q.data_ptr(), _addr(k), _addr(v), table.data_ptr(), _addr(positions),
+          q_out.data_ptr(), _addr(k_out), _addr(v_out))
+    return q_out, k_out, v_out
 
 
-def _like(name, t, shape, dtype, dev):
-    """A contiguous tensor of the given shape, dtype and device (outputs, saved data)."""
-    if t.dtype != dtype or t.device != dev or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
+def _vec(name, t, D, dev):
+    """A parameter vector, or None."""
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.device != dev or t.shape != (D,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 [{D}] tensor on {dev}")
     return t
 
 
-def _norm_prologue(y, x, gate, act, post, pre, post_eps, pre_eps, alpha, vectors, dh=None, du=None):
-    """Checks of both block-norm wrappers; returns (B, T, D, descriptor, parameters)."""
-    _tokens("y", y, 4 if y.dim() == 4 else 3)
-    if y.dim() == 4:
+def _norm_prologue(y, x, gate, act, post, pre, post_eps, pre_eps, alpha, w1, b1, scale, w2, b2, dh=None, du=None):
+    """Checks of both block-norm wrappers; returns (token shape, descriptor, parameters)."""
+    dt, dev, sy = y.dtype, y.device, y.stride()
+    io = _IO.get(dt)
+    if io is None or not y.is_cuda or len(sy) not in (3, 4) or sy[-1] != 1:
+        _tokens("y", y, 4 if len(sy) == 4 else 3)
+    if len(sy) == 4:
         B, heads, T, d = y.shape
-        D, ys = heads * d, y.stride()[:3]
+        D, sy = heads * d, sy[:3]
     else:
-        (B, T, D), heads = y.shape, 1
-        ys = (y.stride(0), 0, y.stride(1))
+        B, T, D = y.shape
+        heads, sy = 1, (sy[0], 0, sy[1])
     if (gate is None) != (act == "none"):
         raise ValueError('a gate goes with an act other than "none"')
-    strides = [*ys]
-    for name, t in (("x", x), ("gate", gate), ("dh", dh), ("du", du)):
-        if t is None:
-            strides += (0, 0)
-            continue
-        _tokens(name, t, 3, y)
-        if t.shape != (B, T, D):
-            raise ValueError(f"{name} must be [B,T,D] = {(B, T, D)}")
-        strides += t.stride()[:2]
-    for name, t in vectors.items():
-        if t is not None:
-            _like(name, t, (D,), torch.float32, y.device)
-    desc = BlockNormDesc(B, T, D, heads, _IO[y.dtype], NORMS[post], NORMS[pre], GATES[act], post_eps, pre_eps, alpha,
-                         (ctypes.c_longlong * 11)(*strides))
-    return B, T, D, desc, BlockNormVectors(*(_addr(t) for t in vectors.values()))
+    shape = (B, T, D)
+    sx = _NO_STRIDE2 if x is None else _rows("x", x, y, shape, dt, dev)
+    sg = _NO_STRIDE2 if gate is None else _rows("gate", gate, y, shape, dt, dev)
+    sdh = _NO_STRIDE2 if dh is None else _rows("dh", dh, y, shape, dt, dev)
+    sdu = _NO_STRIDE2 if du is None else _rows("du", du, y, shape, dt, dev)
+    par = (_vec("post_weight", w1, D, dev), _vec("post_bias", b1, D, dev), _vec("scale", scale, D, dev),
+           _vec("pre_weight", w2, D, dev), _vec("pre_bias", b2, D, dev))
+    desc = _NORM_DESC.pack(B, T, D, heads, io, NORMS[post], NORMS[pre], GATES[act], post_eps, pre_eps, alpha, *sy, *sx,
+                           *sg, *sdh, *sdu)
+    return shape, desc, par
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _vectors(par):
+    return _NORM_PAR.pack(*[0 if t is None else t.data_ptr() for t in par])
 
 
 def ttt_block_norm_fwd(y, x=None, gate=None, act=None, post="none", post_weight=None, post_bias=None, scale=None,
@@ -569,22 +624,20 @@ def ttt_block_norm_fwd(y, x=None, gate=None, act=None, post="none", post_weight=
     pass.  h may be x.  Returns (h, u or None, stats or None)."""
     if act is None:
         act = "none" if gate is None else "silu"
-    B, T, D, desc, par = _norm_prologue(y, x, gate, act, post, pre, post_eps, pre_eps, alpha,
-                                        dict(post_weight=post_weight, post_bias=post_bias, scale=scale,
-                                             pre_weight=pre_weight, pre_bias=pre_bias))
-    dev = y.device
-    h = torch.empty((B, T, D), dtype=y.dtype, device=dev) if h is None else _like("h", h, (B, T, D), y.dtype, dev)
-    if pre == "none":
-        if u is not None:
-            raise ValueError("u is written with a pre norm only")
-    else:
-        u = torch.empty((B, T, D), dtype=y.dtype, device=dev) if u is None else _like("u", u, (B, T, D), y.dtype, dev)
+    shape, desc, par = _norm_prologue(y, x, gate, act, post, pre, post_eps, pre_eps, alpha, post_weight, post_bias, scale,
+                                      pre_weight, pre_bias)
+    dev, dt = y.device, y.dtype
+    if pre != "none":
+        u = _empty(shape, dtype=dt, device=dev) if u is None else _like("u", u, shape, dt, dev)
+    elif u is not None:
+        raise ValueError("u is written with a pre norm only")
     if stats is not None:
-        _like("stats", stats, (B, T, 4), torch.float32, dev)
+        _like("stats", stats, (shape[0], shape[1], 4), torch.float32, dev)
     elif want_stats:
-        stats = torch.empty((B, T, 4), dtype=torch.float32, device=dev)
-    _call("ttt_block_norm_fwd", dev, stream, desc, par, y.data_ptr(), _addr(x), _addr(gate), h.data_ptr(), _addr(u),
-          _addr(stats))
+        stats = _empty((shape[0], shape[1], 4), dtype=torch.float32, device=dev)
+    h = _empty(shape, dtype=dt, device=dev) if h is None else _like("h", h, shape, dt, dev)
+    _call("ttt_block_norm_fwd", dev, stream, desc, _vectors(par), y.data_ptr(), _addr(x), _addr(gate), h.data_ptr(),
+          _addr(u), _addr(stats))
     return h, u, stats
 
 
@@ -609,22 +662,23 @@ def ttt_block_norm_bwd(dh, du, y, stats, x=None, gate=None, act=None, post="none
     tensor of ttt_block_norm_bwd_workspace(...) bytes, allocated here when None."""
     if act is None:
         act = "none" if gate is None else "silu"
-    vectors = dict(post_weight=post_weight, post_bias=post_bias, scale=scale, pre_weight=pre_weight, pre_bias=pre_bias)
-    B, T, D, desc, par = _norm_prologue(y, x, gate, act, post, pre, post_eps, pre_eps, alpha, vectors, dh, du)
-    dev = y.device
+    shape, desc, par = _norm_prologue(y, x, gate, act, post, pre, post_eps, pre_eps, alpha, post_weight, post_bias, scale,
+                                      pre_weight, pre_bias, dh, du)
+    B, T, D = shape
+    dev, dt = y.device, y.dtype
     _like("stats", stats, (B, T, 4), torch.float32, dev)
-    dy = torch.empty(y.shape, dtype=y.dtype, device=dev)
-    dx = None if x is None else torch.empty((B, T, D), dtype=y.dtype, device=dev)
-    dg = None if gate is None else torch.empty((B, T, D), dtype=y.dtype, device=dev)
-    gv = [None if t is None else torch.empty(D, dtype=torch.float32, device=dev) for t in vectors.values()]
-    need = int(lib().ttt_block_norm_bwd_workspace(desc))
+    dy = _empty(y.shape, dtype=dt, device=dev)
+    dx = None if x is None else _empty(shape, dtype=dt, device=dev)
+    dg = None if gate is None else _empty(shape, dtype=dt, device=dev)
+    gv = [None if t is None else _empty(D, dtype=torch.float32, device=dev)
+          for t in (post_weight, post_bias, scale, pre_weight, pre_bias)]
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _empty(ttt_block_norm_bwd_workspace(B, T, D), dtype=torch.uint8, device=dev)
     elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on y's device")
-    _call("ttt_block_norm_bwd", dev, stream, desc, par, _addr(dh), _addr(du), y.data_ptr(), _addr(x), _addr(gate),
-          stats.data_ptr(), dy.data_ptr(), _addr(dx), _addr(dg), BlockNormVectors(*(_addr(t) for t in gv)),
-          workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _call("ttt_block_norm_bwd", dev, stream, desc, _vectors(par), _addr(dh), _addr(du), y.data_ptr(), _addr(x),
+          _addr(gate), stats.data_ptr(), dy.data_ptr(), _addr(dx), _addr(dg), _vectors(gv), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
     return BlockNormGrads(dy, dx, dg, *gv)
 
 
@@ -635,22 +689,19 @@ def ttt_block_norm_bwd_workspace(B, T, D) -> int:
 
 
 def _recurrence_prologue(x, f, mode, reset, dh=None):
-    """Checks of both recurrence wrappers; returns (B, T, C, descriptor)."""
-    _tokens("x", x, 3)
-    B, T, C = x.shape
-    strides = [*x.stride()[:2]]
-    for name, t in (("f", f), ("dh", dh)):
-        if t is None:
-            strides += (0, 0)
-            continue
-        _tokens(name, t, 3, x)
-        if t.shape != x.shape:
-            raise ValueError(f"{name} must be [B,T,C] like x")
-        strides += t.stride()[:2]
-    if reset is not None and (reset.dtype not in (torch.bool, torch.uint8) or reset.device != x.device
-                              or tuple(reset.shape) != (B, T) or not reset.is_contiguous()):
-        raise ValueError("reset must be a contiguous bool or uint8 [B,T] tensor on x's device")
-    return B, T, C, RecurrenceDesc(B, T, C, _IO[x.dtype], RECURRENCE_MODES[mode], (ctypes.c_longlong * 6)(*strides))
+    """Checks of both recurrence wrappers; returns (shape, descriptor)."""
+    dt, dev, sx = x.dtype, x.device, x.stride()
+    io = _IO.get(dt)
+    if io is None or not x.is_cuda or len(sx) != 3 or sx[2] != 1:
+        _tokens("x", x, 3)
+    B, T, C = shape = x.shape
+    sf = _rows("f", f, x, shape, dt, dev)
+    sd = _NO_STRIDE2 if dh is None else _rows("dh", dh, x, shape, dt, dev)
+    if reset is not None:
+        if (reset.dtype not in (torch.bool, torch.uint8) or reset.device != dev or reset.shape != (B, T)
+                or not reset.is_contiguous()):
+            raise ValueError("reset must be a contiguous bool or uint8 [B,T] tensor on x's device")
+    return shape, _RECUR_DESC.pack(B, T, C, io, RECURRENCE_MODES[mode], sx[0], sx[1], *sf, *sd)
 
 
 def ttt_recurrence_fwd(x, f, h0=None, mode="mix", reset=None, h=None, h_last=None, want_states=False, states=None,
@@ -661,20 +712,17 @@ def ttt_recurrence_fwd(x, f, h0=None, mode="mix", reset=None, h=None, h_last=Non
     bool or uint8 [B,T], True where a packed sequence begins (h_{t-1} taken as zero).
     h0: fp32 [B,C] or None; h_last may be h0 (a decoder's states stepped in place).
     want_states (or states) for the backward pass.  Returns (h, h_last, states or None)."""
-    B, T, C, desc = _recurrence_prologue(x, f, mode, reset)
-    dev = x.device
+    shape, desc = _recurrence_prologue(x, f, mode, reset)
+    B, T, C = shape
+    dev, dt, f32 = x.device, x.dtype, torch.float32
     if h0 is not None:
-        _like("h0", h0, (B, C), torch.float32, dev)
-    h = torch.empty((B, T, C), dtype=x.dtype, device=dev) if h is None else _like("h", h, (B, T, C), x.dtype, dev)
-    if h_last is None:
-        h_last = torch.empty((B, C), dtype=torch.float32, device=dev)
-    else:
-        _like("h_last", h_last, (B, C), torch.float32, dev)
-    shape = (B, -(-T // RECURRENCE_CHUNK), C)
+        _like("h0", h0, (B, C), f32, dev)
     if states is not None:
-        _like("states", states, shape, torch.float32, dev)
+        _like("states", states, (B, -(-T // RECURRENCE_CHUNK), C), f32, dev)
     elif want_states:
-        states = torch.empty(shape, dtype=torch.float32, device=dev)
+        states = _empty((B, -(-T // RECURRENCE_CHUNK), C), dtype=f32, device=dev)
+    h = _empty(shape, dtype=dt, device=dev) if h is None else _like("h", h, shape, dt, dev)
+    h_last = _empty((B, C), dtype=f32, device=dev) if h_last is None else _like("h_last", h_last, (B, C), f32, dev)
     _call("ttt_recurrence_fwd", dev, stream, desc, x.data_ptr(), f.data_ptr(), _addr(reset), _addr(h0), h.data_ptr(),
           h_last.data_ptr(), _addr(states))
     return h, h_last, states
@@ -683,17 +731,15 @@ def ttt_recurrence_fwd(x, f, h0=None, mode="mix", reset=None, h=None, h_last=Non
 def ttt_recurrence_bwd(dh, x, f, states, mode="mix", reset=None, dh_last=None, dx=None, df=None, dh0=None, stream=None):
     """Gradients of ttt_recurrence_fwd from dh ([B,T,C] or None) and dh_last (fp32 [B,C]
     or None), with the forward's inputs and the states it stored.  Returns (dx, df, dh0)."""
-    B, T, C, desc = _recurrence_prologue(x, f, mode, reset, dh)
-    dev = x.device
-    _like("states", states, (B, -(-T // RECURRENCE_CHUNK), C), torch.float32, dev)
+    shape, desc = _recurrence_prologue(x, f, mode, reset, dh)
+    B, T, C = shape
+    dev, dt, f32 = x.device, x.dtype, torch.float32
+    _like("states", states, (B, -(-T // RECURRENCE_CHUNK), C), f32, dev)
     if dh_last is not None:
-        _like("dh_last", dh_last, (B, C), torch.float32, dev)
-    dx = torch.empty((B, T, C), dtype=x.dtype, device=dev) if dx is None else _like("dx", dx, (B, T, C), x.dtype, dev)
-    df = torch.empty((B, T, C), dtype=x.dtype, device=dev) if df is None else _like("df", df, (B, T, C), x.dtype, dev)
-    if dh0 is None:
-        dh0 = torch.empty((B, C), dtype=torch.float32, device=dev)
-    else:
-        _like("dh0", dh0, (B, C), torch.float32, dev)
+        _like("dh_last", dh_last, (B, C), f32, dev)
+    dx = _empty(shape, dtype=dt, device=dev) if dx is None else _like("dx", dx, shape, dt, dev)
+    df = _empty(shape, dtype=dt, device=dev) if df is None else _like("df", df, shape, dt, dev)
+    dh0 = _empty((B, C), dtype=f32, device=dev) if dh0 is None else _like("dh0", dh0, (B, C), f32, dev)
     _call("ttt_recurrence_bwd", dev, stream, desc, _addr(dh), x.data_ptr(), f.data_ptr(), _addr(reset),
           states.data_ptr(), _addr(dh_last), dx.data_ptr(), df.data_ptr(), dh0.data_ptr())
     return dx, df, dh0
