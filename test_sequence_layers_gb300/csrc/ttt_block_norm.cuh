@@ -1,0 +1,933 @@
+// ttt_block_norm.cuh -- what stands around a block's inner layer, in one pass over the
+// rows (tokens), forward and backward:
+//     p = N1(y),  m = scale * act(gate) * p,  h = alpha x + m,  u = N2(h)
+// N1, N2: none, RMS (v / sqrt(mean v^2 + eps) * w) or layer norm ((v - mean) /
+// sqrt(var + eps) * w + b) over the D features; y token-major or the TTT layer's
+// head-major output.  Backward with dn the gradient of a normalised row n = (v - mean) r:
+//     dv = r (dn - [layer] mean(dn) - n mean(dn n)).
+//
+// Every tensor is read or written once.  A row belongs to a group of `lanes` threads (part
+// of a warp up to 256 features, else the whole block), a thread holding K chunks of eight
+// features in fp32 registers, so a row's statistics and its outputs come from one read.
+// The variance is taken about the mean, never as a difference of squares.
+//
+// What bounds these kernels is issue slots as much as HBM (some 30 .. 60 instructions a
+// feature against 10 or 16 bytes): arithmetic on paired fp32 instructions, the parts that
+// a call has or lacks (POST, PRE, ACT) known at compile time, parameter vectors that are
+// absent replaced by ones and zeros instead of branches, rows copied ahead with cp.async.
+#pragma once
+
+#include <cstdint>
+#include <mutex>
+
+#include <cuda_runtime.h>
+
+#include "ttt_internal.h"
+#include "ttt_vec.cuh"
+
+namespace ttt {
+
+constexpr int kNormChunk = 8;  // features of a chunk
+
+// row / T for rows below 2^31: multiply by ceil(2^(32 + shift) / T), keep the high part
+// (Granlund and Montgomery, Division by invariant integers using multiplication).
+struct Div {
+    uint32_t d, mul, shift;
+    __device__ __forceinline__ uint32_t operator()(uint32_t n) const
+    {
+        return d == 1 ? n : __umulhi(n, mul) >> shift;
+    }
+};
+
+inline Div make_div(int d)
+{
+    Div r = {(uint32_t)d, 0, 0};
+    if (d > 1) {
+        while ((1u << r.shift) < (uint32_t)d) ++r.shift;  // 2^shift >= d, shift >= 1
+        --r.shift;
+        r.mul = (uint32_t)(((1ull << (32 + r.shift)) + d - 1) / d);
+    }
+    return r;
+}
+
+struct NormVectors {  // fp32 [D], never null (absent: ones or zeros)
+    const float *w1, *b1, *sc, *w2, *b2;
+};
+
+struct NormFwdParams {
+    const void *y, *x, *g;
+    void *h, *u;
+    float *stats;
+    NormVectors v;
+    long long ys[3], xs[2], gs[2];
+    uint32_t rows;
+    Div byT;
+    int T, D, dh, lanes, post, pre, act;
+    int even;  // every tensor token-major and contiguous: one offset for all
+    float eps1, eps2, alpha;
+};
+
+struct NormBwdParams {
+    const void *y, *x, *g, *dh_in, *du;
+    void *dy, *dx, *dg;
+    const float *stats;
+    float *part;  // [blocks][nvec][D] partial parameter gradients
+    NormVectors v;
+    long long ys[3], xs[2], gs[2], dhs[2], dus[2];
+    uint32_t rows;
+    Div byT;
+    int T, D, dh, lanes, post, pre, act;
+    int even;
+    int slot[5];  // slot of each parameter gradient among the nvec, -1: absent
+    int nvec;
+    float alpha;
+};
+
+// Threads of a row and chunks of a thread.
+struct NormShape {
+    int lanes, threads, K;
+    bool block;
+};
+
+// One direction and type each (a translation unit each); limit: the most blocks, 0 none.
+int norm_fwd_bf16(const NormFwdParams &p, const NormShape &s, bool vec, cudaStream_t st);
+int norm_fwd_f32(const NormFwdParams &p, const NormShape &s, bool vec, cudaStream_t st);
+int norm_bwd_bf16(const NormBwdParams &p, const NormShape &s, bool vec, int limit, cudaStream_t st, int *blocks);
+int norm_bwd_f32(const NormBwdParams &p, const NormShape &s, bool vec, int limit, cudaStream_t st, int *blocks);
+
+namespace {
+
+constexpr int kSMs = 152, kC = kNormChunk;
+
+// Eight features as four pairs: the arithmetic is on paired fp32 instructions, which
+// halves what these kernels are short of, issue slots.
+constexpr int kP = kC / 2;
+struct V8 {
+    float2 p[kP];
+};
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ V8 splat(float v)
+{
+    V8 r;
+#pragma unroll
+    for (int i = 0; i < kP; ++i) r.p[i] = both(v);
+    return r;
+}
+__device__ __forceinline__ V8 mul(const V8 &a, const V8 &b)
+{
+    V8 r;
+#pragma unroll
+    for (int i = 0; i < kP; ++i) r.p[i] = __fmul2_rn(a.p[i], b.p[i]);
+    return r;
+}
+__device__ __forceinline__ V8 mul(const V8 &a, float b)
+{
+    V8 r;
+#pragma unroll
+    for (int i = 0; i < kP; ++i) r.p[i] = __fmul2_rn(a.p[i], both(b));
+    return r;
+}
+__device__ __forceinline__ V8 add(const V8 &a, const V8 &b)
+{
+    V8 r;
+#pragma unroll
+    for (int i = 0; i < kP; ++i) r.p[i] = __fadd2_rn(a.p[i], b.p[i]);
+    return r;
+}
+__device__ __forceinline__ V8 fma(const V8 &a, const V8 &b, const V8 &c)
+{
+    V8 r;
+#pragma unroll
+    for (int i = 0; i < kP; ++i) r.p[i] = __ffma2_rn(a.p[i], b.p[i], c.p[i]);
+    return r;
+}
+__device__ __forceinline__ V8 fma(const V8 &a, float b, const V8 &c)
+{
+    V8 r;
+#pragma unroll
+    for (int i = 0; i < kP; ++i) r.p[i] = __ffma2_rn(a.p[i], both(b), c.p[i]);
+    return r;
+}
+// (a - m) r: the difference first, so that what it cancels does not come back scaled
+__device__ __forceinline__ V8 centre(const V8 &a, float m, float r)
+{
+    V8 v;
+#pragma unroll
+    for (int i = 0; i < kP; ++i) v.p[i] = __fmul2_rn(__fadd2_rn(a.p[i], both(-m)), both(r));
+    return v;
+}
+__device__ __forceinline__ float total(const V8 &a)
+{
+    const float2 s = __fadd2_rn(__fadd2_rn(a.p[0], a.p[1]), __fadd2_rn(a.p[2], a.p[3]));
+    return s.x + s.y;
+}
+__device__ __forceinline__ float dot(const V8 &a, const V8 &b)
+{
+    float2 s = __fmul2_rn(a.p[0], b.p[0]);
+#pragma unroll
+    for (int i = 1; i < kP; ++i) s = __ffma2_rn(a.p[i], b.p[i], s);
+    return s.x + s.y;
+}
+
+// ------------------------------------------------------------------- activations
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 1 / (1 + exp(-g)); 0 and 1 where exp(-g) leaves the range
+__device__ __forceinline__ float2 logistic(float2 g)
+{
+    const float2 t = __fmul2_rn(g, both(-1.4426950408889634f));
+    const float2 d = __fadd2_rn(make_float2(exp2_approx(t.x), exp2_approx(t.y)), both(1.f));
+    return make_float2(rcp_approx(d.x), rcp_approx(d.y));
+}
+
+// Phi(g) and the normal density.  For bf16 tensors Phi is 1 - w or w with w =
+// poly(1 / (1 + 0.3275911 |g| / sqrt 2)) exp(-g^2 / 2) / 2 (Abramowitz & Stegun 7.1.26, error
+// below 1e-7, far below the output's rounding; the exponential is the density's too); for
+// fp32 tensors CUDA's normcdff.
+template <typename T> __device__ __forceinline__ float2 gelu_cdf(float2 g, float2 &density)
+{
+    if constexpr (sizeof(T) == 2) {
+        const float2 m = make_float2(fabsf(g.x), fabsf(g.y));
+        const float2 d = __ffma2_rn(m, both(0.3275911f * 0.70710678118654752f), both(1.f));
+        const float2 t = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+        const float2 q = __fmul2_rn(__fmul2_rn(g, g), both(-0.5f * 1.4426950408889634f));
+        const float2 e = make_float2(exp2_approx(q.x), exp2_approx(q.y));
+        float2 w = __ffma2_rn(t, both(0.5f * 1.061405429f), both(-0.5f * 1.453152027f));
+        w = __ffma2_rn(t, w, both(0.5f * 1.421413741f));
+        w = __ffma2_rn(t, w, both(-0.5f * 0.284496736f));
+        w = __ffma2_rn(t, w, both(0.5f * 0.254829592f));
+        w = __fmul2_rn(__fmul2_rn(t, w), e);
+        density = __fmul2_rn(e, both(0.3989422804014327f));
+        const float2 h = __ffma2_rn(w, both(-1.f), both(0.5f));
+        return __fadd2_rn(make_float2(copysignf(h.x, g.x), copysignf(h.y, g.y)), both(0.5f));
+    } else {
+        density = make_float2(expf(-0.5f * g.x * g.x) * 0.3989422804014327f, expf(-0.5f * g.y * g.y) * 0.3989422804014327f);
+        return make_float2(normcdff(g.x), normcdff(g.y));
+    }
+}
+
+// act(g): 1 sigmoid, 2 SiLU, 3 GELU (g Phi(g))
+template <typename T> __device__ __forceinline__ V8 act_value(int act, const V8 &g)
+{
+    V8 r;
+    if (act == 2) {
+#pragma unroll
+        for (int i = 0; i < kP; ++i) r.p[i] = __fmul2_rn(g.p[i], logistic(g.p[i]));
+    } else if (act == 3) {
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+            float2 d;
+            r.p[i] = __fmul2_rn(g.p[i], gelu_cdf<T>(g.p[i], d));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kP; ++i) r.p[i] = logistic(g.p[i]);
+    }
+    return r;
+}
+
+// act(g) and its derivative
+template <typename T> __device__ __forceinline__ void act_and_slope(int act, const V8 &g, V8 &a, V8 &da)
+{
+    if (act == 2) {
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+            const float2 s = logistic(g.p[i]);
+            a.p[i] = __fmul2_rn(g.p[i], s);
+            da.p[i] = __ffma2_rn(a.p[i], __ffma2_rn(s, both(-1.f), both(1.f)), s);
+        }
+    } else if (act == 3) {
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+            float2 d;
+            const float2 c = gelu_cdf<T>(g.p[i], d);
+            a.p[i] = __fmul2_rn(g.p[i], c);
+            da.p[i] = __ffma2_rn(g.p[i], d, c);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+            a.p[i] = logistic(g.p[i]);
+            da.p[i] = __fmul2_rn(a.p[i], __ffma2_rn(a.p[i], both(-1.f), both(1.f)));
+        }
+    }
+}
+
+// ------------------------------------------------------------------ chunk access
+
+// Eight features in the I/O type.
+template <typename T, bool VEC> struct Raw {
+    static constexpr int V = VEC ? 16 / (int)sizeof(T) : 1, N = kC / V;
+    Pack<T, V> q[N];
+    __device__ __forceinline__ V8 get() const
+    {
+        V8 r;
+        float *v = &r.p[0].x;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float w[V];
+            unpack(q[i], w);
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[i * V + j] = w[j];
+        }
+        return r;
+    }
+    __device__ __forceinline__ void put(const V8 &r)
+    {
+        const float *v = &r.p[0].x;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float w[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) w[j] = v[i * V + j];
+            pack(q[i], w);
+        }
+    }
+};
+
+// Which eight features of a row a thread holds: consecutive ones (VEC) or `lanes` apart.
+// VEC: a thread past the row's end works on the row's last chunk (`at`) and neither counts
+// nor stores.  Else features past D read as zeros.
+//
+// A row comes through shared memory: fetch() starts copies of the thread's own features,
+// get() reads them back once they have landed.  Only the thread itself reads what it
+// copied, so there is no barrier, and no load waits in a register.  slot: the thread's
+// place in a stage, 16-byte units `pitch` apart.  Where the copies do not go (DIRECT: bf16
+// rows that are not 16-byte aligned, as copies are 4 bytes at least, and widths whose sums
+// leave no room for stages) the slot holds the row's address and get() loads; not through
+// the read-only path, as h may be written over x.
+template <typename T, bool VEC, bool DIRECT = (!VEC && sizeof(T) == 2)> struct Chunk {
+    using R = Raw<T, VEC>;
+    static constexpr int kUnits = DIRECT ? 1 : kC * (int)sizeof(T) / 16;  // 16-byte units of a chunk
+    // rows in flight or landed.  Three were slower than two (8 x 2048 x 768 sandwich forward
+    // 35 us against 31, 2 x 32768 x 2048 306 against 287): the stages take the L1 that holds
+    // the parameter vectors.
+    static constexpr int kAhead = DIRECT ? 1 : 2;
+    int c0, at, step, D;
+    __device__ __forceinline__ Chunk(int r, int k, int lanes, int D_)
+        : c0(VEC ? (k * lanes + r) * kC : r + k * kC * lanes), step(VEC ? 1 : lanes), D(D_)
+    {
+        at = VEC ? min(c0, D - kC) : c0;
+    }
+    __device__ __forceinline__ bool has(int j) const { return VEC ? c0 < D : c0 + j * step < D; }
+    // zeros in the absent features (VEC: the whole chunk counts or not, see counted())
+    __device__ __forceinline__ void mask(V8 &v) const
+    {
+        if constexpr (!VEC) {
+            float *f = &v.p[0].x;
+#pragma unroll
+            for (int j = 0; j < kC; ++j) f[j] = has(j) ? f[j] : 0.f;
+        }
+    }
+    __device__ __forceinline__ float counted(float sum) const { return !VEC || c0 < D ? sum : 0.f; }
+    // Elements that feature c's head adds to its offset in a row whose features lie in heads
+    // of dh, sh elements apart (dh = D: none).  VEC: a chunk lies inside one head.
+    __device__ __forceinline__ long long head(int c, int dh, long long sh) const
+    {
+        return dh < D ? (long long)(c / dh) * (sh - dh) : 0;
+    }
+    // row: the token's first feature; off (VEC): head(at, ..)
+    __device__ __forceinline__ void fetch(const T *row, int dh, long long sh, long long off, uint4 *slot, int pitch) const
+    {
+        if constexpr (DIRECT) {
+            *reinterpret_cast<const T **>(slot) = row;
+        } else if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) copy_async16(slot + i * pitch, row + off + at + i * (16 / (int)sizeof(T)));
+        } else {
+#pragma unroll
+            for (int j = 0; j < kC; ++j) {
+                const int c = c0 + j * step;
+                if (c < D) copy_async4(reinterpret_cast<float *>(slot + j / 4 * pitch) + j % 4, row + head(c, dh, sh) + c);
+            }
+        }
+    }
+    __device__ __forceinline__ V8 get(const uint4 *slot, int pitch, int dh, long long sh, long long off) const
+    {
+        constexpr int V = 16 / (int)sizeof(T);
+        if constexpr (DIRECT) {
+            const T *row = *reinterpret_cast<const T *const *>(slot);
+            R q;
+#pragma unroll
+            for (int i = 0; i < R::N; ++i) {
+                const int c = VEC ? at + i * R::V : c0 + i * step;
+                q.q[i].raw = {};
+                if (VEC || c < D) q.q[i].load_rw(row + (VEC ? off : head(c, dh, sh)) + c);
+            }
+            return q.get();
+        } else {
+            Raw<T, true> q;
+#pragma unroll
+            for (int i = 0; i < kC / V; ++i) q.q[i].raw = slot[i * pitch];
+            V8 r = q.get();
+            mask(r);
+            return r;
+        }
+    }
+    // row (VEC: with the head's offset already in it)
+    __device__ __forceinline__ void store(T *row, const V8 &v) const
+    {
+        R r;
+        r.put(v);
+#pragma unroll
+        for (int i = 0; i < R::N; ++i)
+            if (has(i)) r.q[i].store(row + c0 + i * (VEC ? R::V : step));
+    }
+    __device__ __forceinline__ void store_heads(T *row, int dh, long long sh, long long off, const V8 &v) const
+    {
+        if constexpr (VEC) {
+            store(row + off, v);
+        } else {
+            R r;
+            r.put(v);
+#pragma unroll
+            for (int j = 0; j < kC; ++j) {
+                const int c = c0 + j * step;
+                if (c < D) r.q[j].store(row + head(c, dh, sh) + c);
+            }
+        }
+    }
+    // a parameter vector
+    __device__ __forceinline__ V8 vec(const float *p) const
+    {
+        V8 r = {};
+        if constexpr (VEC) {
+#pragma unroll
+            for (int j = 0; j < kP; j += 2) {
+                const float4 w = __ldg(reinterpret_cast<const float4 *>(p + at + 2 * j));
+                r.p[j] = make_float2(w.x, w.y);
+                r.p[j + 1] = make_float2(w.z, w.w);
+            }
+        } else {
+            float *v = &r.p[0].x;
+#pragma unroll
+            for (int j = 0; j < kC; ++j)
+                if (has(j)) v[j] = __ldg(p + c0 + j * step);
+        }
+        return r;
+    }
+};
+
+// -------------------------------------------------------------------- reductions
+
+// Sums over a row's group of threads.  BLOCK: over the block, through two shared slots
+// used in turn (a slot is written again only after the next reduction's barrier); the
+// slots of warps that are not there stay zero, and four warps' numbers are read at once.
+template <bool BLOCK> struct Group {
+    int lanes, warps;
+    float *red, *mine;  // the slot in use: all warps', this warp's (or half warp's) own
+
+    __device__ __forceinline__ float warp_sum(float v) const
+    {
+        if constexpr (BLOCK) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        } else {
+            for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        }
+        return v;
+    }
+    __device__ __forceinline__ void turn()
+    {
+        const int d = (reinterpret_cast<uintptr_t>(red) & 128) ? -32 : 32;
+        red += d;
+        mine += d;
+    }
+    // sums of a and of b
+    __device__ __forceinline__ float2 sum2(float a, float b)
+    {
+        if constexpr (BLOCK) {
+            // they share the shuffles: after the first exchange each half of the warp carries
+            // one of them
+            const bool up = threadIdx.x & 16;
+            float v = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, 16);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            if ((threadIdx.x & 15) == 0) *mine = v;
+            __syncthreads();
+            const float4 *q = reinterpret_cast<const float4 *>(red);
+            float2 s[2] = {both(0.f), both(0.f)};  // [0]: a of warps 0-3, ..
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (4 * i < warps) {
+                    const float4 x = q[i], y = q[4 + i];
+                    s[0] = __fadd2_rn(s[0], __fadd2_rn(make_float2(x.x, x.y), make_float2(x.z, x.w)));
+                    s[1] = __fadd2_rn(s[1], __fadd2_rn(make_float2(y.x, y.y), make_float2(y.z, y.w)));
+                }
+            turn();
+            return make_float2(s[0].x + s[0].y, s[1].x + s[1].y);
+        } else {
+            return make_float2(warp_sum(a), warp_sum(b));
+        }
+    }
+    __device__ __forceinline__ float sum1(float a)
+    {
+        a = warp_sum(a);
+        if constexpr (BLOCK) {
+            if ((threadIdx.x & 31) == 0) *mine = a;
+            __syncthreads();
+            const float4 *q = reinterpret_cast<const float4 *>(red);
+            float2 s = both(0.f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (4 * i < warps) {
+                    const float4 x = q[i];
+                    s = __fadd2_rn(s, __fadd2_rn(make_float2(x.x, x.y), make_float2(x.z, x.w)));
+                }
+            turn();
+            a = s.x + s.y;
+        }
+        return a;
+    }
+};
+
+// red: two slots of 16 warps' numbers for each of two sums
+template <bool BLOCK> __device__ __forceinline__ Group<BLOCK> make_group(float *red, int lanes)
+{
+    Group<BLOCK> g;
+    g.lanes = lanes;
+    g.warps = blockDim.x >> 5;
+    g.red = red;
+    // the upper half warp carries the second of two sums
+    g.mine = red + (threadIdx.x >> 5) + (threadIdx.x & 16);
+    if constexpr (BLOCK) {
+        for (int i = threadIdx.x; i < 64; i += blockDim.x) red[i] = 0.f;
+        __syncthreads();
+    }
+    return g;
+}
+
+// mean and 1 / sqrt(.. + eps) of a row held as v[K] (absent features are zeros or do not
+// count)
+template <typename T, bool VEC, int K, bool BLOCK>
+__device__ __forceinline__ float2 row_stats(Group<BLOCK> &g, int kind, float eps, float inv, const V8 (&v)[K], int r, int D)
+{
+    float mean = 0.f, s = 0.f;
+    if (kind == 2) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) s += Chunk<T, VEC>(r, k, g.lanes, D).counted(total(v[k]));
+        mean = g.sum1(s) * inv;
+        s = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const Chunk<T, VEC> c(r, k, g.lanes, D);
+            V8 d = add(v[k], splat(-mean));
+            c.mask(d);
+            s += c.counted(dot(d, d));
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < K; ++k) s += Chunk<T, VEC>(r, k, g.lanes, D).counted(dot(v[k], v[k]));
+    }
+    return make_float2(mean, rsqrtf(g.sum1(s) * inv + eps));
+}
+
+// ----------------------------------------------------------------------- forward
+
+// POST, PRE, ACT: 0 and 1 known, -1 by the parameters.  The rows' tensors are copied
+// kAhead rows ahead into the thread's ring of stages.
+template <typename T, bool VEC, int K, bool BLOCK, int POST, int PRE, int ACT>
+__global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(const __grid_constant__ NormFwdParams p)
+{
+    using C = Chunk<T, VEC>;
+    constexpr int kAhead = C::kAhead;
+    __shared__ __align__(256) float red[64];
+    extern __shared__ uint4 stages[];  // [kAhead][3][K][units][threads]
+    const int lanes = p.lanes, tid = threadIdx.x, r = BLOCK ? tid : tid & (lanes - 1), pitch = blockDim.x;
+    const uint32_t per = BLOCK ? 1 : blockDim.x / lanes, mine = BLOCK ? 0 : tid / lanes;
+    Group<BLOCK> g = make_group<BLOCK>(red, lanes);
+    const bool post = POST < 0 ? p.post != 0 : POST != 0, pre = PRE < 0 ? p.pre != 0 : PRE != 0;
+    const bool act = ACT < 0 ? p.act != 0 : ACT != 0, has_x = p.x != nullptr;
+    // a warp's groups leave the loop together: rows past the end are computed, not written
+    const uint32_t warp_first = BLOCK ? 0 : (tid & ~31) / lanes;
+    const T *yb = static_cast<const T *>(p.y), *xb = static_cast<const T *>(p.x), *gb = static_cast<const T *>(p.g);
+    const float inv = 1.f / (float)p.D;
+    const uint32_t stride = gridDim.x * per;
+    long long hoff[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) hoff[k] = VEC ? C(r, k, lanes, p.D).head(C(r, k, lanes, p.D).at, p.dh, p.ys[1]) : 0;
+    auto slot = [&](int stage, int tensor, int k) { return stages + ((stage * 3 + tensor) * K + k) * C::kUnits * pitch + tid; };
+    auto fetch = [&](uint32_t base, int stage) {
+        if (base + warp_first < p.rows) {
+            const uint32_t row = BLOCK ? base : min(base + mine, p.rows - 1);
+            const T *y, *gt, *x;
+            if (p.even) {
+                const size_t o = (size_t)row * p.D;
+                y = yb + o;
+                gt = gb + o;
+                x = xb + o;
+            } else {
+                const uint32_t b = p.byT(row), t = row - b * p.T;
+                y = yb + b * p.ys[0] + t * p.ys[2];
+                gt = gb + b * p.gs[0] + t * p.gs[1];
+                x = xb + b * p.xs[0] + t * p.xs[1];
+            }
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const C c(r, k, lanes, p.D);
+                c.fetch(y, p.dh, p.ys[1], hoff[k], slot(stage, 0, k), pitch);
+                if (act) c.fetch(gt, p.D, 0, 0, slot(stage, 1, k), pitch);
+                if (has_x) c.fetch(x, p.D, 0, 0, slot(stage, 2, k), pitch);
+            }
+        }
+        copy_commit();
+    };
+    uint32_t base = blockIdx.x * per;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch(base + i * stride, i);
+    for (int stage = 0; base + warp_first < p.rows; base += stride, stage = stage + 1 == kAhead ? 0 : stage + 1) {
+        const bool live = BLOCK || base + mine < p.rows;
+        const size_t off = (size_t)(base + mine) * p.D;
+        copy_wait<kAhead - 1>();
+        V8 v[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] = C(r, k, lanes, p.D).get(slot(stage, 0, k), pitch, p.dh, p.ys[1], hoff[k]);
+        float2 s1 = make_float2(0.f, 1.f), s2 = make_float2(0.f, 1.f);
+        if (post) s1 = row_stats<T, VEC, K, BLOCK>(g, p.post, p.eps1, inv, v, r, p.D);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const C c(r, k, lanes, p.D);
+            if (post) v[k] = fma(centre(v[k], s1.x, s1.y), c.vec(p.v.w1), c.vec(p.v.b1));
+            if (act) v[k] = mul(v[k], act_value<T>(p.act, c.get(slot(stage, 1, k), pitch, p.D, 0, 0)));
+            v[k] = mul(v[k], c.vec(p.v.sc));
+            if (has_x) v[k] = fma(c.get(slot(stage, 2, k), pitch, p.D, 0, 0), p.alpha, v[k]);
+            if (live) c.store(static_cast<T *>(p.h) + off, v[k]);
+            c.mask(v[k]);
+        }
+        fetch(base + kAhead * stride, stage);
+        if (pre) {
+            // of h in fp32, before the rounding that stores it
+            s2 = row_stats<T, VEC, K, BLOCK>(g, p.pre, p.eps2, inv, v, r, p.D);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const C c(r, k, lanes, p.D);
+                v[k] = fma(centre(v[k], s2.x, s2.y), c.vec(p.v.w2), c.vec(p.v.b2));
+                if (live) c.store(static_cast<T *>(p.u) + off, v[k]);
+            }
+        }
+        if (p.stats && live && r == 0)
+            *reinterpret_cast<float4 *>(p.stats + 4 * (size_t)(base + mine)) = make_float4(s1.x, s1.y, s2.x, s2.y);
+    }
+}
+
+// ---------------------------------------------------------------------- backward
+
+// Parameter gradients: every thread sums its own features over the block's rows (K = 1:
+// in registers; K > 1: in shared memory, which leaves none for stages), blocks write
+// partial sums, a second kernel adds those in order.  The result depends on the sizes and
+// the SM count only.
+template <typename T, bool VEC, int K, bool BLOCK, int MAXT, int POST, int PRE, int ACT>
+__global__ void __launch_bounds__(MAXT, 512 / MAXT) ttt_block_norm_bwd_kernel(const __grid_constant__ NormBwdParams p)
+{
+    constexpr bool DIRECT = K > 1 || (!VEC && sizeof(T) == 2);
+    using C = Chunk<T, VEC, DIRECT>;
+    constexpr int kAhead = C::kAhead, kStage = 5 * C::kUnits + 1;
+    __shared__ __align__(256) float red[64];
+    extern __shared__ uint4 stages[];  // [kAhead][5 units + 1][threads], then the sums:
+    // K > 1: [nvec][K][4][threads] pairs; K = 1, not BLOCK: [4][threads]
+    const int lanes = p.lanes, tid = threadIdx.x, threads = blockDim.x, r = BLOCK ? tid : tid & (lanes - 1);
+    float2 *accs = reinterpret_cast<float2 *>(stages + kAhead * kStage * threads);
+    const uint32_t per = BLOCK ? 1 : threads / lanes, mine = BLOCK ? 0 : tid / lanes;
+    Group<BLOCK> g = make_group<BLOCK>(red, lanes);
+    const bool post = POST < 0 ? p.post != 0 : POST != 0, pre = PRE < 0 ? p.pre != 0 : PRE != 0;
+    const bool act = ACT < 0 ? p.act != 0 : ACT != 0;
+    const bool has_x = pre && p.x, has_dh = p.dh_in != nullptr;
+    const uint32_t warp_first = BLOCK ? 0 : (tid & ~31) / lanes;
+    V8 acc[K == 1 ? 5 : 1];
+#pragma unroll
+    for (int i = 0; i < (K == 1 ? 5 : 1); ++i) acc[i] = splat(0.f);
+    if constexpr (K > 1)
+        for (int i = 0; i < p.nvec * K * kP; ++i) accs[i * threads + tid] = make_float2(0.f, 0.f);
+    // += a b
+    auto add_to = [&](int which, int k, const V8 &x, const V8 &y) {
+        if constexpr (K == 1) {
+            acc[which] = fma(x, y, acc[which]);
+        } else if (p.slot[which] >= 0) {
+#pragma unroll
+            for (int i = 0; i < kP; ++i) {
+                float2 &s = accs[((p.slot[which] * K + k) * kP + i) * threads + tid];
+                s = __ffma2_rn(x.p[i], y.p[i], s);
+            }
+        }
+    };
+    const V8 one = splat(1.f);
+    const float inv = 1.f / (float)p.D;
+    const T *yb = static_cast<const T *>(p.y), *xb = static_cast<const T *>(p.x), *gb = static_cast<const T *>(p.g);
+    const T *dhb = static_cast<const T *>(p.dh_in), *dub = static_cast<const T *>(p.du);
+    long long hoff[K], dyoff[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const C c(r, k, lanes, p.D);
+        hoff[k] = VEC ? c.head(c.at, p.dh, p.ys[1]) : 0;
+        dyoff[k] = VEC ? c.head(c.at, p.dh, (long long)p.T * p.dh) : 0;
+    }
+    const uint32_t stride = gridDim.x * per;
+    // K > 1 keeps addresses, which the chunks of a row share
+    auto slot = [&](int stage, int tensor) { return stages + (stage * kStage + tensor * C::kUnits) * threads + tid; };
+    auto fetch = [&](uint32_t base, int stage) {
+        if (base + warp_first < p.rows) {
+            const uint32_t row = BLOCK ? base : min(base + mine, p.rows - 1);
+            const T *y, *gt, *x, *du, *dh;
+            if (p.even) {
+                const size_t o = (size_t)row * p.D;
+                y = yb + o;
+                gt = gb + o;
+                x = xb + o;
+                du = dub + o;
+                dh = dhb + o;
+            } else {
+                const uint32_t b = p.byT(row), t = row - b * p.T;
+                y = yb + b * p.ys[0] + t * p.ys[2];
+                gt = gb + b * p.gs[0] + t * p.gs[1];
+                x = xb + b * p.xs[0] + t * p.xs[1];
+                du = dub + b * p.dus[0] + t * p.dus[1];
+                dh = dhb + b * p.dhs[0] + t * p.dhs[1];
+            }
+            const C c(r, 0, lanes, p.D);
+            copy_async16(slot(stage, 5), p.stats + 4 * (size_t)row);
+            c.fetch(y, p.dh, p.ys[1], hoff[0], slot(stage, 0), threads);
+            if (act) c.fetch(gt, p.D, 0, 0, slot(stage, 1), threads);
+            if (has_x) c.fetch(x, p.D, 0, 0, slot(stage, 2), threads);
+            if (pre) c.fetch(du, p.D, 0, 0, slot(stage, 3), threads);
+            if (has_dh) c.fetch(dh, p.D, 0, 0, slot(stage, 4), threads);
+        }
+        copy_commit();
+    };
+    uint32_t base = blockIdx.x * per;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch(base + i * stride, i);
+    for (int stage = 0; base + warp_first < p.rows; base += stride, stage = stage + 1 == kAhead ? 0 : stage + 1) {
+        const bool live = BLOCK || base + mine < p.rows;
+        const size_t off = (size_t)(base + mine) * p.D;
+        copy_wait<kAhead - 1>();
+        const float4 st = *reinterpret_cast<const float4 *>(slot(stage, 5));
+        V8 yn[K], A[K], dA[K], hn[K], G[K];
+        float a = 0.f, c2 = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const C c(r, k, lanes, p.D);
+            yn[k] = c.get(slot(stage, 0), threads, p.dh, p.ys[1], hoff[k]);
+            if (post) yn[k] = centre(yn[k], st.x, st.y);
+            c.mask(yn[k]);
+            if (act) act_and_slope<T>(p.act, c.get(slot(stage, 1), threads, p.D, 0, 0), A[k], dA[k]);
+            if (pre) {
+                // h again from the inputs, its normalised form, and the norm's backward sums
+                V8 h = post ? fma(yn[k], c.vec(p.v.w1), c.vec(p.v.b1)) : yn[k];
+                if (act) h = mul(h, A[k]);
+                h = mul(h, c.vec(p.v.sc));
+                if (has_x) h = fma(c.get(slot(stage, 2), threads, p.D, 0, 0), p.alpha, h);
+                hn[k] = centre(h, st.z, st.w);
+                c.mask(hn[k]);
+                G[k] = c.get(slot(stage, 3), threads, p.D, 0, 0);
+                if (live) {
+                    add_to(3, k, G[k], hn[k]);
+                    add_to(4, k, G[k], one);
+                }
+                G[k] = mul(G[k], c.vec(p.v.w2));
+                a += c.counted(total(G[k]));
+                c2 += c.counted(dot(G[k], hn[k]));
+            }
+        }
+        float ma = 0.f, mc = 0.f;
+        if (pre) {
+            const float2 m = g.sum2(a, c2);
+            ma = p.pre == 2 ? m.x * inv : 0.f;
+            mc = m.y * inv;
+        }
+        a = c2 = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const C c(r, k, lanes, p.D);
+            // G = dh + r (dn - mean(dn) - n mean(dn n))
+            G[k] = pre ? centre(fma(hn[k], -mc, G[k]), ma, st.w) : splat(0.f);
+            if (has_dh) G[k] = add(G[k], c.get(slot(stage, 4), threads, p.D, 0, 0));
+            if (p.dx && live) c.store(static_cast<T *>(p.dx) + off, mul(G[k], p.alpha));
+            const V8 pv = post ? fma(yn[k], c.vec(p.v.w1), c.vec(p.v.b1)) : yn[k];
+            if (live) add_to(2, k, act ? mul(G[k], A[k]) : G[k], pv);
+            G[k] = mul(G[k], c.vec(p.v.sc));
+            if (act) {
+                if (live) c.store(static_cast<T *>(p.dg) + off, mul(mul(G[k], pv), dA[k]));
+                G[k] = mul(G[k], A[k]);
+            }
+            // G is now dp
+            if (post) {
+                if (live) {
+                    add_to(0, k, G[k], yn[k]);
+                    add_to(1, k, G[k], one);
+                }
+                G[k] = mul(G[k], c.vec(p.v.w1));
+                c.mask(G[k]);
+                a += c.counted(total(G[k]));
+                c2 += c.counted(dot(G[k], yn[k]));
+            }
+        }
+        fetch(base + kAhead * stride, stage);
+        if (post) {
+            const float2 m = g.sum2(a, c2);
+            ma = p.post == 2 ? m.x * inv : 0.f;
+            mc = m.y * inv;
+        }
+        // dy is contiguous in y's own layout
+        T *dy = static_cast<T *>(p.dy) + off;
+        if (p.dh < p.D) {
+            const uint32_t row = BLOCK ? base : min(base + mine, p.rows - 1), b = p.byT(row), t = row - b * p.T;
+            dy = static_cast<T *>(p.dy) + (size_t)b * p.T * p.D + (size_t)t * p.dh;
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const C c(r, k, lanes, p.D);
+            if (post) G[k] = centre(fma(yn[k], -mc, G[k]), ma, st.y);
+            if (live) c.store_heads(dy, p.dh, (long long)p.T * p.dh, dyoff[k], G[k]);
+        }
+    }
+    if (p.nvec == 0) return;
+    float *part = p.part + (size_t)blockIdx.x * p.nvec * p.D;
+    if constexpr (!BLOCK) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+        if (p.slot[i] < 0) continue;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const C c(r, k, lanes, p.D);
+            V8 s;
+            if constexpr (K > 1) {
+#pragma unroll
+                for (int j = 0; j < kP; ++j) s.p[j] = accs[((p.slot[i] * K + k) * kP + j) * threads + tid];
+            } else if constexpr (BLOCK) {
+                s = acc[i];
+            } else {
+                // the block's row groups, added in order
+#pragma unroll
+                for (int j = 0; j < kP; ++j) accs[j * threads + tid] = acc[i].p[j];
+                __syncthreads();
+                s = splat(0.f);
+                if (tid < lanes)
+#pragma unroll
+                    for (int j = 0; j < kP; ++j)
+                        for (int m = r; m < threads; m += lanes) s.p[j] = __fadd2_rn(s.p[j], accs[j * threads + m]);
+                __syncthreads();
+            }
+            const float *f = &s.p[0].x;
+            if (BLOCK || tid < lanes)
+#pragma unroll
+                for (int j = 0; j < kC; ++j)
+                    if (c.has(j)) part[(size_t)p.slot[i] * p.D + c.c0 + j * c.step] = f[j];
+        }
+    }
+}
+
+// ------------------------------------------------------------------------ launch
+
+// Blocks of an SM for this kernel and shared memory (asked once for each).
+template <typename P> int resident(void (*kernel)(P), int threads, int smem)
+{
+    static std::mutex mu;
+    static struct {
+        void (*k)(P);
+        int dev, threads, smem, n;
+    } memo[128];
+    static int used = 0;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < used; ++i)
+        if (memo[i].k == kernel && memo[i].dev == dev && memo[i].threads == threads && memo[i].smem == smem) return memo[i].n;
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n < 1) n = 1;
+    if (used < 128) memo[used++] = {kernel, dev, threads, smem, n};
+    return n;
+}
+
+// Launches with as many blocks as the GPU holds at once (no more than limit, if any).
+template <typename P>
+int launch(void (*kernel)(P), const P &p, const NormShape &s, int limit, int smem, cudaStream_t st, int *blocks)
+{
+    if (smem > 40 * 1024 &&  // with the static part, past the 48 KB that need no asking
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return -4;
+    const long long per = s.block ? 1 : s.threads / s.lanes, groups = (p.rows + per - 1) / per;
+    long long n = (long long)kSMs * resident(kernel, s.threads, smem);
+    if (limit > 0 && n > limit) n = limit;
+    if (n > groups) n = groups;
+    *blocks = (int)n;
+    kernel<<<(int)n, s.threads, smem, st>>>(p);
+    return cudaGetLastError() == cudaSuccess ? 0 : -4;
+}
+
+template <typename T, bool VEC, int POST, int PRE, int ACT>
+int run_fwd(const NormFwdParams &p, const NormShape &s, cudaStream_t st)
+{
+    using C = Chunk<T, VEC>;
+    const int smem = C::kAhead * 3 * s.K * C::kUnits * s.threads * 16;
+    int n;
+    if (!s.block) return launch(ttt_block_norm_fwd_kernel<T, VEC, 1, false, POST, PRE, ACT>, p, s, 0, smem, st, &n);
+    return s.K == 1 ? launch(ttt_block_norm_fwd_kernel<T, VEC, 1, true, POST, PRE, ACT>, p, s, 0, smem, st, &n)
+                    : launch(ttt_block_norm_fwd_kernel<T, VEC, 2, true, POST, PRE, ACT>, p, s, 0, smem, st, &n);
+}
+
+template <typename T, bool VEC, int POST, int PRE, int ACT>
+int run_bwd(const NormBwdParams &p, const NormShape &s, int limit, cudaStream_t st, int *blocks)
+{
+    using C = Chunk<T, VEC>;
+    const int sums = s.block ? 0 : kC * 4, smem = (C::kAhead * (5 * C::kUnits + 1) * 16 + sums) * s.threads;
+    if (!s.block) return launch(ttt_block_norm_bwd_kernel<T, VEC, 1, false, 128, POST, PRE, ACT>, p, s, limit, smem, st, blocks);
+    return s.threads <= 256
+               ? launch(ttt_block_norm_bwd_kernel<T, VEC, 1, true, 256, POST, PRE, ACT>, p, s, limit, smem, st, blocks)
+               : launch(ttt_block_norm_bwd_kernel<T, VEC, 1, true, 512, POST, PRE, ACT>, p, s, limit, smem, st, blocks);
+}
+
+// Two chunks a thread: sums in shared memory, the parts by the parameters.
+template <typename T, bool VEC>
+int run_bwd_wide(const NormBwdParams &p, const NormShape &s, int limit, cudaStream_t st, int *blocks)
+{
+    using C = Chunk<T, VEC, true>;
+    const int smem = (C::kAhead * (5 * C::kUnits + 1) * 16 + p.nvec * 2 * kC * 4) * s.threads;
+    return launch(ttt_block_norm_bwd_kernel<T, VEC, 2, true, 512, -1, -1, -1>, p, s, limit, smem, st, blocks);
+}
+
+template <typename T> int norm_fwd(const NormFwdParams &p, const NormShape &s, bool vec, cudaStream_t st)
+{
+    if (!vec) return run_fwd<T, false, -1, -1, -1>(p, s, st);
+    switch ((p.post ? 4 : 0) | (p.pre ? 2 : 0) | (p.act ? 1 : 0)) {
+    case 0: return run_fwd<T, true, 0, 0, 0>(p, s, st);
+    case 1: return run_fwd<T, true, 0, 0, 1>(p, s, st);
+    case 2: return run_fwd<T, true, 0, 1, 0>(p, s, st);
+    case 3: return run_fwd<T, true, 0, 1, 1>(p, s, st);
+    case 4: return run_fwd<T, true, 1, 0, 0>(p, s, st);
+    case 5: return run_fwd<T, true, 1, 0, 1>(p, s, st);
+    case 6: return run_fwd<T, true, 1, 1, 0>(p, s, st);
+    default: return run_fwd<T, true, 1, 1, 1>(p, s, st);
+    }
+}
+
+template <typename T>
+int norm_bwd(const NormBwdParams &p, const NormShape &s, bool vec, int limit, cudaStream_t st, int *blocks)
+{
+    if (s.K > 1) return vec ? run_bwd_wide<T, true>(p, s, limit, st, blocks) : run_bwd_wide<T, false>(p, s, limit, st, blocks);
+    if (!vec) return run_bwd<T, false, -1, -1, -1>(p, s, limit, st, blocks);
+    switch ((p.post ? 4 : 0) | (p.pre ? 2 : 0) | (p.act ? 1 : 0)) {
+    case 0: return run_bwd<T, true, 0, 0, 0>(p, s, limit, st, blocks);
+    case 1: return run_bwd<T, true, 0, 0, 1>(p, s, limit, st, blocks);
+    case 2: return run_bwd<T, true, 0, 1, 0>(p, s, limit, st, blocks);
+    case 3: return run_bwd<T, true, 0, 1, 1>(p, s, limit, st, blocks);
+    case 4: return run_bwd<T, true, 1, 0, 0>(p, s, limit, st, blocks);
+    case 5: return run_bwd<T, true, 1, 0, 1>(p, s, limit, st, blocks);
+    case 6: return run_bwd<T, true, 1, 1, 0>(p, s, limit, st, blocks);
+    default: return run_bwd<T, true, 1, 1, 1>(p, s, limit, st, blocks);
+    }
+}
+
+}  // namespace
+}  // namespace ttt
