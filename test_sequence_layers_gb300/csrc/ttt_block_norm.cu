@@ -42,29 +42,38 @@ bool vectors(const BlockNormArgs &a, NormVectors &v)
     return true;
 }
 
-// Adds the blocks' partial parameter gradients in a fixed order.
+// Adds the blocks' partial parameter gradients in a fixed order: 32 columns a block, 32
+// threads a column, eight loads of each in flight.  Starts while the backward kernel ends
+// and waits for it on the device.
 struct ReduceParams {
     const float *part;
     float *out[5];  // by slot
     int nblocks, nvec, D;
 };
 
-__global__ void __launch_bounds__(512) ttt_block_norm_reduce_kernel(const __grid_constant__ ReduceParams p)
+__global__ void __launch_bounds__(1024) ttt_block_norm_reduce_kernel(const __grid_constant__ ReduceParams p)
 {
-    __shared__ float s[16][33];
-    const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane, slot = blockIdx.y;
+    __shared__ float s[32][33];
+    const int lane = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + lane, slot = blockIdx.y;
+    const size_t row = (size_t)p.nvec * p.D;
+    const float *src = p.part + (size_t)slot * p.D + c;
+    cudaGridDependencySynchronize();
     float v = 0.f;
     if (c < p.D)
-        for (int i = y; i < p.nblocks; i += 16) v += p.part[((size_t)i * p.nvec + slot) * p.D + c];
+        for (int i = y; i < p.nblocks; i += 32 * 8) {
+            float w[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) w[u] = i + 32 * u < p.nblocks ? src[(i + 32 * u) * row] : 0.f;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v += w[u];
+        }
     s[y][lane] = v;
     __syncthreads();
-    if (y == 0 && c < p.D) {
-        float t = 0.f;
+    v = s[lane][y];  // column y, partial sums across the warp
 #pragma unroll
-        for (int i = 0; i < 16; ++i) t += s[i][lane];
-        p.out[slot][c] = t;
-    }
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const int col = blockIdx.x * 32 + y;
+    if (lane == 0 && col < p.D) p.out[slot][col] = v;
 }
 
 // Threads of a row and chunks of a thread: part of a warp up to 256 features, then one
@@ -87,10 +96,11 @@ NormShape row_shape(int D, int two_from)
     return s;
 }
 
-// Forward: two chunks from 1024 features on halve what a row costs every thread: 287 us
-// against 327 at 2 x 32768 x 2048.  Backward: one, as its sums are registers.
+// Two chunks from 1024 features on halve what a row costs every thread: 2 x 32768 x 2048
+// forward 287 us against 327, backward (whose sums then take all 255 registers) 527
+// against 577; backward only with 16-byte rows.
 NormShape fwd_shape(int D) { return row_shape(D, 1024); }
-NormShape bwd_shape(int D) { return row_shape(D, 512 * kNormChunk); }
+NormShape bwd_shape(int D, bool vec) { return row_shape(D, vec ? 1024 : 512 * kNormChunk); }
 
 // 16-byte accesses: rows, strides and pointers in whole vectors, eight features a chunk.
 bool vector_ok(int es, int D, int dh, const void *const *ptr, int np, const long long *st, int ns)
@@ -112,11 +122,11 @@ bool even(const BlockNormArgs &a, const void *p, long long sb, long long st)
 
 }  // namespace
 
-// Blocks of the backward pass by size alone (the workspace holds their sums): 512 threads
-// an SM, which is what the kernels' registers allow.
+// The most blocks of the backward pass, by size alone (the workspace holds their sums): 512
+// threads an SM, which is what the kernels' registers allow; of two chunks each, fewer.
 int block_norm_bwd_blocks(int D, long long rows)
 {
-    const NormShape s = bwd_shape(D);
+    const NormShape s = bwd_shape(D, false);
     const long long per = s.block ? 1 : s.threads / s.lanes, groups = (rows + per - 1) / per;
     const long long fit = 152LL * (512 / s.threads);
     return (int)(groups < fit ? groups : fit);
@@ -179,7 +189,11 @@ int launch_block_norm_bwd(const BlockNormArgs &a)
         p.dhs[i] = a.dhs[i];
         p.dus[i] = a.dus[i];
     }
-    const NormShape s = bwd_shape(a.D);
+    const void *ptr[] = {a.y, a.x, a.gate, a.dh_in, a.du, a.dy, a.dx, a.dgate, a.w1, a.b1, a.scale, a.w2, a.b2};
+    const long long st[] = {a.ys[0],  a.ys[1],  a.ys[2],  a.xs[0],  a.xs[1], a.gs[0],
+                            a.gs[1], a.dhs[0], a.dhs[1], a.dus[0], a.dus[1]};
+    const bool vec = vector_ok(a.bf16 ? 2 : 4, a.D, a.dh, ptr, 13, st, 11);
+    const NormShape s = bwd_shape(a.D, vec);
     p.rows = (uint32_t)((long long)a.B * a.T);
     p.byT = make_div(a.T > 0 ? a.T : 1);
     p.T = a.T;
@@ -198,10 +212,6 @@ int launch_block_norm_bwd(const BlockNormArgs &a)
         p.slot[i] = a.dvec[i] ? p.nvec : -1;
         if (a.dvec[i]) q.out[p.nvec++] = a.dvec[i];
     }
-    const void *ptr[] = {a.y, a.x, a.gate, a.dh_in, a.du, a.dy, a.dx, a.dgate, a.w1, a.b1, a.scale, a.w2, a.b2};
-    const long long st[] = {a.ys[0],  a.ys[1],  a.ys[2],  a.xs[0],  a.xs[1], a.gs[0],
-                            a.gs[1], a.dhs[0], a.dhs[1], a.dus[0], a.dus[1]};
-    const bool vec = vector_ok(a.bf16 ? 2 : 4, a.D, a.dh, ptr, 13, st, 11);
     int blocks = 0;
     if (p.rows > 0) {  // no tokens: only the sums, all zero
         const int limit = block_norm_bwd_blocks(a.D, p.rows);
@@ -213,8 +223,16 @@ int launch_block_norm_bwd(const BlockNormArgs &a)
         q.nblocks = blocks;
         q.nvec = p.nvec;
         q.D = a.D;
-        ttt_block_norm_reduce_kernel<<<dim3((a.D + 31) / 32, p.nvec), 512, 0, a.stream>>>(q);
-        if (cudaGetLastError() != cudaSuccess) return -4;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((a.D + 31) / 32, p.nvec);
+        cfg.blockDim = dim3(1024);
+        cfg.stream = a.stream;
+        cudaLaunchAttribute at;
+        at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, ttt_block_norm_reduce_kernel, q) != cudaSuccess) return -4;
     }
     return 0;
 }

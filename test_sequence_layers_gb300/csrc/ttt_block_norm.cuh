@@ -624,19 +624,20 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(c
 
 // ---------------------------------------------------------------------- backward
 
-// Parameter gradients: every thread sums its own features over the block's rows (K = 1:
-// in registers; K > 1: in shared memory, which leaves none for stages), blocks write
+// Parameter gradients: every thread sums its own features over the block's rows (in
+// registers; WIDE: in shared memory, which leaves none for stages), blocks write
 // partial sums, a second kernel adds those in order.  The result depends on the sizes and
 // the SM count only.
 template <typename T, bool VEC, int K, bool BLOCK, int MAXT, int POST, int PRE, int ACT>
-__global__ void __launch_bounds__(MAXT, 512 / MAXT) ttt_block_norm_bwd_kernel(const __grid_constant__ NormBwdParams p)
+__global__ void __launch_bounds__(MAXT, K == 2 && MAXT == 256 ? 1 : 512 / MAXT) ttt_block_norm_bwd_kernel(const __grid_constant__ NormBwdParams p)
 {
-    constexpr bool DIRECT = K > 1 || (!VEC && sizeof(T) == 2);
+    constexpr bool WIDE = K > 1 && MAXT > 256;  // sums in shared memory
+    constexpr bool DIRECT = WIDE || (!VEC && sizeof(T) == 2);
     using C = Chunk<T, VEC, DIRECT>;
-    constexpr int kAhead = C::kAhead, kStage = 5 * C::kUnits + 1;
+    constexpr int KS = DIRECT ? 1 : K, kAhead = C::kAhead, kStage = 5 * KS * C::kUnits + 1;
     __shared__ __align__(256) float red[64];
     extern __shared__ uint4 stages[];  // [kAhead][5 units + 1][threads], then the sums:
-    // K > 1: [nvec][K][4][threads] pairs; K = 1, not BLOCK: [4][threads]
+    // WIDE: [nvec][K][4][threads] pairs; not BLOCK: [4][threads]
     const int lanes = p.lanes, tid = threadIdx.x, threads = blockDim.x, r = BLOCK ? tid : tid & (lanes - 1);
     float2 *accs = reinterpret_cast<float2 *>(stages + kAhead * kStage * threads);
     const uint32_t per = BLOCK ? 1 : threads / lanes, mine = BLOCK ? 0 : tid / lanes;
@@ -645,15 +646,17 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) ttt_block_norm_bwd_kernel(co
     const bool act = ACT < 0 ? p.act != 0 : ACT != 0;
     const bool has_x = pre && p.x, has_dh = p.dh_in != nullptr;
     const uint32_t warp_first = BLOCK ? 0 : (tid & ~31) / lanes;
-    V8 acc[K == 1 ? 5 : 1];
+    V8 acc[WIDE ? 1 : 5][K];
 #pragma unroll
-    for (int i = 0; i < (K == 1 ? 5 : 1); ++i) acc[i] = splat(0.f);
-    if constexpr (K > 1)
+    for (int i = 0; i < (WIDE ? 1 : 5); ++i)
+#pragma unroll
+        for (int k = 0; k < K; ++k) acc[i][k] = splat(0.f);
+    if constexpr (WIDE)
         for (int i = 0; i < p.nvec * K * kP; ++i) accs[i * threads + tid] = make_float2(0.f, 0.f);
     // += a b
     auto add_to = [&](int which, int k, const V8 &x, const V8 &y) {
-        if constexpr (K == 1) {
-            acc[which] = fma(x, y, acc[which]);
+        if constexpr (!WIDE) {
+            acc[which][k] = fma(x, y, acc[which][k]);
         } else if (p.slot[which] >= 0) {
 #pragma unroll
             for (int i = 0; i < kP; ++i) {
@@ -674,8 +677,10 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) ttt_block_norm_bwd_kernel(co
         dyoff[k] = VEC ? c.head(c.at, p.dh, (long long)p.T * p.dh) : 0;
     }
     const uint32_t stride = gridDim.x * per;
-    // K > 1 keeps addresses, which the chunks of a row share
-    auto slot = [&](int stage, int tensor) { return stages + (stage * kStage + tensor * C::kUnits) * threads + tid; };
+    // DIRECT keeps addresses, which the chunks of a row share
+    auto slot = [&](int stage, int tensor, int k) {
+        return stages + (stage * kStage + (tensor * KS + (DIRECT ? 0 : k)) * C::kUnits) * threads + tid;
+    };
     auto fetch = [&](uint32_t base, int stage) {
         if (base + warp_first < p.rows) {
             const uint32_t row = BLOCK ? base : min(base + mine, p.rows - 1);
@@ -695,13 +700,16 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) ttt_block_norm_bwd_kernel(co
                 du = dub + b * p.dus[0] + t * p.dus[1];
                 dh = dhb + b * p.dhs[0] + t * p.dhs[1];
             }
-            const C c(r, 0, lanes, p.D);
-            copy_async16(slot(stage, 5), p.stats + 4 * (size_t)row);
-            c.fetch(y, p.dh, p.ys[1], hoff[0], slot(stage, 0), threads);
-            if (act) c.fetch(gt, p.D, 0, 0, slot(stage, 1), threads);
-            if (has_x) c.fetch(x, p.D, 0, 0, slot(stage, 2), threads);
-            if (pre) c.fetch(du, p.D, 0, 0, slot(stage, 3), threads);
-            if (has_dh) c.fetch(dh, p.D, 0, 0, slot(stage, 4), threads);
+            copy_async16(slot(stage, 5, 0), p.stats + 4 * (size_t)row);
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                const C c(r, k, lanes, p.D);
+                c.fetch(y, p.dh, p.ys[1], hoff[k], slot(stage, 0, k), threads);
+                if (act) c.fetch(gt, p.D, 0, 0, slot(stage, 1, k), threads);
+                if (has_x) c.fetch(x, p.D, 0, 0, slot(stage, 2, k), threads);
+                if (pre) c.fetch(du, p.D, 0, 0, slot(stage, 3, k), threads);
+                if (has_dh) c.fetch(dh, p.D, 0, 0, slot(stage, 4, k), threads);
+            }
         }
         copy_commit();
     };
@@ -712,25 +720,25 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) ttt_block_norm_bwd_kernel(co
         const bool live = BLOCK || base + mine < p.rows;
         const size_t off = (size_t)(base + mine) * p.D;
         copy_wait<kAhead - 1>();
-        const float4 st = *reinterpret_cast<const float4 *>(slot(stage, 5));
+        const float4 st = *reinterpret_cast<const float4 *>(slot(stage, 5, 0));
         V8 yn[K], A[K], dA[K], hn[K], G[K];
         float a = 0.f, c2 = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const C c(r, k, lanes, p.D);
-            yn[k] = c.get(slot(stage, 0), threads, p.dh, p.ys[1], hoff[k]);
+            yn[k] = c.get(slot(stage, 0, k), threads, p.dh, p.ys[1], hoff[k]);
             if (post) yn[k] = centre(yn[k], st.x, st.y);
             c.mask(yn[k]);
-            if (act) act_and_slope<T>(p.act, c.get(slot(stage, 1), threads, p.D, 0, 0), A[k], dA[k]);
+            if (act) act_and_slope<T>(p.act, c.get(slot(stage, 1, k), threads, p.D, 0, 0), A[k], dA[k]);
             if (pre) {
                 // h again from the inputs, its normalised form, and the norm's backward sums
                 V8 h = post ? fma(yn[k], c.vec(p.v.w1), c.vec(p.v.b1)) : yn[k];
                 if (act) h = mul(h, A[k]);
                 h = mul(h, c.vec(p.v.sc));
-                if (has_x) h = fma(c.get(slot(stage, 2), threads, p.D, 0, 0), p.alpha, h);
+                if (has_x) h = fma(c.get(slot(stage, 2, k), threads, p.D, 0, 0), p.alpha, h);
                 hn[k] = centre(h, st.z, st.w);
                 c.mask(hn[k]);
-                G[k] = c.get(slot(stage, 3), threads, p.D, 0, 0);
+                G[k] = c.get(slot(stage, 3, k), threads, p.D, 0, 0);
                 if (live) {
                     add_to(3, k, G[k], hn[k]);
                     add_to(4, k, G[k], one);
@@ -752,7 +760,7 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) ttt_block_norm_bwd_kernel(co
             const C c(r, k, lanes, p.D);
             // G = dh + r (dn - mean(dn) - n mean(dn n))
             G[k] = pre ? centre(fma(hn[k], -mc, G[k]), ma, st.w) : splat(0.f);
-            if (has_dh) G[k] = add(G[k], c.get(slot(stage, 4), threads, p.D, 0, 0));
+            if (has_dh) G[k] = add(G[k], c.get(slot(stage, 4, k), threads, p.D, 0, 0));
             if (p.dx && live) c.store(static_cast<T *>(p.dx) + off, mul(G[k], p.alpha));
             const V8 pv = post ? fma(yn[k], c.vec(p.v.w1), c.vec(p.v.b1)) : yn[k];
             if (live) add_to(2, k, act ? mul(G[k], A[k]) : G[k], pv);
@@ -802,15 +810,15 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) ttt_block_norm_bwd_kernel(co
         for (int k = 0; k < K; ++k) {
             const C c(r, k, lanes, p.D);
             V8 s;
-            if constexpr (K > 1) {
+            if constexpr (WIDE) {
 #pragma unroll
                 for (int j = 0; j < kP; ++j) s.p[j] = accs[((p.slot[i] * K + k) * kP + j) * threads + tid];
             } else if constexpr (BLOCK) {
-                s = acc[i];
+                s = acc[i][k];
             } else {
                 // the block's row groups, added in order
 #pragma unroll
-                for (int j = 0; j < kP; ++j) accs[j * threads + tid] = acc[i].p[j];
+                for (int j = 0; j < kP; ++j) accs[j * threads + tid] = acc[i][k].p[j];
                 __syncthreads();
                 s = splat(0.f);
                 if (tid < lanes)
@@ -881,14 +889,17 @@ template <typename T, bool VEC, int POST, int PRE, int ACT>
 int run_bwd(const NormBwdParams &p, const NormShape &s, int limit, cudaStream_t st, int *blocks)
 {
     using C = Chunk<T, VEC>;
-    const int sums = s.block ? 0 : kC * 4, smem = (C::kAhead * (5 * C::kUnits + 1) * 16 + sums) * s.threads;
+    const int sums = s.block ? 0 : kC * 4, smem = (C::kAhead * (5 * s.K * C::kUnits + 1) * 16 + sums) * s.threads;
+    if constexpr (VEC)
+        if (s.K == 2)
+            return launch(ttt_block_norm_bwd_kernel<T, VEC, 2, true, 256, POST, PRE, ACT>, p, s, limit, smem, st, blocks);
     if (!s.block) return launch(ttt_block_norm_bwd_kernel<T, VEC, 1, false, 128, POST, PRE, ACT>, p, s, limit, smem, st, blocks);
     return s.threads <= 256
                ? launch(ttt_block_norm_bwd_kernel<T, VEC, 1, true, 256, POST, PRE, ACT>, p, s, limit, smem, st, blocks)
                : launch(ttt_block_norm_bwd_kernel<T, VEC, 1, true, 512, POST, PRE, ACT>, p, s, limit, smem, st, blocks);
 }
 
-// Two chunks a thread: sums in shared memory, the parts by the parameters.
+// Past 4096 features: sums in shared memory, the parts by the parameters.
 template <typename T, bool VEC>
 int run_bwd_wide(const NormBwdParams &p, const NormShape &s, int limit, cudaStream_t st, int *blocks)
 {
@@ -915,7 +926,7 @@ template <typename T> int norm_fwd(const NormFwdParams &p, const NormShape &s, b
 template <typename T>
 int norm_bwd(const NormBwdParams &p, const NormShape &s, bool vec, int limit, cudaStream_t st, int *blocks)
 {
-    if (s.K > 1) return vec ? run_bwd_wide<T, true>(p, s, limit, st, blocks) : run_bwd_wide<T, false>(p, s, limit, st, blocks);
+    if (s.threads > 256 && s.K > 1) return vec ? run_bwd_wide<T, true>(p, s, limit, st, blocks) : run_bwd_wide<T, false>(p, s, limit, st, blocks);
     if (!vec) return run_bwd<T, false, -1, -1, -1>(p, s, limit, st, blocks);
     switch ((p.post ? 4 : 0) | (p.pre ? 2 : 0) | (p.act ? 1 : 0)) {
     case 0: return run_bwd<T, true, 0, 0, 0>(p, s, limit, st, blocks);
