@@ -301,20 +301,23 @@ template <typename T, bool VEC> struct Raw {
 // VEC: a thread past the row's end works on the row's last chunk (`at`) and neither counts
 // nor stores.  Else features past D read as zeros.
 //
-// A row comes through shared memory: fetch() starts copies of the thread's own features,
-// get() reads them back once they have landed.  Only the thread itself reads what it
-// copied, so there is no barrier, and no load waits in a register.  slot: the thread's
-// place in a stage, 16-byte units `pitch` apart.  Where the copies do not go (DIRECT: bf16
-// rows that are not 16-byte aligned, as copies are 4 bytes at least, and widths whose sums
-// leave no room for stages) the slot holds the row's address and get() loads; not through
-// the read-only path, as h may be written over x.
-template <typename T, bool VEC, bool DIRECT = (!VEC && sizeof(T) == 2)> struct Chunk {
+// How a row's features arrive (FEED):
+//   kStaged (16-byte rows): through shared memory.  fetch() starts copies of the thread's
+//     own features, get() reads them back once they have landed.  Only the thread itself
+//     reads what it copied, so there is no barrier, and no load waits in a register.  slot:
+//     the thread's place in a stage, 16-byte units `pitch` apart.
+//   kRegisters (other rows): loaded a row ahead into registers, element by element.
+//   kDirect (widths whose sums leave room for neither): when they are used.
+// Loads do not go through the read-only path, as h may be written over x.
+enum Feed { kStaged, kRegisters, kDirect };
+
+template <typename T, bool VEC> struct Chunk {
     using R = Raw<T, VEC>;
-    static constexpr int kUnits = DIRECT ? 1 : kC * (int)sizeof(T) / 16;  // 16-byte units of a chunk
-    // rows in flight or landed.  Three were slower than two (8 x 2048 x 768 sandwich forward
-    // 35 us against 31, 2 x 32768 x 2048 306 against 287): the stages take the L1 that holds
-    // the parameter vectors.
-    static constexpr int kAhead = DIRECT ? 1 : 2;
+    static constexpr int kUnits = kC * (int)sizeof(T) / 16;  // 16-byte units of a chunk
+    // rows in flight or landed (kStaged).  Three were slower than two (8 x 2048 x 768 sandwich
+    // forward 35 us against 31, 2 x 32768 x 2048 306 against 287): the stages take the L1
+    // that holds the parameter vectors.
+    static constexpr int kAhead = 2;
     int c0, at, step, D;
     __device__ __forceinline__ Chunk(int r, int k, int lanes, int D_)
         : c0(VEC ? (k * lanes + r) * kC : r + k * kC * lanes), step(VEC ? 1 : lanes), D(D_)
@@ -339,41 +342,25 @@ template <typename T, bool VEC, bool DIRECT = (!VEC && sizeof(T) == 2)> struct C
         return dh < D ? (long long)(c / dh) * (sh - dh) : 0;
     }
     // row: the token's first feature; off (VEC): head(at, ..)
-    __device__ __forceinline__ void fetch(const T *row, int dh, long long sh, long long off, uint4 *slot, int pitch) const
+    __device__ __forceinline__ void fetch(const T *row, long long off, uint4 *slot, int pitch) const
     {
-        if constexpr (DIRECT) {
-            *reinterpret_cast<const T **>(slot) = row;
-        } else if constexpr (VEC) {
 #pragma unroll
-            for (int i = 0; i < kUnits; ++i) copy_async16(slot + i * pitch, row + off + at + i * (16 / (int)sizeof(T)));
-        } else {
-#pragma unroll
-            for (int j = 0; j < kC; ++j) {
-                const int c = c0 + j * step;
-                if (c < D) copy_async4(reinterpret_cast<float *>(slot + j / 4 * pitch) + j % 4, row + head(c, dh, sh) + c);
-            }
-        }
+        for (int i = 0; i < kUnits; ++i) copy_async16(slot + i * pitch, row + off + at + i * (16 / (int)sizeof(T)));
     }
-    __device__ __forceinline__ V8 get(const uint4 *slot, int pitch, int dh, long long sh, long long off) const
+    __device__ __forceinline__ V8 get(const uint4 *slot, int pitch) const
     {
-        constexpr int V = 16 / (int)sizeof(T);
-        if constexpr (DIRECT) {
-            const T *row = *reinterpret_cast<const T *const *>(slot);
-            R q;
+        Raw<T, true> q;
 #pragma unroll
-            for (int i = 0; i < R::N; ++i) {
-                const int c = VEC ? at + i * R::V : c0 + i * step;
-                q.q[i].raw = {};
-                if (VEC || c < D) q.q[i].load_rw(row + (VEC ? off : head(c, dh, sh)) + c);
-            }
-            return q.get();
-        } else {
-            Raw<T, true> q;
+        for (int i = 0; i < Raw<T, true>::N; ++i) q.q[i].raw = slot[i * pitch];
+        return q.get();
+    }
+    __device__ __forceinline__ void load(const T *row, int dh, long long sh, long long off, R &r) const
+    {
 #pragma unroll
-            for (int i = 0; i < kC / V; ++i) q.q[i].raw = slot[i * pitch];
-            V8 r = q.get();
-            mask(r);
-            return r;
+        for (int i = 0; i < R::N; ++i) {
+            const int c = VEC ? at + i * R::V : c0 + i * step;
+            r.q[i].raw = {};
+            if (VEC || c < D) r.q[i].load_rw(row + (VEC ? off : head(c, dh, sh)) + c);
         }
     }
     // row (VEC: with the head's offset already in it)
@@ -536,15 +523,15 @@ __device__ __forceinline__ float2 row_stats(Group<BLOCK> &g, int kind, float eps
 
 // ----------------------------------------------------------------------- forward
 
-// POST, PRE, ACT: 0 and 1 known, -1 by the parameters.  The rows' tensors are copied
-// kAhead rows ahead into the thread's ring of stages.
+// POST, PRE, ACT: 0 and 1 known, -1 by the parameters.
 template <typename T, bool VEC, int K, bool BLOCK, int POST, int PRE, int ACT>
 __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(const __grid_constant__ NormFwdParams p)
 {
     using C = Chunk<T, VEC>;
-    constexpr int kAhead = C::kAhead;
+    constexpr Feed FEED = VEC ? kStaged : kRegisters;
+    constexpr int kAhead = FEED == kStaged ? C::kAhead : 1;
     __shared__ __align__(256) float red[64];
-    extern __shared__ uint4 stages[];  // [kAhead][3][K][units][threads]
+    extern __shared__ uint4 stages[];  // kStaged: [kAhead][3][K][units][threads]
     const int lanes = p.lanes, tid = threadIdx.x, r = BLOCK ? tid : tid & (lanes - 1), pitch = blockDim.x;
     const uint32_t per = BLOCK ? 1 : blockDim.x / lanes, mine = BLOCK ? 0 : tid / lanes;
     Group<BLOCK> g = make_group<BLOCK>(red, lanes);
@@ -558,6 +545,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(c
     long long hoff[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) hoff[k] = VEC ? C(r, k, lanes, p.D).head(C(r, k, lanes, p.D).at, p.dh, p.ys[1]) : 0;
+    Raw<T, VEC> regs[3][K];
     auto slot = [&](int stage, int tensor, int k) { return stages + ((stage * 3 + tensor) * K + k) * C::kUnits * pitch + tid; };
     auto fetch = [&](uint32_t base, int stage) {
         if (base + warp_first < p.rows) {
@@ -577,12 +565,18 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(c
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 const C c(r, k, lanes, p.D);
-                c.fetch(y, p.dh, p.ys[1], hoff[k], slot(stage, 0, k), pitch);
-                if (act) c.fetch(gt, p.D, 0, 0, slot(stage, 1, k), pitch);
-                if (has_x) c.fetch(x, p.D, 0, 0, slot(stage, 2, k), pitch);
+                if constexpr (FEED == kStaged) {
+                    c.fetch(y, hoff[k], slot(stage, 0, k), pitch);
+                    if (act) c.fetch(gt, 0, slot(stage, 1, k), pitch);
+                    if (has_x) c.fetch(x, 0, slot(stage, 2, k), pitch);
+                } else {
+                    c.load(y, p.dh, p.ys[1], 0, regs[0][k]);
+                    if (act) c.load(gt, p.D, 0, 0, regs[1][k]);
+                    if (has_x) c.load(x, p.D, 0, 0, regs[2][k]);
+                }
             }
         }
-        copy_commit();
+        if constexpr (FEED == kStaged) copy_commit();
     };
     uint32_t base = blockIdx.x * per;
 #pragma unroll
@@ -590,19 +584,23 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(c
     for (int stage = 0; base + warp_first < p.rows; base += stride, stage = stage + 1 == kAhead ? 0 : stage + 1) {
         const bool live = BLOCK || base + mine < p.rows;
         const size_t off = (size_t)(base + mine) * p.D;
-        copy_wait<kAhead - 1>();
+        if constexpr (FEED == kStaged) copy_wait<kAhead - 1>();
+        auto take = [&](int tensor, int k, const C &c) {
+            if constexpr (FEED == kStaged) return c.get(slot(stage, tensor, k), pitch);
+            else return regs[tensor][k].get();
+        };
         V8 v[K];
 #pragma unroll
-        for (int k = 0; k < K; ++k) v[k] = C(r, k, lanes, p.D).get(slot(stage, 0, k), pitch, p.dh, p.ys[1], hoff[k]);
+        for (int k = 0; k < K; ++k) v[k] = take(0, k, C(r, k, lanes, p.D));
         float2 s1 = make_float2(0.f, 1.f), s2 = make_float2(0.f, 1.f);
         if (post) s1 = row_stats<T, VEC, K, BLOCK>(g, p.post, p.eps1, inv, v, r, p.D);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const C c(r, k, lanes, p.D);
             if (post) v[k] = fma(centre(v[k], s1.x, s1.y), c.vec(p.v.w1), c.vec(p.v.b1));
-            if (act) v[k] = mul(v[k], act_value<T>(p.act, c.get(slot(stage, 1, k), pitch, p.D, 0, 0)));
+            if (act) v[k] = mul(v[k], act_value<T>(p.act, take(1, k, c)));
             v[k] = mul(v[k], c.vec(p.v.sc));
-            if (has_x) v[k] = fma(c.get(slot(stage, 2, k), pitch, p.D, 0, 0), p.alpha, v[k]);
+            if (has_x) v[k] = fma(take(2, k, c), p.alpha, v[k]);
             if (live) c.store(static_cast<T *>(p.h) + off, v[k]);
             c.mask(v[k]);
         }
@@ -629,17 +627,17 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(c
 // partial sums, a second kernel adds those in order.  The result depends on the sizes and
 // the SM count only.
 template <typename T, bool VEC, int K, bool BLOCK, int MAXT, int POST, int PRE, int ACT>
-__global__ void __launch_bounds__(MAXT, K == 2 && MAXT == 256 ? 1 : 512 / MAXT) ttt_block_norm_bwd_kernel(const __grid_constant__ NormBwdParams p)
+__global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : (VEC && K == 1 ? 512 : 256) / MAXT) ttt_block_norm_bwd_kernel(const __grid_constant__ NormBwdParams p)
 {
     constexpr bool WIDE = K > 1 && MAXT > 256;  // sums in shared memory
-    constexpr bool DIRECT = WIDE || (!VEC && sizeof(T) == 2);
-    using C = Chunk<T, VEC, DIRECT>;
-    constexpr int KS = DIRECT ? 1 : K, kAhead = C::kAhead, kStage = 5 * KS * C::kUnits + 1;
+    constexpr Feed FEED = WIDE ? kDirect : VEC ? kStaged : kRegisters;
+    using C = Chunk<T, VEC>;
+    constexpr int kAhead = FEED == kStaged ? C::kAhead : 1, kStage = 5 * K * C::kUnits + 1;
     __shared__ __align__(256) float red[64];
-    extern __shared__ uint4 stages[];  // [kAhead][5 units + 1][threads], then the sums:
+    extern __shared__ uint4 stages[];  // kStaged: [kAhead][5 K units + 1][threads]; the sums:
     // WIDE: [nvec][K][4][threads] pairs; not BLOCK: [4][threads]
     const int lanes = p.lanes, tid = threadIdx.x, threads = blockDim.x, r = BLOCK ? tid : tid & (lanes - 1);
-    float2 *accs = reinterpret_cast<float2 *>(stages + kAhead * kStage * threads);
+    float2 *accs = reinterpret_cast<float2 *>(stages + (FEED == kStaged ? kAhead * kStage * threads : 0));
     const uint32_t per = BLOCK ? 1 : threads / lanes, mine = BLOCK ? 0 : tid / lanes;
     Group<BLOCK> g = make_group<BLOCK>(red, lanes);
     const bool post = POST < 0 ? p.post != 0 : POST != 0, pre = PRE < 0 ? p.pre != 0 : PRE != 0;
@@ -677,10 +675,10 @@ __global__ void __launch_bounds__(MAXT, K == 2 && MAXT == 256 ? 1 : 512 / MAXT) 
         dyoff[k] = VEC ? c.head(c.at, p.dh, (long long)p.T * p.dh) : 0;
     }
     const uint32_t stride = gridDim.x * per;
-    // DIRECT keeps addresses, which the chunks of a row share
-    auto slot = [&](int stage, int tensor, int k) {
-        return stages + (stage * kStage + (tensor * KS + (DIRECT ? 0 : k)) * C::kUnits) * threads + tid;
-    };
+    Raw<T, VEC> regs[5][FEED == kRegisters ? K : 1];
+    float4 next_st = make_float4(0.f, 1.f, 0.f, 1.f);
+    const T *rows[5];  // kDirect: the row's addresses
+    auto slot = [&](int stage, int tensor, int k) { return stages + (stage * kStage + (tensor * K + k) * C::kUnits) * threads + tid; };
     auto fetch = [&](uint32_t base, int stage) {
         if (base + warp_first < p.rows) {
             const uint32_t row = BLOCK ? base : min(base + mine, p.rows - 1);
@@ -700,18 +698,39 @@ __global__ void __launch_bounds__(MAXT, K == 2 && MAXT == 256 ? 1 : 512 / MAXT) 
                 du = dub + b * p.dus[0] + t * p.dus[1];
                 dh = dhb + b * p.dhs[0] + t * p.dhs[1];
             }
-            copy_async16(slot(stage, 5, 0), p.stats + 4 * (size_t)row);
+            if constexpr (FEED == kStaged) {
+                copy_async16(slot(stage, 5, 0), p.stats + 4 * (size_t)row);
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                const C c(r, k, lanes, p.D);
-                c.fetch(y, p.dh, p.ys[1], hoff[k], slot(stage, 0, k), threads);
-                if (act) c.fetch(gt, p.D, 0, 0, slot(stage, 1, k), threads);
-                if (has_x) c.fetch(x, p.D, 0, 0, slot(stage, 2, k), threads);
-                if (pre) c.fetch(du, p.D, 0, 0, slot(stage, 3, k), threads);
-                if (has_dh) c.fetch(dh, p.D, 0, 0, slot(stage, 4, k), threads);
+                for (int k = 0; k < K; ++k) {
+                    const C c(r, k, lanes, p.D);
+                    c.fetch(y, hoff[k], slot(stage, 0, k), threads);
+                    if (act) c.fetch(gt, 0, slot(stage, 1, k), threads);
+                    if (has_x) c.fetch(x, 0, slot(stage, 2, k), threads);
+                    if (pre) c.fetch(du, 0, slot(stage, 3, k), threads);
+                    if (has_dh) c.fetch(dh, 0, slot(stage, 4, k), threads);
+                }
+            } else {
+                next_st = *reinterpret_cast<const float4 *>(p.stats + 4 * (size_t)row);
+                if constexpr (FEED == kRegisters) {
+#pragma unroll
+                    for (int k = 0; k < K; ++k) {
+                        const C c(r, k, lanes, p.D);
+                        c.load(y, p.dh, p.ys[1], hoff[k], regs[0][k]);
+                        if (act) c.load(gt, p.D, 0, 0, regs[1][k]);
+                        if (has_x) c.load(x, p.D, 0, 0, regs[2][k]);
+                        if (pre) c.load(du, p.D, 0, 0, regs[3][k]);
+                        if (has_dh) c.load(dh, p.D, 0, 0, regs[4][k]);
+                    }
+                } else {
+                    rows[0] = y;
+                    rows[1] = gt;
+                    rows[2] = x;
+                    rows[3] = du;
+                    rows[4] = dh;
+                }
             }
         }
-        copy_commit();
+        if constexpr (FEED == kStaged) copy_commit();
     };
     uint32_t base = blockIdx.x * per;
 #pragma unroll
@@ -719,26 +738,41 @@ __global__ void __launch_bounds__(MAXT, K == 2 && MAXT == 256 ? 1 : 512 / MAXT) 
     for (int stage = 0; base + warp_first < p.rows; base += stride, stage = stage + 1 == kAhead ? 0 : stage + 1) {
         const bool live = BLOCK || base + mine < p.rows;
         const size_t off = (size_t)(base + mine) * p.D;
-        copy_wait<kAhead - 1>();
-        const float4 st = *reinterpret_cast<const float4 *>(slot(stage, 5, 0));
+        float4 st = next_st;
+        if constexpr (FEED == kStaged) {
+            copy_wait<kAhead - 1>();
+            st = *reinterpret_cast<const float4 *>(slot(stage, 5, 0));
+        }
+        auto take = [&](int tensor, int k, const C &c) {
+            if constexpr (FEED == kStaged) {
+                return c.get(slot(stage, tensor, k), threads);
+            } else if constexpr (FEED == kRegisters) {
+                return regs[tensor][k].get();
+            } else {
+                Raw<T, VEC> q;
+                if (tensor == 0) c.load(rows[0], p.dh, p.ys[1], hoff[k], q);
+                else c.load(rows[tensor], p.D, 0, 0, q);
+                return q.get();
+            }
+        };
         V8 yn[K], A[K], dA[K], hn[K], G[K];
         float a = 0.f, c2 = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const C c(r, k, lanes, p.D);
-            yn[k] = c.get(slot(stage, 0, k), threads, p.dh, p.ys[1], hoff[k]);
+            yn[k] = take(0, k, c);
             if (post) yn[k] = centre(yn[k], st.x, st.y);
             c.mask(yn[k]);
-            if (act) act_and_slope<T>(p.act, c.get(slot(stage, 1, k), threads, p.D, 0, 0), A[k], dA[k]);
+            if (act) act_and_slope<T>(p.act, take(1, k, c), A[k], dA[k]);
             if (pre) {
                 // h again from the inputs, its normalised form, and the norm's backward sums
                 V8 h = post ? fma(yn[k], c.vec(p.v.w1), c.vec(p.v.b1)) : yn[k];
                 if (act) h = mul(h, A[k]);
                 h = mul(h, c.vec(p.v.sc));
-                if (has_x) h = fma(c.get(slot(stage, 2, k), threads, p.D, 0, 0), p.alpha, h);
+                if (has_x) h = fma(take(2, k, c), p.alpha, h);
                 hn[k] = centre(h, st.z, st.w);
                 c.mask(hn[k]);
-                G[k] = c.get(slot(stage, 3, k), threads, p.D, 0, 0);
+                G[k] = take(3, k, c);
                 if (live) {
                     add_to(3, k, G[k], hn[k]);
                     add_to(4, k, G[k], one);
@@ -760,7 +794,7 @@ __global__ void __launch_bounds__(MAXT, K == 2 && MAXT == 256 ? 1 : 512 / MAXT) 
             const C c(r, k, lanes, p.D);
             // G = dh + r (dn - mean(dn) - n mean(dn n))
             G[k] = pre ? centre(fma(hn[k], -mc, G[k]), ma, st.w) : splat(0.f);
-            if (has_dh) G[k] = add(G[k], c.get(slot(stage, 4, k), threads, p.D, 0, 0));
+            if (has_dh) G[k] = add(G[k], take(4, k, c));
             if (p.dx && live) c.store(static_cast<T *>(p.dx) + off, mul(G[k], p.alpha));
             const V8 pv = post ? fma(yn[k], c.vec(p.v.w1), c.vec(p.v.b1)) : yn[k];
             if (live) add_to(2, k, act ? mul(G[k], A[k]) : G[k], pv);
@@ -878,7 +912,7 @@ template <typename T, bool VEC, int POST, int PRE, int ACT>
 int run_fwd(const NormFwdParams &p, const NormShape &s, cudaStream_t st)
 {
     using C = Chunk<T, VEC>;
-    const int smem = C::kAhead * 3 * s.K * C::kUnits * s.threads * 16;
+    const int smem = VEC ? C::kAhead * 3 * s.K * C::kUnits * s.threads * 16 : 0;
     int n;
     if (!s.block) return launch(ttt_block_norm_fwd_kernel<T, VEC, 1, false, POST, PRE, ACT>, p, s, 0, smem, st, &n);
     return s.K == 1 ? launch(ttt_block_norm_fwd_kernel<T, VEC, 1, true, POST, PRE, ACT>, p, s, 0, smem, st, &n)
@@ -889,7 +923,7 @@ template <typename T, bool VEC, int POST, int PRE, int ACT>
 int run_bwd(const NormBwdParams &p, const NormShape &s, int limit, cudaStream_t st, int *blocks)
 {
     using C = Chunk<T, VEC>;
-    const int sums = s.block ? 0 : kC * 4, smem = (C::kAhead * (5 * s.K * C::kUnits + 1) * 16 + sums) * s.threads;
+    const int sums = s.block ? 0 : kC * 4, smem = ((VEC ? C::kAhead * (5 * s.K * C::kUnits + 1) * 16 : 0) + sums) * s.threads;
     if constexpr (VEC)
         if (s.K == 2)
             return launch(ttt_block_norm_bwd_kernel<T, VEC, 2, true, 256, POST, PRE, ACT>, p, s, limit, smem, st, blocks);
@@ -903,8 +937,7 @@ int run_bwd(const NormBwdParams &p, const NormShape &s, int limit, cudaStream_t 
 template <typename T, bool VEC>
 int run_bwd_wide(const NormBwdParams &p, const NormShape &s, int limit, cudaStream_t st, int *blocks)
 {
-    using C = Chunk<T, VEC, true>;
-    const int smem = (C::kAhead * (5 * C::kUnits + 1) * 16 + p.nvec * 2 * kC * 4) * s.threads;
+    const int smem = p.nvec * 2 * kC * 4 * s.threads;
     return launch(ttt_block_norm_bwd_kernel<T, VEC, 2, true, 512, -1, -1, -1>, p, s, limit, smem, st, blocks);
 }
 
