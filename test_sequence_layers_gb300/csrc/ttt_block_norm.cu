@@ -100,18 +100,19 @@ NormShape row_shape(int D, int two_from)
 // forward 287 us against 327, backward (whose sums then take all 255 registers) 527
 // against 577; backward only with 16-byte rows.
 NormShape fwd_shape(int D) { return row_shape(D, 1024); }
-NormShape bwd_shape(int D, bool vec) { return row_shape(D, vec ? 1024 : 512 * kNormChunk); }
+NormShape bwd_shape(int D, bool whole) { return row_shape(D, whole ? 1024 : 512 * kNormChunk); }
 
-// 16-byte accesses: rows, strides and pointers in whole vectors, eight features a chunk.
-bool vector_ok(int es, int D, int dh, const void *const *ptr, int np, const long long *st, int ns)
+// Features that stand together in every tensor: eight (16-byte pointers and strides, D and
+// the heads multiples of eight), two (pairs aligned), or one.
+int features_together(int es, int D, int dh, const void *const *ptr, int np, const void *const *vec, const long long *st, int ns)
 {
-    const int v = 16 / es;
-    if (D % kNormChunk || dh % kNormChunk) return false;
-    for (int i = 0; i < np; ++i)
-        if (ptr[i] && reinterpret_cast<uintptr_t>(ptr[i]) % 16) return false;
-    for (int i = 0; i < ns; ++i)
-        if (st[i] % v) return false;
-    return true;
+    long long elems = D | dh, bytes = 0;
+    for (int i = 0; i < np; ++i) bytes |= (long long)reinterpret_cast<uintptr_t>(ptr[i]);
+    for (int i = 0; i < ns; ++i) bytes |= st[i] * es;
+    long long vb = 0;
+    for (int i = 0; i < 5; ++i) vb |= (long long)reinterpret_cast<uintptr_t>(vec[i]);
+    if (elems % kNormChunk == 0 && bytes % 16 == 0 && vb % 16 == 0) return kNormChunk;
+    return elems % 2 == 0 && bytes % (2 * es) == 0 && vb % 8 == 0 ? 2 : 1;
 }
 
 // Is a token-major tensor contiguous, or absent?
@@ -162,10 +163,10 @@ int launch_block_norm_fwd(const BlockNormArgs &a)
     p.eps1 = a.eps1;
     p.eps2 = a.eps2;
     p.alpha = a.alpha;
-    const void *ptr[] = {a.y, a.x, a.gate, a.h, a.u, a.w1, a.b1, a.scale, a.w2, a.b2};
+    const void *ptr[] = {a.y, a.x, a.gate, a.h, a.u}, *vec[] = {a.w1, a.b1, a.scale, a.w2, a.b2};
     const long long st[] = {a.ys[0], a.ys[1], a.ys[2], a.xs[0], a.xs[1], a.gs[0], a.gs[1]};
-    const bool vec = vector_ok(a.bf16 ? 2 : 4, a.D, a.dh, ptr, 10, st, 7);
-    return a.bf16 ? norm_fwd_bf16(p, s, vec, a.stream) : norm_fwd_f32(p, s, vec, a.stream);
+    const int group = features_together(a.bf16 ? 2 : 4, a.D, a.dh, ptr, 5, vec, st, 7);
+    return a.bf16 ? norm_fwd_bf16(p, s, group, a.stream) : norm_fwd_f32(p, s, group, a.stream);
 }
 
 int launch_block_norm_bwd(const BlockNormArgs &a)
@@ -189,11 +190,11 @@ int launch_block_norm_bwd(const BlockNormArgs &a)
         p.dhs[i] = a.dhs[i];
         p.dus[i] = a.dus[i];
     }
-    const void *ptr[] = {a.y, a.x, a.gate, a.dh_in, a.du, a.dy, a.dx, a.dgate, a.w1, a.b1, a.scale, a.w2, a.b2};
+    const void *ptr[] = {a.y, a.x, a.gate, a.dh_in, a.du, a.dy, a.dx, a.dgate}, *vec[] = {a.w1, a.b1, a.scale, a.w2, a.b2};
     const long long st[] = {a.ys[0],  a.ys[1],  a.ys[2],  a.xs[0],  a.xs[1], a.gs[0],
                             a.gs[1], a.dhs[0], a.dhs[1], a.dus[0], a.dus[1]};
-    const bool vec = vector_ok(a.bf16 ? 2 : 4, a.D, a.dh, ptr, 13, st, 11);
-    const NormShape s = bwd_shape(a.D, vec);
+    const int group = features_together(a.bf16 ? 2 : 4, a.D, a.dh, ptr, 8, vec, st, 11);
+    const NormShape s = bwd_shape(a.D, group == kNormChunk);
     p.rows = (uint32_t)((long long)a.B * a.T);
     p.byT = make_div(a.T > 0 ? a.T : 1);
     p.T = a.T;
@@ -215,7 +216,7 @@ int launch_block_norm_bwd(const BlockNormArgs &a)
     int blocks = 0;
     if (p.rows > 0) {  // no tokens: only the sums, all zero
         const int limit = block_norm_bwd_blocks(a.D, p.rows);
-        const int rc = a.bf16 ? norm_bwd_bf16(p, s, vec, limit, a.stream, &blocks) : norm_bwd_f32(p, s, vec, limit, a.stream, &blocks);
+        const int rc = a.bf16 ? norm_bwd_bf16(p, s, group, limit, a.stream, &blocks) : norm_bwd_f32(p, s, group, limit, a.stream, &blocks);
         if (rc) return rc;
     }
     if (p.nvec) {

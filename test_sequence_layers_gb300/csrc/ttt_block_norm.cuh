@@ -89,11 +89,12 @@ struct NormShape {
     bool block;
 };
 
-// One direction and type each (a translation unit each); limit: the most blocks, 0 none.
-int norm_fwd_bf16(const NormFwdParams &p, const NormShape &s, bool vec, cudaStream_t st);
-int norm_fwd_f32(const NormFwdParams &p, const NormShape &s, bool vec, cudaStream_t st);
-int norm_bwd_bf16(const NormBwdParams &p, const NormShape &s, bool vec, int limit, cudaStream_t st, int *blocks);
-int norm_bwd_f32(const NormBwdParams &p, const NormShape &s, bool vec, int limit, cudaStream_t st, int *blocks);
+// One direction and type each (a translation unit each); group: features that stand
+// together (8, 2, 1); limit: the most blocks.
+int norm_fwd_bf16(const NormFwdParams &p, const NormShape &s, int group, cudaStream_t st);
+int norm_fwd_f32(const NormFwdParams &p, const NormShape &s, int group, cudaStream_t st);
+int norm_bwd_bf16(const NormBwdParams &p, const NormShape &s, int group, int limit, cudaStream_t st, int *blocks);
+int norm_bwd_f32(const NormBwdParams &p, const NormShape &s, int group, int limit, cudaStream_t st, int *blocks);
 
 namespace {
 
@@ -267,9 +268,9 @@ template <typename T> __device__ __forceinline__ void act_and_slope(int act, con
 
 // ------------------------------------------------------------------ chunk access
 
-// Eight features in the I/O type.
-template <typename T, bool VEC> struct Raw {
-    static constexpr int V = VEC ? 16 / (int)sizeof(T) : 1, N = kC / V;
+// Eight features in the I/O type, G together in memory.
+template <typename T, int G> struct Raw {
+    static constexpr int V = G == kC ? 16 / (int)sizeof(T) : G, N = kC / V;  // features of a load, loads
     Pack<T, V> q[N];
     __device__ __forceinline__ V8 get() const
     {
@@ -297,9 +298,10 @@ template <typename T, bool VEC> struct Raw {
     }
 };
 
-// Which eight features of a row a thread holds: consecutive ones (VEC) or `lanes` apart.
-// VEC: a thread past the row's end works on the row's last chunk (`at`) and neither counts
-// nor stores.  Else features past D read as zeros.
+// Which eight features of a row a thread holds: consecutive ones (G = 8: rows of whole 16
+// bytes), or pieces of G `lanes` pieces apart (G = 2: pairs never straddle a row's end or an
+// alignment; G = 1).  G = 8: a thread past the row's end works on the row's last chunk
+// (`at`) and neither counts nor stores.  Else features past D read as zeros.
 //
 // How a row's features arrive (FEED):
 //   kStaged (16-byte rows): through shared memory.  fetch() starts copies of the thread's
@@ -311,8 +313,9 @@ template <typename T, bool VEC> struct Raw {
 // Loads do not go through the read-only path, as h may be written over x.
 enum Feed { kStaged, kRegisters, kDirect };
 
-template <typename T, bool VEC> struct Chunk {
-    using R = Raw<T, VEC>;
+template <typename T, int G> struct Chunk {
+    using R = Raw<T, G>;
+    static constexpr bool VEC = G == kC;
     static constexpr int kUnits = kC * (int)sizeof(T) / 16;  // 16-byte units of a chunk
     // rows in flight or landed (kStaged).  Three were slower than two (8 x 2048 x 768 sandwich
     // forward 35 us against 31, 2 x 32768 x 2048 306 against 287): the stages take the L1
@@ -320,23 +323,25 @@ template <typename T, bool VEC> struct Chunk {
     static constexpr int kAhead = 2;
     int c0, at, step, D;
     __device__ __forceinline__ Chunk(int r, int k, int lanes, int D_)
-        : c0(VEC ? (k * lanes + r) * kC : r + k * kC * lanes), step(VEC ? 1 : lanes), D(D_)
+        : c0(VEC ? (k * lanes + r) * kC : r * G + k * kC * lanes), step(lanes * G), D(D_)
     {
         at = VEC ? min(c0, D - kC) : c0;
     }
-    __device__ __forceinline__ bool has(int j) const { return VEC ? c0 < D : c0 + j * step < D; }
+    // first feature of load i, and whether it is there
+    __device__ __forceinline__ int col(int i) const { return VEC ? at + i * R::V : c0 + i * step; }
+    __device__ __forceinline__ bool has(int i) const { return VEC ? c0 < D : c0 + i * step < D; }
     // zeros in the absent features (VEC: the whole chunk counts or not, see counted())
     __device__ __forceinline__ void mask(V8 &v) const
     {
         if constexpr (!VEC) {
             float *f = &v.p[0].x;
 #pragma unroll
-            for (int j = 0; j < kC; ++j) f[j] = has(j) ? f[j] : 0.f;
+            for (int j = 0; j < kC; ++j) f[j] = has(j / G) ? f[j] : 0.f;
         }
     }
     __device__ __forceinline__ float counted(float sum) const { return !VEC || c0 < D ? sum : 0.f; }
     // Elements that feature c's head adds to its offset in a row whose features lie in heads
-    // of dh, sh elements apart (dh = D: none).  VEC: a chunk lies inside one head.
+    // of dh, sh elements apart (dh = D: none).  A load lies inside one head.
     __device__ __forceinline__ long long head(int c, int dh, long long sh) const
     {
         return dh < D ? (long long)(c / dh) * (sh - dh) : 0;
@@ -349,44 +354,37 @@ template <typename T, bool VEC> struct Chunk {
     }
     __device__ __forceinline__ V8 get(const uint4 *slot, int pitch) const
     {
-        Raw<T, true> q;
+        Raw<T, kC> q;
 #pragma unroll
-        for (int i = 0; i < Raw<T, true>::N; ++i) q.q[i].raw = slot[i * pitch];
+        for (int i = 0; i < Raw<T, kC>::N; ++i) q.q[i].raw = slot[i * pitch];
         return q.get();
     }
     __device__ __forceinline__ void load(const T *row, int dh, long long sh, long long off, R &r) const
     {
 #pragma unroll
         for (int i = 0; i < R::N; ++i) {
-            const int c = VEC ? at + i * R::V : c0 + i * step;
             r.q[i].raw = {};
-            if (VEC || c < D) r.q[i].load_rw(row + (VEC ? off : head(c, dh, sh)) + c);
+            if (VEC || has(i)) r.q[i].load_rw(row + (VEC ? off : head(col(i), dh, sh)) + col(i));
         }
     }
-    // row (VEC: with the head's offset already in it)
+    // VEC: row with the head's offset already in it
     __device__ __forceinline__ void store(T *row, const V8 &v) const
     {
         R r;
         r.put(v);
 #pragma unroll
         for (int i = 0; i < R::N; ++i)
-            if (has(i)) r.q[i].store(row + c0 + i * (VEC ? R::V : step));
+            if (has(i)) r.q[i].store(row + col(i));
     }
     __device__ __forceinline__ void store_heads(T *row, int dh, long long sh, long long off, const V8 &v) const
     {
-        if constexpr (VEC) {
-            store(row + off, v);
-        } else {
-            R r;
-            r.put(v);
+        R r;
+        r.put(v);
 #pragma unroll
-            for (int j = 0; j < kC; ++j) {
-                const int c = c0 + j * step;
-                if (c < D) r.q[j].store(row + head(c, dh, sh) + c);
-            }
-        }
+        for (int i = 0; i < R::N; ++i)
+            if (has(i)) r.q[i].store(row + (VEC ? off : head(col(i), dh, sh)) + col(i));
     }
-    // a parameter vector
+    // a parameter vector (G = 8: 16-byte, G = 2: 8-byte aligned)
     __device__ __forceinline__ V8 vec(const float *p) const
     {
         V8 r = {};
@@ -397,14 +395,20 @@ template <typename T, bool VEC> struct Chunk {
                 r.p[j] = make_float2(w.x, w.y);
                 r.p[j + 1] = make_float2(w.z, w.w);
             }
+        } else if constexpr (G == 2) {
+#pragma unroll
+            for (int j = 0; j < kP; ++j)
+                if (has(j)) r.p[j] = __ldg(reinterpret_cast<const float2 *>(p + col(j)));
         } else {
             float *v = &r.p[0].x;
 #pragma unroll
             for (int j = 0; j < kC; ++j)
-                if (has(j)) v[j] = __ldg(p + c0 + j * step);
+                if (has(j)) v[j] = __ldg(p + col(j));
         }
         return r;
     }
+    // feature j of a chunk, for the partial sums
+    __device__ __forceinline__ int feature(int j) const { return VEC ? c0 + j : c0 + j / G * step + j % G; }
 };
 
 // -------------------------------------------------------------------- reductions
@@ -498,25 +502,25 @@ template <bool BLOCK> __device__ __forceinline__ Group<BLOCK> make_group(float *
 
 // mean and 1 / sqrt(.. + eps) of a row held as v[K] (absent features are zeros or do not
 // count)
-template <typename T, bool VEC, int K, bool BLOCK>
+template <typename T, int G, int K, bool BLOCK>
 __device__ __forceinline__ float2 row_stats(Group<BLOCK> &g, int kind, float eps, float inv, const V8 (&v)[K], int r, int D)
 {
     float mean = 0.f, s = 0.f;
     if (kind == 2) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) s += Chunk<T, VEC>(r, k, g.lanes, D).counted(total(v[k]));
+        for (int k = 0; k < K; ++k) s += Chunk<T, G>(r, k, g.lanes, D).counted(total(v[k]));
         mean = g.sum1(s) * inv;
         s = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const Chunk<T, VEC> c(r, k, g.lanes, D);
+            const Chunk<T, G> c(r, k, g.lanes, D);
             V8 d = add(v[k], splat(-mean));
             c.mask(d);
             s += c.counted(dot(d, d));
         }
     } else {
 #pragma unroll
-        for (int k = 0; k < K; ++k) s += Chunk<T, VEC>(r, k, g.lanes, D).counted(dot(v[k], v[k]));
+        for (int k = 0; k < K; ++k) s += Chunk<T, G>(r, k, g.lanes, D).counted(dot(v[k], v[k]));
     }
     return make_float2(mean, rsqrtf(g.sum1(s) * inv + eps));
 }
@@ -524,17 +528,18 @@ __device__ __forceinline__ float2 row_stats(Group<BLOCK> &g, int kind, float eps
 // ----------------------------------------------------------------------- forward
 
 // POST, PRE, ACT: 0 and 1 known, -1 by the parameters.
-template <typename T, bool VEC, int K, bool BLOCK, int POST, int PRE, int ACT>
+template <typename T, int G, int K, bool BLOCK, int POST, int PRE, int ACT>
 __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(const __grid_constant__ NormFwdParams p)
 {
-    using C = Chunk<T, VEC>;
+    using C = Chunk<T, G>;
+    constexpr bool VEC = C::VEC;
     constexpr Feed FEED = VEC ? kStaged : kRegisters;
     constexpr int kAhead = FEED == kStaged ? C::kAhead : 1;
     __shared__ __align__(256) float red[64];
     extern __shared__ uint4 stages[];  // kStaged: [kAhead][3][K][units][threads]
     const int lanes = p.lanes, tid = threadIdx.x, r = BLOCK ? tid : tid & (lanes - 1), pitch = blockDim.x;
     const uint32_t per = BLOCK ? 1 : blockDim.x / lanes, mine = BLOCK ? 0 : tid / lanes;
-    Group<BLOCK> g = make_group<BLOCK>(red, lanes);
+    Group<BLOCK> grp = make_group<BLOCK>(red, lanes);
     const bool post = POST < 0 ? p.post != 0 : POST != 0, pre = PRE < 0 ? p.pre != 0 : PRE != 0;
     const bool act = ACT < 0 ? p.act != 0 : ACT != 0, has_x = p.x != nullptr;
     // a warp's groups leave the loop together: rows past the end are computed, not written
@@ -545,7 +550,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(c
     long long hoff[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) hoff[k] = VEC ? C(r, k, lanes, p.D).head(C(r, k, lanes, p.D).at, p.dh, p.ys[1]) : 0;
-    Raw<T, VEC> regs[3][K];
+    Raw<T, G> regs[3][K];
     auto slot = [&](int stage, int tensor, int k) { return stages + ((stage * 3 + tensor) * K + k) * C::kUnits * pitch + tid; };
     auto fetch = [&](uint32_t base, int stage) {
         if (base + warp_first < p.rows) {
@@ -593,7 +598,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(c
 #pragma unroll
         for (int k = 0; k < K; ++k) v[k] = take(0, k, C(r, k, lanes, p.D));
         float2 s1 = make_float2(0.f, 1.f), s2 = make_float2(0.f, 1.f);
-        if (post) s1 = row_stats<T, VEC, K, BLOCK>(g, p.post, p.eps1, inv, v, r, p.D);
+        if (post) s1 = row_stats<T, G, K, BLOCK>(grp, p.post, p.eps1, inv, v, r, p.D);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const C c(r, k, lanes, p.D);
@@ -607,7 +612,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(c
         fetch(base + kAhead * stride, stage);
         if (pre) {
             // of h in fp32, before the rounding that stores it
-            s2 = row_stats<T, VEC, K, BLOCK>(g, p.pre, p.eps2, inv, v, r, p.D);
+            s2 = row_stats<T, G, K, BLOCK>(grp, p.pre, p.eps2, inv, v, r, p.D);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 const C c(r, k, lanes, p.D);
@@ -626,12 +631,13 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(c
 // registers; WIDE: in shared memory, which leaves none for stages), blocks write
 // partial sums, a second kernel adds those in order.  The result depends on the sizes and
 // the SM count only.
-template <typename T, bool VEC, int K, bool BLOCK, int MAXT, int POST, int PRE, int ACT>
-__global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : (VEC && K == 1 ? 512 : 256) / MAXT) ttt_block_norm_bwd_kernel(const __grid_constant__ NormBwdParams p)
+template <typename T, int G, int K, bool BLOCK, int MAXT, int POST, int PRE, int ACT>
+__global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : (G == kC && K == 1 ? 512 : 256) / MAXT) ttt_block_norm_bwd_kernel(const __grid_constant__ NormBwdParams p)
 {
     constexpr bool WIDE = K > 1 && MAXT > 256;  // sums in shared memory
+    using C = Chunk<T, G>;
+    constexpr bool VEC = C::VEC;
     constexpr Feed FEED = WIDE ? kDirect : VEC ? kStaged : kRegisters;
-    using C = Chunk<T, VEC>;
     constexpr int kAhead = FEED == kStaged ? C::kAhead : 1, kStage = 5 * K * C::kUnits + 1;
     __shared__ __align__(256) float red[64];
     extern __shared__ uint4 stages[];  // kStaged: [kAhead][5 K units + 1][threads]; the sums:
@@ -639,7 +645,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : (VEC && K == 1 ? 512 :
     const int lanes = p.lanes, tid = threadIdx.x, threads = blockDim.x, r = BLOCK ? tid : tid & (lanes - 1);
     float2 *accs = reinterpret_cast<float2 *>(stages + (FEED == kStaged ? kAhead * kStage * threads : 0));
     const uint32_t per = BLOCK ? 1 : threads / lanes, mine = BLOCK ? 0 : tid / lanes;
-    Group<BLOCK> g = make_group<BLOCK>(red, lanes);
+    Group<BLOCK> grp = make_group<BLOCK>(red, lanes);
     const bool post = POST < 0 ? p.post != 0 : POST != 0, pre = PRE < 0 ? p.pre != 0 : PRE != 0;
     const bool act = ACT < 0 ? p.act != 0 : ACT != 0;
     const bool has_x = pre && p.x, has_dh = p.dh_in != nullptr;
@@ -675,7 +681,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : (VEC && K == 1 ? 512 :
         dyoff[k] = VEC ? c.head(c.at, p.dh, (long long)p.T * p.dh) : 0;
     }
     const uint32_t stride = gridDim.x * per;
-    Raw<T, VEC> regs[5][FEED == kRegisters ? K : 1];
+    Raw<T, G> regs[5][FEED == kRegisters ? K : 1];
     float4 next_st = make_float4(0.f, 1.f, 0.f, 1.f);
     const T *rows[5];  // kDirect: the row's addresses
     auto slot = [&](int stage, int tensor, int k) { return stages + (stage * kStage + (tensor * K + k) * C::kUnits) * threads + tid; };
@@ -749,13 +755,13 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : (VEC && K == 1 ? 512 :
             } else if constexpr (FEED == kRegisters) {
                 return regs[tensor][k].get();
             } else {
-                Raw<T, VEC> q;
+                Raw<T, G> q;
                 if (tensor == 0) c.load(rows[0], p.dh, p.ys[1], hoff[k], q);
                 else c.load(rows[tensor], p.D, 0, 0, q);
                 return q.get();
             }
         };
-        V8 yn[K], A[K], dA[K], hn[K], G[K];
+        V8 yn[K], A[K], dA[K], hn[K], gr[K];
         float a = 0.f, c2 = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -772,19 +778,19 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : (VEC && K == 1 ? 512 :
                 if (has_x) h = fma(take(2, k, c), p.alpha, h);
                 hn[k] = centre(h, st.z, st.w);
                 c.mask(hn[k]);
-                G[k] = take(3, k, c);
+                gr[k] = take(3, k, c);
                 if (live) {
-                    add_to(3, k, G[k], hn[k]);
-                    add_to(4, k, G[k], one);
+                    add_to(3, k, gr[k], hn[k]);
+                    add_to(4, k, gr[k], one);
                 }
-                G[k] = mul(G[k], c.vec(p.v.w2));
-                a += c.counted(total(G[k]));
-                c2 += c.counted(dot(G[k], hn[k]));
+                gr[k] = mul(gr[k], c.vec(p.v.w2));
+                a += c.counted(total(gr[k]));
+                c2 += c.counted(dot(gr[k], hn[k]));
             }
         }
         float ma = 0.f, mc = 0.f;
         if (pre) {
-            const float2 m = g.sum2(a, c2);
+            const float2 m = grp.sum2(a, c2);
             ma = p.pre == 2 ? m.x * inv : 0.f;
             mc = m.y * inv;
         }
@@ -792,32 +798,32 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : (VEC && K == 1 ? 512 :
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const C c(r, k, lanes, p.D);
-            // G = dh + r (dn - mean(dn) - n mean(dn n))
-            G[k] = pre ? centre(fma(hn[k], -mc, G[k]), ma, st.w) : splat(0.f);
-            if (has_dh) G[k] = add(G[k], take(4, k, c));
-            if (p.dx && live) c.store(static_cast<T *>(p.dx) + off, mul(G[k], p.alpha));
+            // gr = dh + r (dn - mean(dn) - n mean(dn n)), the gradient of h
+            gr[k] = pre ? centre(fma(hn[k], -mc, gr[k]), ma, st.w) : splat(0.f);
+            if (has_dh) gr[k] = add(gr[k], take(4, k, c));
+            if (p.dx && live) c.store(static_cast<T *>(p.dx) + off, mul(gr[k], p.alpha));
             const V8 pv = post ? fma(yn[k], c.vec(p.v.w1), c.vec(p.v.b1)) : yn[k];
-            if (live) add_to(2, k, act ? mul(G[k], A[k]) : G[k], pv);
-            G[k] = mul(G[k], c.vec(p.v.sc));
+            if (live) add_to(2, k, act ? mul(gr[k], A[k]) : gr[k], pv);
+            gr[k] = mul(gr[k], c.vec(p.v.sc));
             if (act) {
-                if (live) c.store(static_cast<T *>(p.dg) + off, mul(mul(G[k], pv), dA[k]));
-                G[k] = mul(G[k], A[k]);
+                if (live) c.store(static_cast<T *>(p.dg) + off, mul(mul(gr[k], pv), dA[k]));
+                gr[k] = mul(gr[k], A[k]);
             }
-            // G is now dp
+            // gr is now dp
             if (post) {
                 if (live) {
-                    add_to(0, k, G[k], yn[k]);
-                    add_to(1, k, G[k], one);
+                    add_to(0, k, gr[k], yn[k]);
+                    add_to(1, k, gr[k], one);
                 }
-                G[k] = mul(G[k], c.vec(p.v.w1));
-                c.mask(G[k]);
-                a += c.counted(total(G[k]));
-                c2 += c.counted(dot(G[k], yn[k]));
+                gr[k] = mul(gr[k], c.vec(p.v.w1));
+                c.mask(gr[k]);
+                a += c.counted(total(gr[k]));
+                c2 += c.counted(dot(gr[k], yn[k]));
             }
         }
         fetch(base + kAhead * stride, stage);
         if (post) {
-            const float2 m = g.sum2(a, c2);
+            const float2 m = grp.sum2(a, c2);
             ma = p.post == 2 ? m.x * inv : 0.f;
             mc = m.y * inv;
         }
@@ -830,8 +836,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : (VEC && K == 1 ? 512 :
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const C c(r, k, lanes, p.D);
-            if (post) G[k] = centre(fma(yn[k], -mc, G[k]), ma, st.y);
-            if (live) c.store_heads(dy, p.dh, (long long)p.T * p.dh, dyoff[k], G[k]);
+            if (post) gr[k] = centre(fma(yn[k], -mc, gr[k]), ma, st.y);
+            if (live) c.store_heads(dy, p.dh, (long long)p.T * p.dh, dyoff[k], gr[k]);
         }
     }
     if (p.nvec == 0) return;
@@ -865,7 +871,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : (VEC && K == 1 ? 512 :
             if (BLOCK || tid < lanes)
 #pragma unroll
                 for (int j = 0; j < kC; ++j)
-                    if (c.has(j)) part[(size_t)p.slot[i] * p.D + c.c0 + j * c.step] = f[j];
+                    if (VEC ? c.has(0) : c.has(j / G)) part[(size_t)p.slot[i] * p.D + c.feature(j)] = f[j];
         }
     }
 }
@@ -908,68 +914,72 @@ int launch(void (*kernel)(P), const P &p, const NormShape &s, int limit, int sme
     return cudaGetLastError() == cudaSuccess ? 0 : -4;
 }
 
-template <typename T, bool VEC, int POST, int PRE, int ACT>
+template <typename T, int G, int POST, int PRE, int ACT>
 int run_fwd(const NormFwdParams &p, const NormShape &s, cudaStream_t st)
 {
-    using C = Chunk<T, VEC>;
-    const int smem = VEC ? C::kAhead * 3 * s.K * C::kUnits * s.threads * 16 : 0;
+    using C = Chunk<T, G>;
+    const int smem = C::VEC ? C::kAhead * 3 * s.K * C::kUnits * s.threads * 16 : 0;
     int n;
-    if (!s.block) return launch(ttt_block_norm_fwd_kernel<T, VEC, 1, false, POST, PRE, ACT>, p, s, 0, smem, st, &n);
-    return s.K == 1 ? launch(ttt_block_norm_fwd_kernel<T, VEC, 1, true, POST, PRE, ACT>, p, s, 0, smem, st, &n)
-                    : launch(ttt_block_norm_fwd_kernel<T, VEC, 2, true, POST, PRE, ACT>, p, s, 0, smem, st, &n);
+    if (!s.block) return launch(ttt_block_norm_fwd_kernel<T, G, 1, false, POST, PRE, ACT>, p, s, 0, smem, st, &n);
+    return s.K == 1 ? launch(ttt_block_norm_fwd_kernel<T, G, 1, true, POST, PRE, ACT>, p, s, 0, smem, st, &n)
+                    : launch(ttt_block_norm_fwd_kernel<T, G, 2, true, POST, PRE, ACT>, p, s, 0, smem, st, &n);
 }
 
-template <typename T, bool VEC, int POST, int PRE, int ACT>
+template <typename T, int G, int POST, int PRE, int ACT>
 int run_bwd(const NormBwdParams &p, const NormShape &s, int limit, cudaStream_t st, int *blocks)
 {
-    using C = Chunk<T, VEC>;
-    const int sums = s.block ? 0 : kC * 4, smem = ((VEC ? C::kAhead * (5 * s.K * C::kUnits + 1) * 16 : 0) + sums) * s.threads;
-    if constexpr (VEC)
+    using C = Chunk<T, G>;
+    const int sums = s.block ? 0 : kC * 4, smem = ((C::VEC ? C::kAhead * (5 * s.K * C::kUnits + 1) * 16 : 0) + sums) * s.threads;
+    if constexpr (C::VEC)
         if (s.K == 2)
-            return launch(ttt_block_norm_bwd_kernel<T, VEC, 2, true, 256, POST, PRE, ACT>, p, s, limit, smem, st, blocks);
-    if (!s.block) return launch(ttt_block_norm_bwd_kernel<T, VEC, 1, false, 128, POST, PRE, ACT>, p, s, limit, smem, st, blocks);
+            return launch(ttt_block_norm_bwd_kernel<T, G, 2, true, 256, POST, PRE, ACT>, p, s, limit, smem, st, blocks);
+    if (!s.block) return launch(ttt_block_norm_bwd_kernel<T, G, 1, false, 128, POST, PRE, ACT>, p, s, limit, smem, st, blocks);
     return s.threads <= 256
-               ? launch(ttt_block_norm_bwd_kernel<T, VEC, 1, true, 256, POST, PRE, ACT>, p, s, limit, smem, st, blocks)
-               : launch(ttt_block_norm_bwd_kernel<T, VEC, 1, true, 512, POST, PRE, ACT>, p, s, limit, smem, st, blocks);
+               ? launch(ttt_block_norm_bwd_kernel<T, G, 1, true, 256, POST, PRE, ACT>, p, s, limit, smem, st, blocks)
+               : launch(ttt_block_norm_bwd_kernel<T, G, 1, true, 512, POST, PRE, ACT>, p, s, limit, smem, st, blocks);
 }
 
 // Past 4096 features: sums in shared memory, the parts by the parameters.
-template <typename T, bool VEC>
+template <typename T, int G>
 int run_bwd_wide(const NormBwdParams &p, const NormShape &s, int limit, cudaStream_t st, int *blocks)
 {
     const int smem = p.nvec * 2 * kC * 4 * s.threads;
-    return launch(ttt_block_norm_bwd_kernel<T, VEC, 2, true, 512, -1, -1, -1>, p, s, limit, smem, st, blocks);
+    return launch(ttt_block_norm_bwd_kernel<T, G, 2, true, 512, -1, -1, -1>, p, s, limit, smem, st, blocks);
 }
 
-template <typename T> int norm_fwd(const NormFwdParams &p, const NormShape &s, bool vec, cudaStream_t st)
+template <typename T> int norm_fwd(const NormFwdParams &p, const NormShape &s, int group, cudaStream_t st)
 {
-    if (!vec) return run_fwd<T, false, -1, -1, -1>(p, s, st);
+    if (group < kC) return group == 2 ? run_fwd<T, 2, -1, -1, -1>(p, s, st) : run_fwd<T, 1, -1, -1, -1>(p, s, st);
     switch ((p.post ? 4 : 0) | (p.pre ? 2 : 0) | (p.act ? 1 : 0)) {
-    case 0: return run_fwd<T, true, 0, 0, 0>(p, s, st);
-    case 1: return run_fwd<T, true, 0, 0, 1>(p, s, st);
-    case 2: return run_fwd<T, true, 0, 1, 0>(p, s, st);
-    case 3: return run_fwd<T, true, 0, 1, 1>(p, s, st);
-    case 4: return run_fwd<T, true, 1, 0, 0>(p, s, st);
-    case 5: return run_fwd<T, true, 1, 0, 1>(p, s, st);
-    case 6: return run_fwd<T, true, 1, 1, 0>(p, s, st);
-    default: return run_fwd<T, true, 1, 1, 1>(p, s, st);
+    case 0: return run_fwd<T, kC, 0, 0, 0>(p, s, st);
+    case 1: return run_fwd<T, kC, 0, 0, 1>(p, s, st);
+    case 2: return run_fwd<T, kC, 0, 1, 0>(p, s, st);
+    case 3: return run_fwd<T, kC, 0, 1, 1>(p, s, st);
+    case 4: return run_fwd<T, kC, 1, 0, 0>(p, s, st);
+    case 5: return run_fwd<T, kC, 1, 0, 1>(p, s, st);
+    case 6: return run_fwd<T, kC, 1, 1, 0>(p, s, st);
+    default: return run_fwd<T, kC, 1, 1, 1>(p, s, st);
     }
 }
 
 template <typename T>
-int norm_bwd(const NormBwdParams &p, const NormShape &s, bool vec, int limit, cudaStream_t st, int *blocks)
+int norm_bwd(const NormBwdParams &p, const NormShape &s, int group, int limit, cudaStream_t st, int *blocks)
 {
-    if (s.threads > 256 && s.K > 1) return vec ? run_bwd_wide<T, true>(p, s, limit, st, blocks) : run_bwd_wide<T, false>(p, s, limit, st, blocks);
-    if (!vec) return run_bwd<T, false, -1, -1, -1>(p, s, limit, st, blocks);
+    if (s.threads > 256 && s.K > 1)
+        return group == kC  ? run_bwd_wide<T, kC>(p, s, limit, st, blocks)
+               : group == 2 ? run_bwd_wide<T, 2>(p, s, limit, st, blocks)
+                            : run_bwd_wide<T, 1>(p, s, limit, st, blocks);
+    if (group < kC)
+        return group == 2 ? run_bwd<T, 2, -1, -1, -1>(p, s, limit, st, blocks) : run_bwd<T, 1, -1, -1, -1>(p, s, limit, st, blocks);
     switch ((p.post ? 4 : 0) | (p.pre ? 2 : 0) | (p.act ? 1 : 0)) {
-    case 0: return run_bwd<T, true, 0, 0, 0>(p, s, limit, st, blocks);
-    case 1: return run_bwd<T, true, 0, 0, 1>(p, s, limit, st, blocks);
-    case 2: return run_bwd<T, true, 0, 1, 0>(p, s, limit, st, blocks);
-    case 3: return run_bwd<T, true, 0, 1, 1>(p, s, limit, st, blocks);
-    case 4: return run_bwd<T, true, 1, 0, 0>(p, s, limit, st, blocks);
-    case 5: return run_bwd<T, true, 1, 0, 1>(p, s, limit, st, blocks);
-    case 6: return run_bwd<T, true, 1, 1, 0>(p, s, limit, st, blocks);
-    default: return run_bwd<T, true, 1, 1, 1>(p, s, limit, st, blocks);
+    case 0: return run_bwd<T, kC, 0, 0, 0>(p, s, limit, st, blocks);
+    case 1: return run_bwd<T, kC, 0, 0, 1>(p, s, limit, st, blocks);
+    case 2: return run_bwd<T, kC, 0, 1, 0>(p, s, limit, st, blocks);
+    case 3: return run_bwd<T, kC, 0, 1, 1>(p, s, limit, st, blocks);
+    case 4: return run_bwd<T, kC, 1, 0, 0>(p, s, limit, st, blocks);
+    case 5: return run_bwd<T, kC, 1, 0, 1>(p, s, limit, st, blocks);
+    case 6: return run_bwd<T, kC, 1, 1, 0>(p, s, limit, st, blocks);
+    default: return run_bwd<T, kC, 1, 1, 1>(p, s, limit, st, blocks);
     }
 }
 

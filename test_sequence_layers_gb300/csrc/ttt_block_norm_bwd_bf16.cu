@@ -3,9 +3,9 @@
 
 namespace ttt {
 
-int norm_bwd_bf16(const NormBwdParams &p, const NormShape &s, bool vec, int limit, cudaStream_t st, int *blocks)
+int norm_bwd_bf16(const NormBwdParams &p, const NormShape &s, int group, int limit, cudaStream_t st, int *blocks)
 {
-    return norm_bwd<__nv_bfloat16>(p, s, vec, limit, st, blocks);
+    return norm_bwd<__nv_bfloat16>(p, s, group, limit, st, blocks);
 }
 
 }  // namespace ttt

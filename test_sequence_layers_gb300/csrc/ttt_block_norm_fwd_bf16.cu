@@ -3,9 +3,9 @@
 
 namespace ttt {
 
-int norm_fwd_bf16(const NormFwdParams &p, const NormShape &s, bool vec, cudaStream_t st)
+int norm_fwd_bf16(const NormFwdParams &p, const NormShape &s, int group, cudaStream_t st)
 {
-    return norm_fwd<__nv_bfloat16>(p, s, vec, st);
+    return norm_fwd<__nv_bfloat16>(p, s, group, st);
 }
 
 }  // namespace ttt

@@ -3,9 +3,9 @@
 
 namespace ttt {
 
-int norm_fwd_f32(const NormFwdParams &p, const NormShape &s, bool vec, cudaStream_t st)
+int norm_fwd_f32(const NormFwdParams &p, const NormShape &s, int group, cudaStream_t st)
 {
-    return norm_fwd<float>(p, s, vec, st);
+    return norm_fwd<float>(p, s, group, st);
 }
 
 }  // namespace ttt

@@ -29,6 +29,7 @@ struct RecurParams {
     long long xs[2], fs[2], ds[2];
     int B, T, C, chunks;
     int cluster, cblocks;  // tile kernels: blocks of a cluster, channel blocks of a batch entry
+    int pairs;             // not TMA, bf16: two channels are aligned to four bytes everywhere
     int *status;           // device status word (timeouts)
 };
 
@@ -248,17 +249,30 @@ template <int N, bool WIDE, typename T> __device__ __forceinline__ void put_part
     }
 }
 
+template <int N, typename T> __device__ __forceinline__ void put_tokens(T *p, int c, int C, bool pairs, F<N> v)
+{
+    if (N == 2 && pairs) {
+        if (c < C) put(p + c, v);
+    } else {
+        put_part<N, false>(p, c, C, v);
+    }
+}
+
 // A lane's channels of a warp's tokens t0 .. t0 + n - 1 into the stage, zeros behind them:
-// cp.async for fp32, loads and stores for bf16.
+// four bytes by cp.async where they are aligned (fp32, pairs of bf16), else by loads and
+// stores.
 template <typename T, int N>
-__device__ __forceinline__ void copy_rows(const T *src, long long stride, int c, int C, int n, unsigned char *dst)
+__device__ __forceinline__ void copy_rows(const T *src, long long stride, int c, int C, int n, bool pairs, unsigned char *dst)
 {
     src += c;
     if (n == kS && c + N <= C) {
+        if (N == 1 || pairs) {
 #pragma unroll
-        for (int s = 0; s < kS; ++s, src += stride) {
-            if constexpr (N == 1) copy_async4(dst + s * kRowBytes, src);
-            else *reinterpret_cast<uint32_t *>(dst + s * kRowBytes) = pack2(ld1(src), ld1(src + 1));
+            for (int s = 0; s < kS; ++s, src += stride) copy_async4(dst + s * kRowBytes, src);
+        } else {
+#pragma unroll
+            for (int s = 0; s < kS; ++s, src += stride)
+                *reinterpret_cast<uint32_t *>(dst + s * kRowBytes) = pack2(ld1(src), ld1(src + 1));
         }
         return;
     }
@@ -424,8 +438,8 @@ __global__ void __launch_bounds__(32 * kW, 2)
         const long long t0 = (long long)(round * P + rank) * kRecurChunk + warp * kS;
         const int n = (int)min(max(p.T - t0, 0LL), (long long)kS);
         unsigned char *dst = stages + (round % kFwdStages) * 2 * kPlane + warp * kS * kRowBytes + lane * 4;
-        copy_rows<T, N>(static_cast<const T *>(p.f) + b * p.fs[0] + t0 * p.fs[1], p.fs[1], c, p.C, n, dst);
-        copy_rows<T, N>(static_cast<const T *>(p.x) + b * p.xs[0] + t0 * p.xs[1], p.xs[1], c, p.C, n, dst + kPlane);
+        copy_rows<T, N>(static_cast<const T *>(p.f) + b * p.fs[0] + t0 * p.fs[1], p.fs[1], c, p.C, n, p.pairs, dst);
+        copy_rows<T, N>(static_cast<const T *>(p.x) + b * p.xs[0] + t0 * p.xs[1], p.xs[1], c, p.C, n, p.pairs, dst + kPlane);
     };
     int t0 = rank * kRecurChunk + warp * kS;
     if (!TMA) {
@@ -522,7 +536,7 @@ __global__ void __launch_bounds__(32 * kW, 2)
             for (int s = 0; s < kS; ++s) {
                 if (RESET && (cuts >> s & 1u)) h = splat<N>(0.f);
                 h = fma(a[s], h, u[s]);
-                if (s < n) put_part<N, false>(hp + (size_t)s * p.C, c, p.C, h);
+                if (s < n) put_tokens<N>(hp + (size_t)s * p.C, c, p.C, p.pairs, h);
             }
         }
     }
@@ -586,10 +600,10 @@ __global__ void __launch_bounds__(32 * kW, 2)
         const long long t0 = (long long)(last - round * P) * kRecurChunk + warp * kS;
         const int n = (int)min(max(p.T - t0, 0LL), (long long)kS);
         unsigned char *dst = stages + (round % kBwdStages) * 3 * kPlane + warp * kS * kRowBytes + lane * 4;
-        copy_rows<T, N>(static_cast<const T *>(p.f) + b * p.fs[0] + t0 * p.fs[1], p.fs[1], c, p.C, n, dst);
-        copy_rows<T, N>(static_cast<const T *>(p.x) + b * p.xs[0] + t0 * p.xs[1], p.xs[1], c, p.C, n, dst + kPlane);
+        copy_rows<T, N>(static_cast<const T *>(p.f) + b * p.fs[0] + t0 * p.fs[1], p.fs[1], c, p.C, n, p.pairs, dst);
+        copy_rows<T, N>(static_cast<const T *>(p.x) + b * p.xs[0] + t0 * p.xs[1], p.xs[1], c, p.C, n, p.pairs, dst + kPlane);
         if (p.dh)
-            copy_rows<T, N>(static_cast<const T *>(p.dh) + b * p.ds[0] + t0 * p.ds[1], p.ds[1], c, p.C, n, dst + 2 * kPlane);
+            copy_rows<T, N>(static_cast<const T *>(p.dh) + b * p.ds[0] + t0 * p.ds[1], p.ds[1], c, p.C, n, p.pairs, dst + 2 * kPlane);
     };
     if (!TMA) {
         copy(0);
@@ -698,8 +712,8 @@ __global__ void __launch_bounds__(32 * kW, 2)
                 put(reinterpret_cast<T *>(mine + kPlane + s * kRowBytes), gx);
                 put(reinterpret_cast<T *>(mine + 2 * kPlane + s * kRowBytes), gf);
             } else if (s < n) {
-                put_part<N, false>(dx + (size_t)s * p.C, c, p.C, gx);
-                put_part<N, false>(df + (size_t)s * p.C, c, p.C, gf);
+                put_tokens<N>(dx + (size_t)s * p.C, c, p.C, p.pairs, gx);
+                put_tokens<N>(df + (size_t)s * p.C, c, p.C, p.pairs, gf);
             }
             if (RESET && (cuts >> s & 1u)) r = splat<N>(0.f);
         }
@@ -882,14 +896,25 @@ bool make_maps(const RecurArgs &a, bool bwd, CUtensorMap *maps)
     return true;
 }
 
+bool pairs_aligned(const RecurArgs &a)
+{
+    long long m = a.C;
+    for (int i = 0; i < 2; ++i) m |= a.xs[i] | a.fs[i] | a.ds[i];
+    uintptr_t q = 0;
+    for (const void *v : {a.x, a.f, a.dh, (const void *)a.h, (const void *)a.dx, (const void *)a.df})
+        q |= reinterpret_cast<uintptr_t>(v);
+    return m % 2 == 0 && q % 4 == 0;
+}
+
 template <typename T, int MODE> int run(const RecurArgs &a, bool bwd)
 {
-    const RecurParams p = params_of(a);
+    RecurParams p = params_of(a);
     if (a.T > kS) {
         CUtensorMap maps[5] = {};
         if (make_maps(a, bwd, maps))
             return a.reset ? run_tiles<T, MODE, true, true>(p, maps, bwd, a.stream)
                            : run_tiles<T, MODE, false, true>(p, maps, bwd, a.stream);
+        p.pairs = pairs_aligned(a);
         return a.reset ? run_tiles<T, MODE, true, false>(p, maps, bwd, a.stream)
                        : run_tiles<T, MODE, false, false>(p, maps, bwd, a.stream);
     }
