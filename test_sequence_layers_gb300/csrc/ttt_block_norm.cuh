@@ -27,6 +27,9 @@
 
 namespace ttt {
 
+#ifndef HOLDX
+#define HOLDX 1
+#endif
 constexpr int kNormChunk = 8;  // features of a chunk
 
 // row / T for rows below 2^31: multiply by ceil(2^(32 + shift) / T), keep the high part
@@ -527,7 +530,9 @@ __device__ __forceinline__ float2 row_stats(Group<BLOCK> &g, int kind, float eps
 
 // ----------------------------------------------------------------------- forward
 
-// POST, PRE, ACT: 0 and 1 known, -1 by the parameters.
+// POST, PRE: the norm's kind (0 none, 1 RMS, 2 layer), ACT: whether there is a gate; -1: by
+// the parameters.  Parameter vectors in registers where a thread has one chunk: at 768
+// features the loads of three to five of them a row were a third of what kept L1 85% busy.
 template <typename T, int G, int K, bool BLOCK, int POST, int PRE, int ACT>
 __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(const __grid_constant__ NormFwdParams p)
 {
@@ -540,7 +545,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(c
     const int lanes = p.lanes, tid = threadIdx.x, r = BLOCK ? tid : tid & (lanes - 1), pitch = blockDim.x;
     const uint32_t per = BLOCK ? 1 : blockDim.x / lanes, mine = BLOCK ? 0 : tid / lanes;
     Group<BLOCK> grp = make_group<BLOCK>(red, lanes);
-    const bool post = POST < 0 ? p.post != 0 : POST != 0, pre = PRE < 0 ? p.pre != 0 : PRE != 0;
+    const int post = POST < 0 ? p.post : POST, pre = PRE < 0 ? p.pre : PRE;
     const bool act = ACT < 0 ? p.act != 0 : ACT != 0, has_x = p.x != nullptr;
     // a warp's groups leave the loop together: rows past the end are computed, not written
     const uint32_t warp_first = BLOCK ? 0 : (tid & ~31) / lanes;
@@ -550,6 +555,23 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(c
     long long hoff[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) hoff[k] = VEC ? C(r, k, lanes, p.D).head(C(r, k, lanes, p.D).at, p.dh, p.ys[1]) : 0;
+    // the parameter vectors, held or loaded for every row
+    constexpr bool HOLD = VEC && K == 1 && HOLDX;
+    V8 par[5][HOLD ? K : 1];
+    if constexpr (HOLD)
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const C c(r, k, lanes, p.D);
+            par[0][k] = c.vec(p.v.w1);
+            par[1][k] = c.vec(p.v.b1);
+            par[2][k] = c.vec(p.v.sc);
+            par[3][k] = c.vec(p.v.w2);
+            par[4][k] = c.vec(p.v.b2);
+        }
+    auto normed = [&](int kind, const V8 &a, float2 s, const V8 &w, const V8 &b, const C &c, const float *wp, const float *bp) {
+        if (kind == 2) return fma(centre(a, s.x, s.y), HOLD ? w : c.vec(wp), HOLD ? b : c.vec(bp));
+        return mul(mul(a, s.y), HOLD ? w : c.vec(wp));
+    };
     Raw<T, G> regs[3][K];
     auto slot = [&](int stage, int tensor, int k) { return stages + ((stage * 3 + tensor) * K + k) * C::kUnits * pitch + tid; };
     auto fetch = [&](uint32_t base, int stage) {
@@ -598,13 +620,13 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(c
 #pragma unroll
         for (int k = 0; k < K; ++k) v[k] = take(0, k, C(r, k, lanes, p.D));
         float2 s1 = make_float2(0.f, 1.f), s2 = make_float2(0.f, 1.f);
-        if (post) s1 = row_stats<T, G, K, BLOCK>(grp, p.post, p.eps1, inv, v, r, p.D);
+        if (post) s1 = row_stats<T, G, K, BLOCK>(grp, post, p.eps1, inv, v, r, p.D);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const C c(r, k, lanes, p.D);
-            if (post) v[k] = fma(centre(v[k], s1.x, s1.y), c.vec(p.v.w1), c.vec(p.v.b1));
+            if (post) v[k] = normed(post, v[k], s1, par[0][HOLD ? k : 0], par[1][HOLD ? k : 0], c, p.v.w1, p.v.b1);
             if (act) v[k] = mul(v[k], act_value<T>(p.act, take(1, k, c)));
-            v[k] = mul(v[k], c.vec(p.v.sc));
+            v[k] = mul(v[k], HOLD ? par[2][HOLD ? k : 0] : c.vec(p.v.sc));
             if (has_x) v[k] = fma(take(2, k, c), p.alpha, v[k]);
             if (live) c.store(static_cast<T *>(p.h) + off, v[k]);
             c.mask(v[k]);
@@ -612,11 +634,11 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(c
         fetch(base + kAhead * stride, stage);
         if (pre) {
             // of h in fp32, before the rounding that stores it
-            s2 = row_stats<T, G, K, BLOCK>(grp, p.pre, p.eps2, inv, v, r, p.D);
+            s2 = row_stats<T, G, K, BLOCK>(grp, pre, p.eps2, inv, v, r, p.D);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 const C c(r, k, lanes, p.D);
-                v[k] = fma(centre(v[k], s2.x, s2.y), c.vec(p.v.w2), c.vec(p.v.b2));
+                v[k] = normed(pre, v[k], s2, par[3][HOLD ? k : 0], par[4][HOLD ? k : 0], c, p.v.w2, p.v.b2);
                 if (live) c.store(static_cast<T *>(p.u) + off, v[k]);
             }
         }
@@ -646,7 +668,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : (G == kC && K == 1 ? 5
     float2 *accs = reinterpret_cast<float2 *>(stages + (FEED == kStaged ? kAhead * kStage * threads : 0));
     const uint32_t per = BLOCK ? 1 : threads / lanes, mine = BLOCK ? 0 : tid / lanes;
     Group<BLOCK> grp = make_group<BLOCK>(red, lanes);
-    const bool post = POST < 0 ? p.post != 0 : POST != 0, pre = PRE < 0 ? p.pre != 0 : PRE != 0;
+    const int post = POST < 0 ? p.post : POST, pre = PRE < 0 ? p.pre : PRE;
     const bool act = ACT < 0 ? p.act != 0 : ACT != 0;
     const bool has_x = pre && p.x, has_dh = p.dh_in != nullptr;
     const uint32_t warp_first = BLOCK ? 0 : (tid & ~31) / lanes;
@@ -762,36 +784,39 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : (G == kC && K == 1 ? 5
             }
         };
         V8 yn[K], A[K], dA[K], hn[K], gr[K];
+        auto weighted = [&](int k, const C &c) {
+            return post == 2 ? fma(yn[k], c.vec(p.v.w1), c.vec(p.v.b1)) : mul(yn[k], c.vec(p.v.w1));
+        };
         float a = 0.f, c2 = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const C c(r, k, lanes, p.D);
             yn[k] = take(0, k, c);
-            if (post) yn[k] = centre(yn[k], st.x, st.y);
+            if (post) yn[k] = post == 2 ? centre(yn[k], st.x, st.y) : mul(yn[k], st.y);
             c.mask(yn[k]);
             if (act) act_and_slope<T>(p.act, take(1, k, c), A[k], dA[k]);
             if (pre) {
                 // h again from the inputs, its normalised form, and the norm's backward sums
-                V8 h = post ? fma(yn[k], c.vec(p.v.w1), c.vec(p.v.b1)) : yn[k];
+                V8 h = post ? weighted(k, c) : yn[k];
                 if (act) h = mul(h, A[k]);
                 h = mul(h, c.vec(p.v.sc));
                 if (has_x) h = fma(take(2, k, c), p.alpha, h);
-                hn[k] = centre(h, st.z, st.w);
+                hn[k] = pre == 2 ? centre(h, st.z, st.w) : mul(h, st.w);
                 c.mask(hn[k]);
                 gr[k] = take(3, k, c);
                 if (live) {
                     add_to(3, k, gr[k], hn[k]);
-                    add_to(4, k, gr[k], one);
+                    if (pre == 2) add_to(4, k, gr[k], one);
                 }
                 gr[k] = mul(gr[k], c.vec(p.v.w2));
-                a += c.counted(total(gr[k]));
+                if (pre == 2) a += c.counted(total(gr[k]));
                 c2 += c.counted(dot(gr[k], hn[k]));
             }
         }
         float ma = 0.f, mc = 0.f;
         if (pre) {
-            const float2 m = grp.sum2(a, c2);
-            ma = p.pre == 2 ? m.x * inv : 0.f;
+            const float2 m = pre == 2 ? grp.sum2(a, c2) : make_float2(0.f, grp.sum1(c2));
+            ma = m.x * inv;
             mc = m.y * inv;
         }
         a = c2 = 0.f;
@@ -799,10 +824,10 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : (G == kC && K == 1 ? 5
         for (int k = 0; k < K; ++k) {
             const C c(r, k, lanes, p.D);
             // gr = dh + r (dn - mean(dn) - n mean(dn n)), the gradient of h
-            gr[k] = pre ? centre(fma(hn[k], -mc, gr[k]), ma, st.w) : splat(0.f);
+            gr[k] = pre == 2 ? centre(fma(hn[k], -mc, gr[k]), ma, st.w) : pre ? mul(fma(hn[k], -mc, gr[k]), st.w) : splat(0.f);
             if (has_dh) gr[k] = add(gr[k], take(4, k, c));
             if (p.dx && live) c.store(static_cast<T *>(p.dx) + off, mul(gr[k], p.alpha));
-            const V8 pv = post ? fma(yn[k], c.vec(p.v.w1), c.vec(p.v.b1)) : yn[k];
+            const V8 pv = post ? weighted(k, c) : yn[k];
             if (live) add_to(2, k, act ? mul(gr[k], A[k]) : gr[k], pv);
             gr[k] = mul(gr[k], c.vec(p.v.sc));
             if (act) {
@@ -813,18 +838,18 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : (G == kC && K == 1 ? 5
             if (post) {
                 if (live) {
                     add_to(0, k, gr[k], yn[k]);
-                    add_to(1, k, gr[k], one);
+                    if (post == 2) add_to(1, k, gr[k], one);
                 }
                 gr[k] = mul(gr[k], c.vec(p.v.w1));
                 c.mask(gr[k]);
-                a += c.counted(total(gr[k]));
+                if (post == 2) a += c.counted(total(gr[k]));
                 c2 += c.counted(dot(gr[k], yn[k]));
             }
         }
         fetch(base + kAhead * stride, stage);
         if (post) {
-            const float2 m = grp.sum2(a, c2);
-            ma = p.post == 2 ? m.x * inv : 0.f;
+            const float2 m = post == 2 ? grp.sum2(a, c2) : make_float2(0.f, grp.sum1(c2));
+            ma = m.x * inv;
             mc = m.y * inv;
         }
         // dy is contiguous in y's own layout
@@ -836,7 +861,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : (G == kC && K == 1 ? 5
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const C c(r, k, lanes, p.D);
-            if (post) gr[k] = centre(fma(yn[k], -mc, gr[k]), ma, st.y);
+            if (post) gr[k] = post == 2 ? centre(fma(yn[k], -mc, gr[k]), ma, st.y) : mul(fma(yn[k], -mc, gr[k]), st.y);
             if (live) c.store_heads(dy, p.dh, (long long)p.T * p.dh, dyoff[k], gr[k]);
         }
     }
@@ -950,15 +975,25 @@ int run_bwd_wide(const NormBwdParams &p, const NormShape &s, int limit, cudaStre
 template <typename T> int norm_fwd(const NormFwdParams &p, const NormShape &s, int group, cudaStream_t st)
 {
     if (group < kC) return group == 2 ? run_fwd<T, 2, -1, -1, -1>(p, s, st) : run_fwd<T, 1, -1, -1, -1>(p, s, st);
-    switch ((p.post ? 4 : 0) | (p.pre ? 2 : 0) | (p.act ? 1 : 0)) {
+    switch (p.post * 6 + p.pre * 2 + (p.act ? 1 : 0)) {
     case 0: return run_fwd<T, kC, 0, 0, 0>(p, s, st);
     case 1: return run_fwd<T, kC, 0, 0, 1>(p, s, st);
     case 2: return run_fwd<T, kC, 0, 1, 0>(p, s, st);
     case 3: return run_fwd<T, kC, 0, 1, 1>(p, s, st);
-    case 4: return run_fwd<T, kC, 1, 0, 0>(p, s, st);
-    case 5: return run_fwd<T, kC, 1, 0, 1>(p, s, st);
-    case 6: return run_fwd<T, kC, 1, 1, 0>(p, s, st);
-    default: return run_fwd<T, kC, 1, 1, 1>(p, s, st);
+    case 4: return run_fwd<T, kC, 0, 2, 0>(p, s, st);
+    case 5: return run_fwd<T, kC, 0, 2, 1>(p, s, st);
+    case 6: return run_fwd<T, kC, 1, 0, 0>(p, s, st);
+    case 7: return run_fwd<T, kC, 1, 0, 1>(p, s, st);
+    case 8: return run_fwd<T, kC, 1, 1, 0>(p, s, st);
+    case 9: return run_fwd<T, kC, 1, 1, 1>(p, s, st);
+    case 10: return run_fwd<T, kC, 1, 2, 0>(p, s, st);
+    case 11: return run_fwd<T, kC, 1, 2, 1>(p, s, st);
+    case 12: return run_fwd<T, kC, 2, 0, 0>(p, s, st);
+    case 13: return run_fwd<T, kC, 2, 0, 1>(p, s, st);
+    case 14: return run_fwd<T, kC, 2, 1, 0>(p, s, st);
+    case 15: return run_fwd<T, kC, 2, 1, 1>(p, s, st);
+    case 16: return run_fwd<T, kC, 2, 2, 0>(p, s, st);
+    default: return run_fwd<T, kC, 2, 2, 1>(p, s, st);
     }
 }
 
@@ -971,15 +1006,25 @@ int norm_bwd(const NormBwdParams &p, const NormShape &s, int group, int limit, c
                             : run_bwd_wide<T, 1>(p, s, limit, st, blocks);
     if (group < kC)
         return group == 2 ? run_bwd<T, 2, -1, -1, -1>(p, s, limit, st, blocks) : run_bwd<T, 1, -1, -1, -1>(p, s, limit, st, blocks);
-    switch ((p.post ? 4 : 0) | (p.pre ? 2 : 0) | (p.act ? 1 : 0)) {
+    switch (p.post * 6 + p.pre * 2 + (p.act ? 1 : 0)) {
     case 0: return run_bwd<T, kC, 0, 0, 0>(p, s, limit, st, blocks);
     case 1: return run_bwd<T, kC, 0, 0, 1>(p, s, limit, st, blocks);
     case 2: return run_bwd<T, kC, 0, 1, 0>(p, s, limit, st, blocks);
     case 3: return run_bwd<T, kC, 0, 1, 1>(p, s, limit, st, blocks);
-    case 4: return run_bwd<T, kC, 1, 0, 0>(p, s, limit, st, blocks);
-    case 5: return run_bwd<T, kC, 1, 0, 1>(p, s, limit, st, blocks);
-    case 6: return run_bwd<T, kC, 1, 1, 0>(p, s, limit, st, blocks);
-    default: return run_bwd<T, kC, 1, 1, 1>(p, s, limit, st, blocks);
+    case 4: return run_bwd<T, kC, 0, 2, 0>(p, s, limit, st, blocks);
+    case 5: return run_bwd<T, kC, 0, 2, 1>(p, s, limit, st, blocks);
+    case 6: return run_bwd<T, kC, 1, 0, 0>(p, s, limit, st, blocks);
+    case 7: return run_bwd<T, kC, 1, 0, 1>(p, s, limit, st, blocks);
+    case 8: return run_bwd<T, kC, 1, 1, 0>(p, s, limit, st, blocks);
+    case 9: return run_bwd<T, kC, 1, 1, 1>(p, s, limit, st, blocks);
+    case 10: return run_bwd<T, kC, 1, 2, 0>(p, s, limit, st, blocks);
+    case 11: return run_bwd<T, kC, 1, 2, 1>(p, s, limit, st, blocks);
+    case 12: return run_bwd<T, kC, 2, 0, 0>(p, s, limit, st, blocks);
+    case 13: return run_bwd<T, kC, 2, 0, 1>(p, s, limit, st, blocks);
+    case 14: return run_bwd<T, kC, 2, 1, 0>(p, s, limit, st, blocks);
+    case 15: return run_bwd<T, kC, 2, 1, 1>(p, s, limit, st, blocks);
+    case 16: return run_bwd<T, kC, 2, 2, 0>(p, s, limit, st, blocks);
+    default: return run_bwd<T, kC, 2, 2, 1>(p, s, limit, st, blocks);
     }
 }
 
