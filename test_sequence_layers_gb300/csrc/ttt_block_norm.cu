@@ -124,7 +124,7 @@ bool even(const BlockNormArgs &a, const void *p, long long sb, long long st)
 }  // namespace
 
 // The most blocks of the backward pass, by size alone (the workspace holds their sums): 512
-// threads an SM, which is what the kernels' registers allow; of two chunks each, fewer.
+// threads an SM, no fewer than the kernels' registers allow.
 int block_norm_bwd_blocks(int D, long long rows)
 {
     const NormShape s = bwd_shape(D, false);

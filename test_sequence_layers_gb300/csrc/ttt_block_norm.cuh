@@ -27,9 +27,6 @@
 
 namespace ttt {
 
-#ifndef HOLDX
-#define HOLDX 1
-#endif
 constexpr int kNormChunk = 8;  // features of a chunk
 
 // row / T for rows below 2^31: multiply by ceil(2^(32 + shift) / T), keep the high part
@@ -531,8 +528,9 @@ __device__ __forceinline__ float2 row_stats(Group<BLOCK> &g, int kind, float eps
 // ----------------------------------------------------------------------- forward
 
 // POST, PRE: the norm's kind (0 none, 1 RMS, 2 layer), ACT: whether there is a gate; -1: by
-// the parameters.  Parameter vectors in registers where a thread has one chunk: at 768
-// features the loads of three to five of them a row were a third of what kept L1 85% busy.
+// the parameters.  With 16-byte rows the parameter vectors stay in registers: loading
+// three to five of them for every row kept L1 85% busy (2 x 32768 x 2048 257 us against
+// 225, 8 x 2048 x 768 sandwich 25.3 against 23.2).
 template <typename T, int G, int K, bool BLOCK, int POST, int PRE, int ACT>
 __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(const __grid_constant__ NormFwdParams p)
 {
@@ -556,7 +554,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(c
 #pragma unroll
     for (int k = 0; k < K; ++k) hoff[k] = VEC ? C(r, k, lanes, p.D).head(C(r, k, lanes, p.D).at, p.dh, p.ys[1]) : 0;
     // the parameter vectors, held or loaded for every row
-    constexpr bool HOLD = VEC && K == 1 && HOLDX;
+    constexpr bool HOLD = VEC;
     V8 par[5][HOLD ? K : 1];
     if constexpr (HOLD)
 #pragma unroll
@@ -654,7 +652,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(c
 // partial sums, a second kernel adds those in order.  The result depends on the sizes and
 // the SM count only.
 template <typename T, int G, int K, bool BLOCK, int MAXT, int POST, int PRE, int ACT>
-__global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : (G == kC && K == 1 ? 512 : 256) / MAXT) ttt_block_norm_bwd_kernel(const __grid_constant__ NormBwdParams p)
+__global__ void __launch_bounds__(MAXT, MAXT >= 256 ? 1 : 256 / MAXT) ttt_block_norm_bwd_kernel(const __grid_constant__ NormBwdParams p)
 {
     constexpr bool WIDE = K > 1 && MAXT > 256;  // sums in shared memory
     using C = Chunk<T, G>;
@@ -703,6 +701,20 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : (G == kC && K == 1 ? 5
         dyoff[k] = VEC ? c.head(c.at, p.dh, (long long)p.T * p.dh) : 0;
     }
     const uint32_t stride = gridDim.x * per;
+    // the parameter vectors: held (8 x 2048 x 768 47 us against 51), or loaded when they are
+    // used where two chunks' sums leave no registers
+    constexpr bool HOLD = VEC && K == 1;
+    V8 par[4] = {};
+    if constexpr (HOLD) {
+        const C c(r, 0, lanes, p.D);
+        par[0] = c.vec(p.v.w1);
+        par[1] = c.vec(p.v.b1);
+        par[2] = c.vec(p.v.sc);
+        par[3] = c.vec(p.v.w2);
+    }
+    auto w1 = [&](int, const C &c) { return HOLD ? par[0] : c.vec(p.v.w1); };
+    auto sc = [&](int, const C &c) { return HOLD ? par[2] : c.vec(p.v.sc); };
+    auto w2 = [&](int, const C &c) { return HOLD ? par[3] : c.vec(p.v.w2); };
     Raw<T, G> regs[5][FEED == kRegisters ? K : 1];
     float4 next_st = make_float4(0.f, 1.f, 0.f, 1.f);
     const T *rows[5];  // kDirect: the row's addresses
@@ -785,7 +797,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : (G == kC && K == 1 ? 5
         };
         V8 yn[K], A[K], dA[K], hn[K], gr[K];
         auto weighted = [&](int k, const C &c) {
-            return post == 2 ? fma(yn[k], c.vec(p.v.w1), c.vec(p.v.b1)) : mul(yn[k], c.vec(p.v.w1));
+            return post == 2 ? fma(yn[k], w1(k, c), HOLD ? par[1] : c.vec(p.v.b1)) : mul(yn[k], w1(k, c));
         };
         float a = 0.f, c2 = 0.f;
 #pragma unroll
@@ -799,7 +811,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : (G == kC && K == 1 ? 5
                 // h again from the inputs, its normalised form, and the norm's backward sums
                 V8 h = post ? weighted(k, c) : yn[k];
                 if (act) h = mul(h, A[k]);
-                h = mul(h, c.vec(p.v.sc));
+                h = mul(h, sc(k, c));
                 if (has_x) h = fma(take(2, k, c), p.alpha, h);
                 hn[k] = pre == 2 ? centre(h, st.z, st.w) : mul(h, st.w);
                 c.mask(hn[k]);
@@ -808,7 +820,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : (G == kC && K == 1 ? 5
                     add_to(3, k, gr[k], hn[k]);
                     if (pre == 2) add_to(4, k, gr[k], one);
                 }
-                gr[k] = mul(gr[k], c.vec(p.v.w2));
+                gr[k] = mul(gr[k], w2(k, c));
                 if (pre == 2) a += c.counted(total(gr[k]));
                 c2 += c.counted(dot(gr[k], hn[k]));
             }
@@ -829,7 +841,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : (G == kC && K == 1 ? 5
             if (p.dx && live) c.store(static_cast<T *>(p.dx) + off, mul(gr[k], p.alpha));
             const V8 pv = post ? weighted(k, c) : yn[k];
             if (live) add_to(2, k, act ? mul(gr[k], A[k]) : gr[k], pv);
-            gr[k] = mul(gr[k], c.vec(p.v.sc));
+            gr[k] = mul(gr[k], sc(k, c));
             if (act) {
                 if (live) c.store(static_cast<T *>(p.dg) + off, mul(mul(gr[k], pv), dA[k]));
                 gr[k] = mul(gr[k], A[k]);
@@ -840,7 +852,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : (G == kC && K == 1 ? 5
                     add_to(0, k, gr[k], yn[k]);
                     if (post == 2) add_to(1, k, gr[k], one);
                 }
-                gr[k] = mul(gr[k], c.vec(p.v.w1));
+                gr[k] = mul(gr[k], w1(k, c));
                 c.mask(gr[k]);
                 if (post == 2) a += c.counted(total(gr[k]));
                 c2 += c.counted(dot(gr[k], yn[k]));
@@ -959,8 +971,8 @@ int run_bwd(const NormBwdParams &p, const NormShape &s, int limit, cudaStream_t 
         if (s.K == 2)
             return launch(ttt_block_norm_bwd_kernel<T, G, 2, true, 256, POST, PRE, ACT>, p, s, limit, smem, st, blocks);
     if (!s.block) return launch(ttt_block_norm_bwd_kernel<T, G, 1, false, 128, POST, PRE, ACT>, p, s, limit, smem, st, blocks);
-    return s.threads <= 256
-               ? launch(ttt_block_norm_bwd_kernel<T, G, 1, true, 256, POST, PRE, ACT>, p, s, limit, smem, st, blocks)
+    return s.threads <= 384
+               ? launch(ttt_block_norm_bwd_kernel<T, G, 1, true, 384, POST, PRE, ACT>, p, s, limit, smem, st, blocks)
                : launch(ttt_block_norm_bwd_kernel<T, G, 1, true, 512, POST, PRE, ACT>, p, s, limit, smem, st, blocks);
 }
 
