@@ -452,6 +452,14 @@ def _fn(name):
     return f
 
 
+def _norm_workspace(desc):
+    f = _fns.get("workspace")
+    if f is None:
+        f = _fns["workspace"] = lib()["ttt_block_norm_bwd_workspace"]
+        f.argtypes, f.restype = [ctypes.c_void_p], ctypes.c_size_t
+    return f(desc)
+
+
 def _tokens(name, t, dims, like=None):
     """Why a token tensor is refused: CUDA, bf16 or fp32, `dims` dimensions, the last one
     contiguous; `like`: shares its dtype and device."""
@@ -670,10 +678,9 @@ def ttt_block_norm_bwd(dh, du, y, stats, x=None, gate=None, act=None, post="none
     dy = _empty(y.shape, dtype=dt, device=dev)
     dx = None if x is None else _empty(shape, dtype=dt, device=dev)
     dg = None if gate is None else _empty(shape, dtype=dt, device=dev)
-    gv = [None if t is None else _empty(D, dtype=torch.float32, device=dev)
-          for t in (post_weight, post_bias, scale, pre_weight, pre_bias)]
+    gv = [None if t is None else _empty(D, dtype=torch.float32, device=dev) for t in par]
     if workspace is None:
-        workspace = _empty(ttt_block_norm_bwd_workspace(B, T, D), dtype=torch.uint8, device=dev)
+        workspace = _empty(_norm_workspace(desc), dtype=torch.uint8, device=dev)
     elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on y's device")
     _call("ttt_block_norm_bwd", dev, stream, desc, _vectors(par), _addr(dh), _addr(du), y.data_ptr(), _addr(x),
@@ -684,8 +691,7 @@ def ttt_block_norm_bwd(dh, du, y, stats, x=None, gate=None, act=None, post="none
 
 def ttt_block_norm_bwd_workspace(B, T, D) -> int:
     """Workspace bytes of ttt_block_norm_bwd for B x T tokens of D features."""
-    desc = BlockNormDesc(B, T, D, 1, TTT_BF16, 0, 0, 0, 1e-6, 1e-6, 1.0)
-    return int(lib().ttt_block_norm_bwd_workspace(desc))
+    return _norm_workspace(_NORM_DESC.pack(B, T, D, 1, TTT_BF16, 0, 0, 0, 1e-6, 1e-6, 1.0, *[0] * 11))
 
 
 def _recurrence_prologue(x, f, mode, reset, dh=None):
