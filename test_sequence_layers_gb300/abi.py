@@ -429,13 +429,15 @@ def ttt_eta_gate(x, theta, eta_base=1.0, eta=None, stream=None):
 #
 # A decoding step calls these on a few hundred KB, where the host's time is the whole
 # cost: descriptors are packed bytes, the current stream and device are read without their
-# Python wrappers, and each check is one expression that only asks why when it fails.
+# Python wrappers, each check is one expression that only asks why when it fails, and
+# devices are compared by their numbers.
 
 _IO = {torch.bfloat16: TTT_BF16, torch.float32: TTT_F32}
 _ROPE_DESC, _NORM_DESC, _NORM_PAR = struct.Struct("@11i20q"), struct.Struct("@8i3f11q"), struct.Struct("@5Q")
 _RECUR_DESC = struct.Struct("@5i6q")
 _NO_STRIDE2, _NO_STRIDE3 = (0, 0), (0, 0, 0)
-_empty = torch.empty
+_empty, _F32, _I64 = torch.empty, torch.float32, torch.int64
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 _fns: dict = {}
 
 
@@ -475,37 +477,36 @@ def _tokens(name, t, dims, like=None):
         raise ValueError(f"{name} must share the dtype and device of the first tensor")
 
 
-def _rows(name, t, like, shape, dt, dev):
+def _rows(name, t, like, shape, dt, di):
     """Strides (all but the last) of a token tensor of this shape, dtype and device."""
     st = t.stride()
-    if t.dtype != dt or t.device != dev or t.shape != shape or st[-1] != 1:
+    if t.dtype is not dt or t.get_device() != di or t.shape != shape or st[-1] != 1:
         _tokens(name, t, len(shape), like)
         if t.shape != shape:
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return st[:-1]
 
 
-def _like(name, t, shape, dtype, dev):
+def _like(name, t, shape, dtype, di):
     """A contiguous tensor of the given shape, dtype and device."""
-    if t.dtype != dtype or t.device != dev or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
+    if t.dtype is not dtype or t.get_device() != di or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{di}")
     return t
 
 
-def _call(name, dev, stream, *args):
-    """Runs one library entry point on dev's current stream (or `stream`)."""
-    i = dev.index
+def _call(name, di, stream, *args):
+    """Runs one library entry point on device di's current stream (or `stream`)."""
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(i)
-    elif stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device} but the tensors on {dev}")
+        raw = _raw_stream(di)
+    elif stream.device.index != di:
+        raise ValueError(f"the stream is on {stream.device} but the tensors on cuda:{di}")
     else:
         raw = stream.cuda_stream
     f = _fns.get(name) or _fn(name)
-    if torch._C._cuda_getDevice() == i:
+    if _current_device() == di:
         rc = f(*args, raw)
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(di):
             rc = f(*args, raw)
     if rc != 0:
         raise TTTError(name, rc)
@@ -525,7 +526,7 @@ def ttt_rope(q, k, v, table, positions=None, pos0=0, period=0, interleaved=False
     [B,H,T,d] unless q_out, k_out, v_out are given (any strides; an output may be its
     own input).  Returns (q_out, k_out, v_out).  A position outside the table gives NaN
     and TTT_ERR_RANGE from ttt_sync_status."""
-    dt, dev, sq = q.dtype, q.device, q.stride()
+    dt, dev, di, sq = q.dtype, q.device, q.get_device(), q.stride()
     io = _IO.get(dt)
     if io is None or not q.is_cuda or len(sq) != 4 or sq[3] != 1:
         _tokens("q", q, 4)
@@ -533,18 +534,18 @@ def ttt_rope(q, k, v, table, positions=None, pos0=0, period=0, interleaved=False
     hk, sk, sv = 0, _NO_STRIDE3, _NO_STRIDE3
     if k is not None:
         hk = k.shape[1]
-        sk = _rows("k", k, q, shape if hk == H else (B, hk, T, d), dt, dev)
+        sk = _rows("k", k, q, shape if hk == H else (B, hk, T, d), dt, di)
     if v is not None:
         if k is None:
             hk = v.shape[1]
-        sv = _rows("v", v, q, shape if hk == H else (B, hk, T, d), dt, dev)
+        sv = _rows("v", v, q, shape if hk == H else (B, hk, T, d), dt, di)
     tshape = table.shape
-    if (table.dtype != torch.float32 or table.device != dev or len(tshape) != 3 or tshape[2] != 2
+    if (table.dtype is not _F32 or table.get_device() != di or len(tshape) != 3 or tshape[2] != 2
             or not table.is_contiguous()):
         raise ValueError("table must be a contiguous float32 [rows, rot/2, 2] tensor on q's device")
     pbs = 0
     if positions is not None:
-        if positions.dtype != torch.int64 or positions.device != dev or not positions.is_contiguous():
+        if positions.dtype is not _I64 or positions.get_device() != di or not positions.is_contiguous():
             raise ValueError("positions must be a contiguous int64 tensor on q's device")
         if positions.shape == (B, T):
             pbs = T
@@ -554,7 +555,7 @@ def ttt_rope(q, k, v, table, positions=None, pos0=0, period=0, interleaved=False
     if q_out is None:
         q_out, so = _empty(shape, dtype=dt, device=dev), (H * Td, Td, d)
     else:
-        so = _rows("q_out", q_out, q, shape, dt, dev)
+        so = _rows("q_out", q_out, q, shape, dt, di)
     sko = svo = _NO_STRIDE3
     if k is None:
         if k_out is not None:
@@ -562,33 +563,33 @@ def ttt_rope(q, k, v, table, positions=None, pos0=0, period=0, interleaved=False
     elif k_out is None:
         k_out, sko = _empty(k.shape, dtype=dt, device=dev), (hk * Td, Td, d)
     else:
-        sko = _rows("k_out", k_out, q, k.shape, dt, dev)
+        sko = _rows("k_out", k_out, q, k.shape, dt, di)
     if v is None:
         if v_out is not None:
             raise ValueError("v_out given without its input")
     elif v_out is None:
         v_out, svo = _empty(v.shape, dtype=dt, device=dev), (hk * Td, Td, d)
     else:
-        svo = _rows("v_out", v_out, q, v.shape, dt, dev)
+        svo = _rows("v_out", v_out, q, v.shape, dt, di)
     desc = _ROPE_DESC.pack(B, T, H, hk, d, 2 * tshape[1], interleaved, inverse, io, tshape[0], period, pos0, pbs,
                            *sq[:3], *sk, *sv, *so, *sko, *svo)
-    _call("ttt_rope", dev, stream, desc, q.data_ptr(), _addr(k), _addr(v), table.data_ptr(), _addr(positions),
-          q_out.data_ptr(), _addr(k_out), _addr(v_out))
+    _call("ttt_rope", di, stream, desc, q.data_ptr(), 0 if k is None else k.data_ptr(), 0 if v is None else v.data_ptr(),
+          table.data_ptr(), 0 if positions is None else positions.data_ptr(), q_out.data_ptr(),
+          0 if k is None else k_out.data_ptr(), 0 if v is None else v_out.data_ptr())
     return q_out, k_out, v_out
 
 
-def _vec(name, t, D, dev):
-    """A parameter vector, or None."""
-    if t is None:
-        return None
-    if t.dtype != torch.float32 or t.device != dev or t.shape != (D,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float32 [{D}] tensor on {dev}")
-    return t
+def _vec(name, t, vshape, di):
+    """The address of a parameter vector."""
+    if t.dtype is not _F32 or t.get_device() != di or t.shape != vshape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 [{vshape[0]}] tensor on cuda:{di}")
+    return t.data_ptr()
 
 
 def _norm_prologue(y, x, gate, act, post, pre, post_eps, pre_eps, alpha, w1, b1, scale, w2, b2, dh=None, du=None):
-    """Checks of both block-norm wrappers; returns (token shape, descriptor, parameters)."""
-    dt, dev, sy = y.dtype, y.device, y.stride()
+    """Checks of both block-norm wrappers; returns (token shape, dtype, device and its
+    number, descriptor, parameters)."""
+    dt, di, sy = y.dtype, y.get_device(), y.stride()
     io = _IO.get(dt)
     if io is None or not y.is_cuda or len(sy) not in (3, 4) or sy[-1] != 1:
         _tokens("y", y, 4 if len(sy) == 4 else 3)
@@ -600,24 +601,19 @@ def _norm_prologue(y, x, gate, act, post, pre, post_eps, pre_eps, alpha, w1, b1,
         heads, sy = 1, (sy[0], 0, sy[1])
     if (gate is None) != (act == "none"):
         raise ValueError('a gate goes with an act other than "none"')
-    shape = (B, T, D)
-    sx = _NO_STRIDE2 if x is None else _rows("x", x, y, shape, dt, dev)
-    sg = _NO_STRIDE2 if gate is None else _rows("gate", gate, y, shape, dt, dev)
-    sdh = _NO_STRIDE2 if dh is None else _rows("dh", dh, y, shape, dt, dev)
-    sdu = _NO_STRIDE2 if du is None else _rows("du", du, y, shape, dt, dev)
-    par = (_vec("post_weight", w1, D, dev), _vec("post_bias", b1, D, dev), _vec("scale", scale, D, dev),
-           _vec("pre_weight", w2, D, dev), _vec("pre_bias", b2, D, dev))
+    shape, vec = (B, T, D), (D,)
+    sx = _NO_STRIDE2 if x is None else _rows("x", x, y, shape, dt, di)
+    sg = _NO_STRIDE2 if gate is None else _rows("gate", gate, y, shape, dt, di)
+    sdh = _NO_STRIDE2 if dh is None else _rows("dh", dh, y, shape, dt, di)
+    sdu = _NO_STRIDE2 if du is None else _rows("du", du, y, shape, dt, di)
+    par = _NORM_PAR.pack(0 if w1 is None else _vec("post_weight", w1, vec, di),
+                         0 if b1 is None else _vec("post_bias", b1, vec, di),
+                         0 if scale is None else _vec("scale", scale, vec, di),
+                         0 if w2 is None else _vec("pre_weight", w2, vec, di),
+                         0 if b2 is None else _vec("pre_bias", b2, vec, di))
     desc = _NORM_DESC.pack(B, T, D, heads, io, NORMS[post], NORMS[pre], GATES[act], post_eps, pre_eps, alpha, *sy, *sx,
                            *sg, *sdh, *sdu)
-    return shape, desc, par
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _vectors(par):
-    return _NORM_PAR.pack(*[0 if t is None else t.data_ptr() for t in par])
+    return shape, dt, y.device, di, desc, par
 
 
 def ttt_block_norm_fwd(y, x=None, gate=None, act=None, post="none", post_weight=None, post_bias=None, scale=None,
@@ -632,20 +628,20 @@ def ttt_block_norm_fwd(y, x=None, gate=None, act=None, post="none", post_weight=
     pass.  h may be x.  Returns (h, u or None, stats or None)."""
     if act is None:
         act = "none" if gate is None else "silu"
-    shape, desc, par = _norm_prologue(y, x, gate, act, post, pre, post_eps, pre_eps, alpha, post_weight, post_bias, scale,
-                                      pre_weight, pre_bias)
-    dev, dt = y.device, y.dtype
+    shape, dt, dev, di, desc, par = _norm_prologue(y, x, gate, act, post, pre, post_eps, pre_eps, alpha, post_weight,
+                                                   post_bias, scale, pre_weight, pre_bias)
     if pre != "none":
-        u = _empty(shape, dtype=dt, device=dev) if u is None else _like("u", u, shape, dt, dev)
+        u = _empty(shape, dtype=dt, device=dev) if u is None else _like("u", u, shape, dt, di)
     elif u is not None:
         raise ValueError("u is written with a pre norm only")
     if stats is not None:
-        _like("stats", stats, (shape[0], shape[1], 4), torch.float32, dev)
+        _like("stats", stats, (shape[0], shape[1], 4), _F32, di)
     elif want_stats:
-        stats = _empty((shape[0], shape[1], 4), dtype=torch.float32, device=dev)
-    h = _empty(shape, dtype=dt, device=dev) if h is None else _like("h", h, shape, dt, dev)
-    _call("ttt_block_norm_fwd", dev, stream, desc, _vectors(par), y.data_ptr(), _addr(x), _addr(gate), h.data_ptr(),
-          _addr(u), _addr(stats))
+        stats = _empty((shape[0], shape[1], 4), dtype=_F32, device=dev)
+    h = _empty(shape, dtype=dt, device=dev) if h is None else _like("h", h, shape, dt, di)
+    _call("ttt_block_norm_fwd", di, stream, desc, par, y.data_ptr(), 0 if x is None else x.data_ptr(),
+          0 if gate is None else gate.data_ptr(), h.data_ptr(), 0 if u is None else u.data_ptr(),
+          0 if stats is None else stats.data_ptr())
     return h, u, stats
 
 
@@ -670,22 +666,24 @@ def ttt_block_norm_bwd(dh, du, y, stats, x=None, gate=None, act=None, post="none
     tensor of ttt_block_norm_bwd_workspace(...) bytes, allocated here when None."""
     if act is None:
         act = "none" if gate is None else "silu"
-    shape, desc, par = _norm_prologue(y, x, gate, act, post, pre, post_eps, pre_eps, alpha, post_weight, post_bias, scale,
-                                      pre_weight, pre_bias, dh, du)
+    shape, dt, dev, di, desc, par = _norm_prologue(y, x, gate, act, post, pre, post_eps, pre_eps, alpha, post_weight,
+                                                   post_bias, scale, pre_weight, pre_bias, dh, du)
     B, T, D = shape
-    dev, dt = y.device, y.dtype
-    _like("stats", stats, (B, T, 4), torch.float32, dev)
+    _like("stats", stats, (B, T, 4), _F32, di)
     dy = _empty(y.shape, dtype=dt, device=dev)
     dx = None if x is None else _empty(shape, dtype=dt, device=dev)
     dg = None if gate is None else _empty(shape, dtype=dt, device=dev)
-    gv = [None if t is None else _empty(D, dtype=torch.float32, device=dev) for t in par]
+    gv = [None if t is None else _empty(D, dtype=_F32, device=dev)
+          for t in (post_weight, post_bias, scale, pre_weight, pre_bias)]
     if workspace is None:
         workspace = _empty(_norm_workspace(desc), dtype=torch.uint8, device=dev)
-    elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+    elif workspace.get_device() != di or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on y's device")
-    _call("ttt_block_norm_bwd", dev, stream, desc, _vectors(par), _addr(dh), _addr(du), y.data_ptr(), _addr(x),
-          _addr(gate), stats.data_ptr(), dy.data_ptr(), _addr(dx), _addr(dg), _vectors(gv), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size())
+    _call("ttt_block_norm_bwd", di, stream, desc, par, 0 if dh is None else dh.data_ptr(),
+          0 if du is None else du.data_ptr(), y.data_ptr(), 0 if x is None else x.data_ptr(),
+          0 if gate is None else gate.data_ptr(), stats.data_ptr(), dy.data_ptr(), 0 if dx is None else dx.data_ptr(),
+          0 if dg is None else dg.data_ptr(), _NORM_PAR.pack(*[0 if t is None else t.data_ptr() for t in gv]),
+          workspace.data_ptr(), workspace.nbytes)
     return BlockNormGrads(dy, dx, dg, *gv)
 
 
@@ -695,19 +693,20 @@ def ttt_block_norm_bwd_workspace(B, T, D) -> int:
 
 
 def _recurrence_prologue(x, f, mode, reset, dh=None):
-    """Checks of both recurrence wrappers; returns (shape, descriptor)."""
-    dt, dev, sx = x.dtype, x.device, x.stride()
+    """Checks of both recurrence wrappers; returns (shape, dtype, device and its
+    number, descriptor)."""
+    dt, di, sx = x.dtype, x.get_device(), x.stride()
     io = _IO.get(dt)
     if io is None or not x.is_cuda or len(sx) != 3 or sx[2] != 1:
         _tokens("x", x, 3)
     B, T, C = shape = x.shape
-    sf = _rows("f", f, x, shape, dt, dev)
-    sd = _NO_STRIDE2 if dh is None else _rows("dh", dh, x, shape, dt, dev)
+    sf = _rows("f", f, x, shape, dt, di)
+    sd = _NO_STRIDE2 if dh is None else _rows("dh", dh, x, shape, dt, di)
     if reset is not None:
-        if (reset.dtype not in (torch.bool, torch.uint8) or reset.device != dev or reset.shape != (B, T)
+        if (reset.dtype not in (torch.bool, torch.uint8) or reset.get_device() != di or reset.shape != (B, T)
                 or not reset.is_contiguous()):
             raise ValueError("reset must be a contiguous bool or uint8 [B,T] tensor on x's device")
-    return shape, _RECUR_DESC.pack(B, T, C, io, RECURRENCE_MODES[mode], sx[0], sx[1], *sf, *sd)
+    return shape, dt, x.device, di, _RECUR_DESC.pack(B, T, C, io, RECURRENCE_MODES[mode], sx[0], sx[1], *sf, *sd)
 
 
 def ttt_recurrence_fwd(x, f, h0=None, mode="mix", reset=None, h=None, h_last=None, want_states=False, states=None,
@@ -718,36 +717,35 @@ def ttt_recurrence_fwd(x, f, h0=None, mode="mix", reset=None, h=None, h_last=Non
     bool or uint8 [B,T], True where a packed sequence begins (h_{t-1} taken as zero).
     h0: fp32 [B,C] or None; h_last may be h0 (a decoder's states stepped in place).
     want_states (or states) for the backward pass.  Returns (h, h_last, states or None)."""
-    shape, desc = _recurrence_prologue(x, f, mode, reset)
+    shape, dt, dev, di, desc = _recurrence_prologue(x, f, mode, reset)
     B, T, C = shape
-    dev, dt, f32 = x.device, x.dtype, torch.float32
     if h0 is not None:
-        _like("h0", h0, (B, C), f32, dev)
+        _like("h0", h0, (B, C), _F32, di)
     if states is not None:
-        _like("states", states, (B, -(-T // RECURRENCE_CHUNK), C), f32, dev)
+        _like("states", states, (B, -(-T // RECURRENCE_CHUNK), C), _F32, di)
     elif want_states:
-        states = _empty((B, -(-T // RECURRENCE_CHUNK), C), dtype=f32, device=dev)
-    h = _empty(shape, dtype=dt, device=dev) if h is None else _like("h", h, shape, dt, dev)
-    h_last = _empty((B, C), dtype=f32, device=dev) if h_last is None else _like("h_last", h_last, (B, C), f32, dev)
-    _call("ttt_recurrence_fwd", dev, stream, desc, x.data_ptr(), f.data_ptr(), _addr(reset), _addr(h0), h.data_ptr(),
-          h_last.data_ptr(), _addr(states))
+        states = _empty((B, -(-T // RECURRENCE_CHUNK), C), dtype=_F32, device=dev)
+    h = _empty(shape, dtype=dt, device=dev) if h is None else _like("h", h, shape, dt, di)
+    h_last = _empty((B, C), dtype=_F32, device=dev) if h_last is None else _like("h_last", h_last, (B, C), _F32, di)
+    _call("ttt_recurrence_fwd", di, stream, desc, x.data_ptr(), f.data_ptr(), 0 if reset is None else reset.data_ptr(),
+          0 if h0 is None else h0.data_ptr(), h.data_ptr(), h_last.data_ptr(), 0 if states is None else states.data_ptr())
     return h, h_last, states
 
 
 def ttt_recurrence_bwd(dh, x, f, states, mode="mix", reset=None, dh_last=None, dx=None, df=None, dh0=None, stream=None):
     """Gradients of ttt_recurrence_fwd from dh ([B,T,C] or None) and dh_last (fp32 [B,C]
     or None), with the forward's inputs and the states it stored.  Returns (dx, df, dh0)."""
-    shape, desc = _recurrence_prologue(x, f, mode, reset, dh)
+    shape, dt, dev, di, desc = _recurrence_prologue(x, f, mode, reset, dh)
     B, T, C = shape
-    dev, dt, f32 = x.device, x.dtype, torch.float32
-    _like("states", states, (B, -(-T // RECURRENCE_CHUNK), C), f32, dev)
+    _like("states", states, (B, -(-T // RECURRENCE_CHUNK), C), _F32, di)
     if dh_last is not None:
-        _like("dh_last", dh_last, (B, C), f32, dev)
-    dx = _empty(shape, dtype=dt, device=dev) if dx is None else _like("dx", dx, shape, dt, dev)
-    df = _empty(shape, dtype=dt, device=dev) if df is None else _like("df", df, shape, dt, dev)
-    dh0 = _empty((B, C), dtype=f32, device=dev) if dh0 is None else _like("dh0", dh0, (B, C), f32, dev)
-    _call("ttt_recurrence_bwd", dev, stream, desc, _addr(dh), x.data_ptr(), f.data_ptr(), _addr(reset),
-          states.data_ptr(), _addr(dh_last), dx.data_ptr(), df.data_ptr(), dh0.data_ptr())
+        _like("dh_last", dh_last, (B, C), _F32, di)
+    dx = _empty(shape, dtype=dt, device=dev) if dx is None else _like("dx", dx, shape, dt, di)
+    df = _empty(shape, dtype=dt, device=dev) if df is None else _like("df", df, shape, dt, di)
+    dh0 = _empty((B, C), dtype=_F32, device=dev) if dh0 is None else _like("dh0", dh0, (B, C), _F32, di)
+    _call("ttt_recurrence_bwd", di, stream, desc, 0 if dh is None else dh.data_ptr(), x.data_ptr(), f.data_ptr(),
+          0 if reset is None else reset.data_ptr(), states.data_ptr(), 0 if dh_last is None else dh_last.data_ptr(),
+          dx.data_ptr(), df.data_ptr(), dh0.data_ptr())
     return dx, df, dh0
 
 

@@ -97,6 +97,9 @@ class _Dev:
     def dim(self):
         return len(self.shape)
 
+    def get_device(self):
+        return self.device.index if self.is_cuda else -1
+
     def stride(self, i=None):
         s = [self.last]
         for n in reversed(self.shape[1:]):
