@@ -29,7 +29,6 @@ struct RecurParams {
     long long xs[2], fs[2], ds[2];
     int B, T, C, chunks;
     int cluster, cblocks;  // tile kernels: blocks of a cluster, channel blocks of a batch entry
-    int pairs;             // not TMA, bf16: two channels are aligned to four bytes everywhere
     int *status;           // device status word (timeouts)
 };
 
@@ -145,8 +144,7 @@ __global__ void __launch_bounds__(kThreads) ttt_recurrence_bwd_kernel(const __gr
 // A warp takes kS tokens of 32 CPL channels, a block of kW warps a tile of kRecurChunk
 // tokens, a cluster of P blocks P neighbouring tiles, and the cluster walks along the
 // sequence in rounds of P tiles.  Every tensor is read once, by TMA into a ring of stages;
-// where rows or pointers are not 16-byte aligned (TMA = false) every lane copies its own
-// channels into the same places, fp32 a round ahead with cp.async.  A
+// where rows or pointers are not 16-byte aligned, into the same places with cp.async.  A
 // warp folds its tokens into one map h -> A h + H (the product of the decays, the tokens'
 // own contribution); the warps' maps are joined in shared memory, the blocks' totals
 // through the cluster's distributed shared memory (stores that complete on the reader's
@@ -249,46 +247,115 @@ template <int N, bool WIDE, typename T> __device__ __forceinline__ void put_part
     }
 }
 
-template <int N, typename T> __device__ __forceinline__ void put_tokens(T *p, int c, int C, bool pairs, F<N> v)
+// How a tile's rows arrive and leave, by alignment (every tensor's):
+//   kTma     16-byte rows: boxes into a ring of stages, outputs as boxes out of them.
+//   kWords   4-byte rows (fp32; bf16 of even width): every lane copies its own words into
+//            the same places a round ahead, and stores its outputs.
+//   kHalves  bf16 rows of odd width: a warp copies the 16-byte blocks around its rows, so
+//            that a row begins some bytes into its place, and moves every row to the start
+//            of its place once it has landed; outputs leave the same way.  These loops over
+//            rows are short on purpose: unrolled into the arithmetic they outgrew the
+//            instruction cache (2 x 8192 x 1001 backward 231 us against 151; loads of
+//            single channels 238).
+enum RowFeed { kTma, kWords, kHalves };
+constexpr int kRaggedPitch = kRowBytes + 16;
+__host__ __device__ constexpr int row_pitch(int feed) { return feed == kHalves ? kRaggedPitch : kRowBytes; }
+
+// A warp's tokens t0 .. of channels c0 on, by words, into its rows dst; zeros past the end.
+template <typename T>
+__device__ __forceinline__ void copy_words(const void *x, const long long (&st)[2], int b, long long t0, int c0, int T_, int C,
+                                           unsigned char *dst)
 {
-    if (N == 2 && pairs) {
-        if (c < C) put(p + c, v);
+    constexpr int N = 4 / (int)sizeof(T);
+    const int n = (int)min(max(T_ - t0, 0LL), (long long)kS), c = c0 + (threadIdx.x & 31) * N;
+    const T *q = static_cast<const T *>(x) + b * st[0] + t0 * st[1] + c;
+    dst += (threadIdx.x & 31) * 4;
+    if (n == kS && c < C) {
+#pragma unroll
+        for (int s = 0; s < kS; ++s, q += st[1], dst += kRowBytes) copy_async4(dst, q, 4);
     } else {
-        put_part<N, false>(p, c, C, v);
+#pragma unroll 4
+        for (int s = 0; s < kS; ++s, q += st[1], dst += kRowBytes) copy_async4(dst, q, s < n && c < C ? 4 : 0);
     }
 }
 
-// A lane's channels of a warp's tokens t0 .. t0 + n - 1 into the stage, zeros behind them:
-// four bytes by cp.async where they are aligned (fp32, pairs of bf16), else by loads and
-// stores.
-template <typename T, int N>
-__device__ __forceinline__ void copy_rows(const T *src, long long stride, int c, int C, int n, bool pairs, unsigned char *dst)
-{
-    src += c;
-    if (n == kS && c + N <= C) {
-        if (N == 1 || pairs) {
+// kHalves.
+struct Ragged {
+    static constexpr int kPitch = kRaggedPitch, kBlocks = kPitch / 16;
+    using T = __nv_bfloat16;
+
+    // base: the tensor, rows: channel c0 of token 0 of the warp's n, stride: elements to the
+    // next, bytes: left of a row from there on.  Nothing behind a row's end is read, and
+    // before its start only what shares 16 bytes with it inside the tensor.  27 lanes take
+    // three rows at a time.
+    static __device__ __forceinline__ void copy(const T *base, const T *rows, long long stride, int n, int bytes, unsigned char *dst)
+    {
+        const int lane = threadIdx.x & 31, r = lane / kBlocks, k = lane - r * kBlocks;
+        if (r > 2) return;
+        const char *q = reinterpret_cast<const char *>(rows + r * stride) + 16 * k;
+        const int have = min(bytes, kRowBytes) - 16 * k;
+        // a tensor that does not begin on 16: its first bytes one by one
+        const bool head = reinterpret_cast<const char *>(rows) - reinterpret_cast<const char *>(base) < 16;
+        dst += r * kPitch + 16 * k;
 #pragma unroll
-            for (int s = 0; s < kS; ++s, src += stride) copy_async4(dst + s * kRowBytes, src);
-        } else {
-#pragma unroll
-            for (int s = 0; s < kS; ++s, src += stride)
-                *reinterpret_cast<uint32_t *>(dst + s * kRowBytes) = pack2(ld1(src), ld1(src + 1));
+        for (int s = 0; s < kS; s += 3, q += 3 * stride * (int)sizeof(T), dst += 3 * kPitch) {
+            if (s + 3 > kS && s + r >= kS) break;
+            const int off = (int)(reinterpret_cast<uintptr_t>(q) & 15), size = s + r < n ? min(max(have + off, 0), 16) : 0;
+            const char *from = q - off;
+            if (head && from < reinterpret_cast<const char *>(base)) {
+                for (int e = 0; e < size; e += (int)sizeof(T)) {
+                    const T *v = reinterpret_cast<const T *>(from + e);
+                    if (v >= base) *reinterpret_cast<T *>(dst + e) = *v;
+                }
+            } else {
+                copy_async16_part(dst, from, size);
+            }
         }
-        return;
     }
-    src -= c;
-    for (int s = 0; s < kS; ++s, dst += kRowBytes) {
-        if (s < n && c < C && N == 1) {
-            copy_async4(dst, src + s * stride + c);
-        } else {
-            float v[2] = {0.f, 0.f};
+    // at, step: low bits of the address of a row and of the distance to the next
+    static __device__ __forceinline__ void align(uint32_t at, uint32_t step, unsigned char *dst)
+    {
+        constexpr int kRows = 8;  // at a time
+        uint32_t *w = reinterpret_cast<uint32_t *>(dst) + (threadIdx.x & 31);
+#pragma unroll 1
+        for (int s = 0; s < kS; s += kRows, w += kRows * (kPitch / 4)) {
+            uint32_t v[kRows];
 #pragma unroll
-            for (int j = 0; j < N; ++j)
-                if (s < n && c + j < C) v[j] = ld1(src + s * stride + c + j);
-            *reinterpret_cast<uint32_t *>(dst) = N == 1 ? 0u : pack2(v[0], v[1]);
+            for (int j = 0; j < kRows; ++j, at += step) {
+                const uint32_t *q = w + j * (kPitch / 4) + (at >> 2 & 3);
+                v[j] = __funnelshift_r(q[0], q[1], (at & 2) * 8);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < kRows; ++j) w[j * (kPitch / 4)] = v[j];
         }
     }
-}
+    // n rows of outputs to channels c on of row (its channel 0) and the rows behind it.  bf16
+    // rows that begin on an odd half word (odd: the first one's bit, of all lanes) leave as
+    // words of neighbouring lanes' halves.
+    static __device__ __forceinline__ void store(const unsigned char *src, T *row, int c, int C, int n, uint32_t odd)
+    {
+        const int lane = threadIdx.x & 31;
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(src) + lane;
+        T *q = row + c;
+        const bool in = c < C, pair = c + 1 < C, left_in = lane > 0 && c <= C;
+#pragma unroll 4
+        for (int s = 0; s < n; ++s, q += C, w += kPitch / 4) {
+            const uint32_t v = *w;
+            unsigned short *e = reinterpret_cast<unsigned short *>(q);
+            if (((odd + (uint32_t)s * (uint32_t)C) & 1) == 0) {
+                if (pair) *reinterpret_cast<uint32_t *>(e) = v;
+                else if (in) *e = (unsigned short)v;
+            } else {
+                const uint32_t left = __shfl_up_sync(0xffffffffu, v, 1);
+                if (in && left_in) *reinterpret_cast<uint32_t *>(e - 1) = __byte_perm(left, v, 0x5432);
+                else if (left_in) e[-1] = (unsigned short)(left >> 16);
+                else if (in) *e = (unsigned short)v;
+                if (lane == 31 && pair) e[1] = (unsigned short)(v >> 16);
+            }
+        }
+    }
+};
 
 // A map of one direction: v -> a v + c.
 template <int N> struct alignas(8 * N) Map {
@@ -398,17 +465,46 @@ __device__ __forceinline__ void drain(unsigned long long *full, int rounds_issue
         if (!mbar_wait(smem_u32(&full[r % stages]), (r / stages) & 1, status, kSiteDrain)) break;
 }
 
-template <typename T, int MODE, bool RESET, bool TMA>
+// A tensor's tile of channels from c0 on, of a warp's tokens from t0 on, into its rows dst.
+template <typename T, int FEED>
+__device__ __forceinline__ void copy_rows(const void *x, const long long (&st)[2], int b, long long t0, int c0, int T_, int C,
+                                          unsigned char *dst)
+{
+    if constexpr (FEED == kWords) {
+        copy_words<T>(x, st, b, t0, c0, T_, C, dst);
+    } else {
+        const Ragged::T *base = static_cast<const Ragged::T *>(x);
+        Ragged::copy(base, base + b * st[0] + t0 * st[1] + c0, st[1], (int)min(max(T_ - t0, 0LL), (long long)kS),
+                     min(C - c0, kRowBytes) * 2, dst);
+    }
+}
+// kHalves: warps' tokens lie whole multiples of 16 bytes apart, so the offsets are token 0's.
+__device__ __forceinline__ void align_rows(const void *x, const long long (&st)[2], int b, int c0, unsigned char *dst)
+{
+    Ragged::align((uint32_t)reinterpret_cast<uintptr_t>(static_cast<const Ragged::T *>(x) + b * st[0] + c0), (uint32_t)st[1] * 2u, dst);
+}
+__device__ __forceinline__ void store_rows(const unsigned char *src, void *y, int b, int t0, int c, int T_, int C, int n)
+{
+    Ragged::T *first = static_cast<Ragged::T *>(y) + (size_t)b * T_ * C;
+    Ragged::store(src, first + (size_t)t0 * C, c, C, n, (uint32_t)(reinterpret_cast<uintptr_t>(first) >> 1));
+}
+// Bytes of the stages.  kTma: [stages][f, x(, dh)], forward h; else forward f, x and h, backward
+// f, x [2], dh [2]: f (forward: both) is refilled as soon as it is read.
+__host__ __device__ constexpr int fwd_bytes(int feed) { return (feed == kTma ? kFwdStages * 2 + 1 : 3) * kRecurChunk * row_pitch(feed); }
+__host__ __device__ constexpr int bwd_bytes(int feed) { return (feed == kTma ? kBwdStages * 3 : 5) * kRecurChunk * row_pitch(feed); }
+
+template <typename T, int MODE, bool RESET, int FEED>
 __global__ void __launch_bounds__(32 * kW, 2)
     ttt_recurrence_fwd_tile_kernel(const __grid_constant__ RecurParams p, const __grid_constant__ CUtensorMap tf,
                                    const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap th)
 {
-    constexpr int N = 4 / (int)sizeof(T), CH = 32 * N;
+    constexpr int N = 4 / (int)sizeof(T), CH = 32 * N, kPitch = row_pitch(FEED), kStep = kRecurChunk * kPitch;
+    constexpr bool TMA = FEED == kTma;
     using P_ = Pack<T, N>;
     __shared__ TileShared<N, false> sh;
     extern __shared__ unsigned char dynamic[];
-    unsigned char *stages = dynamic + (-smem_u32(dynamic) & 127u);  // [kFwdStages][f, x][kPlane], h [kPlane]
-    Map<N> *totals = reinterpret_cast<Map<N> *>(stages + (kFwdStages * 2 + 1) * kPlane);
+    unsigned char *stages = dynamic + (-smem_u32(dynamic) & 127u);
+    Map<N> *totals = reinterpret_cast<Map<N> *>(stages + fwd_bytes(FEED));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int P = p.cluster, rank = P > 1 ? (int)cluster_rank() : 0;
     const int chain = blockIdx.x / P, b = chain / p.cblocks, c0 = (chain % p.cblocks) * CH, c = c0 + lane * N;
@@ -434,18 +530,15 @@ __global__ void __launch_bounds__(32 * kW, 2)
     }
     F<N> carry = splat<N>(0.f);
     if (on && p.h0) carry = get_state<N, TMA>(p.h0 + bC, c, p.C);
-    auto copy = [&](int round) {  // not TMA: this lane's part of its warp's tokens
+    unsigned char *own = stages + warp * kS * kPitch;  // this warp's rows of f (not kTma)
+    auto copy = [&](int round) {
         const long long t0 = (long long)(round * P + rank) * kRecurChunk + warp * kS;
-        const int n = (int)min(max(p.T - t0, 0LL), (long long)kS);
-        unsigned char *dst = stages + (round % kFwdStages) * 2 * kPlane + warp * kS * kRowBytes + lane * 4;
-        copy_rows<T, N>(static_cast<const T *>(p.f) + b * p.fs[0] + t0 * p.fs[1], p.fs[1], c, p.C, n, p.pairs, dst);
-        copy_rows<T, N>(static_cast<const T *>(p.x) + b * p.xs[0] + t0 * p.xs[1], p.xs[1], c, p.C, n, p.pairs, dst + kPlane);
+        copy_rows<T, FEED>(p.f, p.fs, b, t0, c0, p.T, p.C, own);
+        copy_rows<T, FEED>(p.x, p.xs, b, t0, c0, p.T, p.C, own + kStep);
+        copy_commit();
     };
     int t0 = rank * kRecurChunk + warp * kS;
-    if (!TMA) {
-        copy(0);
-        copy_commit();
-    }
+    if (!TMA) copy(0);
     __syncthreads();
     if (P > 1) cluster_barrier();  // every block runs, its barriers set, before it is written to
     bool ok = true;
@@ -454,22 +547,30 @@ __global__ void __launch_bounds__(32 * kW, 2)
         const int buf = round & 1;
         const int n = min(max(p.T - t0, 0), kS);  // this warp's tokens
         const unsigned cuts = RESET ? reset_bits(reset, t0, n, lane) : 0u;
-        const unsigned char *mine = stages + (round % kFwdStages) * 2 * kPlane + warp * kS * kRowBytes + lane * 4;
+        const unsigned char *fm = (TMA ? stages + (round % kFwdStages) * 2 * kPlane + warp * kS * kRowBytes : own) + lane * 4;
+        const unsigned char *xm = fm + kStep;
         if (TMA) {
             ok &= mbar_wait(smem_u32(&sh.full[round % kFwdStages]), (round / kFwdStages) & 1, p.status, kSiteConsumerFull);
         } else {
-            if (round + 1 < rounds) copy(round + 1);
-            copy_commit();
-            copy_wait<1>();
+            copy_wait<0>();
+            __syncwarp();
+            if (FEED == kHalves) {
+                align_rows(p.f, p.fs, b, c0, own);
+                align_rows(p.x, p.xs, b, c0, own + kStep);
+            }
         }
         F<N> a[kS], u[kS];
         Map<N> m = {splat<N>(1.f), splat<N>(0.f)};
 #pragma unroll
         for (int s = 0; s < kS; ++s) {
-            const F<N> x = widen(*reinterpret_cast<const P_ *>(mine + kPlane + s * kRowBytes));
+            const F<N> x = widen(*reinterpret_cast<const P_ *>(xm + s * kPitch));
             F<N> eta;
-            gates<T, MODE>(widen(*reinterpret_cast<const P_ *>(mine + s * kRowBytes)), a[s], eta);
+            gates<T, MODE>(widen(*reinterpret_cast<const P_ *>(fm + s * kPitch)), a[s], eta);
             u[s] = MODE == kRecurMix ? mul(eta, x) : x;
+        }
+        if (!TMA && round + 1 < rounds) {
+            __syncwarp();
+            copy(round + 1);
         }
         if (n < kS) {  // tokens past the end: the identity
 #pragma unroll
@@ -531,13 +632,16 @@ __global__ void __launch_bounds__(32 * kW, 2)
             __syncwarp();
             if (lane == 0 && n > 0) tma_store_3d(&th, smem_u32(out), c0, t0, b);
         } else {
-            T *hp = static_cast<T *>(p.h) + ((size_t)b * p.T + t0) * p.C;
+            T *row = static_cast<T *>(p.h) + ((size_t)b * p.T + t0) * p.C + c;
+            unsigned char *out = own + 2 * kStep + lane * 4;
 #pragma unroll
             for (int s = 0; s < kS; ++s) {
                 if (RESET && (cuts >> s & 1u)) h = splat<N>(0.f);
                 h = fma(a[s], h, u[s]);
-                if (s < n) put_tokens<N>(hp + (size_t)s * p.C, c, p.C, p.pairs, h);
+                if (FEED == kHalves) put(reinterpret_cast<T *>(out + s * kPitch), h);
+                else if (s < n && on) put(row + (size_t)s * p.C, h);
             }
+            if (FEED == kHalves) store_rows(out - lane * 4, p.h, b, t0, c, p.T, p.C, n);
         }
     }
     if (TMA && lane == 0) tma_store_read();
@@ -551,18 +655,19 @@ __global__ void __launch_bounds__(32 * kW, 2)
 // it h_{t-1}, and backward r -> A r + R with R = sum_s (a_0 .. a_s) dh_s, gathered in token
 // order beside the forward one.  x and dh are read again from the stage for the outputs,
 // so a stage is refilled one round after its own.
-template <typename T, int MODE, bool RESET, bool TMA>
+template <typename T, int MODE, bool RESET, int FEED>
 __global__ void __launch_bounds__(32 * kW, 2)
     ttt_recurrence_bwd_tile_kernel(const __grid_constant__ RecurParams p, const __grid_constant__ CUtensorMap tf,
                                    const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap td,
                                    const __grid_constant__ CUtensorMap tdx, const __grid_constant__ CUtensorMap tdf)
 {
-    constexpr int N = 4 / (int)sizeof(T), CH = 32 * N;
+    constexpr int N = 4 / (int)sizeof(T), CH = 32 * N, kPitch = row_pitch(FEED), kStep = kRecurChunk * kPitch;
+    constexpr bool TMA = FEED == kTma;
     using P_ = Pack<T, N>;
     __shared__ TileShared<N, true> sh;
     extern __shared__ unsigned char dynamic[];
-    unsigned char *stages = dynamic + (-smem_u32(dynamic) & 127u);  // [kBwdStages][f, x, dh][kPlane]
-    Map<N> *totals = reinterpret_cast<Map<N> *>(stages + kBwdStages * 3 * kPlane);
+    unsigned char *stages = dynamic + (-smem_u32(dynamic) & 127u);
+    Map<N> *totals = reinterpret_cast<Map<N> *>(stages + bwd_bytes(FEED));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int P = p.cluster, rank = P > 1 ? (int)cluster_rank() : 0;
     const int chain = blockIdx.x / P, b = chain / p.cblocks, c0 = (chain % p.cblocks) * CH, c = c0 + lane * N;
@@ -596,19 +701,15 @@ __global__ void __launch_bounds__(32 * kW, 2)
     auto fetch = [&](int tile) {
         if (tile < p.chunks && on) next_start = get_state<N, TMA>(p.states_in + ((size_t)b * p.chunks + tile) * p.C, c, p.C);
     };
-    auto copy = [&](int round) {  // not TMA: this lane's part of its warp's tokens
+    unsigned char *own = stages + warp * kS * kPitch;  // this warp's rows of f (not kTma)
+    auto copy = [&](int round) {
         const long long t0 = (long long)(last - round * P) * kRecurChunk + warp * kS;
-        const int n = (int)min(max(p.T - t0, 0LL), (long long)kS);
-        unsigned char *dst = stages + (round % kBwdStages) * 3 * kPlane + warp * kS * kRowBytes + lane * 4;
-        copy_rows<T, N>(static_cast<const T *>(p.f) + b * p.fs[0] + t0 * p.fs[1], p.fs[1], c, p.C, n, p.pairs, dst);
-        copy_rows<T, N>(static_cast<const T *>(p.x) + b * p.xs[0] + t0 * p.xs[1], p.xs[1], c, p.C, n, p.pairs, dst + kPlane);
-        if (p.dh)
-            copy_rows<T, N>(static_cast<const T *>(p.dh) + b * p.ds[0] + t0 * p.ds[1], p.ds[1], c, p.C, n, p.pairs, dst + 2 * kPlane);
-    };
-    if (!TMA) {
-        copy(0);
+        copy_rows<T, FEED>(p.f, p.fs, b, t0, c0, p.T, p.C, own);
+        copy_rows<T, FEED>(p.x, p.xs, b, t0, c0, p.T, p.C, own + (1 + (round & 1)) * kStep);
+        if (p.dh) copy_rows<T, FEED>(p.dh, p.ds, b, t0, c0, p.T, p.C, own + (3 + (round & 1)) * kStep);
         copy_commit();
-    }
+    };
+    if (!TMA) copy(0);
     fetch(last);
     __syncthreads();
     if (P > 1) cluster_barrier();
@@ -618,22 +719,25 @@ __global__ void __launch_bounds__(32 * kW, 2)
         const int tile = last - round * P, t0 = tile * kRecurChunk + warp * kS, buf = round & 1;
         const int n = min(max(p.T - t0, 0), kS);
         const unsigned cuts = RESET ? reset_bits(reset, t0, n, lane) : 0u;
-        unsigned char *rows = stages + (round % kBwdStages) * 3 * kPlane + warp * kS * kRowBytes, *mine = rows + lane * 4;
+        unsigned char *rows = TMA ? stages + (round % kBwdStages) * 3 * kPlane + warp * kS * kRowBytes : own;
+        unsigned char *fm = rows + lane * 4, *xm = fm + (TMA ? 1 : 1 + (round & 1)) * kStep, *dm = xm + (TMA ? 1 : 2) * kStep;
         if (TMA) {
             ok &= mbar_wait(smem_u32(&sh.full[round % kBwdStages]), (round / kBwdStages) & 1, p.status, kSiteConsumerFull);
         } else {
-            if (round + 1 < rounds) copy(round + 1);
-            copy_commit();
-            copy_wait<1>();
+            copy_wait<0>();
+            __syncwarp();
+            if (FEED == kHalves) {
+                align_rows(p.f, p.fs, b, c0, rows);
+                align_rows(p.x, p.xs, b, c0, xm - lane * 4);
+                if (p.dh) align_rows(p.dh, p.ds, b, c0, dm - lane * 4);
+            }
         }
-        auto load_x = [&](int s) { return widen(*reinterpret_cast<const P_ *>(mine + kPlane + s * kRowBytes)); };
-        auto load_d = [&](int s) {
-            return p.dh ? widen(*reinterpret_cast<const P_ *>(mine + 2 * kPlane + s * kRowBytes)) : splat<N>(0.f);
-        };
+        auto load_x = [&](int s) { return widen(*reinterpret_cast<const P_ *>(xm + s * kPitch)); };
+        auto load_d = [&](int s) { return p.dh ? widen(*reinterpret_cast<const P_ *>(dm + s * kPitch)) : splat<N>(0.f); };
         F<N> a[kS], eta[kS], h = next_start, r;
 #pragma unroll
         for (int s = 0; s < kS; ++s)
-            gates<T, MODE>(widen(*reinterpret_cast<const P_ *>(mine + s * kRowBytes)), a[s], eta[s]);
+            gates<T, MODE>(widen(*reinterpret_cast<const P_ *>(fm + s * kPitch)), a[s], eta[s]);
         if (n < kS) {  // tokens past the end, whose x and dh read as zeros: the identity
 #pragma unroll
             for (int s = 0; s < kS; ++s)
@@ -642,7 +746,13 @@ __global__ void __launch_bounds__(32 * kW, 2)
                     eta[s] = splat<N>(0.f);
                 }
         }
-        if (round + 1 < rounds) fetch(tile - P);
+        if (round + 1 < rounds) {
+            if (!TMA) {
+                __syncwarp();  // every lane is done with f, and with the round before
+                copy(round + 1);
+            }
+            fetch(tile - P);
+        }
         Map<N> mf = {splat<N>(1.f), splat<N>(0.f)};
         F<N> back = splat<N>(0.f);
         F<N> live = splat<N>(1.f);  // a_0 .. a_s, and zero from a reset on
@@ -700,20 +810,20 @@ __global__ void __launch_bounds__(32 * kW, 2)
             g[s] = MODE == kRecurMix ? sub(h, x) : h;
             h = fma(a[s], h, MODE == kRecurMix ? mul(eta[s], x) : x);
         }
-        const size_t o = ((size_t)b * p.T + t0) * p.C;
+        const size_t o = ((size_t)b * p.T + t0) * p.C + c;
         T *dx = static_cast<T *>(p.dx) + o, *df = static_cast<T *>(p.df) + o;
 #pragma unroll
         for (int s = kS - 1; s >= 0; --s) {
             const F<N> sv = add(load_d(s), r);
             r = mul(a[s], sv);
-            const F<N> gx = MODE == kRecurMix ? mul(eta[s], sv) : sv;
-            const F<N> gf = MODE == kRecurDecay ? mul(sv, g[s]) : mul(mul(r, g[s]), eta[s]);
-            if constexpr (TMA) {  // over x and dh, which this lane has read
-                put(reinterpret_cast<T *>(mine + kPlane + s * kRowBytes), gx);
-                put(reinterpret_cast<T *>(mine + 2 * kPlane + s * kRowBytes), gf);
-            } else if (s < n) {
-                put_tokens<N>(dx + (size_t)s * p.C, c, p.C, p.pairs, gx);
-                put_tokens<N>(df + (size_t)s * p.C, c, p.C, p.pairs, gf);
+            const F<N> dxv = MODE == kRecurMix ? mul(eta[s], sv) : sv;
+            const F<N> dfv = MODE == kRecurDecay ? mul(sv, g[s]) : mul(mul(r, g[s]), eta[s]);
+            if (FEED != kWords) {  // over x and dh, which this lane has read
+                put(reinterpret_cast<T *>(xm + s * kPitch), dxv);
+                put(reinterpret_cast<T *>(dm + s * kPitch), dfv);
+            } else if (s < n && on) {
+                put(dx + (size_t)s * p.C, dxv);
+                put(df + (size_t)s * p.C, dfv);
             }
             if (RESET && (cuts >> s & 1u)) r = splat<N>(0.f);
         }
@@ -724,6 +834,9 @@ __global__ void __launch_bounds__(32 * kW, 2)
                 tma_store_3d(&tdx, smem_u32(rows + kPlane), c0, t0, b);
                 tma_store_3d(&tdf, smem_u32(rows + 2 * kPlane), c0, t0, b);
             }
+        } else if (FEED == kHalves) {
+            store_rows(xm - lane * 4, p.dx, b, t0, c, p.T, p.C, n);
+            store_rows(dm - lane * 4, p.df, b, t0, c, p.T, p.C, n);
         }
     }
     if (TMA && lane == 0) tma_store_read();
@@ -862,14 +975,14 @@ int launch_tiles(void (*kernel)(KArgs...), RecurParams p, int ch, int smem, cuda
     return cudaLaunchKernelEx(&cfg, kernel, p, maps...) == cudaSuccess ? 0 : -4;
 }
 
-template <typename T, int MODE, bool RESET, bool TMA>
+template <typename T, int MODE, bool RESET, int FEED>
 int run_tiles(const RecurParams &p, const CUtensorMap *maps, bool bwd, cudaStream_t st)
 {
     constexpr int CH = 128 / (int)sizeof(T);
     if (bwd)
-        return launch_tiles(ttt_recurrence_bwd_tile_kernel<T, MODE, RESET, TMA>, p, CH, kBwdStages * 3 * kPlane, st,
+        return launch_tiles(ttt_recurrence_bwd_tile_kernel<T, MODE, RESET, FEED>, p, CH, bwd_bytes(FEED), st,
                             maps[0], maps[1], maps[2], maps[3], maps[4]);
-    return launch_tiles(ttt_recurrence_fwd_tile_kernel<T, MODE, RESET, TMA>, p, CH, (kFwdStages * 2 + 1) * kPlane, st,
+    return launch_tiles(ttt_recurrence_fwd_tile_kernel<T, MODE, RESET, FEED>, p, CH, fwd_bytes(FEED), st,
                         maps[0], maps[1], maps[3]);
 }
 
@@ -896,6 +1009,7 @@ bool make_maps(const RecurArgs &a, bool bwd, CUtensorMap *maps)
     return true;
 }
 
+// Do two channels of bf16 stand in a word everywhere?
 bool pairs_aligned(const RecurArgs &a)
 {
     long long m = a.C;
@@ -912,11 +1026,14 @@ template <typename T, int MODE> int run(const RecurArgs &a, bool bwd)
     if (a.T > kS) {
         CUtensorMap maps[5] = {};
         if (make_maps(a, bwd, maps))
-            return a.reset ? run_tiles<T, MODE, true, true>(p, maps, bwd, a.stream)
-                           : run_tiles<T, MODE, false, true>(p, maps, bwd, a.stream);
-        p.pairs = pairs_aligned(a);
-        return a.reset ? run_tiles<T, MODE, true, false>(p, maps, bwd, a.stream)
-                       : run_tiles<T, MODE, false, false>(p, maps, bwd, a.stream);
+            return a.reset ? run_tiles<T, MODE, true, kTma>(p, maps, bwd, a.stream)
+                           : run_tiles<T, MODE, false, kTma>(p, maps, bwd, a.stream);
+        if constexpr (sizeof(T) == 2)
+            if (!pairs_aligned(a))
+                return a.reset ? run_tiles<T, MODE, true, kHalves>(p, maps, bwd, a.stream)
+                               : run_tiles<T, MODE, false, kHalves>(p, maps, bwd, a.stream);
+        return a.reset ? run_tiles<T, MODE, true, kWords>(p, maps, bwd, a.stream)
+                       : run_tiles<T, MODE, false, kWords>(p, maps, bwd, a.stream);
     }
     const dim3 grid((a.C + kThreads - 1) / kThreads, a.B);
     if (bwd) ttt_recurrence_bwd_kernel<T, MODE><<<grid, kThreads, 0, a.stream>>>(p);
