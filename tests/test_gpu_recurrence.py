@@ -250,3 +250,36 @@ def test_on_a_side_stream():
         got = _run(i, "mix")
     abi.ttt_sync_status(st)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("C", [1, 3, 6, 64, 65, 129])
+def test_rows_that_begin_anywhere(C, dtype):
+    """Tensors that start at every element of 16 bytes between NaNs, inputs and outputs: what
+    stands around them neither gets in nor is written over."""
+    B, T = 2, 150
+    i = _inputs(B, T, C, "mix", dtype, resets=0.02, seed=C)
+    n = B * T * C
+
+    def placed(t, off):
+        flat = torch.full((n + 16,), float("nan"), device="cuda", dtype=dtype)
+        if t is not None:
+            flat[off:off + n] = t.flatten()
+        return flat, flat[off:off + n].view(B, T, C)
+
+    def around(flat, off):
+        return torch.cat((flat[:off], flat[off + n:]))
+    want = _loop(i, "mix")
+    for off in range(16 // i["x"].element_size()):
+        j = dict(i, **{k: placed(i[k], (off + s) % 8)[1] for s, k in enumerate(("x", "f", "dh"))})
+        (hb, h), (xb, dx), (fb, df) = (placed(None, (off + s) % 8) for s in range(3))
+        _, hl, st = abi.ttt_recurrence_fwd(j["x"], j["f"], j["h0"], mode="mix", reset=j["reset"], want_states=True, h=h)
+        _, _, dh0 = abi.ttt_recurrence_bwd(j["dh"], j["x"], j["f"], st, mode="mix", reset=j["reset"], dh_last=j["dh_last"],
+                                           dx=dx, df=df)
+        abi.ttt_sync_status()
+        for s, flat in enumerate((hb, xb, fb)):
+            assert around(flat, (off + s) % 8).isnan().all()
+        for name, a, b in zip(("h", "h_last", "dx", "df", "dh0"), (h, hl, dx, df, dh0), want):
+            a, e = a.double().cpu().numpy(), TOL[a.dtype]
+            assert np.isfinite(a).all(), name
+            assert np.abs(a - b).max() <= e * max(1.0, np.abs(b).max()), name
