@@ -97,8 +97,8 @@ NormShape row_shape(int D, int two_from)
 }
 
 // Two chunks from 1024 features on halve what a row costs every thread: 2 x 32768 x 2048
-// forward 287 us against 327, backward (whose sums then take all 255 registers) 527
-// against 577; backward only with 16-byte rows.
+// forward 287 us against 327 before the parameter vectors were held in registers, backward
+// (whose sums then take all 255 registers) 512 against 579; backward only with 16-byte rows.
 NormShape fwd_shape(int D) { return row_shape(D, 1024); }
 NormShape bwd_shape(int D, bool whole) { return row_shape(D, whole ? 1024 : 512 * kNormChunk); }
 

@@ -11,10 +11,14 @@
 // features in fp32 registers, so a row's statistics and its outputs come from one read.
 // The variance is taken about the mean, never as a difference of squares.
 //
-// What bounds these kernels is issue slots as much as HBM (some 30 .. 60 instructions a
-// feature against 10 or 16 bytes): arithmetic on paired fp32 instructions, the parts that
+// What bounds these kernels is issue slots as much as HBM (some 40 instructions a feature
+// forward and 60 backward, against 10 and 16 bytes): arithmetic on paired fp32 instructions, the parts that
 // a call has or lacks (POST, PRE, ACT) known at compile time, parameter vectors that are
 // absent replaced by ones and zeros instead of branches, rows copied ahead with cp.async.
+// Measured (bf16, gate, residual and both norms; of the copy bandwidth): 8 x 2048 x 768
+// forward 25 us (0.75) and backward 47 us (0.63), 2 x 32768 x 2048 224 us (0.88) and 512 us
+// (0.62: registers leave eight warps an SM); y and gate alone, layer norm and GELU, 8 x 2048 x
+// 768 23.5 us (0.47: as many instructions for three fifths of the bytes).
 #pragma once
 
 #include <cstdint>
@@ -321,14 +325,23 @@ template <typename T, int G> struct Chunk {
     // forward 35 us against 31, 2 x 32768 x 2048 306 against 287): the stages take the L1
     // that holds the parameter vectors.
     static constexpr int kAhead = 2;
+    // fp32: a chunk is two loads, and two threads' chunks make four; where D and the heads are
+    // multiples of 16 a thread takes every other one of them (SPLIT), so that the two threads
+    // fill a 32-byte sector with each (2 x 8192 x 768 forward 50 us against 64, backward 91
+    // against 114).
+    static constexpr bool SPLIT = VEC && sizeof(T) == 4;
     int c0, at, step, D;
-    __device__ __forceinline__ Chunk(int r, int k, int lanes, int D_)
-        : c0(VEC ? (k * lanes + r) * kC : r * G + k * kC * lanes), step(lanes * G), D(D_)
+    __device__ __forceinline__ Chunk(int r, int k, int lanes, int D_, int dh = 1)
+        : c0(VEC ? (k * lanes + r) * kC : r * G + k * kC * lanes), step(VEC ? R::V : lanes * G), D(D_)
     {
         at = VEC ? min(c0, D - kC) : c0;
+        if (SPLIT && ((D | dh) & 15) == 0) {
+            at -= (at & 8) >> 1;
+            step = 2 * R::V;
+        }
     }
     // first feature of load i, and whether it is there
-    __device__ __forceinline__ int col(int i) const { return VEC ? at + i * R::V : c0 + i * step; }
+    __device__ __forceinline__ int col(int i) const { return (VEC ? at : c0) + i * step; }
     __device__ __forceinline__ bool has(int i) const { return VEC ? c0 < D : c0 + i * step < D; }
     // zeros in the absent features (VEC: the whole chunk counts or not, see counted())
     __device__ __forceinline__ void mask(V8 &v) const
@@ -350,7 +363,7 @@ template <typename T, int G> struct Chunk {
     __device__ __forceinline__ void fetch(const T *row, long long off, uint4 *slot, int pitch) const
     {
 #pragma unroll
-        for (int i = 0; i < kUnits; ++i) copy_async16(slot + i * pitch, row + off + at + i * (16 / (int)sizeof(T)));
+        for (int i = 0; i < kUnits; ++i) copy_async16(slot + i * pitch, row + off + col(i));
     }
     __device__ __forceinline__ V8 get(const uint4 *slot, int pitch) const
     {
@@ -391,7 +404,7 @@ template <typename T, int G> struct Chunk {
         if constexpr (VEC) {
 #pragma unroll
             for (int j = 0; j < kP; j += 2) {
-                const float4 w = __ldg(reinterpret_cast<const float4 *>(p + at + 2 * j));
+                const float4 w = __ldg(reinterpret_cast<const float4 *>(p + (SPLIT ? col(j / 2) : at + 2 * j)));
                 r.p[j] = make_float2(w.x, w.y);
                 r.p[j + 1] = make_float2(w.z, w.w);
             }
@@ -408,7 +421,7 @@ template <typename T, int G> struct Chunk {
         return r;
     }
     // feature j of a chunk, for the partial sums
-    __device__ __forceinline__ int feature(int j) const { return VEC ? c0 + j : c0 + j / G * step + j % G; }
+    __device__ __forceinline__ int feature(int j) const { return SPLIT ? col(j / 4) + j % 4 : VEC ? c0 + j : c0 + j / G * step + j % G; }
 };
 
 // -------------------------------------------------------------------- reductions
@@ -552,14 +565,14 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(c
     const uint32_t stride = gridDim.x * per;
     long long hoff[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) hoff[k] = VEC ? C(r, k, lanes, p.D).head(C(r, k, lanes, p.D).at, p.dh, p.ys[1]) : 0;
+    for (int k = 0; k < K; ++k) hoff[k] = VEC ? C(r, k, lanes, p.D, p.dh).head(C(r, k, lanes, p.D, p.dh).at, p.dh, p.ys[1]) : 0;
     // the parameter vectors, held or loaded for every row
     constexpr bool HOLD = VEC;
     V8 par[5][HOLD ? K : 1];
     if constexpr (HOLD)
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const C c(r, k, lanes, p.D);
+            const C c(r, k, lanes, p.D, p.dh);
             par[0][k] = c.vec(p.v.w1);
             par[1][k] = c.vec(p.v.b1);
             par[2][k] = c.vec(p.v.sc);
@@ -589,7 +602,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(c
             }
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const C c(r, k, lanes, p.D);
+                const C c(r, k, lanes, p.D, p.dh);
                 if constexpr (FEED == kStaged) {
                     c.fetch(y, hoff[k], slot(stage, 0, k), pitch);
                     if (act) c.fetch(gt, 0, slot(stage, 1, k), pitch);
@@ -616,12 +629,12 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(c
         };
         V8 v[K];
 #pragma unroll
-        for (int k = 0; k < K; ++k) v[k] = take(0, k, C(r, k, lanes, p.D));
+        for (int k = 0; k < K; ++k) v[k] = take(0, k, C(r, k, lanes, p.D, p.dh));
         float2 s1 = make_float2(0.f, 1.f), s2 = make_float2(0.f, 1.f);
         if (post) s1 = row_stats<T, G, K, BLOCK>(grp, post, p.eps1, inv, v, r, p.D);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const C c(r, k, lanes, p.D);
+            const C c(r, k, lanes, p.D, p.dh);
             if (post) v[k] = normed(post, v[k], s1, par[0][HOLD ? k : 0], par[1][HOLD ? k : 0], c, p.v.w1, p.v.b1);
             if (act) v[k] = mul(v[k], act_value<T>(p.act, take(1, k, c)));
             v[k] = mul(v[k], HOLD ? par[2][HOLD ? k : 0] : c.vec(p.v.sc));
@@ -635,7 +648,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(c
             s2 = row_stats<T, G, K, BLOCK>(grp, pre, p.eps2, inv, v, r, p.D);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const C c(r, k, lanes, p.D);
+                const C c(r, k, lanes, p.D, p.dh);
                 v[k] = normed(pre, v[k], s2, par[3][HOLD ? k : 0], par[4][HOLD ? k : 0], c, p.v.w2, p.v.b2);
                 if (live) c.store(static_cast<T *>(p.u) + off, v[k]);
             }
@@ -696,7 +709,7 @@ __global__ void __launch_bounds__(MAXT, MAXT >= 256 ? 1 : 256 / MAXT) ttt_block_
     long long hoff[K], dyoff[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const C c(r, k, lanes, p.D);
+        const C c(r, k, lanes, p.D, p.dh);
         hoff[k] = VEC ? c.head(c.at, p.dh, p.ys[1]) : 0;
         dyoff[k] = VEC ? c.head(c.at, p.dh, (long long)p.T * p.dh) : 0;
     }
@@ -706,7 +719,7 @@ __global__ void __launch_bounds__(MAXT, MAXT >= 256 ? 1 : 256 / MAXT) ttt_block_
     constexpr bool HOLD = VEC && K == 1;
     V8 par[4] = {};
     if constexpr (HOLD) {
-        const C c(r, 0, lanes, p.D);
+        const C c(r, 0, lanes, p.D, p.dh);
         par[0] = c.vec(p.v.w1);
         par[1] = c.vec(p.v.b1);
         par[2] = c.vec(p.v.sc);
@@ -742,7 +755,7 @@ __global__ void __launch_bounds__(MAXT, MAXT >= 256 ? 1 : 256 / MAXT) ttt_block_
                 copy_async16(slot(stage, 5, 0), p.stats + 4 * (size_t)row);
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
-                    const C c(r, k, lanes, p.D);
+                    const C c(r, k, lanes, p.D, p.dh);
                     c.fetch(y, hoff[k], slot(stage, 0, k), threads);
                     if (act) c.fetch(gt, 0, slot(stage, 1, k), threads);
                     if (has_x) c.fetch(x, 0, slot(stage, 2, k), threads);
@@ -754,7 +767,7 @@ __global__ void __launch_bounds__(MAXT, MAXT >= 256 ? 1 : 256 / MAXT) ttt_block_
                 if constexpr (FEED == kRegisters) {
 #pragma unroll
                     for (int k = 0; k < K; ++k) {
-                        const C c(r, k, lanes, p.D);
+                        const C c(r, k, lanes, p.D, p.dh);
                         c.load(y, p.dh, p.ys[1], hoff[k], regs[0][k]);
                         if (act) c.load(gt, p.D, 0, 0, regs[1][k]);
                         if (has_x) c.load(x, p.D, 0, 0, regs[2][k]);
@@ -802,7 +815,7 @@ __global__ void __launch_bounds__(MAXT, MAXT >= 256 ? 1 : 256 / MAXT) ttt_block_
         float a = 0.f, c2 = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const C c(r, k, lanes, p.D);
+            const C c(r, k, lanes, p.D, p.dh);
             yn[k] = take(0, k, c);
             if (post) yn[k] = post == 2 ? centre(yn[k], st.x, st.y) : mul(yn[k], st.y);
             c.mask(yn[k]);
@@ -834,7 +847,7 @@ __global__ void __launch_bounds__(MAXT, MAXT >= 256 ? 1 : 256 / MAXT) ttt_block_
         a = c2 = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const C c(r, k, lanes, p.D);
+            const C c(r, k, lanes, p.D, p.dh);
             // gr = dh + r (dn - mean(dn) - n mean(dn n)), the gradient of h
             gr[k] = pre == 2 ? centre(fma(hn[k], -mc, gr[k]), ma, st.w) : pre ? mul(fma(hn[k], -mc, gr[k]), st.w) : splat(0.f);
             if (has_dh) gr[k] = add(gr[k], take(4, k, c));
@@ -872,7 +885,7 @@ __global__ void __launch_bounds__(MAXT, MAXT >= 256 ? 1 : 256 / MAXT) ttt_block_
         }
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const C c(r, k, lanes, p.D);
+            const C c(r, k, lanes, p.D, p.dh);
             if (post) gr[k] = post == 2 ? centre(fma(yn[k], -mc, gr[k]), ma, st.y) : mul(fma(yn[k], -mc, gr[k]), st.y);
             if (live) c.store_heads(dy, p.dh, (long long)p.T * p.dh, dyoff[k], gr[k]);
         }
@@ -885,7 +898,7 @@ __global__ void __launch_bounds__(MAXT, MAXT >= 256 ? 1 : 256 / MAXT) ttt_block_
         if (p.slot[i] < 0) continue;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const C c(r, k, lanes, p.D);
+            const C c(r, k, lanes, p.D, p.dh);
             V8 s;
             if constexpr (WIDE) {
 #pragma unroll

@@ -7,7 +7,9 @@
 // fetched once per thread, and HB heads' loads are in flight together.  In the half
 // layout a thread's two vectors are the features [uV, uV + V) and [rot/2 + uV, ...);
 // interleaved, two neighbouring vectors.  Features past rot are units of two vectors
-// that are copied.
+// that are copied.  Measured (cold L2, of the copy bandwidth): 2 x 32768 tokens of 3 x 32
+// heads of 64 in bf16 251 us (0.95), 8 x 2048 of 3 x 12 heads 28 us (0.79: ramp-up and tail),
+// heads of 20 (4- and 8-byte accesses) 0.55.
 #include "ttt_internal.h"
 #include "ttt_vec.cuh"
 
