@@ -16,9 +16,9 @@
 // a call has or lacks (POST, PRE, ACT) known at compile time, parameter vectors that are
 // absent replaced by ones and zeros instead of branches, rows copied ahead with cp.async.
 // Measured (bf16, gate, residual and both norms; of the copy bandwidth): 8 x 2048 x 768
-// forward 25 us (0.75) and backward 47 us (0.63), 2 x 32768 x 2048 224 us (0.88) and 512 us
+// forward 24 us (0.77) and backward 47 us (0.63), 2 x 32768 x 2048 224 us (0.88) and 511 us
 // (0.62: registers leave eight warps an SM); y and gate alone, layer norm and GELU, 8 x 2048 x
-// 768 23.5 us (0.47: as many instructions for three fifths of the bytes).
+// 768 22 us (0.51: as many instructions for three fifths of the bytes).
 #pragma once
 
 #include <cstdint>
@@ -544,8 +544,16 @@ __device__ __forceinline__ float2 row_stats(Group<BLOCK> &g, int kind, float eps
 // the parameters.  With 16-byte rows the parameter vectors stay in registers: loading
 // three to five of them for every row kept L1 85% busy (2 x 32768 x 2048 257 us against
 // 225, 8 x 2048 x 768 sandwich 25.3 against 23.2).
+//
+// Six blocks of 128 threads an SM, 80 registers, for one chunk a thread (8 x 2048 x 768 with
+// layer norm, GELU and RMS norm 27.6 us against 33.3 with 84 registers left to the
+// compiler; GELU and layer norm alone 21.9 against 23.5), but not with two layer norms, whose five
+// vectors would spill (fp32 2 x 8192 x 768: 52.5 against 47.5).
+constexpr int fwd_blocks(int K, int post, int pre) { return K == 1 && post >= 0 && post + pre < 4 ? 6 : 1; }
+constexpr int fwd_threads(bool block, int K, int post, int pre) { return block && fwd_blocks(K, post, pre) == 1 ? 512 : 128; }
+
 template <typename T, int G, int K, bool BLOCK, int POST, int PRE, int ACT>
-__global__ void __launch_bounds__(BLOCK ? 512 : 128) ttt_block_norm_fwd_kernel(const __grid_constant__ NormFwdParams p)
+__global__ void __launch_bounds__(fwd_threads(BLOCK, K, POST, PRE), fwd_blocks(K, POST, PRE)) ttt_block_norm_fwd_kernel(const __grid_constant__ NormFwdParams p)
 {
     using C = Chunk<T, G>;
     constexpr bool VEC = C::VEC;
