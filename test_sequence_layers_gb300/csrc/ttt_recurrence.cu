@@ -651,6 +651,7 @@ __global__ void __launch_bounds__(32 * kW, 2)
         }
     }
     if (TMA && lane == 0) tma_store_read();
+    if (!TMA) copy_wait<0>();  // a block that gave up has some in flight
     if (!ok && TMA && threadIdx.x == 0) drain(sh.full, min(rounds, round + kFwdStages), kFwdStages, p.status);
     if (P > 1) cluster_barrier();  // no block leaves while another may write to it
     if (ok && p.h_last && on && rank == 0 && warp == 0) put_part<N, TMA>(p.h_last + bC, c, p.C, carry);
@@ -846,6 +847,7 @@ __global__ void __launch_bounds__(32 * kW, 2)
         }
     }
     if (TMA && lane == 0) tma_store_read();
+    if (!TMA) copy_wait<0>();  // a block that gave up has some in flight
     if (!ok && TMA && threadIdx.x == 0) drain(sh.full, min(rounds, max(round + 1, kBwdStages)), kBwdStages, p.status);
     if (P > 1) cluster_barrier();
     if (ok && p.dh0 && on && rank == 0 && warp == 0) put_part<N, TMA>(p.dh0 + bC, c, p.C, carry);
