@@ -261,8 +261,8 @@ template <int N, bool WIDE, typename T> __device__ __forceinline__ void put_part
 //            that a row begins some bytes into its place, and moves every row to the start
 //            of its place once it has landed; outputs leave the same way.  These loops over
 //            rows are short on purpose: unrolled into the arithmetic they outgrew the
-//            instruction cache (2 x 8192 x 1001 backward 231 us against 151; loads of
-//            single channels 238).
+//            instruction cache (2 x 8192 x 1001 backward, clusters of four, 231 us against
+//            151, and loads of single channels 238; 106 with the eight that are chosen).
 enum RowFeed { kTma, kWords, kHalves };
 constexpr int kRaggedPitch = kRowBytes + 16;
 __host__ __device__ constexpr int row_pitch(int feed) { return feed == kHalves ? kRaggedPitch : kRowBytes; }
@@ -930,6 +930,26 @@ template <typename... KArgs> Capacity query_capacity(void (*kernel)(KArgs...), i
     return c;
 }
 
+// The same, asked once for each kernel and device.
+template <typename... KArgs> Capacity capacity(void (*kernel)(KArgs...), int smem, int per_block)
+{
+    static std::mutex mu;
+    static struct {
+        void (*kernel)(KArgs...);
+        int dev;
+        Capacity c;
+    } memo[256];
+    static int used = 0;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < used; ++i)
+        if (memo[i].kernel == kernel && memo[i].dev == dev) return memo[i].c;
+    const Capacity c = query_capacity(kernel, smem, per_block);
+    if (used < 256) memo[used++] = {kernel, dev, c};
+    return c;
+}
+
 // Blocks of a cluster.  A round of a block alone on its SM is the unit of time, 1.2 us
 // forward and 2.1 us backward (bf16, mix); 1.33 with the exchange between blocks; two
 // blocks on an SM take `two` each, 1.95 in bf16, 1.5 in fp32, which has half the channels
@@ -964,17 +984,7 @@ int launch_tiles(void (*kernel)(KArgs...), RecurParams p, int ch, int smem, cuda
     const long long chains = (long long)p.B * p.cblocks;
     const int per_block = 2 * ch * 8;  // each block's totals, twice
     smem += 128;                       // alignment
-    static std::mutex mu;
-    static Capacity caps[64];
-    static bool known[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -4;
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        if (!known[dev]) caps[dev] = query_capacity(kernel, smem, per_block);
-        known[dev] = true;
-    }
-    p.cluster = plan_cluster(chains, p.chunks, ch < 64 ? 1.5 : 1.95, caps[dev]);
+    p.cluster = plan_cluster(chains, p.chunks, ch < 64 ? 1.5 : 1.95, capacity(kernel, smem, per_block));
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute at;
     if (chains * p.cluster > 0x7fffffffLL ||
