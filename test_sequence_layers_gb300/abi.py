@@ -494,20 +494,40 @@ def _like(name, t, shape, dtype, di):
     return t
 
 
-def _call(name, di, stream, *args):
-    """Runs one library entry point on device di's current stream (or `stream`)."""
-    if stream is None:
-        raw = _raw_stream(di)
-    elif stream.device.index != di:
-        raise ValueError(f"the stream is on {stream.device} but the tensors on cuda:{di}")
-    else:
-        raw = stream.cuda_stream
+def _each_tensor(x, act):
+    if isinstance(x, (tuple, list)):
+        for t in x:
+            _each_tensor(t, act)
+    elif hasattr(x, "record_stream"):
+        act(x)
+
+
+def _on_stream(stream, like, fn, *args):
+    """fn(*args) on `stream`, another than the current one of `like`'s device, and safe
+    for PyTorch's allocator: what the call allocates belongs to `stream` (memory that the
+    current stream may still be using is not handed out, and a workspace is not reused
+    before the kernels are done with it), the inputs are not reused before then either
+    when the caller drops them, nor the results before the current stream's work on them."""
+    if like.is_cuda:
+        if stream.device != like.device:
+            raise ValueError(f"the stream is on {stream.device} but the tensors on {like.device}")
+        current = torch.cuda.current_stream(like.device)
+        with torch.cuda.stream(stream):
+            out = fn(*args)
+        _each_tensor(args, lambda t: t.record_stream(stream))
+        _each_tensor(out, lambda t: t.record_stream(current))
+        return out
+    return fn(*args)  # refuses
+
+
+def _call(name, di, *args):
+    """Runs one library entry point on device di's current stream."""
     f = _fns.get(name) or _fn(name)
     if _current_device() == di:
-        rc = f(*args, raw)
+        rc = f(*args, _raw_stream(di))
     else:
         with torch.cuda.device(di):
-            rc = f(*args, raw)
+            rc = f(*args, _raw_stream(di))
     if rc != 0:
         raise TTTError(name, rc)
 
@@ -526,6 +546,9 @@ def ttt_rope(q, k, v, table, positions=None, pos0=0, period=0, interleaved=False
     [B,H,T,d] unless q_out, k_out, v_out are given (any strides; an output may be its
     own input).  Returns (q_out, k_out, v_out).  A position outside the table gives NaN
     and TTT_ERR_RANGE from ttt_sync_status."""
+    if stream is not None:
+        return _on_stream(stream, q, ttt_rope, q, k, v, table, positions, pos0, period, interleaved, inverse, q_out,
+                          k_out, v_out)
     dt, dev, di, sq = q.dtype, q.device, q.get_device(), q.stride()
     io = _IO.get(dt)
     if io is None or not q.is_cuda or len(sq) != 4 or sq[3] != 1:
@@ -573,7 +596,7 @@ def ttt_rope(q, k, v, table, positions=None, pos0=0, period=0, interleaved=False
         svo = _rows("v_out", v_out, q, v.shape, dt, di)
     desc = _ROPE_DESC.pack(B, T, H, hk, d, 2 * tshape[1], interleaved, inverse, io, tshape[0], period, pos0, pbs,
                            *sq[:3], *sk, *sv, *so, *sko, *svo)
-    _call("ttt_rope", di, stream, desc, q.data_ptr(), 0 if k is None else k.data_ptr(), 0 if v is None else v.data_ptr(),
+    _call("ttt_rope", di, desc, q.data_ptr(), 0 if k is None else k.data_ptr(), 0 if v is None else v.data_ptr(),
           table.data_ptr(), 0 if positions is None else positions.data_ptr(), q_out.data_ptr(),
           0 if k is None else k_out.data_ptr(), 0 if v is None else v_out.data_ptr())
     return q_out, k_out, v_out
@@ -626,6 +649,9 @@ def ttt_block_norm_fwd(y, x=None, gate=None, act=None, post="none", post_weight=
     "silu" or "gelu" (default: "silu" with a gate); post, pre "none", "rms" or "layer".
     Weights, biases and scale: fp32 [D] or None.  want_stats (or stats) for the backward
     pass.  h may be x.  Returns (h, u or None, stats or None)."""
+    if stream is not None:
+        return _on_stream(stream, y, ttt_block_norm_fwd, y, x, gate, act, post, post_weight, post_bias, scale, alpha,
+                          pre, pre_weight, pre_bias, post_eps, pre_eps, want_stats, h, u, stats)
     if act is None:
         act = "none" if gate is None else "silu"
     shape, dt, dev, di, desc, par = _norm_prologue(y, x, gate, act, post, pre, post_eps, pre_eps, alpha, post_weight,
@@ -639,7 +665,7 @@ def ttt_block_norm_fwd(y, x=None, gate=None, act=None, post="none", post_weight=
     elif want_stats:
         stats = _empty((shape[0], shape[1], 4), dtype=_F32, device=dev)
     h = _empty(shape, dtype=dt, device=dev) if h is None else _like("h", h, shape, dt, di)
-    _call("ttt_block_norm_fwd", di, stream, desc, par, y.data_ptr(), 0 if x is None else x.data_ptr(),
+    _call("ttt_block_norm_fwd", di, desc, par, y.data_ptr(), 0 if x is None else x.data_ptr(),
           0 if gate is None else gate.data_ptr(), h.data_ptr(), 0 if u is None else u.data_ptr(),
           0 if stats is None else stats.data_ptr())
     return h, u, stats
@@ -664,6 +690,9 @@ def ttt_block_norm_bwd(dh, du, y, stats, x=None, gate=None, act=None, post="none
     the forward's inputs and its stats.  Returns BlockNormGrads: y's in y's shape
     (contiguous), fp32 [D] for every parameter vector given.  workspace: a CUDA uint8
     tensor of ttt_block_norm_bwd_workspace(...) bytes, allocated here when None."""
+    if stream is not None:
+        return _on_stream(stream, y, ttt_block_norm_bwd, dh, du, y, stats, x, gate, act, post, post_weight, post_bias,
+                          scale, alpha, pre, pre_weight, pre_bias, post_eps, pre_eps, workspace)
     if act is None:
         act = "none" if gate is None else "silu"
     shape, dt, dev, di, desc, par = _norm_prologue(y, x, gate, act, post, pre, post_eps, pre_eps, alpha, post_weight,
@@ -679,7 +708,7 @@ def ttt_block_norm_bwd(dh, du, y, stats, x=None, gate=None, act=None, post="none
         workspace = _empty(_norm_workspace(desc), dtype=torch.uint8, device=dev)
     elif workspace.get_device() != di or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on y's device")
-    _call("ttt_block_norm_bwd", di, stream, desc, par, 0 if dh is None else dh.data_ptr(),
+    _call("ttt_block_norm_bwd", di, desc, par, 0 if dh is None else dh.data_ptr(),
           0 if du is None else du.data_ptr(), y.data_ptr(), 0 if x is None else x.data_ptr(),
           0 if gate is None else gate.data_ptr(), stats.data_ptr(), dy.data_ptr(), 0 if dx is None else dx.data_ptr(),
           0 if dg is None else dg.data_ptr(), _NORM_PAR.pack(*[0 if t is None else t.data_ptr() for t in gv]),
@@ -717,6 +746,8 @@ def ttt_recurrence_fwd(x, f, h0=None, mode="mix", reset=None, h=None, h_last=Non
     bool or uint8 [B,T], True where a packed sequence begins (h_{t-1} taken as zero).
     h0: fp32 [B,C] or None; h_last may be h0 (a decoder's states stepped in place).
     want_states (or states) for the backward pass.  Returns (h, h_last, states or None)."""
+    if stream is not None:
+        return _on_stream(stream, x, ttt_recurrence_fwd, x, f, h0, mode, reset, h, h_last, want_states, states)
     shape, dt, dev, di, desc = _recurrence_prologue(x, f, mode, reset)
     B, T, C = shape
     if h0 is not None:
@@ -727,7 +758,7 @@ def ttt_recurrence_fwd(x, f, h0=None, mode="mix", reset=None, h=None, h_last=Non
         states = _empty((B, -(-T // RECURRENCE_CHUNK), C), dtype=_F32, device=dev)
     h = _empty(shape, dtype=dt, device=dev) if h is None else _like("h", h, shape, dt, di)
     h_last = _empty((B, C), dtype=_F32, device=dev) if h_last is None else _like("h_last", h_last, (B, C), _F32, di)
-    _call("ttt_recurrence_fwd", di, stream, desc, x.data_ptr(), f.data_ptr(), 0 if reset is None else reset.data_ptr(),
+    _call("ttt_recurrence_fwd", di, desc, x.data_ptr(), f.data_ptr(), 0 if reset is None else reset.data_ptr(),
           0 if h0 is None else h0.data_ptr(), h.data_ptr(), h_last.data_ptr(), 0 if states is None else states.data_ptr())
     return h, h_last, states
 
@@ -735,6 +766,8 @@ def ttt_recurrence_fwd(x, f, h0=None, mode="mix", reset=None, h=None, h_last=Non
 def ttt_recurrence_bwd(dh, x, f, states, mode="mix", reset=None, dh_last=None, dx=None, df=None, dh0=None, stream=None):
     """Gradients of ttt_recurrence_fwd from dh ([B,T,C] or None) and dh_last (fp32 [B,C]
     or None), with the forward's inputs and the states it stored.  Returns (dx, df, dh0)."""
+    if stream is not None:
+        return _on_stream(stream, x, ttt_recurrence_bwd, dh, x, f, states, mode, reset, dh_last, dx, df, dh0)
     shape, dt, dev, di, desc = _recurrence_prologue(x, f, mode, reset, dh)
     B, T, C = shape
     _like("states", states, (B, -(-T // RECURRENCE_CHUNK), C), _F32, di)
@@ -743,7 +776,7 @@ def ttt_recurrence_bwd(dh, x, f, states, mode="mix", reset=None, dh_last=None, d
     dx = _empty(shape, dtype=dt, device=dev) if dx is None else _like("dx", dx, shape, dt, di)
     df = _empty(shape, dtype=dt, device=dev) if df is None else _like("df", df, shape, dt, di)
     dh0 = _empty((B, C), dtype=_F32, device=dev) if dh0 is None else _like("dh0", dh0, (B, C), _F32, di)
-    _call("ttt_recurrence_bwd", di, stream, desc, 0 if dh is None else dh.data_ptr(), x.data_ptr(), f.data_ptr(),
+    _call("ttt_recurrence_bwd", di, desc, 0 if dh is None else dh.data_ptr(), x.data_ptr(), f.data_ptr(),
           0 if reset is None else reset.data_ptr(), states.data_ptr(), 0 if dh_last is None else dh_last.data_ptr(),
           dx.data_ptr(), df.data_ptr(), dh0.data_ptr())
     return dx, df, dh0
