@@ -209,6 +209,32 @@ def _check_call(dev, stream, tensors, shapes):
         raise ValueError(f"the stream is on {stream.device} but the tensors on {dev}")
 
 
+def _each_tensor(x, act):
+    if isinstance(x, (tuple, list)):
+        for t in x:
+            _each_tensor(t, act)
+    elif hasattr(x, "record_stream"):
+        act(x)
+
+
+def _on_stream(stream, like, fn, *args):
+    """fn(*args) on `stream`, another than the current one of `like`'s device, and safe
+    for PyTorch's allocator: what the call allocates belongs to `stream` (memory that the
+    current stream may still be using is not handed out, and a workspace is not reused
+    before the kernels are done with it), the inputs are not reused before then either
+    when the caller drops them, nor the results before the current stream's work on them."""
+    if like.is_cuda:
+        if stream.device != like.device:
+            raise ValueError(f"the stream is on {stream.device} but the tensors on {like.device}")
+        current = torch.cuda.current_stream(like.device)
+        with torch.cuda.stream(stream):
+            out = fn(*args)
+        _each_tensor(args, lambda t: t.record_stream(stream))
+        _each_tensor(out, lambda t: t.record_stream(current))
+        return out
+    return fn(*args)  # refuses
+
+
 def _out_like_q(z, q):
     if z is not None and (z.dtype != q.dtype or not z.is_contiguous()):
         raise ValueError("z must be a contiguous tensor of q's dtype")
@@ -244,6 +270,9 @@ def ttt_linear_fwd(q, k, v, W0, mini_batch, causal=True, eta=None, eta_scalar=1.
     loss "mse" or "dot"; epochs > 1: repeated full-batch steps (causal=False,
     mini_batch >= T); ln_gamma, ln_beta: fp32 [H,d] for the inner model
     x + LN(x W).  Returns (z, W_final or None)."""
+    if stream is not None:
+        return _on_stream(stream, q, ttt_linear_fwd, q, k, v, W0, mini_batch, causal, eta, eta_scalar, z, W_out, want_W,
+                          None, loss, epochs, ln_gamma, ln_beta, ln_eps)
     io, w0s = _linear_prologue(q, k, v, W0, eta, z, W_out, stream, ln_gamma, ln_beta)
     B, H, T, d = q.shape
     with torch.cuda.device(q.device):
@@ -274,6 +303,9 @@ def ttt_linear_fwd_seqpar(q, k, v, W0, mini_batch, causal=True, eta=None, eta_sc
     """Sequence-parallel TTT-Linear forward (same arguments as ttt_linear_fwd).
     workspace: a CUDA uint8 tensor of at least ttt_linear_seqpar_workspace(...) bytes,
     allocated here when None.  Returns (z, W_final or None)."""
+    if stream is not None:
+        return _on_stream(stream, q, ttt_linear_fwd_seqpar, q, k, v, W0, mini_batch, causal, eta, eta_scalar, z, W_out,
+                          want_W, workspace, None, loss)
     io, w0s = _linear_prologue(q, k, v, W0, eta, z, W_out, stream)
     _check_call(q.device, None, {"workspace": workspace}, {})
     if workspace is not None and not workspace.is_contiguous():
@@ -320,6 +352,9 @@ def ttt_dwconv_fwd(q, k, v, W0, height, width, eta=None, eta_scalar=1.0, loss="m
     """Depthwise 3x3 convolution inner model, full-batch inner GD.  q,k,v: [B,H,N,d]
     with N = height*width tokens in row-major grid order; W0: fp32 taps [H,9,d] or
     [B,H,9,d].  Returns (z, W_final [B,H,9,d] or None)."""
+    if stream is not None:
+        return _on_stream(stream, q, ttt_dwconv_fwd, q, k, v, W0, height, width, eta, eta_scalar, loss, epochs, z, W_out,
+                          want_W)
     io = _check_tokens(q, k, v)
     B, H, N, d = q.shape
     if N != height * width:
@@ -356,6 +391,9 @@ def ttt_mlp_fwd(q, k, v, W1, c1, W2, c2, mini_batch, causal=True, eta=None, eta_
     Parameters fp32, per head ([H,...]) or per (batch, head) ([B,H,...]).  outs: the
     final-weight tensors (W1, c1, W2, c2), each [B,H,...] fp32 or None.  Returns
     (z, (W1,c1,W2,c2) final or None)."""
+    if stream is not None:
+        return _on_stream(stream, q, ttt_mlp_fwd, q, k, v, W1, c1, W2, c2, mini_batch, causal, eta, eta_scalar, z, outs,
+                          want_W, None, activation, ln_gamma, ln_beta, ln_eps)
     io = _check_tokens(q, k, v)
     B, H, T, d = q.shape
     W1, c1, W2, c2 = (_f32(t, n) for t, n in ((W1, "W1"), (c1, "c1"), (W2, "W2"), (c2, "c2")))
@@ -405,6 +443,8 @@ def ttt_eta_gate(x, theta, eta_base=1.0, eta=None, stream=None):
     x[b,t]).  x: bf16 [B,T,dm] (the layer's input tokens); theta: bf16 [H,dm] (one
     vector per head).  Returns eta, fp32 [B,H,T] (the layout the TTT entry points
     read)."""
+    if stream is not None:
+        return _on_stream(stream, x, ttt_eta_gate, x, theta, eta_base, eta)
     for name, t in (("x", x), ("theta", theta)):
         if not t.is_cuda or t.dtype != torch.bfloat16 or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous bfloat16 CUDA tensor (no CPU path)")
@@ -492,32 +532,6 @@ def _like(name, t, shape, dtype, di):
     if t.dtype is not dtype or t.get_device() != di or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{di}")
     return t
-
-
-def _each_tensor(x, act):
-    if isinstance(x, (tuple, list)):
-        for t in x:
-            _each_tensor(t, act)
-    elif hasattr(x, "record_stream"):
-        act(x)
-
-
-def _on_stream(stream, like, fn, *args):
-    """fn(*args) on `stream`, another than the current one of `like`'s device, and safe
-    for PyTorch's allocator: what the call allocates belongs to `stream` (memory that the
-    current stream may still be using is not handed out, and a workspace is not reused
-    before the kernels are done with it), the inputs are not reused before then either
-    when the caller drops them, nor the results before the current stream's work on them."""
-    if like.is_cuda:
-        if stream.device != like.device:
-            raise ValueError(f"the stream is on {stream.device} but the tensors on {like.device}")
-        current = torch.cuda.current_stream(like.device)
-        with torch.cuda.stream(stream):
-            out = fn(*args)
-        _each_tensor(args, lambda t: t.record_stream(stream))
-        _each_tensor(out, lambda t: t.record_stream(current))
-        return out
-    return fn(*args)  # refuses
 
 
 def _call(name, di, *args):

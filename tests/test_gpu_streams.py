@@ -54,6 +54,23 @@ def test_backward_workspace_outlives_the_call():
     assert all(bool((t == 0xff).all()) for t in keep)
 
 
+def test_split_forward_workspace_outlives_the_call():
+    inp = G.synth.make("linear", B=1, H=4, T=2048, d=64, b=16, causal=True, eta="sigmoid", seed=700)
+    q, k, v, eta, W0 = (t.cuda() for t in (inp.q, inp.k, inp.v, inp.eta, inp.params["W0"]))
+    need = abi.ttt_linear_seqpar_workspace(1, 4, 2048, 64, 16)
+    assert need > 0
+    want = abi.ttt_linear_fwd_seqpar(q, k, v, W0, 16, eta=eta)
+    side = torch.cuda.Stream()
+    _ready(side)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(HOLD)
+    got = abi.ttt_linear_fwd_seqpar(q, k, v, W0, 16, eta=eta, stream=side)
+    keep = _overwrite([need])
+    abi.ttt_sync_status(side)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert all(bool((t == 0xff).all()) for t in keep)
+
+
 def test_results_are_not_put_where_the_current_stream_still_reads():
     y, dh, du, kw = _norm()
     x, f = (torch.randn(4, 700, 768, device="cuda").to(BF) for _ in range(2))

@@ -116,6 +116,46 @@ def test_recurrence_backward(gpu):
     assert len(_check(gpu, abi.ttt_recurrence_bwd, dh, x, f, _T((2, 1, 8), F32))) == 3
 
 
+def _library(monkeypatch, gpu):
+    side, made, calls = gpu
+
+    class Lib:
+        def __getattr__(self, name):
+            if name.endswith("workspace"):
+                return lambda *a: 4096
+            return lambda *a: calls.append(torch.cuda.current_stream().name) or 0
+    monkeypatch.setattr(abi, "lib", Lib)
+
+
+def test_linear(gpu, monkeypatch):
+    _library(monkeypatch, gpu)
+    q, W = _T((2, 3, 256, 64)), _T((3, 64, 64), F32)
+    assert len(_check(gpu, abi.ttt_linear_fwd, q, q, q, W, 16, eta=_T((2, 3, 256), F32))) == 2
+
+
+def test_linear_seqpar_workspace(gpu, monkeypatch):
+    _library(monkeypatch, gpu)
+    q, W = _T((2, 3, 256, 64)), _T((3, 64, 64), F32)
+    made = _check(gpu, abi.ttt_linear_fwd_seqpar, q, q, q, W, 16)
+    assert len(made) == 3 and sum("current" in t.used_on for t in made) == 2
+
+
+def test_mlp(gpu, monkeypatch):
+    _library(monkeypatch, gpu)
+    q = _T((2, 3, 256, 64))
+    P = [_T(s, F32) for s in ((3, 64, 256), (3, 256), (3, 256, 64), (3, 64))]
+    made = _check(gpu, abi.ttt_mlp_fwd, q, q, q, *P, 16)
+    assert len(made) == 5 and all("current" in t.used_on for t in made)
+
+
+def test_dwconv_and_gate(gpu, monkeypatch):
+    _library(monkeypatch, gpu)
+    q = _T((1, 2, 196, 64))
+    assert len(_check(gpu, abi.ttt_dwconv_fwd, q, q, q, _T((2, 9, 64), F32), 14, 14)) == 2
+    gpu[1].clear(), gpu[2].clear()
+    assert len(_check(gpu, abi.ttt_eta_gate, _T((2, 50, 256)), _T((4, 256)))) == 1
+
+
 def test_a_stream_of_another_device_is_refused(gpu):
     side, made, calls = gpu
     side.device = torch.device("cuda", 1)
