@@ -323,8 +323,10 @@ typedef struct {
  *               A position < 0 or (with period 0) >= table_rows reads nothing: the
  *               token's rotated features become NaN and ttt_sync_status returns
  *               TTT_ERR_RANGE.  pos0 + t is checked before the launch (TTT_ERR_ARG).
- * An output may be its own input (same pointer and strides) and may not overlap an
- * input otherwise, except as interleaved slices of one buffer with equal strides
+ * An output may be its own input (same pointer and strides).  Otherwise it may not share
+ * memory with an input, with another output, with the table or the positions, nor hold an
+ * element twice: each of its dimensions steps over all of those inside it.  Slices of one
+ * buffer with equal strides are told apart exactly, other views by their ends
  * (TTT_ERR_ARG).  Data pointers: aligned to their element (TTT_ERR_ALIGN); 16-byte
  * aligned pointers and strides with rot/2 a multiple of 8 (bf16) or 4 (fp32) move 16
  * bytes at a time.  The rotation is computed in fp32 and rounded once.

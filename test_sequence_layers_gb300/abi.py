@@ -557,8 +557,9 @@ def ttt_rope(q, k, v, table, positions=None, pos0=0, period=0, interleaved=False
     or [T] on the device, or None for pos0 + t; period > 0 takes them modulo period.
     interleaved: pairs (2i, 2i+1) instead of (i, i + rot/2).  inverse=True rotates back:
     the gradients of q, k, v from those of the outputs.  Outputs are contiguous
-    [B,H,T,d] unless q_out, k_out, v_out are given (any strides; an output may be its
-    own input).  Returns (q_out, k_out, v_out).  A position outside the table gives NaN
+    [B,H,T,d] unless q_out, k_out, v_out are given (views whose dimensions
+    step over those inside them; an output may be its own input, and shares memory with
+    nothing else).  Returns (q_out, k_out, v_out).  A position outside the table gives NaN
     and TTT_ERR_RANGE from ttt_sync_status."""
     if stream is not None:
         return _on_stream(stream, q, ttt_rope, q, k, v, table, positions, pos0, period, interleaved, inverse, q_out,

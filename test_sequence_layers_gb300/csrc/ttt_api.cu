@@ -475,7 +475,97 @@ long long span(const long long st[3], int B, int H, int T, int d)
     return st[0] * (B - 1) + st[1] * (H - 1) + st[2] * (T - 1) + d;
 }
 
-bool same_strides(const long long a[3], const long long b[3]) { return a[0] == b[0] && a[1] == b[1] && a[2] == b[2]; }
+// A [n0,n1,n2,d] view by rising stride, without its dimensions of one entry.
+struct Nest {
+    int dims;
+    long long stride[3], extent[3];  // extent[i]: elements from first to one past the last, dimensions 0 .. i
+    int n[3];
+    long long inner(int i) const { return i > 0 ? extent[i - 1] : d; }
+    long long d;
+    bool nested;  // every dimension steps over all of those inside it: no element twice
+};
+
+Nest nest(const long long st[3], const int n[3], int d)
+{
+    Nest v = {};
+    v.d = d;
+    v.nested = true;
+    for (int i = 0; i < 3; ++i) {
+        if (n[i] <= 1) continue;
+        int j = v.dims++;
+        for (; j > 0 && v.stride[j - 1] > st[i]; --j) {
+            v.stride[j] = v.stride[j - 1];
+            v.n[j] = v.n[j - 1];
+        }
+        v.stride[j] = st[i];
+        v.n[j] = n[i];
+    }
+    for (int i = 0; i < v.dims; ++i) {
+        v.nested = v.nested && v.stride[i] >= v.inner(i);
+        v.extent[i] = v.stride[i] * (v.n[i] - 1) + v.inner(i);
+    }
+    return v;
+}
+
+// Do two nested views with equal strides, the second `off` elements behind the first, share
+// an element?  With off = q s + r along the outermost stride s, block k of the first meets
+// at most blocks k - q (r further on) and k - q - 1 (s - r before) of the second.
+bool share(const Nest &a, const Nest &b, int dims, long long off)
+{
+    if (dims == 0) return off > -a.d && off < a.d;
+    const int i = dims - 1;
+    const long long s = a.stride[i], q = off >= 0 ? off / s : -((-off + s - 1) / s), r = off - q * s;
+    for (int up = 0; up < 2; ++up) {
+        const long long m = -(q + up);  // block 0 of the first meets block m of the second
+        if (m < b.n[i] && m > -(long long)a.n[i] && share(a, b, i, r - up * s)) return true;
+    }
+    return false;
+}
+
+// A [B,H,T,d] view: its first element and strides.
+struct HeadView {
+    const void *p;
+    long long st[3];
+    int n[3];
+};
+
+// Do two views share memory, or may they?  Told apart exactly where their strides agree
+// and their dimensions nest (slices of one buffer); else by their ends.
+bool shares_memory(const HeadView &a, const HeadView &b, int d, int es)
+{
+    if (!overlaps(a.p, es * span(a.st, a.n[0], a.n[1], a.n[2], d), b.p, es * span(b.st, b.n[0], b.n[1], b.n[2], d))) return false;
+    const long long bytes = (long long)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p));
+    if (bytes % es) return true;
+    long long sa[3], sb[3];
+    int na[3], nb[3], n[3];
+    for (int i = 0; i < 3; ++i) {
+        // a dimension of one entry takes the other's stride
+        sa[i] = a.n[i] > 1 ? a.st[i] : b.st[i];
+        sb[i] = b.n[i] > 1 ? b.st[i] : a.st[i];
+        if (sa[i] != sb[i]) return true;
+        n[i] = a.n[i] > b.n[i] ? a.n[i] : b.n[i];
+        na[i] = a.n[i];
+        nb[i] = b.n[i];
+    }
+    Nest x = nest(sa, n, d), y = x;  // one order of dimensions for both
+    if (!x.nested) return true;
+    // x and y have the larger count of each dimension; put their own back
+    for (int j = 0; j < x.dims; ++j)
+        for (int i = 0; i < 3; ++i)
+            if (n[i] > 1 && sa[i] == x.stride[j]) {
+                x.n[j] = na[i];
+                y.n[j] = nb[i];
+            }
+    return share(x, y, x.dims, bytes / es);
+}
+
+// The same elements in the same order.
+bool same_view(const HeadView &a, const HeadView &b)
+{
+    for (int i = 0; i < 3; ++i)
+        if (a.n[i] != b.n[i] || (a.n[i] > 1 && a.st[i] != b.st[i])) return false;
+    return a.p == b.p;
+}
 
 }  // namespace
 
@@ -513,14 +603,23 @@ ttt_status ttt_rope(const ttt_rope_desc *desc, const void *q, const void *k, con
         }
     }
     if (D.rot > 0 && (!aligned(table, 8) || (positions && !aligned(positions, 8)))) return TTT_ERR_ALIGN;
+    const size_t table_bytes = (size_t)D.table_rows * D.rot * 4,
+                 pos_bytes = positions ? 8 * (size_t)(D.positions_batch_stride * (D.B - 1) + D.T) : 0;
+    HeadView vi[3], vo[3];
+    for (int i = 0; i < 3; ++i) {
+        if (!in[i]) continue;
+        vi[i] = {in[i], {a.in_stride[i][0], a.in_stride[i][1], a.in_stride[i][2]}, {D.B, H[i], D.T}};
+        vo[i] = {out[i], {a.out_stride[i][0], a.out_stride[i][1], a.out_stride[i][2]}, {D.B, H[i], D.T}};
+        if (!nest(vo[i].st, vo[i].n, D.d).nested) return TTT_ERR_ARG;
+        const size_t bytes = es * span(vo[i].st, D.B, H[i], D.T, D.d);
+        if (D.rot > 0 && (overlaps(out[i], bytes, table, table_bytes) || (positions && overlaps(out[i], bytes, positions, pos_bytes))))
+            return TTT_ERR_ARG;
+    }
     for (int i = 0; i < 3; ++i)
         for (int j = 0; j < 3; ++j) {
             if (!in[i] || !in[j]) continue;
-            const bool apart = !overlaps(in[i], es * span(a.in_stride[i], D.B, H[i], D.T, D.d), out[j],
-                                         es * span(a.out_stride[j], D.B, H[j], D.T, D.d));
-            if (apart) continue;
-            if (!same_strides(a.in_stride[i], a.out_stride[j]) || (i == j ? in[i] != out[j] : in[i] == out[j]))
-                return TTT_ERR_ARG;
+            if (!(i == j && same_view(vi[i], vo[i])) && shares_memory(vi[i], vo[j], D.d, es)) return TTT_ERR_ARG;
+            if (i < j && shares_memory(vo[i], vo[j], D.d, es)) return TTT_ERR_ARG;
         }
     a.B = D.B;
     a.T = D.T;
