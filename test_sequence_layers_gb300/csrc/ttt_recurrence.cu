@@ -309,9 +309,11 @@ struct Ragged {
             const int off = (int)(reinterpret_cast<uintptr_t>(q) & 15), size = s + r < n ? min(max(have + off, 0), 16) : 0;
             const char *from = q - off;
             if (head && from < reinterpret_cast<const char *>(base)) {
-                for (int e = 0; e < size; e += (int)sizeof(T)) {
+                // (and zeros behind them: tokens past the end come here too where the rows of a
+                // broadcast tensor all begin at its first byte)
+                for (int e = 0; e < 16; e += (int)sizeof(T)) {
                     const T *v = reinterpret_cast<const T *>(from + e);
-                    if (v >= base) *reinterpret_cast<T *>(dst + e) = *v;
+                    *reinterpret_cast<T *>(dst + e) = v >= base && e < size ? *v : T(0.f);
                 }
             } else {
                 copy_async16_part(dst, from, size);
