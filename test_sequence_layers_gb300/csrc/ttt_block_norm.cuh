@@ -197,26 +197,28 @@ __device__ __forceinline__ float2 logistic(float2 g)
     return make_float2(rcp_approx(d.x), rcp_approx(d.y));
 }
 
-// Phi(g) and the normal density.  For bf16 tensors Phi is 1 - w or w with w =
-// poly(1 / (1 + 0.3275911 |g| / sqrt 2)) exp(-g^2 / 2) / 2 (Abramowitz & Stegun 7.1.26, error
-// below 1e-7, far below the output's rounding; the exponential is the density's too); for
-// fp32 tensors CUDA's normcdff.
+// Phi(g) and the normal density.  For bf16 tensors w = Phi(-|g|) = t P(t) exp(-g^2 / 2) with
+// t = 1 / (1 + 0.375 |g|) (the form of Hastings, Approximations for Digital Computers; the
+// exponential is the density's too), and Phi is w or 1 - w.  P, of degree 4 with P(1) = 1/2,
+// minimises the largest RELATIVE error of w over |g| <= 14 (linear programming): 3.5e-5 in fp32
+// over every bf16 g there, 2^-5 of the output's rounding, far into the tail that GELU
+// keeps.  For fp32 tensors CUDA's normcdff.
 template <typename T> __device__ __forceinline__ float2 gelu_cdf(float2 g, float2 &density)
 {
     if constexpr (sizeof(T) == 2) {
         const float2 m = make_float2(fabsf(g.x), fabsf(g.y));
-        const float2 d = __ffma2_rn(m, both(0.3275911f * 0.70710678118654752f), both(1.f));
+        const float2 d = __ffma2_rn(m, both(0.375f), both(1.f));
         const float2 t = make_float2(rcp_approx(d.x), rcp_approx(d.y));
         const float2 q = __fmul2_rn(__fmul2_rn(g, g), both(-0.5f * 1.4426950408889634f));
         const float2 e = make_float2(exp2_approx(q.x), exp2_approx(q.y));
-        float2 w = __ffma2_rn(t, both(0.5f * 1.061405429f), both(-0.5f * 1.453152027f));
-        w = __ffma2_rn(t, w, both(0.5f * 1.421413741f));
-        w = __ffma2_rn(t, w, both(-0.5f * 0.284496736f));
-        w = __ffma2_rn(t, w, both(0.5f * 0.254829592f));
+        float2 w = __ffma2_rn(t, both(-0.090480238f), both(0.199919820f));
+        w = __ffma2_rn(t, w, both(0.0838441253f));
+        w = __ffma2_rn(t, w, both(0.157645911f));
+        w = __ffma2_rn(t, w, both(0.149070382f));
         w = __fmul2_rn(__fmul2_rn(t, w), e);
         density = __fmul2_rn(e, both(0.3989422804014327f));
-        const float2 h = __ffma2_rn(w, both(-1.f), both(0.5f));
-        return __fadd2_rn(make_float2(copysignf(h.x, g.x), copysignf(h.y, g.y)), both(0.5f));
+        const float2 h = __ffma2_rn(w, both(-1.f), both(1.f));
+        return make_float2(g.x < 0.f ? w.x : h.x, g.y < 0.f ? w.y : h.y);
     } else {
         density = make_float2(expf(-0.5f * g.x * g.x) * 0.3989422804014327f, expf(-0.5f * g.y * g.y) * 0.3989422804014327f);
         return make_float2(normcdff(g.x), normcdff(g.y));
