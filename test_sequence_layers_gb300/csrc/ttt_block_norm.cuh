@@ -189,11 +189,19 @@ __device__ __forceinline__ float rcp_approx(float x)
     return y;
 }
 
-// 1 / (1 + exp(-g)); 0 and 1 where exp(-g) leaves the range
-__device__ __forceinline__ float2 logistic(float2 g)
+// 1 / (1 + exp(-g)); 0 and 1 where exp(-g) leaves the range.  bf16 tensors: one ex2 of a rounded
+// product, off by |g| 2^-24 of itself, far below the output's rounding.  fp32 tensors: CUDA's
+// expf.
+template <typename T> __device__ __forceinline__ float2 logistic(float2 g)
 {
-    const float2 t = __fmul2_rn(g, both(-1.4426950408889634f));
-    const float2 d = __fadd2_rn(make_float2(exp2_approx(t.x), exp2_approx(t.y)), both(1.f));
+    float2 e;
+    if constexpr (sizeof(T) == 2) {
+        const float2 t = __fmul2_rn(g, both(-1.4426950408889634f));
+        e = make_float2(exp2_approx(t.x), exp2_approx(t.y));
+    } else {
+        e = make_float2(expf(-g.x), expf(-g.y));
+    }
+    const float2 d = __fadd2_rn(e, both(1.f));
     return make_float2(rcp_approx(d.x), rcp_approx(d.y));
 }
 
@@ -231,7 +239,7 @@ template <typename T> __device__ __forceinline__ V8 act_value(int act, const V8 
     V8 r;
     if (act == 2) {
 #pragma unroll
-        for (int i = 0; i < kP; ++i) r.p[i] = __fmul2_rn(g.p[i], logistic(g.p[i]));
+        for (int i = 0; i < kP; ++i) r.p[i] = __fmul2_rn(g.p[i], logistic<T>(g.p[i]));
     } else if (act == 3) {
 #pragma unroll
         for (int i = 0; i < kP; ++i) {
@@ -240,7 +248,7 @@ template <typename T> __device__ __forceinline__ V8 act_value(int act, const V8 
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < kP; ++i) r.p[i] = logistic(g.p[i]);
+        for (int i = 0; i < kP; ++i) r.p[i] = logistic<T>(g.p[i]);
     }
     return r;
 }
@@ -251,7 +259,7 @@ template <typename T> __device__ __forceinline__ void act_and_slope(int act, con
     if (act == 2) {
 #pragma unroll
         for (int i = 0; i < kP; ++i) {
-            const float2 s = logistic(g.p[i]);
+            const float2 s = logistic<T>(g.p[i]);
             a.p[i] = __fmul2_rn(g.p[i], s);
             da.p[i] = __ffma2_rn(a.p[i], __ffma2_rn(s, both(-1.f), both(1.f)), s);
         }
@@ -266,7 +274,7 @@ template <typename T> __device__ __forceinline__ void act_and_slope(int act, con
     } else {
 #pragma unroll
         for (int i = 0; i < kP; ++i) {
-            a.p[i] = logistic(g.p[i]);
+            a.p[i] = logistic<T>(g.p[i]);
             da.p[i] = __fmul2_rn(a.p[i], __ffma2_rn(a.p[i], both(-1.f), both(1.f)));
         }
     }
