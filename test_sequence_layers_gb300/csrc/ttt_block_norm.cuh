@@ -191,10 +191,9 @@ __device__ __forceinline__ float rcp_approx(float x)
 
 // 1 / (1 + exp(-g)); 0 and 1 where exp(-g) leaves the range.  bf16 tensors: one ex2 of a rounded
 // product, off by |g| 2^-24 of itself, far below the output's rounding.  fp32 tensors: CUDA's
-// expf.
-template <typename T> __device__ __forceinline__ float2 logistic(float2 g)
+// expf.  e: exp(-g).
+template <typename T> __device__ __forceinline__ float2 logistic(float2 g, float2 &e)
 {
-    float2 e;
     if constexpr (sizeof(T) == 2) {
         const float2 t = __fmul2_rn(g, both(-1.4426950408889634f));
         e = make_float2(exp2_approx(t.x), exp2_approx(t.y));
@@ -203,6 +202,11 @@ template <typename T> __device__ __forceinline__ float2 logistic(float2 g)
     }
     const float2 d = __fadd2_rn(e, both(1.f));
     return make_float2(rcp_approx(d.x), rcp_approx(d.y));
+}
+template <typename T> __device__ __forceinline__ float2 logistic(float2 g)
+{
+    float2 e;
+    return logistic<T>(g, e);
 }
 
 // Phi(g) and the normal density.  For bf16 tensors w = Phi(-|g|) = t P(t) exp(-g^2 / 2) with
@@ -274,8 +278,11 @@ template <typename T> __device__ __forceinline__ void act_and_slope(int act, con
     } else {
 #pragma unroll
         for (int i = 0; i < kP; ++i) {
-            a.p[i] = logistic<T>(g.p[i]);
-            da.p[i] = __fmul2_rn(a.p[i], __ffma2_rn(a.p[i], both(-1.f), both(1.f)));
+            float2 e;
+            const float2 s = logistic<T>(g.p[i], e), c = __ffma2_rn(s, both(-1.f), both(1.f)), es = __fmul2_rn(e, s);
+            a.p[i] = s;
+            // 1 - s, which cancels for large g and is exp(-g) s there
+            da.p[i] = __fmul2_rn(s, make_float2(g.p[i].x > 0.f ? es.x : c.x, g.p[i].y > 0.f ? es.y : c.y));
         }
     }
 }
