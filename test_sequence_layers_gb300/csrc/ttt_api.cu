@@ -84,6 +84,33 @@ void *noalloc_scratch()
 
 }  // namespace
 
+bool ttt::allow_shared(const void *kernel, int bytes)
+{
+    // what is known of each kernel and device, by open addressing; past its size the
+    // limit is set anew each time, to the same value
+    static std::mutex mu;
+    static struct {
+        const void *kernel;
+        int dev, most;
+    } memo[1024];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    std::lock_guard<std::mutex> lock(mu);
+    unsigned at = (unsigned)((reinterpret_cast<uintptr_t>(kernel) >> 4) * 31 + dev) % 1024;
+    int probes = 0;
+    for (; probes < 1024 && memo[at].kernel; ++probes, at = (at + 1) % 1024)
+        if (memo[at].kernel == kernel && memo[at].dev == dev) return bytes <= memo[at].most;
+    int most = 0;
+    cudaFuncAttributes attr;
+    if (cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
+        cudaFuncGetAttributes(&attr, kernel) != cudaSuccess)
+        return false;
+    most -= (int)attr.sharedSizeBytes;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess) return false;
+    if (probes < 1024) memo[at] = {kernel, dev, most};
+    return bytes <= most;
+}
+
 // q/k/v viewed as a 3-D tensor [B*H][T][d] of bf16; box = `rows` tokens x min(d,64)
 // features, swizzled to the box row length so that ldmatrix is conflict-free.
 bool ttt::encode_token_map(CUtensorMap *m, const void *ptr, int BH, int T, int d, int rows, int cols)

@@ -977,9 +977,8 @@ template <typename P> int resident(void (*kernel)(P), int threads, int smem)
 template <typename P>
 int launch(void (*kernel)(P), const P &p, const NormShape &s, int limit, int smem, cudaStream_t st, int *blocks)
 {
-    if (smem > 40 * 1024 &&  // with the static part, past the 48 KB that need no asking
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return -4;
+    // with the static part, past the 48 KB that need no asking
+    if (smem > 40 * 1024 && !allow_shared(kernel, smem)) return -4;
     const long long per = s.block ? 1 : s.threads / s.lanes, groups = (p.rows + per - 1) / per;
     long long n = (long long)kSMs * resident(kernel, s.threads, smem);
     if (limit > 0 && n > limit) n = limit;

@@ -176,6 +176,15 @@ int launch_linear_seqpar_serial(const LinearArgs &a, const SeqparPlan &pl, void 
 size_t dwconv_smem(int hh, int ww, int d, int es);
 int launch_dwconv(const DwconvArgs &a);
 int launch_eta_gate(const GateArgs &a);  // H <= 64; -2 otherwise
+// May this kernel be launched with that much dynamic shared memory on the current device?
+// Its limit is raised once, to the most the device has, and never lowered: host threads
+// that launch the same kernel with other sizes do not disturb each other.
+bool allow_shared(const void *kernel, int bytes);
+template <typename... KArgs> bool allow_shared(void (*kernel)(KArgs...), int bytes)
+{
+    return allow_shared(reinterpret_cast<const void *>(kernel), bytes);
+}
+
 int launch_rope(const RopeArgs &a);
 int launch_recurrence(const RecurArgs &a, bool backward);
 int launch_block_norm_fwd(const BlockNormArgs &a);

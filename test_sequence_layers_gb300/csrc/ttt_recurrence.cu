@@ -890,9 +890,7 @@ bool cluster_config(void (*kernel)(KArgs...), int cluster, int blocks, int smem,
 {
     if (cluster > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
         return false;
-    if (smem > 40 * 1024 &&
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return false;
+    if (smem > 40 * 1024 && !allow_shared(kernel, smem)) return false;
     cfg = {};
     cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(32 * kW);
