@@ -45,6 +45,15 @@ EncodeTiledFn encode_fn()
             q == cudaDriverEntryPointSuccess)
             fn = reinterpret_cast<EncodeTiledFn>(ptr);
     });
+    // The driver call wants this thread to have a context: a host thread whose first CUDA
+    // work is a call of this library gets its device's here.
+    static thread_local int ready = -1;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+    if (dev != ready) {
+        if (cudaSetDevice(dev) != cudaSuccess) return nullptr;
+        ready = dev;
+    }
     return fn;
 }
 
