@@ -418,7 +418,7 @@ template <typename TIO, int NB, int DC>
 int launch_nb(const CUtensorMap &tmk, const CUtensorMap &tmq, const DwParams &p, size_t smem, cudaStream_t st)
 {
     auto kern = ttt_dwconv_kernel<TIO, NB, DC>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return -4;
+    if (!allow_shared(kern, (int)smem)) return -4;
     int dev = 0, sms = 0, per_sm = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, dw_threads<NB>, smem) != cudaSuccess || per_sm < 1)

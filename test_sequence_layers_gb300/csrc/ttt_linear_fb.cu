@@ -236,8 +236,7 @@ int launch_linear_fb(const LinearArgs &a)
     CUtensorMap maps[3];
     if (!encode_qkv(maps, a.q, a.k, a.v, a.B * a.H, a.T, a.d, 64)) return -4;
     const int smem = C::smem_bytes((a.T + 63) / 64);
-    if (cudaFuncSetAttribute(ttt_linear_fb_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return -4;
+    if (!allow_shared(ttt_linear_fb_kernel, smem)) return -4;
     FbParams p;
     p.H = a.H;
     p.T = a.T;

@@ -164,9 +164,7 @@ int launch_linear_f32(const LinearArgs &a)
 {
     const int D = a.d;
     const size_t smem = sizeof(float) * (2 * D * D + 3 * D + kTile * (3 * D + 1));
-    if (cudaFuncSetAttribute(ttt_linear_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem) != cudaSuccess)
-        return -4;
+    if (!allow_shared(ttt_linear_f32_kernel, (int)smem)) return -4;
     LinF32Params p;
     p.H = a.H;
     p.T = a.T;
@@ -382,9 +380,7 @@ int launch_mlp_f32(const MlpArgs &a)
 {
     if (!mlp_f32_fits(a.d, a.m)) return -2;
     const size_t smem = mlp_f32_floats(a.d, a.m) * sizeof(float);
-    if (cudaFuncSetAttribute(ttt_mlp_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem) != cudaSuccess)
-        return -4;
+    if (!allow_shared(ttt_mlp_f32_kernel, (int)smem)) return -4;
     MlpF32Params p;
     p.H = a.H;
     p.T = a.T;

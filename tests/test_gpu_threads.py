@@ -102,3 +102,25 @@ def test_recurrence_of_two_shapes(monkeypatch):
         x, f = (torch.randn(B, T, C, device="cuda").to(BF) for _ in range(2))
         return _Recorded(monkeypatch, abi.ttt_recurrence_fwd, x, f)
     _in_threads([call(1, 2048, 64), call(1, 128, 64)])
+
+
+@pytest.mark.parametrize("kind", ["linear_f32", "mlp_f32", "full_batch", "dwconv"])
+def test_layer_of_two_shapes(kind, monkeypatch):
+    def call(n):
+        r = lambda *s: 0.1 * torch.randn(*s, device="cuda")
+        if kind == "linear_f32":
+            d = (128, 32)[n]
+            q, W = r(1, 2, 16, d), r(2, d, d)
+            return _Recorded(monkeypatch, abi.ttt_linear_fwd, q, q, q, W, 16)
+        if kind == "mlp_f32":
+            d, m = ((64, 128), (32, 64))[n]
+            q, P = r(1, 2, 16, d), (r(2, d, m), r(2, m), r(2, m, d), r(2, d))
+            return _Recorded(monkeypatch, abi.ttt_mlp_fwd, q, q, q, *P, 16, want_W=False)
+        if kind == "full_batch":
+            T = (256, 64)[n]
+            q, W = r(1, 2, T, 64).to(BF), r(2, 64, 64)
+            return _Recorded(monkeypatch, abi.ttt_linear_fwd, q, q, q, W, T, causal=False, epochs=2)
+        N = (14, 8)[n]
+        q, W = r(1, 2, N * N, 64).to(BF), r(2, 9, 64)
+        return _Recorded(monkeypatch, abi.ttt_dwconv_fwd, q, q, q, W, N, N)
+    _in_threads([call(0), call(1)])
