@@ -459,7 +459,8 @@ ttt_status ttt_recurrence_bwd(const ttt_recurrence_desc *desc, const void *dh, c
 
 /* Waits for `stream`, then reports (and clears) a kernel wait timeout
  * (TTT_ERR_TIMEOUT) or a position out of range (TTT_ERR_RANGE) recorded on the current
- * device, or a CUDA error seen while waiting. */
+ * device, or a CUDA error seen while waiting.  Of both, the timeout is reported first and
+ * the position by the next call. */
 ttt_status ttt_sync_status(void *stream);
 
 /* Static description of a status code. */

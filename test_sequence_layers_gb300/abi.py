@@ -798,7 +798,8 @@ def ttt_recurrence_bwd(dh, x, f, states, mode="mix", reset=None, dh_last=None, d
 
 
 def ttt_sync_status(stream=None):
-    """Waits for the stream; raises TTTError if a kernel wait timed out."""
+    """Waits for the stream; raises TTTError if a kernel wait timed out (code -5) or, reported
+    after that, ttt_rope met a position outside its table (-7)."""
     rc = lib().ttt_sync_status(_stream(stream))
     if rc != 0:
         raise TTTError("ttt_sync_status", rc)

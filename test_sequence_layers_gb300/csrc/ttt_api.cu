@@ -12,9 +12,10 @@
 #include "ttt_internal.h"
 #include "ttt_vec.cuh"
 
-// Status word written by kernels whose bounded on-chip wait ran out (one per
-// device: every device that loads the library has its own copy).
-__device__ int g_ttt_status;
+// Status words (one pair per device: every device that loads the library has its own
+// copy): [0] written by kernels whose bounded on-chip wait ran out, [1] by ttt_rope for
+// a position outside its table.  Neither hides the other.
+__device__ int g_ttt_status[2];
 
 // Fixed scratch of ttt_linear_fwd_seqpar_noalloc (affine maps and segment start
 // weights of a split run).  Every device that loads the library holds it until the
@@ -57,7 +58,7 @@ EncodeTiledFn encode_fn()
     return fn;
 }
 
-// Address of this device's status word (looked up once per device).
+// Address of this device's status words (looked up once per device).
 int *status_word()
 {
     static std::mutex mu;
@@ -678,9 +679,10 @@ ttt_status ttt_rope(const ttt_rope_desc *desc, const void *q, const void *k, con
     a.v_out = v_out;
     a.table = table;
     a.positions = positions;
-    a.status = status_word();
+    int *const status = status_word();
+    if (!status) return TTT_ERR_LAUNCH;
+    a.range_status = status + 1;
     a.stream = static_cast<cudaStream_t>(stream);
-    if (!a.status) return TTT_ERR_LAUNCH;
     const int rc = ttt::launch_rope(a);
     if (rc == 0) g_launches.fetch_add(1, std::memory_order_relaxed);
     return code(rc);
@@ -994,13 +996,14 @@ ttt_status ttt_recurrence_bwd(const ttt_recurrence_desc *desc, const void *dh, c
 ttt_status ttt_sync_status(void *stream)
 {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return TTT_ERR_LAUNCH;
-    int v = 0;
-    if (cudaMemcpyFromSymbol(&v, g_ttt_status, sizeof(int)) != cudaSuccess) return TTT_ERR_LAUNCH;
-    if (v != 0) {
-        const int zero = 0;
-        cudaMemcpyToSymbol(g_ttt_status, &zero, sizeof(int));
-        return v == ttt::kSitePositionRange ? TTT_ERR_RANGE : TTT_ERR_TIMEOUT;
-    }
+    int v[2] = {0, 0};
+    if (cudaMemcpyFromSymbol(v, g_ttt_status, sizeof(v)) != cudaSuccess) return TTT_ERR_LAUNCH;
+    for (int i = 0; i < 2; ++i)
+        if (v[i] != 0) {
+            const int zero = 0;
+            cudaMemcpyToSymbol(g_ttt_status, &zero, sizeof(int), i * sizeof(int));
+            return i == 0 ? TTT_ERR_TIMEOUT : TTT_ERR_RANGE;
+        }
     return TTT_OK;
 }
 

@@ -72,7 +72,7 @@ struct RopeArgs {
     long long in_stride[3][3], out_stride[3][3];  // [q, k, v][batch, head, token], elements
     const float *table;          // [table_rows][rot/2][2] cos, sin
     const long long *positions;  // or null: pos0 + t
-    int *status;                 // device status word (positions out of range)
+    int *range_status;           // device status word of positions out of range
     cudaStream_t stream;
 };
 

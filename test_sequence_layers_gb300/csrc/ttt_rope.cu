@@ -32,7 +32,7 @@ struct RopeParams {
     long long ntok, pos0, pos_bstride;
     const long long *positions;
     const float *table;
-    int *status;
+    int *range_status;
 };
 
 template <typename T, int V, bool INTER, bool INV>
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(1024) ttt_rope_kernel(const __grid_constant__ 
         if (p.period > 0 && !neg)
             pos = pos <= 0x7fffffffLL ? (long long)((unsigned)pos % (unsigned)p.period) : pos % p.period;
         if (neg || pos >= p.rows) {
-            atomicCAS(p.status, 0, kSitePositionRange);
+            *p.range_status = 1;
 #pragma unroll
             for (int j = 0; j < V; ++j) cs[j] = sn[j] = __int_as_float(0x7fffffff);
         } else {
@@ -187,7 +187,7 @@ int launch_rope(const RopeArgs &a)
     p.pos_bstride = a.pos_bstride;
     p.positions = a.positions;
     p.table = a.table;
-    p.status = a.status;
+    p.range_status = a.range_status;
     p.units = a.rot / 2 / V + (a.d - a.rot + 2 * V - 1) / (2 * V);
     p.tok_per_block = p.units >= kRopeThreads ? 1 : kRopeThreads / p.units;
     if ((long long)p.tok_per_block > p.ntok) p.tok_per_block = (int)p.ntok;

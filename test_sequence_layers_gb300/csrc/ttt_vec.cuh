@@ -9,10 +9,6 @@
 
 namespace ttt {
 
-// Code recorded in the status word by ttt_rope for a position outside its table (the
-// codes of timed-out waits lie below it).
-constexpr int kSitePositionRange = 64;
-
 template <int BYTES> struct RawOf;
 template <> struct RawOf<2> { using type = unsigned short; };
 template <> struct RawOf<4> { using type = unsigned int; };
