@@ -478,7 +478,9 @@ unsigned long long ttt_launch_count(void);
  * that nothing arrives at, bounded by ns nanoseconds: the wait runs out, the kernel
  * records TTT_ERR_TIMEOUT in the device status word, skips its products (outputs
  * undefined), still waits for its own copies in flight and frees its tensor memory,
- * and ttt_sync_status() reports the timeout.  ns = 0 restores normal operation.  The
+ * and ttt_sync_status() reports the timeout.  So do the recurrence's tile kernels (more than
+ * 16 tokens): each cluster's last block gives up first, then its other blocks, which
+ * wait for it.  ns = 0 restores normal operation.  The
  * setting is process-wide (read at each launch); other kernels ignore it.
  */
 void ttt_debug_wait_limit(unsigned long long ns);

@@ -811,6 +811,6 @@ def ttt_launch_count() -> int:
 
 def ttt_debug_wait_limit(ns: int) -> None:
     """Test hook of the timeout path: ns > 0 makes the first consumer wait of the
-    b = 16 and full-batch TTT-Linear kernels run out after ns nanoseconds (see
-    include/ttt.h); 0 restores normal operation."""
+    b = 16 and full-batch TTT-Linear kernels, of the full-batch TTT-MLP kernel and of the
+    recurrence run out after ns nanoseconds (see include/ttt.h); 0 restores normal operation."""
     lib().ttt_debug_wait_limit(int(ns))

@@ -953,6 +953,7 @@ ttt_status ttt_recurrence_fwd(const ttt_recurrence_desc *desc, const void *x, co
     a.states = states;
     a.status = status_word();
     if (!a.status) return TTT_ERR_LAUNCH;
+    a.test_stall_ns = g_test_stall_ns.load(std::memory_order_relaxed);
     const int rc = ttt::launch_recurrence(a, false);
     if (rc == 0) g_launches.fetch_add(1, std::memory_order_relaxed);
     return code(rc);
@@ -988,6 +989,7 @@ ttt_status ttt_recurrence_bwd(const ttt_recurrence_desc *desc, const void *dh, c
     a.dh0 = dh0;
     a.status = status_word();
     if (!a.status) return TTT_ERR_LAUNCH;
+    a.test_stall_ns = g_test_stall_ns.load(std::memory_order_relaxed);
     const int rc = ttt::launch_recurrence(a, true);
     if (rc == 0) g_launches.fetch_add(1, std::memory_order_relaxed);
     return code(rc);

@@ -103,6 +103,7 @@ struct RecurArgs {
     void *h, *dx, *df;
     float *h_last, *states, *dh0;  // states: written by the forward, read by the backward
     int *status;                   // device status word (timeouts)
+    unsigned long long test_stall_ns = 0;
     cudaStream_t stream;
 };
 

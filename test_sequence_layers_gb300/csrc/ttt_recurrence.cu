@@ -30,6 +30,7 @@ struct RecurParams {
     int B, T, C, chunks;
     int cluster, cblocks;  // tile kernels: blocks of a cluster, channel blocks of a batch entry
     int *status;           // device status word (timeouts)
+    unsigned long long test_stall_ns;  // > 0: the timeout test (see stalled())
 };
 
 __device__ __forceinline__ float exp2_approx(float x)
@@ -384,6 +385,7 @@ template <int N, bool BWD> struct TileShared {
     int wcut[2][kW];
     int tcut[2][kMaxCluster];
     unsigned long long full[2], joined[2];  // mbarriers: a stage's copies, the cluster's totals
+    unsigned long long dead;                // one that nothing arrives at (timeout test)
 };
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -394,6 +396,7 @@ __device__ __forceinline__ uint32_t cluster_rank()
 }
 __device__ __forceinline__ void cluster_barrier()
 {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -427,7 +430,7 @@ __device__ __forceinline__ void send(uint32_t dst, uint32_t bar, int v)
 // goes through all of them, and the value before this block's tile is returned.
 template <int N, bool RESET, bool BWD>
 __device__ __forceinline__ F<N> join_blocks(TileShared<N, BWD> &sh, Map<N> *totals, const Map<N> &total, bool cut, F<N> &carry,
-                                            int P, int rank, int buf, int phase, int *status, bool &ok)
+                                            int P, int rank, int buf, int phase, const RecurParams &p, bool &ok)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t bar = smem_u32(&sh.joined[buf]);
@@ -438,7 +441,7 @@ __device__ __forceinline__ F<N> join_blocks(TileShared<N, BWD> &sh, Map<N> *tota
         send(remote(smem_u32(totals + rank * 32), i), rbar, total);
         if (RESET && lane == 0) send(remote(smem_u32(&sh.tcut[buf][rank]), i), rbar, (int)cut);
     }
-    ok &= mbar_wait(bar, phase, status, kSiteStage);
+    ok &= mbar_wait(bar, phase, p.status, kSiteStage, p.test_stall_ns ? p.test_stall_ns : kWaitLimitNs);
     F<N> before = carry;
     for (int i = 0; i < P; ++i) {
         carry = apply(totals[i * 32], carry, RESET && sh.tcut[buf][i]);
@@ -465,8 +468,21 @@ __device__ __forceinline__ unsigned reset_bits(const unsigned char *reset, int t
     return __ballot_sync(0xffffffffu, lane < n && reset[t0 + lane] != 0);
 }
 
-// A block that gave up waiting (never expected) lets its copies land, then leaves with
-// its cluster.
+// The timeout test: a cluster's last block gives up first, on a barrier that nothing arrives
+// at, and the others as it does not send its totals.
+template <typename S> __device__ __forceinline__ bool stalled(const S &sh, const RecurParams &p, int rank)
+{
+    return p.test_stall_ns && rank == p.cluster - 1 && !mbar_wait(smem_u32(&sh.dead), 0, p.status, kSiteStage, p.test_stall_ns);
+}
+
+// The way out of a block that gave up waiting (never expected): its own copies land (drain),
+// its cluster's blocks meet, having sent all that they will, and what they sent to it has a
+// hundred microseconds to land, as nothing counts it any more.
+__device__ __forceinline__ void settle()
+{
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 100000) __nanosleep(1000);
+}
 __device__ __forceinline__ void drain(unsigned long long *full, int rounds_issued, int stages, int *status)
 {
     for (int r = max(0, rounds_issued - stages); r < rounds_issued; ++r)
@@ -532,6 +548,7 @@ __global__ void __launch_bounds__(32 * kW, 2)
             mbar_init(smem_u32(&sh.full[i]), 1);
             mbar_init(smem_u32(&sh.joined[i]), 1);
         }
+        mbar_init(smem_u32(&sh.dead), 1);
         fence_barrier_init();
         if (TMA)
             for (int i = 0; i < kFwdStages && i < rounds; ++i) issue(i);
@@ -549,7 +566,7 @@ __global__ void __launch_bounds__(32 * kW, 2)
     if (!TMA) copy(0);
     __syncthreads();
     if (P > 1) cluster_barrier();  // every block runs, its barriers set, before it is written to
-    bool ok = true;
+    bool ok = !stalled(sh, p, rank);
     int round = 0;
     for (; round < rounds; ++round, t0 += P * kRecurChunk) {
         const int buf = round & 1;
@@ -612,7 +629,7 @@ __global__ void __launch_bounds__(32 * kW, 2)
                 total.a = mul(w.a, total.a);
                 cut |= ci;
             }
-            st = join_blocks<N, RESET>(sh, totals, total, cut, carry, P, rank, buf, (round >> 1) & 1, p.status, ok);
+            st = join_blocks<N, RESET>(sh, totals, total, cut, carry, P, rank, buf, (round >> 1) & 1, p, ok);
         }
         if (warp == 0 && p.states && on && n > 0)
             put_part<N, TMA>(p.states + ((size_t)b * p.chunks + t0 / kRecurChunk) * p.C, c, p.C, st);
@@ -655,7 +672,10 @@ __global__ void __launch_bounds__(32 * kW, 2)
     if (TMA && lane == 0) tma_store_read();
     if (!TMA) copy_wait<0>();  // a block that gave up has some in flight
     if (!ok && TMA && threadIdx.x == 0) drain(sh.full, min(rounds, round + kFwdStages), kFwdStages, p.status);
-    if (P > 1) cluster_barrier();  // no block leaves while another may write to it
+    if (P > 1) {
+        cluster_barrier();  // no block leaves while another may write to it
+        if (!ok) settle();
+    }
     if (ok && p.h_last && on && rank == 0 && warp == 0) put_part<N, TMA>(p.h_last + bC, c, p.C, carry);
 }
 
@@ -700,6 +720,7 @@ __global__ void __launch_bounds__(32 * kW, 2)
             mbar_init(smem_u32(&sh.full[i]), 1);
             mbar_init(smem_u32(&sh.joined[i]), 1);
         }
+        mbar_init(smem_u32(&sh.dead), 1);
         fence_barrier_init();
         if (TMA)
             for (int i = 0; i < kBwdStages && i < rounds; ++i) issue(i);
@@ -722,7 +743,7 @@ __global__ void __launch_bounds__(32 * kW, 2)
     fetch(last);
     __syncthreads();
     if (P > 1) cluster_barrier();
-    bool ok = true;
+    bool ok = !stalled(sh, p, rank);
     int round = 0;
     for (; round < rounds; ++round) {
         const int tile = last - round * P, t0 = tile * kRecurChunk + warp * kS, buf = round & 1;
@@ -797,7 +818,7 @@ __global__ void __launch_bounds__(32 * kW, 2)
                 total.a = mul(w.a, total.a);
                 cut |= ci;
             }
-            st = join_blocks<N, RESET>(sh, totals, total, cut, carry, P, rank, buf, (round >> 1) & 1, p.status, ok);
+            st = join_blocks<N, RESET>(sh, totals, total, cut, carry, P, rank, buf, (round >> 1) & 1, p, ok);
         }
 #pragma unroll
         for (int i = 0; i < kW - 1; ++i)
@@ -851,7 +872,10 @@ __global__ void __launch_bounds__(32 * kW, 2)
     if (TMA && lane == 0) tma_store_read();
     if (!TMA) copy_wait<0>();  // a block that gave up has some in flight
     if (!ok && TMA && threadIdx.x == 0) drain(sh.full, min(rounds, max(round + 1, kBwdStages)), kBwdStages, p.status);
-    if (P > 1) cluster_barrier();
+    if (P > 1) {
+        cluster_barrier();
+        if (!ok) settle();
+    }
     if (ok && p.dh0 && on && rank == 0 && warp == 0) put_part<N, TMA>(p.dh0 + bC, c, p.C, carry);
 }
 
@@ -877,6 +901,7 @@ RecurParams params_of(const RecurArgs &a)
         p.ds[i] = a.ds[i];
     }
     p.status = a.status;
+    p.test_stall_ns = a.test_stall_ns;
     p.B = a.B;
     p.T = a.T;
     p.C = a.C;
