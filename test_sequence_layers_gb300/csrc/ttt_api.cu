@@ -616,7 +616,7 @@ ttt_status ttt_rope(const ttt_rope_desc *desc, const void *q, const void *k, con
     if (D.io_dtype != TTT_F32 && D.io_dtype != TTT_BF16) return TTT_ERR_ARG;
     if (D.table_rows < 0 || D.period < 0 || D.period > D.table_rows || D.pos0 < 0 || D.pos0 > (1LL << 62) || D.positions_batch_stride < 0)
         return TTT_ERR_ARG;
-    if (D.d > 1024 || (long long)D.B * D.T > 0x7fffffffLL) return TTT_ERR_UNSUPPORTED;
+    if (D.d > 1024 || (long long)D.B * D.T > 0x7fffffffLL || D.Hq + 2LL * D.Hk > 0x7fff0000LL) return TTT_ERR_UNSUPPORTED;
     if (D.B == 0 || D.T == 0) return TTT_OK;
     if (!q || !q_out || (k && !k_out) || (v && !v_out) || ((k || v) && D.Hk < 1)) return TTT_ERR_ARG;
     if (D.rot > 0 && !table) return TTT_ERR_ARG;

@@ -197,6 +197,9 @@ int launch_rope(const RopeArgs &a)
     if (heads == 0) return 0;
     const long long fill = p.ntok * p.units * heads / (2048LL * kSMs);
     p.heads_per_thread = (int)(fill < 1 ? 1 : fill > heads ? heads : fill);
+    // a grid has 65535 rows of blocks at most
+    const int least = (heads + 65534) / 65535;
+    if (p.heads_per_thread < least) p.heads_per_thread = least;
     if (a.bf16) {
         switch (V) {
         case 8: return launch_rope_v<__nv_bfloat16, 8>(p, a);
