@@ -209,28 +209,50 @@ template <typename T> __device__ __forceinline__ float2 logistic(float2 g)
     return logistic<T>(g, e);
 }
 
-// Phi(g) and the normal density.  For bf16 tensors w = Phi(-|g|) = t P(t) exp(-g^2 / 2) with
-// t = 1 / (1 + 0.375 |g|) (the form of Hastings, Approximations for Digital Computers; the
-// exponential is the density's too), and Phi is w or 1 - w.  P, of degree 4 with P(1) = 1/2,
-// minimises the largest RELATIVE error of w over |g| <= 14 (linear programming): 3.5e-5 in fp32
-// over every bf16 g there, 2^-5 of the output's rounding, far into the tail that GELU
-// keeps.  For fp32 tensors CUDA's normcdff.
+// GELU of bf16 tensors, from w = Phi(-|g|) = t P(t) exp(-g^2 / 2) with t = 1 / (3.46 + |g|) (the form of
+// Hastings, Approximations for Digital Computers; the exponential is the density's too): g Phi(g)
+// = max(g, 0) - |g| w, and Phi is w or 1 - w, so the tail is never a difference.  P, of degree 5
+// with w(0) = 1/2, minimises over |g| <= 14 the larger of w's absolute error (5e-8; parameter
+// gradients, fp32 sums over many tokens, see it) and 1/2400 of its relative one (1.3e-4, 2^-4 of the
+// output's rounding where GELU is all tail), by linear programming; in fp32 2e-7 and 1.3e-4 over
+// every bf16 g there.
+struct GeluTail {
+    float2 m, density, neg;  // |g| (finite), phi(g), -w
+
+    __device__ __forceinline__ explicit GeluTail(float2 g)
+    {
+        m = make_float2(fminf(fabsf(g.x), 1e30f), fminf(fabsf(g.y), 1e30f));
+        const float2 d = __fadd2_rn(m, both(3.4602077f)), t = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+        const float2 q = __fmul2_rn(__fmul2_rn(g, g), both(-0.5f * 1.4426950408889634f));
+        const float2 e = make_float2(exp2_approx(q.x), exp2_approx(q.y));
+        density = __fmul2_rn(e, both(0.3989422804014327f));
+        neg = __ffma2_rn(t, both(155.2399f), both(-145.96509f));
+        neg = __ffma2_rn(t, neg, both(15.05492f));
+        neg = __ffma2_rn(t, neg, both(-7.710322f));
+        neg = __ffma2_rn(t, neg, both(-1.1785265f));
+        neg = __ffma2_rn(t, neg, both(-0.40367082f));
+        neg = __fmul2_rn(__fmul2_rn(t, neg), e);
+    }
+};
+
+template <typename T> __device__ __forceinline__ float2 gelu(float2 g)
+{
+    if constexpr (sizeof(T) == 2) {
+        const GeluTail w(g);
+        return __ffma2_rn(w.m, w.neg, make_float2(fmaxf(g.x, 0.f), fmaxf(g.y, 0.f)));
+    } else {
+        return make_float2(g.x * normcdff(g.x), g.y * normcdff(g.y));
+    }
+}
+
+// Phi(g) and the normal density (fp32 tensors: CUDA's normcdff)
 template <typename T> __device__ __forceinline__ float2 gelu_cdf(float2 g, float2 &density)
 {
     if constexpr (sizeof(T) == 2) {
-        const float2 m = make_float2(fabsf(g.x), fabsf(g.y));
-        const float2 d = __ffma2_rn(m, both(0.375f), both(1.f));
-        const float2 t = make_float2(rcp_approx(d.x), rcp_approx(d.y));
-        const float2 q = __fmul2_rn(__fmul2_rn(g, g), both(-0.5f * 1.4426950408889634f));
-        const float2 e = make_float2(exp2_approx(q.x), exp2_approx(q.y));
-        float2 w = __ffma2_rn(t, both(-0.090480238f), both(0.199919820f));
-        w = __ffma2_rn(t, w, both(0.0838441253f));
-        w = __ffma2_rn(t, w, both(0.157645911f));
-        w = __ffma2_rn(t, w, both(0.149070382f));
-        w = __fmul2_rn(__fmul2_rn(t, w), e);
-        density = __fmul2_rn(e, both(0.3989422804014327f));
-        const float2 h = __ffma2_rn(w, both(-1.f), both(1.f));
-        return make_float2(g.x < 0.f ? w.x : h.x, g.y < 0.f ? w.y : h.y);
+        const GeluTail w(g);
+        density = w.density;
+        const float2 h = __fadd2_rn(w.neg, both(1.f));
+        return make_float2(g.x < 0.f ? -w.neg.x : h.x, g.y < 0.f ? -w.neg.y : h.y);
     } else {
         density = make_float2(expf(-0.5f * g.x * g.x) * 0.3989422804014327f, expf(-0.5f * g.y * g.y) * 0.3989422804014327f);
         return make_float2(normcdff(g.x), normcdff(g.y));
@@ -246,10 +268,7 @@ template <typename T> __device__ __forceinline__ V8 act_value(int act, const V8 
         for (int i = 0; i < kP; ++i) r.p[i] = __fmul2_rn(g.p[i], logistic<T>(g.p[i]));
     } else if (act == 3) {
 #pragma unroll
-        for (int i = 0; i < kP; ++i) {
-            float2 d;
-            r.p[i] = __fmul2_rn(g.p[i], gelu_cdf<T>(g.p[i], d));
-        }
+        for (int i = 0; i < kP; ++i) r.p[i] = gelu<T>(g.p[i]);
     } else {
 #pragma unroll
         for (int i = 0; i < kP; ++i) r.p[i] = logistic<T>(g.p[i]);
