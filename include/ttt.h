@@ -394,8 +394,10 @@ size_t ttt_block_norm_bwd_workspace(const ttt_block_norm_desc *desc);
  * exactly when pre is TTT_NORM_NONE), the forward's inputs and its stats.
  *   dy    : contiguous in y's layout ([B,heads,T,D/heads] or [B,T,D])
  *   dx    : [B,T,D] or NULL;  dgate: [B,T,D], NULL exactly when act is TTT_GATE_NONE
- *   grads : gradients of the parameter vectors, summed over all tokens in an order that
- *           depends on the sizes only (the same bits on every run), or NULL
+ *   grads : gradients of the parameter vectors, summed over all tokens, or NULL.  The order
+ *           of the sums is fixed by the sizes, dtype, norms and gate, the alignment and
+ *           strides of the tensors, the gradients asked for and the device: the same call
+ *           gives the same bits on every run
  *   workspace : device scratch, 16-byte aligned, at least
  *           ttt_block_norm_bwd_workspace(desc) bytes (NULL allowed when no parameter
  *           gradient is asked for), free again once the work on `stream` is done
@@ -439,7 +441,11 @@ typedef struct {
  *            that a decoder steps its states in place
  *   states : [B, ceil(T / TTT_RECURRENCE_CHUNK), C] fp32 or NULL: the state before every
  *            chunk of tokens, which the backward pass reads
- * States are fp32 throughout; sums run in an order that depends on the sizes only.  Data
+ * States are fp32 throughout; sums run in an order that is fixed by the sizes, dtype, mode,
+ * alignment and strides of the tensors and the device (the same call gives the same bits on
+ * every run).  TTT_RECUR_DECAY is meant for |f| <= 1: with larger factors h is right as long as
+ * the product of any 2048 neighbouring ones stays inside fp32's range, past which it can be
+ * infinite or NaN where the state itself would not be.  Data
  * pointers: aligned to their element; 16-byte alignment, strides of whole 16 bytes and C a
  * multiple of 8 move wide vectors.  Outputs may not overlap inputs (h_last as above).
  */

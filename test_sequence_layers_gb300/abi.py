@@ -758,8 +758,8 @@ def _recurrence_prologue(x, f, mode, reset, dh=None):
 def ttt_recurrence_fwd(x, f, h0=None, mode="mix", reset=None, h=None, h_last=None, want_states=False, states=None,
                        stream=None):
     """Gated linear recurrence h_t = a_t h_{t-1} + c_t x_t of every channel.  x, f: [B,T,C]
-    bf16 or fp32, strided as long as the channels are contiguous.  mode "decay": a = f,
-    c = 1; "sigmoid": a = sigmoid(f), c = 1; "mix": a = sigmoid(f), c = 1 - a.  reset:
+    bf16 or fp32, strided as long as the channels are contiguous.  mode "decay": a = f
+    (|f| <= 1, see include/ttt.h), c = 1; "sigmoid": a = sigmoid(f), c = 1; "mix": a = sigmoid(f), c = 1 - a.  reset:
     bool or uint8 [B,T], True where a packed sequence begins (h_{t-1} taken as zero).
     h0: fp32 [B,C] or None; h_last may be h0 (a decoder's states stepped in place).
     want_states (or states) for the backward pass.  Returns (h, h_last, states or None)."""

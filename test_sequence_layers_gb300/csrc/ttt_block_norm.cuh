@@ -16,9 +16,10 @@
 // a call has or lacks (POST, PRE, ACT) known at compile time, parameter vectors that are
 // absent replaced by ones and zeros instead of branches, rows copied ahead with cp.async.
 // Measured (bf16, gate, residual and both norms; of the copy bandwidth): 8 x 2048 x 768
-// forward 24 us (0.77) and backward 47 us (0.63), 2 x 32768 x 2048 224 us (0.88) and 511 us
-// (0.62: registers leave eight warps an SM); y and gate alone, layer norm and GELU, 8 x 2048 x
-// 768 22 us (0.51: as many instructions for three fifths of the bytes).
+// forward 24 us (0.77) and backward 48 us (0.62), 2 x 32768 x 2048 with layer norm and GELU 227 us
+// (0.87) and 515 us (0.61: registers leave eight warps an SM); y and gate alone, layer norm and
+// GELU, 8 x 2048 x 768 22 us (0.50: as many instructions, and as many reductions to wait for, for
+// three fifths of the bytes).
 #pragma once
 
 #include <cstdint>
@@ -706,8 +707,9 @@ __global__ void __launch_bounds__(fwd_threads(BLOCK, K, POST, PRE), fwd_blocks(K
 
 // Parameter gradients: every thread sums its own features over the block's rows (in
 // registers; WIDE: in shared memory, which leaves none for stages), blocks write
-// partial sums, a second kernel adds those in order.  The result depends on the sizes and
-// the SM count only.
+// partial sums, a second kernel adds those in order.  The order is fixed by the sizes, the
+// type, the tensors' alignment, the parts that a call has and asks for, and how many
+// blocks the device holds.
 template <typename T, int G, int K, bool BLOCK, int MAXT, int POST, int PRE, int ACT>
 __global__ void __launch_bounds__(MAXT, MAXT >= 256 ? 1 : 256 / MAXT) ttt_block_norm_bwd_kernel(const __grid_constant__ NormBwdParams p)
 {

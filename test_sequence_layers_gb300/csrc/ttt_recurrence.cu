@@ -263,7 +263,7 @@ template <int N, bool WIDE, typename T> __device__ __forceinline__ void put_part
 //            of its place once it has landed; outputs leave the same way.  These loops over
 //            rows are short on purpose: unrolled into the arithmetic they outgrew the
 //            instruction cache (2 x 8192 x 1001 backward, clusters of four, 231 us against
-//            151, and loads of single channels 238; 106 with the eight that are chosen).
+//            151, and loads of single channels 238; 95 with the eight that are chosen).
 enum RowFeed { kTma, kWords, kHalves };
 constexpr int kRaggedPitch = kRowBytes + 16;
 __host__ __device__ constexpr int row_pitch(int feed) { return feed == kHalves ? kRaggedPitch : kRowBytes; }
@@ -979,10 +979,12 @@ template <typename... KArgs> Capacity capacity(void (*kernel)(KArgs...), int sme
 // forward and 2.1 us backward (bf16, mix); 1.33 with the exchange between blocks; two
 // blocks on an SM take `two` each, 1.95 in bf16, 1.5 in fp32, which has half the channels
 // to compute for the same bytes; a start costs about 3, that of a later wave of clusters
-// 6.  Timed over 12 shapes of 1 .. 768 chains and 2 .. 256 chunks with every P of 1 .. 16,
-// this picks the fastest P or one within 6% of it: 64 chains of 256 chunks forward 150 us
-// at P = 4 against 305, 203, 166 at 1, 2, 8; 12 chains 50 us at 16 against 303 and 59 at 1
-// and 8; 192 chains of 8 chunks 20 us at 1 against 26 and 29 at 2 and 4.
+// 6.  Fitted to 12 shapes of 1 .. 768 chains and 2 .. 256 chunks of 16-byte rows, timed with
+// every P of 1 .. 16, where it picked the fastest P or one within 6% of it: 64 chains of 256
+// chunks forward 150 us at P = 4 against 305, 203, 166 at 1, 2, 8; 12 chains 50 us at 16
+// against 303 and 59 at 1 and 8; 192 chains of 8 chunks 20 us at 1 against 26 and 29 at 2 and
+// 4.  Not fitted to the other rows, whose kernels hold other numbers of clusters: 2 x 8192 x
+// 1002 in bf16 backward takes 78 us with its choice and took 71 with an earlier one.
 int plan_cluster(long long chains, int chunks, double two, const Capacity &cap)
 {
     int best = 1;
