@@ -477,7 +477,7 @@ _ROPE_DESC, _NORM_DESC, _NORM_PAR = struct.Struct("@11i20q"), struct.Struct("@8i
 _RECUR_DESC = struct.Struct("@5i6q")
 _NO_STRIDE2, _NO_STRIDE3 = (0, 0), (0, 0, 0)
 _empty, _F32, _I64 = torch.empty, torch.float32, torch.int64
-# the functions behind torch.cuda.current_stream and current_device, where this build has them
+# the functions behind torch.cuda.current_stream and current_device, where PyTorch has them
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda di: torch.cuda.current_stream(di).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _fns: dict = {}

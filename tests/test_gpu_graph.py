@@ -86,3 +86,23 @@ def test_training_pass():
         step()
         abi.ttt_sync_status()
         assert all(torch.equal(a, b) for a, b in zip(replayed, got["out"]))
+
+
+def test_capture_on_the_given_stream():
+    """stream= naming the stream that is captured: outputs come from the graph's own pool."""
+    x, f = (torch.randn(2, 300, 64, device="cuda").to(BF) for _ in range(2))
+    side, got = torch.cuda.Stream(), {}
+    side.wait_stream(torch.cuda.current_stream())
+    abi.ttt_recurrence_fwd(x, f, stream=side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        got["h"], got["last"], _ = abi.ttt_recurrence_fwd(x, f, stream=side)
+    for seed in range(3):
+        torch.manual_seed(seed)
+        x.copy_(torch.randn(x.shape, device="cuda"))
+        g.replay()
+        abi.ttt_sync_status()
+        h, last, _ = abi.ttt_recurrence_fwd(x, f)
+        abi.ttt_sync_status()
+        assert torch.equal(h, got["h"]) and torch.equal(last, got["last"])
