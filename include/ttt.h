@@ -334,6 +334,34 @@ typedef struct {
 ttt_status ttt_rope(const ttt_rope_desc *desc, const void *q, const void *k, const void *v, const float *table,
                     const long long *positions, void *q_out, void *k_out, void *v_out, void *stream);
 
+/* Most axes of ttt_rope_axes. */
+#define TTT_ROPE_MAX_AXES 4
+
+/* Rotary positions with several axes.  rope.period is 0. */
+typedef struct {
+    ttt_rope_desc rope;
+    int axes;                       /* 1 .. TTT_ROPE_MAX_AXES                             */
+    int grid[TTT_ROPE_MAX_AXES];    /* extents of the token grid, when positions is NULL  */
+    long long positions_axis_stride; /* elements from one axis' positions to the next's   */
+} ttt_rope_axes_desc;
+
+/*
+ * ttt_rope for the tokens of images and video: pair i of a head turns by the token's
+ * position on axis pair_axis[i] (time, height, width, ..), (cos, sin) =
+ * table[position on that axis][i].
+ *   pair_axis : [rot/2] bytes on the host, each < axes; read during the call
+ *   positions : [axes,B,T] or [axes,T] 64-bit integers on the device (the strides in the
+ *               description), or NULL: token t is element pos0 + t of a row-major grid
+ *               (the last axis moves fastest), pos0 + T <= the product of its extents
+ *               < 2^31, no extent above table_rows (TTT_ERR_ARG)
+ * Everything else is ttt_rope's: layouts, tables, outputs, positions out of range (the
+ * pairs of that axis become NaN).  Neighbouring pairs of one axis, 8 (bf16) or 4 (fp32)
+ * at a time, read the table 16 bytes at a time.
+ */
+ttt_status ttt_rope_axes(const ttt_rope_axes_desc *desc, const unsigned char *pair_axis, const void *q, const void *k,
+                         const void *v, const float *table, const long long *positions, void *q_out, void *k_out,
+                         void *v_out, void *stream);
+
 /* Norms of ttt_block_norm_fwd / _bwd, over the D features of a token.
  *   TTT_NORM_RMS:   w v / sqrt(mean(v^2) + eps)
  *   TTT_NORM_LAYER: w (v - mean) / sqrt(var + eps) + b */
@@ -462,6 +490,136 @@ ttt_status ttt_recurrence_fwd(const ttt_recurrence_desc *desc, const void *x, co
 ttt_status ttt_recurrence_bwd(const ttt_recurrence_desc *desc, const void *dh, const void *x, const void *f,
                               const unsigned char *reset, const float *states, const float *dh_last, void *dx,
                               void *df, float *dh0, void *stream);
+
+/* Activation of the short convolution. */
+typedef enum { TTT_CONV_NONE = 0, TTT_CONV_SILU = 1 } ttt_conv_act;
+
+/* Short causal convolution problem description.  Strides in elements (batch, token);
+ * channels are contiguous. */
+typedef struct {
+    int B, T, C;               /* batch, tokens (<= 2^30), channels                     */
+    int width;                 /* K, taps of a channel: 1 .. 4 (TTT_ERR_UNSUPPORTED above) */
+    ttt_dtype io_dtype;        /* dtype of x, y, the states, dy, dx                     */
+    int act;                   /* ttt_conv_act                                          */
+    long long x_stride[2], dy_stride[2];
+} ttt_short_conv_desc;
+
+/*
+ * Short causal convolution along the tokens, every channel by itself (the temporal
+ * convolution of the Mamba backbone, "Learning to (Learn at Test Time)" walkthrough,
+ * section 2.2.4):
+ *     y_t = act(bias + sum_{j=0}^{K-1} weight[j] x_{t-K+1+j})
+ *   x         : [B,T,C] io_dtype
+ *   weight    : [C,K] fp32, bias: [C] fp32 or NULL
+ *   reset     : [B,T] bytes or NULL; where not zero, a packed sequence begins: its tokens
+ *               see zeros for every row before it, whatever they hold
+ *   state     : [B,K-1,C] io_dtype, the K-1 inputs before the first token, oldest first,
+ *               or NULL (zeros)
+ *   y         : [B,T,C] io_dtype, contiguous
+ *   state_out : [B,K-1,C] io_dtype or NULL: the last K-1 inputs of the running sequence
+ *               (zeros before its start); may be state itself
+ * Sums in fp32, rounded once.  Data pointers: aligned to their element; 16-byte alignment,
+ * strides of whole 16 bytes and C a multiple of 8 (bf16) or 4 (fp32) move 16 bytes at a
+ * time.  Outputs may not overlap inputs or each other (state_out as above).
+ */
+ttt_status ttt_short_conv_fwd(const ttt_short_conv_desc *desc, const void *x, const float *weight, const float *bias,
+                              const unsigned char *reset, const void *state, void *y, void *state_out, void *stream);
+
+/* Bytes of workspace the backward pass needs (0 for a description it refuses). */
+size_t ttt_short_conv_bwd_workspace(const ttt_short_conv_desc *desc);
+
+/*
+ * Gradients of ttt_short_conv_fwd from dy [B,T,C] (of y) and dstate_out [B,K-1,C] fp32 (of
+ * state_out; NULL: zero), with the forward's inputs.
+ *   dx       : [B,T,C] io_dtype, contiguous
+ *   dweight  : [C,K] fp32, dbias: [C] fp32, dstate: [B,K-1,C] fp32, each may be NULL
+ *              (overwritten, not added to)
+ *   workspace: device scratch, 16-byte aligned, at least ttt_short_conv_bwd_workspace(desc)
+ *              bytes (NULL allowed when neither dweight nor dbias is asked for), free again
+ *              once the work on `stream` is done
+ * Sums over the tokens run in an order that is fixed by the sizes, dtype, alignment and
+ * strides: the same call gives the same bits.
+ */
+ttt_status ttt_short_conv_bwd(const ttt_short_conv_desc *desc, const void *dy, const void *x, const float *weight,
+                              const float *bias, const unsigned char *reset, const void *state,
+                              const float *dstate_out, void *dx, float *dweight, float *dbias, float *dstate,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/* Tokens from one stored state to the next (ttt_selective_scan_fwd's states). */
+#define TTT_SCAN_CHUNK 32
+
+/* Selective scan problem description.  Strides in elements; channels (B and C: states)
+ * are contiguous. */
+typedef struct {
+    int B, T, C;               /* batch (<= 65535), tokens (<= 2^30; B T G < 2^31), channels */
+    int N;                     /* states of a channel, 1 .. 64 (TTT_ERR_UNSUPPORTED above) */
+    int G;                     /* groups of C / G neighbouring channels with one B and C  */
+    ttt_dtype io_dtype;        /* dtype of every token tensor                           */
+    int softplus;              /* 1: the rate is softplus(delta + bias); 0: delta + bias  */
+    long long x_stride[2], delta_stride[2], z_stride[2], dy_stride[2]; /* batch, token   */
+    long long b_stride[3], c_stride[3];                                /* batch, token, group */
+} ttt_scan_desc;
+
+/* Parameters, fp32 on the device; D and delta_bias may be NULL (zeros). */
+typedef struct {
+    const float *A;            /* [C,N]                                                 */
+    const float *D, *delta_bias; /* [C]                                                 */
+} ttt_scan_params;
+
+/* Their gradients (overwritten, not added to), each may be NULL. */
+typedef struct {
+    float *A, *D, *delta_bias;
+} ttt_scan_grads;
+
+/* Bytes of workspace of the forward pass (0 where it needs none). */
+size_t ttt_selective_scan_fwd_workspace(const ttt_scan_desc *desc);
+
+/*
+ * Selective state space scan (the Mamba backbone's layer behind the short convolution),
+ * every channel c with N states:
+ *     d_t = softplus(delta_t + bias),  h_t[n] = exp(d_t A[n]) h_{t-1}[n] + d_t x_t B_t[n],
+ *     y_t = (sum_n C_t[n] h_t[n] + D x_t) silu(z_t)
+ *   x, delta : [B,T,C] io_dtype;  z: [B,T,C] or NULL (no gate)
+ *   Bm, Cm   : [B,T,G,N] io_dtype
+ *   reset    : [B,T] bytes or NULL; where not zero, h_{t-1} is taken as zero (a packed
+ *              sequence begins), whatever it held
+ *   h0       : [B,C,N] fp32 start states or NULL (zeros)
+ *   y        : [B,T,C] io_dtype, contiguous
+ *   h_last   : [B,C,N] fp32 or NULL: the last state (h0 when T = 0); may be h0 itself, so
+ *              that a decoder steps its states in place
+ *   states   : [B, ceil(T / TTT_SCAN_CHUNK), C, N] fp32 or NULL: the state before every chunk
+ *              of tokens, which the backward pass reads
+ *   workspace: device scratch, 16-byte aligned, at least ttt_selective_scan_fwd_workspace(desc)
+ *              bytes, free again once the work on `stream` is done
+ * A is finite and meant for d A <= 0 (decays).  States are fp32 throughout; sums run in an
+ * order that is fixed by the sizes, dtype, alignment and strides (the same call gives the
+ * same bits).  Data pointers: aligned to their element; 16-byte alignment, strides of whole
+ * 16 bytes, C / G and N multiples of 8 (bf16) or 4 (fp32) move 16 bytes at a time.
+ * Outputs may not overlap inputs or each other (h_last as above).
+ */
+ttt_status ttt_selective_scan_fwd(const ttt_scan_desc *desc, const ttt_scan_params *params, const void *x,
+                                  const void *delta, const void *Bm, const void *Cm, const void *z,
+                                  const unsigned char *reset, const float *h0, void *y, float *h_last, float *states,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace the backward pass needs (0 for a description it refuses). */
+size_t ttt_selective_scan_bwd_workspace(const ttt_scan_desc *desc);
+
+/*
+ * Gradients of ttt_selective_scan_fwd from dy [B,T,C] (of y) and dh_last [B,C,N] fp32 (of
+ * h_last; NULL: zero), the forward's inputs and the states it stored.
+ *   dx, ddelta : [B,T,C] io_dtype, contiguous (ddelta: of delta itself, through the softplus)
+ *   dz         : [B,T,C], NULL exactly when z is NULL
+ *   dB, dC     : [B,T,G,N] io_dtype, contiguous, summed over a group's channels
+ *   dh0        : [B,C,N] fp32 or NULL
+ *   workspace  : device scratch, 16-byte aligned, ttt_selective_scan_bwd_workspace(desc) bytes
+ * Sums over channels and tokens run in fixed orders, as the forward pass's.
+ */
+ttt_status ttt_selective_scan_bwd(const ttt_scan_desc *desc, const ttt_scan_params *params, const void *dy,
+                                  const void *x, const void *delta, const void *Bm, const void *Cm, const void *z,
+                                  const unsigned char *reset, const float *states, const float *dh_last, void *dx,
+                                  void *ddelta, void *dB, void *dC, void *dz, const ttt_scan_grads *grads, float *dh0,
+                                  void *workspace, size_t workspace_bytes, void *stream);
 
 /* Waits for `stream`, then reports (and clears) a kernel wait timeout
  * (TTT_ERR_TIMEOUT) or a position out of range (TTT_ERR_RANGE) recorded on the current

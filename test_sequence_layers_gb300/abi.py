@@ -26,7 +26,10 @@ STATUS = {0: "TTT_OK", -1: "TTT_ERR_ARG", -2: "TTT_ERR_UNSUPPORTED", -3: "TTT_ER
 EXPORTS = ("ttt_linear_fwd", "ttt_linear_seqpar_workspace", "ttt_linear_fwd_seqpar",
            "ttt_linear_fwd_seqpar_noalloc", "ttt_dwconv_fwd", "ttt_eta_gate",
            "ttt_mlp_fwd", "ttt_rope", "ttt_block_norm_fwd", "ttt_block_norm_bwd_workspace",
-           "ttt_block_norm_bwd", "ttt_recurrence_fwd", "ttt_recurrence_bwd", "ttt_sync_status", "ttt_status_str", "ttt_launch_count",
+           "ttt_block_norm_bwd", "ttt_recurrence_fwd", "ttt_recurrence_bwd",
+           "ttt_rope_axes", "ttt_short_conv_fwd", "ttt_short_conv_bwd_workspace", "ttt_short_conv_bwd",
+           "ttt_selective_scan_fwd_workspace", "ttt_selective_scan_fwd", "ttt_selective_scan_bwd_workspace",
+           "ttt_selective_scan_bwd", "ttt_sync_status", "ttt_status_str", "ttt_launch_count",
            "ttt_debug_wait_limit")
 
 
@@ -90,6 +93,31 @@ class RecurrenceDesc(ctypes.Structure):
 
 RECURRENCE_MODES = {"decay": 0, "sigmoid": 1, "mix": 2}
 RECURRENCE_CHUNK = 128
+
+
+class RopeAxesDesc(ctypes.Structure):
+    _fields_ = [*RopeDesc._fields_, ("axes", ctypes.c_int), ("grid", ctypes.c_int * 4),
+                ("positions_axis_stride", ctypes.c_longlong)]
+
+ROPE_MAX_AXES = 4
+
+
+class ShortConvDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("C", ctypes.c_int), ("width", ctypes.c_int),
+                ("io_dtype", ctypes.c_int), ("act", ctypes.c_int), ("strides", ctypes.c_longlong * 4)]
+
+CONV_ACTS = {"none": 0, "silu": 1}
+
+
+class ScanDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("C", ctypes.c_int), ("N", ctypes.c_int), ("G", ctypes.c_int),
+                ("io_dtype", ctypes.c_int), ("softplus", ctypes.c_int), ("strides", ctypes.c_longlong * 14)]
+
+
+class ScanVectors(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("A", "D", "delta_bias")]
+
+SCAN_CHUNK = 32
 
 
 class TTTError(RuntimeError):
@@ -475,6 +503,8 @@ def ttt_eta_gate(x, theta, eta_base=1.0, eta=None, stream=None):
 _IO = {torch.bfloat16: TTT_BF16, torch.float32: TTT_F32}
 _ROPE_DESC, _NORM_DESC, _NORM_PAR = struct.Struct("@11i20q"), struct.Struct("@8i3f11q"), struct.Struct("@5Q")
 _RECUR_DESC = struct.Struct("@5i6q")
+_AXES_DESC, _CONV_DESC, _SCAN_DESC, _THREE = (struct.Struct("@11i20q5iq"), struct.Struct("@6i4q"), struct.Struct("@7i14q"),
+                                              struct.Struct("@3Q"))
 _NO_STRIDE2, _NO_STRIDE3 = (0, 0), (0, 0, 0)
 _empty, _F32, _I64 = torch.empty, torch.float32, torch.int64
 # the functions behind torch.cuda.current_stream and current_device, where PyTorch has them
@@ -489,19 +519,35 @@ def _fn(name):
     if f is None:
         f = lib()[name]
         n = {"ttt_rope": 10, "ttt_block_norm_fwd": 9, "ttt_block_norm_bwd": 15, "ttt_recurrence_fwd": 9,
-             "ttt_recurrence_bwd": 11}[name]
+             "ttt_recurrence_bwd": 11, "ttt_rope_axes": 11, "ttt_short_conv_fwd": 9, "ttt_short_conv_bwd": 15,
+             "ttt_selective_scan_fwd": 15, "ttt_selective_scan_bwd": 21}[name]
         f.argtypes = [ctypes.c_void_p] * n
         f.restype = ctypes.c_int
         _fns[name] = f
     return f
 
 
-def _norm_workspace(desc):
-    f = _fns.get("workspace")
+def _workspace_bytes(name, desc):
+    f = _fns.get(name)
     if f is None:
-        f = _fns["workspace"] = lib()["ttt_block_norm_bwd_workspace"]
+        f = _fns[name] = lib()[name]
         f.argtypes, f.restype = [ctypes.c_void_p], ctypes.c_size_t
     return f(desc)
+
+
+def _norm_workspace(desc):
+    return _workspace_bytes("ttt_block_norm_bwd_workspace", desc)
+
+
+def _scratch(name, workspace, need, dev, di):
+    """The caller's workspace, or one of the need's size from PyTorch's pool; (address, bytes, keeper)."""
+    if workspace is None:
+        if need == 0:
+            return 0, 0, None
+        workspace = _empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.get_device() != di or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {name}'s device")
+    return workspace.data_ptr(), workspace.nbytes, workspace
 
 
 def _tokens(name, t, dims, like=None):
@@ -566,6 +612,27 @@ def ttt_rope(q, k, v, table, positions=None, pos0=0, period=0, interleaved=False
     if stream is not None:
         return _on_stream(stream, q, ttt_rope, q, k, v, table, positions, pos0, period, interleaved, inverse, q_out,
                           k_out, v_out)
+    return _rope(q, k, v, table, positions, pos0, period, interleaved, inverse, q_out, k_out, v_out, None, None)
+
+
+def ttt_rope_axes(q, k, v, table, pair_axis, positions=None, grid=None, pos0=0, interleaved=False, inverse=False,
+                  q_out=None, k_out=None, v_out=None, stream=None):
+    """ttt_rope with several axes: pair i of a head turns by the token's position on axis
+    pair_axis[i] (time, height, width, ...), rows of the table (rotary.rope_axes and
+    rotary.rope_axes_table make both).  pair_axis: rot/2 small integers (bytes or a
+    sequence).  positions: int64 [axes,B,T] or [axes,T] on the device; or grid: the
+    extents of a row-major token grid, the last axis moving fastest, whose element pos0 + t
+    token t is.  The rest as ttt_rope."""
+    if stream is not None:
+        return _on_stream(stream, q, ttt_rope_axes, q, k, v, table, pair_axis, positions, grid, pos0, interleaved, inverse,
+                          q_out, k_out, v_out)
+    if (positions is None) == (grid is None):
+        raise ValueError("give either positions or grid")
+    return _rope(q, k, v, table, positions, pos0, 0, interleaved, inverse, q_out, k_out, v_out, pair_axis, grid)
+
+
+def _rope(q, k, v, table, positions, pos0, period, interleaved, inverse, q_out, k_out, v_out, pair_axis, grid):
+    """ttt_rope, or with pair_axis ttt_rope_axes."""
     dt, dev, di, sq = q.dtype, q.device, q.get_device(), q.stride()
     io = _IO.get(dt)
     if io is None or not q.is_cuda or len(sq) != 4 or sq[3] != 1:
@@ -587,7 +654,14 @@ def ttt_rope(q, k, v, table, positions=None, pos0=0, period=0, interleaved=False
     if positions is not None:
         if positions.dtype is not _I64 or positions.get_device() != di or not positions.is_contiguous():
             raise ValueError("positions must be a contiguous int64 tensor on q's device")
-        if positions.shape == (B, T):
+        if pair_axis is not None:
+            axes = positions.shape[0] if positions.dim() else 0
+            pas = T
+            if positions.shape == (axes, B, T):
+                pbs, pas = T, B * T
+            elif positions.shape != (axes, T):
+                raise ValueError("positions must be [axes,B,T] or [axes,T]")
+        elif positions.shape == (B, T):
             pbs = T
         elif positions.shape != (T,):
             raise ValueError("positions must be [B,T] or [T]")
@@ -611,6 +685,21 @@ def ttt_rope(q, k, v, table, positions=None, pos0=0, period=0, interleaved=False
         v_out, svo = _empty(v.shape, dtype=dt, device=dev), (hk * Td, Td, d)
     else:
         svo = _rows("v_out", v_out, q, v.shape, dt, di)
+    if pair_axis is not None:
+        pair_axis = bytes(pair_axis)
+        if len(pair_axis) != tshape[1]:
+            raise ValueError("pair_axis must name an axis for each of the table's pairs")
+        if positions is None:
+            axes, pas = len(grid), 0
+        if not 1 <= axes <= ROPE_MAX_AXES:
+            raise ValueError(f"there must be 1 to {ROPE_MAX_AXES} axes")
+        extents = (0,) * ROPE_MAX_AXES if grid is None else (*grid, *(1,) * (ROPE_MAX_AXES - axes))
+        desc = _AXES_DESC.pack(B, T, H, hk, d, 2 * tshape[1], interleaved, inverse, io, tshape[0], 0, pos0, pbs, *sq[:3], *sk,
+                               *sv, *so, *sko, *svo, axes, *extents, pas)
+        _call("ttt_rope_axes", di, desc, pair_axis, q.data_ptr(), 0 if k is None else k.data_ptr(),
+              0 if v is None else v.data_ptr(), table.data_ptr(), 0 if positions is None else positions.data_ptr(),
+              q_out.data_ptr(), 0 if k is None else k_out.data_ptr(), 0 if v is None else v_out.data_ptr())
+        return q_out, k_out, v_out
     desc = _ROPE_DESC.pack(B, T, H, hk, d, 2 * tshape[1], interleaved, inverse, io, tshape[0], period, pos0, pbs,
                            *sq[:3], *sk, *sv, *so, *sko, *svo)
     _call("ttt_rope", di, desc, q.data_ptr(), 0 if k is None else k.data_ptr(), 0 if v is None else v.data_ptr(),
@@ -797,6 +886,220 @@ def ttt_recurrence_bwd(dh, x, f, states, mode="mix", reset=None, dh_last=None, d
           0 if reset is None else reset.data_ptr(), states.data_ptr(), 0 if dh_last is None else dh_last.data_ptr(),
           dx.data_ptr(), df.data_ptr(), dh0.data_ptr())
     return dx, df, dh0
+
+
+def _reset(reset, shape, di):
+    if (reset.dtype not in (torch.bool, torch.uint8) or reset.get_device() != di or reset.shape != shape[:2]
+            or not reset.is_contiguous()):
+        raise ValueError("reset must be a contiguous bool or uint8 [B,T] tensor on x's device")
+
+
+def _conv_prologue(x, weight, bias, act, reset, state, dy=None):
+    """Checks of both convolution wrappers; returns (shape, width, dtype, device and its
+    number, state shape, descriptor)."""
+    dt, di, sx = x.dtype, x.get_device(), x.stride()
+    io = _IO.get(dt)
+    if io is None or not x.is_cuda or len(sx) != 3 or sx[2] != 1:
+        _tokens("x", x, 3)
+        sx = (*sx[:2], 1)
+    B, T, C = shape = x.shape
+    if weight.dim() != 2:
+        raise ValueError("weight must be [C,K]")
+    K = weight.shape[1]
+    _like("weight", weight, (C, K), _F32, di)
+    if bias is not None:
+        _like("bias", bias, (C,), _F32, di)
+    sd = _NO_STRIDE2 if dy is None else _rows("dy", dy, x, shape, dt, di)
+    if reset is not None:
+        _reset(reset, shape, di)
+    sshape = (B, K - 1, C)
+    if state is not None:
+        _like("state", state, sshape, dt, di)
+    return shape, K, dt, x.device, di, sshape, _CONV_DESC.pack(B, T, C, K, io, CONV_ACTS[act], sx[0], sx[1], *sd)
+
+
+def ttt_short_conv_fwd(x, weight, bias=None, act="silu", reset=None, state=None, y=None, want_state=False, state_out=None,
+                       stream=None):
+    """Short causal convolution of every channel along the tokens: y_t = act(bias + sum_j
+    weight[:, j] x_{t-K+1+j}).  x: [B,T,C] bf16 or fp32, strided as long as the channels are
+    contiguous; weight: fp32 [C,K], K up to 4; bias: fp32 [C] or None; act "none" or "silu".
+    reset: bool or uint8 [B,T], True where a packed sequence begins (its tokens see zeros
+    before it).  state: [B,K-1,C] in x's dtype, the inputs before the first token, oldest
+    first, or None (zeros).  want_state (or state_out, which may be state: a decoder's
+    states stepped in place) for the last K-1 inputs.  Returns (y, state_out or None)."""
+    if stream is not None:
+        return _on_stream(stream, x, ttt_short_conv_fwd, x, weight, bias, act, reset, state, y, want_state, state_out)
+    shape, _, dt, dev, di, sshape, desc = _conv_prologue(x, weight, bias, act, reset, state)
+    y = _empty(shape, dtype=dt, device=dev) if y is None else _like("y", y, shape, dt, di)
+    if state_out is not None:
+        _like("state_out", state_out, sshape, dt, di)
+    elif want_state:
+        state_out = _empty(sshape, dtype=dt, device=dev)
+    _call("ttt_short_conv_fwd", di, desc, x.data_ptr(), weight.data_ptr(), 0 if bias is None else bias.data_ptr(),
+          0 if reset is None else reset.data_ptr(), 0 if state is None else state.data_ptr(), y.data_ptr(),
+          0 if state_out is None else state_out.data_ptr())
+    return y, state_out
+
+
+class ShortConvGrads(NamedTuple):
+    """Gradients of ttt_short_conv_fwd's inputs, None for an absent input."""
+    x: torch.Tensor
+    weight: torch.Tensor
+    bias: Optional[torch.Tensor]
+    state: Optional[torch.Tensor]
+
+
+def ttt_short_conv_bwd(dy, x, weight, bias=None, act="silu", reset=None, state=None, dstate_out=None, workspace=None,
+                       stream=None):
+    """Gradients of ttt_short_conv_fwd from dy [B,T,C] and dstate_out (of state_out, fp32
+    [B,K-1,C], or None), with the forward's inputs.  Returns ShortConvGrads: x's in x's
+    dtype, the rest fp32.  workspace: a CUDA tensor of ttt_short_conv_bwd_workspace's bytes,
+    allocated here when None."""
+    if stream is not None:
+        return _on_stream(stream, x, ttt_short_conv_bwd, dy, x, weight, bias, act, reset, state, dstate_out, workspace)
+    shape, K, dt, dev, di, sshape, desc = _conv_prologue(x, weight, bias, act, reset, state, dy)
+    if dstate_out is not None:
+        _like("dstate_out", dstate_out, sshape, _F32, di)
+    dx = _empty(shape, dtype=dt, device=dev)
+    dw = _empty((shape[2], K), dtype=_F32, device=dev)
+    db = None if bias is None else _empty(shape[2], dtype=_F32, device=dev)
+    ds = None if state is None else _empty(sshape, dtype=_F32, device=dev)
+    ws, nws, _keep = _scratch("x", workspace, _workspace_bytes("ttt_short_conv_bwd_workspace", desc), dev, di)
+    _call("ttt_short_conv_bwd", di, desc, dy.data_ptr(), x.data_ptr(), weight.data_ptr(), 0 if bias is None else bias.data_ptr(),
+          0 if reset is None else reset.data_ptr(), 0 if state is None else state.data_ptr(),
+          0 if dstate_out is None else dstate_out.data_ptr(), dx.data_ptr(), dw.data_ptr(), 0 if db is None else db.data_ptr(),
+          0 if ds is None else ds.data_ptr(), ws, nws)
+    return ShortConvGrads(dx, dw, db, ds)
+
+
+def ttt_short_conv_bwd_workspace(B, T, C, K) -> int:
+    """Workspace bytes of ttt_short_conv_bwd for B x T tokens of C channels, K taps."""
+    return _workspace_bytes("ttt_short_conv_bwd_workspace", _CONV_DESC.pack(B, T, C, K, TTT_BF16, 0, 0, 0, 0, 0))
+
+
+def _scan_prologue(x, delta, A, B, C, D, z, delta_bias, softplus, reset, dy=None):
+    """Checks of both scan wrappers; returns (token shape, states' [C,N], B's and C's shapes,
+    dtype, device and its number, descriptor, parameters)."""
+    dt, di, sx = x.dtype, x.get_device(), x.stride()
+    io = _IO.get(dt)
+    if io is None or not x.is_cuda or len(sx) != 3 or sx[2] != 1:
+        _tokens("x", x, 3)
+        sx = (*sx[:2], 1)
+    nb, T, ch = shape = x.shape
+    if A.dim() != 2:
+        raise ValueError("A must be [C,N]")
+    N = A.shape[1]
+    _like("A", A, (ch, N), _F32, di)
+    sdl = _rows("delta", delta, x, shape, dt, di)
+    if B.dim() == 4:
+        G = B.shape[2]
+        bshape = (nb, T, G, N)
+        sb = _rows("B", B, x, bshape, dt, di)
+        sc = _rows("C", C, x, bshape, dt, di)
+    else:
+        G = 1
+        bshape = (nb, T, N)
+        sb = (*_rows("B", B, x, bshape, dt, di), 0)
+        sc = (*_rows("C", C, x, bshape, dt, di), 0)
+    if G < 1 or ch % G:
+        raise ValueError("the groups of B and C must divide the channels")
+    sz = _NO_STRIDE2 if z is None else _rows("z", z, x, shape, dt, di)
+    sdy = _NO_STRIDE2 if dy is None else _rows("dy", dy, x, shape, dt, di)
+    if reset is not None:
+        _reset(reset, shape, di)
+    vec = (ch,)
+    par = _THREE.pack(A.data_ptr(), 0 if D is None else _vec("D", D, vec, di),
+                      0 if delta_bias is None else _vec("delta_bias", delta_bias, vec, di))
+    desc = _SCAN_DESC.pack(nb, T, ch, N, G, io, bool(softplus), sx[0], sx[1], *sdl, *sz, *sdy, *sb, *sc)
+    return shape, (ch, N), bshape, dt, x.device, di, desc, par
+
+
+def ttt_selective_scan_fwd(x, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=True, reset=None, h0=None, y=None,
+                           h_last=None, want_states=False, states=None, workspace=None, stream=None):
+    """Selective state space scan, N states a channel: with d = softplus(delta + delta_bias)
+    (softplus=False: without it),
+        h_t = exp(d_t A) h_{t-1} + d_t x_t B_t,   y_t = (C_t . h_t + D x_t) silu(z_t).
+    x, delta, z: [B,T,C] bf16 or fp32, B, C: [B,T,N] or, for G groups of channels,
+    [B,T,G,N], all strided as long as the last dimension is contiguous (slices of a
+    projection); A: fp32 [C,N], D, delta_bias: fp32 [C] or None; z None: no gate.
+    reset: bool or uint8 [B,T], True where a packed sequence begins.  h0: fp32 [B,C,N] or
+    None; h_last may be h0 (a decoder's states stepped in place).  want_states (or states)
+    for the backward pass.  Returns (y, h_last, states or None)."""
+    if stream is not None:
+        return _on_stream(stream, x, ttt_selective_scan_fwd, x, delta, A, B, C, D, z, delta_bias, softplus, reset, h0, y,
+                          h_last, want_states, states, workspace)
+    shape, cn, _, dt, dev, di, desc, par = _scan_prologue(x, delta, A, B, C, D, z, delta_bias, softplus, reset)
+    nb, T, _ = shape
+    hshape = (nb, *cn)
+    if h0 is not None:
+        _like("h0", h0, hshape, _F32, di)
+    if states is not None:
+        _like("states", states, (nb, -(-T // SCAN_CHUNK), *cn), _F32, di)
+    elif want_states:
+        states = _empty((nb, -(-T // SCAN_CHUNK), *cn), dtype=_F32, device=dev)
+    y = _empty(shape, dtype=dt, device=dev) if y is None else _like("y", y, shape, dt, di)
+    h_last = _empty(hshape, dtype=_F32, device=dev) if h_last is None else _like("h_last", h_last, hshape, _F32, di)
+    # (a single token needs no workspace)
+    need = _workspace_bytes("ttt_selective_scan_fwd_workspace", desc) if T > 1 and workspace is None else 0
+    ws, nws, _keep = _scratch("x", workspace, need, dev, di)
+    _call("ttt_selective_scan_fwd", di, desc, par, x.data_ptr(), delta.data_ptr(), B.data_ptr(), C.data_ptr(),
+          0 if z is None else z.data_ptr(), 0 if reset is None else reset.data_ptr(), 0 if h0 is None else h0.data_ptr(),
+          y.data_ptr(), h_last.data_ptr(), 0 if states is None else states.data_ptr(), ws, nws)
+    return y, h_last, states
+
+
+class SelectiveScanGrads(NamedTuple):
+    """Gradients of ttt_selective_scan_fwd's inputs, None for an absent input."""
+    x: torch.Tensor
+    delta: torch.Tensor
+    A: torch.Tensor
+    B: torch.Tensor
+    C: torch.Tensor
+    D: Optional[torch.Tensor]
+    z: Optional[torch.Tensor]
+    delta_bias: Optional[torch.Tensor]
+    h0: torch.Tensor
+
+
+def ttt_selective_scan_bwd(dy, x, delta, A, B, C, states, D=None, z=None, delta_bias=None, softplus=True, reset=None,
+                           dh_last=None, workspace=None, stream=None):
+    """Gradients of ttt_selective_scan_fwd from dy [B,T,C] and dh_last (of h_last, fp32
+    [B,C,N], or None), with the forward's inputs and the states it stored.  Returns
+    SelectiveScanGrads: the token tensors' in their dtype, contiguous, the rest fp32 (h0's
+    whether or not one was given).  workspace: a CUDA tensor of
+    ttt_selective_scan_bwd_workspace's bytes, allocated here when None."""
+    if stream is not None:
+        return _on_stream(stream, x, ttt_selective_scan_bwd, dy, x, delta, A, B, C, states, D, z, delta_bias, softplus,
+                          reset, dh_last, workspace)
+    shape, cn, bshape, dt, dev, di, desc, par = _scan_prologue(x, delta, A, B, C, D, z, delta_bias, softplus, reset, dy)
+    nb, T, ch = shape
+    _like("states", states, (nb, -(-T // SCAN_CHUNK), *cn), _F32, di)
+    if dh_last is not None:
+        _like("dh_last", dh_last, (nb, *cn), _F32, di)
+    dx, dd = _empty(shape, dtype=dt, device=dev), _empty(shape, dtype=dt, device=dev)
+    dz = None if z is None else _empty(shape, dtype=dt, device=dev)
+    dB, dC = _empty(bshape, dtype=dt, device=dev), _empty(bshape, dtype=dt, device=dev)
+    dA, dh0 = _empty(cn, dtype=_F32, device=dev), _empty((nb, *cn), dtype=_F32, device=dev)
+    dD = None if D is None else _empty(ch, dtype=_F32, device=dev)
+    db = None if delta_bias is None else _empty(ch, dtype=_F32, device=dev)
+    need = _workspace_bytes("ttt_selective_scan_bwd_workspace", desc) if workspace is None else 0
+    ws, nws, _keep = _scratch("x", workspace, need, dev, di)
+    grads = _THREE.pack(dA.data_ptr(), 0 if dD is None else dD.data_ptr(), 0 if db is None else db.data_ptr())
+    _call("ttt_selective_scan_bwd", di, desc, par, dy.data_ptr(), x.data_ptr(), delta.data_ptr(), B.data_ptr(), C.data_ptr(),
+          0 if z is None else z.data_ptr(), 0 if reset is None else reset.data_ptr(), states.data_ptr(),
+          0 if dh_last is None else dh_last.data_ptr(), dx.data_ptr(), dd.data_ptr(), dB.data_ptr(), dC.data_ptr(),
+          0 if dz is None else dz.data_ptr(), grads, dh0.data_ptr(), ws, nws)
+    return SelectiveScanGrads(dx, dd, dA, dB, dC, dD, dz, db, dh0)
+
+
+def ttt_selective_scan_fwd_workspace(B, T, C, N, G=1) -> int:
+    """Workspace bytes of ttt_selective_scan_fwd."""
+    return _workspace_bytes("ttt_selective_scan_fwd_workspace", _SCAN_DESC.pack(B, T, C, N, G, TTT_BF16, 1, *[0] * 14))
+
+
+def ttt_selective_scan_bwd_workspace(B, T, C, N, G=1) -> int:
+    """Workspace bytes of ttt_selective_scan_bwd."""
+    return _workspace_bytes("ttt_selective_scan_bwd_workspace", _SCAN_DESC.pack(B, T, C, N, G, TTT_BF16, 1, *[0] * 14))
 
 
 def ttt_sync_status(stream=None):

@@ -606,11 +606,13 @@ bool same_view(const HeadView &a, const HeadView &b)
 
 }  // namespace
 
-ttt_status ttt_rope(const ttt_rope_desc *desc, const void *q, const void *k, const void *v, const float *table,
-                    const long long *positions, void *q_out, void *k_out, void *v_out, void *stream)
+namespace {
+
+// ttt_rope, or with `axes` ttt_rope_axes.
+ttt_status rope(const ttt_rope_desc &D, const ttt_rope_axes_desc *axes, const unsigned char *pair_axis, const void *q,
+                const void *k, const void *v, const float *table, const long long *positions, void *q_out, void *k_out,
+                void *v_out, void *stream)
 {
-    if (!desc) return TTT_ERR_ARG;
-    const ttt_rope_desc D = *desc;
     if (D.B < 0 || D.T < 0 || D.Hq < 1 || D.Hk < 0 || D.d < 1 || D.rot < 0 || D.rot > D.d || D.rot % 2) return TTT_ERR_ARG;
     if (D.interleaved < 0 || D.interleaved > 1 || D.inverse < 0 || D.inverse > 1) return TTT_ERR_ARG;
     if (D.io_dtype != TTT_F32 && D.io_dtype != TTT_BF16) return TTT_ERR_ARG;
@@ -620,7 +622,23 @@ ttt_status ttt_rope(const ttt_rope_desc *desc, const void *q, const void *k, con
     if (D.B == 0 || D.T == 0) return TTT_OK;
     if (!q || !q_out || (k && !k_out) || (v && !v_out) || ((k || v) && D.Hk < 1)) return TTT_ERR_ARG;
     if (D.rot > 0 && !table) return TTT_ERR_ARG;
-    if (D.rot > 0 && !positions && D.period == 0 && D.pos0 > (long long)D.table_rows - D.T) return TTT_ERR_ARG;
+    if (D.rot > 0 && !positions && !axes && D.period == 0 && D.pos0 > (long long)D.table_rows - D.T) return TTT_ERR_ARG;
+    if (axes && D.rot > 0) {
+        if (D.period != 0 || !pair_axis) return TTT_ERR_ARG;
+        for (int i = 0; i < D.rot / 2; ++i)
+            if (pair_axis[i] >= axes->axes) return TTT_ERR_ARG;
+        if (positions) {
+            if (axes->positions_axis_stride < 0) return TTT_ERR_ARG;
+        } else {
+            long long tokens = 1;
+            for (int i = 0; i < axes->axes; ++i) {
+                if (axes->grid[i] < 1 || axes->grid[i] > D.table_rows) return TTT_ERR_ARG;
+                tokens *= axes->grid[i];
+                if (tokens > 0x7fffffffLL) return TTT_ERR_ARG;
+            }
+            if (D.pos0 > tokens - D.T) return TTT_ERR_ARG;
+        }
+    }
     const int es = D.io_dtype == TTT_BF16 ? 2 : 4;
     ttt::RopeArgs a = {};
     const void *in[3] = {q, k, v};
@@ -641,7 +659,7 @@ ttt_status ttt_rope(const ttt_rope_desc *desc, const void *q, const void *k, con
     }
     if (D.rot > 0 && (!aligned(table, 8) || (positions && !aligned(positions, 8)))) return TTT_ERR_ALIGN;
     const size_t table_bytes = (size_t)D.table_rows * D.rot * 4,
-                 pos_bytes = positions ? 8 * (size_t)(D.positions_batch_stride * (D.B - 1) + D.T) : 0;
+                 pos_bytes = positions ? 8 * (size_t)((axes ? axes->positions_axis_stride * (axes->axes - 1) : 0) + D.positions_batch_stride * (D.B - 1) + D.T) : 0;
     HeadView vi[3], vo[3];
     for (int i = 0; i < 3; ++i) {
         if (!in[i]) continue;
@@ -683,9 +701,32 @@ ttt_status ttt_rope(const ttt_rope_desc *desc, const void *q, const void *k, con
     if (!status) return TTT_ERR_LAUNCH;
     a.range_status = status + 1;
     a.stream = static_cast<cudaStream_t>(stream);
+    if (axes) {
+        a.axes = axes->axes;
+        a.axis_stride = axes->axes > 1 ? axes->positions_axis_stride : 0;
+        for (int i = 0; i < axes->axes; ++i) a.grid[i] = axes->grid[i];
+        a.pair_axis = pair_axis;
+    }
     const int rc = ttt::launch_rope(a);
     if (rc == 0) g_launches.fetch_add(1, std::memory_order_relaxed);
     return code(rc);
+}
+
+}  // namespace
+
+ttt_status ttt_rope(const ttt_rope_desc *desc, const void *q, const void *k, const void *v, const float *table,
+                    const long long *positions, void *q_out, void *k_out, void *v_out, void *stream)
+{
+    if (!desc) return TTT_ERR_ARG;
+    return rope(*desc, nullptr, nullptr, q, k, v, table, positions, q_out, k_out, v_out, stream);
+}
+
+ttt_status ttt_rope_axes(const ttt_rope_axes_desc *desc, const unsigned char *pair_axis, const void *q, const void *k,
+                         const void *v, const float *table, const long long *positions, void *q_out, void *k_out,
+                         void *v_out, void *stream)
+{
+    if (!desc || desc->axes < 1 || desc->axes > TTT_ROPE_MAX_AXES) return TTT_ERR_ARG;
+    return rope(desc->rope, desc, pair_axis, q, k, v, table, positions, q_out, k_out, v_out, stream);
 }
 
 namespace {
@@ -993,6 +1034,345 @@ ttt_status ttt_recurrence_bwd(const ttt_recurrence_desc *desc, const void *dh, c
     const int rc = ttt::launch_recurrence(a, true);
     if (rc == 0) g_launches.fetch_add(1, std::memory_order_relaxed);
     return code(rc);
+}
+
+namespace {
+
+bool conv_desc_ok(const ttt_short_conv_desc &D)
+{
+    if (D.B < 0 || D.T < 0 || D.C < 1 || D.width < 1 || D.act < 0 || D.act > 1) return false;
+    return D.io_dtype == TTT_F32 || D.io_dtype == TTT_BF16;
+}
+
+// Checks the part both directions share and fills the launch arguments.
+ttt_status conv_args(const ttt_short_conv_desc *desc, const void *x, const float *weight, const float *bias,
+                     const unsigned char *reset, const void *state, void *stream, ttt::ConvArgs &a)
+{
+    if (!desc || !conv_desc_ok(*desc)) return TTT_ERR_ARG;
+    const ttt_short_conv_desc &D = *desc;
+    for (int i = 0; i < 2; ++i)
+        if (D.x_stride[i] < 0 || D.dy_stride[i] < 0) return TTT_ERR_ARG;
+    if (D.width > ttt::kConvMaxWidth || (long long)D.B * D.T > 0x7fffffffLL || D.T > 1 << 30) return TTT_ERR_UNSUPPORTED;
+    const int es = D.io_dtype == TTT_BF16 ? 2 : 4;
+    if (!weight) return TTT_ERR_ARG;
+    if (!aligned(weight, 4) || (bias && !aligned(bias, 4)) || (state && !aligned(state, es))) return TTT_ERR_ALIGN;
+    if (D.B > 0 && D.T > 0) {
+        if (!x) return TTT_ERR_ARG;
+        if (!aligned(x, es)) return TTT_ERR_ALIGN;
+    }
+    a = {};
+    a.B = D.B;
+    a.T = D.T;
+    a.C = D.C;
+    a.K = D.width;
+    a.bf16 = D.io_dtype == TTT_BF16;
+    a.silu = D.act == TTT_CONV_SILU;
+    a.x = x;
+    a.weight = weight;
+    a.bias = bias;
+    a.reset = reset;
+    a.state = D.width > 1 ? state : nullptr;
+    const int n[2] = {D.B, D.T};
+    for (int i = 0; i < 2; ++i) {
+        a.xs[i] = n[i] > 1 ? D.x_stride[i] : 0;
+        a.dys[i] = n[i] > 1 ? D.dy_stride[i] : 0;
+    }
+    a.stream = static_cast<cudaStream_t>(stream);
+    return TTT_OK;
+}
+
+// Does any output overlap an input or another output?
+bool any_clash(const Range *out, int no, const Range *in, int ni)
+{
+    if (clash(out, no, in, ni)) return true;
+    for (int i = 0; i + 1 < no; ++i)
+        if (clash(out + i, 1, out + i + 1, no - 1 - i)) return true;
+    return false;
+}
+
+ttt_status copy_bytes(void *dst, const void *src, size_t n, cudaStream_t st)
+{
+    if (!dst || dst == src || n == 0) return TTT_OK;
+    const cudaError_t e = src ? cudaMemcpyAsync(dst, src, n, cudaMemcpyDeviceToDevice, st) : cudaMemsetAsync(dst, 0, n, st);
+    return e == cudaSuccess ? TTT_OK : TTT_ERR_LAUNCH;
+}
+
+}  // namespace
+
+ttt_status ttt_short_conv_fwd(const ttt_short_conv_desc *desc, const void *x, const float *weight, const float *bias,
+                              const unsigned char *reset, const void *state, void *y, void *state_out, void *stream)
+{
+    ttt::ConvArgs a;
+    const ttt_status st = conv_args(desc, x, weight, bias, reset, state, stream, a);
+    if (st != TTT_OK) return st;
+    const int es = a.bf16 ? 2 : 4;
+    if (a.K == 1) state_out = nullptr;
+    if (state_out && !aligned(state_out, es)) return TTT_ERR_ALIGN;
+    const size_t ns = (size_t)a.B * (a.K - 1) * a.C * es, n = (size_t)a.B * a.T * a.C * es;
+    if (state_out && a.state && state_out != a.state && overlaps(a.state, ns, state_out, ns)) return TTT_ERR_ARG;
+    if (a.B == 0 || a.T == 0) return copy_bytes(state_out, a.state, ns, a.stream);
+    if (!y) return TTT_ERR_ARG;
+    if (!aligned(y, es)) return TTT_ERR_ALIGN;
+    const Range in[] = {{x, rows_span(a.xs, a.B, a.T, a.C, es)}, {weight, (size_t)a.C * a.K * 4}, {bias, (size_t)a.C * 4},
+                        {reset, (size_t)a.B * a.T}, {state_out == a.state ? nullptr : a.state, ns}};
+    const Range out[] = {{y, n}, {state_out, ns}}, start = {a.state, ns};
+    if (any_clash(out, 2, in, 5) || clash(out, 1, &start, 1)) return TTT_ERR_ARG;
+    a.y = y;
+    a.state_out = state_out;
+    const int rc = ttt::launch_conv_fwd(a);
+    if (rc > 0) g_launches.fetch_add(rc, std::memory_order_relaxed);
+    return rc < 0 ? code(rc) : TTT_OK;
+}
+
+size_t ttt_short_conv_bwd_workspace(const ttt_short_conv_desc *desc)
+{
+    if (!desc || !conv_desc_ok(*desc) || desc->width > ttt::kConvMaxWidth || desc->B == 0 || desc->T == 0) return 0;
+    return ttt::conv_bwd_workspace(desc->B, desc->T, desc->C, desc->width);
+}
+
+ttt_status ttt_short_conv_bwd(const ttt_short_conv_desc *desc, const void *dy, const void *x, const float *weight,
+                              const float *bias, const unsigned char *reset, const void *state,
+                              const float *dstate_out, void *dx, float *dweight, float *dbias, float *dstate,
+                              void *workspace, size_t workspace_bytes, void *stream)
+{
+    ttt::ConvArgs a;
+    ttt_status st = conv_args(desc, x, weight, bias, reset, state, stream, a);
+    if (st != TTT_OK) return st;
+    const int es = a.bf16 ? 2 : 4;
+    for (const float *q : {dstate_out, (const float *)dweight, (const float *)dbias, (const float *)dstate})
+        if (q && !aligned(q, 4)) return TTT_ERR_ALIGN;
+    if (a.K == 1) {
+        dstate = nullptr;
+        dstate_out = nullptr;
+    }
+    const size_t nr = (size_t)a.B * (a.K - 1) * a.C, n = (size_t)a.B * a.T * a.C * es;
+    const size_t need = dweight || dbias ? ttt_short_conv_bwd_workspace(desc) : 0;
+    if (need && (!workspace || workspace_bytes < need)) return TTT_ERR_ARG;
+    if (need && !aligned(workspace, 16)) return TTT_ERR_ALIGN;
+    const bool empty = a.B == 0 || a.T == 0;
+    if (!empty) {
+        if (!dy || !dx) return TTT_ERR_ARG;
+        if (!aligned(dy, es) || !aligned(dx, es)) return TTT_ERR_ALIGN;
+    }
+    const Range in[] = {{x, empty ? 0 : rows_span(a.xs, a.B, a.T, a.C, es)}, {dy, empty ? 0 : rows_span(a.dys, a.B, a.T, a.C, es)},
+                        {weight, (size_t)a.C * a.K * 4}, {bias, (size_t)a.C * 4}, {reset, (size_t)a.B * a.T},
+                        {a.state, nr * es}, {dstate_out, nr * 4}};
+    const Range out[] = {{empty ? nullptr : dx, n}, {dweight, (size_t)a.C * a.K * 4}, {dbias, (size_t)a.C * 4}, {dstate, nr * 4},
+                         {need ? workspace : nullptr, need}};
+    if (any_clash(out, 5, in, 7)) return TTT_ERR_ARG;
+    if (empty) {
+        // no token: the states pass through, the parameters have no gradient
+        if ((st = copy_bytes(dstate, dstate_out, nr * 4, a.stream)) != TTT_OK) return st;
+        if ((st = copy_bytes(dweight, nullptr, (size_t)a.C * a.K * 4, a.stream)) != TTT_OK) return st;
+        return copy_bytes(dbias, nullptr, (size_t)a.C * 4, a.stream);
+    }
+    a.dy = dy;
+    a.dstate_out = dstate_out;
+    a.dx = dx;
+    a.dweight = dweight;
+    a.dbias = dbias;
+    a.dstate = dstate;
+    a.ws = workspace;
+    const int rc = ttt::launch_conv_bwd(a);
+    if (rc > 0) g_launches.fetch_add(rc, std::memory_order_relaxed);
+    return rc < 0 ? code(rc) : TTT_OK;
+}
+
+namespace {
+
+static_assert(ttt::kScanChunk == TTT_SCAN_CHUNK, "");
+
+bool scan_desc_ok(const ttt_scan_desc &D)
+{
+    if (D.B < 0 || D.T < 0 || D.C < 1 || D.N < 1 || D.G < 1 || D.C % D.G || D.softplus < 0 || D.softplus > 1) return false;
+    return D.io_dtype == TTT_F32 || D.io_dtype == TTT_BF16;
+}
+bool scan_desc_fits(const ttt_scan_desc &D)
+{
+    return D.N <= ttt::kScanMaxN && D.B <= 65535 && D.T <= 1 << 30 && (long long)D.C * D.N <= 0x7fff0000LL &&
+           (long long)D.B * D.T <= 0x7fff0000LL / D.G;
+}
+size_t scan_bc_span(const long long st[3], int B, int T, int G, int N, int es)
+{
+    return es * (size_t)(st[0] * (B - 1) + st[1] * (T - 1) + st[2] * (G - 1) + N);
+}
+
+// Checks the part both directions share and fills the launch arguments.
+ttt_status scan_args(const ttt_scan_desc *desc, const ttt_scan_params *params, const void *x, const void *delta,
+                     const void *Bm, const void *Cm, const void *z, const unsigned char *reset, void *stream, ttt::ScanArgs &a)
+{
+    if (!desc || !params || !scan_desc_ok(*desc)) return TTT_ERR_ARG;
+    const ttt_scan_desc &D = *desc;
+    for (int i = 0; i < 2; ++i)
+        if (D.x_stride[i] < 0 || D.delta_stride[i] < 0 || D.z_stride[i] < 0 || D.dy_stride[i] < 0) return TTT_ERR_ARG;
+    for (int i = 0; i < 3; ++i)
+        if (D.b_stride[i] < 0 || D.c_stride[i] < 0) return TTT_ERR_ARG;
+    if (!scan_desc_fits(D)) return TTT_ERR_UNSUPPORTED;
+    if (!params->A) return TTT_ERR_ARG;
+    for (const float *q : {params->A, params->D, params->delta_bias})
+        if (q && !aligned(q, 4)) return TTT_ERR_ALIGN;
+    const int es = D.io_dtype == TTT_BF16 ? 2 : 4;
+    if (D.B > 0 && D.T > 0)
+        for (const void *q : {x, delta, Bm, Cm}) {
+            if (!q) return TTT_ERR_ARG;
+            if (!aligned(q, es)) return TTT_ERR_ALIGN;
+        }
+    if (z && !aligned(z, es)) return TTT_ERR_ALIGN;
+    a = {};
+    a.B = D.B;
+    a.T = D.T;
+    a.C = D.C;
+    a.N = D.N;
+    a.G = D.G;
+    a.bf16 = D.io_dtype == TTT_BF16;
+    a.softplus = D.softplus;
+    a.x = x;
+    a.delta = delta;
+    a.z = z;
+    a.Bm = Bm;
+    a.Cm = Cm;
+    a.A = params->A;
+    a.D = params->D;
+    a.bias = params->delta_bias;
+    a.reset = reset;
+    const int n[3] = {D.B, D.T, D.G};
+    for (int i = 0; i < 2; ++i) {
+        a.xs[i] = n[i] > 1 ? D.x_stride[i] : 0;
+        a.ds[i] = n[i] > 1 ? D.delta_stride[i] : 0;
+        a.zs[i] = z && n[i] > 1 ? D.z_stride[i] : 0;
+    }
+    for (int i = 0; i < 3; ++i) {
+        a.bs[i] = n[i] > 1 ? D.b_stride[i] : 0;
+        a.cs[i] = n[i] > 1 ? D.c_stride[i] : 0;
+    }
+    a.stream = static_cast<cudaStream_t>(stream);
+    return TTT_OK;
+}
+
+// The nine inputs of a call with tokens, as memory ranges.
+void scan_inputs(const ttt::ScanArgs &a, Range *in)
+{
+    const int es = a.bf16 ? 2 : 4;
+    const size_t nv = (size_t)a.C * 4;
+    in[0] = {a.x, rows_span(a.xs, a.B, a.T, a.C, es)};
+    in[1] = {a.delta, rows_span(a.ds, a.B, a.T, a.C, es)};
+    in[2] = {a.z, rows_span(a.zs, a.B, a.T, a.C, es)};
+    in[3] = {a.Bm, scan_bc_span(a.bs, a.B, a.T, a.G, a.N, es)};
+    in[4] = {a.Cm, scan_bc_span(a.cs, a.B, a.T, a.G, a.N, es)};
+    in[5] = {a.reset, (size_t)a.B * a.T};
+    in[6] = {a.A, nv * a.N};
+    in[7] = {a.D, nv};
+    in[8] = {a.bias, nv};
+}
+
+}  // namespace
+
+size_t ttt_selective_scan_fwd_workspace(const ttt_scan_desc *desc)
+{
+    if (!desc || !scan_desc_ok(*desc) || !scan_desc_fits(*desc) || desc->B == 0 || desc->T == 0) return 0;
+    return ttt::scan_fwd_workspace(desc->B, desc->T, desc->C, desc->N, desc->G);
+}
+
+ttt_status ttt_selective_scan_fwd(const ttt_scan_desc *desc, const ttt_scan_params *params, const void *x,
+                                  const void *delta, const void *Bm, const void *Cm, const void *z,
+                                  const unsigned char *reset, const float *h0, void *y, float *h_last, float *states,
+                                  void *workspace, size_t workspace_bytes, void *stream)
+{
+    ttt::ScanArgs a;
+    const ttt_status st = scan_args(desc, params, x, delta, Bm, Cm, z, reset, stream, a);
+    if (st != TTT_OK) return st;
+    for (const float *q : {h0, (const float *)h_last, (const float *)states})
+        if (q && !aligned(q, 4)) return TTT_ERR_ALIGN;
+    const size_t nh = (size_t)a.B * a.C * a.N * 4;
+    if (h0 != h_last && h0 && h_last && overlaps(h0, nh, h_last, nh)) return TTT_ERR_ARG;
+    if (a.B == 0 || a.T == 0) return copy_bytes(h_last, h0, nh, a.stream);
+    const int es = a.bf16 ? 2 : 4;
+    if (!y) return TTT_ERR_ARG;
+    if (!aligned(y, es)) return TTT_ERR_ALIGN;
+    const size_t need = ttt_selective_scan_fwd_workspace(desc);
+    if (need && (!workspace || workspace_bytes < need)) return TTT_ERR_ARG;
+    if (need && !aligned(workspace, 16)) return TTT_ERR_ALIGN;
+    Range in[10];
+    scan_inputs(a, in);
+    in[9] = {h0 == h_last ? nullptr : h0, nh};
+    const size_t n = (size_t)a.B * a.T * a.C * es, ns = nh * ((a.T + ttt::kScanChunk - 1) / ttt::kScanChunk);
+    const Range out[] = {{y, n}, {states, ns}, {need ? workspace : nullptr, need}, {h_last, nh}}, start = {h0, nh};
+    if (any_clash(out, 4, in, 10) || clash(out, 3, &start, 1)) return TTT_ERR_ARG;
+    a.h0 = h0;
+    a.y = y;
+    a.h_last = h_last;
+    a.states = states;
+    a.ws = workspace;
+    const int rc = ttt::launch_scan_fwd(a);
+    if (rc > 0) g_launches.fetch_add(rc, std::memory_order_relaxed);
+    return rc < 0 ? code(rc) : TTT_OK;
+}
+
+size_t ttt_selective_scan_bwd_workspace(const ttt_scan_desc *desc)
+{
+    if (!desc || !scan_desc_ok(*desc) || !scan_desc_fits(*desc) || desc->B == 0 || desc->T == 0) return 0;
+    return ttt::scan_bwd_workspace(desc->B, desc->T, desc->C, desc->N, desc->G);
+}
+
+ttt_status ttt_selective_scan_bwd(const ttt_scan_desc *desc, const ttt_scan_params *params, const void *dy,
+                                  const void *x, const void *delta, const void *Bm, const void *Cm, const void *z,
+                                  const unsigned char *reset, const float *states, const float *dh_last, void *dx,
+                                  void *ddelta, void *dB, void *dC, void *dz, const ttt_scan_grads *grads, float *dh0,
+                                  void *workspace, size_t workspace_bytes, void *stream)
+{
+    ttt::ScanArgs a;
+    ttt_status st = scan_args(desc, params, x, delta, Bm, Cm, z, reset, stream, a);
+    if (st != TTT_OK) return st;
+    const ttt_scan_grads none = {}, &gr = grads ? *grads : none;
+    for (const float *q : {states, dh_last, (const float *)dh0, (const float *)gr.A, (const float *)gr.D, (const float *)gr.delta_bias})
+        if (q && !aligned(q, 4)) return TTT_ERR_ALIGN;
+    if ((gr.D && !a.D) || (gr.delta_bias && !a.bias)) return TTT_ERR_ARG;
+    const size_t nh = (size_t)a.B * a.C * a.N * 4, nv = (size_t)a.C * 4;
+    const bool empty = a.B == 0 || a.T == 0;
+    const int es = a.bf16 ? 2 : 4;
+    const size_t need = ttt_selective_scan_bwd_workspace(desc);
+    Range in[12] = {};
+    if (!empty) {
+        if (!dy || !states || !dx || !ddelta || !dB || !dC || (z != nullptr) != (dz != nullptr)) return TTT_ERR_ARG;
+        for (const void *q : {dy, (const void *)dx, (const void *)ddelta, (const void *)dB, (const void *)dC, (const void *)dz})
+            if (q && !aligned(q, es)) return TTT_ERR_ALIGN;
+        if (!workspace || workspace_bytes < need) return TTT_ERR_ARG;
+        if (!aligned(workspace, 16)) return TTT_ERR_ALIGN;
+        a.dys[0] = a.B > 1 ? desc->dy_stride[0] : 0;
+        a.dys[1] = a.T > 1 ? desc->dy_stride[1] : 0;
+        scan_inputs(a, in);
+        in[9] = {dy, rows_span(a.dys, a.B, a.T, a.C, es)};
+        in[10] = {states, nh * ((a.T + ttt::kScanChunk - 1) / ttt::kScanChunk)};
+    }
+    in[11] = {dh_last, nh};
+    const size_t n = empty ? 0 : (size_t)a.B * a.T * a.C * es, nbc = empty ? 0 : (size_t)a.B * a.T * a.G * a.N * es;
+    const Range out[] = {{empty ? nullptr : dx, n}, {empty ? nullptr : ddelta, n}, {empty ? nullptr : dz, n},
+                         {empty ? nullptr : dB, nbc}, {empty ? nullptr : dC, nbc}, {gr.A, nv * a.N}, {gr.D, nv},
+                         {gr.delta_bias, nv}, {dh0, nh}, {empty ? nullptr : workspace, need}};
+    if (any_clash(out, 10, in, 12)) return TTT_ERR_ARG;
+    if (empty) {
+        // no token: the states pass through, the parameters have no gradient
+        if ((st = copy_bytes(dh0, dh_last, nh, a.stream)) != TTT_OK) return st;
+        if ((st = copy_bytes(gr.A, nullptr, nv * a.N, a.stream)) != TTT_OK) return st;
+        if ((st = copy_bytes(gr.D, nullptr, nv, a.stream)) != TTT_OK) return st;
+        return copy_bytes(gr.delta_bias, nullptr, nv, a.stream);
+    }
+    a.dy = dy;
+    a.states = const_cast<float *>(states);
+    a.dh_last = dh_last;
+    a.dx = dx;
+    a.ddelta = ddelta;
+    a.dB = dB;
+    a.dC = dC;
+    a.dz = dz;
+    a.dA = gr.A;
+    a.dD = gr.D;
+    a.dbias = gr.delta_bias;
+    a.dh0 = dh0;
+    a.ws = workspace;
+    const int rc = ttt::launch_scan_bwd(a);
+    if (rc > 0) g_launches.fetch_add(rc, std::memory_order_relaxed);
+    return rc < 0 ? code(rc) : TTT_OK;
 }
 
 ttt_status ttt_sync_status(void *stream)

@@ -73,6 +73,10 @@ struct RopeArgs {
     const float *table;          // [table_rows][rot/2][2] cos, sin
     const long long *positions;  // or null: pos0 + t
     int *range_status;           // device status word of positions out of range
+    int axes = 0;                // > 0: several axes, positions [axes][..] or coordinates on the grid
+    long long axis_stride = 0;
+    int grid[4] = {};
+    const unsigned char *pair_axis = nullptr;  // host, [rot/2]
     cudaStream_t stream;
 };
 
@@ -104,6 +108,43 @@ struct RecurArgs {
     float *h_last, *states, *dh0;  // states: written by the forward, read by the backward
     int *status;                   // device status word (timeouts)
     unsigned long long test_stall_ns = 0;
+    cudaStream_t stream;
+};
+
+constexpr int kConvMaxWidth = 4;
+
+struct ConvArgs {
+    int B, T, C, K, bf16, silu;
+    const void *x, *dy;
+    long long xs[2], dys[2];
+    const float *weight, *bias;
+    const unsigned char *reset;
+    const void *state;         // [B][K-1][C] io dtype or null
+    void *y, *state_out;       // forward
+    const float *dstate_out;   // backward, [B][K-1][C] fp32 or null
+    void *dx;
+    float *dweight, *dbias, *dstate;
+    void *ws;
+    cudaStream_t stream;
+};
+
+constexpr int kScanChunk = 32;      // tokens from one stored state to the next
+constexpr int kScanMaxN = 64;
+constexpr int kScanStepTokens = 8;  // up to here token after token straight from memory
+
+struct ScanArgs {
+    int B, T, C, N, G, bf16, softplus;
+    const void *x, *delta, *z, *Bm, *Cm, *dy;
+    long long xs[2], ds[2], zs[2], dys[2], bs[3], cs[3];
+    const float *A, *D, *bias;
+    const unsigned char *reset;
+    const float *h0;
+    void *y;
+    float *h_last, *states;  // states: written by the forward, read by the backward
+    const float *dh_last;
+    void *dx, *ddelta, *dz, *dB, *dC;
+    float *dA, *dD, *dbias, *dh0;
+    void *ws;
     cudaStream_t stream;
 };
 
@@ -188,6 +229,18 @@ template <typename... KArgs> bool allow_shared(void (*kernel)(KArgs...), int byt
 
 int launch_rope(const RopeArgs &a);
 int launch_recurrence(const RecurArgs &a, bool backward);
+// how the scan's two directions cut a sequence: pieces, tokens of one
+struct ScanPieces {
+    int segs, len;
+};
+size_t conv_bwd_workspace(int B, int T, int C, int K);
+int launch_conv_fwd(const ConvArgs &a);
+int launch_conv_bwd(const ConvArgs &a);  // 2 kernels
+size_t scan_fwd_workspace(int B, int T, int C, int N, int G);
+size_t scan_bwd_workspace(int B, int T, int C, int N, int G);
+// each returns the number of its launches or a negative status
+int launch_scan_fwd(const ScanArgs &a);
+int launch_scan_bwd(const ScanArgs &a);
 int launch_block_norm_fwd(const BlockNormArgs &a);
 int launch_block_norm_bwd(const BlockNormArgs &a);
 int block_norm_bwd_blocks(int D, long long rows);  // partial sums per parameter gradient

@@ -35,53 +35,13 @@ struct RopeParams {
     int *range_status;
 };
 
+// One token's unit of features (at e0 and, if two, e1), turned by cs and sn where rotate, in
+// this block's share of the heads.
 template <typename T, int V, bool INTER, bool INV>
-__global__ void __launch_bounds__(1024) ttt_rope_kernel(const __grid_constant__ RopeParams p)
+__device__ __forceinline__ void turn_heads(const RopeParams &p, int b, int t, int e0, int e1, bool two, bool rotate,
+                                           const float (&cs)[V], const float (&sn)[V])
 {
     constexpr int HB = 4;  // heads whose loads are issued together
-    const int unit = threadIdx.x % p.units, slot = threadIdx.x / p.units;
-    const long long tok = (long long)blockIdx.x * p.tok_per_block + slot;
-    if (tok >= p.ntok) return;
-    const int b = (int)(tok / p.T), t = (int)(tok % p.T);
-    const int half = p.rot >> 1, rot_units = half / V;
-    const bool rotate = unit < rot_units;
-    int e0, e1;
-    if (rotate) {
-        e0 = INTER ? 2 * unit * V : unit * V;
-        e1 = INTER ? e0 + V : half + unit * V;
-    } else {
-        e0 = p.rot + 2 * (unit - rot_units) * V;
-        e1 = e0 + V;
-    }
-    const bool two = e1 < p.d;
-    float cs[V], sn[V];
-    if (rotate) {
-        long long pos = p.positions ? p.positions[b * p.pos_bstride + t] : p.pos0 + t;
-        const bool neg = pos < 0;
-        if (p.period > 0 && !neg)
-            pos = pos <= 0x7fffffffLL ? (long long)((unsigned)pos % (unsigned)p.period) : pos % p.period;
-        if (neg || pos >= p.rows) {
-            *p.range_status = 1;
-#pragma unroll
-            for (int j = 0; j < V; ++j) cs[j] = sn[j] = __int_as_float(0x7fffffff);
-        } else {
-            const float2 *row = reinterpret_cast<const float2 *>(p.table) + pos * half + unit * V;
-            if constexpr (V % 2 == 0) {
-#pragma unroll
-                for (int j = 0; j < V; j += 2) {
-                    const float4 w = __ldg(reinterpret_cast<const float4 *>(row + j));
-                    cs[j] = w.x;
-                    sn[j] = w.y;
-                    cs[j + 1] = w.z;
-                    sn[j + 1] = w.w;
-                }
-            } else {
-                const float2 w = __ldg(row);
-                cs[0] = w.x;
-                sn[0] = w.y;
-            }
-        }
-    }
     // heads of q, k and v in one row: this block's share [first, last)
     int first = blockIdx.y * p.heads_per_thread, last = first + p.heads_per_thread;
 #pragma unroll
@@ -135,6 +95,135 @@ __global__ void __launch_bounds__(1024) ttt_rope_kernel(const __grid_constant__ 
     }
 }
 
+template <typename T, int V, bool INTER, bool INV>
+__global__ void __launch_bounds__(1024) ttt_rope_kernel(const __grid_constant__ RopeParams p)
+{
+    const int unit = threadIdx.x % p.units, slot = threadIdx.x / p.units;
+    const long long tok = (long long)blockIdx.x * p.tok_per_block + slot;
+    if (tok >= p.ntok) return;
+    const int b = (int)(tok / p.T), t = (int)(tok % p.T);
+    const int half = p.rot >> 1, rot_units = half / V;
+    const bool rotate = unit < rot_units;
+    int e0, e1;
+    if (rotate) {
+        e0 = INTER ? 2 * unit * V : unit * V;
+        e1 = INTER ? e0 + V : half + unit * V;
+    } else {
+        e0 = p.rot + 2 * (unit - rot_units) * V;
+        e1 = e0 + V;
+    }
+    const bool two = e1 < p.d;
+    float cs[V], sn[V];
+    if (rotate) {
+        long long pos = p.positions ? p.positions[b * p.pos_bstride + t] : p.pos0 + t;
+        const bool neg = pos < 0;
+        if (p.period > 0 && !neg)
+            pos = pos <= 0x7fffffffLL ? (long long)((unsigned)pos % (unsigned)p.period) : pos % p.period;
+        if (neg || pos >= p.rows) {
+            *p.range_status = 1;
+#pragma unroll
+            for (int j = 0; j < V; ++j) cs[j] = sn[j] = __int_as_float(0x7fffffff);
+        } else {
+            const float2 *row = reinterpret_cast<const float2 *>(p.table) + pos * half + unit * V;
+            if constexpr (V % 2 == 0) {
+#pragma unroll
+                for (int j = 0; j < V; j += 2) {
+                    const float4 w = __ldg(reinterpret_cast<const float4 *>(row + j));
+                    cs[j] = w.x;
+                    sn[j] = w.y;
+                    cs[j + 1] = w.z;
+                    sn[j + 1] = w.w;
+                }
+            } else {
+                const float2 w = __ldg(row);
+                cs[0] = w.x;
+                sn[0] = w.y;
+            }
+        }
+    }
+    turn_heads<T, V, INTER, INV>(p, b, t, e0, e1, two, rotate, cs, sn);
+}
+
+// Several axes: pair i turns by the position of axis[i], whose column of the table has the
+// pair's own frequency.  Positions are given per axis or are the token's coordinates on a
+// row-major grid.
+constexpr int kRopeMaxAxes = 4;
+struct RopeAxesParams {
+    RopeParams r;
+    int axes, uniform;  // uniform: a unit's V pairs are of one axis
+    long long axis_stride;
+    int grid[kRopeMaxAxes];
+    unsigned char axis[512];
+};
+
+template <typename T, int V, bool INTER, bool INV>
+__global__ void __launch_bounds__(1024) ttt_rope_axes_kernel(const __grid_constant__ RopeAxesParams q)
+{
+    const RopeParams &p = q.r;
+    const int unit = threadIdx.x % p.units, slot = threadIdx.x / p.units;
+    const long long tok = (long long)blockIdx.x * p.tok_per_block + slot;
+    if (tok >= p.ntok) return;
+    const int b = (int)(tok / p.T), t = (int)(tok % p.T);
+    const int half = p.rot >> 1, rot_units = half / V;
+    const bool rotate = unit < rot_units;
+    int e0, e1;
+    if (rotate) {
+        e0 = INTER ? 2 * unit * V : unit * V;
+        e1 = INTER ? e0 + V : half + unit * V;
+    } else {
+        e0 = p.rot + 2 * (unit - rot_units) * V;
+        e1 = e0 + V;
+    }
+    float cs[V], sn[V];
+    if (rotate) {
+        long long pos[kRopeMaxAxes] = {};
+        if (p.positions) {
+#pragma unroll
+            for (int a = 0; a < kRopeMaxAxes; ++a)
+                if (a < q.axes) pos[a] = p.positions[a * q.axis_stride + b * p.pos_bstride + t];
+        } else {
+            // pos0 + t < 2^31: the grid was checked
+            unsigned i = (unsigned)(p.pos0 + t);
+#pragma unroll
+            for (int a = kRopeMaxAxes - 1; a > 0; --a)
+                if (a < q.axes) {
+                    const unsigned n = q.grid[a];
+                    pos[a] = i % n;
+                    i /= n;
+                }
+            pos[0] = i;
+        }
+        auto of = [&](int a) { return a == 0 ? pos[0] : a == 1 ? pos[1] : a == 2 ? pos[2] : pos[3]; };
+        const float2 *col = reinterpret_cast<const float2 *>(p.table) + unit * V;
+        const float nan = __int_as_float(0x7fffffff);
+        if (V % 2 == 0 && q.uniform) {
+            const long long at = of(q.axis[unit * V]);
+            const bool out = at < 0 || at >= p.rows;
+            if (out) *p.range_status = 1;
+#pragma unroll
+            for (int j = 0; j + 1 < V; j += 2) {
+                float4 w = make_float4(nan, nan, nan, nan);
+                if (!out) w = __ldg(reinterpret_cast<const float4 *>(col + at * half + j));
+                cs[j] = w.x;
+                sn[j] = w.y;
+                cs[j + 1] = w.z;
+                sn[j + 1] = w.w;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const long long at = of(q.axis[unit * V + j]);
+                float2 w = make_float2(nan, nan);
+                if (at < 0 || at >= p.rows) *p.range_status = 1;
+                else w = __ldg(col + at * half + j);
+                cs[j] = w.x;
+                sn[j] = w.y;
+            }
+        }
+    }
+    turn_heads<T, V, INTER, INV>(p, b, t, e0, e1, e1 < p.d, rotate, cs, sn);
+}
+
 template <typename T, int V>
 int launch_rope_v(const RopeParams &p, const RopeArgs &a)
 {
@@ -142,6 +231,24 @@ int launch_rope_v(const RopeParams &p, const RopeArgs &a)
     const int blocks = (int)((p.ntok + p.tok_per_block - 1) / p.tok_per_block);
     const dim3 grid(blocks, (heads + p.heads_per_thread - 1) / p.heads_per_thread);
     const int threads = p.units * p.tok_per_block;
+    if (a.axes) {
+        RopeAxesParams q = {};
+        q.r = p;
+        q.axes = a.axes;
+        q.axis_stride = a.axis_stride;
+        q.uniform = 1;
+        for (int i = 0; i < a.axes; ++i) q.grid[i] = a.grid[i];
+        for (int i = 0; i < a.rot / 2; ++i) {
+            q.axis[i] = a.pair_axis[i];
+            if (q.axis[i] != a.pair_axis[i / V * V]) q.uniform = 0;
+        }
+        if (a.interleaved)
+            if (a.inverse) ttt_rope_axes_kernel<T, V, true, true><<<grid, threads, 0, a.stream>>>(q);
+            else ttt_rope_axes_kernel<T, V, true, false><<<grid, threads, 0, a.stream>>>(q);
+        else if (a.inverse) ttt_rope_axes_kernel<T, V, false, true><<<grid, threads, 0, a.stream>>>(q);
+        else ttt_rope_axes_kernel<T, V, false, false><<<grid, threads, 0, a.stream>>>(q);
+        return cudaGetLastError() == cudaSuccess ? 0 : -4;
+    }
     if (a.interleaved)
         if (a.inverse) ttt_rope_kernel<T, V, true, true><<<grid, threads, 0, a.stream>>>(p);
         else ttt_rope_kernel<T, V, true, false><<<grid, threads, 0, a.stream>>>(p);

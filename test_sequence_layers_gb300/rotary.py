@@ -47,3 +47,32 @@ def rope_table(rows, rot, device="cuda", **scaling):
     inv, m = rope_frequencies(rot, **scaling)
     ang = torch.arange(rows, device=device, dtype=torch.float64)[:, None] * inv.to(device)
     return (m * torch.stack([ang.cos(), ang.sin()], -1)).float().contiguous()
+
+
+def rope_axes(sections, layout="blocks"):
+    """The axis of every pair, for ``abi.ttt_rope_axes``: sections[a] pairs turn by axis a,
+    one block after the other ("blocks") or the axes in turn for as long as each has pairs
+    left ("cyclic")."""
+    sections = [int(n) for n in sections]
+    if not sections or min(sections) < 0:
+        raise ValueError("sections must be the axes' numbers of pairs")
+    if layout == "blocks":
+        return bytes(a for a, n in enumerate(sections) for _ in range(n))
+    if layout == "cyclic":
+        return bytes(a for j in range(max(sections)) for a, n in enumerate(sections) if j < n)
+    raise ValueError('layout must be "blocks" or "cyclic"')
+
+
+def rope_axes_table(rows, pair_axis, per_axis=True, device="cuda", **scaling):
+    """The table of ``abi.ttt_rope_axes``, fp32 [rows, rot/2, 2].  per_axis: every axis has
+    the frequencies of a head of its own pairs alone (a picture's two halves); else pair i
+    keeps the frequency it has with one axis.  Keyword arguments as rope_frequencies, per
+    axis if per_axis."""
+    pair_axis = bytes(pair_axis)
+    inv, m = rope_frequencies(2 * len(pair_axis), **scaling)
+    if per_axis:
+        for a in set(pair_axis):
+            at = [i for i, b in enumerate(pair_axis) if b == a]
+            inv[at], m = rope_frequencies(2 * len(at), **scaling)
+    ang = torch.arange(rows, device=device, dtype=torch.float64)[:, None] * inv.to(device)
+    return (m * torch.stack([ang.cos(), ang.sin()], -1)).float().contiguous()
