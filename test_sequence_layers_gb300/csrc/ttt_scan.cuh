@@ -47,19 +47,25 @@ __device__ __forceinline__ float sigmoid(float v) { return rcp(1.f + ex2(-kLog2e
 
 // log(1 + e) for 0 <= e <= 1 as e P(e), P the Chebyshev interpolation of log(1 + e) / e in
 // e on [0, 1]: relative error below 2^-22, also where e is small.
+__host__ __device__ constexpr float log1p_term(int i)
+{
+    constexpr float c[] = {1.f, -4.999989271e-01f, 3.332971036e-01f, -2.495161593e-01f, 1.966327429e-01f,
+                           -1.526966691e-01f, 1.054362357e-01f, -5.637361109e-02f, 1.954252645e-02f, -3.176057013e-03f};
+    return c[i];
+}
 __device__ __forceinline__ float log1p_unit(float e)
 {
-    float p = -3.176057013e-03f;
-    p = fmaf(p, e, 1.954252645e-02f);
-    p = fmaf(p, e, -5.637361109e-02f);
-    p = fmaf(p, e, 1.054362357e-01f);
-    p = fmaf(p, e, -1.526966691e-01f);
-    p = fmaf(p, e, 1.966327429e-01f);
-    p = fmaf(p, e, -2.495161593e-01f);
-    p = fmaf(p, e, 3.332971036e-01f);
-    p = fmaf(p, e, -4.999989271e-01f);
-    p = fmaf(p, e, 1.f);
+    float p = log1p_term(9);
+#pragma unroll
+    for (int i = 8; i >= 0; --i) p = fmaf(p, e, log1p_term(i));
     return e * p;
+}
+__device__ __forceinline__ float2 log1p_unit(float2 e)
+{
+    float2 p = make_float2(log1p_term(9), log1p_term(9));
+#pragma unroll
+    for (int i = 8; i >= 0; --i) p = __ffma2_rn(p, e, make_float2(log1p_term(i), log1p_term(i)));
+    return __fmul2_rn(e, p);
 }
 
 // max(v, 0) + log(1 + exp(-|v|)); e = exp(-|v|) for the slope.  Nothing overflows.
@@ -85,6 +91,54 @@ template <typename T> __device__ __forceinline__ void put(T *p, float x)
     const float v[1] = {x};
     pack(q, v);
     q.store(p);
+}
+
+// Rates of V values, two at a time (the polynomial is most of the work).
+template <int V> __device__ __forceinline__ void softplus_all(float (&v)[V])
+{
+    if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int j = 0; j < V; j += 2) {
+            const float2 e = make_float2(ex2(-kLog2e * fabsf(v[j])), ex2(-kLog2e * fabsf(v[j + 1])));
+            const float2 l = log1p_unit(e);
+            v[j] = v[j] > 0.f ? v[j] + l.x : v[j] <= 0.f ? l.x : v[j];  // NaN stays
+            v[j + 1] = v[j + 1] > 0.f ? v[j + 1] + l.y : v[j + 1] <= 0.f ? l.y : v[j + 1];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            float e;
+            v[j] = softplus(v[j], e);
+        }
+    }
+}
+
+// V floats to or from shared memory, four at a time where there are four.
+template <int V> __device__ __forceinline__ void put_floats(float *p, const float (&v)[V])
+{
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+        for (int j = 0; j < V; j += 4) *reinterpret_cast<float4 *>(p + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) p[j] = v[j];
+    }
+}
+template <int V> __device__ __forceinline__ void get_floats(const float *p, float (&v)[V])
+{
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+        for (int j = 0; j < V; j += 4) {
+            const float4 q = *reinterpret_cast<const float4 *>(p + j);
+            v[j] = q.x;
+            v[j + 1] = q.y;
+            v[j + 2] = q.z;
+            v[j + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = p[j];
+    }
 }
 
 // Sums of M values over the L lanes that differ in the bits S, 2 S, .. (L/2) S of the lane
@@ -158,10 +212,12 @@ __device__ __forceinline__ void step(Quad &h, float d, float u, const Quad &A, f
     h.a = __ffma2_rn(a.a, h.a, __fmul2_rn(uu, make_float2(Bt.x, Bt.y)));
     h.b = __ffma2_rn(a.b, h.b, __fmul2_rn(uu, make_float2(Bt.z, Bt.w)));
 }
-__device__ __forceinline__ float dot(const Quad &h, float4 Ct)
+// s += C . h, two and two (first: s = C . h)
+__device__ __forceinline__ void dot(float2 &s, const Quad &h, float4 Ct, bool first)
 {
-    const float2 s = __ffma2_rn(h.a, make_float2(Ct.x, Ct.y), __fmul2_rn(h.b, make_float2(Ct.z, Ct.w)));
-    return s.x + s.y;
+    const float2 lo = make_float2(Ct.x, Ct.y);
+    s = first ? __fmul2_rn(h.a, lo) : __ffma2_rn(h.a, lo, s);
+    s = __ffma2_rn(h.b, make_float2(Ct.z, Ct.w), s);
 }
 
 

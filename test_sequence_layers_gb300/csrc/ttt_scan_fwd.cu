@@ -15,7 +15,9 @@ namespace {
 using namespace scan;
 
 constexpr int kTile = kScanChunk;  // tokens staged at a time: a chunk between stored states
-constexpr int kCB = 16;            // channels of a block: 32 bytes of a bf16 row, one sector
+template <bool V> struct Is {
+    static constexpr bool value = V;
+};
 
 // ------------------------------------------------------------------ a few tokens
 //
@@ -51,7 +53,9 @@ template <typename T, int LN> __global__ void __launch_bounds__(128) ttt_scan_st
         float d = get(dl + t * p.ds[1]) + bias, e;
         if (p.softplus) d = softplus(d, e);
         step(h, d, d * xv, A, Bt);
-        float y = dot(h, Ct);
+        float2 s2;
+        dot(s2, h, Ct, true);
+        float y = s2.x + s2.y;
 #pragma unroll
         for (int s = LN / 2; s > 0; s >>= 1) y += __shfl_xor_sync(0xffffffffu, y, s);
         y = fmaf(D, xv, y);
@@ -63,199 +67,207 @@ template <typename T, int LN> __global__ void __launch_bounds__(128) ttt_scan_st
 
 // ------------------------------------------------------------------------- tiles
 //
-// A block takes kCB channels of a group and one piece of the sequence, a tile of tokens at a
-// time: rates, inputs, B and C go to shared memory in fp32 once, then every warp scans its
-// 32 / LN channels with LN lanes a channel (the upper lane bits, so that lanes next to each
-// other read the same B and C), then the outputs get D x and the gate.  The next tile's
-// tensors are on their way in registers during the scan.
+// A lane keeps 4 Q states of a channel in registers, LN lanes a channel (the upper lane bits,
+// so that lanes next to each other read the same B and C), a warp 32 / LN neighbouring
+// channels, a block four warps of a group's channels and one piece of the sequence.  B and C
+// go to shared memory in fp32, a tile of tokens at a time and one tile ahead; x, delta and z
+// come straight from memory, kAt tokens ahead.
 // SUM: only the piece's map, from a zero state (its sum of rates, its own contribution).
-template <typename T, int LN, bool VEC, bool SUM>
-__global__ void __launch_bounds__(kCB *LN) ttt_scan_fwd_kernel(const __grid_constant__ Params p)
-{
-    constexpr int kThreads = kCB * LN, CL = 32 / LN, NP = 4 * LN;
-    constexpr int V = VEC ? 16 / (int)sizeof(T) : 1;      // elements of one access
-    constexpr int kRowVecs = kCB / V, kVecs = kTile * kRowVecs, kIt = (kVecs + kThreads - 1) / kThreads;
-    constexpr int kBV = V < NP ? V : NP, kBVecs = kTile * NP / kBV, kBIt = (kBVecs + kThreads - 1) / kThreads;
-    constexpr int kYPitch = 24;                           // rows of outputs on different banks
-    __shared__ float2 du[kTile][kCB];
-    __shared__ __align__(16) float bs[kTile][NP];
-    __shared__ __align__(16) float cs[SUM ? 1 : kTile][NP];
-    __shared__ __align__(16) float ys[SUM ? 1 : kTile][kYPitch];
+constexpr int kWarps = 4;
 
-    const int g = blockIdx.x / p.blocks, c0 = g * p.cpg + (blockIdx.x % p.blocks) * kCB;
-    const int cend = (g + 1) * p.cpg, seg = blockIdx.y, b = blockIdx.z;
+template <typename T, int LN, int Q, bool VEC, bool SUM>
+__global__ void __launch_bounds__(32 * kWarps, 4) ttt_scan_fwd_kernel(const __grid_constant__ Params p)
+{
+    constexpr int NT = 32 * kWarps, CL = 32 / LN, CB = kWarps * CL, NP = 4 * LN * Q, kAt = 4;
+    constexpr int V = VEC ? 16 / (int)sizeof(T) : 1;  // elements of one access of B and C
+    constexpr int kVecs = kTile * NP / V, kIt = (kVecs + NT - 1) / NT;
+    __shared__ __align__(16) float bs[2][kTile][NP];
+    __shared__ __align__(16) float cs[SUM ? 1 : 2][SUM ? 1 : kTile][NP];
+
+    const int g = blockIdx.x / p.blocks, cend = (g + 1) * p.cpg, seg = blockIdx.y, b = blockIdx.z;
     const int tb = seg * p.seg_len, te = min(p.T, tb + p.seg_len);
     const int tid = threadIdx.x, lane = tid & 31;
-    const int cl = tid / 32 * CL + lane % CL, n0 = 4 * (lane / CL), c = c0 + cl;
+    const int n0 = 4 * (lane / CL);  // this lane's states: n0 + 4 LN q .. + 3
+    int c = g * p.cpg + (blockIdx.x % p.blocks) * CB + tid / 32 * CL + lane % CL;
     const bool on = c < cend;
+    if (!on) c = cend - 1;  // (reads what it may, writes nothing)
 
-    const T *x = static_cast<const T *>(p.x) + b * p.xs[0], *dl = static_cast<const T *>(p.delta) + b * p.ds[0];
-    const T *z = static_cast<const T *>(p.z) + b * p.zs[0];
+    const T *x = static_cast<const T *>(p.x) + b * p.xs[0] + c, *dl = static_cast<const T *>(p.delta) + b * p.ds[0] + c;
+    const T *z = static_cast<const T *>(p.z) + b * p.zs[0] + c;
+    const bool gated = p.z;
     const T *Bm = static_cast<const T *>(p.Bm) + b * p.bs[0] + g * p.bs[2], *Cm = static_cast<const T *>(p.Cm) + b * p.cs[0] + g * p.cs[2];
     const unsigned char *reset = p.reset ? p.reset + (size_t)b * p.T : nullptr;
+    T *y = static_cast<T *>(p.y) + (size_t)b * p.T * p.C + c;
+    const float bias = p.bias ? p.bias[c] : 0.f, D = p.D ? p.D[c] : 0.f;
 
-    Quad A = quad(make_float4(0.f, 0.f, 0.f, 0.f)), h = A;
-    if (on) {
-        A = quad(load_states(p.A + (size_t)c * p.N, n0, p.N, 0.f));
-        A.a = __fmul2_rn(A.a, make_float2(kLog2e, kLog2e));
-        A.b = __fmul2_rn(A.b, make_float2(kLog2e, kLog2e));
-        if (!SUM && p.start) h = quad(load_states(p.start + (((size_t)b * p.segs + seg) * p.C + c) * p.N, n0, p.N, 0.f));
+    const Quad zero = quad(make_float4(0.f, 0.f, 0.f, 0.f));
+    Quad A[Q], h[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        A[q] = quad(load_states(p.A + (size_t)c * p.N, n0 + 4 * LN * q, p.N, 0.f));
+        A[q].a = __fmul2_rn(A[q].a, make_float2(kLog2e, kLog2e));
+        A[q].b = __fmul2_rn(A[q].b, make_float2(kLog2e, kLog2e));
+        h[q] = zero;
+        if (!SUM && p.start) h[q] = quad(load_states(p.start + (((size_t)b * p.segs + seg) * p.C + c) * p.N, n0 + 4 * LN * q, p.N, 0.f));
     }
 
-    // the tile's raw tensors
-    Pack<T, V> px[kIt], pd[kIt], pz[SUM ? 1 : kIt];
-    Pack<T, kBV> pb[kBIt], pc[SUM ? 1 : kBIt];
+    Pack<T, V> pb[kIt], pc[SUM ? 1 : kIt];
     auto fetch = [&](int t0) {
 #pragma unroll
         for (int i = 0; i < kIt; ++i) {
-            const int v = tid + i * kThreads, t = t0 + v / kRowVecs, ch = c0 + v % kRowVecs * V;
-            px[i].raw = pd[i].raw = {};
-            if constexpr (!SUM) pz[i].raw = {};
-            if ((kVecs % kThreads == 0 || v < kVecs) && t < te && ch < cend) {
-                px[i].load(x + t * p.xs[1] + ch);
-                pd[i].load(dl + t * p.ds[1] + ch);
-                if constexpr (!SUM)
-                    if (p.z) pz[i].load(z + t * p.zs[1] + ch);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kBIt; ++i) {
-            const int v = tid + i * kThreads, t = t0 + v / (NP / kBV), n = v % (NP / kBV) * kBV;
+            const int v = tid + i * NT, t = t0 + v / (NP / V), n = v % (NP / V) * V;
             pb[i].raw = {};
             if constexpr (!SUM) pc[i].raw = {};
-            if ((kBVecs % kThreads == 0 || v < kBVecs) && t < te && n < p.N) {
+            if ((kVecs % NT == 0 || v < kVecs) && t < te && n < p.N) {
                 pb[i].load(Bm + t * p.bs[1] + n);
                 if constexpr (!SUM) pc[i].load(Cm + t * p.cs[1] + n);
             }
         }
     };
-    float bias[V], Dv[V];
-    // (a thread's channels are the same in every pass: kThreads is a multiple of a row's vectors)
-    static_assert(kThreads % kRowVecs == 0, "");
-    {
-        const int ch = c0 + tid % kRowVecs * V;
+    auto stage = [&](int buf) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            bias[j] = p.bias && ch + j < cend ? p.bias[ch + j] : 0.f;
-            Dv[j] = p.D && ch + j < cend ? p.D[ch + j] : 0.f;
+        for (int i = 0; i < kIt; ++i) {
+            const int v = tid + i * NT, t = v / (NP / V), n = v % (NP / V) * V;
+            if (kVecs % NT && v >= kVecs) break;
+            float f[V];
+            unpack(pb[i], f);
+            put_floats(&bs[buf][t][n], f);
+            if constexpr (!SUM) {
+                unpack(pc[i], f);
+                put_floats(&cs[buf][t][n], f);
+            }
         }
-    }
-    float rate_sum = 0.f;  // SUM: of this thread's tokens and channel pieces
+    };
+    // kAt tokens of the lane's channel from x, dl, z on, zeros past the end
+    Pack<T, 1> px[kAt], pd[kAt], pz[SUM ? 1 : kAt];
+    const long long xs = p.xs[1], dls = p.ds[1], zs = p.zs[1];
+    x += tb * xs;
+    dl += tb * dls;
+    z += tb * zs;
+    y += (size_t)tb * p.C;
+    auto load = [&](int t0) {
+        if (t0 + kAt <= te) {
+#pragma unroll
+            for (int k = 0; k < kAt; ++k) {
+                px[k].load(x + k * xs);
+                pd[k].load(dl + k * dls);
+                if constexpr (!SUM)
+                    if (gated) pz[k].load(z + k * zs);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kAt; ++k) {
+                px[k].raw = pd[k].raw = {};
+                if constexpr (!SUM) pz[k].raw = {};
+                if (t0 + k < te) {
+                    px[k].load(x + k * xs);
+                    pd[k].load(dl + k * dls);
+                    if constexpr (!SUM)
+                        if (gated) pz[k].load(z + k * zs);
+                }
+            }
+        }
+        x += kAt * xs;
+        dl += kAt * dls;
+        if constexpr (!SUM) z += kAt * zs;
+    };
+    float rate_sum = 0.f;
     unsigned any_cut = 0;
 
     fetch(tb);
-    for (int t0 = tb; t0 < te; t0 += kTile) {
+    load(tb);
+    stage(0);
+    __syncthreads();
+    int buf = 0;
+    for (int t0 = tb; t0 < te; t0 += kTile, buf ^= 1) {
         const int nt = min(kTile, te - t0);
+        const bool more = t0 + kTile < te;
+        if (more) fetch(t0 + kTile);
         if (!SUM && p.states && on)
-            store_states(p.states + (((size_t)b * p.chunks + t0 / kScanChunk) * p.C + c) * p.N, n0, p.N, four(h));
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+                store_states(p.states + (((size_t)b * p.chunks + t0 / kScanChunk) * p.C + c) * p.N, n0 + 4 * LN * q, p.N, four(h[q]));
         unsigned cut = 0;  // tokens of the tile with a reset
         if (reset) cut = __ballot_sync(0xffffffffu, lane < nt && reset[t0 + lane]);
         any_cut |= cut;
-        float xf[kIt][V];
-#pragma unroll
-        for (int i = 0; i < kIt; ++i) {
-            const int v = tid + i * kThreads, t = v / kRowVecs, ch = v % kRowVecs * V;
-            if (kVecs % kThreads && v >= kVecs) break;
-            float d[V];
-            unpack(px[i], xf[i]);
-            unpack(pd[i], d);
-            const bool live = t < nt && c0 + ch < cend;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                float e;
-                d[j] += bias[j];
-                if (p.softplus) d[j] = softplus(d[j], e);
-                if (!live) d[j] = 0.f;  // past the end: the state stays
-                du[t][ch + j] = make_float2(d[j], d[j] * xf[i][j]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kBIt; ++i) {
-            const int v = tid + i * kThreads, t = v / (NP / kBV), n = v % (NP / kBV) * kBV;
-            if (kBVecs % kThreads && v >= kBVecs) break;
-            float f[kBV];
-            unpack(pb[i], f);
-#pragma unroll
-            for (int j = 0; j < kBV; ++j) bs[t][n + j] = f[j];
-            if constexpr (!SUM) {
-                unpack(pc[i], f);
-#pragma unroll
-                for (int j = 0; j < kBV; ++j) cs[t][n + j] = f[j];
-            }
-        }
-        float zf[SUM ? 1 : kIt][V];
-        if constexpr (!SUM)
-#pragma unroll
-            for (int i = 0; i < kIt; ++i) unpack(pz[i], zf[i]);
-        if (t0 + kTile < te) fetch(t0 + kTile);
-        __syncthreads();
-        if constexpr (SUM) {
-#pragma unroll 4
-            for (int t = 0; t < kTile; ++t) {
-                const float2 w = du[t][cl];
-                if (cut >> t & 1) {
-                    h = quad(make_float4(0.f, 0.f, 0.f, 0.f));
-                    rate_sum = 0.f;
-                }
-                step(h, w.x, w.y, A, *reinterpret_cast<const float4 *>(&bs[t][n0]));
-                rate_sum += w.x;
-            }
-            __syncthreads();
-        } else {
 #pragma unroll 1
-            for (int t = 0; t < kTile; t += 4) {
-                float yv[4];
-                if (cut >> t & 15) {
+        for (int t = 0; t < nt; t += kAt) {
+            float d[kAt], u[kAt], xf[kAt], zf[kAt];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 w = du[t + k][cl];
-                        if (cut >> (t + k) & 1) h = quad(make_float4(0.f, 0.f, 0.f, 0.f));
-                        step(h, w.x, w.y, A, *reinterpret_cast<const float4 *>(&bs[t + k][n0]));
-                        yv[k] = dot(h, *reinterpret_cast<const float4 *>(&cs[t + k][n0]));
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 w = du[t + k][cl];
-                        step(h, w.x, w.y, A, *reinterpret_cast<const float4 *>(&bs[t + k][n0]));
-                        yv[k] = dot(h, *reinterpret_cast<const float4 *>(&cs[t + k][n0]));
-                    }
+            for (int k = 0; k < kAt; ++k) {
+                float v[1];
+                unpack(px[k], v);
+                xf[k] = v[0];
+                unpack(pd[k], v);
+                d[k] = v[0] + bias;
+                if constexpr (!SUM) {
+                    unpack(pz[k], v);
+                    zf[k] = v[0];
                 }
-                spread_sum<4, LN, CL>(yv);
-                // LN lanes hold the four tokens' sums: 4 / LN each, or LN / 4 lanes the same one
-                constexpr int K = LN < 4 ? 4 / LN : 1, dup = LN > 4 ? LN / 4 : 1;
-                const int at = lane / CL / dup * K;
-                if (lane / CL % dup == 0)
-#pragma unroll
-                    for (int k = 0; k < K; ++k) ys[t + at + k][cl] = yv[k];
             }
-            __syncthreads();
+            load(t0 + t + kAt);
+            if (p.softplus) softplus_all(d);
+            if (t + kAt > nt)
 #pragma unroll
-            for (int i = 0; i < kIt; ++i) {
-                const int v = tid + i * kThreads, t = v / kRowVecs, ch = v % kRowVecs * V;
-                if (kVecs % kThreads && v >= kVecs) break;
-                if (t >= nt || c0 + ch >= cend) continue;
-                float o[V];
+                for (int k = 0; k < kAt; ++k)
+                    if (t + k >= nt) d[k] = 0.f;  // past the end: the state stays
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    o[j] = fmaf(Dv[j], xf[i][j], ys[t][ch + j]);
-                    if (p.z) o[j] *= zf[i][j] * sigmoid(zf[i][j]);
+            for (int k = 0; k < kAt; ++k) u[k] = d[k] * xf[k];
+            float o[kAt];
+            auto tokens = [&](auto resets) {
+#pragma unroll
+                for (int k = 0; k < kAt; ++k) {
+                    if (decltype(resets)::value && (cut >> (t + k) & 1)) {
+#pragma unroll
+                        for (int q = 0; q < Q; ++q) h[q] = zero;
+                        rate_sum = 0.f;
+                    }
+                    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) {
+                        step(h[q], d[k], u[k], A[q], *reinterpret_cast<const float4 *>(&bs[buf][t + k][n0 + 4 * LN * q]));
+                        if constexpr (!SUM) dot(s, h[q], *reinterpret_cast<const float4 *>(&cs[buf][t + k][n0 + 4 * LN * q]), q == 0);
+                    }
+                    if constexpr (SUM) {
+                        rate_sum += d[k];
+                    } else {
+                        o[k] = s.x + s.y;
+#pragma unroll
+                        for (int i = CL; i < 32; i *= 2) o[k] += __shfl_xor_sync(0xffffffffu, o[k], i);
+                        const float w = gated ? zf[k] * sigmoid(zf[k]) : 1.f;
+                        o[k] = fmaf(D, xf[k], o[k]) * w;
+                    }
                 }
-                Pack<T, V> q;
-                pack(q, o);
-                q.store(static_cast<T *>(p.y) + ((size_t)b * p.T + t0 + t) * p.C + c0 + ch);
+            };
+            if (cut >> t & 15) tokens(Is<true>());
+            else tokens(Is<false>());
+            if constexpr (!SUM) {
+                if (on && (LN == 1 || n0 == 0)) {
+                    if (t + kAt <= nt) {
+#pragma unroll
+                        for (int k = 0; k < kAt; ++k) put(y + (size_t)k * p.C, o[k]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < kAt; ++k)
+                            if (t + k < nt) put(y + (size_t)k * p.C, o[k]);
+                    }
+                }
+                y += (size_t)kAt * p.C;
             }
         }
+        if (more) stage(buf ^ 1);
+        __syncthreads();
     }
+    if (!on) return;
     if constexpr (SUM) {
         const size_t at = ((size_t)b * p.segs + seg) * p.C + c;
-        if (on) {
-            store_states(p.H + at * p.N, n0, p.N, four(h));
-            if (n0 == 0) p.rate_sum[at] = rate_sum;
-        }
+#pragma unroll
+        for (int q = 0; q < Q; ++q) store_states(p.H + at * p.N, n0 + 4 * LN * q, p.N, four(h[q]));
+        if (n0 == 0) p.rate_sum[at] = rate_sum;
         if (blockIdx.x == 0 && tid == 0) p.cut[b * p.segs + seg] = any_cut != 0;
-    } else if (p.y_state && on && seg == p.segs - 1) {
-        store_states(p.y_state + ((size_t)b * p.C + c) * p.N, n0, p.N, four(h));
+    } else if (p.y_state && seg == p.segs - 1) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) store_states(p.y_state + ((size_t)b * p.C + c) * p.N, n0 + 4 * LN * q, p.N, four(h[q]));
     }
 }
 
@@ -278,51 +290,57 @@ __global__ void __launch_bounds__(256) ttt_scan_join_kernel(const __grid_constan
     }
 }
 
-template <typename T, int LN, bool VEC> int launch_tiles(Params &p, const ScanArgs &a)
+// The tile kernel's lanes of a channel: 8 or 16 states a lane.
+constexpr int tile_lanes(int N) { return N <= 16 ? 1 : N <= 32 ? 2 : 4; }
+
+template <typename T, int LN, int Q, bool VEC> int launch_tiles(Params &p, const ScanArgs &a)
 {
-    p.blocks = (p.cpg + kCB - 1) / kCB;
+    constexpr int CB = kWarps * 32 / LN;
+    p.blocks = (p.cpg + CB - 1) / CB;
     const dim3 grid(p.G * p.blocks, p.segs, p.B);
     if (p.segs > 1) {
         const dim3 part(grid.x, p.segs - 1, p.B);
-        ttt_scan_fwd_kernel<T, LN, VEC, true><<<part, kCB * LN, 0, a.stream>>>(p);
+        ttt_scan_fwd_kernel<T, LN, Q, VEC, true><<<part, 32 * kWarps, 0, a.stream>>>(p);
         const dim3 jg((unsigned)(((long long)p.C * p.N + 255) / 256), p.B);
         ttt_scan_join_kernel<<<jg, 256, 0, a.stream>>>(p, a.h0);
         p.start = p.H;
     }
-    ttt_scan_fwd_kernel<T, LN, VEC, false><<<grid, kCB * LN, 0, a.stream>>>(p);
+    ttt_scan_fwd_kernel<T, LN, Q, VEC, false><<<grid, 32 * kWarps, 0, a.stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? (p.segs > 1 ? 3 : 1) : -4;
 }
 
-template <typename T, int LN> int launch_lanes(Params &p, const ScanArgs &a, bool vec)
+template <typename T, int LN> int launch_step(Params &p, const ScanArgs &a)
 {
-    if (p.T <= kScanStepTokens) {
-        const dim3 grid((unsigned)(((long long)p.C * LN + 127) / 128), p.B);
-        ttt_scan_step_kernel<T, LN><<<grid, 128, 0, a.stream>>>(p);
-        return cudaGetLastError() == cudaSuccess ? 1 : -4;
-    }
-    return vec ? launch_tiles<T, LN, true>(p, a) : launch_tiles<T, LN, false>(p, a);
+    const dim3 grid((unsigned)(((long long)p.C * LN + 127) / 128), p.B);
+    ttt_scan_step_kernel<T, LN><<<grid, 128, 0, a.stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? 1 : -4;
 }
 
 template <typename T> int launch_type(Params &p, const ScanArgs &a, bool vec)
 {
-    switch (lanes(p.N)) {
-    case 2: return launch_lanes<T, 2>(p, a, vec);
-    case 4: return launch_lanes<T, 4>(p, a, vec);
-    case 8: return launch_lanes<T, 8>(p, a, vec);
-    default: return launch_lanes<T, 16>(p, a, vec);
+    if (p.T <= kScanStepTokens) {
+        switch (lanes(p.N)) {
+        case 2: return launch_step<T, 2>(p, a);
+        case 4: return launch_step<T, 4>(p, a);
+        case 8: return launch_step<T, 8>(p, a);
+        default: return launch_step<T, 16>(p, a);
+        }
+    }
+    if (p.N <= 8) return vec ? launch_tiles<T, 1, 2, true>(p, a) : launch_tiles<T, 1, 2, false>(p, a);
+    switch (tile_lanes(p.N)) {
+    case 1: return vec ? launch_tiles<T, 1, 4, true>(p, a) : launch_tiles<T, 1, 4, false>(p, a);
+    case 2: return vec ? launch_tiles<T, 2, 4, true>(p, a) : launch_tiles<T, 2, 4, false>(p, a);
+    default: return vec ? launch_tiles<T, 4, 4, true>(p, a) : launch_tiles<T, 4, 4, false>(p, a);
     }
 }
 
-}  // namespace
-
-namespace {
-
-// Pieces of the sequence: as many as give every scheduler two warps, of 256 tokens and more.
+// Pieces of the sequence: as many as fill the SMs with the 16 warps that each holds, of 64
+// tokens and more.
 ScanPieces pieces(int B, int T, int C, int N, int G)
 {
-    const int LN = scan::lanes(N), chunks = (T + kScanChunk - 1) / kScanChunk;
-    const long long warps = (long long)B * G * ((C / G + kCB - 1) / kCB) * kCB * LN / 32;
-    return scan::cut(chunks, warps, 8LL * 152, 8);
+    const int CL = 32 / tile_lanes(N), chunks = (T + kScanChunk - 1) / kScanChunk;
+    const long long warps = (long long)B * G * ((C / G + CL - 1) / CL);
+    return scan::cut(chunks, warps, 16LL * 152, 2);
 }
 
 }  // namespace

@@ -34,11 +34,60 @@ __device__ __forceinline__ float sigmoid(float v)
     return r;
 }
 
+// acc += a b, two and two where V is even.
+template <int V> __device__ __forceinline__ void fma_all(float (&acc)[V], const float (&a)[V], const float (&b)[V])
+{
+    if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int j = 0; j < V; j += 2) {
+            const float2 r = __ffma2_rn(make_float2(a[j], a[j + 1]), make_float2(b[j], b[j + 1]), make_float2(acc[j], acc[j + 1]));
+            acc[j] = r.x;
+            acc[j + 1] = r.y;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[j] = fmaf(a[j], b[j], acc[j]);
+    }
+}
+template <int V> __device__ __forceinline__ void clear(float (&v)[V])
+{
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = 0.f;
+}
+
 template <typename T, int V> __device__ __forceinline__ void load_row(const T *p, float (&v)[V])
 {
     Pack<T, V> q;
     q.load(p);
     unpack(q, v);
+}
+
+// The taps of V neighbouring channels ([C,K] fp32), 16 bytes at a time where they lie so.
+template <int V, int K> __device__ __forceinline__ void load_taps(const float *w, float (&v)[K][V])
+{
+    float f[V * K];
+    if constexpr (V * K % 4 == 0) {
+        if ((reinterpret_cast<uintptr_t>(w) & 15) == 0) {
+#pragma unroll
+            for (int i = 0; i < V * K; i += 4) {
+                const float4 q = __ldg(reinterpret_cast<const float4 *>(w + i));
+                f[i] = q.x;
+                f[i + 1] = q.y;
+                f[i + 2] = q.z;
+                f[i + 3] = q.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V * K; ++i) f[i] = __ldg(w + i);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V * K; ++i) f[i] = __ldg(w + i);
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k][j] = f[j * K + k];
 }
 
 // Rows t - (K-1) .. t - 1 before a piece (win[i] is row t - K + 1 + i) as the token t sees
@@ -85,12 +134,9 @@ template <typename T, int V, int K> __global__ void __launch_bounds__(kThreads) 
     T *y = static_cast<T *>(p.y) + (size_t)b * p.T * p.C + c;
 
     float w[K][V], bias[V], win[K][V];
+    load_taps<V, K>(p.weight + (size_t)c * K, w);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) w[k][j] = p.weight[(size_t)(c + j) * K + k];
-        bias[j] = p.bias ? p.bias[c + j] : 0.f;
-    }
+    for (int j = 0; j < V; ++j) bias[j] = p.bias ? p.bias[c + j] : 0.f;
     rows_before<T, V, K>(p, x, state, reset, t0, win);
     // The state behind the last token, by the thread that has read the one before the first
     // (they may be one array).
@@ -112,35 +158,50 @@ template <typename T, int V, int K> __global__ void __launch_bounds__(kThreads) 
 #pragma unroll
         for (int k = 0; k < K - 1; ++k) last[k].store(out + k * p.C);
     }
-    // kAhead rows are loaded together; the window turns in place over K of them
+    // kAhead rows are on their way while the ones before them are worked on; the window turns
+    // in place over K of them: row t + a goes to place (a + K - 1) % K, row t + a - K + 1 is at
+    // a % K
     constexpr int kAhead = K == 3 ? 3 : 4;
-    for (int t = t0; t < t1; t += kAhead) {
-        Pack<T, V> q[kAhead];
+    Pack<T, V> q[kAhead], r[kAhead];
+    const T *xt = x + t0 * p.xs[1];
+    T *yt = y + (size_t)t0 * p.C;
+    auto load = [&](int t) {
 #pragma unroll
         for (int a = 0; a < kAhead; ++a)
-            if (t + a < t1) q[a].load(x + (t + a) * p.xs[1]);
+            if (t + a < t1) r[a].load(xt + a * p.xs[1]);
+        xt += kAhead * p.xs[1];
+    };
+    auto token = [&](int a, int t) {
+        if (reset && reset[t])
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
-            if (t + a >= t1) break;
-            if (reset && reset[t + a])
+            for (int k = 0; k < K; ++k) clear(win[k]);
+        unpack(q[a], win[(a + K - 1) % K]);
+        float o[V];
 #pragma unroll
-                for (int k = 0; k < K; ++k)
+        for (int j = 0; j < V; ++j) o[j] = bias[j];
 #pragma unroll
-                    for (int j = 0; j < V; ++j) win[k][j] = 0.f;
-            // row t + a goes to place (a + K - 1) % K, row t + a - K + 1 is at a % K
-            unpack(q[a], win[(a + K - 1) % K]);
-            float o[V];
+        for (int k = 0; k < K; ++k) fma_all(o, w[k], win[(a + k) % K]);
+        if (p.silu)
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                float s = bias[j];
+            for (int j = 0; j < V; ++j) o[j] *= sigmoid(o[j]);
+        Pack<T, V> out;
+        pack(out, o);
+        out.store(yt + (size_t)a * p.C);
+    };
+    load(t0);
+    for (int t = t0; t < t1; t += kAhead) {
 #pragma unroll
-                for (int k = 0; k < K; ++k) s = fmaf(w[k][j], win[(a + k) % K][j], s);
-                o[j] = p.silu ? s * sigmoid(s) : s;
-            }
-            Pack<T, V> r;
-            pack(r, o);
-            r.store(y + (size_t)(t + a) * p.C);
+        for (int a = 0; a < kAhead; ++a) q[a] = r[a];
+        load(t + kAhead);
+        if (t + kAhead <= t1) {
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a) token(a, t + a);
+        } else {
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a)
+                if (t + a < t1) token(a, t + a);
         }
+        yt += (size_t)kAhead * p.C;
     }
 }
 
@@ -148,7 +209,7 @@ template <typename T, int V, int K> __global__ void __launch_bounds__(kThreads) 
 // been taken (or hidden from it), so the walk runs K - 1 tokens past the piece.  A block is
 // 32 channel vectors wide and kRows pieces high, whose sums it adds up.
 constexpr int kRows = kThreads / 32;
-template <typename T, int V, int K> __global__ void __launch_bounds__(kThreads) ttt_short_conv_bwd_kernel(const __grid_constant__ ConvParams p)
+template <typename T, int V, int K> __global__ void __launch_bounds__(kThreads, 3) ttt_short_conv_bwd_kernel(const __grid_constant__ ConvParams p)
 {
     __shared__ float sums[kRows][32][V * (K + 1) + 1];
     const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
@@ -172,13 +233,11 @@ template <typename T, int V, int K> __global__ void __launch_bounds__(kThreads) 
         const unsigned char *reset = p.reset ? p.reset + (size_t)b * p.T : nullptr;
         T *dx = static_cast<T *>(p.dx) + (size_t)b * p.T * p.C + c;
         float w[K][V], bias[V], win[K][V], pend[K][V];
+        load_taps<V, K>(p.weight + (size_t)c * K, w);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                w[k][j] = p.weight[(size_t)(c + j) * K + k];
-                pend[k][j] = 0.f;
-            }
+            for (int k = 0; k < K; ++k) pend[k][j] = 0.f;
             bias[j] = p.bias ? p.bias[c + j] : 0.f;
         }
         rows_before<T, V, K>(p, x, state, reset, t0, win);
@@ -194,69 +253,93 @@ template <typename T, int V, int K> __global__ void __launch_bounds__(kThreads) 
                     if (reset[r]) live = r;
         }
         // at token t + a row t + a - d waits at place (a + K - d) % K
+        Pack<T, V> qx[K], qg[K], rx[K], rg[K];
+        const T *xt = x + t0 * p.xs[1], *gt = dy + t0 * p.dys[1];
+        T *dxt = dx + ((long long)t0 - (K - 1)) * p.C;
+        auto load = [&](int t) {
+#pragma unroll
+            for (int a = 0; a < K; ++a)
+                if (t + a < tend) {
+                    rx[a].load(xt + a * p.xs[1]);
+                    rg[a].load(gt + a * p.dys[1]);
+                }
+            xt += K * p.xs[1];
+            gt += K * p.dys[1];
+        };
+        auto token = [&](int a, int t, bool own) {
+            if (reset && reset[t]) {
+                age = 0;
+#pragma unroll
+                for (int k = 0; k < K; ++k) clear(win[k]);
+            }
+            float g[V];
+            unpack(qx[a], win[(a + K - 1) % K]);
+            unpack(qg[a], g);
+            if (p.silu) {
+                float s[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) s[j] = bias[j];
+#pragma unroll
+                for (int k = 0; k < K; ++k) fma_all(s, w[k], win[(a + k) % K]);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float sg = sigmoid(s[j]);
+                    g[j] *= sg * fmaf(s[j], 1.f - sg, 1.f);
+                }
+            }
+            if (own) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) db[j] += g[j];
+#pragma unroll
+                for (int k = 0; k < K; ++k) fma_all(dw[k], g, win[(a + k) % K]);
+            }
+#pragma unroll
+            for (int d = 0; d < K; ++d)
+                if (!reset || d <= age) fma_all(pend[(a + K - d) % K], w[K - 1 - d], g);
+            age = min(age + 1, K - 1);
+        };
+        auto finish = [&](int a, int s) {
+            float (&o)[V] = pend[(a + 1) % K];
+            if (p.dstate_out && s >= live) {
+                const float *ds = p.dstate_out + ((size_t)b * (K - 1) + s - (p.T - (K - 1))) * p.C + c;
+#pragma unroll
+                for (int j = 0; j < V; ++j) o[j] += ds[j];
+            }
+            if (s >= 0) {
+                Pack<T, V> q;
+                pack(q, o);
+                q.store(dxt + (long long)a * p.C);
+            } else if (p.dstate) {
+                float *ds = p.dstate + ((size_t)b * (K - 1) + s + K - 1) * p.C + c;
+#pragma unroll
+                for (int j = 0; j < V; ++j) ds[j] = o[j];
+            }
+        };
+        load(t0);
         for (int t = t0; t < t1 + K - 1; t += K) {
 #pragma unroll
             for (int a = 0; a < K; ++a) {
-                const int tt = t + a;
-                if (tt >= t1 + K - 1) break;
+                qx[a] = rx[a];
+                qg[a] = rg[a];
+            }
+            load(t + K);
+            if (t >= t0 + K - 1 && t + K <= t1) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) pend[a][j] = 0.f;
-                if (tt < tend) {
-                    if (reset && reset[tt]) {
-                        age = 0;
-#pragma unroll
-                        for (int k = 0; k < K; ++k)
-#pragma unroll
-                            for (int j = 0; j < V; ++j) win[k][j] = 0.f;
-                    }
-                    float g[V];
-                    load_row<T, V>(x + tt * p.xs[1], win[(a + K - 1) % K]);
-                    load_row<T, V>(dy + tt * p.dys[1], g);
-                    if (p.silu)
-#pragma unroll
-                        for (int j = 0; j < V; ++j) {
-                            float s = bias[j];
-#pragma unroll
-                            for (int k = 0; k < K; ++k) s = fmaf(w[k][j], win[(a + k) % K][j], s);
-                            const float sg = sigmoid(s);
-                            g[j] *= sg * fmaf(s, 1.f - sg, 1.f);
-                        }
-                    if (tt < t1)
-#pragma unroll
-                        for (int j = 0; j < V; ++j) {
-                            db[j] += g[j];
-#pragma unroll
-                            for (int k = 0; k < K; ++k) dw[k][j] = fmaf(g[j], win[(a + k) % K][j], dw[k][j]);
-                        }
-#pragma unroll
-                    for (int d = 0; d < K; ++d)
-                        if (d <= age)
-#pragma unroll
-                            for (int j = 0; j < V; ++j)
-                                pend[(a + K - d) % K][j] = fmaf(w[K - 1 - d][j], g[j], pend[(a + K - d) % K][j]);
-                    age = min(age + 1, K - 1);
+                for (int a = 0; a < K; ++a) {
+                    clear(pend[a]);
+                    token(a, t + a, true);
+                    finish(a, t + a - (K - 1));
                 }
-                const int s = tt - (K - 1);
-                if (s >= lo && s < t1) {
-                    float o[V];
+            } else {
 #pragma unroll
-                    for (int j = 0; j < V; ++j) o[j] = pend[(a + 1) % K][j];
-                    if (p.dstate_out && s >= live) {
-                        const float *ds = p.dstate_out + ((size_t)b * (K - 1) + s - (p.T - (K - 1))) * p.C + c;
-#pragma unroll
-                        for (int j = 0; j < V; ++j) o[j] += ds[j];
-                    }
-                    if (s >= 0) {
-                        Pack<T, V> q;
-                        pack(q, o);
-                        q.store(dx + (size_t)s * p.C);
-                    } else if (p.dstate) {
-                        float *ds = p.dstate + ((size_t)b * (K - 1) + s + K - 1) * p.C + c;
-#pragma unroll
-                        for (int j = 0; j < V; ++j) ds[j] = o[j];
-                    }
+                for (int a = 0; a < K; ++a) {
+                    clear(pend[a]);
+                    if (t + a < tend) token(a, t + a, t + a < t1);
+                    const int s = t + a - (K - 1);
+                    if (s >= lo && s < t1) finish(a, s);
                 }
             }
+            dxt += (long long)K * p.C;
         }
     }
     if (!p.part) return;
@@ -343,9 +426,11 @@ template <typename T, int V> int fwd_width(const ConvArgs &a)
 {
     ConvParams p;
     conv_params(a, p, V);
-    // tokens a thread walks: as many as leave two full loads of threads, 4 .. 32
-    const long long all = (long long)a.B * a.T * p.nv, fill = all / (2LL * 2048 * kSMs);
-    p.len = (int)(fill < 4 ? 4 : fill > 32 ? 32 : fill);
+    // tokens a thread walks: 4 .. 64, as many as leave 512 threads an SM (K - 1 rows and the
+    // taps are read once a piece; 8 x 2048 x 768 bf16: 20 tokens 14.8 us, 4 tokens 58 us, and
+    // at 2 x 32768 x 2048 64 tokens 95 us, 32 101, 16 116)
+    const long long fill = (long long)a.B * a.T * p.nv / (512LL * kSMs);
+    p.len = (int)(fill < 4 ? 4 : fill > 64 ? 64 : fill);
     p.pieces = (a.T + p.len - 1) / p.len;
     const long long n = (long long)a.B * p.pieces * p.nv;
     const long long blocks = (n + kThreads - 1) / kThreads;
@@ -359,11 +444,14 @@ template <typename T, int V> int fwd_width(const ConvArgs &a)
     return cudaGetLastError() == cudaSuccess ? 1 : -4;
 }
 
-// The backward pass' pieces: 64 tokens, fewer where that leaves SMs without work.
+// The backward pass' pieces: 128 tokens, fewer where that leaves an SM fewer than 300 threads
+// (8 x 2048 x 768 bf16: 64 tokens 23.9 us, 32 27.9, 16 34.2; 3 x 701 x 1001 fp32: 32 tokens
+// 11.7 us, 64 17.7).  By sizes alone, as the workspace is.
 int bwd_len(int B, int T, int C)
 {
-    int len = 64;
-    while (len > 8 && (long long)B * ((T + len - 1) / len) * C < 4LL * 1024 * kSMs) len /= 2;
+    const long long vecs = (long long)B * (C % 4 ? C : C / 4);
+    int len = 128;
+    while (len > 8 && vecs * ((T + len - 1) / len) < 300LL * kSMs) len /= 2;
     return len;
 }
 long long bwd_part_rows(int B, int T, int C)
@@ -397,21 +485,15 @@ template <typename T, int V> int bwd_width(const ConvArgs &a)
 
 }  // namespace
 
+// Four channels a thread at most, 8 bytes of bf16: with eight the window, the taps and their
+// sums take so many registers that too few threads are left to wait for memory (2 x 32768 x
+// 2048 forward: 95 us against 107).
 int launch_conv_fwd(const ConvArgs &a)
 {
-    const int V = widest(a, a.bf16 ? 8 : 4);
-    if (a.bf16) {
-        switch (V) {
-        case 8: return fwd_width<__nv_bfloat16, 8>(a);
-        case 4: return fwd_width<__nv_bfloat16, 4>(a);
-        case 2: return fwd_width<__nv_bfloat16, 2>(a);
-        default: return fwd_width<__nv_bfloat16, 1>(a);
-        }
-    }
-    switch (V) {
-    case 4: return fwd_width<float, 4>(a);
-    case 2: return fwd_width<float, 2>(a);
-    default: return fwd_width<float, 1>(a);
+    switch (widest(a, 4)) {
+    case 4: return a.bf16 ? fwd_width<__nv_bfloat16, 4>(a) : fwd_width<float, 4>(a);
+    case 2: return a.bf16 ? fwd_width<__nv_bfloat16, 2>(a) : fwd_width<float, 2>(a);
+    default: return a.bf16 ? fwd_width<__nv_bfloat16, 1>(a) : fwd_width<float, 1>(a);
     }
 }
 
@@ -419,18 +501,10 @@ size_t conv_bwd_workspace(int B, int T, int C, int K) { return 4 * (size_t)bwd_p
 
 int launch_conv_bwd(const ConvArgs &a)
 {
-    const int V = widest(a, a.bf16 ? 4 : 4);
-    if (a.bf16) {
-        switch (V) {
-        case 4: return bwd_width<__nv_bfloat16, 4>(a);
-        case 2: return bwd_width<__nv_bfloat16, 2>(a);
-        default: return bwd_width<__nv_bfloat16, 1>(a);
-        }
-    }
-    switch (V) {
-    case 4: return bwd_width<float, 4>(a);
-    case 2: return bwd_width<float, 2>(a);
-    default: return bwd_width<float, 1>(a);
+    switch (widest(a, 4)) {
+    case 4: return a.bf16 ? bwd_width<__nv_bfloat16, 4>(a) : bwd_width<float, 4>(a);
+    case 2: return a.bf16 ? bwd_width<__nv_bfloat16, 2>(a) : bwd_width<float, 2>(a);
+    default: return a.bf16 ? bwd_width<__nv_bfloat16, 1>(a) : bwd_width<float, 1>(a);
     }
 }
 
