@@ -170,6 +170,19 @@ def lib():
         L.ttt_recurrence_fwd.restype = ctypes.c_int
         L.ttt_recurrence_bwd.argtypes = [ctypes.POINTER(RecurrenceDesc), vp, vp, vp, vp, fp, fp, vp, vp, fp, vp]
         L.ttt_recurrence_bwd.restype = ctypes.c_int
+        sz, P = ctypes.c_size_t, ctypes.POINTER
+        L.ttt_rope_axes.argtypes = [P(RopeAxesDesc), ctypes.c_char_p, vp, vp, vp, fp, vp, vp, vp, vp, vp]
+        L.ttt_short_conv_fwd.argtypes = [P(ShortConvDesc), vp, fp, fp, vp, vp, vp, vp, vp]
+        L.ttt_short_conv_bwd.argtypes = [P(ShortConvDesc), vp, vp, fp, fp, vp, vp, fp, vp, fp, fp, fp, vp, sz, vp]
+        L.ttt_selective_scan_fwd.argtypes = [P(ScanDesc), P(ScanVectors), vp, vp, vp, vp, vp, vp, fp, vp, fp, fp, vp, sz, vp]
+        L.ttt_selective_scan_bwd.argtypes = [P(ScanDesc), P(ScanVectors), vp, vp, vp, vp, vp, vp, vp, fp, fp, vp, vp, vp, vp,
+                                             vp, P(ScanVectors), fp, vp, sz, vp]
+        for fn in (L.ttt_rope_axes, L.ttt_short_conv_fwd, L.ttt_short_conv_bwd, L.ttt_selective_scan_fwd,
+                   L.ttt_selective_scan_bwd):
+            fn.restype = ctypes.c_int
+        for fn, desc in ((L.ttt_short_conv_bwd_workspace, ShortConvDesc), (L.ttt_selective_scan_fwd_workspace, ScanDesc),
+                         (L.ttt_selective_scan_bwd_workspace, ScanDesc)):
+            fn.argtypes, fn.restype = [P(desc)], sz
         L.ttt_sync_status.argtypes = [vp]
         L.ttt_sync_status.restype = ctypes.c_int
         L.ttt_status_str.argtypes = [ctypes.c_int]

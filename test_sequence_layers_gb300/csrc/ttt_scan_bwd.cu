@@ -216,16 +216,20 @@ __global__ void __launch_bounds__(block_threads(LN)) ttt_scan_bwd_kernel(const _
             unpack(pg, gf);
             unpack(pz, zf);
 #pragma unroll
+            for (int j = 0; j < V; ++j) df[j] += bias[j];
+            if (p.softplus) softplus_all(df);
+#pragma unroll
             for (int j = 0; j < V; ++j) {
-                float e, d = df[j] + bias[j];
-                if (p.softplus) d = softplus(d, e);
-                if (!live) d = 0.f;
-                if (p.z) gf[j] *= zf[j] * sigmoid(zf[j]);
-                const int at = t * CB + vch + j;
-                sm[L::d + at] = d;
-                sm[L::u + at] = d * xf[j];
-                sm[L::g + at] = gf[j];
+                if (!live) df[j] = 0.f;  // past the end: nothing moves
+                xf[j] *= df[j];
             }
+            if (p.z)
+#pragma unroll
+                for (int j = 0; j < V; ++j) gf[j] *= zf[j] * sigmoid(zf[j]);
+            const int at = t * CB + vch;
+            put_floats(sm + L::d + at, df);
+            put_floats(sm + L::u + at, xf);
+            put_floats(sm + L::g + at, gf);
         }
         for (int v = tid; v < kBVecs; v += NT) {
             const int t = v / (NP / kBV), n = v % (NP / kBV) * kBV;
@@ -237,11 +241,9 @@ __global__ void __launch_bounds__(block_threads(LN)) ttt_scan_bwd_kernel(const _
             }
             float f[kBV];
             unpack(pb, f);
-#pragma unroll
-            for (int j = 0; j < kBV; ++j) sm[L::Bm + t * NP + n + j] = f[j];
+            put_floats(sm + L::Bm + t * NP + n, f);
             unpack(pc, f);
-#pragma unroll
-            for (int j = 0; j < kBV; ++j) sm[L::Cm + t * NP + n + j] = f[j];
+            put_floats(sm + L::Cm + t * NP + n, f);
         }
         float2 h[2][2];
 #pragma unroll
@@ -385,15 +387,17 @@ __global__ void __launch_bounds__(block_threads(LN)) ttt_scan_bwd_kernel(const _
             pg.load(dy + (t0 + t) * p.dys[1] + c0 + vch);
             pz.raw = {};
             if (p.z) pz.load(z + (t0 + t) * p.zs[1] + c0 + vch);
-            float xf[V], df[V], gf[V], zf[V], dx[V], dd[V], dz[V];
+            float xf[V], df[V], gf[V], zf[V], dx[V], dd[V], dz[V], es[V], qs[V], ys[V];
             unpack(px, xf);
             unpack(pd, df);
             unpack(pg, gf);
             unpack(pz, zf);
+            get_floats(sm + L::u + t * CB + vch, es);
+            get_floats(sm + L::d + t * CB + vch, qs);
+            get_floats(sm + L::g + t * CB + vch, ys);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const int at = t * CB + vch + j;
-                const float e = sm[L::u + at], q = sm[L::d + at];
+                const float e = es[j], q = qs[j];
                 float d = df[j] + bias[j], slope = 1.f, g = gf[j];
                 if (p.softplus) {
                     const float v2 = d;
@@ -403,7 +407,7 @@ __global__ void __launch_bounds__(block_threads(LN)) ttt_scan_bwd_kernel(const _
                     if (v2 < 0.f) slope *= ee;
                 }
                 if (p.z) {
-                    const float sg = sigmoid(zf[j]), y = fmaf(Dv[j], xf[j], sm[L::g + at]);
+                    const float sg = sigmoid(zf[j]), y = fmaf(Dv[j], xf[j], ys[j]);
                     dz[j] = g * y * sg * fmaf(zf[j], 1.f - sg, 1.f);
                     g *= zf[j] * sg;
                 }
