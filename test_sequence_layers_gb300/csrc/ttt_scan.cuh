@@ -10,6 +10,11 @@ namespace scan {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// a truth value known at compile time
+template <bool V> struct Is {
+    static constexpr bool value = V;
+};
+
 struct Params {
     const void *x, *delta, *z, *Bm, *Cm, *dy;
     const unsigned char *reset;

@@ -19,14 +19,20 @@ constexpr int kTile = kScanChunk, kSub = 8, kSubs = kTile / kSub;
 constexpr int block_channels(int LN) { return LN <= 8 ? 64 : 32; }
 constexpr int block_threads(int LN) { return block_channels(LN) * LN / 2; }
 
-// Shared memory of a block, in floats.
-template <int LN> struct Layout {
+// Shared memory of a block, in floats: rates, inputs, gated gradients (then e and y' in the
+// places of the latter two) and sum q A; B and C; the states before every kSub tokens; a warp's
+// sums for dB and dC, twice; the tensors as they come, x, delta, dy, z, B, C (kRaw tiles).
+template <typename T, int LN, bool VEC> struct Layout {
     static constexpr int CB = block_channels(LN), NT = block_threads(LN), NP = 4 * LN, W = NT / 32;
-    static constexpr int d = 0, u = d + kTile * CB, g = u + kTile * CB;  // rate, rate x, dy silu(z); then sum q A, e, y'
-    static constexpr int Bm = g + kTile * CB, Cm = Bm + kTile * NP;
-    static constexpr int ck = Cm + kTile * NP;                          // states before every kSub tokens
-    static constexpr int red = ck + kSubs * NT * 8;                     // a warp's sums for dB and dC
-    static constexpr int floats = red + W * kSub * 2 * NP;
+    static constexpr int kRaw = !VEC ? 0 : sizeof(T) == 2 ? 2 : 1;  // (two of fp32 would leave one block an SM)
+    static constexpr int d = 0, u = d + kTile * CB, g = u + kTile * CB, q = g + kTile * CB;
+    static constexpr int Bm = q + kTile * CB, Cm = Bm + kTile * NP;
+    static constexpr int ck = Cm + kTile * NP;
+    static constexpr int red = ck + kSubs * NT * 8, red_one = W * kSub * 2 * NP;
+    static constexpr int raw = red + 2 * red_one;
+    static constexpr int raw_tokens = kTile * CB * (int)sizeof(T), raw_bc = kTile * NP * (int)sizeof(T);  // bytes of one tensor
+    static constexpr int raw_bytes = 4 * raw_tokens + 2 * raw_bc;
+    static constexpr int bytes = raw * 4 + kRaw * raw_bytes;
 };
 
 // The gradient map of a piece, v -> exp(A rate_sum) v + R, from its end to its start.
@@ -150,7 +156,7 @@ __global__ void __launch_bounds__(256) ttt_scan_bwd_join_kernel(const __grid_con
 template <typename T, int LN, bool VEC>
 __global__ void __launch_bounds__(block_threads(LN)) ttt_scan_bwd_kernel(const __grid_constant__ Params p)
 {
-    using L = Layout<LN>;
+    using L = Layout<T, LN, VEC>;
     constexpr int CB = L::CB, NT = L::NT, NP = L::NP, CL = 32 / LN;
     constexpr int V = VEC ? 16 / (int)sizeof(T) : 1, kRowVecs = CB / V, kVecs = kTile * kRowVecs;
     constexpr int kBV = V < NP ? V : NP, kBVecs = kTile * NP / kBV;
@@ -194,27 +200,80 @@ __global__ void __launch_bounds__(block_threads(LN)) ttt_scan_bwd_kernel(const _
         sD[j] = sb[j] = 0.f;
     }
 
-    for (int t0 = tb + (te - tb - 1) / kTile * kTile; t0 >= tb; t0 -= kTile) {
+    // The tile's tensors: asynchronous copies of 16 bytes, each read by the thread that asked
+    // for it (token t, channels vch ..), or plain loads where they are not aligned.
+    unsigned char *const raw = reinterpret_cast<unsigned char *>(sm + L::raw);
+    constexpr int kVecIt = (kVecs + NT - 1) / NT;
+    auto copy = [&](int t0, int stage) {
+        unsigned char *to = raw + stage * L::raw_bytes;
+        const bool in = c0 + vch < cend;
+#pragma unroll
+        for (int i = 0; i < kVecIt; ++i) {
+            const int v = tid + i * NT, t = t0 + v / kRowVecs, n = in && t < te ? 16 : 0;
+            if (kVecs % NT && v >= kVecs) break;
+            const int r = n ? t : tb, ch = n ? c0 + vch : c0;  // (nothing is read where n is 0)
+            copy_async16_part(to + v * 16, x + r * p.xs[1] + ch, n);
+            copy_async16_part(to + L::raw_tokens + v * 16, dl + r * p.ds[1] + ch, n);
+            copy_async16_part(to + 2 * L::raw_tokens + v * 16, dy + r * p.dys[1] + ch, n);
+            if (p.z) copy_async16_part(to + 3 * L::raw_tokens + v * 16, z + r * p.zs[1] + ch, n);
+        }
+        for (int v = tid; v < kBVecs; v += NT) {
+            const int t = t0 + v / (NP / kBV), k = v % (NP / kBV) * kBV, n = t < te && k < p.N ? 16 : 0;
+            const int r = n ? t : tb, m = n ? k : 0;
+            copy_async16_part(to + 4 * L::raw_tokens + v * 16, Bm + r * p.bs[1] + m, n);
+            copy_async16_part(to + 4 * L::raw_tokens + L::raw_bc + v * 16, Cm + r * p.cs[1] + m, n);
+        }
+        copy_commit();
+    };
+    // the four tensors' vector v of the tile at t0
+    auto tensors = [&](int t0, int nt, int stage, int v, float (&xf)[V], float (&df)[V], float (&gf)[V], float (&zf)[V]) {
+        const int t = v / kRowVecs;
+        Pack<T, V> px, pd, pg, pz;
+        px.raw = pd.raw = pg.raw = pz.raw = {};
+        if constexpr (L::kRaw > 0) {
+            const unsigned char *from = raw + stage * L::raw_bytes + v * 16;
+            px.load_rw(reinterpret_cast<const T *>(from));
+            pd.load_rw(reinterpret_cast<const T *>(from + L::raw_tokens));
+            pg.load_rw(reinterpret_cast<const T *>(from + 2 * L::raw_tokens));
+            if (p.z) pz.load_rw(reinterpret_cast<const T *>(from + 3 * L::raw_tokens));
+        } else if (t < nt && c0 + vch < cend) {
+            px.load(x + (t0 + t) * p.xs[1] + c0 + vch);
+            pd.load(dl + (t0 + t) * p.ds[1] + c0 + vch);
+            pg.load(dy + (t0 + t) * p.dys[1] + c0 + vch);
+            if (p.z) pz.load(z + (t0 + t) * p.zs[1] + c0 + vch);
+        }
+        unpack(px, xf);
+        unpack(pd, df);
+        unpack(pg, gf);
+        unpack(pz, zf);
+    };
+
+    int t0 = tb + (te - tb - 1) / kTile * kTile, stage = 0;
+    if constexpr (L::kRaw > 0) copy(t0, 0);
+    for (; t0 >= tb; t0 -= kTile) {
         const int nt = min(kTile, te - t0);
         unsigned cut = 0;
         if (reset) cut = __ballot_sync(0xffffffffu, lane < nt && reset[t0 + lane]);
+        float2 h[2][2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int c = c0 + cl + k;
+            Quad q = quad(zero4);
+            if (c < cend) q = quad(load_states(p.states + (((size_t)b * p.chunks + t0 / kScanChunk) * p.C + c) * p.N, n0, p.N, 0.f));
+            h[k][0] = q.a;
+            h[k][1] = q.b;
+        }
+        if constexpr (L::kRaw > 0) copy_wait<0>();
+        if constexpr (L::kRaw == 2)
+            if (t0 > tb) copy(t0 - kTile, stage ^ 1);
         // rates, inputs and gated gradients in fp32
-        for (int v = tid; v < kVecs; v += NT) {
-            const int t = v / kRowVecs;
+#pragma unroll
+        for (int i = 0; i < kVecIt; ++i) {
+            const int v = tid + i * NT, t = v / kRowVecs;
+            if (kVecs % NT && v >= kVecs) break;
             const bool live = t < nt && c0 + vch < cend;
-            Pack<T, V> px, pd, pg, pz;
-            px.raw = pd.raw = pg.raw = pz.raw = {};
-            if (live) {
-                px.load(x + (t0 + t) * p.xs[1] + c0 + vch);
-                pd.load(dl + (t0 + t) * p.ds[1] + c0 + vch);
-                pg.load(dy + (t0 + t) * p.dys[1] + c0 + vch);
-                if (p.z) pz.load(z + (t0 + t) * p.zs[1] + c0 + vch);
-            }
             float xf[V], df[V], gf[V], zf[V];
-            unpack(px, xf);
-            unpack(pd, df);
-            unpack(pg, gf);
-            unpack(pz, zf);
+            tensors(t0, nt, stage, v, xf, df, gf, zf);
 #pragma unroll
             for (int j = 0; j < V; ++j) df[j] += bias[j];
             if (p.softplus) softplus_all(df);
@@ -235,7 +294,11 @@ __global__ void __launch_bounds__(block_threads(LN)) ttt_scan_bwd_kernel(const _
             const int t = v / (NP / kBV), n = v % (NP / kBV) * kBV;
             Pack<T, kBV> pb, pc;
             pb.raw = pc.raw = {};
-            if (t < nt && n < p.N) {
+            if constexpr (L::kRaw > 0) {
+                const unsigned char *from = raw + stage * L::raw_bytes + 4 * L::raw_tokens + v * 16;
+                pb.load_rw(reinterpret_cast<const T *>(from));
+                pc.load_rw(reinterpret_cast<const T *>(from + L::raw_bc));
+            } else if (t < nt && n < p.N) {
                 pb.load(Bm + (t0 + t) * p.bs[1] + n);
                 pc.load(Cm + (t0 + t) * p.cs[1] + n);
             }
@@ -245,174 +308,162 @@ __global__ void __launch_bounds__(block_threads(LN)) ttt_scan_bwd_kernel(const _
             unpack(pc, f);
             put_floats(sm + L::Cm + t * NP + n, f);
         }
-        float2 h[2][2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int c = c0 + cl + k;
-            Quad q = quad(zero4);
-            if (c < cend) q = quad(load_states(p.states + (((size_t)b * p.chunks + t0 / kScanChunk) * p.C + c) * p.N, n0, p.N, 0.f));
-            h[k][0] = q.a;
-            h[k][1] = q.b;
-        }
         __syncthreads();
 
-        auto forward = [&](int t, float2 (&hh)[2][2], bool zero) {
-            const float2 d = *reinterpret_cast<const float2 *>(&sm[L::d + t * CB + cl]);
-            const float2 u = *reinterpret_cast<const float2 *>(&sm[L::u + t * CB + cl]);
-            const float4 Bt = *reinterpret_cast<const float4 *>(&sm[L::Bm + t * NP + n0]);
+        auto scan_tile = [&](auto resets) {
+            constexpr bool kResets = decltype(resets)::value;
+            auto forward = [&](int t, float2 (&hh)[2][2]) {
+                const bool zero = kResets && (cut >> t & 1);
+                const float2 d = *reinterpret_cast<const float2 *>(&sm[L::d + t * CB + cl]);
+                const float2 u = *reinterpret_cast<const float2 *>(&sm[L::u + t * CB + cl]);
+                const float4 Bt = *reinterpret_cast<const float4 *>(&sm[L::Bm + t * NP + n0]);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float2 dd = k ? make_float2(d.y, d.y) : make_float2(d.x, d.x), uu = k ? make_float2(u.y, u.y) : make_float2(u.x, u.x);
+                for (int k = 0; k < 2; ++k) {
+                    const float2 dd = k ? make_float2(d.y, d.y) : make_float2(d.x, d.x), uu = k ? make_float2(u.y, u.y) : make_float2(u.x, u.x);
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const float2 e = __fmul2_rn(dd, A[k][m]), in = __fmul2_rn(uu, m ? make_float2(Bt.z, Bt.w) : make_float2(Bt.x, Bt.y));
-                    const float2 prev = zero ? zero2 : hh[k][m];
-                    hh[k][m] = __ffma2_rn(make_float2(ex2(e.x), ex2(e.y)), prev, in);
+                    for (int m = 0; m < 2; ++m) {
+                        const float2 e = __fmul2_rn(dd, A[k][m]), in = __fmul2_rn(uu, m ? make_float2(Bt.z, Bt.w) : make_float2(Bt.x, Bt.y));
+                        const float2 prev = kResets && zero ? zero2 : hh[k][m];
+                        hh[k][m] = __ffma2_rn(make_float2(ex2(e.x), ex2(e.y)), prev, in);
+                    }
+                }
+            };
+            // states before every kSub tokens of the tile
+            float4 *ck = reinterpret_cast<float4 *>(sm + L::ck) + tid;
+#pragma unroll 1
+            for (int s = 0; s < kSubs; ++s) {
+                ck[(2 * s) * NT] = make_float4(h[0][0].x, h[0][0].y, h[0][1].x, h[0][1].y);
+                ck[(2 * s + 1) * NT] = make_float4(h[1][0].x, h[1][0].y, h[1][1].x, h[1][1].y);
+                if (s + 1 < kSubs)
+#pragma unroll
+                    for (int t = 0; t < kSub; ++t) forward(s * kSub + t, h);
+            }
+#pragma unroll 1
+            for (int s = kSubs - 1; s >= 0; --s) {
+                const int ts = s * kSub;
+                float *const red = sm + L::red + (s & 1) * L::red_one;
+                float2 hs[kSub + 1][2][2];
+                {
+                    const float4 k0 = ck[(2 * s) * NT], k1 = ck[(2 * s + 1) * NT];
+                    hs[0][0][0] = make_float2(k0.x, k0.y);
+                    hs[0][0][1] = make_float2(k0.z, k0.w);
+                    hs[0][1][0] = make_float2(k1.x, k1.y);
+                    hs[0][1][1] = make_float2(k1.z, k1.w);
+                }
+#pragma unroll
+                for (int t = 0; t < kSub; ++t) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) hs[t + 1][k][m] = hs[t][k][m];
+                    forward(ts + t, hs[t + 1]);
+                }
+#pragma unroll
+                for (int half = kSub / 4 - 1; half >= 0; --half) {
+                    float ve[8], vq[8], vy[8];  // [token of four][channel]: e, sum q A, y'
+#pragma unroll
+                    for (int i = 3; i >= 0; --i) {
+                        const int j = half * 4 + i, t = ts + j;
+                        const bool zero = kResets && (cut >> t & 1);
+                        const float2 d = *reinterpret_cast<const float2 *>(&sm[L::d + t * CB + cl]);
+                        const float2 u = *reinterpret_cast<const float2 *>(&sm[L::u + t * CB + cl]);
+                        const float2 g = *reinterpret_cast<const float2 *>(&sm[L::g + t * CB + cl]);
+                        const float4 B4 = *reinterpret_cast<const float4 *>(&sm[L::Bm + t * NP + n0]);
+                        const float4 C4 = *reinterpret_cast<const float4 *>(&sm[L::Cm + t * NP + n0]);
+                        float2 dB[2], dC[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float2 dd = k ? make_float2(d.y, d.y) : make_float2(d.x, d.x);
+                            const float2 uu = k ? make_float2(u.y, u.y) : make_float2(u.x, u.x);
+                            const float2 gg = k ? make_float2(g.y, g.y) : make_float2(g.x, g.x);
+                            float2 e2, q2, y2;
+#pragma unroll
+                            for (int m = 0; m < 2; ++m) {
+                                const float2 Bt = m ? make_float2(B4.z, B4.w) : make_float2(B4.x, B4.y);
+                                const float2 Ct = m ? make_float2(C4.z, C4.w) : make_float2(C4.x, C4.y);
+                                const float2 arg = __fmul2_rn(dd, A[k][m]);
+                                const float2 s2 = __ffma2_rn(gg, Ct, r[k][m]);
+                                dC[m] = k ? __ffma2_rn(gg, hs[j + 1][k][m], dC[m]) : __fmul2_rn(gg, hs[j + 1][k][m]);
+                                dB[m] = k ? __ffma2_rn(uu, s2, dB[m]) : __fmul2_rn(uu, s2);
+                                y2 = m ? __ffma2_rn(Ct, hs[j + 1][k][m], y2) : __fmul2_rn(Ct, hs[j + 1][k][m]);
+                                e2 = m ? __ffma2_rn(Bt, s2, e2) : __fmul2_rn(Bt, s2);
+                                const float2 as = __fmul2_rn(make_float2(ex2(arg.x), ex2(arg.y)), s2);
+                                const float2 q = kResets && zero ? zero2 : __fmul2_rn(as, hs[j][k][m]);
+                                q2 = m ? __ffma2_rn(q, A[k][m], q2) : __fmul2_rn(q, A[k][m]);
+                                dA[k][m] = __ffma2_rn(q, dd, dA[k][m]);
+                                r[k][m] = kResets && zero ? zero2 : as;
+                            }
+                            ve[2 * i + k] = e2.x + e2.y;
+                            vq[2 * i + k] = q2.x + q2.y;
+                            vy[2 * i + k] = y2.x + y2.y;
+                        }
+                        float bc[8] = {dB[0].x, dB[0].y, dB[1].x, dB[1].y, dC[0].x, dC[0].y, dC[1].x, dC[1].y};
+                        spread_sum<8, CL, 1>(bc);
+                        constexpr int K = CL < 8 ? 8 / CL : 1, dup = CL > 8 ? CL / 8 : 1;
+                        float *to = red + (warp * kSub + j) * 2 * NP + n0;
+                        if (lane % CL % dup == 0)
+#pragma unroll
+                            for (int m = 0; m < K; ++m) {
+                                const int v = lane % CL / dup * K + m;
+                                to[(v / 4) * NP + v % 4] = bc[m];
+                            }
+                    }
+                    spread_sum<8, LN, CL>(ve);
+                    spread_sum<8, LN, CL>(vq);
+                    spread_sum<8, LN, CL>(vy);
+                    __syncwarp();  // these tokens' inputs and gradients have been read: the sums take their places
+                    constexpr int K = LN < 8 ? 8 / LN : 1, dup = LN > 8 ? LN / 8 : 1;
+                    if (ng % dup == 0)
+#pragma unroll
+                        for (int m = 0; m < K; ++m) {
+                            const int v = ng / dup * K + m, at = (ts + half * 4 + v / 2) * CB + cl + v % 2;
+                            sm[L::u + at] = ve[m];
+                            sm[L::q + at] = vq[m];
+                            sm[L::g + at] = vy[m];
+                        }
+                }
+                __syncthreads();
+                // the block's sums over its channels for these kSub tokens (the next ones' go to
+                // the other half of red, and come back to this one two barriers later)
+                for (int v = tid; v < kSub * 2 * NP; v += NT) {
+                    const int j = v / (2 * NP), w = v / NP % 2, n = v % NP;
+                    if (ts + j < nt && n < p.N) {
+                        float s2 = 0.f;
+#pragma unroll
+                        for (int i = 0; i < L::W; ++i) s2 += red[(i * kSub + j) * 2 * NP + w * NP + n];
+                        p.bc_part[((((size_t)blk * p.B + b) * p.T + t0 + ts + j) * p.G + grp) * 2 * p.N + w * p.N + n] = s2;
+                    }
                 }
             }
         };
-        // states before every kSub tokens of the tile
-        float4 *ck = reinterpret_cast<float4 *>(sm + L::ck) + tid;
-#pragma unroll 1
-        for (int s = 0; s < kSubs; ++s) {
-            ck[(2 * s) * NT] = make_float4(h[0][0].x, h[0][0].y, h[0][1].x, h[0][1].y);
-            ck[(2 * s + 1) * NT] = make_float4(h[1][0].x, h[1][0].y, h[1][1].x, h[1][1].y);
-            if (s + 1 < kSubs)
-#pragma unroll
-                for (int t = 0; t < kSub; ++t) forward(s * kSub + t, h, cut >> (s * kSub + t) & 1);
-        }
-#pragma unroll 1
-        for (int s = kSubs - 1; s >= 0; --s) {
-            const int ts = s * kSub;
-            float2 hs[kSub + 1][2][2];
-            {
-                const float4 k0 = ck[(2 * s) * NT], k1 = ck[(2 * s + 1) * NT];
-                hs[0][0][0] = make_float2(k0.x, k0.y);
-                hs[0][0][1] = make_float2(k0.z, k0.w);
-                hs[0][1][0] = make_float2(k1.x, k1.y);
-                hs[0][1][1] = make_float2(k1.z, k1.w);
-            }
-#pragma unroll
-            for (int t = 0; t < kSub; ++t) {
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) hs[t + 1][k][m] = hs[t][k][m];
-                forward(ts + t, hs[t + 1], cut >> (ts + t) & 1);
-            }
-#pragma unroll
-            for (int half = 1; half >= 0; --half) {
-                float ve[8], vq[8], vy[8];  // [token of four][channel]: e, sum q A, y'
-#pragma unroll
-                for (int i = 3; i >= 0; --i) {
-                    const int j = half * 4 + i, t = ts + j;
-                    const bool zero = cut >> t & 1;
-                    const float2 d = *reinterpret_cast<const float2 *>(&sm[L::d + t * CB + cl]);
-                    const float2 u = *reinterpret_cast<const float2 *>(&sm[L::u + t * CB + cl]);
-                    const float2 g = *reinterpret_cast<const float2 *>(&sm[L::g + t * CB + cl]);
-                    const float4 B4 = *reinterpret_cast<const float4 *>(&sm[L::Bm + t * NP + n0]);
-                    const float4 C4 = *reinterpret_cast<const float4 *>(&sm[L::Cm + t * NP + n0]);
-                    float2 dB[2] = {zero2, zero2}, dC[2] = {zero2, zero2};
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float2 dd = k ? make_float2(d.y, d.y) : make_float2(d.x, d.x);
-                        const float2 uu = k ? make_float2(u.y, u.y) : make_float2(u.x, u.x);
-                        const float2 gg = k ? make_float2(g.y, g.y) : make_float2(g.x, g.x);
-                        float2 e2 = zero2, q2 = zero2, y2 = zero2;
-#pragma unroll
-                        for (int m = 0; m < 2; ++m) {
-                            const float2 Bt = m ? make_float2(B4.z, B4.w) : make_float2(B4.x, B4.y);
-                            const float2 Ct = m ? make_float2(C4.z, C4.w) : make_float2(C4.x, C4.y);
-                            const float2 arg = __fmul2_rn(dd, A[k][m]);
-                            const float2 s2 = __ffma2_rn(gg, Ct, r[k][m]);
-                            dC[m] = __ffma2_rn(gg, hs[j + 1][k][m], dC[m]);
-                            y2 = __ffma2_rn(Ct, hs[j + 1][k][m], y2);
-                            dB[m] = __ffma2_rn(uu, s2, dB[m]);
-                            e2 = __ffma2_rn(Bt, s2, e2);
-                            const float2 as = __fmul2_rn(make_float2(ex2(arg.x), ex2(arg.y)), s2);
-                            const float2 q = zero ? zero2 : __fmul2_rn(as, hs[j][k][m]);
-                            q2 = __ffma2_rn(q, A[k][m], q2);
-                            dA[k][m] = __ffma2_rn(q, dd, dA[k][m]);
-                            r[k][m] = zero ? zero2 : as;
-                        }
-                        ve[2 * i + k] = e2.x + e2.y;
-                        vq[2 * i + k] = kLn2 * (q2.x + q2.y);
-                        vy[2 * i + k] = y2.x + y2.y;
-                    }
-                    float bc[8] = {dB[0].x, dB[0].y, dB[1].x, dB[1].y, dC[0].x, dC[0].y, dC[1].x, dC[1].y};
-                    spread_sum<8, CL, 1>(bc);
-                    constexpr int K = CL < 8 ? 8 / CL : 1, dup = CL > 8 ? CL / 8 : 1;
-                    float *to = sm + L::red + (warp * kSub + j) * 2 * NP + n0;
-                    if (lane % CL % dup == 0)
-#pragma unroll
-                        for (int m = 0; m < K; ++m) {
-                            const int v = lane % CL / dup * K + m;
-                            to[(v / 4) * NP + v % 4] = bc[m];
-                        }
-                }
-                spread_sum<8, LN, CL>(ve);
-                spread_sum<8, LN, CL>(vq);
-                spread_sum<8, LN, CL>(vy);
-                __syncwarp();  // these tokens' rates and inputs have been read: the sums take their places
-                constexpr int K = LN < 8 ? 8 / LN : 1, dup = LN > 8 ? LN / 8 : 1;
-                if (ng % dup == 0)
-#pragma unroll
-                    for (int m = 0; m < K; ++m) {
-                        const int v = ng / dup * K + m, at = (ts + half * 4 + v / 2) * CB + cl + v % 2;
-                        sm[L::u + at] = ve[m];
-                        sm[L::d + at] = vq[m];
-                        sm[L::g + at] = vy[m];
-                    }
-            }
-            __syncthreads();
-            // the block's sums over its channels for these kSub tokens
-            for (int v = tid; v < kSub * 2 * NP; v += NT) {
-                const int j = v / (2 * NP), w = v / NP % 2, n = v % NP;
-                if (ts + j < nt && n < p.N) {
-                    float s2 = 0.f;
-#pragma unroll
-                    for (int i = 0; i < L::W; ++i) s2 += sm[L::red + (i * kSub + j) * 2 * NP + w * NP + n];
-                    p.bc_part[((((size_t)blk * p.B + b) * p.T + t0 + ts + j) * p.G + grp) * 2 * p.N + w * p.N + n] = s2;
-                }
-            }
-            __syncthreads();
-        }
+        if (cut) scan_tile(Is<true>());
+        else scan_tile(Is<false>());
         // the token tensors' gradients
-        for (int v = tid; v < kVecs; v += NT) {
-            const int t = v / kRowVecs;
-            if (t >= nt || c0 + vch >= cend) continue;
-            Pack<T, V> px, pd, pg, pz;
-            px.load(x + (t0 + t) * p.xs[1] + c0 + vch);
-            pd.load(dl + (t0 + t) * p.ds[1] + c0 + vch);
-            pg.load(dy + (t0 + t) * p.dys[1] + c0 + vch);
-            pz.raw = {};
-            if (p.z) pz.load(z + (t0 + t) * p.zs[1] + c0 + vch);
-            float xf[V], df[V], gf[V], zf[V], dx[V], dd[V], dz[V], es[V], qs[V], ys[V];
-            unpack(px, xf);
-            unpack(pd, df);
-            unpack(pg, gf);
-            unpack(pz, zf);
+#pragma unroll
+        for (int i = 0; i < kVecIt; ++i) {
+            const int v = tid + i * NT, t = v / kRowVecs;
+            if ((kVecs % NT && v >= kVecs) || t >= nt || c0 + vch >= cend) continue;
+            float xf[V], df[V], gf[V], zf[V], dx[V], dd[V], dz[V], es[V], qs[V], ys[V], ds[V];
+            tensors(t0, nt, stage, v, xf, df, gf, zf);
             get_floats(sm + L::u + t * CB + vch, es);
-            get_floats(sm + L::d + t * CB + vch, qs);
+            get_floats(sm + L::q + t * CB + vch, qs);
             get_floats(sm + L::g + t * CB + vch, ys);
+            get_floats(sm + L::d + t * CB + vch, ds);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float e = es[j], q = qs[j];
-                float d = df[j] + bias[j], slope = 1.f, g = gf[j];
+                float slope = 1.f, g = gf[j];
                 if (p.softplus) {
-                    const float v2 = d;
-                    float ee;
-                    d = softplus(v2, ee);
-                    slope = rcp(1.f + ee);
-                    if (v2 < 0.f) slope *= ee;
+                    const float w = df[j] + bias[j], e = ex2(-kLog2e * fabsf(w));
+                    slope = rcp(1.f + e);
+                    if (w < 0.f) slope *= e;
                 }
                 if (p.z) {
                     const float sg = sigmoid(zf[j]), y = fmaf(Dv[j], xf[j], ys[j]);
                     dz[j] = g * y * sg * fmaf(zf[j], 1.f - sg, 1.f);
                     g *= zf[j] * sg;
                 }
-                dx[j] = fmaf(e, d, g * Dv[j]);
-                dd[j] = fmaf(e, xf[j], q) * slope;
+                dx[j] = fmaf(es[j], ds[j], g * Dv[j]);
+                dd[j] = fmaf(es[j], xf[j], kLn2 * qs[j]) * slope;
                 sD[j] = fmaf(g, xf[j], sD[j]);
                 sb[j] += dd[j];
             }
@@ -427,8 +478,13 @@ __global__ void __launch_bounds__(block_threads(LN)) ttt_scan_bwd_kernel(const _
                 o.store(static_cast<T *>(p.dz) + at);
             }
         }
-        __syncthreads();
+        // (what the next tile writes of d, u, g and q, and asks for in place of its raw tensors,
+        // this thread alone has read)
+        if constexpr (L::kRaw == 2) stage ^= 1;
+        if constexpr (L::kRaw == 1)
+            if (t0 > tb) copy(t0 - kTile, 0);
     }
+    __syncthreads();
 
     const size_t part = (size_t)b * p.segs + seg;
 #pragma unroll
@@ -523,7 +579,7 @@ Space space(int B, int T, int C, int N, int G)
 
 template <typename T, int LN, bool VEC> int launch_all(Params &p, const ScanArgs &a)
 {
-    using L = Layout<LN>;
+    using L = Layout<T, LN, VEC>;
     int n = 0;
     if (p.segs > 1) {
         const dim3 mg(p.G * ((p.cpg + 15) / 16), p.segs - 1, p.B);
@@ -533,9 +589,9 @@ template <typename T, int LN, bool VEC> int launch_all(Params &p, const ScanArgs
         p.start = p.H;
         n += 2;
     }
-    if (!allow_shared(ttt_scan_bwd_kernel<T, LN, VEC>, L::floats * 4)) return -4;
+    if (!allow_shared(ttt_scan_bwd_kernel<T, LN, VEC>, L::bytes)) return -4;
     const dim3 grid(p.G * p.blocks, p.segs, p.B);
-    ttt_scan_bwd_kernel<T, LN, VEC><<<grid, L::NT, L::floats * 4, a.stream>>>(p);
+    ttt_scan_bwd_kernel<T, LN, VEC><<<grid, L::NT, L::bytes, a.stream>>>(p);
     const long long rows = (long long)p.B * p.T * p.G;
     ttt_scan_bc_kernel<T><<<(unsigned)((rows * 2 * p.N + 255) / 256), 256, 0, a.stream>>>(p.bc_part, p.blocks, rows, p.N,
                                                                                          static_cast<T *>(a.dB), static_cast<T *>(a.dC));

@@ -15,9 +15,6 @@ namespace {
 using namespace scan;
 
 constexpr int kTile = kScanChunk;  // tokens staged at a time: a chunk between stored states
-template <bool V> struct Is {
-    static constexpr bool value = V;
-};
 
 // ------------------------------------------------------------------ a few tokens
 //
