@@ -144,12 +144,24 @@ __global__ void __launch_bounds__(256) ttt_scan_bwd_join_kernel(const __grid_con
     const int c = (int)(i / p.N);
     const float A = p.A[i] * kLog2e;
     float r = dh_last ? dh_last[b * per + i] : 0.f;
-    for (int s = p.segs - 1; s >= 0; --s) {
-        const size_t at = (size_t)b * p.segs + s;
-        float *w = p.H + at * per + i;
-        const float own = s > 0 ? *w : 0.f;
-        *w = r;
-        if (s > 0) r = p.cut[at] ? own : fmaf(ex2(A * p.rate_sum[at * p.C + c]), r, own);
+    constexpr int kAhead = 8;  // pieces whose maps are read together
+    for (int s0 = p.segs - 1; s0 >= 0; s0 -= kAhead) {
+        float own[kAhead], sum[kAhead];
+        int cut[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (s0 - k > 0) {
+                const size_t at = (size_t)b * p.segs + s0 - k;
+                own[k] = p.H[at * per + i];
+                sum[k] = p.rate_sum[at * p.C + c];
+                cut[k] = p.cut[at];
+            }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (s0 - k >= 0) {
+                p.H[((size_t)b * p.segs + s0 - k) * per + i] = r;
+                if (s0 - k > 0) r = cut[k] ? own[k] : fmaf(ex2(A * sum[k]), r, own[k]);
+            }
     }
 }
 
@@ -554,7 +566,7 @@ ScanPieces pieces(int B, int T, int C, int N, int G)
 {
     const int LN = lanes(N), CB = block_channels(LN);
     const long long warps = (long long)B * G * ((C / G + CB - 1) / CB) * block_threads(LN) / 32;
-    return scan::cut((T + kScanChunk - 1) / kScanChunk, warps, 16LL * 152, 4);
+    return scan::cut((T + kScanChunk - 1) / kScanChunk, warps, 16LL * 152, 1);
 }
 
 struct Space {

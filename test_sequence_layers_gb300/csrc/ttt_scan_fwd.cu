@@ -278,12 +278,25 @@ __global__ void __launch_bounds__(256) ttt_scan_join_kernel(const __grid_constan
     const int c = (int)(i / p.N);
     const float A = p.A[i] * kLog2e;
     float h = h0 ? h0[b * per + i] : 0.f;
-    for (int s = 0; s < p.segs; ++s) {
-        const size_t at = (size_t)b * p.segs + s;
-        float *w = p.H + at * per + i;
-        const float own = s + 1 < p.segs ? *w : 0.f;
-        *w = h;
-        if (s + 1 < p.segs) h = p.cut[at] ? own : fmaf(ex2(A * p.rate_sum[at * p.C + c]), h, own);
+    // kAhead pieces' maps are read together: only their order is serial
+    constexpr int kAhead = 8;
+    for (int s0 = 0; s0 < p.segs; s0 += kAhead) {
+        float own[kAhead], sum[kAhead];
+        int cut[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (s0 + k + 1 < p.segs) {
+                const size_t at = (size_t)b * p.segs + s0 + k;
+                own[k] = p.H[at * per + i];
+                sum[k] = p.rate_sum[at * p.C + c];
+                cut[k] = p.cut[at];
+            }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (s0 + k < p.segs) {
+                p.H[((size_t)b * p.segs + s0 + k) * per + i] = h;
+                if (s0 + k + 1 < p.segs) h = cut[k] ? own[k] : fmaf(ex2(A * sum[k]), h, own[k]);
+            }
     }
 }
 
