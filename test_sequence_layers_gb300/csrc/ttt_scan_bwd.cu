@@ -21,7 +21,7 @@ constexpr int block_threads(int LN) { return block_channels(LN) * LN / 2; }
 
 // Shared memory of a block, in floats: rates, inputs, gated gradients (then e and y' in the
 // places of the latter two) and sum q A; B and C; the states before every kSub tokens; a warp's
-// sums for dB and dC, twice; the tensors as they come, x, delta, dy, z, B, C (kRaw tiles).
+// sums for dB and dC, twice; a thread's for dA; the tensors as they come, x, delta, dy, z, B, C (kRaw tiles).
 template <typename T, int LN, bool VEC> struct Layout {
     static constexpr int CB = block_channels(LN), NT = block_threads(LN), NP = 4 * LN, W = NT / 32;
     static constexpr int kRaw = !VEC ? 0 : sizeof(T) == 2 ? 2 : 1;  // (two of fp32 would leave one block an SM)
@@ -29,7 +29,8 @@ template <typename T, int LN, bool VEC> struct Layout {
     static constexpr int Bm = q + kTile * CB, Cm = Bm + kTile * NP;
     static constexpr int ck = Cm + kTile * NP;
     static constexpr int red = ck + kSubs * NT * 8, red_one = W * kSub * 2 * NP;
-    static constexpr int raw = red + 2 * red_one;
+    static constexpr int dA = red + 2 * red_one;  // every thread's sums for dA over the tiles before
+    static constexpr int raw = dA + NT * 8;
     static constexpr int raw_tokens = kTile * CB * (int)sizeof(T), raw_bc = kTile * NP * (int)sizeof(T);  // bytes of one tensor
     static constexpr int raw_bytes = 4 * raw_tokens + 2 * raw_bc;
     static constexpr int bytes = raw * 4 + kRaw * raw_bytes;
@@ -200,6 +201,7 @@ __global__ void __launch_bounds__(block_threads(LN)) ttt_scan_bwd_kernel(const _
         r[k][0] = q.a;
         r[k][1] = q.b;
         dA[k][0] = dA[k][1] = zero2;
+        reinterpret_cast<float4 *>(sm + L::dA)[k * NT + tid] = zero4;
     }
     // this thread's channels before and after the scan, and their sums for dD and dbias
     const int vch = tid % kRowVecs * V;
@@ -334,9 +336,9 @@ __global__ void __launch_bounds__(block_threads(LN)) ttt_scan_bwd_kernel(const _
                     const float2 dd = k ? make_float2(d.y, d.y) : make_float2(d.x, d.x), uu = k ? make_float2(u.y, u.y) : make_float2(u.x, u.x);
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
-                        const float2 e = __fmul2_rn(dd, A[k][m]), in = __fmul2_rn(uu, m ? make_float2(Bt.z, Bt.w) : make_float2(Bt.x, Bt.y));
+                        const float2 a = decay2(dd, A[k][m]), in = __fmul2_rn(uu, m ? make_float2(Bt.z, Bt.w) : make_float2(Bt.x, Bt.y));
                         const float2 prev = kResets && zero ? zero2 : hh[k][m];
-                        hh[k][m] = __ffma2_rn(make_float2(ex2(e.x), ex2(e.y)), prev, in);
+                        hh[k][m] = __ffma2_rn(a, prev, in);
                     }
                 }
             };
@@ -393,13 +395,12 @@ __global__ void __launch_bounds__(block_threads(LN)) ttt_scan_bwd_kernel(const _
                             for (int m = 0; m < 2; ++m) {
                                 const float2 Bt = m ? make_float2(B4.z, B4.w) : make_float2(B4.x, B4.y);
                                 const float2 Ct = m ? make_float2(C4.z, C4.w) : make_float2(C4.x, C4.y);
-                                const float2 arg = __fmul2_rn(dd, A[k][m]);
                                 const float2 s2 = __ffma2_rn(gg, Ct, r[k][m]);
                                 dC[m] = k ? __ffma2_rn(gg, hs[j + 1][k][m], dC[m]) : __fmul2_rn(gg, hs[j + 1][k][m]);
                                 dB[m] = k ? __ffma2_rn(uu, s2, dB[m]) : __fmul2_rn(uu, s2);
                                 y2 = m ? __ffma2_rn(Ct, hs[j + 1][k][m], y2) : __fmul2_rn(Ct, hs[j + 1][k][m]);
                                 e2 = m ? __ffma2_rn(Bt, s2, e2) : __fmul2_rn(Bt, s2);
-                                const float2 as = __fmul2_rn(make_float2(ex2(arg.x), ex2(arg.y)), s2);
+                                const float2 as = __fmul2_rn(decay2(dd, A[k][m]), s2);
                                 const float2 q = kResets && zero ? zero2 : __fmul2_rn(as, hs[j][k][m]);
                                 q2 = m ? __ffma2_rn(q, A[k][m], q2) : __fmul2_rn(q, A[k][m]);
                                 dA[k][m] = __ffma2_rn(q, dd, dA[k][m]);
@@ -490,6 +491,16 @@ __global__ void __launch_bounds__(block_threads(LN)) ttt_scan_bwd_kernel(const _
                 o.store(static_cast<T *>(p.dz) + at);
             }
         }
+        // A tile's part of dA goes to its total by itself: two short sums round less than one
+        // over a whole piece.
+        float4 *total = reinterpret_cast<float4 *>(sm + L::dA) + tid;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float4 w = total[k * NT];
+            w = make_float4(w.x + dA[k][0].x, w.y + dA[k][0].y, w.z + dA[k][1].x, w.w + dA[k][1].y);
+            total[k * NT] = w;
+            dA[k][0] = dA[k][1] = zero2;
+        }
         // (what the next tile writes of d, u, g and q, and asks for in place of its raw tensors,
         // this thread alone has read)
         if constexpr (L::kRaw == 2) stage ^= 1;
@@ -503,7 +514,7 @@ __global__ void __launch_bounds__(block_threads(LN)) ttt_scan_bwd_kernel(const _
     for (int k = 0; k < 2; ++k) {
         const int c = c0 + cl + k;
         if (c >= cend) break;
-        store_states(p.a_part + (part * p.C + c) * p.N, n0, p.N, make_float4(dA[k][0].x, dA[k][0].y, dA[k][1].x, dA[k][1].y));
+        store_states(p.a_part + (part * p.C + c) * p.N, n0, p.N, reinterpret_cast<const float4 *>(sm + L::dA)[k * NT + tid]);
         if (p.dh0 && seg == 0)
             store_states(p.dh0 + ((size_t)b * p.C + c) * p.N, n0, p.N, make_float4(r[k][0].x, r[k][0].y, r[k][1].x, r[k][1].y));
     }
