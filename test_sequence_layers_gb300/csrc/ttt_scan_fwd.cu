@@ -268,6 +268,180 @@ __global__ void __launch_bounds__(32 * kWarps, 4) ttt_scan_fwd_kernel(const __gr
     }
 }
 
+// ----------------------------------------------------------- a whole sequence a block
+//
+// Where batch and channels alone give every scheduler two warps of four states a lane, a
+// sequence need not be cut, and its decays are taken once instead of twice.  A block has
+// kLaneCB channels with LN lanes each (the upper lane bits); rates, inputs, B and C go to shared
+// memory in fp32 once a tile, the next tile's tensors are on their way in registers.
+constexpr int kLaneCB = 16;  // 32 bytes of a bf16 row, one sector
+
+template <typename T, int LN, bool VEC>
+__global__ void __launch_bounds__(kLaneCB *LN) ttt_scan_fwd_lanes_kernel(const __grid_constant__ Params p)
+{
+    constexpr int CB = kLaneCB, NT = CB * LN, CL = 32 / LN, NP = 4 * LN;
+    constexpr int V = VEC ? 16 / (int)sizeof(T) : 1;
+    constexpr int kRowVecs = CB / V, kVecs = kTile * kRowVecs, kIt = (kVecs + NT - 1) / NT;
+    constexpr int kBVecs = kTile * NP / V, kBIt = (kBVecs + NT - 1) / NT;
+    constexpr int kAt = 4;  // tokens whose outputs are summed over the lanes together
+    static_assert(V <= NP && LN <= kAt && NT % kRowVecs == 0, "");
+    __shared__ __align__(16) float ds[kTile][CB], us[kTile][CB], ys[kTile][CB];  // rate, rate x, output
+    __shared__ __align__(16) float bs[kTile][NP], cs[kTile][NP];
+
+    const int g = blockIdx.x / p.blocks, c0 = g * p.cpg + (blockIdx.x % p.blocks) * CB, cend = (g + 1) * p.cpg, b = blockIdx.y;
+    const int tid = threadIdx.x, lane = tid & 31, cl = tid / 32 * CL + lane % CL, n0 = 4 * (lane / CL), c = c0 + cl;
+    const bool on = c < cend;
+    const T *x = static_cast<const T *>(p.x) + b * p.xs[0], *dl = static_cast<const T *>(p.delta) + b * p.ds[0];
+    const T *z = static_cast<const T *>(p.z) + b * p.zs[0];
+    const T *Bm = static_cast<const T *>(p.Bm) + b * p.bs[0] + g * p.bs[2], *Cm = static_cast<const T *>(p.Cm) + b * p.cs[0] + g * p.cs[2];
+    const unsigned char *reset = p.reset ? p.reset + (size_t)b * p.T : nullptr;
+
+    const Quad zero = quad(make_float4(0.f, 0.f, 0.f, 0.f));
+    Quad A = zero, h = zero;
+    if (on) {
+        A = quad(load_states(p.A + (size_t)c * p.N, n0, p.N, 0.f));
+        A.a = __fmul2_rn(A.a, make_float2(kLog2e, kLog2e));
+        A.b = __fmul2_rn(A.b, make_float2(kLog2e, kLog2e));
+        if (p.start) h = quad(load_states(p.start + ((size_t)b * p.C + c) * p.N, n0, p.N, 0.f));
+    }
+    Pack<T, V> px[kIt], pd[kIt], pz[kIt], pb[kBIt], pc[kBIt];
+    const int vch = c0 + tid % kRowVecs * V;  // this thread's channels in every pass
+    auto fetch = [&](int t0) {
+#pragma unroll
+        for (int i = 0; i < kIt; ++i) {
+            const int v = tid + i * NT, t = t0 + v / kRowVecs;
+            px[i].raw = pd[i].raw = pz[i].raw = {};
+            if ((kVecs % NT == 0 || v < kVecs) && t < p.T && vch < cend) {
+                px[i].load(x + t * p.xs[1] + vch);
+                pd[i].load(dl + t * p.ds[1] + vch);
+                if (p.z) pz[i].load(z + t * p.zs[1] + vch);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kBIt; ++i) {
+            const int v = tid + i * NT, t = t0 + v / (NP / V), n = v % (NP / V) * V;
+            pb[i].raw = pc[i].raw = {};
+            if ((kBVecs % NT == 0 || v < kBVecs) && t < p.T && n < p.N) {
+                pb[i].load(Bm + t * p.bs[1] + n);
+                pc[i].load(Cm + t * p.cs[1] + n);
+            }
+        }
+    };
+    float bias[V], Dv[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        bias[j] = p.bias && vch + j < cend ? p.bias[vch + j] : 0.f;
+        Dv[j] = p.D && vch + j < cend ? p.D[vch + j] : 0.f;
+    }
+    fetch(0);
+    for (int t0 = 0; t0 < p.T; t0 += kTile) {
+        const int nt = min(kTile, p.T - t0);
+        if (p.states && on) store_states(p.states + (((size_t)b * p.chunks + t0 / kScanChunk) * p.C + c) * p.N, n0, p.N, four(h));
+        unsigned cut = 0;  // tokens of the tile with a reset
+        if (reset) cut = __ballot_sync(0xffffffffu, lane < nt && reset[t0 + lane]);
+        Pack<T, V> qx[kIt], qz[kIt];  // kept for the outputs
+#pragma unroll
+        for (int i = 0; i < kIt; ++i) {
+            const int v = tid + i * NT, t = v / kRowVecs;
+            if (kVecs % NT && v >= kVecs) break;
+            qx[i] = px[i];
+            qz[i] = pz[i];
+            float d[V], u[V];
+            unpack(px[i], u);
+            unpack(pd[i], d);
+            const bool live = t < nt && vch < cend;
+#pragma unroll
+            for (int j = 0; j < V; ++j) d[j] += bias[j];
+            if (p.softplus) softplus_all(d);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                if (!live) d[j] = 0.f;  // past the end: the state stays
+                u[j] *= d[j];
+            }
+            put_floats(&ds[t][vch - c0], d);
+            put_floats(&us[t][vch - c0], u);
+        }
+#pragma unroll
+        for (int i = 0; i < kBIt; ++i) {
+            const int v = tid + i * NT, t = v / (NP / V), n = v % (NP / V) * V;
+            if (kBVecs % NT && v >= kBVecs) break;
+            float f[V];
+            unpack(pb[i], f);
+            put_floats(&bs[t][n], f);
+            unpack(pc[i], f);
+            put_floats(&cs[t][n], f);
+        }
+        if (t0 + kTile < p.T) fetch(t0 + kTile);
+        __syncthreads();
+        // Three tokens are under way at once: one is read, the one before has its decays taken,
+        // the one before that moves the states.
+        auto tokens = [&](auto resets) {
+            float d, u;
+            float4 Bt, Ct;
+            Quad a, in;
+            float4 Cr;
+            auto read = [&](int t) {
+                d = ds[t][cl];
+                u = us[t][cl];
+                Bt = *reinterpret_cast<const float4 *>(&bs[t][n0]);
+                Ct = *reinterpret_cast<const float4 *>(&cs[t][n0]);
+            };
+            auto ready = [&]() {
+                const float2 uu = make_float2(u, u);
+                a = decays(d, A);
+                in = {__fmul2_rn(uu, make_float2(Bt.x, Bt.y)), __fmul2_rn(uu, make_float2(Bt.z, Bt.w))};
+                Cr = Ct;
+            };
+            read(0);
+            ready();
+            read(1);
+            constexpr int kUnroll = decltype(resets)::value ? 1 : 2;
+#pragma unroll kUnroll
+            for (int t = 0; t < kTile; t += kAt) {
+                float yv[kAt];
+#pragma unroll
+                for (int k = 0; k < kAt; ++k) {
+                    const Quad a1 = a, in1 = in;
+                    const float4 C1 = Cr;
+                    ready();
+                    read((t + k + 2) % kTile);  // (the last two are read for nothing)
+                    if (decltype(resets)::value && (cut >> (t + k) & 1)) h = zero;
+                    h.a = __ffma2_rn(a1.a, h.a, in1.a);
+                    h.b = __ffma2_rn(a1.b, h.b, in1.b);
+                    float2 s;
+                    dot(s, h, C1, true);
+                    yv[k] = s.x + s.y;
+                }
+                spread_sum<kAt, LN, CL>(yv);
+                constexpr int K = kAt / LN;
+#pragma unroll
+                for (int k = 0; k < K; ++k) ys[t + lane / CL * K + k][cl] = yv[k];
+            }
+        };
+        if (cut) tokens(Is<true>());
+        else tokens(Is<false>());
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kIt; ++i) {
+            const int v = tid + i * NT, t = v / kRowVecs;
+            if ((kVecs % NT && v >= kVecs) || t >= nt || vch >= cend) continue;
+            float o[V], xf[V], zf[V];
+            get_floats(&ys[t][vch - c0], o);
+            unpack(qx[i], xf);
+            unpack(qz[i], zf);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                o[j] = fmaf(Dv[j], xf[j], o[j]);
+                if (p.z) o[j] *= zf[j] * sigmoid(zf[j]);
+            }
+            Pack<T, V> r;
+            pack(r, o);
+            r.store(static_cast<T *>(p.y) + ((size_t)b * p.T + t0 + t) * p.C + vch);
+        }
+    }
+    if (p.y_state && on) store_states(p.y_state + ((size_t)b * p.C + c) * p.N, n0, p.N, four(h));
+}
+
 // The state before every piece from the pieces' maps: start [B,segs,C,N] over H (in place),
 // one thread a channel and state.  The last piece's map is not made.
 __global__ void __launch_bounds__(256) ttt_scan_join_kernel(const __grid_constant__ Params p, const float *h0)
@@ -319,11 +493,33 @@ template <typename T, int LN, int Q, bool VEC> int launch_tiles(Params &p, const
     return cudaGetLastError() == cudaSuccess ? (p.segs > 1 ? 3 : 1) : -4;
 }
 
+template <typename T, int LN, bool VEC> int launch_whole(Params &p, const ScanArgs &a)
+{
+    p.blocks = (p.cpg + kLaneCB - 1) / kLaneCB;
+    ttt_scan_fwd_lanes_kernel<T, LN, VEC><<<dim3(p.G * p.blocks, p.B), kLaneCB * LN, 0, a.stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? 1 : -4;
+}
+
 template <typename T, int LN> int launch_step(Params &p, const ScanArgs &a)
 {
     const dim3 grid((unsigned)(((long long)p.C * LN + 127) / 128), p.B);
     ttt_scan_step_kernel<T, LN><<<grid, 128, 0, a.stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? 1 : -4;
+}
+
+// Is the whole-sequence kernel the one to take?  N up to 16, rows that 16-byte accesses can
+// take, seven of its warps an SM at least, and fewer than eight of the tile kernel's, which
+// would then have to cut every sequence (us for B x T x 1536 channels, N = 16, bf16, whole
+// sequences against pieces: 4 x 2048 140 and 130, 6 x 2048 157 and 169, 8 x 2048 192 and 224,
+// 16 x 1024 194 and 206, 32 x 512 169 and 149, where the tile kernel needs no pieces either;
+// rows of 1533 channels and 12 states 142 and 132).
+bool whole_sequences(int B, int T, int C, int N, int G)
+{
+    if (N > 16 || N % 8 || C / G % 8 || T <= kScanStepTokens) return false;
+    const long long LN = N <= 8 ? 2 : 4;
+    const long long warps = (long long)B * G * ((C / G + kLaneCB - 1) / kLaneCB) * kLaneCB * LN / 32;
+    const long long others = (long long)B * G * ((C / G + 31) / 32);
+    return warps >= 7 * 152 && others < 8 * 152;
 }
 
 template <typename T> int launch_type(Params &p, const ScanArgs &a, bool vec)
@@ -335,6 +531,10 @@ template <typename T> int launch_type(Params &p, const ScanArgs &a, bool vec)
         case 8: return launch_step<T, 8>(p, a);
         default: return launch_step<T, 16>(p, a);
         }
+    }
+    if (whole_sequences(p.B, p.T, p.C, p.N, p.G)) {
+        if (p.N <= 8) return vec ? launch_whole<T, 2, true>(p, a) : launch_whole<T, 2, false>(p, a);
+        return vec ? launch_whole<T, 4, true>(p, a) : launch_whole<T, 4, false>(p, a);
     }
     if (p.N <= 8) return vec ? launch_tiles<T, 1, 2, true>(p, a) : launch_tiles<T, 1, 2, false>(p, a);
     switch (tile_lanes(p.N)) {
@@ -348,6 +548,7 @@ template <typename T> int launch_type(Params &p, const ScanArgs &a, bool vec)
 // tokens and more.
 ScanPieces pieces(int B, int T, int C, int N, int G)
 {
+    if (whole_sequences(B, T, C, N, G)) return {1, T};
     const int CL = 32 / tile_lanes(N), chunks = (T + kScanChunk - 1) / kScanChunk;
     const long long warps = (long long)B * G * ((C / G + CL - 1) / CL);
     return scan::cut(chunks, warps, 16LL * 152, 2);

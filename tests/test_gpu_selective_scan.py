@@ -95,6 +95,27 @@ def test_many_channels_without_pieces():
     _check(i)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("N,kw", [(16, {}), (8, {}), (16, dict(gate=False, state=False)), (16, dict(resets=0.05)),
+                                  (16, dict(softplus=False, skip=False))])
+def test_whole_sequences(N, kw, dtype):
+    """Enough channels for a block a sequence, groups with a last block that is not full, a length
+    that ends inside a tile."""
+    assert abi.ttt_selective_scan_fwd_workspace(24, 75, 1056, 16, 2) == 0
+    assert abi.ttt_selective_scan_fwd_workspace(24, 75, 2112, 8, 2) == 0
+    i = D.scan_inputs(24, 75, 1056 * 16 // N, N, 2, dtype=dtype, **kw)
+    if kw.get("resets"):
+        i["x"][3, 20], i["reset"][3, 21] = float("inf"), True  # seen by token 20 alone
+        i["dy"][3, 20], i["dy"][3, :21] = 0, 0
+        got, ref = _run(dict(i, dy=None)), D.scan(dict(i, dy=None))
+        for n in ("y", "h_last"):
+            ok = torch.isfinite(ref[n][0])
+            D.close(n, got[n][ok], ref[n][0][ok], ref[n][1][ok])
+        assert bool(torch.isfinite(got["y"][3, 21:]).all())
+    else:
+        _check(i)
+
+
 @pytest.mark.parametrize("T", [6, 300])
 def test_masked_states_may_hold_anything(T):
     """Infinities and NaN in a packed sequence reach neither the next one nor its gradients."""
