@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(16 * LN) ttt_scan_bwd_map_kernel(const __grid_
     constexpr int V = VEC ? 16 / (int)sizeof(T) : 1, kRowVecs = kCB / V, kVecs = kTile * kRowVecs;
     constexpr int kIt = (kVecs + kThreads - 1) / kThreads;
     constexpr int kBV = V < NP ? V : NP, kBVecs = kTile * NP / kBV, kBIt = (kBVecs + kThreads - 1) / kThreads;
-    __shared__ float2 du[kTile][kCB];
+    __shared__ __align__(16) float ds[kTile][kCB], gs[kTile][kCB];  // rate, gated gradient
     __shared__ __align__(16) float cs[kTile][NP];
 
     const int blocks = (p.cpg + kCB - 1) / kCB;
@@ -71,61 +71,83 @@ __global__ void __launch_bounds__(16 * LN) ttt_scan_bwd_map_kernel(const __grid_
         const int ch = c0 + tid % kRowVecs * V + j;
         bias[j] = p.bias && ch < cend ? p.bias[ch] : 0.f;
     }
-    for (int t0 = tb + (te - tb - 1) / kTile * kTile; t0 >= tb; t0 -= kTile) {
+    // the tile's raw tensors, asked for a tile ahead
+    Pack<T, V> pg[kIt], pd[kIt], pz[kIt];
+    Pack<T, kBV> pc[kBIt];
+    const int vch = c0 + tid % kRowVecs * V;
+    auto fetch = [&](int t0) {
+#pragma unroll
+        for (int i = 0; i < kIt; ++i) {
+            const int v = tid + i * kThreads, t = t0 + v / kRowVecs;
+            pg[i].raw = pd[i].raw = pz[i].raw = {};
+            if ((kVecs % kThreads == 0 || v < kVecs) && t < te && vch < cend) {
+                pg[i].load(dy + t * p.dys[1] + vch);
+                pd[i].load(dl + t * p.ds[1] + vch);
+                if (p.z) pz[i].load(z + t * p.zs[1] + vch);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kBIt; ++i) {
+            const int v = tid + i * kThreads, t = t0 + v / (NP / kBV), n = v % (NP / kBV) * kBV;
+            pc[i].raw = {};
+            if ((kBVecs % kThreads == 0 || v < kBVecs) && t < te && n < p.N) pc[i].load(Cm + t * p.cs[1] + n);
+        }
+    };
+    int t0 = tb + (te - tb - 1) / kTile * kTile;
+    fetch(t0);
+    for (; t0 >= tb; t0 -= kTile) {
         const int nt = min(kTile, te - t0);
         unsigned cut = 0;
         if (reset) cut = __ballot_sync(0xffffffffu, lane < nt && reset[t0 + lane]);
         any_cut |= cut;
 #pragma unroll
         for (int i = 0; i < kIt; ++i) {
-            const int v = tid + i * kThreads, t = v / kRowVecs, ch = v % kRowVecs * V;
+            const int v = tid + i * kThreads, t = v / kRowVecs;
             if (kVecs % kThreads && v >= kVecs) break;
-            const bool live = t < nt && c0 + ch < cend;
-            Pack<T, V> pg, pd, pz;
-            pg.raw = pd.raw = pz.raw = {};
-            if (live) {
-                pg.load(dy + (t0 + t) * p.dys[1] + c0 + ch);
-                pd.load(dl + (t0 + t) * p.ds[1] + c0 + ch);
-                if (p.z) pz.load(z + (t0 + t) * p.zs[1] + c0 + ch);
-            }
+            const bool live = t < nt && vch < cend;
             float gf[V], df[V], zf[V];
-            unpack(pg, gf);
-            unpack(pd, df);
-            unpack(pz, zf);
+            unpack(pg[i], gf);
+            unpack(pd[i], df);
+            unpack(pz[i], zf);
+#pragma unroll
+            for (int j = 0; j < V; ++j) df[j] += bias[j];
+            if (p.softplus) softplus_all(df);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                float e, d = df[j] + bias[j];
-                if (p.softplus) d = softplus(d, e);
+                if (!live) df[j] = 0.f;  // past the end: nothing moves (the gradient is zero there)
                 if (p.z) gf[j] *= zf[j] * sigmoid(zf[j]);
-                du[t][ch + j] = make_float2(live ? d : 0.f, live ? gf[j] : 0.f);
             }
+            put_floats(&ds[t][vch - c0], df);
+            put_floats(&gs[t][vch - c0], gf);
         }
 #pragma unroll
         for (int i = 0; i < kBIt; ++i) {
             const int v = tid + i * kThreads, t = v / (NP / kBV), n = v % (NP / kBV) * kBV;
             if (kBVecs % kThreads && v >= kBVecs) break;
-            Pack<T, kBV> q;
-            q.raw = {};
-            if (t < nt && n < p.N) q.load(Cm + (t0 + t) * p.cs[1] + n);
             float f[kBV];
-            unpack(q, f);
-#pragma unroll
-            for (int j = 0; j < kBV; ++j) cs[t][n + j] = f[j];
+            unpack(pc[i], f);
+            put_floats(&cs[t][n], f);
         }
+        if (t0 > tb) fetch(t0 - kTile);
         __syncthreads();
-#pragma unroll 4
-        for (int t = kTile - 1; t >= 0; --t) {
-            const float2 w = du[t][cl], gg = make_float2(w.y, w.y);
-            const float4 Ct = *reinterpret_cast<const float4 *>(&cs[t][n0]);
-            const Quad a = decays(w.x, A);
-            r.a = __fmul2_rn(a.a, __ffma2_rn(gg, make_float2(Ct.x, Ct.y), r.a));
-            r.b = __fmul2_rn(a.b, __ffma2_rn(gg, make_float2(Ct.z, Ct.w), r.b));
-            rate_sum += w.x;
-            if (cut >> t & 1) {
-                r = quad(make_float4(0.f, 0.f, 0.f, 0.f));
-                rate_sum = 0.f;
+        auto tokens = [&](auto resets) {
+#pragma unroll 8
+            for (int t = kTile - 1; t >= 0; --t) {
+                const float d = ds[t][cl], w = gs[t][cl];
+                const float2 gg = make_float2(w, w);
+                const float4 Ct = *reinterpret_cast<const float4 *>(&cs[t][n0]);
+                const Quad a = decays(d, A);
+                r.a = __fmul2_rn(a.a, __ffma2_rn(gg, make_float2(Ct.x, Ct.y), r.a));
+                r.b = __fmul2_rn(a.b, __ffma2_rn(gg, make_float2(Ct.z, Ct.w), r.b));
+                rate_sum += d;
+                if (decltype(resets)::value && (cut >> t & 1)) {
+                    r = quad(make_float4(0.f, 0.f, 0.f, 0.f));
+                    rate_sum = 0.f;
+                }
             }
-        }
+        };
+        if (cut) tokens(Is<true>());
+        else tokens(Is<false>());
         __syncthreads();
     }
     const size_t at = ((size_t)b * p.segs + seg) * p.C + c;
