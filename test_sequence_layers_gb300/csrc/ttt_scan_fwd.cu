@@ -5,8 +5,13 @@
 // [C,N].  A reset before token t makes h_{t-1} zero there.
 //
 // Bound by the exponentials and the products: one ex2 and four FMA-pipe operations a state
-// and token, 32 states a clock and SM by either pipe; the tensors read and written once take
-// two thirds of that time at N = 16 in bf16.
+// and token, 32 states a clock and SM by either pipe (measured: 9.5e12 a second), 43 us at
+// 8 x 2048 tokens of 1536 channels with 16 states, where the tensors read and written once take
+// 30 us.  Three kernels (bf16, 16 states):
+//   a few tokens       64 x 1 x 1536           7.6 us from cold caches (states 2 x 6.3 MB)
+//   whole sequences    8 x 2048 x 1536         187 us
+//   pieces in parallel 1 x 32768 x 2048        214 us the pieces' maps, 9 us joining them,
+//                                              300 us the outputs (115 us by either pipe each)
 #include "ttt_scan.cuh"
 
 namespace ttt {
@@ -16,22 +21,51 @@ using namespace scan;
 
 constexpr int kTile = kScanChunk;  // tokens staged at a time: a chunk between stored states
 
+// entries n0 .. n0 + 3 of a row of N of B or C, zeros past its end
+template <bool FOURS, typename T> __device__ __forceinline__ float4 load_four(const T *row, int n0, int N)
+{
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (FOURS) {
+        if (n0 < N) {
+            Pack<T, 4> q;
+            q.load(row + n0);
+            unpack(q, v);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (n0 + j < N) v[j] = get(row + n0 + j);
+    }
+    return make_float4(v[0], v[1], v[2], v[3]);
+}
+
 // ------------------------------------------------------------------ a few tokens
 //
 // LN neighbouring lanes a channel, four states each, token after token straight from memory:
 // decoding steps, whose cost is the states' read and write and one trip to memory.
-template <typename T, int LN> __global__ void __launch_bounds__(128) ttt_scan_step_kernel(const __grid_constant__ Params p)
+// FOURS: N a multiple of four, all states, B and C aligned to four of theirs: no branch stands
+// between the loads, which wait for memory together.
+template <typename T, int LN, bool FOURS>
+__global__ void __launch_bounds__(128) ttt_scan_step_kernel(const __grid_constant__ Params p)
 {
+    auto load_states = [](const float *row, int n0, int N) {
+        if constexpr (!FOURS) return scan::load_states(row, n0, N, 0.f);
+        else return n0 < N ? *reinterpret_cast<const float4 *>(row + n0) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    auto store_states = [](float *row, int n0, int N, float4 v) {
+        if constexpr (!FOURS) scan::store_states(row, n0, N, v);
+        else if (n0 < N) *reinterpret_cast<float4 *>(row + n0) = v;
+    };
     const long long i = ((long long)blockIdx.x * 128 + threadIdx.x) / LN;
     const int n0 = 4 * (threadIdx.x % LN), b = blockIdx.y;
     const bool on = i < p.C;
-    const int c = on ? (int)i : p.C - 1, g = c / p.cpg;
+    const int c = on ? (int)i : p.C - 1, g = p.G == 1 ? 0 : c / p.cpg;
     const size_t row = ((size_t)b * p.C + c) * p.N;
     const T *x = static_cast<const T *>(p.x) + b * p.xs[0] + c, *dl = static_cast<const T *>(p.delta) + b * p.ds[0] + c;
     const T *z = p.z ? static_cast<const T *>(p.z) + b * p.zs[0] + c : nullptr;
     const T *Bm = static_cast<const T *>(p.Bm) + b * p.bs[0] + g * p.bs[2], *Cm = static_cast<const T *>(p.Cm) + b * p.cs[0] + g * p.cs[2];
-    Quad h = quad(p.start ? load_states(p.start + row, n0, p.N, 0.f) : make_float4(0.f, 0.f, 0.f, 0.f));
-    Quad A = quad(load_states(p.A + (size_t)c * p.N, n0, p.N, 0.f));
+    Quad h = quad(p.start ? load_states(p.start + row, n0, p.N) : make_float4(0.f, 0.f, 0.f, 0.f));
+    Quad A = quad(load_states(p.A + (size_t)c * p.N, n0, p.N));
     A.a = __fmul2_rn(A.a, make_float2(kLog2e, kLog2e));
     A.b = __fmul2_rn(A.b, make_float2(kLog2e, kLog2e));
     const float D = p.D ? p.D[c] : 0.f, bias = p.bias ? p.bias[c] : 0.f;
@@ -39,13 +73,7 @@ template <typename T, int LN> __global__ void __launch_bounds__(128) ttt_scan_st
         if (p.states && t % kScanChunk == 0 && on)
             store_states(p.states + (((size_t)b * p.chunks + t / kScanChunk) * p.C + c) * p.N, n0, p.N, four(h));
         if (p.reset && p.reset[(size_t)b * p.T + t]) h = quad(make_float4(0.f, 0.f, 0.f, 0.f));
-        float4 Bt = make_float4(0.f, 0.f, 0.f, 0.f), Ct = Bt;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (n0 + j < p.N) {
-                (&Bt.x)[j] = get(Bm + t * p.bs[1] + n0 + j);
-                (&Ct.x)[j] = get(Cm + t * p.cs[1] + n0 + j);
-            }
+        const float4 Bt = load_four<FOURS>(Bm + t * p.bs[1], n0, p.N), Ct = load_four<FOURS>(Cm + t * p.cs[1], n0, p.N);
         const float xv = get(x + t * p.xs[1]), zv = z ? get(z + t * p.zs[1]) : 0.f;
         float d = get(dl + t * p.ds[1]) + bias, e;
         if (p.softplus) d = softplus(d, e);
@@ -70,6 +98,12 @@ template <typename T, int LN> __global__ void __launch_bounds__(128) ttt_scan_st
 // go to shared memory in fp32, a tile of tokens at a time and one tile ahead; x, delta and z
 // come straight from memory, kAt tokens ahead.
 // SUM: only the piece's map, from a zero state (its sum of rates, its own contribution).
+//
+// 16 states a lane: B and C are read once for 512 states, and no output is summed over lanes (4
+// states a lane wait for shared memory, 418 us at 1 x 32768 x 2048 for the outputs alone; 16
+// with the token tensors staged there as well 337 us; straight from memory 300).  111
+// instructions a warp and token, issue slots 62% busy, FMA pipe 52%, ex2 43% (maps 54%).  Four
+// blocks an SM by 128 registers; five or six spill (313 and 334 us).
 constexpr int kWarps = 4;
 
 template <typename T, int LN, int Q, bool VEC, bool SUM>
@@ -273,7 +307,10 @@ __global__ void __launch_bounds__(32 * kWarps, 4) ttt_scan_fwd_kernel(const __gr
 // Where batch and channels alone give every scheduler two warps of four states a lane, a
 // sequence need not be cut, and its decays are taken once instead of twice.  A block has
 // kLaneCB channels with LN lanes each (the upper lane bits); rates, inputs, B and C go to shared
-// memory in fp32 once a tile, the next tile's tensors are on their way in registers.
+// memory in fp32 once a tile, the next tile's tensors are on their way in registers.  Bound by
+// shared memory's data path (69% busy: B and C are read again for every 128 states) and by the
+// latency that two and a half warps a scheduler leave: with the loop's tokens one after the other
+// 214 us at 8 x 2048 x 1536, three under way at once 187.
 constexpr int kLaneCB = 16;  // 32 bytes of a bf16 row, one sector
 
 template <typename T, int LN, bool VEC>
@@ -503,7 +540,13 @@ template <typename T, int LN, bool VEC> int launch_whole(Params &p, const ScanAr
 template <typename T, int LN> int launch_step(Params &p, const ScanArgs &a)
 {
     const dim3 grid((unsigned)(((long long)p.C * LN + 127) / 128), p.B);
-    ttt_scan_step_kernel<T, LN><<<grid, 128, 0, a.stream>>>(p);
+    bool fours = a.N % 4 == 0;
+    for (const void *q : {(const void *)a.A, (const void *)a.h0, (const void *)a.h_last, (const void *)a.states})
+        fours = fours && reinterpret_cast<uintptr_t>(q) % 16 == 0;
+    for (const void *q : {a.Bm, a.Cm}) fours = fours && reinterpret_cast<uintptr_t>(q) % (4 * sizeof(T)) == 0;
+    for (int i = 0; i < 3; ++i) fours = fours && (a.bs[i] | a.cs[i]) % 4 == 0;
+    if (fours) ttt_scan_step_kernel<T, LN, true><<<grid, 128, 0, a.stream>>>(p);
+    else ttt_scan_step_kernel<T, LN, false><<<grid, 128, 0, a.stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? 1 : -4;
 }
 

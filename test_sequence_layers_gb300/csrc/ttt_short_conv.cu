@@ -7,7 +7,11 @@
 // with p computed again from x.
 //
 // Bound by reading and writing every tensor once: a thread walks along the tokens of one
-// piece with the last K - 1 rows of its V neighbouring channels in registers.
+// piece with the last K - 1 rows of its V neighbouring channels in registers.  Measured, K = 4,
+// SiLU, bf16 (of the copy bandwidth by bytes read and written once): 2 x 32768 x 2048 forward
+// 92 us (0.86), backward 192 us (0.62: 163 registers leave 12 warps an SM, issue slots 60%
+// busy; the sums of the taps' gradients alone are 20 of them); 8 x 2048 x 768 forward 14.8 us
+// (0.50: ramp-up and tail), backward 24; fp32 2 x 16384 x 2048 86 and 152 us.
 #include "ttt_internal.h"
 #include "ttt_vec.cuh"
 
