@@ -497,7 +497,7 @@ typedef enum { TTT_CONV_NONE = 0, TTT_CONV_SILU = 1 } ttt_conv_act;
 /* Short causal convolution problem description.  Strides in elements (batch, token);
  * channels are contiguous. */
 typedef struct {
-    int B, T, C;               /* batch, tokens (<= 2^30), channels                     */
+    int B, T, C;               /* batch, tokens, channels (B T < 2^31, T and C <= 2^30)  */
     int width;                 /* K, taps of a channel: 1 .. 4 (TTT_ERR_UNSUPPORTED above) */
     ttt_dtype io_dtype;        /* dtype of x, y, the states, dy, dx                     */
     int act;                   /* ttt_conv_act                                          */
@@ -518,9 +518,9 @@ typedef struct {
  *   y         : [B,T,C] io_dtype, contiguous
  *   state_out : [B,K-1,C] io_dtype or NULL: the last K-1 inputs of the running sequence
  *               (zeros before its start); may be state itself
- * Sums in fp32, rounded once.  Data pointers: aligned to their element; 16-byte alignment,
- * strides of whole 16 bytes and C a multiple of 8 (bf16) or 4 (fp32) move 16 bytes at a
- * time.  Outputs may not overlap inputs or each other (state_out as above).
+ * Sums in fp32, rounded once.  Data pointers: aligned to their element; where pointers,
+ * strides and C are multiples of four elements, four move at a time.  Outputs may not
+ * overlap inputs or each other (state_out as above).
  */
 ttt_status ttt_short_conv_fwd(const ttt_short_conv_desc *desc, const void *x, const float *weight, const float *bias,
                               const unsigned char *reset, const void *state, void *y, void *state_out, void *stream);

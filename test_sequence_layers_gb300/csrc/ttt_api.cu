@@ -1052,7 +1052,8 @@ ttt_status conv_args(const ttt_short_conv_desc *desc, const void *x, const float
     const ttt_short_conv_desc &D = *desc;
     for (int i = 0; i < 2; ++i)
         if (D.x_stride[i] < 0 || D.dy_stride[i] < 0) return TTT_ERR_ARG;
-    if (D.width > ttt::kConvMaxWidth || (long long)D.B * D.T > 0x7fffffffLL || D.T > 1 << 30) return TTT_ERR_UNSUPPORTED;
+    if (D.width > ttt::kConvMaxWidth || (long long)D.B * D.T > 0x7fffffffLL || D.T > 1 << 30 || D.C > 1 << 30)
+        return TTT_ERR_UNSUPPORTED;
     const int es = D.io_dtype == TTT_BF16 ? 2 : 4;
     if (!weight) return TTT_ERR_ARG;
     if (!aligned(weight, 4) || (bias && !aligned(bias, 4)) || (state && !aligned(state, es))) return TTT_ERR_ALIGN;
@@ -1126,7 +1127,8 @@ ttt_status ttt_short_conv_fwd(const ttt_short_conv_desc *desc, const void *x, co
 
 size_t ttt_short_conv_bwd_workspace(const ttt_short_conv_desc *desc)
 {
-    if (!desc || !conv_desc_ok(*desc) || desc->width > ttt::kConvMaxWidth || desc->B == 0 || desc->T == 0) return 0;
+    if (!desc || !conv_desc_ok(*desc) || desc->width > ttt::kConvMaxWidth || desc->C > 1 << 30 || desc->B == 0 || desc->T == 0)
+        return 0;
     return ttt::conv_bwd_workspace(desc->B, desc->T, desc->C, desc->width);
 }
 

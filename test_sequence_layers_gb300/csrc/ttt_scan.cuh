@@ -205,7 +205,7 @@ __device__ __forceinline__ void store_states(float *row, int n0, int N, float4 v
         if (n0 + i < N) row[n0 + i] = f[i];
 }
 
-// 2^(d A), A in units of log2 e.  ex2 of arguments between -0.5 and 0 comes out 5e-9 to 2.2e-8
+// 2^(d A), A in units of log2 e.  ex2 of arguments between -1 and 0 comes out 5e-9 to 2.2e-8
 // too low on average (measured), always the same way, which a slow state sums up over the
 // thousand tokens that it remembers; the addend, which costs nothing in the product, leaves
 // 9e-9 of either sign.  Where d A is 0 the decay is 1 exactly (measured up to addends of 1.1e-7).

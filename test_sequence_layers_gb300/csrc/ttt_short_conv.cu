@@ -28,6 +28,7 @@ struct ConvParams {
     void *y, *state_out, *dx;
     float *dstate, *part;
     int B, T, C, nv, pieces, len, silu;
+    int few;  // forward: fewer than 2^31 threads
 };
 
 __device__ __forceinline__ float sigmoid(float v)
@@ -108,7 +109,7 @@ __device__ __forceinline__ void rows_before(const ConvParams &p, const T *x, con
         if (r >= 0) load_row<T, V>(x + r * p.xs[1], win[i]);
         else if (state) {
             Pack<T, V> q;
-            q.load_rw(state + (r + K - 1) * p.C);
+            q.load_rw(state + (size_t)(r + K - 1) * p.C);
             unpack(q, win[i]);
         }
     }
@@ -129,7 +130,17 @@ __device__ __forceinline__ void rows_before(const ConvParams &p, const T *x, con
 template <typename T, int V, int K> __global__ void __launch_bounds__(kThreads) ttt_short_conv_fwd_kernel(const __grid_constant__ ConvParams p)
 {
     const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
-    const int cv = (int)(i % p.nv), piece = (int)(i / p.nv % p.pieces), b = (int)(i / p.nv / p.pieces);
+    int cv, piece, b;
+    if (p.few) {  // 32-bit divisions do
+        const unsigned j = (unsigned)i, k = j / (unsigned)p.nv;
+        cv = (int)(j - k * (unsigned)p.nv);
+        b = (int)(k / (unsigned)p.pieces);
+        piece = (int)k - b * p.pieces;
+    } else {
+        cv = (int)(i % p.nv);
+        piece = (int)(i / p.nv % p.pieces);
+        b = (int)(i / p.nv / p.pieces);
+    }
     if (b >= p.B) return;
     const int c = cv * V, t0 = piece * p.len, t1 = min(p.T, t0 + p.len);
     const T *x = static_cast<const T *>(p.x) + b * p.xs[0] + c;
@@ -156,11 +167,11 @@ template <typename T, int V, int K> __global__ void __launch_bounds__(kThreads) 
                 if (!hidden) last[k].load(x + r * p.xs[1]);
                 hidden = hidden || (reset && reset[r]);
             } else if (!hidden && state) {
-                last[k].load_rw(state + (r + K - 1) * p.C);
+                last[k].load_rw(state + (size_t)(r + K - 1) * p.C);
             }
         }
 #pragma unroll
-        for (int k = 0; k < K - 1; ++k) last[k].store(out + k * p.C);
+        for (int k = 0; k < K - 1; ++k) last[k].store(out + (size_t)k * p.C);
     }
     // kAhead rows are on their way while the ones before them are worked on; the window turns
     // in place over K of them: row t + a goes to place (a + K - 1) % K, row t + a - K + 1 is at
@@ -430,15 +441,17 @@ template <typename T, int V> int fwd_width(const ConvArgs &a)
 {
     ConvParams p;
     conv_params(a, p, V);
-    // tokens a thread walks: 4 .. 64, as many as leave 512 threads an SM (K - 1 rows and the
-    // taps are read once a piece; 8 x 2048 x 768 bf16: 20 tokens 14.8 us, 4 tokens 58 us, and
-    // at 2 x 32768 x 2048 64 tokens 95 us, 32 101, 16 116)
-    const long long fill = (long long)a.B * a.T * p.nv / (512LL * kSMs);
+    // tokens a thread walks: 4 .. 64, as many as leave 512 threads an SM, 1024 where they move
+    // less at a time (K - 1 rows and the taps are read once a piece; 8 x 2048 x 768 bf16: 20
+    // tokens 14.8 us, 4 tokens 58; 2 x 32768 x 2048: 64 tokens 95 us, 32 101, 16 116; 3 x 701 x
+    // 1001 fp32, K = 3: 13 tokens 8.1 us, 27 10.5)
+    const long long fill = (long long)a.B * a.T * p.nv / ((V == 4 ? 512LL : 1024LL) * kSMs);
     p.len = (int)(fill < 4 ? 4 : fill > 64 ? 64 : fill);
     p.pieces = (a.T + p.len - 1) / p.len;
     const long long n = (long long)a.B * p.pieces * p.nv;
     const long long blocks = (n + kThreads - 1) / kThreads;
     if (blocks > 0x7fffffffLL) return -2;
+    p.few = blocks * kThreads <= 0x7fffffffLL;
     switch (a.K) {
     case 1: ttt_short_conv_fwd_kernel<T, V, 1><<<(unsigned)blocks, kThreads, 0, a.stream>>>(p); break;
     case 2: ttt_short_conv_fwd_kernel<T, V, 2><<<(unsigned)blocks, kThreads, 0, a.stream>>>(p); break;

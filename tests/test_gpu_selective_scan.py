@@ -141,6 +141,16 @@ def test_rates_from_tiny_to_large():
     _check(i)
 
 
+@pytest.mark.parametrize("B,T,C", [(2, 7, 40), (1, 3000, 40), (8, 400, 1536), (40, 40, 2048)])
+@pytest.mark.parametrize("still", ["rate", "A"])
+def test_a_state_without_decay_stays_as_it_is(B, T, C, still):
+    """exp(0) is one exactly: with the rate or A zero and no input, states keep their bits."""
+    i = D.scan_inputs(B, T, C, 16, dtype=F32, softplus=False, train=False)
+    i["B"].zero_()
+    (i["delta"] if still == "rate" else i["A"]).zero_()
+    assert torch.equal(_run(i)["h_last"], i["h0"])
+
+
 def test_gate_far_from_zero():
     i = D.scan_inputs(1, 64, 32, 16, dtype=F32, seed=4)
     i["z"] *= torch.logspace(-2, 1.8, 32, device="cuda")

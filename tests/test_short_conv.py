@@ -57,6 +57,7 @@ def test_conv_forward_refusals(L):
                 dict(state=_at(4), state_out=_at(4) + 16), dict(strides=[-1, 64, 0, 0])):
         assert _conv_fwd(L, **bad) == -1, bad
     assert _conv_fwd(L, width=5) == -2 and _conv_fwd(L, B=1 << 20, T=1 << 20) == -2
+    assert _conv_fwd(L, C=(1 << 30) + 1) == -2
     assert _conv_fwd(L, B=0) == 0 and _conv_fwd(L, T=0) == 0
     for bad in (dict(x=_at(1) + 1), dict(y=_at(3) + 1), dict(w=_at(2) + 2), dict(bias=_at(5) + 1), dict(state=_at(5) + 1),
                 dict(state_out=_at(5) + 1)):
