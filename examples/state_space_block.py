@@ -59,7 +59,7 @@ class SelectiveScan(torch.autograd.Function):
 
 
 class StateSpaceBlock:
-    def __init__(self, H=12, d=64, N=16, rank=48, K=4, grid=(4, 14, 14), dtype=torch.bfloat16, seed=0, device="cuda"):
+    def __init__(self, H=8, d=64, N=16, rank=32, K=4, grid=(4, 14, 14), dtype=torch.bfloat16, seed=0, device="cuda"):
         W, E = H * d, 2 * H * d
         g = torch.Generator().manual_seed(seed)
         self.H, self.d, self.W, self.E, self.N, self.rank, self.K, self.grid, self.dtype = H, d, W, E, N, rank, K, grid, dtype

@@ -916,17 +916,20 @@ def _conv_prologue(x, weight, bias, act, reset, state, dy=None):
         _tokens("x", x, 3)
         sx = (*sx[:2], 1)
     B, T, C = shape = x.shape
-    if weight.dim() != 2:
+    wshape = weight.shape
+    if len(wshape) != 2:
         raise ValueError("weight must be [C,K]")
-    K = weight.shape[1]
-    _like("weight", weight, (C, K), _F32, di)
-    if bias is not None:
+    K = wshape[1]
+    if wshape[0] != C or weight.dtype is not _F32 or weight.get_device() != di or not weight.is_contiguous():
+        _like("weight", weight, (C, K), _F32, di)
+    if bias is not None and (bias.dtype is not _F32 or bias.get_device() != di or bias.shape != (C,) or not bias.is_contiguous()):
         _like("bias", bias, (C,), _F32, di)
     sd = _NO_STRIDE2 if dy is None else _rows("dy", dy, x, shape, dt, di)
     if reset is not None:
         _reset(reset, shape, di)
     sshape = (B, K - 1, C)
-    if state is not None:
+    if state is not None and (state.dtype is not dt or state.get_device() != di or state.shape != sshape
+                              or not state.is_contiguous()):
         _like("state", state, sshape, dt, di)
     return shape, K, dt, x.device, di, sshape, _CONV_DESC.pack(B, T, C, K, io, CONV_ACTS[act], sx[0], sx[1], *sd)
 
@@ -999,21 +1002,20 @@ def _scan_prologue(x, delta, A, B, C, D, z, delta_bias, softplus, reset, dy=None
         _tokens("x", x, 3)
         sx = (*sx[:2], 1)
     nb, T, ch = shape = x.shape
-    if A.dim() != 2:
+    cn, bshape = A.shape, B.shape
+    if len(cn) != 2:
         raise ValueError("A must be [C,N]")
-    N = A.shape[1]
-    _like("A", A, (ch, N), _F32, di)
+    N = cn[1]
+    if cn[0] != ch or A.dtype is not _F32 or A.get_device() != di or not A.is_contiguous():
+        _like("A", A, (ch, N), _F32, di)
     sdl = _rows("delta", delta, x, shape, dt, di)
-    if B.dim() == 4:
-        G = B.shape[2]
+    if len(bshape) == 4:
+        G = bshape[2]
         bshape = (nb, T, G, N)
-        sb = _rows("B", B, x, bshape, dt, di)
-        sc = _rows("C", C, x, bshape, dt, di)
+        sb, sc = _rows("B", B, x, bshape, dt, di), _rows("C", C, x, bshape, dt, di)
     else:
-        G = 1
-        bshape = (nb, T, N)
-        sb = (*_rows("B", B, x, bshape, dt, di), 0)
-        sc = (*_rows("C", C, x, bshape, dt, di), 0)
+        G, bshape = 1, (nb, T, N)
+        sb, sc = (*_rows("B", B, x, bshape, dt, di), 0), (*_rows("C", C, x, bshape, dt, di), 0)
     if G < 1 or ch % G:
         raise ValueError("the groups of B and C must divide the channels")
     sz = _NO_STRIDE2 if z is None else _rows("z", z, x, shape, dt, di)
@@ -1024,7 +1026,7 @@ def _scan_prologue(x, delta, A, B, C, D, z, delta_bias, softplus, reset, dy=None
     par = _THREE.pack(A.data_ptr(), 0 if D is None else _vec("D", D, vec, di),
                       0 if delta_bias is None else _vec("delta_bias", delta_bias, vec, di))
     desc = _SCAN_DESC.pack(nb, T, ch, N, G, io, bool(softplus), sx[0], sx[1], *sdl, *sz, *sdy, *sb, *sc)
-    return shape, (ch, N), bshape, dt, x.device, di, desc, par
+    return shape, cn, bshape, dt, x.device, di, desc, par
 
 
 def ttt_selective_scan_fwd(x, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=True, reset=None, h0=None, y=None,
@@ -1044,7 +1046,7 @@ def ttt_selective_scan_fwd(x, delta, A, B, C, D=None, z=None, delta_bias=None, s
     shape, cn, _, dt, dev, di, desc, par = _scan_prologue(x, delta, A, B, C, D, z, delta_bias, softplus, reset)
     nb, T, _ = shape
     hshape = (nb, *cn)
-    if h0 is not None:
+    if h0 is not None and (h0.dtype is not _F32 or h0.get_device() != di or h0.shape != hshape or not h0.is_contiguous()):
         _like("h0", h0, hshape, _F32, di)
     if states is not None:
         _like("states", states, (nb, -(-T // SCAN_CHUNK), *cn), _F32, di)
@@ -1052,9 +1054,10 @@ def ttt_selective_scan_fwd(x, delta, A, B, C, D=None, z=None, delta_bias=None, s
         states = _empty((nb, -(-T // SCAN_CHUNK), *cn), dtype=_F32, device=dev)
     y = _empty(shape, dtype=dt, device=dev) if y is None else _like("y", y, shape, dt, di)
     h_last = _empty(hshape, dtype=_F32, device=dev) if h_last is None else _like("h_last", h_last, hshape, _F32, di)
-    # (a single token needs no workspace)
-    need = _workspace_bytes("ttt_selective_scan_fwd_workspace", desc) if T > 1 and workspace is None else 0
-    ws, nws, _keep = _scratch("x", workspace, need, dev, di)
+    ws = nws = 0
+    if T > 1 or workspace is not None:  # a single token needs no workspace
+        need = _workspace_bytes("ttt_selective_scan_fwd_workspace", desc) if workspace is None else 0
+        ws, nws, _keep = _scratch("x", workspace, need, dev, di)
     _call("ttt_selective_scan_fwd", di, desc, par, x.data_ptr(), delta.data_ptr(), B.data_ptr(), C.data_ptr(),
           0 if z is None else z.data_ptr(), 0 if reset is None else reset.data_ptr(), 0 if h0 is None else h0.data_ptr(),
           y.data_ptr(), h_last.data_ptr(), 0 if states is None else states.data_ptr(), ws, nws)
