@@ -9,7 +9,7 @@
 // 8 x 2048 tokens of 1536 channels with 16 states, where the tensors read and written once take
 // 30 us.  Three kernels (bf16, 16 states):
 //   a few tokens       64 x 1 x 1536           7.6 us from cold caches (states 2 x 6.3 MB)
-//   whole sequences    8 x 2048 x 1536         187 us
+//   whole sequences    8 x 2048 x 1536         182 us
 //   pieces in parallel 1 x 32768 x 2048        214 us the pieces' maps, 9 us joining them,
 //                                              300 us the outputs (115 us by either pipe each)
 #include "ttt_scan.cuh"
@@ -308,10 +308,41 @@ __global__ void __launch_bounds__(32 * kWarps, 4) ttt_scan_fwd_kernel(const __gr
 // sequence need not be cut, and its decays are taken once instead of twice.  A block has
 // kLaneCB channels with LN lanes each (the upper lane bits); rates, inputs, B and C go to shared
 // memory in fp32 once a tile, the next tile's tensors are on their way in registers.  Bound by
-// shared memory's data path (69% busy: B and C are read again for every 128 states) and by the
+// shared memory's data path (64% busy: B and C are read again for every 128 states) and by the
 // latency that two and a half warps a scheduler leave: with the loop's tokens one after the other
-// 214 us at 8 x 2048 x 1536, three under way at once 187.
+// 214 us at 8 x 2048 x 1536, three under way at once 187, stores without bank conflicts 182.  768
+// blocks on 152 SMs: six on some, five on others.
 constexpr int kLaneCB = 16;  // 32 bytes of a bf16 row, one sector
+
+// Where a row's entry i lies: every other pair of tokens has its groups of four exchanged two
+// and two, so that threads which store neighbouring halves of rows meet different banks.
+__device__ __forceinline__ int turned(int i, int t) { return i ^ ((t & 2) << 1); }
+template <int V> __device__ __forceinline__ void put_turned(float *row, int i, int t, const float (&v)[V])
+{
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+        for (int j = 0; j < V; j += 4) *reinterpret_cast<float4 *>(row + turned(i + j, t)) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) row[turned(i + j, t)] = v[j];
+    }
+}
+template <int V> __device__ __forceinline__ void get_turned(const float *row, int i, int t, float (&v)[V])
+{
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+        for (int j = 0; j < V; j += 4) {
+            const float4 q = *reinterpret_cast<const float4 *>(row + turned(i + j, t));
+            v[j] = q.x;
+            v[j + 1] = q.y;
+            v[j + 2] = q.z;
+            v[j + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = row[turned(i + j, t)];
+    }
+}
 
 template <typename T, int LN, bool VEC>
 __global__ void __launch_bounds__(kLaneCB *LN) ttt_scan_fwd_lanes_kernel(const __grid_constant__ Params p)
@@ -395,8 +426,8 @@ __global__ void __launch_bounds__(kLaneCB *LN) ttt_scan_fwd_lanes_kernel(const _
                 if (!live) d[j] = 0.f;  // past the end: the state stays
                 u[j] *= d[j];
             }
-            put_floats(&ds[t][vch - c0], d);
-            put_floats(&us[t][vch - c0], u);
+            put_turned(ds[t], vch - c0, t, d);
+            put_turned(us[t], vch - c0, t, u);
         }
 #pragma unroll
         for (int i = 0; i < kBIt; ++i) {
@@ -404,9 +435,9 @@ __global__ void __launch_bounds__(kLaneCB *LN) ttt_scan_fwd_lanes_kernel(const _
             if (kBVecs % NT && v >= kBVecs) break;
             float f[V];
             unpack(pb[i], f);
-            put_floats(&bs[t][n], f);
+            put_turned(bs[t], n, t, f);
             unpack(pc[i], f);
-            put_floats(&cs[t][n], f);
+            put_turned(cs[t], n, t, f);
         }
         if (t0 + kTile < p.T) fetch(t0 + kTile);
         __syncthreads();
@@ -417,11 +448,11 @@ __global__ void __launch_bounds__(kLaneCB *LN) ttt_scan_fwd_lanes_kernel(const _
             float4 Bt, Ct;
             Quad a, in;
             float4 Cr;
-            auto read = [&](int t) {
-                d = ds[t][cl];
-                u = us[t][cl];
-                Bt = *reinterpret_cast<const float4 *>(&bs[t][n0]);
-                Ct = *reinterpret_cast<const float4 *>(&cs[t][n0]);
+            auto read = [&](int t, int k) {  // (k has t's low bits, known at compile time)
+                d = ds[t][turned(cl, k)];
+                u = us[t][turned(cl, k)];
+                Bt = *reinterpret_cast<const float4 *>(&bs[t][turned(n0, k)]);
+                Ct = *reinterpret_cast<const float4 *>(&cs[t][turned(n0, k)]);
             };
             auto ready = [&]() {
                 const float2 uu = make_float2(u, u);
@@ -429,9 +460,9 @@ __global__ void __launch_bounds__(kLaneCB *LN) ttt_scan_fwd_lanes_kernel(const _
                 in = {__fmul2_rn(uu, make_float2(Bt.x, Bt.y)), __fmul2_rn(uu, make_float2(Bt.z, Bt.w))};
                 Cr = Ct;
             };
-            read(0);
+            read(0, 0);
             ready();
-            read(1);
+            read(1, 1);
             constexpr int kUnroll = decltype(resets)::value ? 1 : 2;
 #pragma unroll kUnroll
             for (int t = 0; t < kTile; t += kAt) {
@@ -441,7 +472,7 @@ __global__ void __launch_bounds__(kLaneCB *LN) ttt_scan_fwd_lanes_kernel(const _
                     const Quad a1 = a, in1 = in;
                     const float4 C1 = Cr;
                     ready();
-                    read((t + k + 2) % kTile);  // (the last two are read for nothing)
+                    read((t + k + 2) % kTile, k + 2);  // (the last two are read for nothing)
                     if (decltype(resets)::value && (cut >> (t + k) & 1)) h = zero;
                     h.a = __ffma2_rn(a1.a, h.a, in1.a);
                     h.b = __ffma2_rn(a1.b, h.b, in1.b);
@@ -452,7 +483,7 @@ __global__ void __launch_bounds__(kLaneCB *LN) ttt_scan_fwd_lanes_kernel(const _
                 spread_sum<kAt, LN, CL>(yv);
                 constexpr int K = kAt / LN;
 #pragma unroll
-                for (int k = 0; k < K; ++k) ys[t + lane / CL * K + k][cl] = yv[k];
+                for (int k = 0; k < K; ++k) ys[t + lane / CL * K + k][turned(cl, lane / CL * K + k)] = yv[k];
             }
         };
         if (cut) tokens(Is<true>());
@@ -463,7 +494,7 @@ __global__ void __launch_bounds__(kLaneCB *LN) ttt_scan_fwd_lanes_kernel(const _
             const int v = tid + i * NT, t = v / kRowVecs;
             if ((kVecs % NT && v >= kVecs) || t >= nt || vch >= cend) continue;
             float o[V], xf[V], zf[V];
-            get_floats(&ys[t][vch - c0], o);
+            get_turned(ys[t], vch - c0, t, o);
             unpack(qx[i], xf);
             unpack(qz[i], zf);
 #pragma unroll
