@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(16 * LN) ttt_scan_bwd_map_kernel(const __grid_
         A.a = __fmul2_rn(A.a, make_float2(kLog2e, kLog2e));
         A.b = __fmul2_rn(A.b, make_float2(kLog2e, kLog2e));
     }
-    float rate_sum = 0.f;
+    float rate_sum = 0.f, rate_tile = 0.f;  // of the tiles behind, of this one
     unsigned any_cut = 0;
     static_assert(kThreads % kRowVecs == 0, "");
     float bias[V];
@@ -150,15 +150,17 @@ __global__ void __launch_bounds__(16 * LN) ttt_scan_bwd_map_kernel(const __grid_
                 const Quad a = decays(d, A);
                 r.a = __fmul2_rn(a.a, __ffma2_rn(gg, make_float2(Ct.x, Ct.y), r.a));
                 r.b = __fmul2_rn(a.b, __ffma2_rn(gg, make_float2(Ct.z, Ct.w), r.b));
-                rate_sum += d;
+                rate_tile += d;
                 if (decltype(resets)::value && (cut >> t & 1)) {
                     r = quad(make_float4(0.f, 0.f, 0.f, 0.f));
-                    rate_sum = 0.f;
+                    rate_sum = rate_tile = 0.f;
                 }
             }
         };
         if (cut) tokens(Is<true>());
         else tokens(Is<false>());
+        rate_sum += rate_tile;
+        rate_tile = 0.f;
         __syncthreads();
     }
     const size_t at = ((size_t)b * p.segs + seg) * p.C + c;

@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) ttt_scan_fwd_kernel(const __gr
         dl += kAt * dls;
         if constexpr (!SUM) z += kAt * zs;
     };
-    float rate_sum = 0.f;
+    float rate_sum = 0.f, rate_tile = 0.f;  // SUM: of the tiles before, of this one
     unsigned any_cut = 0;
 
     fetch(tb);
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) ttt_scan_fwd_kernel(const __gr
                     if (decltype(resets)::value && (cut >> (t + k) & 1)) {
 #pragma unroll
                         for (int q = 0; q < Q; ++q) h[q] = zero;
-                        rate_sum = 0.f;
+                        rate_sum = rate_tile = 0.f;
                     }
                     float2 s = make_float2(0.f, 0.f);
 #pragma unroll
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) ttt_scan_fwd_kernel(const __gr
                         if constexpr (!SUM) dot(s, h[q], *reinterpret_cast<const float4 *>(&cs[buf][t + k][n0 + 4 * LN * q]), q == 0);
                     }
                     if constexpr (SUM) {
-                        rate_sum += d[k];
+                        rate_tile += d[k];
                     } else {
                         o[k] = s.x + s.y;
 #pragma unroll
@@ -285,6 +285,10 @@ __global__ void __launch_bounds__(32 * kWarps, 4) ttt_scan_fwd_kernel(const __gr
                 }
                 y += (size_t)kAt * p.C;
             }
+        }
+        if constexpr (SUM) {
+            rate_sum += rate_tile;
+            rate_tile = 0.f;
         }
         if (more) stage(buf ^ 1);
         __syncthreads();
