@@ -146,6 +146,37 @@ template <int V> __device__ __forceinline__ void get_floats(const float *p, floa
     }
 }
 
+// Where entry i of a row in shared memory lies: where bit 1 of t is set, its groups of four are
+// exchanged two and two, so that threads which store eight entries each, four at a time, meet
+// different banks (t: the token for rows of 16, i / 16 for rows of 64).
+__device__ __forceinline__ int turned(int i, int t) { return i ^ ((t & 2) << 1); }
+template <int V> __device__ __forceinline__ void put_turned(float *row, int i, int t, const float (&v)[V])
+{
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+        for (int j = 0; j < V; j += 4) *reinterpret_cast<float4 *>(row + turned(i + j, t)) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) row[turned(i + j, t)] = v[j];
+    }
+}
+template <int V> __device__ __forceinline__ void get_turned(const float *row, int i, int t, float (&v)[V])
+{
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+        for (int j = 0; j < V; j += 4) {
+            const float4 q = *reinterpret_cast<const float4 *>(row + turned(i + j, t));
+            v[j] = q.x;
+            v[j + 1] = q.y;
+            v[j + 2] = q.z;
+            v[j + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = row[turned(i + j, t)];
+    }
+}
+
 // Sums of M values over the L lanes that differ in the bits S, 2 S, .. (L/2) S of the lane
 // number, spread over them: while more than one value is left every step halves the values a
 // lane keeps (the lane with the bit clear the first half), after that all lanes add up.

@@ -12,7 +12,7 @@
 // operations, 170 us at 8 x 2048 x 1536 with 16 states; the sums over channels (dB, dC: eight
 // values over the eight lanes of a state) and over states (three values a channel, over four
 // lanes) come on top, and take a quarter of the kernel's time (92 and 60 of 650 us in an earlier
-// build).  Measured there, bf16: pieces' maps 78 us, joining them 4, main kernel 547, dB and
+// build).  Measured there, bf16: pieces' maps 79 us, joining them 4, main kernel 540, dB and
 // dC of the blocks' sums 12, dA, dD and dbias 4; instructions 204 a warp and token of 256
 // states, issue slots 50% busy with the eight warps an SM that 251 registers leave.  Three
 // blocks an SM (168 registers, one stage of raw tensors) took 562 us, and 519 in shorter pieces
@@ -215,6 +215,7 @@ __global__ void __launch_bounds__(block_threads(LN)) ttt_scan_bwd_kernel(const _
     const int c0 = grp * p.cpg + blk * CB, cend = (grp + 1) * p.cpg, seg = blockIdx.y, b = blockIdx.z;
     const int tb = seg * p.seg_len, te = min(p.T, tb + p.seg_len);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cl = warp * 2 * CL + lane % CL * 2, ng = lane / CL, n0 = 4 * ng;
+    const int ct = turned(cl, cl >> 4);  // where channel cl lies in a row
     const T *x = static_cast<const T *>(p.x) + b * p.xs[0], *dl = static_cast<const T *>(p.delta) + b * p.ds[0];
     const T *z = static_cast<const T *>(p.z) + b * p.zs[0], *dy = static_cast<const T *>(p.dy) + b * p.dys[0];
     const T *Bm = static_cast<const T *>(p.Bm) + b * p.bs[0] + grp * p.bs[2], *Cm = static_cast<const T *>(p.Cm) + b * p.cs[0] + grp * p.cs[2];
@@ -334,10 +335,10 @@ __global__ void __launch_bounds__(block_threads(LN)) ttt_scan_bwd_kernel(const _
             if (p.z)
 #pragma unroll
                 for (int j = 0; j < V; ++j) gf[j] *= zf[j] * sigmoid(zf[j]);
-            const int at = t * CB + vch;
-            put_floats(sm + L::d + at, df);
-            put_floats(sm + L::u + at, xf);
-            put_floats(sm + L::g + at, gf);
+            const int at = t * CB;
+            put_turned(sm + L::d + at, vch, vch >> 4, df);
+            put_turned(sm + L::u + at, vch, vch >> 4, xf);
+            put_turned(sm + L::g + at, vch, vch >> 4, gf);
         }
         for (int v = tid; v < kBVecs; v += NT) {
             const int t = v / (NP / kBV), n = v % (NP / kBV) * kBV;
@@ -363,8 +364,8 @@ __global__ void __launch_bounds__(block_threads(LN)) ttt_scan_bwd_kernel(const _
             constexpr bool kResets = decltype(resets)::value;
             auto forward = [&](int t, float2 (&hh)[2][2]) {
                 const bool zero = kResets && (cut >> t & 1);
-                const float2 d = *reinterpret_cast<const float2 *>(&sm[L::d + t * CB + cl]);
-                const float2 u = *reinterpret_cast<const float2 *>(&sm[L::u + t * CB + cl]);
+                const float2 d = *reinterpret_cast<const float2 *>(&sm[L::d + t * CB + ct]);
+                const float2 u = *reinterpret_cast<const float2 *>(&sm[L::u + t * CB + ct]);
                 const float4 Bt = *reinterpret_cast<const float4 *>(&sm[L::Bm + t * NP + n0]);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -414,9 +415,9 @@ __global__ void __launch_bounds__(block_threads(LN)) ttt_scan_bwd_kernel(const _
                     for (int i = 3; i >= 0; --i) {
                         const int j = half * 4 + i, t = ts + j;
                         const bool zero = kResets && (cut >> t & 1);
-                        const float2 d = *reinterpret_cast<const float2 *>(&sm[L::d + t * CB + cl]);
-                        const float2 u = *reinterpret_cast<const float2 *>(&sm[L::u + t * CB + cl]);
-                        const float2 g = *reinterpret_cast<const float2 *>(&sm[L::g + t * CB + cl]);
+                        const float2 d = *reinterpret_cast<const float2 *>(&sm[L::d + t * CB + ct]);
+                        const float2 u = *reinterpret_cast<const float2 *>(&sm[L::u + t * CB + ct]);
+                        const float2 g = *reinterpret_cast<const float2 *>(&sm[L::g + t * CB + ct]);
                         const float4 B4 = *reinterpret_cast<const float4 *>(&sm[L::Bm + t * NP + n0]);
                         const float4 C4 = *reinterpret_cast<const float4 *>(&sm[L::Cm + t * NP + n0]);
                         float2 dB[2], dC[2];
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(block_threads(LN)) ttt_scan_bwd_kernel(const _
                     if (ng % dup == 0)
 #pragma unroll
                         for (int m = 0; m < K; ++m) {
-                            const int v = ng / dup * K + m, at = (ts + half * 4 + v / 2) * CB + cl + v % 2;
+                            const int v = ng / dup * K + m, at = (ts + half * 4 + v / 2) * CB + ct + v % 2;
                             sm[L::u + at] = ve[m];
                             sm[L::q + at] = vq[m];
                             sm[L::g + at] = vy[m];
@@ -493,10 +494,10 @@ __global__ void __launch_bounds__(block_threads(LN)) ttt_scan_bwd_kernel(const _
             if ((kVecs % NT && v >= kVecs) || t >= nt || c0 + vch >= cend) continue;
             float xf[V], df[V], gf[V], zf[V], dx[V], dd[V], dz[V], es[V], qs[V], ys[V], ds[V];
             tensors(t0, nt, stage, v, xf, df, gf, zf);
-            get_floats(sm + L::u + t * CB + vch, es);
-            get_floats(sm + L::q + t * CB + vch, qs);
-            get_floats(sm + L::g + t * CB + vch, ys);
-            get_floats(sm + L::d + t * CB + vch, ds);
+            get_turned(sm + L::u + t * CB, vch, vch >> 4, es);
+            get_turned(sm + L::q + t * CB, vch, vch >> 4, qs);
+            get_turned(sm + L::g + t * CB, vch, vch >> 4, ys);
+            get_turned(sm + L::d + t * CB, vch, vch >> 4, ds);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 float slope = 1.f, g = gf[j];

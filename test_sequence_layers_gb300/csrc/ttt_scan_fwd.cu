@@ -318,36 +318,6 @@ __global__ void __launch_bounds__(32 * kWarps, 4) ttt_scan_fwd_kernel(const __gr
 // blocks on 152 SMs: six on some, five on others.
 constexpr int kLaneCB = 16;  // 32 bytes of a bf16 row, one sector
 
-// Where a row's entry i lies: every other pair of tokens has its groups of four exchanged two
-// and two, so that threads which store neighbouring halves of rows meet different banks.
-__device__ __forceinline__ int turned(int i, int t) { return i ^ ((t & 2) << 1); }
-template <int V> __device__ __forceinline__ void put_turned(float *row, int i, int t, const float (&v)[V])
-{
-    if constexpr (V % 4 == 0) {
-#pragma unroll
-        for (int j = 0; j < V; j += 4) *reinterpret_cast<float4 *>(row + turned(i + j, t)) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) row[turned(i + j, t)] = v[j];
-    }
-}
-template <int V> __device__ __forceinline__ void get_turned(const float *row, int i, int t, float (&v)[V])
-{
-    if constexpr (V % 4 == 0) {
-#pragma unroll
-        for (int j = 0; j < V; j += 4) {
-            const float4 q = *reinterpret_cast<const float4 *>(row + turned(i + j, t));
-            v[j] = q.x;
-            v[j + 1] = q.y;
-            v[j + 2] = q.z;
-            v[j + 3] = q.w;
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = row[turned(i + j, t)];
-    }
-}
-
 template <typename T, int LN, bool VEC>
 __global__ void __launch_bounds__(kLaneCB *LN) ttt_scan_fwd_lanes_kernel(const __grid_constant__ Params p)
 {
