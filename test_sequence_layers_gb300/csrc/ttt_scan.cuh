@@ -25,7 +25,7 @@ struct Params {
     int blocks;   // channel blocks of a group
     int segs, seg_len;       // pieces of the sequence, tokens of one (a multiple of the chunk)
     int chunks;
-    const float *start;      // forward: state before each piece [B,segs,C,N], or [B,C,N] (one piece), or null
+    const float *start;      // state before (backward: gradient behind) each piece [B,segs,C,N], or null
     float *y_state;          // h_last or null
     float *states;           // forward: written; backward: read
     void *y;
