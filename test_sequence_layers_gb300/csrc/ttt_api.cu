@@ -1043,6 +1043,10 @@ bool conv_desc_ok(const ttt_short_conv_desc &D)
     if (D.B < 0 || D.T < 0 || D.C < 1 || D.width < 1 || D.act < 0 || D.act > 1) return false;
     return D.io_dtype == TTT_F32 || D.io_dtype == TTT_BF16;
 }
+bool conv_desc_fits(const ttt_short_conv_desc &D)
+{
+    return D.width <= ttt::kConvMaxWidth && (long long)D.B * D.T <= 0x7fffffffLL && D.T <= 1 << 30 && D.C <= 1 << 30;
+}
 
 // Checks the part both directions share and fills the launch arguments.
 ttt_status conv_args(const ttt_short_conv_desc *desc, const void *x, const float *weight, const float *bias,
@@ -1052,8 +1056,7 @@ ttt_status conv_args(const ttt_short_conv_desc *desc, const void *x, const float
     const ttt_short_conv_desc &D = *desc;
     for (int i = 0; i < 2; ++i)
         if (D.x_stride[i] < 0 || D.dy_stride[i] < 0) return TTT_ERR_ARG;
-    if (D.width > ttt::kConvMaxWidth || (long long)D.B * D.T > 0x7fffffffLL || D.T > 1 << 30 || D.C > 1 << 30)
-        return TTT_ERR_UNSUPPORTED;
+    if (!conv_desc_fits(D)) return TTT_ERR_UNSUPPORTED;
     const int es = D.io_dtype == TTT_BF16 ? 2 : 4;
     if (!weight) return TTT_ERR_ARG;
     if (!aligned(weight, 4) || (bias && !aligned(bias, 4)) || (state && !aligned(state, es))) return TTT_ERR_ALIGN;
@@ -1127,8 +1130,7 @@ ttt_status ttt_short_conv_fwd(const ttt_short_conv_desc *desc, const void *x, co
 
 size_t ttt_short_conv_bwd_workspace(const ttt_short_conv_desc *desc)
 {
-    if (!desc || !conv_desc_ok(*desc) || desc->width > ttt::kConvMaxWidth || desc->C > 1 << 30 || desc->B == 0 || desc->T == 0)
-        return 0;
+    if (!desc || !conv_desc_ok(*desc) || !conv_desc_fits(*desc) || desc->B == 0 || desc->T == 0) return 0;
     return ttt::conv_bwd_workspace(desc->B, desc->T, desc->C, desc->width);
 }
 

@@ -75,6 +75,14 @@ def test_conv_backward_refusals(L):
     assert abi.ttt_short_conv_bwd_workspace(2, 300, 64, 4) >= 64 * 5 * 4
 
 
+@pytest.mark.parametrize("over", [dict(B=1 << 20, T=1 << 20, C=8), dict(B=1, T=(1 << 31) - 1, C=8), dict(C=(1 << 30) + 1),
+                                  dict(width=5), dict(B=1 << 16, T=1 << 15, C=8)])
+def test_no_workspace_for_a_convolution_that_is_refused(L, over):
+    """The binding allocates what the query says before the call can refuse."""
+    assert _conv_bwd(L, **over) == -2 and _conv_fwd(L, **over) == -2
+    assert L.ttt_short_conv_bwd_workspace(_conv_desc(**over)) == 0
+
+
 @pytest.mark.parametrize("bad", [
     dict(x=_Dev((2, 9))), dict(x=_Dev((2, 9, 8), cuda=False)), dict(x=_Dev((2, 9, 8), torch.float16)),
     dict(x=_Dev((2, 9, 8), last=2)), dict(weight=_Dev((8, 4), BF)), dict(weight=_Dev((7, 4), F32)), dict(weight=_Dev((8,), F32)),
