@@ -501,7 +501,7 @@ typedef struct {
     int width;                 /* K, taps of a channel: 1 .. 4 (TTT_ERR_UNSUPPORTED above) */
     ttt_dtype io_dtype;        /* dtype of x, y, the states, dy, dx                     */
     int act;                   /* ttt_conv_act                                          */
-    long long x_stride[2], dy_stride[2];
+    long long x_stride[2], dy_stride[2]; /* dy's: the backward pass alone reads them      */
 } ttt_short_conv_desc;
 
 /*
@@ -556,7 +556,8 @@ typedef struct {
     int G;                     /* groups of C / G neighbouring channels with one B and C  */
     ttt_dtype io_dtype;        /* dtype of every token tensor                           */
     int softplus;              /* 1: the rate is softplus(delta + bias); 0: delta + bias  */
-    long long x_stride[2], delta_stride[2], z_stride[2], dy_stride[2]; /* batch, token   */
+    long long x_stride[2], delta_stride[2], z_stride[2], dy_stride[2]; /* batch, token; dy's:
+                                  the backward pass alone reads them                    */
     long long b_stride[3], c_stride[3];                                /* batch, token, group */
 } ttt_scan_desc;
 

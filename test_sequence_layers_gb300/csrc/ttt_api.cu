@@ -1054,8 +1054,7 @@ ttt_status conv_args(const ttt_short_conv_desc *desc, const void *x, const float
 {
     if (!desc || !conv_desc_ok(*desc)) return TTT_ERR_ARG;
     const ttt_short_conv_desc &D = *desc;
-    for (int i = 0; i < 2; ++i)
-        if (D.x_stride[i] < 0 || D.dy_stride[i] < 0) return TTT_ERR_ARG;
+    if (D.x_stride[0] < 0 || D.x_stride[1] < 0) return TTT_ERR_ARG;
     if (!conv_desc_fits(D)) return TTT_ERR_UNSUPPORTED;
     const int es = D.io_dtype == TTT_BF16 ? 2 : 4;
     if (!weight) return TTT_ERR_ARG;
@@ -1077,10 +1076,7 @@ ttt_status conv_args(const ttt_short_conv_desc *desc, const void *x, const float
     a.reset = reset;
     a.state = D.width > 1 ? state : nullptr;
     const int n[2] = {D.B, D.T};
-    for (int i = 0; i < 2; ++i) {
-        a.xs[i] = n[i] > 1 ? D.x_stride[i] : 0;
-        a.dys[i] = n[i] > 1 ? D.dy_stride[i] : 0;
-    }
+    for (int i = 0; i < 2; ++i) a.xs[i] = n[i] > 1 ? D.x_stride[i] : 0;
     a.stream = static_cast<cudaStream_t>(stream);
     return TTT_OK;
 }
@@ -1143,6 +1139,9 @@ ttt_status ttt_short_conv_bwd(const ttt_short_conv_desc *desc, const void *dy, c
     ttt_status st = conv_args(desc, x, weight, bias, reset, state, stream, a);
     if (st != TTT_OK) return st;
     const int es = a.bf16 ? 2 : 4;
+    if (desc->dy_stride[0] < 0 || desc->dy_stride[1] < 0) return TTT_ERR_ARG;
+    a.dys[0] = a.B > 1 ? desc->dy_stride[0] : 0;
+    a.dys[1] = a.T > 1 ? desc->dy_stride[1] : 0;
     for (const float *q : {dstate_out, (const float *)dweight, (const float *)dbias, (const float *)dstate})
         if (q && !aligned(q, 4)) return TTT_ERR_ALIGN;
     if (a.K == 1) {
@@ -1208,7 +1207,7 @@ ttt_status scan_args(const ttt_scan_desc *desc, const ttt_scan_params *params, c
     if (!desc || !params || !scan_desc_ok(*desc)) return TTT_ERR_ARG;
     const ttt_scan_desc &D = *desc;
     for (int i = 0; i < 2; ++i)
-        if (D.x_stride[i] < 0 || D.delta_stride[i] < 0 || D.z_stride[i] < 0 || D.dy_stride[i] < 0) return TTT_ERR_ARG;
+        if (D.x_stride[i] < 0 || D.delta_stride[i] < 0 || D.z_stride[i] < 0) return TTT_ERR_ARG;
     for (int i = 0; i < 3; ++i)
         if (D.b_stride[i] < 0 || D.c_stride[i] < 0) return TTT_ERR_ARG;
     if (!scan_desc_fits(D)) return TTT_ERR_UNSUPPORTED;
@@ -1327,6 +1326,7 @@ ttt_status ttt_selective_scan_bwd(const ttt_scan_desc *desc, const ttt_scan_para
     ttt::ScanArgs a;
     ttt_status st = scan_args(desc, params, x, delta, Bm, Cm, z, reset, stream, a);
     if (st != TTT_OK) return st;
+    if (desc->dy_stride[0] < 0 || desc->dy_stride[1] < 0) return TTT_ERR_ARG;
     const ttt_scan_grads none = {}, &gr = grads ? *grads : none;
     for (const float *q : {states, dh_last, (const float *)dh0, (const float *)gr.A, (const float *)gr.D, (const float *)gr.delta_bias})
         if (q && !aligned(q, 4)) return TTT_ERR_ALIGN;

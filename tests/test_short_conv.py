@@ -171,6 +171,19 @@ def test_scan_binding_refuses_before_any_launch(bad, monkeypatch):
         abi.ttt_selective_scan_fwd(*[a.pop(n) for n in ("x", "delta", "A", "B", "C")], **a)
 
 
+@pytest.mark.parametrize("st", [-1, 3])
+def test_forward_passes_do_not_look_at_the_gradients_strides(L, st):
+    """A description made for both directions: only the backward pass reads, and refuses, dy's."""
+    conv, scan = _conv_desc(T=0, strides=[64, 64, st, st]), _scan_desc(T=0)
+    scan.strides[6] = scan.strides[7] = st
+    par = abi.ScanVectors(_at(1), None, None)
+    assert L.ttt_short_conv_fwd(conv, _at(1), _at(2), None, None, None, _at(3), None, None) == 0
+    assert L.ttt_selective_scan_fwd(scan, par, *[None] * 11, 0, None) == 0
+    want = -1 if st < 0 else 0
+    assert L.ttt_short_conv_bwd(conv, _at(1), _at(2), _at(3), *[None] * 4, _at(4), *[None] * 4, 0, None) == want
+    assert L.ttt_selective_scan_bwd(scan, par, *[None] * 14, abi.ScanVectors(None, None, None), None, None, 0, None) == want
+
+
 # --------------------------------------------------------------------------- streams
 
 
