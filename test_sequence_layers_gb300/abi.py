@@ -14,6 +14,8 @@ from typing import NamedTuple, Optional
 
 import torch
 
+from .rotary import pair_bytes
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libttt.so")
 
@@ -699,7 +701,8 @@ def _rope(q, k, v, table, positions, pos0, period, interleaved, inverse, q_out, 
     else:
         svo = _rows("v_out", v_out, q, v.shape, dt, di)
     if pair_axis is not None:
-        pair_axis = bytes(pair_axis)
+        if not isinstance(pair_axis, bytes):
+            pair_axis = pair_bytes(pair_axis)
         if len(pair_axis) != tshape[1]:
             raise ValueError("pair_axis must name an axis for each of the table's pairs")
         if positions is None:

@@ -63,12 +63,21 @@ def rope_axes(sections, layout="blocks"):
     raise ValueError('layout must be "blocks" or "cyclic"')
 
 
+def pair_bytes(axes):
+    """A sequence of the pairs' axes, one byte each (a number is none: bytes(n) would be n zeros,
+    and an array's bytes() its memory)."""
+    try:
+        return bytes([*axes])
+    except TypeError:
+        raise ValueError("pair_axis must be a sequence of integers") from None
+
+
 def rope_axes_table(rows, pair_axis, per_axis=True, device="cuda", **scaling):
     """The table of ``abi.ttt_rope_axes``, fp32 [rows, rot/2, 2].  per_axis: every axis has
     the frequencies of a head of its own pairs alone (a picture's two halves); else pair i
     keeps the frequency it has with one axis.  Keyword arguments as rope_frequencies, per
     axis if per_axis."""
-    pair_axis = bytes(pair_axis)
+    pair_axis = pair_bytes(pair_axis)
     inv, m = rope_frequencies(2 * len(pair_axis), **scaling)
     if per_axis:
         for a in set(pair_axis):

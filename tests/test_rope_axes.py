@@ -3,6 +3,7 @@ ttt_rope_axes at the C boundary and in the binding."""
 import ctypes
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -74,3 +75,25 @@ def test_binding_refuses_before_any_launch(bad):
     a.update(bad)
     with pytest.raises(ValueError):
         abi.ttt_rope_axes(a.pop("q"), a.pop("k"), a.pop("v"), a.pop("table"), a.pop("pair_axis"), **a)
+
+
+@pytest.mark.parametrize("bad", [8, "01010101", [0.5] * 8, [-1] * 8, [256] * 8, torch.zeros(8)])
+def test_pair_axes_that_are_no_sequence_of_axes(bad):
+    """A number above all: bytes(8) is eight zeros, a rotation by the first axis alone."""
+    a = dict(k=None, v=None, table=_Dev((9, 8, 2), torch.float32), grid=(2, 2), q_out=_Dev((2, 3, 4, 16)))
+    with pytest.raises(ValueError):
+        abi.ttt_rope_axes(_Dev((2, 3, 4, 16)), pair_axis=bad, **a)
+    with pytest.raises(ValueError):
+        rotary.rope_axes_table(9, bad, device="cpu")
+
+
+@pytest.mark.parametrize("seq", [[0, 1, 1, 0], (0, 1, 1, 0), np.array([0, 1, 1, 0]), torch.tensor([0, 1, 1, 0]), range(4)])
+def test_sequences_of_axes(seq, monkeypatch):
+    got = []
+    monkeypatch.setattr(_Dev, "data_ptr", lambda self: FAKE)
+    monkeypatch.setattr(abi, "_call", lambda name, di, desc, axis, *rest: got.append(axis))
+    q = _Dev((2, 3, 4, 8))
+    abi.ttt_rope_axes(q, None, None, _Dev((9, 4, 2), torch.float32), seq, grid=(2, 2, 1, 1), q_out=_Dev((2, 3, 4, 8)))
+    want = bytes(int(a) for a in seq)
+    assert got == [want]
+    assert torch.equal(rotary.rope_axes_table(9, seq, device="cpu"), rotary.rope_axes_table(9, want, device="cpu"))
