@@ -6,7 +6,7 @@ import ctypes
 import pytest
 import torch
 
-from test_sequence_layers_gb300 import abi, build
+from test_sequence_layers_gb300 import abi, build, rotary
 from tests.test_descriptors import test_same_bytes as same_bytes
 from tests.test_rotary import _Dev
 from tests.test_streams import _T, _check, gpu  # noqa: F401
@@ -28,6 +28,14 @@ def _at(i):
                                            (abi._SCAN_DESC, abi.ScanDesc), (abi._THREE, abi.ScanVectors)])
 def test_packed_descriptors(packed, struct):
     same_bytes(packed, struct)
+
+
+def test_reached_from_the_package():
+    """Next to the operators of their kind."""
+    import test_sequence_layers_gb300 as ttt
+    for n in ("ttt_rope_axes", "ttt_selective_scan_fwd", "ttt_selective_scan_bwd", "ttt_short_conv_fwd", "ttt_short_conv_bwd"):
+        assert getattr(ttt, n) is getattr(abi, n)
+    assert ttt.rope_axes is rotary.rope_axes and ttt.rope_axes_table is rotary.rope_axes_table
 
 
 # ----------------------------------------------------------------------- convolution
