@@ -31,10 +31,13 @@ struct ConvParams {
     int few;  // forward: fewer than 2^31 threads
 };
 
-__device__ __forceinline__ float sigmoid(float v)
+// bf16 tensors: one ex2 of a rounded product, off by |v| 2^-24 of itself, far below the output's
+// rounding.  fp32 tensors: CUDA's expf.
+template <typename T> __device__ __forceinline__ float sigmoid(float v)
 {
     float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.4426950408889634f));
+    if constexpr (sizeof(T) == 2) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.4426950408889634f));
+    else e = expf(-v);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
     return r;
 }
@@ -198,7 +201,7 @@ template <typename T, int V, int K> __global__ void __launch_bounds__(kThreads) 
         for (int k = 0; k < K; ++k) fma_all(o, w[k], win[(a + k) % K]);
         if (p.silu)
 #pragma unroll
-            for (int j = 0; j < V; ++j) o[j] *= sigmoid(o[j]);
+            for (int j = 0; j < V; ++j) o[j] *= sigmoid<T>(o[j]);
         Pack<T, V> out;
         pack(out, o);
         out.store(yt + (size_t)a * p.C);
@@ -298,7 +301,7 @@ template <typename T, int V, int K> __global__ void __launch_bounds__(kThreads, 
                 for (int k = 0; k < K; ++k) fma_all(s, w[k], win[(a + k) % K]);
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const float sg = sigmoid(s[j]);
+                    const float sg = sigmoid<T>(s[j]);
                     g[j] *= sg * fmaf(s[j], 1.f - sg, 1.f);
                 }
             }
