@@ -48,7 +48,13 @@ __device__ __forceinline__ float rcp(float x)
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ float sigmoid(float v) { return rcp(1.f + ex2(-kLog2e * v)); }
+// exp(-v) of a gate or a rate's argument.  bf16 tensors: one ex2 of a rounded product, off by
+// |v| 2^-24 of itself, far below the outputs' rounding.  fp32 tensors: CUDA's expf.
+template <typename T> __device__ __forceinline__ float exp_neg(float v)
+{
+    return sizeof(T) == 2 ? ex2(-kLog2e * v) : expf(-v);
+}
+template <typename T> __device__ __forceinline__ float sigmoid(float v) { return rcp(1.f + exp_neg<T>(v)); }
 
 // log(1 + e) for 0 <= e <= 1 as e P(e), P the Chebyshev interpolation of log(1 + e) / e in
 // e on [0, 1]: relative error below 2^-22, also where e is small.
@@ -73,11 +79,10 @@ __device__ __forceinline__ float2 log1p_unit(float2 e)
     return __fmul2_rn(e, p);
 }
 
-// max(v, 0) + log(1 + exp(-|v|)); e = exp(-|v|) for the slope.  Nothing overflows.
-__device__ __forceinline__ float softplus(float v, float &e)
+// max(v, 0) + log(1 + exp(-|v|)).  Nothing overflows.
+template <typename T> __device__ __forceinline__ float softplus(float v)
 {
-    e = ex2(-kLog2e * fabsf(v));
-    const float l = log1p_unit(e);
+    const float l = log1p_unit(exp_neg<T>(fabsf(v)));
     return v > 0.f ? v + l : v <= 0.f ? l : v;  // NaN stays
 }
 
@@ -99,22 +104,19 @@ template <typename T> __device__ __forceinline__ void put(T *p, float x)
 }
 
 // Rates of V values, two at a time (the polynomial is most of the work).
-template <int V> __device__ __forceinline__ void softplus_all(float (&v)[V])
+template <typename T, int V> __device__ __forceinline__ void softplus_all(float (&v)[V])
 {
     if constexpr (V % 2 == 0) {
 #pragma unroll
         for (int j = 0; j < V; j += 2) {
-            const float2 e = make_float2(ex2(-kLog2e * fabsf(v[j])), ex2(-kLog2e * fabsf(v[j + 1])));
+            const float2 e = make_float2(exp_neg<T>(fabsf(v[j])), exp_neg<T>(fabsf(v[j + 1])));
             const float2 l = log1p_unit(e);
             v[j] = v[j] > 0.f ? v[j] + l.x : v[j] <= 0.f ? l.x : v[j];  // NaN stays
             v[j + 1] = v[j + 1] > 0.f ? v[j + 1] + l.y : v[j + 1] <= 0.f ? l.y : v[j + 1];
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            float e;
-            v[j] = softplus(v[j], e);
-        }
+        for (int j = 0; j < V; ++j) v[j] = softplus<T>(v[j]);
     }
 }
 

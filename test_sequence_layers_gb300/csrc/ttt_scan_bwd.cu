@@ -122,11 +122,11 @@ __global__ void __launch_bounds__(16 * LN) ttt_scan_bwd_map_kernel(const __grid_
             unpack(pz[i], zf);
 #pragma unroll
             for (int j = 0; j < V; ++j) df[j] += bias[j];
-            if (p.softplus) softplus_all(df);
+            if (p.softplus) softplus_all<T>(df);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 if (!live) df[j] = 0.f;  // past the end: nothing moves (the gradient is zero there)
-                if (p.z) gf[j] *= zf[j] * sigmoid(zf[j]);
+                if (p.z) gf[j] *= zf[j] * sigmoid<T>(zf[j]);
             }
             put_floats(&ds[t][vch - c0], df);
             put_floats(&gs[t][vch - c0], gf);
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(block_threads(LN)) ttt_scan_bwd_kernel(const _
             tensors(t0, nt, stage, v, xf, df, gf, zf);
 #pragma unroll
             for (int j = 0; j < V; ++j) df[j] += bias[j];
-            if (p.softplus) softplus_all(df);
+            if (p.softplus) softplus_all<T>(df);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 if (!live) df[j] = 0.f;  // past the end: nothing moves
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(block_threads(LN)) ttt_scan_bwd_kernel(const _
             }
             if (p.z)
 #pragma unroll
-                for (int j = 0; j < V; ++j) gf[j] *= zf[j] * sigmoid(zf[j]);
+                for (int j = 0; j < V; ++j) gf[j] *= zf[j] * sigmoid<T>(zf[j]);
             const int at = t * CB;
             put_turned(sm + L::d + at, vch, vch >> 4, df);
             put_turned(sm + L::u + at, vch, vch >> 4, xf);
@@ -502,12 +502,12 @@ __global__ void __launch_bounds__(block_threads(LN)) ttt_scan_bwd_kernel(const _
             for (int j = 0; j < V; ++j) {
                 float slope = 1.f, g = gf[j];
                 if (p.softplus) {
-                    const float w = df[j] + bias[j], e = ex2(-kLog2e * fabsf(w));
+                    const float w = df[j] + bias[j], e = exp_neg<T>(fabsf(w));
                     slope = rcp(1.f + e);
                     if (w < 0.f) slope *= e;
                 }
                 if (p.z) {
-                    const float sg = sigmoid(zf[j]), y = fmaf(Dv[j], xf[j], ys[j]);
+                    const float sg = sigmoid<T>(zf[j]), y = fmaf(Dv[j], xf[j], ys[j]);
                     dz[j] = g * y * sg * fmaf(zf[j], 1.f - sg, 1.f);
                     g *= zf[j] * sg;
                 }

@@ -75,8 +75,8 @@ __global__ void __launch_bounds__(128) ttt_scan_step_kernel(const __grid_constan
         if (p.reset && p.reset[(size_t)b * p.T + t]) h = quad(make_float4(0.f, 0.f, 0.f, 0.f));
         const float4 Bt = load_four<FOURS>(Bm + t * p.bs[1], n0, p.N), Ct = load_four<FOURS>(Cm + t * p.cs[1], n0, p.N);
         const float xv = get(x + t * p.xs[1]), zv = z ? get(z + t * p.zs[1]) : 0.f;
-        float d = get(dl + t * p.ds[1]) + bias, e;
-        if (p.softplus) d = softplus(d, e);
+        float d = get(dl + t * p.ds[1]) + bias;
+        if (p.softplus) d = softplus<T>(d);
         step(h, d, d * xv, A, Bt);
         float2 s2;
         dot(s2, h, Ct, true);
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(128) ttt_scan_step_kernel(const __grid_constan
 #pragma unroll
         for (int s = LN / 2; s > 0; s >>= 1) y += __shfl_xor_sync(0xffffffffu, y, s);
         y = fmaf(D, xv, y);
-        if (z) y *= zv * sigmoid(zv);
+        if (z) y *= zv * sigmoid<T>(zv);
         if (on && n0 == 0) put(static_cast<T *>(p.y) + ((size_t)b * p.T + t) * p.C + c, y);
     }
     if (p.y_state && on) store_states(p.y_state + row, n0, p.N, four(h));
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) ttt_scan_fwd_kernel(const __gr
                 }
             }
             load(t0 + t + kAt);
-            if (p.softplus) softplus_all(d);
+            if (p.softplus) softplus_all<T>(d);
             if (t + kAt > nt)
 #pragma unroll
                 for (int k = 0; k < kAt; ++k)
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) ttt_scan_fwd_kernel(const __gr
                         o[k] = s.x + s.y;
 #pragma unroll
                         for (int i = CL; i < 32; i *= 2) o[k] += __shfl_xor_sync(0xffffffffu, o[k], i);
-                        const float w = gated ? zf[k] * sigmoid(zf[k]) : 1.f;
+                        const float w = gated ? zf[k] * sigmoid<T>(zf[k]) : 1.f;
                         o[k] = fmaf(D, xf[k], o[k]) * w;
                     }
                 }
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kLaneCB *LN) ttt_scan_fwd_lanes_kernel(const _
             const bool live = t < nt && vch < cend;
 #pragma unroll
             for (int j = 0; j < V; ++j) d[j] += bias[j];
-            if (p.softplus) softplus_all(d);
+            if (p.softplus) softplus_all<T>(d);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 if (!live) d[j] = 0.f;  // past the end: the state stays
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(kLaneCB *LN) ttt_scan_fwd_lanes_kernel(const _
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 o[j] = fmaf(Dv[j], xf[j], o[j]);
-                if (p.z) o[j] *= zf[j] * sigmoid(zf[j]);
+                if (p.z) o[j] *= zf[j] * sigmoid<T>(zf[j]);
             }
             Pack<T, V> r;
             pack(r, o);
