@@ -212,10 +212,10 @@ struct Quad {
 __device__ __forceinline__ Quad quad(float4 v) { return {{v.x, v.y}, {v.z, v.w}}; }
 __device__ __forceinline__ float4 four(const Quad &q) { return make_float4(q.a.x, q.a.y, q.b.x, q.b.y); }
 
-// states n0 .. n0 + 3 of a row of N, `fill` past its end
-__device__ __forceinline__ float4 load_states(const float *row, int n0, int N, float fill)
+// states n0 .. n0 + 3 of a row of N, zeros past its end
+__device__ __forceinline__ float4 load_states(const float *row, int n0, int N)
 {
-    float4 v = make_float4(fill, fill, fill, fill);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (N % 4 == 0 && (reinterpret_cast<uintptr_t>(row) & 15) == 0) {
         if (n0 < N) v = *reinterpret_cast<const float4 *>(row + n0);
         return v;
@@ -273,7 +273,8 @@ __device__ __forceinline__ void dot(float2 &s, const Quad &h, float4 Ct, bool fi
 inline int lanes(int N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
 
 // A sequence of `chunks` cut into pieces so that warps x pieces comes to `want`, pieces of at
-// least `least` chunks.  Two pieces are none: their halves' own maps cost what they gain.
+// least `least` chunks.  Fewer than three are not asked for: their halves' own maps cost what they gain.
+// (Three of four chunks, in the backward pass, come to two by rounding.)
 inline ScanPieces cut(int chunks, long long warps, long long want, int least)
 {
     long long segs = warps > 0 ? want / warps : 1;
@@ -318,7 +319,8 @@ inline void params(const ScanArgs &a, Params &p)
 }
 
 // May every tensor be moved 16 bytes at a time: pointers, strides, a group's channels and
-// a row of states multiples of them.
+// a row of states multiples of them.  One answer for all: where B and C alone are not aligned, or a
+// row of states is not whole, the token tensors move one element at a time too.
 inline bool wide(const ScanArgs &a)
 {
     const int es = a.bf16 ? 2 : 4, V = 16 / es;

@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(16 * LN) ttt_scan_bwd_map_kernel(const __grid_
     const unsigned char *reset = p.reset ? p.reset + (size_t)b * p.T : nullptr;
     Quad A = quad(make_float4(0.f, 0.f, 0.f, 0.f)), r = A;
     if (on) {
-        A = quad(load_states(p.A + (size_t)c * p.N, n0, p.N, 0.f));
+        A = quad(load_states(p.A + (size_t)c * p.N, n0, p.N));
         A.a = __fmul2_rn(A.a, make_float2(kLog2e, kLog2e));
         A.b = __fmul2_rn(A.b, make_float2(kLog2e, kLog2e));
     }
@@ -229,11 +229,11 @@ __global__ void __launch_bounds__(block_threads(LN)) ttt_scan_bwd_kernel(const _
     for (int k = 0; k < 2; ++k) {
         const int c = c0 + cl + k;
         Quad q = quad(zero4);
-        if (c < cend) q = quad(load_states(p.A + (size_t)c * p.N, n0, p.N, 0.f));
+        if (c < cend) q = quad(load_states(p.A + (size_t)c * p.N, n0, p.N));
         A[k][0] = __fmul2_rn(q.a, make_float2(kLog2e, kLog2e));
         A[k][1] = __fmul2_rn(q.b, make_float2(kLog2e, kLog2e));
         q = quad(zero4);
-        if (c < cend && p.start) q = quad(load_states(p.start + (((size_t)b * p.segs + seg) * p.C + c) * p.N, n0, p.N, 0.f));
+        if (c < cend && p.start) q = quad(load_states(p.start + (((size_t)b * p.segs + seg) * p.C + c) * p.N, n0, p.N));
         r[k][0] = q.a;
         r[k][1] = q.b;
         dA[k][0] = dA[k][1] = zero2;
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(block_threads(LN)) ttt_scan_bwd_kernel(const _
         for (int k = 0; k < 2; ++k) {
             const int c = c0 + cl + k;
             Quad q = quad(zero4);
-            if (c < cend) q = quad(load_states(p.states + (((size_t)b * p.chunks + t0 / kScanChunk) * p.C + c) * p.N, n0, p.N, 0.f));
+            if (c < cend) q = quad(load_states(p.states + (((size_t)b * p.chunks + t0 / kScanChunk) * p.C + c) * p.N, n0, p.N));
             h[k][0] = q.a;
             h[k][1] = q.b;
         }

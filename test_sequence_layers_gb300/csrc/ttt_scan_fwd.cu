@@ -49,7 +49,7 @@ template <typename T, int LN, bool FOURS>
 __global__ void __launch_bounds__(128) ttt_scan_step_kernel(const __grid_constant__ Params p)
 {
     auto load_states = [](const float *row, int n0, int N) {
-        if constexpr (!FOURS) return scan::load_states(row, n0, N, 0.f);
+        if constexpr (!FOURS) return scan::load_states(row, n0, N);
         else return n0 < N ? *reinterpret_cast<const float4 *>(row + n0) : make_float4(0.f, 0.f, 0.f, 0.f);
     };
     auto store_states = [](float *row, int n0, int N, float4 v) {
@@ -135,11 +135,11 @@ __global__ void __launch_bounds__(32 * kWarps, 4) ttt_scan_fwd_kernel(const __gr
     Quad A[Q], h[Q];
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-        A[q] = quad(load_states(p.A + (size_t)c * p.N, n0 + 4 * LN * q, p.N, 0.f));
+        A[q] = quad(load_states(p.A + (size_t)c * p.N, n0 + 4 * LN * q, p.N));
         A[q].a = __fmul2_rn(A[q].a, make_float2(kLog2e, kLog2e));
         A[q].b = __fmul2_rn(A[q].b, make_float2(kLog2e, kLog2e));
         h[q] = zero;
-        if (!SUM && p.start) h[q] = quad(load_states(p.start + (((size_t)b * p.segs + seg) * p.C + c) * p.N, n0 + 4 * LN * q, p.N, 0.f));
+        if (!SUM && p.start) h[q] = quad(load_states(p.start + (((size_t)b * p.segs + seg) * p.C + c) * p.N, n0 + 4 * LN * q, p.N));
     }
 
     Pack<T, V> pb[kIt], pc[SUM ? 1 : kIt];
@@ -341,10 +341,10 @@ __global__ void __launch_bounds__(kLaneCB *LN) ttt_scan_fwd_lanes_kernel(const _
     const Quad zero = quad(make_float4(0.f, 0.f, 0.f, 0.f));
     Quad A = zero, h = zero;
     if (on) {
-        A = quad(load_states(p.A + (size_t)c * p.N, n0, p.N, 0.f));
+        A = quad(load_states(p.A + (size_t)c * p.N, n0, p.N));
         A.a = __fmul2_rn(A.a, make_float2(kLog2e, kLog2e));
         A.b = __fmul2_rn(A.b, make_float2(kLog2e, kLog2e));
-        if (p.start) h = quad(load_states(p.start + ((size_t)b * p.C + c) * p.N, n0, p.N, 0.f));
+        if (p.start) h = quad(load_states(p.start + ((size_t)b * p.C + c) * p.N, n0, p.N));
     }
     Pack<T, V> px[kIt], pd[kIt], pz[kIt], pb[kBIt], pc[kBIt];
     const int vch = c0 + tid % kRowVecs * V;  // this thread's channels in every pass
