@@ -551,8 +551,9 @@ ttt_status ttt_short_conv_bwd(const ttt_short_conv_desc *desc, const void *dy, c
 /* Selective scan problem description.  Strides in elements; channels (B and C: states)
  * are contiguous. */
 typedef struct {
-    int B, T, C;               /* batch (<= 65535), tokens (<= 2^30; B T G < 2^31), channels */
-    int N;                     /* states of a channel, 1 .. 64 (TTT_ERR_UNSUPPORTED above) */
+    int B, T, C;               /* batch (<= 65535), tokens (<= 2^30), channels            */
+    int N;                     /* states of a channel, 1 .. 64; B T G and C N at most
+                                  0x7fff0000 (TTT_ERR_UNSUPPORTED above, as for B and T)  */
     int G;                     /* groups of C / G neighbouring channels with one B and C  */
     ttt_dtype io_dtype;        /* dtype of every token tensor                           */
     int softplus;              /* 1: the rate is softplus(delta + bias); 0: delta + bias  */
@@ -594,8 +595,8 @@ size_t ttt_selective_scan_fwd_workspace(const ttt_scan_desc *desc);
  *              bytes, free again once the work on `stream` is done
  * A is finite and meant for d A <= 0 (decays).  States are fp32 throughout; sums run in an
  * order that is fixed by the sizes, dtype, alignment and strides (the same call gives the
- * same bits).  Data pointers: aligned to their element; 16-byte alignment, strides of whole
- * 16 bytes, C / G and N multiples of 8 (bf16) or 4 (fp32) move 16 bytes at a time.
+ * same bits).  Data pointers: aligned to their element; where all have 16-byte alignment, strides
+ * of whole 16 bytes, C / G and N multiples of 8 (bf16) or 4 (fp32), 16 bytes move at a time.
  * Outputs may not overlap inputs or each other (h_last as above).
  */
 ttt_status ttt_selective_scan_fwd(const ttt_scan_desc *desc, const ttt_scan_params *params, const void *x,

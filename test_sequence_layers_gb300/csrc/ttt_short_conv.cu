@@ -9,9 +9,11 @@
 // Bound by reading and writing every tensor once: a thread walks along the tokens of one
 // piece with the last K - 1 rows of its V neighbouring channels in registers.  Measured, K = 4,
 // SiLU, bf16 (of the copy bandwidth by bytes read and written once): 2 x 32768 x 2048 forward
-// 92 us (0.86), backward 192 us (0.62: 163 registers leave 12 warps an SM, issue slots 60%
-// busy; the sums of the taps' gradients alone are 20 of them); 8 x 2048 x 768 forward 14.8 us
-// (0.50: ramp-up and tail), backward 24; fp32 2 x 16384 x 2048 86 and 152 us.
+// 94 us (0.84; 92 under ncu), backward 191 us (0.62: 163 registers leave 12 warps an SM, issue slots
+// 60% busy; the sums of the taps' gradients alone are 20 of them); 8 x 2048 x 768 forward 14.8 us
+// (0.50: ramp-up and tail), backward 24; fp32 2 x 16384 x 2048 86 (0.92) and 165 us (0.72).
+// Fewer than 32 vectors of channels leave lanes of the backward pass without work: 64 x 4096
+// tokens of 8, 16, 64, 128 channels 95, 71, 58, 67 us, and 46, 25, 8, 5 us for the sums of its blocks.
 #include "ttt_internal.h"
 #include "ttt_vec.cuh"
 
@@ -445,9 +447,10 @@ template <typename T, int V> int fwd_width(const ConvArgs &a)
     ConvParams p;
     conv_params(a, p, V);
     // tokens a thread walks: 4 .. 64, as many as leave 512 threads an SM, 1024 where they move
-    // less at a time (K - 1 rows and the taps are read once a piece; 8 x 2048 x 768 bf16: 20
-    // tokens 14.8 us, 4 tokens 58; 2 x 32768 x 2048: 64 tokens 95 us, 32 101, 16 116; 3 x 701 x
-    // 1001 fp32, K = 3: 13 tokens 8.1 us, 27 10.5)
+    // less at a time (K - 1 rows and the taps are read once a piece).  Measured on this build, the
+    // rule's own first: 8 x 2048 x 768 bf16: 40 tokens 14.8 us; 4 25.3, 8 17.9, 12 15.6, 16 16.0, 20
+    // 16.5, 24 13.5, 32 14.2, 64 17.4.  2 x 32768 x 2048: 64 tokens 94 us; 4 227, 8 151, 16 113, 32 99.
+    // 3 x 701 x 1001 fp32, K = 3: 13 tokens 7.8 us; 4 9.4, 8 8.3, 10 7.1, 16 8.5, 27 10.5
     const long long fill = (long long)a.B * a.T * p.nv / ((V == 4 ? 512LL : 1024LL) * kSMs);
     p.len = (int)(fill < 4 ? 4 : fill > 64 ? 64 : fill);
     p.pieces = (a.T + p.len - 1) / p.len;
@@ -507,7 +510,7 @@ template <typename T, int V> int bwd_width(const ConvArgs &a)
 
 // Four channels a thread at most, 8 bytes of bf16: with eight the window, the taps and their
 // sums take so many registers that too few threads are left to wait for memory (2 x 32768 x
-// 2048 forward: 95 us against 107).
+// 2048 forward: 107 us in the build that took 95 with four).
 int launch_conv_fwd(const ConvArgs &a)
 {
     switch (widest(a, 4)) {
